@@ -351,6 +351,119 @@ int qlora_moe_bwd_dev(const void *dY, const void *X, int64_t m, const int64_t *c
                       const void *T, void *dX, void *dA, void *dB, void *ws, size_t ws_bytes,
                       void *stream);
 
+/* ---- Adapters of many requests beside one base ------------------------------------------------
+ * One frozen 4-bit weight, L adapters (1 <= L <= 1024) of rank r [the adapters, not the base, are
+ * what training makes and what is kept for each task: Unsloth v0.1.463-beta release article, "About
+ * the Unsloth Project"], and for every row of X the adapter it belongs to: a batch of requests to
+ * different fine-tuned models, or of different training jobs. With a = ids[i] for row i,
+ *   T_i = X_i A_a^T,   Y_i = X_i deq(W)^T + s[a] T_i B_a^T
+ *   U_i = dY_i B_a,    dX_i = dY_i deq(W) + s[a] U_i A_a
+ *   dA_a = s[a] sum over its rows of U_i^T X_i,   dB_a = s[a] sum over its rows of dY_i^T T_i.
+ * A row whose id lies outside [0, L) has no adapter: T_i = 0, Y_i = X_i deq(W)^T, and it adds to no
+ * gradient but dX. Rows may come in any order. Layout: ids int32 [m]; A bf16 [L, r, k]; B bf16
+ * [L, n, r]; s float32 [L]; all in device memory (nothing waits for it, so the calls can be captured
+ * in a graph whose replays bring other ids). Adapters of a lower rank are padded with zeros.
+ * The low-rank term is part of the fused launch of Y (dX); it is scaled by s[a] in float32. T and U
+ * are rounded to bf16.
+ *
+ * Bytes of device workspace of the forward and the backward. */
+size_t qlora_multi_fwd_workspace_bytes(int64_t m, int64_t n, int64_t k, int32_t r, int32_t L);
+size_t qlora_multi_bwd_workspace_bytes(int64_t m, int64_t n, int64_t k, int32_t r, int32_t L);
+
+/* Forward: Y bf16 [m, n] and T bf16 [m, r] (kept for the backward). Requires n % 8 == 0 and
+ * 1 <= r <= 128. Errors: as qlora_fwd; NF4_EINVAL also for L or r out of range, a NULL or
+ * misaligned ids, s or T (ids and s: 4-byte aligned). */
+int qlora_multi_fwd(const void *X, int64_t m, const nf4_tensor *W, const void *A, const void *B,
+                    const float *s, const int32_t *ids, int32_t L, int32_t r, void *Y, void *T, void *ws,
+                    size_t ws_bytes, void *stream);
+
+/* Backward for dY bf16 [m, n]: dX bf16 [m, k] (skipped when NULL), dA bf16 [L, r, k], dB bf16
+ * [L, n, r], zero for an adapter without rows; T from the forward or NULL (recomputed). Sums over
+ * rows are float32, in an order that the ids alone fix. Non-finite dY: as qlora_bwd.
+ * Errors: as qlora_multi_fwd. */
+int qlora_multi_bwd(const void *dY, const void *X, int64_t m, const nf4_tensor *W, const void *A,
+                    const void *B, const float *s, const int32_t *ids, int32_t L, int32_t r, const void *T,
+                    void *dX, void *dA, void *dB, void *ws, size_t ws_bytes, void *stream);
+
+/* ---- Norm and rotation of query and key heads ---------------------------------------------------
+ * What follows the q and k projections: every head x of d elements is normalised and its first `rot`
+ * elements are rotated in pairs by the angles of the token's position,
+ *   n = x / sqrt(mean(x^2) + eps) * (w + w_offset),
+ *   (n_a, n_b) -> (n_a cos - n_b sin, n_a sin + n_b cos),
+ * pairs (i, i + rot/2), or (2i, 2i + 1) when interleaved; elements past rot are not rotated. Any
+ * layout whose heads are contiguous: q and k may be slices of one packed projection, and an output
+ * may be its input. */
+typedef struct {
+  void *data;                           /* element (token, head, i) at token * token_stride +        */
+  int64_t token_stride, head_stride;    /* head * head_stride + i, strides in elements, >= 0         */
+  int32_t heads;                        /* 0: none (the struct's other fields are ignored)           */
+} nf4_heads;
+
+/* The arguments both directions share (a host object). */
+typedef struct {
+  int64_t tokens;         /* >= 0 (0: nothing to do); tokens * (q heads + k heads) < 2^31            */
+  int32_t d, rot;         /* head size, 2 .. 512, even; rotated elements, 0 .. d, even               */
+  int32_t interleaved;    /* 0: pairs (i, i + rot/2); 1: pairs (2i, 2i + 1)                          */
+  int32_t dtype;          /* nf4_dtype of q, k, their outputs and gradients                          */
+  int32_t w_dtype;        /* nf4_dtype of wq and wk                                                  */
+  const void *wq, *wk;    /* [d] each                                                                */
+  float w_offset, eps;    /* eps >= 0                                                                */
+  const float *cos, *sin; /* [places, rot/2]; ignored (with pos) when rot == 0                       */
+  int64_t places;
+  const void *pos;        /* [tokens] int32 or int64; a token whose position lies outside            */
+  int32_t pos64;          /* [0, places) gets NaN outputs                                            */
+} nf4_head_norm;
+
+/* Forward: q_out, k_out as above, of the heads of q and k. Sums in float32, one rounding.
+ * Errors: NF4_EINVAL for a NULL pointer that is needed, head counts that differ, negative sizes or
+ * strides, a pointer not aligned to its elements, an unknown dtype; NF4_EUNSUPPORTED for d or rot out
+ * of range or odd, or too many heads. */
+int qk_norm_rope_fwd(const nf4_head_norm *p, const nf4_heads *q, const nf4_heads *k,
+                     const nf4_heads *q_out, const nf4_heads *k_out, void *stream);
+
+/* Bytes of device workspace of the backward (parts of dwq and dwk). */
+size_t qk_norm_rope_bwd_workspace_bytes(int32_t d);
+
+/* Backward: dq, dk (strided like any heads: the slices of a packed gradient), and dwq, dwk float32
+ * [d], summed over tokens and heads in a fixed order (NULL: not wanted), from the gradients gq, gk of
+ * the outputs and the forward's inputs q and k. Errors: as the forward; NF4_EINVAL for a short
+ * workspace. */
+int qk_norm_rope_bwd(const nf4_head_norm *p, const nf4_heads *gq, const nf4_heads *gk, const nf4_heads *q,
+                     const nf4_heads *k, const nf4_heads *dq, const nf4_heads *dk, float *dwq, float *dwk,
+                     void *ws, size_t ws_bytes, void *stream);
+
+/* ---- Distillation from a teacher's top logits ---------------------------------------------------
+ * The loss that trains a student on the `top` largest logits a teacher left for each token. With
+ * z = logits / tau, lse = log sum exp z over the v logits and p = softmax(teacher / tau) over the
+ * kept entries of a row,
+ *   loss = sum_j p_j (log p_j - (z[idx_j] - lse)),
+ *   dlogits_i = (w / tau) (exp(z_i - lse) - sum of p_j over the entries j with idx_j == i).
+ * An entry whose index lies outside [0, v) or whose teacher logit is -inf is not there; a row
+ * without entries has loss 0 and a zero gradient. Logits of -inf are masked (they have probability
+ * 0); a row without a finite logit gives NaN.
+ * logits, dlogits: `dtype` [t, v] with row strides ld, ldd >= v in elements (rows need no
+ * alignment); idx int32 [t, top], teacher float32 [t, top], 1 <= top <= 1024; t >= 0 (0: nothing to
+ * do), 1 <= v < 2^30; tau > 0, finite. dlogits may be logits.
+ * Errors: NF4_EINVAL for a NULL pointer, sizes or tau out of range, a stride below v, a pointer not
+ * aligned to its elements or an unknown dtype; NF4_EUNSUPPORTED for t or v too large. */
+
+/* loss float32 [t] and lse float32 [t] (NULL: not wanted). */
+int distill_topk_fwd(const void *logits, int dtype, int64_t t, int64_t v, int64_t ld, const int32_t *idx,
+                     const float *teacher, int32_t top, float tau, float *loss, float *lse, void *stream);
+
+/* dlogits for the gradients grad float32 [t] of the rows' losses, given lse from the forward. A row
+ * whose gradient is 0 is not read: its dlogits are 0. */
+int distill_topk_bwd(const void *logits, int dtype, int64_t t, int64_t v, int64_t ld, const int32_t *idx,
+                     const float *teacher, int32_t top, float tau, const float *lse, const float *grad,
+                     void *dlogits, int64_t ldd, void *stream);
+
+/* Both in one pass over the logits, for a training step that knows each row's weight (its mask, over
+ * the number of tokens): loss float32 [t] (unweighted; 0 for a row of weight 0, which is not read)
+ * and dlogits for weight float32 [t] (NULL: every weight 1). */
+int distill_topk_step(const void *logits, int dtype, int64_t t, int64_t v, int64_t ld, const int32_t *idx,
+                      const float *teacher, int32_t top, float tau, const float *weight, float *loss,
+                      void *dlogits, int64_t ldd, void *stream);
+
 /* Thread-local description of the last non-OK status returned on this thread ("" if none). */
 const char *nf4_last_error(void);
 

@@ -13,6 +13,11 @@ torch fallback: if the library is not built, every call raises.
     dX, dAgu, dBg, dBu = qlora_swiglu_bwd(dH, X, qgu, Agu, Bg, Bu, s, Ygu, Tgu)
     W_merged = qlora_merge(q, A, B, s)                # bf16 deq(W) + s B A (requantize=256: NF4)
     Y, T = qlora_moe_fwd(X, counts, qe, Ae, Be, s)    # experts: rows grouped, tensors stacked
+    Y, T = qlora_multi_fwd(X, q, A, B, s, ids)        # an adapter of its own for every row: A [L, r, k]
+    dX, dA, dB = qlora_multi_bwd(dY, X, q, A, B, s, ids, T)
+    qo, ko = qk_norm_rope_fwd(q, k, wq, wk, cos, sin, pos)   # head norms and rotation, q [m, heads, d]
+    loss, lse = distill_topk_fwd(logits, idx, teacher, tau)  # from a teacher's top logits
+    loss, dlogits = distill_topk_step(logits, idx, teacher, tau, weight)   # with the gradient, one pass
 """
 from __future__ import annotations
 
@@ -35,7 +40,10 @@ EXPORTED = ("nf4_quantize", "nf4_dequantize", "nf4_codebook", "qlora_fwd_workspa
             "qlora_swiglu_fwd_fused",
             "qlora_swiglu_bwd", "qlora_merge", "qlora_moe_workspace_bytes", "qlora_moe_fwd",
             "qlora_moe_fwd_fused", "qlora_moe_bwd", "qlora_moe_workspace_bytes_dev", "qlora_moe_fwd_dev",
-            "qlora_moe_bwd_dev", "qlora_fwd_noalloc", "nf4_last_error")
+            "qlora_moe_bwd_dev", "qlora_fwd_noalloc", "nf4_last_error",
+            "qlora_multi_fwd_workspace_bytes", "qlora_multi_bwd_workspace_bytes", "qlora_multi_fwd",
+            "qlora_multi_bwd", "qk_norm_rope_fwd", "qk_norm_rope_bwd_workspace_bytes", "qk_norm_rope_bwd",
+            "distill_topk_fwd", "distill_topk_bwd", "distill_topk_step")
 
 
 class NF4Error(RuntimeError):
@@ -50,6 +58,19 @@ class _NF4TensorC(ctypes.Structure):
                 ("absmax", ctypes.c_void_p), ("absmax_scale", ctypes.c_void_p)]
 
 
+class _HeadsC(ctypes.Structure):
+    _fields_ = [("data", ctypes.c_void_p), ("token_stride", ctypes.c_int64),
+                ("head_stride", ctypes.c_int64), ("heads", ctypes.c_int32)]
+
+
+class _HeadNormC(ctypes.Structure):
+    _fields_ = [("tokens", ctypes.c_int64), ("d", ctypes.c_int32), ("rot", ctypes.c_int32),
+                ("interleaved", ctypes.c_int32), ("dtype", ctypes.c_int32), ("w_dtype", ctypes.c_int32),
+                ("wq", ctypes.c_void_p), ("wk", ctypes.c_void_p), ("w_offset", ctypes.c_float),
+                ("eps", ctypes.c_float), ("cos", ctypes.c_void_p), ("sin", ctypes.c_void_p),
+                ("places", ctypes.c_int64), ("pos", ctypes.c_void_p), ("pos64", ctypes.c_int32)]
+
+
 def library() -> ctypes.CDLL:
     """Load libnf4qlora.so (built by nf4_dequant_gemm_amd.build); raises if it is missing."""
     global _lib
@@ -60,6 +81,7 @@ def library() -> ctypes.CDLL:
     lib = ctypes.CDLL(_LIB_PATH)
     vp, i64, i32, f32, sz = ctypes.c_void_p, ctypes.c_int64, ctypes.c_int32, ctypes.c_float, ctypes.c_size_t
     P = ctypes.POINTER(_NF4TensorC)
+    N, H = ctypes.POINTER(_HeadNormC), ctypes.POINTER(_HeadsC)
     sig = {
         "nf4_quantize": (ctypes.c_int, [vp, ctypes.c_int, P, vp]),
         "nf4_dequantize": (ctypes.c_int, [P, vp, ctypes.c_int, vp]),
@@ -87,6 +109,16 @@ def library() -> ctypes.CDLL:
         "qlora_swiglu_bwd": (ctypes.c_int, [vp, vp, i64, P, vp, vp, vp, i32, f32, vp, vp, vp, vp, vp, vp,
                                             vp, sz, vp]),
         "nf4_last_error": (ctypes.c_char_p, []),
+        "qlora_multi_fwd_workspace_bytes": (sz, [i64, i64, i64, i32, i32]),
+        "qlora_multi_bwd_workspace_bytes": (sz, [i64, i64, i64, i32, i32]),
+        "qlora_multi_fwd": (ctypes.c_int, [vp, i64, P, vp, vp, vp, vp, i32, i32, vp, vp, vp, sz, vp]),
+        "qlora_multi_bwd": (ctypes.c_int, [vp, vp, i64, P, vp, vp, vp, vp, i32, i32, vp, vp, vp, vp, vp, sz, vp]),
+        "qk_norm_rope_fwd": (ctypes.c_int, [N, H, H, H, H, vp]),
+        "qk_norm_rope_bwd_workspace_bytes": (sz, [i32]),
+        "qk_norm_rope_bwd": (ctypes.c_int, [N, H, H, H, H, H, H, vp, vp, vp, sz, vp]),
+        "distill_topk_fwd": (ctypes.c_int, [vp, ctypes.c_int, i64, i64, i64, vp, vp, i32, f32, vp, vp, vp]),
+        "distill_topk_bwd": (ctypes.c_int, [vp, ctypes.c_int, i64, i64, i64, vp, vp, i32, f32, vp, vp, vp, i64, vp]),
+        "distill_topk_step": (ctypes.c_int, [vp, ctypes.c_int, i64, i64, i64, vp, vp, i32, f32, vp, vp, vp, i64, vp]),
     }
     for name, (res, args) in sig.items():
         fn = getattr(lib, name)
@@ -550,6 +582,238 @@ def qlora_swiglu_bwd(dH: torch.Tensor, X: torch.Tensor, q: NF4Tensor, Agu: Optio
     return dX, dAgu, dBg, dBu
 
 
+def _same_device(dev: torch.device, **tensors):
+    for name, t in tensors.items():
+        if t is not None and t.device != dev:
+            raise ValueError(f"{name} must be on {dev} (got {t.device})")
+
+
+def _multi_args(X, q: NF4Tensor, A, B, s, ids):
+    if A.dim() != 3 or B.dim() != 3:
+        raise ValueError("A must be [L, r, k] and B [L, n, r]")
+    m, (L, r) = X.shape[0], A.shape[:2]
+    _need(X, "X", torch.bfloat16, (m, q.k))
+    _need(A, "A", torch.bfloat16, (L, r, q.k))
+    _need(B, "B", torch.bfloat16, (L, q.n, r))
+    _need(s, "s", torch.float32, (L,))
+    _need(ids, "ids", torch.int32, (m,))
+    _same_device(X.device, q=q, A=A, B=B, s=s, ids=ids)
+    return m, L, r
+
+
+def qlora_multi_fwd(X: torch.Tensor, q: NF4Tensor, A: torch.Tensor, B: torch.Tensor, s: torch.Tensor,
+                    ids: torch.Tensor) -> Tuple[torch.Tensor, torch.Tensor]:
+    """(Y, T) of the layer whose row i has the adapter a = ids[i] of A [L, r, k], B [L, n, r] with the
+    scale s[a] (float32 [L]): Y_i = X_i deq(W)^T + s[a] T_i B_a^T, T_i = X_i A_a^T. ids int32 [m], in
+    any order; a row whose id lies outside [0, L) has no adapter (T_i = 0)."""
+    m, L, r = _multi_args(X, q, A, B, s, ids)
+    dev = X.device
+    Y = torch.empty(m, q.n, dtype=torch.bfloat16, device=dev)
+    T = torch.empty(m, r, dtype=torch.bfloat16, device=dev)
+    lib = library()
+    wsb = lib.qlora_multi_fwd_workspace_bytes(m, q.n, q.k, r, L)
+    ws = torch.empty(max(wsb, 1), dtype=torch.uint8, device=dev)
+    st = q.c_struct()
+    _check(lib.qlora_multi_fwd(_ptr(X), m, ctypes.byref(st), _ptr(A), _ptr(B), _ptr(s), _ptr(ids), L, r,
+                               _ptr(Y), _ptr(T), _ptr(ws), wsb, _stream(dev)))
+    return Y, T
+
+
+def qlora_multi_bwd(dY: torch.Tensor, X: torch.Tensor, q: NF4Tensor, A: torch.Tensor, B: torch.Tensor,
+                    s: torch.Tensor, ids: torch.Tensor, T: Optional[torch.Tensor], need_dx: bool = True):
+    """(dX, dA, dB) of qlora_multi_fwd for dY [m, n]; dX is None when need_dx is False, T None is
+    recomputed. dA [L, r, k] and dB [L, n, r] are zero for an adapter without rows."""
+    m, L, r = _multi_args(X, q, A, B, s, ids)
+    _need(dY, "dY", torch.bfloat16, (m, q.n))
+    if T is not None:
+        _need(T, "T", torch.bfloat16, (m, r))
+    dev = X.device
+    _same_device(dev, dY=dY, T=T)
+    dX = torch.empty(m, q.k, dtype=torch.bfloat16, device=dev) if need_dx else None
+    dA, dB = torch.empty_like(A), torch.empty_like(B)
+    lib = library()
+    wsb = lib.qlora_multi_bwd_workspace_bytes(m, q.n, q.k, r, L)
+    ws = torch.empty(max(wsb, 1), dtype=torch.uint8, device=dev)
+    st = q.c_struct()
+    _check(lib.qlora_multi_bwd(_ptr(dY), _ptr(X), m, ctypes.byref(st), _ptr(A), _ptr(B), _ptr(s), _ptr(ids), L, r,
+                               _ptr(T), _ptr(dX), _ptr(dA), _ptr(dB), _ptr(ws), wsb, _stream(dev)))
+    return dX, dA, dB
+
+
+def _dtype_code(t: torch.Tensor, name: str) -> int:
+    if t.dtype not in (torch.bfloat16, torch.float32):
+        raise ValueError(f"{name} must be bfloat16 or float32 (got {t.dtype})")
+    return NF4_F32 if t.dtype == torch.float32 else NF4_BF16
+
+
+def _heads(t: Optional[torch.Tensor], name: str, like: Optional[torch.Tensor] = None) -> _HeadsC:
+    """Descriptor of a [m, heads, d] tensor whose heads are contiguous (None: no heads)."""
+    if t is None:
+        return _HeadsC(None, 0, 0, 0)
+    if not t.is_cuda or t.dim() != 3:
+        raise ValueError(f"{name} must be a device tensor [m, heads, d]")
+    if like is not None and (t.shape != like.shape or t.dtype != like.dtype or t.device != like.device):
+        raise ValueError(f"{name} must match its input in shape, type and device")
+    if t.numel() and t.shape[2] > 1 and t.stride(2) != 1:
+        raise ValueError(f"{name} must have contiguous heads")
+    return _HeadsC(t.data_ptr(), t.stride(0), t.stride(1), t.shape[1])
+
+
+def _head_norm(q, k, wq, wk, cos, sin, pos, eps, interleaved, weight_offset) -> _HeadNormC:
+    x, w = (q, wq) if q is not None else (k, wk)
+    if x is None or w is None:
+        raise ValueError("q or k must be given, with its weight")
+    if x.dim() != 3:
+        raise ValueError("q and k must be [m, heads, d]")
+    m, _, d = x.shape
+    if q is not None and k is not None and (k.dim() != 3 or k.shape[0] != m or k.shape[2] != d or
+                                            k.dtype != q.dtype or k.device != q.device):
+        raise ValueError("q and k must agree in tokens, head size, type and device")
+    code, w_code = _dtype_code(x, "q and k"), _dtype_code(w, "the weights")
+    for t, wt, name in ((q, wq, "wq"), (k, wk, "wk")):
+        if t is not None:
+            _need(wt, name, w.dtype, (d,))
+    rot = 0
+    if cos is not None:
+        if pos is None or sin is None:
+            raise ValueError("cos, sin and pos come together")
+        if pos.dtype not in (torch.int32, torch.int64):
+            raise ValueError("pos must be int32 or int64")
+        rot = 2 * cos.shape[1]
+        _need(cos, "cos", torch.float32)
+        _need(sin, "sin", torch.float32, cos.shape)
+        _need(pos, "pos", pos.dtype, (m,))
+    _same_device(x.device, wq=wq if q is not None else None, wk=wk if k is not None else None,
+                 cos=cos, sin=sin if rot else None, pos=pos if rot else None)
+    return _HeadNormC(m, d, rot, int(interleaved), code, w_code, wq.data_ptr() if q is not None else None,
+                      wk.data_ptr() if k is not None else None, float(weight_offset), float(eps),
+                      cos.data_ptr() if rot else None, sin.data_ptr() if rot else None,
+                      cos.shape[0] if rot else 0, pos.data_ptr() if rot else None,
+                      int(rot and pos.dtype == torch.int64))
+
+
+def _out_like(t, out, name):
+    if t is None:
+        return None
+    if out is None:
+        return torch.empty(t.shape, dtype=t.dtype, device=t.device)
+    return out
+
+
+def qk_norm_rope_fwd(q: Optional[torch.Tensor], k: Optional[torch.Tensor], wq: Optional[torch.Tensor],
+                     wk: Optional[torch.Tensor], cos: Optional[torch.Tensor], sin: Optional[torch.Tensor],
+                     pos: Optional[torch.Tensor], eps: float = 1e-6, interleaved: bool = False,
+                     weight_offset: float = 0.0, out=(None, None)):
+    """(q', k'): every head of q [m, heads_q, d] and k [m, heads_k, d] (bfloat16 or float32, heads
+    contiguous, any other strides: slices of a packed projection) times 1 / sqrt(mean(x^2) + eps) and
+    wq / wk + weight_offset, its first rot = 2 * cos.shape[1] elements then rotated by the angles
+    cos, sin (float32 [places, rot/2]) of pos (int32 or int64 [m]): pairs (i, i + rot/2), or
+    (2i, 2i + 1) when interleaved. cos None: the norms alone. A token whose position lies outside the
+    table gets NaN. k (or q) may be None. out: tensors to write, the inputs themselves among them."""
+    p = _head_norm(q, k, wq, wk, cos, sin, pos, eps, interleaved, weight_offset)
+    qo, ko = _out_like(q, out[0], "q_out"), _out_like(k, out[1], "k_out")
+    dev = (q if q is not None else k).device
+    _check(library().qk_norm_rope_fwd(ctypes.byref(p), ctypes.byref(_heads(q, "q")), ctypes.byref(_heads(k, "k")),
+                                      ctypes.byref(_heads(qo, "q_out", q)), ctypes.byref(_heads(ko, "k_out", k)),
+                                      _stream(dev)))
+    return qo, ko
+
+
+def qk_norm_rope_bwd(gq: Optional[torch.Tensor], gk: Optional[torch.Tensor], q: Optional[torch.Tensor],
+                     k: Optional[torch.Tensor], wq: Optional[torch.Tensor], wk: Optional[torch.Tensor],
+                     cos: Optional[torch.Tensor], sin: Optional[torch.Tensor], pos: Optional[torch.Tensor],
+                     eps: float = 1e-6, interleaved: bool = False, weight_offset: float = 0.0,
+                     out=(None, None)):
+    """(dq, dk, dwq, dwk) of qk_norm_rope_fwd for the gradients gq, gk of its outputs; dwq and dwk are
+    float32 [d]. out: tensors for dq and dk (the slices of a packed gradient)."""
+    p = _head_norm(q, k, wq, wk, cos, sin, pos, eps, interleaved, weight_offset)
+    dq, dk = _out_like(q, out[0], "dq"), _out_like(k, out[1], "dk")
+    dev, d = (q if q is not None else k).device, int(p.d)
+    dwq = torch.empty(d, dtype=torch.float32, device=dev) if q is not None else None
+    dwk = torch.empty(d, dtype=torch.float32, device=dev) if k is not None else None
+    lib = library()
+    wsb = lib.qk_norm_rope_bwd_workspace_bytes(d)
+    ws = torch.empty(wsb, dtype=torch.uint8, device=dev)
+    if (gq is None) != (q is None) or (gk is None) != (k is None):
+        raise ValueError("gq and gk must be given for the inputs that are")
+    _check(lib.qk_norm_rope_bwd(ctypes.byref(p), ctypes.byref(_heads(gq, "gq", q)),
+                                ctypes.byref(_heads(gk, "gk", k)), ctypes.byref(_heads(q, "q")),
+                                ctypes.byref(_heads(k, "k")), ctypes.byref(_heads(dq, "dq", q)),
+                                ctypes.byref(_heads(dk, "dk", k)), _ptr(dwq), _ptr(dwk), _ptr(ws), wsb,
+                                _stream(dev)))
+    return dq, dk, dwq, dwk
+
+
+def _distill_args(logits, idx, teacher):
+    if logits.dim() != 2 or not logits.is_cuda:
+        raise ValueError("logits must be a device tensor [t, v]")
+    code = _dtype_code(logits, "logits")
+    t, v = logits.shape
+    if logits.numel() and v > 1 and logits.stride(1) != 1:
+        raise ValueError("logits must have contiguous rows")
+    if idx.dim() != 2:
+        raise ValueError("idx must be [t, top]")
+    _need(idx, "idx", torch.int32, (t, idx.shape[1]))
+    _need(teacher, "teacher", torch.float32, idx.shape)
+    _same_device(logits.device, idx=idx, teacher=teacher)
+    ld = logits.stride(0) if t > 1 else v
+    return code, t, v, ld, idx.shape[1]
+
+
+def _distill_out(logits, out):
+    if out is None:
+        return torch.empty(logits.shape, dtype=logits.dtype, device=logits.device)
+    if out.shape != logits.shape or out.dtype != logits.dtype or out.device != logits.device:
+        raise ValueError("out must match logits in shape, type and device")
+    if out.numel() and out.shape[1] > 1 and out.stride(1) != 1:
+        raise ValueError("out must have contiguous rows")
+    return out
+
+
+def distill_topk_fwd(logits: torch.Tensor, idx: torch.Tensor, teacher: torch.Tensor, tau: float):
+    """(loss, lse), float32 [t] each: the divergence of the student's softmax(logits / tau) from the
+    teacher's, softmax(teacher / tau) over its kept entries. logits bfloat16 or float32 [t, v] (rows
+    contiguous), idx int32 [t, top], teacher float32 [t, top]. An index outside [0, v) or a teacher
+    logit of -inf marks an entry that is not there; a row without entries has loss 0."""
+    code, t, v, ld, top = _distill_args(logits, idx, teacher)
+    loss = torch.empty(t, dtype=torch.float32, device=logits.device)
+    lse = torch.empty(t, dtype=torch.float32, device=logits.device)
+    _check(library().distill_topk_fwd(_ptr(logits), code, t, v, ld, _ptr(idx), _ptr(teacher), top, float(tau),
+                                      _ptr(loss), _ptr(lse), _stream(logits.device)))
+    return loss, lse
+
+
+def distill_topk_bwd(grad: torch.Tensor, logits: torch.Tensor, idx: torch.Tensor, teacher: torch.Tensor,
+                     tau: float, lse: torch.Tensor, out: Optional[torch.Tensor] = None) -> torch.Tensor:
+    """dlogits for the gradients grad (float32 [t]) of distill_topk_fwd's losses; out may be logits."""
+    code, t, v, ld, top = _distill_args(logits, idx, teacher)
+    _need(grad, "grad", torch.float32, (t,))
+    _need(lse, "lse", torch.float32, (t,))
+    _same_device(logits.device, grad=grad, lse=lse)
+    dz = _distill_out(logits, out)
+    _check(library().distill_topk_bwd(_ptr(logits), code, t, v, ld, _ptr(idx), _ptr(teacher), top, float(tau),
+                                      _ptr(lse), _ptr(grad), _ptr(dz), dz.stride(0) if t > 1 else v,
+                                      _stream(logits.device)))
+    return dz
+
+
+def distill_topk_step(logits: torch.Tensor, idx: torch.Tensor, teacher: torch.Tensor, tau: float,
+                      weight: Optional[torch.Tensor] = None, out: Optional[torch.Tensor] = None):
+    """(loss, dlogits) in one pass over the logits: loss float32 [t] as distill_topk_fwd (0 where the
+    weight is 0) and the gradient of sum(weight * loss), weight float32 [t] (None: all 1). out may be
+    logits."""
+    code, t, v, ld, top = _distill_args(logits, idx, teacher)
+    if weight is not None:
+        _need(weight, "weight", torch.float32, (t,))
+        _same_device(logits.device, weight=weight)
+    loss = torch.empty(t, dtype=torch.float32, device=logits.device)
+    dz = _distill_out(logits, out)
+    _check(library().distill_topk_step(_ptr(logits), code, t, v, ld, _ptr(idx), _ptr(teacher), top, float(tau),
+                                       _ptr(weight), _ptr(loss), _ptr(dz), dz.stride(0) if t > 1 else v,
+                                       _stream(logits.device)))
+    return loss, dz
+
+
 class QLoRALinearFunction(torch.autograd.Function):
     """Y = X deq(W)^T + s (X A^T) B^T with W frozen; gradients flow to X, A and B."""
 
@@ -585,3 +849,55 @@ class QLoRASwiGLUFunction(torch.autograd.Function):
         dX, dAgu, dBg, dBu = qlora_swiglu_bwd(dH.contiguous(), X, ctx.q, Agu, Bg, Bu, ctx.s, Ygu, Tgu,
                                               need_dx=ctx.needs_input_grad[0])
         return dX, None, dAgu, dBg, dBu, None
+
+
+class QLoRAMultiFunction(torch.autograd.Function):
+    """The layer with an adapter of its own for every row (qlora_multi_fwd), W and s fixed; gradients
+    flow to X, A and B."""
+
+    @staticmethod
+    def forward(ctx, X, q: NF4Tensor, A, B, s, ids):
+        Y, T = qlora_multi_fwd(X, q, A, B, s, ids)
+        ctx.q = q
+        ctx.save_for_backward(X, A, B, s, ids, T)
+        return Y
+
+    @staticmethod
+    def backward(ctx, dY):
+        X, A, B, s, ids, T = ctx.saved_tensors
+        dX, dA, dB = qlora_multi_bwd(dY.contiguous(), X, ctx.q, A, B, s, ids, T, need_dx=ctx.needs_input_grad[0])
+        return dX, None, dA, dB, None, None
+
+
+class QKNormRopeFunction(torch.autograd.Function):
+    """Head norms and rotation (qk_norm_rope_fwd); gradients flow to q, k, wq and wk."""
+
+    @staticmethod
+    def forward(ctx, q, k, wq, wk, cos, sin, pos, eps: float = 1e-6, interleaved: bool = False,
+                weight_offset: float = 0.0):
+        ctx.args = (eps, interleaved, weight_offset)
+        ctx.save_for_backward(q, k, wq, wk, cos, sin, pos)
+        return qk_norm_rope_fwd(q, k, wq, wk, cos, sin, pos, *ctx.args)
+
+    @staticmethod
+    def backward(ctx, gq, gk):
+        q, k, wq, wk, cos, sin, pos = ctx.saved_tensors
+        rows = lambda g: g if g.stride(2) == 1 else g.contiguous()
+        dq, dk, dwq, dwk = qk_norm_rope_bwd(rows(gq), rows(gk), q, k, wq, wk, cos, sin, pos, *ctx.args)
+        return dq, dk, dwq.to(wq.dtype), dwk.to(wk.dtype), None, None, None, None, None, None
+
+
+class DistillTopKFunction(torch.autograd.Function):
+    """The losses of distill_topk_fwd, float32 [t]; the gradient flows to the logits."""
+
+    @staticmethod
+    def forward(ctx, logits, idx, teacher, tau: float):
+        loss, lse = distill_topk_fwd(logits, idx, teacher, tau)
+        ctx.tau = tau
+        ctx.save_for_backward(logits, idx, teacher, lse)
+        return loss
+
+    @staticmethod
+    def backward(ctx, grad):
+        logits, idx, teacher, lse = ctx.saved_tensors
+        return distill_topk_bwd(grad.contiguous(), logits, idx, teacher, ctx.tau, lse), None, None, None

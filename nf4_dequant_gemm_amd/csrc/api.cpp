@@ -1036,3 +1036,357 @@ int qlora_bwd_dx(const void *dY, int64_t m, const nf4_tensor *W, const void *U, 
 }
 
 }  // extern "C"
+
+// ---------------------------------------------------------------- an adapter of its own for every row
+namespace {
+
+// Forward: the rows' order, then float partials of T. Backward: the rows' order, U [m, r], B
+// transposed [L, r, n], A transposed [L, k, r], T (recomputed when the caller passes none), then
+// float partials of the row projections or of the sums over rows (never both at once).
+struct MultiWs {
+  int sp_k = 1, sp_n = 1, sa = 1, sb = 1;
+  size_t plan = 0, u = 0, bt = 0, at = 0, t = 0, part = 0, total = 0;
+};
+
+MultiWs multi_ws(int64_t m, int64_t n, int64_t k, int32_t r, int32_t L, bool bwd) {
+  MultiWs w;
+  w.sp_k = nf4q::multi_rows_splits(m, k);
+  w.plan = align256(nf4q::multi_plan_bytes(m, L));
+  size_t p = w.sp_k > 1 ? (size_t)w.sp_k * m * r * 4 : 0;
+  if (bwd) {
+    w.sp_n = nf4q::multi_rows_splits(m, n);
+    w.sa = nf4q::multi_sum_splits(m, k, L);
+    w.sb = nf4q::multi_sum_splits(m, n, L);
+    w.u = w.t = align256((size_t)m * r * 2);
+    w.bt = align256((size_t)L * r * n * 2);
+    w.at = align256((size_t)L * r * k * 2);
+    if (w.sp_n > 1) p = std::max(p, (size_t)w.sp_n * m * r * 4);
+    if (w.sa > 1) p = std::max(p, (size_t)L * w.sa * r * k * 4);
+    if (w.sb > 1) p = std::max(p, (size_t)L * w.sb * r * n * 4);
+  }
+  w.part = align256(p);
+  w.total = w.plan + w.u + w.bt + w.at + w.t + w.part;
+  return w;
+}
+
+int check_multi_rest(const float *s, const int32_t *ids, const MultiWs &lay, void *ws, size_t ws_bytes) {
+  if (!s || !ids || (reinterpret_cast<uintptr_t>(s) & 3) || (reinterpret_cast<uintptr_t>(ids) & 3))
+    return fail(NF4_EINVAL, "s and ids must be non-NULL and 4-byte aligned");
+  if (ws_bytes < lay.total || !ws)
+    return fail(NF4_EINVAL, "workspace of %zu bytes is smaller than the %zu required", ws_bytes, lay.total);
+  if (!aligned16(ws)) return fail(NF4_EINVAL, "ws must be 16-byte aligned");
+  return NF4_OK;
+}
+
+int check_multi_shape(const void *X, int64_t m, const nf4_tensor *W, const void *A, const void *B, int32_t L,
+                      int32_t r) {
+  if (L < 1 || L > nf4q::kMultiMaxAdapters)
+    return fail(NF4_EINVAL, "L must lie in [1, %d] (got %d)", nf4q::kMultiMaxAdapters, L);
+  if (r < 1) return fail(NF4_EINVAL, "r must lie in [1, 128] (got %d)", r);
+  return check_layer(X, m, W, A, B, r);
+}
+
+nf4q::GemmArgs multi_gemm(const void *in, int64_t m, const nf4_tensor *W, int64_t C, int64_t R, void *out) {
+  nf4q::GemmArgs g;
+  g.a_side = (const uint16_t *)in;
+  g.lda = R;
+  g.lora_a = g.lora_b = nullptr;
+  g.w = desc(W);
+  g.M = m;
+  g.C = C;
+  g.R = R;
+  g.r = 0;
+  g.s = 0.f;
+  g.out = (uint16_t *)out;
+  g.ldo = C;
+  g.t = tables();
+  return g;
+}
+
+}  // namespace
+
+extern "C" {
+
+size_t qlora_multi_fwd_workspace_bytes(int64_t m, int64_t n, int64_t k, int32_t r, int32_t L) {
+  if (m < 1 || n < 1 || k < 1 || r < 1 || L < 1) return 0;
+  return multi_ws(m, n, k, r, L, false).total;
+}
+
+size_t qlora_multi_bwd_workspace_bytes(int64_t m, int64_t n, int64_t k, int32_t r, int32_t L) {
+  if (m < 1 || n < 1 || k < 1 || r < 1 || L < 1) return 0;
+  return multi_ws(m, n, k, r, L, true).total;
+}
+
+int qlora_multi_fwd(const void *X, int64_t m, const nf4_tensor *W, const void *A, const void *B,
+                    const float *s, const int32_t *ids, int32_t L, int32_t r, void *Y, void *T, void *ws,
+                    size_t ws_bytes, void *stream) {
+  int st = check_multi_shape(X, m, W, A, B, L, r);
+  if (st) return st;
+  if (!Y || !aligned16(Y) || !T || !aligned16(T))
+    return fail(NF4_EINVAL, "Y and T must be non-NULL and 16-byte aligned");
+  const int64_t n = W->n, k = W->k;
+  const MultiWs lay = multi_ws(m, n, k, r, L, false);
+  st = check_multi_rest(s, ids, lay, ws, ws_bytes);
+  if (st) return st;
+  hipStream_t sm = (hipStream_t)stream;
+  char *base = (char *)ws;
+  const nf4q::MultiPlan pl = nf4q::multi_plan_at(base, m, L);
+  hipError_t e = nf4q::launch_multi_plan(ids, m, L, pl, sm);
+  if (e != hipSuccess) return hip_status(e, "qlora_multi_fwd plan launch");
+  e = nf4q::launch_multi_rows((const uint16_t *)X, k, (const uint16_t *)A, (int64_t)r * k, k, m, k, r, L, lay.sp_k,
+                              (float *)(base + lay.plan), (uint16_t *)T, pl, sm);
+  if (e != hipSuccess) return hip_status(e, "qlora_multi_fwd T launch");
+  const nf4q::MultiArgs mu{ids, s, (const uint16_t *)T, (const uint16_t *)B, L, r};
+  return hip_status(nf4q::launch_gemm_fwd_multi(multi_gemm(X, m, W, n, k, Y), mu, sm), "qlora_multi_fwd launch");
+}
+
+int qlora_multi_bwd(const void *dY, const void *X, int64_t m, const nf4_tensor *W, const void *A,
+                    const void *B, const float *s, const int32_t *ids, int32_t L, int32_t r, const void *T,
+                    void *dX, void *dA, void *dB, void *ws, size_t ws_bytes, void *stream) {
+  int st = check_multi_shape(X, m, W, A, B, L, r);
+  if (st) return st;
+  if (!dY || !aligned16(dY)) return fail(NF4_EINVAL, "dY must be non-NULL and 16-byte aligned");
+  if ((dX && !aligned16(dX)) || (T && !aligned16(T))) return fail(NF4_EINVAL, "dX and T must be 16-byte aligned");
+  if (!dA || !aligned16(dA) || !dB || !aligned16(dB))
+    return fail(NF4_EINVAL, "dA and dB must be non-NULL and 16-byte aligned");
+  const int64_t n = W->n, k = W->k;
+  const MultiWs lay = multi_ws(m, n, k, r, L, true);
+  st = check_multi_rest(s, ids, lay, ws, ws_bytes);
+  if (st) return st;
+  hipStream_t sm = (hipStream_t)stream;
+  char *base = (char *)ws;
+  const nf4q::MultiPlan pl = nf4q::multi_plan_at(base, m, L);
+  uint16_t *U = (uint16_t *)(base + lay.plan);
+  uint16_t *Bt = (uint16_t *)(base + lay.plan + lay.u);
+  uint16_t *At = (uint16_t *)(base + lay.plan + lay.u + lay.bt);
+  uint16_t *Tw = (uint16_t *)(base + lay.plan + lay.u + lay.bt + lay.at);
+  float *part = (float *)(base + lay.plan + lay.u + lay.bt + lay.at + lay.t);
+  const uint16_t *dy = (const uint16_t *)dY, *x = (const uint16_t *)X;
+  hipError_t e = nf4q::launch_multi_plan(ids, m, L, pl, sm);
+  if (e != hipSuccess) return hip_status(e, "qlora_multi_bwd plan launch");
+  if (!T) {
+    e = nf4q::launch_multi_rows(x, k, (const uint16_t *)A, (int64_t)r * k, k, m, k, r, L, lay.sp_k, part, Tw, pl, sm);
+    if (e != hipSuccess) return hip_status(e, "qlora_multi_bwd T launch");
+    T = Tw;
+  }
+  e = nf4q::launch_multi_transpose((const uint16_t *)B, n, r, L, Bt, sm);
+  if (e != hipSuccess) return hip_status(e, "qlora_multi_bwd transpose launch");
+  e = nf4q::launch_multi_rows(dy, n, Bt, (int64_t)r * n, n, m, n, r, L, lay.sp_n, part, U, pl, sm);
+  if (e != hipSuccess) return hip_status(e, "qlora_multi_bwd U launch");
+  if (dX) {
+    e = nf4q::launch_multi_transpose((const uint16_t *)A, r, k, L, At, sm);
+    if (e != hipSuccess) return hip_status(e, "qlora_multi_bwd transpose launch");
+    const nf4q::MultiArgs mu{ids, s, U, At, L, r};
+    e = nf4q::launch_gemm_dx_multi(multi_gemm(dY, m, W, k, n, dX), mu, sm);
+    if (e != hipSuccess) return hip_status(e, "qlora_multi_bwd dX launch");
+  }
+  e = nf4q::launch_multi_sum(U, x, k, k, r, L, s, lay.sa, part, (uint16_t *)dA, false, pl, sm);
+  if (e != hipSuccess) return hip_status(e, "qlora_multi_bwd dA launch");
+  e = nf4q::launch_multi_sum((const uint16_t *)T, dy, n, n, r, L, s, lay.sb, part, (uint16_t *)dB, true, pl, sm);
+  return hip_status(e, "qlora_multi_bwd dB launch");
+}
+
+}  // extern "C"
+
+// ---------------------------------------------------------------- norm and rotation of heads
+namespace {
+
+int check_heads(const nf4_heads *h, const char *name, int32_t heads, size_t esz, int64_t tokens) {
+  if (!h || h->heads != heads) return fail(NF4_EINVAL, "%s must be given, with as many heads as its input", name);
+  if (heads == 0 || tokens == 0) return NF4_OK;
+  if (!h->data) return fail(NF4_EINVAL, "%s data is NULL", name);
+  if (reinterpret_cast<uintptr_t>(h->data) % esz) return fail(NF4_EINVAL, "%s is not aligned to its elements", name);
+  if (h->token_stride < 0 || h->head_stride < 0) return fail(NF4_EINVAL, "%s has a negative stride", name);
+  return NF4_OK;
+}
+
+int check_head_norm(const nf4_head_norm *p, const nf4_heads *q, const nf4_heads *k, size_t *esz) {
+  if (!p || !q || !k) return fail(NF4_EINVAL, "the descriptor, q and k must be non-NULL");
+  if (p->tokens < 0) return fail(NF4_EINVAL, "tokens must be >= 0 (got %lld)", (long long)p->tokens);
+  if ((p->dtype != NF4_BF16 && p->dtype != NF4_F32) || (p->w_dtype != NF4_BF16 && p->w_dtype != NF4_F32))
+    return fail(NF4_EINVAL, "unknown dtype %d or w_dtype %d", p->dtype, p->w_dtype);
+  if (p->d < 2 || p->d > 512 || (p->d & 1)) return fail(NF4_EUNSUPPORTED, "d must be even, 2 .. 512 (got %d)", p->d);
+  if (p->rot < 0 || p->rot > p->d || (p->rot & 1))
+    return fail(NF4_EUNSUPPORTED, "rot must be even, 0 .. d (got %d)", p->rot);
+  if (q->heads < 0 || k->heads < 0) return fail(NF4_EINVAL, "negative head count");
+  const int64_t heads = (int64_t)q->heads + k->heads;
+  if (heads == 0) return fail(NF4_EINVAL, "q and k have no heads");
+  if (p->tokens > ((int64_t(1) << 31) - 1) / heads) return fail(NF4_EUNSUPPORTED, "tokens * heads must be below 2^31");
+  if (!(p->eps >= 0.f)) return fail(NF4_EINVAL, "eps must be >= 0");
+  *esz = p->dtype == NF4_F32 ? 4 : 2;
+  const size_t wsz = p->w_dtype == NF4_F32 ? 4 : 2;
+  if ((q->heads && (!p->wq || reinterpret_cast<uintptr_t>(p->wq) % wsz)) ||
+      (k->heads && (!p->wk || reinterpret_cast<uintptr_t>(p->wk) % wsz)))
+    return fail(NF4_EINVAL, "wq and wk must be non-NULL and aligned to their elements");
+  if (p->rot > 0 && p->tokens > 0) {
+    if (!p->cos || !p->sin || !p->pos || p->places < 1)
+      return fail(NF4_EINVAL, "cos, sin and pos must be non-NULL and places >= 1 when rot > 0");
+    if (((reinterpret_cast<uintptr_t>(p->cos) | reinterpret_cast<uintptr_t>(p->sin)) & 3) ||
+        reinterpret_cast<uintptr_t>(p->pos) % (p->pos64 ? 8 : 4))
+      return fail(NF4_EINVAL, "cos, sin and pos must be aligned to their elements");
+  }
+  int st = check_heads(q, "q", q->heads, *esz, p->tokens);
+  return st ? st : check_heads(k, "k", k->heads, *esz, p->tokens);
+}
+
+nf4q::HeadSide head_side(const nf4_heads *x, const nf4_heads *y, const nf4_heads *g, const void *w) {
+  nf4q::HeadSide h;
+  h.heads = x->heads;
+  if (!h.heads) return h;
+  h.x = x->data;
+  h.x_ts = x->token_stride;
+  h.x_hs = x->head_stride;
+  h.y = y->data;
+  h.y_ts = y->token_stride;
+  h.y_hs = y->head_stride;
+  if (g) {
+    h.g = g->data;
+    h.g_ts = g->token_stride;
+    h.g_hs = g->head_stride;
+  }
+  h.w = w;
+  return h;
+}
+
+nf4q::HeadArgs head_args(const nf4_head_norm *p) {
+  nf4q::HeadArgs a;
+  a.m = p->tokens;
+  a.d = p->d;
+  a.rot = p->rot;
+  a.w_f32 = p->w_dtype == NF4_F32;
+  a.pos64 = p->pos64 != 0;
+  a.w_offset = p->w_offset;
+  a.eps = p->eps;
+  a.cos = p->cos;
+  a.sin = p->sin;
+  a.places = p->places;
+  a.pos = p->pos;
+  return a;
+}
+
+}  // namespace
+
+extern "C" {
+
+int qk_norm_rope_fwd(const nf4_head_norm *p, const nf4_heads *q, const nf4_heads *k,
+                     const nf4_heads *q_out, const nf4_heads *k_out, void *stream) {
+  size_t esz = 0;
+  int st = check_head_norm(p, q, k, &esz);
+  if (st) return st;
+  if ((st = check_heads(q_out, "q_out", q->heads, esz, p->tokens))) return st;
+  if ((st = check_heads(k_out, "k_out", k->heads, esz, p->tokens))) return st;
+  if (p->tokens == 0) return ok();
+  nf4q::HeadArgs a = head_args(p);
+  a.q = head_side(q, q_out, nullptr, p->wq);
+  a.k = head_side(k, k_out, nullptr, p->wk);
+  return hip_status(nf4q::launch_head_norm(a, p->dtype == NF4_F32, p->interleaved != 0, false, nullptr, nullptr,
+                                           (hipStream_t)stream),
+                    "qk_norm_rope_fwd launch");
+}
+
+size_t qk_norm_rope_bwd_workspace_bytes(int32_t d) {
+  return d < 1 ? 0 : align256((size_t)nf4q::head_norm_max_blocks() * d * 4);
+}
+
+int qk_norm_rope_bwd(const nf4_head_norm *p, const nf4_heads *gq, const nf4_heads *gk, const nf4_heads *q,
+                     const nf4_heads *k, const nf4_heads *dq, const nf4_heads *dk, float *dwq, float *dwk,
+                     void *ws, size_t ws_bytes, void *stream) {
+  size_t esz = 0;
+  int st = check_head_norm(p, q, k, &esz);
+  if (st) return st;
+  if ((st = check_heads(gq, "gq", q->heads, esz, p->tokens))) return st;
+  if ((st = check_heads(gk, "gk", k->heads, esz, p->tokens))) return st;
+  if ((st = check_heads(dq, "dq", q->heads, esz, p->tokens))) return st;
+  if ((st = check_heads(dk, "dk", k->heads, esz, p->tokens))) return st;
+  if ((reinterpret_cast<uintptr_t>(dwq) | reinterpret_cast<uintptr_t>(dwk)) & 3)
+    return fail(NF4_EINVAL, "dwq and dwk must be 4-byte aligned");
+  const size_t need = qk_norm_rope_bwd_workspace_bytes(p->d);
+  if (ws_bytes < need || !ws)
+    return fail(NF4_EINVAL, "workspace of %zu bytes is smaller than the %zu required", ws_bytes, need);
+  if (!aligned16(ws)) return fail(NF4_EINVAL, "ws must be 16-byte aligned");
+  nf4q::HeadArgs a = head_args(p);
+  a.q = head_side(q, dq, gq, p->wq);
+  a.k = head_side(k, dk, gk, p->wk);
+  a.part = (float *)ws;
+  return hip_status(nf4q::launch_head_norm(a, p->dtype == NF4_F32, p->interleaved != 0, true, dwq, dwk,
+                                           (hipStream_t)stream),
+                    "qk_norm_rope_bwd launch");
+}
+
+}  // extern "C"
+
+// ---------------------------------------------------------------- distillation
+namespace {
+
+int check_distill(const void *logits, int dtype, int64_t t, int64_t v, int64_t ld, const int32_t *idx,
+                  const float *teacher, int32_t top, float tau) {
+  if (dtype != NF4_BF16 && dtype != NF4_F32) return fail(NF4_EINVAL, "unknown dtype %d", dtype);
+  if (t < 0) return fail(NF4_EINVAL, "t must be >= 0 (got %lld)", (long long)t);
+  if (v < 1) return fail(NF4_EINVAL, "v must be >= 1 (got %lld)", (long long)v);
+  if (t >= (int64_t(1) << 31) || v >= (int64_t(1) << 30))
+    return fail(NF4_EUNSUPPORTED, "t must be below 2^31 and v below 2^30");
+  if (top < 1 || top > nf4q::kDistillMaxTop)
+    return fail(NF4_EINVAL, "top must lie in [1, %d] (got %d)", nf4q::kDistillMaxTop, top);
+  if (!(tau > 0.f) || !std::isfinite(tau) || !std::isfinite(1.f / tau))
+    return fail(NF4_EINVAL, "tau must be positive, it and its inverse finite");
+  if (ld < v) return fail(NF4_EINVAL, "ld must be >= v (got %lld)", (long long)ld);
+  if (t == 0) return NF4_OK;
+  if (!logits || !idx || !teacher) return fail(NF4_EINVAL, "logits, idx and teacher must be non-NULL");
+  const size_t esz = dtype == NF4_F32 ? 4 : 2;
+  if (reinterpret_cast<uintptr_t>(logits) % esz ||
+      ((reinterpret_cast<uintptr_t>(idx) | reinterpret_cast<uintptr_t>(teacher)) & 3))
+    return fail(NF4_EINVAL, "logits, idx and teacher must be aligned to their elements");
+  return NF4_OK;
+}
+
+int check_dlogits(const void *dlogits, int dtype, int64_t t, int64_t v, int64_t ldd) {
+  if (ldd < v) return fail(NF4_EINVAL, "ldd must be >= v (got %lld)", (long long)ldd);
+  if (t && (!dlogits || reinterpret_cast<uintptr_t>(dlogits) % (dtype == NF4_F32 ? 4 : 2)))
+    return fail(NF4_EINVAL, "dlogits must be non-NULL and aligned to its elements");
+  return NF4_OK;
+}
+
+bool words(const void *p) { return (reinterpret_cast<uintptr_t>(p) & 3) == 0; }
+
+}  // namespace
+
+extern "C" {
+
+int distill_topk_fwd(const void *logits, int dtype, int64_t t, int64_t v, int64_t ld, const int32_t *idx,
+                     const float *teacher, int32_t top, float tau, float *loss, float *lse, void *stream) {
+  int st = check_distill(logits, dtype, t, v, ld, idx, teacher, top, tau);
+  if (st) return st;
+  if (t && !loss) return fail(NF4_EINVAL, "loss is NULL");
+  if (!words(loss) || !words(lse)) return fail(NF4_EINVAL, "loss and lse must be 4-byte aligned");
+  if (t == 0) return ok();
+  const nf4q::DistillArgs a{logits, t, v, ld, idx, teacher, top, tau, nullptr, nullptr, loss, lse, nullptr, 0};
+  return hip_status(nf4q::launch_distill(a, dtype == NF4_F32, (hipStream_t)stream), "distill_topk_fwd launch");
+}
+
+int distill_topk_bwd(const void *logits, int dtype, int64_t t, int64_t v, int64_t ld, const int32_t *idx,
+                     const float *teacher, int32_t top, float tau, const float *lse, const float *grad,
+                     void *dlogits, int64_t ldd, void *stream) {
+  int st = check_distill(logits, dtype, t, v, ld, idx, teacher, top, tau);
+  if (!st) st = check_dlogits(dlogits, dtype, t, v, ldd);
+  if (st) return st;
+  if (t && (!lse || !grad)) return fail(NF4_EINVAL, "lse and grad must be non-NULL");
+  if (!words(lse) || !words(grad)) return fail(NF4_EINVAL, "lse and grad must be 4-byte aligned");
+  if (t == 0) return ok();
+  const nf4q::DistillArgs a{logits, t, v, ld, idx, teacher, top, tau, grad, lse, nullptr, nullptr, dlogits, ldd};
+  return hip_status(nf4q::launch_distill(a, dtype == NF4_F32, (hipStream_t)stream), "distill_topk_bwd launch");
+}
+
+int distill_topk_step(const void *logits, int dtype, int64_t t, int64_t v, int64_t ld, const int32_t *idx,
+                      const float *teacher, int32_t top, float tau, const float *weight, float *loss,
+                      void *dlogits, int64_t ldd, void *stream) {
+  int st = check_distill(logits, dtype, t, v, ld, idx, teacher, top, tau);
+  if (!st) st = check_dlogits(dlogits, dtype, t, v, ldd);
+  if (st) return st;
+  if (t && !loss) return fail(NF4_EINVAL, "loss is NULL");
+  if (!words(weight) || !words(loss)) return fail(NF4_EINVAL, "weight and loss must be 4-byte aligned");
+  if (t == 0) return ok();
+  const nf4q::DistillArgs a{logits, t, v, ld, idx, teacher, top, tau, weight, nullptr, loss, nullptr, dlogits, ldd};
+  return hip_status(nf4q::launch_distill(a, dtype == NF4_F32, (hipStream_t)stream), "distill_topk_step launch");
+}
+
+}  // extern "C"

@@ -37,6 +37,7 @@
 // Generation of Hardware"] (template parameters of dx_body).
 #include "common.h"
 #include "launch.h"
+#include "multi.h"
 
 namespace nf4q {
 namespace {
@@ -158,8 +159,11 @@ __device__ __forceinline__ void dx_origin(int64_t m_lo, int64_t m_hi, int tiles_
   k0 = (int64_t)(gin / gm) * kT;
 }
 
-template <int kFmt, bool kGrp>
-__device__ __forceinline__ void dx_body(const GemmArgs &g, const GroupArgs &gr) {
+// kMulti: the rows have adapters of their own (mu; g.r is 0): after the reduction, each wave adds the
+// low-rank term of its block from the transposed adapters, straight from registers (multi_term,
+// multi.h).
+template <int kFmt, bool kGrp, bool kMulti = false>
+__device__ __forceinline__ void dx_body(const GemmArgs &g, const GroupArgs &gr, const MultiArgs &mu) {
   constexpr bool kDQ = kFmt == 1, kFP4 = kFmt == 2;
   // separate LDS arrays per buffer: the compiler then knows that accesses to one do not alias
   // the DMA in flight into another (one array of two would make it wait for the DMA)
@@ -476,7 +480,17 @@ __device__ __forceinline__ void dx_body(const GemmArgs &g, const GroupArgs &gr) 
     uint4 *blk = (wave >> 1) == 0 ? sY0 : (wave >> 1) == 1 ? sY1 : (wave >> 1) == 2 ? sW0 : sW1;
     blk += (wave & 1) * (kYChunks / 2);
     uint2 *b2 = reinterpret_cast<uint2 *>(blk);
-    const float tsc = kFP4 ? tscale() : 1.f;
+    float tsc = kFP4 ? tscale() : 1.f;
+    if constexpr (kMulti) {   // E2M1: the sums leave the units of the tensor scale first
+      if (kFP4) {
+#pragma unroll
+        for (int kt = 0; kt < 4; ++kt)
+#pragma unroll
+          for (int mt = 0; mt < 8; ++mt) acc[kt][mt] *= tsc;
+        tsc = 1.f;
+      }
+      multi_term<4, 8>(acc, mu, m0 + wm * 128, m_hi, k0 + wk * 64, g.C);
+    }
 #pragma unroll
     for (int kt = 0; kt < 4; ++kt)
 #pragma unroll
@@ -503,11 +517,15 @@ __device__ __forceinline__ void dx_body(const GemmArgs &g, const GroupArgs &gr) 
 
 template <int kFmt>
 __global__ __launch_bounds__(kThreads) void dx_fused_kernel(GemmArgs g) {
-  dx_body<kFmt, false>(g, GroupArgs{});
+  dx_body<kFmt, false>(g, GroupArgs{}, MultiArgs{});
 }
 template <int kFmt>
 __global__ __launch_bounds__(kThreads) void dx_grouped_kernel(GemmArgs g, GroupArgs gr) {
-  dx_body<kFmt, true>(g, gr);
+  dx_body<kFmt, true>(g, gr, MultiArgs{});
+}
+template <int kFmt>
+__global__ __launch_bounds__(kThreads) void dx_multi_kernel(GemmArgs g, MultiArgs mu) {
+  dx_body<kFmt, false, true>(g, GroupArgs{}, mu);
 }
 
 // The split tiles of a grouped dX launch: workgroups 4 i .. 4 i + 3 add the S float32 pieces of
@@ -588,6 +606,19 @@ hipError_t launch_gemm_dx_grouped(const GemmArgs &g, const GroupArgs &gr, hipStr
     else
       dx_tail_kernel<0><<<dim3((unsigned)tail_grid), dim3(kThreads), 0, st>>>(g, gr);
   }
+  return hipGetLastError();
+}
+
+hipError_t launch_gemm_dx_multi(const GemmArgs &g, const MultiArgs &mu, hipStream_t st) {
+  if (((g.C | g.ldo) & 7) != 0 || (reinterpret_cast<uintptr_t>(g.out) & 15) != 0 || g.R != g.w.n || g.r != 0)
+    return hipErrorInvalidValue;
+  const int64_t tiles = ((g.C + kT - 1) / kT) * ((g.M + kT - 1) / kT);
+  if (g.w.fp4)
+    dx_multi_kernel<2><<<dim3((unsigned)tiles), dim3(kThreads), 0, st>>>(g, mu);
+  else if (g.w.dq)
+    dx_multi_kernel<1><<<dim3((unsigned)tiles), dim3(kThreads), 0, st>>>(g, mu);
+  else
+    dx_multi_kernel<0><<<dim3((unsigned)tiles), dim3(kThreads), 0, st>>>(g, mu);
   return hipGetLastError();
 }
 

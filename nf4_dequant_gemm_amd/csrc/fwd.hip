@@ -41,6 +41,7 @@
 // "NVFP4: A Quantization Format for the Next Generation of Hardware"].
 #include "common.h"
 #include "launch.h"
+#include "multi.h"
 
 namespace nf4q {
 namespace {
@@ -223,8 +224,10 @@ __device__ void stage_lora_pair(const GemmArgs &g, float sb, int64_t m0, int64_t
 // columns of the same indices (weight rows N + n0 .., Bu rows n0 ..),
 // so the epilogue holds Yg and Yu of the same columns: it writes both to g.out ([M, 2N], gate then
 // up) and H = silu(Yg) * Yu, from their float32 sums, to g.hout ([M, N], row stride g.ldh).
-template <int kFmt, bool kGrp, bool kPair = false>
-__device__ __forceinline__ void fwd_body(const GemmArgs &g, const GroupArgs &gr) {
+// kMulti: the rows have adapters of their own (mu; g.r is 0): after the walk over K, each wave adds
+// the low-rank term of its block straight from registers (multi_term, multi.h).
+template <int kFmt, bool kGrp, bool kPair = false, bool kMulti = false>
+__device__ __forceinline__ void fwd_body(const GemmArgs &g, const GroupArgs &gr, const MultiArgs &mu) {
   constexpr bool kDQ = kFmt == 1, kFP4 = kFmt == 2;
   constexpr int kTN = kPair ? kT / 2 : kT;   // columns of each output a tile advances by
   // X and W tiles as separate arrays: the compiler then knows that LDS accesses to one do not
@@ -524,6 +527,7 @@ __device__ __forceinline__ void fwd_body(const GemmArgs &g, const GroupArgs &gr)
 #pragma unroll
       for (int mt = 0; mt < 8; ++mt) acc[nt][mt] *= tsc;
   }
+  if constexpr (kMulti) multi_term<4, 8>(acc, mu, m0 + wm * 128, m_hi, n0 + wn * 64, g.C);
   uint4 *blk = (wave >> 1) == 0 ? sX0 : (wave >> 1) == 1 ? sX1 : (wave >> 1) == 2 ? sW0 : sW1;
   blk += (wave & 1) * (kChunks / 2);
   uint2 *b2 = reinterpret_cast<uint2 *>(blk);
@@ -606,17 +610,22 @@ __device__ __forceinline__ void fwd_body(const GemmArgs &g, const GroupArgs &gr)
 
 template <int kFmt>
 __global__ __launch_bounds__(kThreads) void fwd_fused_kernel(GemmArgs g) {
-  fwd_body<kFmt, false>(g, GroupArgs{});
+  fwd_body<kFmt, false>(g, GroupArgs{}, MultiArgs{});
 }
 
 template <int kFmt>
 __global__ __launch_bounds__(kThreads) void fwd_grouped_kernel(GemmArgs g, GroupArgs gr) {
-  fwd_body<kFmt, true>(g, gr);
+  fwd_body<kFmt, true>(g, gr, MultiArgs{});
 }
 
 template <int kFmt>
 __global__ __launch_bounds__(kThreads) void fwd_pair_kernel(GemmArgs g) {
-  fwd_body<kFmt, false, true>(g, GroupArgs{});
+  fwd_body<kFmt, false, true>(g, GroupArgs{}, MultiArgs{});
+}
+
+template <int kFmt>
+__global__ __launch_bounds__(kThreads) void fwd_multi_kernel(GemmArgs g, MultiArgs mu) {
+  fwd_body<kFmt, false, false, true>(g, GroupArgs{}, mu);
 }
 
 }  // namespace
@@ -631,6 +640,19 @@ hipError_t launch_gemm_fwd(const GemmArgs &g, hipStream_t st) {
     fwd_fused_kernel<1><<<dim3((unsigned)tiles), dim3(kThreads), 0, st>>>(g);
   else
     fwd_fused_kernel<0><<<dim3((unsigned)tiles), dim3(kThreads), 0, st>>>(g);
+  return hipGetLastError();
+}
+
+hipError_t launch_gemm_fwd_multi(const GemmArgs &g, const MultiArgs &mu, hipStream_t st) {
+  if (((g.C | g.ldo) & 7) != 0 || (reinterpret_cast<uintptr_t>(g.out) & 15) != 0 || g.r != 0)
+    return hipErrorInvalidValue;
+  const int64_t tiles = ((g.C + kT - 1) / kT) * ((g.M + kT - 1) / kT);
+  if (g.w.fp4)
+    fwd_multi_kernel<2><<<dim3((unsigned)tiles), dim3(kThreads), 0, st>>>(g, mu);
+  else if (g.w.dq)
+    fwd_multi_kernel<1><<<dim3((unsigned)tiles), dim3(kThreads), 0, st>>>(g, mu);
+  else
+    fwd_multi_kernel<0><<<dim3((unsigned)tiles), dim3(kThreads), 0, st>>>(g, mu);
   return hipGetLastError();
 }
 

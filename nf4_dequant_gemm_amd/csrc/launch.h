@@ -5,6 +5,7 @@
 #include <stdint.h>
 
 #include "common.h"
+#include "multi.h"
 
 namespace nf4q {
 
@@ -207,5 +208,68 @@ hipError_t launch_diagblocks(const uint16_t *db2, int64_t n, int r, uint16_t *db
 // LoRA merge (merge.hip): out bf16 [n, k] = bf16(deq(W) + s B A), 0 <= r <= 128, k % 64 == 0.
 hipError_t launch_merge(const WDesc &w, const uint16_t *A, const uint16_t *B, int r, float s,
                         const Tables &t, uint16_t *out, hipStream_t st);
+
+// The layer with an adapter of its own for every row (multi.h). Forward: g.r 0, mu.P = T, mu.Q = B
+// [L][N][r]; dX: mu.P = U, mu.Q = A transposed [L][K][r].
+hipError_t launch_gemm_fwd_multi(const GemmArgs &g, const MultiArgs &mu, hipStream_t st);
+hipError_t launch_gemm_dx_multi(const GemmArgs &g, const MultiArgs &mu, hipStream_t st);
+// The rows' order, and the thin products over it (multi.hip): out[i] = in[i] p_a^T for the rows i of
+// adapter a (zero without one), p_a = p + a * pstride of r rows of leading dimension ldp, with
+// splits * M * r partial floats; and out[a] = s[a] * (sum over its rows of P_i^T Q_i), [r][C] or
+// transposed [C][r], with L * splits * r * C partial floats (none for one split).
+hipError_t launch_multi_plan(const int32_t *ids, int64_t M, int L, const MultiPlan &pl, hipStream_t st);
+int multi_rows_splits(int64_t M, int64_t Lr);
+hipError_t launch_multi_rows(const uint16_t *in, int64_t ldin, const uint16_t *p, int64_t pstride, int64_t ldp,
+                             int64_t M, int64_t Lr, int r, int L, int splits, float *part, uint16_t *out,
+                             const MultiPlan &pl, hipStream_t st);
+int multi_sum_splits(int64_t M, int64_t C, int L);
+hipError_t launch_multi_sum(const uint16_t *P, const uint16_t *Q, int64_t ldq, int64_t C, int r, int L,
+                            const float *s, int splits, float *part, uint16_t *out, bool transposed,
+                            const MultiPlan &pl, hipStream_t st);
+// dst[b][c][j] = src[b][j][c] of `batch` bf16 matrices [R][C].
+hipError_t launch_multi_transpose(const uint16_t *src, int64_t R, int64_t C, int batch, uint16_t *dst, hipStream_t st);
+
+// Norm and rotation of query and key heads (headnorm.hip). One side (q or k): element strides of a
+// token (ts) and a head (hs), the d elements of a head contiguous; heads == 0: no such side.
+struct HeadSide {
+  const void *x = nullptr;
+  void *y = nullptr;         // forward: the output; backward: dx
+  const void *g = nullptr;   // backward: the gradient of the output
+  const void *w = nullptr;
+  int64_t x_ts = 0, x_hs = 0, y_ts = 0, y_hs = 0, g_ts = 0, g_hs = 0;
+  int heads = 0;
+};
+struct HeadArgs {
+  HeadSide q, k;
+  int64_t m;                 // tokens; m * (q.heads + k.heads) < 2^31
+  int d, rot;                // 2 <= d <= 512, both even, 0 <= rot <= d
+  bool w_f32, pos64;
+  float w_offset, eps;
+  const float *cos, *sin;    // [places][rot / 2]
+  int64_t places;
+  const void *pos;           // int32 or int64 [m]
+  float *part = nullptr;     // backward: head_norm_max_blocks() * d floats
+  int lanes = 0, blocks_q = 0;   // set by launch_head_norm
+};
+hipError_t launch_head_norm(HeadArgs a, bool f32, bool inter, bool bwd, float *dwq, float *dwk,
+                            hipStream_t st);
+int head_norm_max_blocks();
+
+// Distillation from a teacher's top logits (distill.hip).
+struct DistillArgs {
+  const void *z;             // student logits [t][v], row stride ld
+  int64_t t, v, ld;
+  const int32_t *idx;        // [t][top]
+  const float *teacher;      // [t][top]
+  int top;                   // <= kDistillMaxTop
+  float tau;
+  const float *weight;       // [t] or NULL (all 1): with dz
+  const float *lse_in;       // [t]: the rows' log-sum-exp, known (backward alone)
+  float *loss, *lse;         // [t] or NULL
+  void *dz;                  // [t][v], row stride ldd, or NULL; may be z
+  int64_t ldd;
+};
+constexpr int kDistillMaxTop = 1024;
+hipError_t launch_distill(const DistillArgs &a, bool f32, hipStream_t st);
 
 }  // namespace nf4q

@@ -1,0 +1,573 @@
+// Thin products of the layer with an adapter of its own for every row (gfx950, bf16 MFMA): the rows'
+// order, T = X A_a^T and U = dY B_a, dA_a = s_a U^T X and dB_a = s_a dY^T T over the rows of adapter
+// a, and the transposes they and dX take. The low-rank term of Y and dX is part of the fused kernels
+// (multi.h).
+//
+// Rows are not moved: a table holds them in the order of their adapters and the kernels gather
+// through it, so that every 16- or 64-row block has one adapter, whose factor is read once for the
+// block. Sums over rows are split into float32 parts that are added in a fixed order.
+#include "launch.h"
+#include "multi.h"
+
+namespace nf4q {
+namespace {
+
+// ------------------------------------------------------------------------------------ row order
+// One workgroup: a stable counting sort of the rows by adapter. Wave w counts its run of rows in LDS,
+// the counts are scanned over adapters and waves, and each wave then places its rows in order,
+// ranking the lanes of equal adapter by a ballot.
+constexpr int kPlanThreads = 1024, kPlanWaves = kPlanThreads / 64;
+
+__global__ __launch_bounds__(kPlanThreads) void multi_plan_kernel(const int32_t *__restrict__ ids, int64_t M,
+                                                                  int L, MultiPlan pl) {
+  extern __shared__ int32_t cnt[];   // [kPlanWaves][L + 1]
+  __shared__ int32_t scan[3][kPlanThreads];
+  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+  const int G = L + 1;
+  for (int i = tid; i < kPlanWaves * G; i += kPlanThreads) cnt[i] = 0;
+  __syncthreads();
+  const int64_t per = ((M + kPlanWaves - 1) / kPlanWaves + 63) / 64 * 64;
+  const int64_t lo = wave * per, hi = lo + per < M ? lo + per : M;
+  volatile int32_t *mine = cnt + wave * G;   // written by one lane, read by the others of its wave
+  auto group = [&](int64_t i) {
+    const int a = ids[i];
+    return a >= 0 && a < L ? a : L;
+  };
+  for (int64_t i = lo + lane; i < hi; i += 64) atomicAdd(&cnt[wave * G + group(i)], 1);
+  __syncthreads();
+  // adapter g = thread g: its rows, and blocks of 16 and 64; inclusive scans over the adapters
+  int32_t n = 0;
+  if (tid < L)
+    for (int w = 0; w < kPlanWaves; ++w) n += cnt[w * G + tid];
+  int32_t v[3] = {n, (n + 15) / 16, (n + 63) / 64};
+  const int32_t own[3] = {v[0], v[1], v[2]};
+#pragma unroll
+  for (int q = 0; q < 3; ++q) scan[q][tid] = v[q];
+  __syncthreads();
+  for (int o = 1; o < L; o <<= 1) {
+#pragma unroll
+    for (int q = 0; q < 3; ++q) v[q] = tid >= o ? scan[q][tid - o] : 0;
+    __syncthreads();
+#pragma unroll
+    for (int q = 0; q < 3; ++q) scan[q][tid] += v[q];
+    __syncthreads();
+  }
+  int32_t *out[3] = {pl.off, pl.blk16, pl.blk64};
+  if (tid < L) {
+#pragma unroll
+    for (int q = 0; q < 3; ++q) out[q][tid] = scan[q][tid] - own[q];
+    int32_t at = scan[0][tid] - own[0];
+    for (int w = 0; w < kPlanWaves; ++w) {
+      const int32_t c = cnt[w * G + tid];
+      cnt[w * G + tid] = at;
+      at += c;
+    }
+  }
+  if (tid == 0) {
+    int32_t at = scan[0][L - 1];
+    const int32_t none = (int32_t)M - at;
+    pl.off[L] = at;
+    pl.off[L + 1] = (int32_t)M;
+    pl.blk16[L] = scan[1][L - 1];
+    pl.blk16[L + 1] = scan[1][L - 1] + (none + 15) / 16;
+    pl.blk64[L] = scan[2][L - 1];
+    pl.blk64[L + 1] = scan[2][L - 1] + (none + 63) / 64;
+    for (int w = 0; w < kPlanWaves; ++w) {
+      const int32_t c = cnt[w * G + L];
+      cnt[w * G + L] = at;
+      at += c;
+    }
+  }
+  __syncthreads();
+  for (int64_t i0 = lo; i0 < hi; i0 += 64) {
+    const int64_t i = i0 + lane;
+    const int g = i < hi ? group(i) : -1;
+    uint64_t left = __ballot(i < hi);
+    while (left) {
+      const int a = __builtin_amdgcn_readlane(g, __builtin_ctzll(left));
+      const uint64_t same = __ballot(g == a);
+      const int32_t at = mine[a];   // a wave's LDS accesses are in order
+      if (g == a) {
+        const int32_t rank = __popcll(same & ((uint64_t(1) << lane) - 1));
+        pl.perm[at + rank] = (int32_t)i;
+        if (rank == 0) mine[a] = at + __popcll(same);
+      }
+      left &= ~same;
+    }
+  }
+}
+
+// The group of block b in a first-block table [L + 2]: every thread tests some groups, the match goes
+// through LDS. Called by the whole workgroup; b < first[L + 1].
+__device__ __forceinline__ int group_of_block(const int32_t *first, int L, int b) {
+  __shared__ int s_group;
+  for (int t = threadIdx.x; t <= L; t += blockDim.x)
+    if (b >= first[t] && b < first[t + 1]) s_group = t;
+  __syncthreads();
+  return __builtin_amdgcn_readfirstlane(s_group);
+}
+
+// ------------------------------------------------------------------------------------ row projection
+// out[i][j] = sum over l of in[i][l] * p_a[j][l] for the rows i of adapter a; zero for rows without
+// one. p_a = p + a * pstride, rows of leading dimension ldp.
+
+// Blocks of at most 16 rows: latency sets the time, so each wave issues all the loads of a pass
+// straight into operand registers. Wave w takes 32-column slices 4 u + w of the workgroup's split
+// of the reduction; the four waves' sums are added in wave order in LDS. L % 8 == 0.
+template <int TN>
+__global__ __launch_bounds__(256) void multi_rows16_kernel(const uint16_t *__restrict__ in, int64_t ldin,
+                                                           const uint16_t *__restrict__ p, int64_t pstride,
+                                                           int64_t ldp, int64_t M, int64_t Lr, int r, int L,
+                                                           int64_t lsplit, float *__restrict__ part,
+                                                           uint16_t *__restrict__ out, MultiPlan pl) {
+  __shared__ f32x4 red[4][TN][64];
+  const int b = blockIdx.x;
+  if (b >= pl.blk16[L + 1]) return;
+  const int a = group_of_block(pl.blk16, L, b);
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  const int split = blockIdx.y, nl = lane & 15, kg = lane >> 4;
+  const int32_t row0 = pl.off[a] + (b - pl.blk16[a]) * 16, rowe = pl.off[a + 1];
+  const bool have = row0 + nl < rowe && a < L;
+  const uint16_t *x = in + (have ? (int64_t)pl.perm[row0 + nl] * ldin : 0);
+  const uint16_t *pa = p + (a < L ? a : 0) * pstride;
+  const int64_t lb = split * lsplit, le = lb + lsplit < Lr ? lb + lsplit : Lr;
+  f32x4 acc[TN];
+#pragma unroll
+  for (int t = 0; t < TN; ++t) acc[t] = f32x4{0.f, 0.f, 0.f, 0.f};
+  if (a < L) {
+#pragma unroll 1
+    for (int64_t k0 = lb + 32 * wave; k0 < le; k0 += 256) {
+      const u32x4 zero = {0u, 0u, 0u, 0u};
+      u32x4 xv[2], pv[2][TN];
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        const int64_t c = k0 + 128 * h + 8 * kg;
+        xv[h] = have && c < le ? *reinterpret_cast<const u32x4 *>(x + c) : zero;
+#pragma unroll
+        for (int t = 0; t < TN; ++t) {
+          const int j = 16 * t + nl;
+          pv[h][t] = j < r && c < le ? *reinterpret_cast<const u32x4 *>(pa + j * ldp + c) : zero;
+        }
+      }
+#pragma unroll
+      for (int h = 0; h < 2; ++h)
+#pragma unroll
+        for (int t = 0; t < TN; ++t)
+          acc[t] = mfma16x16x32(__builtin_bit_cast(bf16x8, xv[h]), __builtin_bit_cast(bf16x8, pv[h][t]), acc[t]);
+    }
+  }
+#pragma unroll
+  for (int t = 0; t < TN; ++t) red[wave][t][lane] = acc[t];
+  __syncthreads();
+  // D[row][j]: lane l holds column j = l % 16 and rows 4 (l / 16) + v; wave w finishes tiles w, w + 4
+  for (int t = wave; t < TN; t += 4) {
+    f32x4 s = red[0][t][lane];
+#pragma unroll
+    for (int w = 1; w < 4; ++w) s += red[w][t][lane];
+#pragma unroll
+    for (int v = 0; v < 4; ++v) {
+      const int32_t row = row0 + 4 * kg + v;
+      const int j = 16 * t + nl;
+      if (row < rowe && j < r) {
+        const int64_t i = pl.perm[row];
+        if (part)
+          part[((int64_t)split * M + i) * r + j] = s[v];
+        else
+          out[i * r + j] = (uint16_t)(pack_bf16x2(s[v], 0.f) & 0xFFFFu);
+      }
+    }
+  }
+}
+
+// Blocks of at most 64 rows (one 16-row tile a wave): in- and p-tiles of 64 columns loaded two steps
+// ahead in whole 128-byte rows and staged in LDS, chunk c of row i at slot c ^ ((i >> 1) & 7).
+__device__ __forceinline__ int swzm(int row, int c) { return row * 8 + (c ^ ((row >> 1) & 7)); }
+
+template <int TN>
+__global__ __launch_bounds__(256) void multi_rows64_kernel(const uint16_t *__restrict__ in, int64_t ldin,
+                                                           const uint16_t *__restrict__ p, int64_t pstride,
+                                                           int64_t ldp, int64_t M, int64_t Lr, int r, int L,
+                                                           int64_t lsplit, float *__restrict__ part,
+                                                           uint16_t *__restrict__ out, MultiPlan pl) {
+  constexpr int PCH = TN * 16 * 8;                 // p-tile chunks per step
+  constexpr int PPT = (PCH + 255) / 256;           // p-tile chunks per thread
+  __shared__ uint4 sI[2][64 * 8];
+  __shared__ uint4 sP[2][PCH];
+  const int b = blockIdx.x;
+  if (b >= pl.blk64[L + 1]) return;
+  const int a = group_of_block(pl.blk64, L, b);
+  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+  const int split = blockIdx.y;
+  const int32_t row0 = pl.off[a] + (b - pl.blk64[a]) * 64, rowe = pl.off[a + 1];
+  const uint16_t *pa = p + (a < L ? a : 0) * pstride;
+  const int64_t lb = split * lsplit, le = lb + lsplit < Lr ? lb + lsplit : Lr;
+  // this thread's rows of the in-tile (tid / 8 and 32 more), and chunk tid % 8 of each
+  const uint16_t *x[2];
+  bool have[2];
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    const int32_t row = row0 + (tid >> 3) + 32 * i;
+    have[i] = row < rowe && a < L;
+    x[i] = in + (have[i] ? (int64_t)pl.perm[row] * ldin : 0) + (tid & 7) * 8;
+  }
+  f32x4 acc[TN];
+#pragma unroll
+  for (int t = 0; t < TN; ++t) acc[t] = f32x4{0.f, 0.f, 0.f, 0.f};
+  struct Stage {
+    uint4 x[2];
+    uint4 q[PPT];
+  };
+  auto load = [&](int64_t l0, Stage &st) {
+#pragma unroll
+    for (int i = 0; i < 2; ++i)
+      st.x[i] = have[i] && l0 + (tid & 7) * 8 < le ? *reinterpret_cast<const uint4 *>(x[i] + l0) : make_uint4(0, 0, 0, 0);
+#pragma unroll
+    for (int i = 0; i < PPT; ++i) {
+      const int qd = tid + 256 * i;
+      const int j = qd >> 3;
+      const int64_t l = l0 + (qd & 7) * 8;
+      st.q[i] = (qd < PCH && j < r && l < le) ? *reinterpret_cast<const uint4 *>(pa + (int64_t)j * ldp + l)
+                                              : make_uint4(0, 0, 0, 0);
+    }
+  };
+  auto store = [&](const Stage &st, int buf) {
+#pragma unroll
+    for (int i = 0; i < 2; ++i) sI[buf][swzm((tid >> 3) + 32 * i, tid & 7)] = st.x[i];
+#pragma unroll
+    for (int i = 0; i < PPT; ++i) {
+      const int qd = tid + 256 * i;
+      if (qd < PCH) sP[buf][swzm(qd >> 3, qd & 7)] = st.q[i];
+    }
+  };
+  auto mma = [&](int buf) {
+#pragma unroll
+    for (int kk = 0; kk < 2; ++kk) {
+      const int c = kk * 4 + (lane >> 4);
+      const bf16x8 xa = __builtin_bit_cast(bf16x8, sI[buf][swzm(wave * 16 + (lane & 15), c)]);
+#pragma unroll
+      for (int t = 0; t < TN; ++t)
+        acc[t] = mfma16x16x32(xa, __builtin_bit_cast(bf16x8, sP[buf][swzm(t * 16 + (lane & 15), c)]), acc[t]);
+    }
+  };
+  Stage s0, s1;
+  const int64_t nst = a < L ? (le - lb + 63) / 64 : 0;
+  if (nst > 0) load(lb, s0);
+  if (nst > 1) load(lb + 64, s1);
+  if (nst > 0) store(s0, 0);
+  __syncthreads();
+  // step i: MFMAs on buffer i & 1; loads of step i + 2; stores of step i + 1 into the other buffer
+#pragma unroll 1
+  for (int64_t i = 0; i < nst; i += 2) {
+    if (i + 2 < nst) load(lb + (i + 2) * 64, s0);
+    mma(0);
+    if (i + 1 < nst) store(s1, 1);
+    __syncthreads();
+    if (i + 1 >= nst) break;
+    if (i + 3 < nst) load(lb + (i + 3) * 64, s1);
+    mma(1);
+    if (i + 2 < nst) store(s0, 0);
+    __syncthreads();
+  }
+#pragma unroll
+  for (int v = 0; v < 4; ++v) {
+    const int32_t row = row0 + wave * 16 + 4 * (lane >> 4) + v;
+    if (row >= rowe) continue;
+    const int64_t i = pl.perm[row];
+#pragma unroll
+    for (int t = 0; t < TN; ++t) {
+      const int j = t * 16 + (lane & 15);
+      if (j < r) {
+        if (part)
+          part[((int64_t)split * M + i) * r + j] = acc[t][v];
+        else
+          out[i * r + j] = (uint16_t)(pack_bf16x2(acc[t][v], 0.f) & 0xFFFFu);
+      }
+    }
+  }
+}
+
+// out = bf16(sum over the splits of part [splits][n]), in split order.
+__global__ void multi_rows_sum_kernel(const float *__restrict__ part, int64_t n, int splits,
+                                      uint16_t *__restrict__ out) {
+  for (int64_t i = blockIdx.x * (int64_t)blockDim.x + threadIdx.x; i < n; i += (int64_t)gridDim.x * blockDim.x) {
+    float a = 0.f;
+    int s = 0;
+    for (; s + 8 <= splits; s += 8) {
+      float v[8];
+#pragma unroll
+      for (int j = 0; j < 8; ++j) v[j] = part[(int64_t)(s + j) * n + i];
+#pragma unroll
+      for (int j = 0; j < 8; ++j) a += v[j];
+    }
+    for (; s < splits; ++s) a += part[(int64_t)s * n + i];
+    out[i] = (uint16_t)(pack_bf16x2(a, 0.f) & 0xFFFFu);
+  }
+}
+
+// ------------------------------------------------------------------------------------ sums over rows
+// part[a][split][j][c] = sum over the rows i of adapter a in the split of P[i][j] * Q[i][c]
+// (dA: P = U, Q = X; dB: P = T, Q = dY); with one split, s[a] times it goes straight to out. Workgroup: 128 columns x all r ranks, in stages of 64 rows
+// loaded two stages ahead, staged row-major in LDS (rows padded by 32 bytes) and read with the
+// transposing LDS load, which gives a lane 4 consecutive rows of one column: the MFMA operand with
+// the rows as its reduction index.
+constexpr int kRB = 64, kCB = 128, kQRow = kCB + 16;
+typedef __attribute__((ext_vector_type(4))) short s16x4;
+typedef __attribute__((ext_vector_type(8))) short s16x8;
+
+__device__ __forceinline__ s16x4 lds_tr(const uint16_t *p) {
+  return __builtin_amdgcn_ds_read_tr16_b64_v4i16((__attribute__((address_space(3))) s16x4 *)(p));
+}
+
+template <int TJ>
+__global__ __launch_bounds__(256) void multi_sum_kernel(const uint16_t *__restrict__ P,
+                                                        const uint16_t *__restrict__ Q, int64_t ldq,
+                                                        int64_t C, int r, float *__restrict__ part,
+                                                        const float *__restrict__ s, bool transposed,
+                                                        uint16_t *__restrict__ out, MultiPlan pl) {
+  constexpr int PROW = TJ * 16 + 16;
+  __shared__ uint16_t sQ[2][kRB * kQRow];
+  __shared__ uint16_t sP[2][kRB * PROW];
+  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+  const int64_t c0 = (int64_t)blockIdx.x * kCB;
+  const int a = blockIdx.z, split = blockIdx.y;
+  const int32_t lo = pl.off[a], hi = pl.off[a + 1];
+  int32_t per = (hi - lo + (int)gridDim.y - 1) / (int)gridDim.y;
+  per = (per + kRB - 1) / kRB * kRB;
+  const int32_t mb = lo + split * per, me = mb + per < hi ? mb + per : hi;
+  const bool pvec = (r & 7) == 0;
+  f32x4 acc[TJ][2];
+#pragma unroll
+  for (int t = 0; t < TJ; ++t)
+#pragma unroll
+    for (int u = 0; u < 2; ++u) acc[t][u] = f32x4{0.f, 0.f, 0.f, 0.f};
+  struct Stage {
+    uint4 q[4];
+    uint4 p[(TJ + 1) / 2];
+  };
+  auto load = [&](int32_t ms, Stage &st) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const int q = tid + 256 * i;
+      const int32_t m = ms + (q >> 4);
+      const int64_t c = c0 + (q & 15) * 8;
+      st.q[i] = (m < me && c < C) ? *reinterpret_cast<const uint4 *>(Q + (int64_t)pl.perm[m] * ldq + c)
+                                  : make_uint4(0, 0, 0, 0);
+    }
+    if (pvec) {
+#pragma unroll
+      for (int i = 0; i < (TJ + 1) / 2; ++i) {
+        const int q = tid + 256 * i, row = q / (2 * TJ), j = q % (2 * TJ) * 8;
+        const int32_t m = ms + row;
+        st.p[i] = (row < kRB && m < me && j < r) ? *reinterpret_cast<const uint4 *>(P + (int64_t)pl.perm[m] * r + j)
+                                                 : make_uint4(0, 0, 0, 0);
+      }
+    }
+  };
+  auto store = [&](int32_t ms, const Stage &st, int buf) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const int q = tid + 256 * i;
+      *reinterpret_cast<uint4 *>(&sQ[buf][(q >> 4) * kQRow + (q & 15) * 8]) = st.q[i];
+    }
+    if (pvec) {
+#pragma unroll
+      for (int i = 0; i < (TJ + 1) / 2; ++i) {
+        const int q = tid + 256 * i, row = q / (2 * TJ);
+        if (row < kRB) *reinterpret_cast<uint4 *>(&sP[buf][row * PROW + q % (2 * TJ) * 8]) = st.p[i];
+      }
+    } else {
+      for (int q = tid; q < kRB * TJ * 16; q += 256) {
+        const int row = q / (TJ * 16), j = q % (TJ * 16);
+        const int32_t m = ms + row;
+        sP[buf][row * PROW + j] = (m < me && j < r) ? P[(int64_t)pl.perm[m] * r + j] : (uint16_t)0;
+      }
+    }
+  };
+  const int g16 = lane >> 4, l16 = lane & 15;
+  auto frag = [&](const uint16_t *S, int stride, int col0, int ks) {
+    const int m0 = ks * 32 + g16 * 8 + (l16 >> 2), col = col0 + 4 * (l16 & 3);
+    const s16x4 x = lds_tr(S + m0 * stride + col), y = lds_tr(S + (m0 + 4) * stride + col);
+    const s16x8 v = {x[0], x[1], x[2], x[3], y[0], y[1], y[2], y[3]};
+    return __builtin_bit_cast(bf16x8, v);
+  };
+  auto mma = [&](int buf) {
+#pragma unroll
+    for (int ks = 0; ks < 2; ++ks) {
+      bf16x8 q[2];
+#pragma unroll
+      for (int u = 0; u < 2; ++u) q[u] = frag(sQ[buf], kQRow, wave * 32 + u * 16, ks);
+#pragma unroll
+      for (int t = 0; t < TJ; ++t) {
+        const bf16x8 p = frag(sP[buf], PROW, t * 16, ks);
+#pragma unroll
+        for (int u = 0; u < 2; ++u) acc[t][u] = mfma16x16x32(p, q[u], acc[t][u]);
+      }
+    }
+  };
+  const int nst = me > mb ? (me - mb + kRB - 1) / kRB : 0;
+  Stage s0, s1;
+  if (nst > 0) load(mb, s0);
+  if (nst > 1) load(mb + kRB, s1);
+  if (nst > 0) store(mb, s0, 0);
+  __syncthreads();
+#pragma unroll 1
+  for (int i = 0; i < nst; i += 2) {
+    if (i + 2 < nst) load(mb + (i + 2) * kRB, s0);
+    mma(0);
+    if (i + 1 < nst) store(mb + (i + 1) * kRB, s1, 1);
+    __syncthreads();
+    if (i + 1 >= nst) break;
+    if (i + 3 < nst) load(mb + (i + 3) * kRB, s1);
+    mma(1);
+    if (i + 2 < nst) store(mb + (i + 2) * kRB, s0, 0);
+    __syncthreads();
+  }
+#pragma unroll
+  for (int t = 0; t < TJ; ++t)
+#pragma unroll
+    for (int u = 0; u < 2; ++u)
+#pragma unroll
+      for (int v = 0; v < 4; ++v) {
+        const int j = t * 16 + 4 * g16 + v;
+        const int64_t c = c0 + wave * 32 + u * 16 + l16;
+        if (j >= r || c >= C) continue;
+        if (gridDim.y > 1) {
+          part[(((int64_t)a * gridDim.y + split) * r + j) * C + c] = acc[t][u][v];
+        } else {
+          const uint16_t y = (uint16_t)(pack_bf16x2(s[a] * acc[t][u][v], 0.f) & 0xFFFFu);
+          out[(int64_t)a * r * C + (transposed ? c * r + j : j * C + c)] = y;
+        }
+      }
+}
+
+// out[a] = bf16(s[a] * (sum over the splits of part[a])): [r][C], or [C][r] when transposed.
+__global__ void multi_sum_final_kernel(const float *__restrict__ part, int64_t C, int r, int splits, int L,
+                                       const float *__restrict__ s, bool transposed, uint16_t *__restrict__ out) {
+  const int64_t n = (int64_t)r * C;
+  for (int64_t i = blockIdx.x * (int64_t)blockDim.x + threadIdx.x; i < n * L; i += (int64_t)gridDim.x * blockDim.x) {
+    const int64_t a = i / n, ia = i - a * n;
+    const float *pa = part + a * splits * n + ia;
+    float x = 0.f;
+    int q = 0;
+    for (; q + 8 <= splits; q += 8) {
+      float v[8];
+#pragma unroll
+      for (int j = 0; j < 8; ++j) v[j] = pa[(int64_t)(q + j) * n];
+#pragma unroll
+      for (int j = 0; j < 8; ++j) x += v[j];
+    }
+    for (; q < splits; ++q) x += pa[(int64_t)q * n];
+    const uint16_t y = (uint16_t)(pack_bf16x2(s[a] * x, 0.f) & 0xFFFFu);
+    const int64_t j = ia / C, c = ia % C;
+    if (transposed)
+      out[a * n + c * r + j] = y;
+    else
+      out[i] = y;
+  }
+}
+
+// ------------------------------------------------------------------------------------ transposes
+// dst[b][c][j] = src[b][j][c] for `batch` bf16 matrices [R][C], through 64 x 64 LDS tiles.
+__global__ __launch_bounds__(256) void multi_transpose_kernel(const uint16_t *__restrict__ src, int64_t R,
+                                                              int64_t C, uint16_t *__restrict__ dst) {
+  __shared__ uint16_t t[64][66];
+  const int64_t tiles_c = (C + 63) / 64;
+  const int64_t c0 = (int64_t)blockIdx.x % tiles_c * 64, r0 = (int64_t)blockIdx.x / tiles_c * 64;
+  src += (int64_t)blockIdx.y * R * C;
+  dst += (int64_t)blockIdx.y * R * C;
+  const int x = threadIdx.x & 63, y = threadIdx.x >> 6;
+  for (int i = y; i < 64; i += 4)
+    if (r0 + i < R && c0 + x < C) t[i][x] = src[(r0 + i) * C + c0 + x];
+  __syncthreads();
+  for (int i = y; i < 64; i += 4)
+    if (c0 + i < C && r0 + x < R) dst[(c0 + i) * R + r0 + x] = t[x][i];
+}
+
+int64_t blocks_for(int64_t n) {
+  const int64_t b = (n + 255) / 256;
+  return b < 4096 ? (b > 0 ? b : 1) : 4096;
+}
+
+}  // namespace
+
+hipError_t launch_multi_plan(const int32_t *ids, int64_t M, int L, const MultiPlan &pl, hipStream_t st) {
+  if (L < 1 || L > kMultiMaxAdapters || M < 1 || M >= (int64_t(1) << 30)) return hipErrorInvalidValue;
+  multi_plan_kernel<<<dim3(1), dim3(kPlanThreads), sizeof(int32_t) * kPlanWaves * (L + 1), st>>>(ids, M, L, pl);
+  return hipGetLastError();
+}
+
+// Rows per block of the row projection: 16 up to 1024 rows, where the groups of a serving batch are a
+// few rows each, else 64, which reads an adapter's factor a fourth as often.
+static int multi_rows_block(int64_t M) { return M <= 1024 ? 16 : 64; }
+
+// Splits of its reduction: about 1024 workgroups, at least 256 elements each.
+int multi_rows_splits(int64_t M, int64_t Lr) {
+  const int64_t wgs = (M + multi_rows_block(M) - 1) / multi_rows_block(M);
+  int64_t s = (1024 + wgs - 1) / wgs;
+  const int64_t most = (Lr + 255) / 256;
+  s = s < most ? s : most;
+  return (int)(s > 1 ? s : 1);
+}
+
+hipError_t launch_multi_rows(const uint16_t *in, int64_t ldin, const uint16_t *p, int64_t pstride, int64_t ldp,
+                             int64_t M, int64_t Lr, int r, int L, int splits, float *part, uint16_t *out,
+                             const MultiPlan &pl, hipStream_t st) {
+  const int64_t rows = multi_rows_block(M);
+  int64_t lsplit = (Lr + splits - 1) / splits;
+  lsplit = (lsplit + 63) / 64 * 64;
+  int64_t blocks = (M + (rows - 1) * (L + 1)) / rows;   // >= the sum of ceil(rows of a group / rows)
+  blocks = blocks < M ? blocks : M;
+  const dim3 grid((unsigned)blocks, (unsigned)splits);
+  float *pp = splits > 1 ? part : nullptr;
+  switch ((r + 15) / 16) {
+#define MR_CASE(T)                                                                                                 \
+  case T:                                                                                                          \
+    if (rows == 16)                                                                                                \
+      multi_rows16_kernel<T><<<grid, dim3(256), 0, st>>>(in, ldin, p, pstride, ldp, M, Lr, r, L, lsplit, pp, out, pl); \
+    else                                                                                                           \
+      multi_rows64_kernel<T><<<grid, dim3(256), 0, st>>>(in, ldin, p, pstride, ldp, M, Lr, r, L, lsplit, pp, out, pl); \
+    break;
+    MR_CASE(1) MR_CASE(2) MR_CASE(3) MR_CASE(4) MR_CASE(5) MR_CASE(6) MR_CASE(7) MR_CASE(8)
+#undef MR_CASE
+    default: return hipErrorInvalidValue;
+  }
+  hipError_t e = hipGetLastError();
+  if (e != hipSuccess || splits == 1) return e;
+  multi_rows_sum_kernel<<<dim3((unsigned)blocks_for(M * r)), dim3(256), 0, st>>>(part, M * r, splits, out);
+  return hipGetLastError();
+}
+
+// Splits of the sums over rows: about 1024 workgroups over the column tiles and adapters.
+int multi_sum_splits(int64_t M, int64_t C, int L) {
+  const int64_t tiles = (C + kCB - 1) / kCB * L;
+  int64_t s = (1024 + tiles - 1) / tiles;
+  const int64_t most = (M + kRB - 1) / kRB;
+  s = s < most ? s : most;
+  return (int)(s > 1 ? s : 1);
+}
+
+hipError_t launch_multi_sum(const uint16_t *P, const uint16_t *Q, int64_t ldq, int64_t C, int r, int L,
+                            const float *s, int splits, float *part, uint16_t *out, bool transposed,
+                            const MultiPlan &pl, hipStream_t st) {
+  const dim3 grid((unsigned)((C + kCB - 1) / kCB), (unsigned)splits, (unsigned)L);
+  switch ((r + 15) / 16) {
+#define MS_CASE(T) \
+  case T: multi_sum_kernel<T><<<grid, dim3(256), 0, st>>>(P, Q, ldq, C, r, part, s, transposed, out, pl); break;
+    MS_CASE(1) MS_CASE(2) MS_CASE(3) MS_CASE(4) MS_CASE(5) MS_CASE(6) MS_CASE(7) MS_CASE(8)
+#undef MS_CASE
+    default: return hipErrorInvalidValue;
+  }
+  hipError_t e = hipGetLastError();
+  if (e != hipSuccess || splits == 1) return e;
+  multi_sum_final_kernel<<<dim3((unsigned)blocks_for((int64_t)L * r * C)), dim3(256), 0, st>>>(part, C, r, splits, L, s,
+                                                                                             transposed, out);
+  return hipGetLastError();
+}
+
+hipError_t launch_multi_transpose(const uint16_t *src, int64_t R, int64_t C, int batch, uint16_t *dst, hipStream_t st) {
+  const dim3 grid((unsigned)((C + 63) / 64 * ((R + 63) / 64)), (unsigned)batch);
+  multi_transpose_kernel<<<grid, dim3(256), 0, st>>>(src, R, C, dst);
+  return hipGetLastError();
+}
+
+}  // namespace nf4q
