@@ -1040,33 +1040,74 @@ int qlora_bwd_dx(const void *dY, int64_t m, const nf4_tensor *W, const void *U, 
 // ---------------------------------------------------------------- an adapter of its own for every row
 namespace {
 
-// Forward: the rows' order, then float partials of T. Backward: the rows' order, U [m, r], B
-// transposed [L, r, n], A transposed [L, k, r], T (recomputed when the caller passes none), then
-// float partials of the row projections or of the sums over rows (never both at once).
+// The kernel of a forward. Up to 16 rows: the stream kernel when its workgroups of 112 weight rows are
+// more than 128, half the CUs; below that the mid kernel splits the reduction instead (16 rows, k
+// 4096, r 16, whole call, stream / mid: n 4096 24.3 / 18.9 us, 11008 24.9 / 21.2, 14336 24.8 / 23.9,
+// 22016 25.4 / 27.5, 28672 27.1 / 31.9). More rows: the mid kernel while 256 x 256 tiles would fill at
+// most half the CUs, then the large one (k 4096, mid / large: 64 tiles 75 / 123 us, 128 tiles
+// 107 / 125, 172 tiles 179 / 128). Up to 256 rows have no table of the rows' order and always take
+// the small kernels.
+enum class MultiKernel { kStream, kMid, kLarge };
+MultiKernel multi_kernel(int64_t m, const nf4_tensor *W, int32_t r) {
+  if (stream16_shape(m, W) && r % 8 == 0 && W->n > 128 * 112) return MultiKernel::kStream;
+  if (m <= nf4q::kMultiSmallM) return MultiKernel::kMid;
+  const int64_t tiles = ((m + 255) / 256) * ((W->n + 255) / 256);
+  return tiles <= 128 ? MultiKernel::kMid : MultiKernel::kLarge;
+}
+
+int padded(int32_t r) { return (r + 7) & ~7; }
+
+// Slices of T's reduction before the stream kernel: 1024 elements each (one round of loads), fewer for
+// the high ranks, whose sums every workgroup of that kernel adds (16 r of them times the slices).
+int stream_tsplits(int64_t k, int32_t r) {
+  const int64_t s = std::min<int64_t>((k + 1023) / 1024, 512 / r);
+  return (int)std::max<int64_t>(s, 1);
+}
+
+// Workspace of the layer with an adapter for every row. Forward: the rows' order, then B and T with the
+// ranks padded to a multiple of 8 (when they are not one), then float sums (of T, then of Y).
+// Backward: the rows' order, U [m, r] and its padded form, B transposed [L, r, n], A transposed [L, k,
+// r padded], T (recomputed when the caller passes none) and its padded form, then float sums of the
+// row projections or of the sums over rows (never both at once).
 struct MultiWs {
   int sp_k = 1, sp_n = 1, sa = 1, sb = 1;
-  size_t plan = 0, u = 0, bt = 0, at = 0, t = 0, part = 0, total = 0;
+  size_t plan = 0, bp = 0, u = 0, up = 0, bt = 0, at = 0, t = 0, tp = 0, part = 0, total = 0;
 };
 
 MultiWs multi_ws(int64_t m, int64_t n, int64_t k, int32_t r, int32_t L, bool bwd) {
   MultiWs w;
+  const int rp = padded(r);
   w.sp_k = nf4q::multi_rows_splits(m, k);
   w.plan = align256(nf4q::multi_plan_bytes(m, L));
+  if (rp != r) w.tp = align256((size_t)m * rp * 2);
   size_t p = w.sp_k > 1 ? (size_t)w.sp_k * m * r * 4 : 0;
   if (bwd) {
     w.sp_n = nf4q::multi_rows_splits(m, n);
     w.sa = nf4q::multi_sum_splits(m, k, L);
     w.sb = nf4q::multi_sum_splits(m, n, L);
     w.u = w.t = align256((size_t)m * r * 2);
+    w.up = w.tp;
     w.bt = align256((size_t)L * r * n * 2);
-    w.at = align256((size_t)L * r * k * 2);
+    w.at = align256((size_t)L * rp * k * 2);
     if (w.sp_n > 1) p = std::max(p, (size_t)w.sp_n * m * r * 4);
     if (w.sa > 1) p = std::max(p, (size_t)L * w.sa * r * k * 4);
     if (w.sb > 1) p = std::max(p, (size_t)L * w.sb * r * n * 4);
+  } else {
+    if (rp != r) w.bp = align256((size_t)L * n * rp * 2);
+    p = std::max(p, nf4q::mid_fwd_bytes(m, n, k, rp));   // T is whole before the sums of Y start
+    if (m <= 16) p = std::max(p, (size_t)stream_tsplits(k, r) * m * r * 4);
   }
   w.part = align256(p);
-  w.total = w.plan + w.u + w.bt + w.at + w.t + w.part;
+  w.total = w.plan + w.bp + w.u + w.up + w.bt + w.at + w.t + w.tp + w.part;
   return w;
+}
+
+// bf16 [rows, r] with the ranks padded to a multiple of 8: itself, or a copy in the workspace.
+hipError_t pad_ranks(const uint16_t **src, int64_t rows, int32_t r, char *to, hipStream_t sm) {
+  if (padded(r) == r) return hipSuccess;
+  const hipError_t e = nf4q::launch_multi_pad(*src, rows, r, padded(r), (uint16_t *)to, sm);
+  *src = (const uint16_t *)to;
+  return e;
 }
 
 int check_multi_rest(const float *s, const int32_t *ids, const MultiWs &lay, void *ws, size_t ws_bytes) {
@@ -1083,7 +1124,12 @@ int check_multi_shape(const void *X, int64_t m, const nf4_tensor *W, const void 
   if (L < 1 || L > nf4q::kMultiMaxAdapters)
     return fail(NF4_EINVAL, "L must lie in [1, %d] (got %d)", nf4q::kMultiMaxAdapters, L);
   if (r < 1) return fail(NF4_EINVAL, "r must lie in [1, 128] (got %d)", r);
-  return check_layer(X, m, W, A, B, r);
+  const int st = check_layer(X, m, W, A, B, r);
+  if (st) return st;
+  // the copies that gather rows reach 32-bit offsets
+  if (m * std::max(W->n, W->k) * 2 > nf4q::kMultiMaxGather)
+    return fail(NF4_EUNSUPPORTED, "X and Y must be below %lld bytes each", (long long)nf4q::kMultiMaxGather);
+  return NF4_OK;
 }
 
 nf4q::GemmArgs multi_gemm(const void *in, int64_t m, const nf4_tensor *W, int64_t C, int64_t R, void *out) {
@@ -1130,14 +1176,34 @@ int qlora_multi_fwd(const void *X, int64_t m, const nf4_tensor *W, const void *A
   if (st) return st;
   hipStream_t sm = (hipStream_t)stream;
   char *base = (char *)ws;
-  const nf4q::MultiPlan pl = nf4q::multi_plan_at(base, m, L);
-  hipError_t e = nf4q::launch_multi_plan(ids, m, L, pl, sm);
-  if (e != hipSuccess) return hip_status(e, "qlora_multi_fwd plan launch");
-  e = nf4q::launch_multi_rows((const uint16_t *)X, k, (const uint16_t *)A, (int64_t)r * k, k, m, k, r, L, lay.sp_k,
-                              (float *)(base + lay.plan), (uint16_t *)T, pl, sm);
-  if (e != hipSuccess) return hip_status(e, "qlora_multi_fwd T launch");
-  const nf4q::MultiArgs mu{ids, s, (const uint16_t *)T, (const uint16_t *)B, L, r};
-  return hip_status(nf4q::launch_gemm_fwd_multi(multi_gemm(X, m, W, n, k, Y), mu, sm), "qlora_multi_fwd launch");
+  const uint16_t *x = (const uint16_t *)X, *a = (const uint16_t *)A, *b = (const uint16_t *)B;
+  const uint16_t *t = (const uint16_t *)T;
+  float *part = (float *)(base + lay.plan + lay.bp + lay.tp);
+  const int rp = padded(r);
+  hipError_t e = pad_ranks(&b, (int64_t)L * n, r, base + lay.plan, sm);
+  if (e != hipSuccess) return hip_status(e, "qlora_multi_fwd launch");
+  const MultiKernel kernel = multi_kernel(m, W, r);
+  nf4q::MultiArgs mu{ids, s, nullptr, b, L, rp};
+  const nf4q::GemmArgs g = multi_gemm(X, m, W, n, k, Y);
+  if (kernel == MultiKernel::kStream) {
+    const int splits = stream_tsplits(k, r);
+    e = nf4q::launch_multi_rows_part(x, k, a, (int64_t)r * k, k, ids, m, k, r, L, splits, part, sm);
+    if (e != hipSuccess) return hip_status(e, "qlora_multi_fwd T launch");
+    return hip_status(nf4q::launch_stream16_fwd_multi(g, mu, part, splits, (uint16_t *)T, sm), "qlora_multi_fwd launch");
+  }
+  if (m > nf4q::kMultiSmallM) {
+    const nf4q::MultiPlan pl = nf4q::multi_plan_at(base, m, L);
+    e = nf4q::launch_multi_plan(ids, m, L, pl, sm);
+    if (e == hipSuccess)
+      e = nf4q::launch_multi_rows(x, k, a, (int64_t)r * k, k, m, k, r, L, lay.sp_k, part, (uint16_t *)T, pl, sm);
+    if (e == hipSuccess) e = pad_ranks(&t, m, r, base + lay.plan + lay.bp, sm);
+    if (e != hipSuccess) return hip_status(e, "qlora_multi_fwd T launch");
+    mu.P = t;
+    mu.perm = pl.perm;
+  }
+  e = kernel == MultiKernel::kMid ? nf4q::launch_mid_fwd_multi(g, mu, a, r, (uint16_t *)T, part, sm)
+                                  : nf4q::launch_gemm_fwd_multi(g, mu, sm);
+  return hip_status(e, "qlora_multi_fwd launch");
 }
 
 int qlora_multi_bwd(const void *dY, const void *X, int64_t m, const nf4_tensor *W, const void *A,
@@ -1156,33 +1222,44 @@ int qlora_multi_bwd(const void *dY, const void *X, int64_t m, const nf4_tensor *
   hipStream_t sm = (hipStream_t)stream;
   char *base = (char *)ws;
   const nf4q::MultiPlan pl = nf4q::multi_plan_at(base, m, L);
-  uint16_t *U = (uint16_t *)(base + lay.plan);
-  uint16_t *Bt = (uint16_t *)(base + lay.plan + lay.u);
-  uint16_t *At = (uint16_t *)(base + lay.plan + lay.u + lay.bt);
-  uint16_t *Tw = (uint16_t *)(base + lay.plan + lay.u + lay.bt + lay.at);
-  float *part = (float *)(base + lay.plan + lay.u + lay.bt + lay.at + lay.t);
-  const uint16_t *dy = (const uint16_t *)dY, *x = (const uint16_t *)X;
+  char *at = base + lay.plan;
+  auto take = [&](size_t bytes) {
+    char *q = at;
+    at += bytes;
+    return q;
+  };
+  uint16_t *U = (uint16_t *)take(lay.u);
+  char *Up = take(lay.up);
+  uint16_t *Bt = (uint16_t *)take(lay.bt);
+  uint16_t *At = (uint16_t *)take(lay.at);
+  uint16_t *Tw = (uint16_t *)take(lay.t);
+  char *Tp = take(lay.tp);
+  float *part = (float *)at;
+  const int rp = padded(r);
+  const uint16_t *dy = (const uint16_t *)dY, *x = (const uint16_t *)X, *t = (const uint16_t *)T, *u = U;
   hipError_t e = nf4q::launch_multi_plan(ids, m, L, pl, sm);
   if (e != hipSuccess) return hip_status(e, "qlora_multi_bwd plan launch");
-  if (!T) {
+  if (!t) {
     e = nf4q::launch_multi_rows(x, k, (const uint16_t *)A, (int64_t)r * k, k, m, k, r, L, lay.sp_k, part, Tw, pl, sm);
     if (e != hipSuccess) return hip_status(e, "qlora_multi_bwd T launch");
-    T = Tw;
+    t = Tw;
   }
-  e = nf4q::launch_multi_transpose((const uint16_t *)B, n, r, L, Bt, sm);
+  e = pad_ranks(&t, m, r, Tp, sm);
+  if (e == hipSuccess) e = nf4q::launch_multi_transpose((const uint16_t *)B, n, r, n, L, Bt, sm);
   if (e != hipSuccess) return hip_status(e, "qlora_multi_bwd transpose launch");
   e = nf4q::launch_multi_rows(dy, n, Bt, (int64_t)r * n, n, m, n, r, L, lay.sp_n, part, U, pl, sm);
+  if (e == hipSuccess) e = pad_ranks(&u, m, r, Up, sm);
   if (e != hipSuccess) return hip_status(e, "qlora_multi_bwd U launch");
   if (dX) {
-    e = nf4q::launch_multi_transpose((const uint16_t *)A, r, k, L, At, sm);
+    e = nf4q::launch_multi_transpose((const uint16_t *)A, r, k, rp, L, At, sm);
     if (e != hipSuccess) return hip_status(e, "qlora_multi_bwd transpose launch");
-    const nf4q::MultiArgs mu{ids, s, U, At, L, r};
+    const nf4q::MultiArgs mu{ids, s, u, At, L, rp, pl.perm};
     e = nf4q::launch_gemm_dx_multi(multi_gemm(dY, m, W, k, n, dX), mu, sm);
     if (e != hipSuccess) return hip_status(e, "qlora_multi_bwd dX launch");
   }
-  e = nf4q::launch_multi_sum(U, x, k, k, r, L, s, lay.sa, part, (uint16_t *)dA, false, pl, sm);
+  e = nf4q::launch_multi_sum(u, rp, x, k, k, r, L, s, lay.sa, part, (uint16_t *)dA, false, pl, sm);
   if (e != hipSuccess) return hip_status(e, "qlora_multi_bwd dA launch");
-  e = nf4q::launch_multi_sum((const uint16_t *)T, dy, n, n, r, L, s, lay.sb, part, (uint16_t *)dB, true, pl, sm);
+  e = nf4q::launch_multi_sum(t, rp, dy, n, n, r, L, s, lay.sb, part, (uint16_t *)dB, true, pl, sm);
   return hip_status(e, "qlora_multi_bwd dB launch");
 }
 

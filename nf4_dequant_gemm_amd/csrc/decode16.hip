@@ -44,6 +44,7 @@
 // Requires M <= 16, double quantisation, K % 256 == 0; the host sends other shapes elsewhere.
 #include "common.h"
 #include "launch.h"
+#include "multi.h"
 
 namespace nf4q {
 namespace {
@@ -155,8 +156,11 @@ __device__ __forceinline__ uint32_t cvt_fp4x2(uint32_t w) {
 // in units of S, which multiplies the tile at the end.
 // kQ: rank tiles of 16 of T = X A^T formed in the kernel (0: T given, or added from split
 // partials; E2M1 at most 1).
-template <bool kFP4, int kQ>
-__global__ __launch_bounds__(kThreads) void decode16_fwd_kernel(Dec16Args g) {
+// kMulti: the rows have adapters of their own (mu holds the adapters' B, the ids and scales; g.r is 0,
+// T comes as split partials). The adapters that occur among the rows are listed in LDS before the
+// main loop; the finishing waves add the low-rank term from them.
+template <bool kFP4, int kQ, bool kMulti>
+__device__ __forceinline__ void stream16_body(const Dec16Args &g, const MultiArgs &mu) {
   static_assert(!kFP4 || kQ <= 1, "the E2M1 form forms T for r <= 16 only");
   // E2M1 forming T: A's slice (16 ranks x 256 elements, laid out as X's) follows the group scales
   // in each slot, copied by the copying waves, which form T
@@ -180,6 +184,9 @@ __global__ __launch_bounds__(kThreads) void decode16_fwd_kernel(Dec16Args g) {
   constexpr int kTab = kFP4 ? kRed + 4 * kQ * 64 * 16 : kTabBytes;
   static_assert(kRed + 4 * kQ * 64 * 16 <= kTab, "cross-wave sums exceed the table area");
   __shared__ __align__(16) uint32_t stab[kTab / 4];
+  // kMulti: the rows' adapters (-1: none), the distinct ones in order of first occurrence (then zeros)
+  // and their number
+  __shared__ int sids[kMulti ? 16 : 1], slist[kMulti ? 16 : 1], snum;
   auto slot = [&](int i) -> uint8_t * {
     return i == 0 ? slot0 : i == 1 ? slot1 : i == 2 ? slot2 : slot3;
   };
@@ -288,9 +295,9 @@ __global__ __launch_bounds__(kThreads) void decode16_fwd_kernel(Dec16Args g) {
   // copies, so the first stage wait covers them.
   const int tfin = 4 * (wave >> 2) + (wave & 3);
   const int nlf = lane & 15, glf = lane >> 4;
-  const bool lvec = g.r > 0 && g.r % 8 == 0 && tfin < kTiles;
+  const bool lvec = (kMulti ? mu.r > 0 : g.r > 0 && g.r % 8 == 0) && tfin < kTiles;
   u32x4 tpre[4], bpre[4];
-  {
+  if constexpr (!kMulti) {
     // every load is issued (no branch, no register copies that would wait for them); those not
     // needed read outside the buffers and return zero (T is read from LDS at the end when the
     // kernel forms it)
@@ -371,6 +378,23 @@ __global__ __launch_bounds__(kThreads) void decode16_fwd_kernel(Dec16Args g) {
     }
   }
 
+  if constexpr (kMulti) {
+    if (wave == 0) {
+      int id = lane < g.M ? mu.ids[lane] : -1;
+      id = id >= 0 && id < mu.L ? id : -1;
+      if (lane < 16) {
+        sids[lane] = id;
+        slist[lane] = 0;
+      }
+      int nd = 0;
+      for (uint64_t left = __ballot(id >= 0); left; ++nd) {
+        const int a = __builtin_amdgcn_readlane(id, __builtin_ctzll(left));
+        if (lane == 0) slist[nd] = a;
+        left &= ~__ballot(id == a);
+      }
+      if (lane == 0) snum = nd;
+    }
+  }
   // T from split partials: every workgroup adds them (in split order, as the separate reduction
   // does) into bf16 T in LDS (slot 3, after the levels), workgroup 0 also stores T, and the
   // finishing waves take their LoRA operands from LDS. The partial loads wait for the copies
@@ -378,7 +402,7 @@ __global__ __launch_bounds__(kThreads) void decode16_fwd_kernel(Dec16Args g) {
   // for them anyway.
   if (kQ == 0 && g.tpart) {
     uint16_t *tl = reinterpret_cast<uint16_t *>(slot3 + 1024);
-    const int r = g.r;
+    const int r = kMulti ? mu.r : g.r;
     for (int idx = tid; idx < 16 * r; idx += kThreads) {
       const int m = idx / r, j = idx - m * r;
       float a = 0.f;
@@ -645,10 +669,40 @@ __global__ __launch_bounds__(kThreads) void decode16_fwd_kernel(Dec16Args g) {
     y *= S > 0.f ? S : 1.f;
   }
 
+  if constexpr (kMulti) {
+    // lane (gl, nl) holds Y[4 gl + v][n0 + row]. T (A operand) was kept in registers, the adapters' B
+    // rows (B operand) come from memory, all the adapters' together for 32 ranks: one round trip.
+    const int r = mu.r, nd = snum;
+    int idv[4];
+#pragma unroll
+    for (int v = 0; v < 4; ++v) idv[v] = sids[4 * gl + v];
+#pragma unroll
+    for (int q = 0; q < 4; ++q) {
+      if (32 * q >= r) break;
+      const int j = 32 * q + 8 * gl;
+      const bf16x8 tf = __builtin_bit_cast(bf16x8, tpre[q]);
+      bf16x8 bf[16];
+#pragma unroll
+      for (int e = 0; e < 16; ++e) {
+        const int a = __builtin_amdgcn_readfirstlane(slist[e]);   // 0 past the last
+        const __amdgpu_buffer_rsrc_t rB = make_rsrc(mu.Q + ((int64_t)a * N + n0) * r, e < nd ? rows * r * 2 : 0);
+        bf[e] = rank_frag(rB, row, j, r);
+      }
+#pragma unroll
+      for (int e = 0; e < 16; ++e) {
+        const int a = __builtin_amdgcn_readfirstlane(slist[e]);
+        const float sa = mu.s[a];
+        const f32x4 lp = mfma16x16x32(tf, bf[e], f32x4{0.f, 0.f, 0.f, 0.f});
+#pragma unroll
+        for (int v = 0; v < 4; ++v) y[v] += e < nd && idv[v] == a ? sa * lp[v] : 0.f;
+      }
+    }
+  }
+
   // LoRA term on the matrix cores: s * T[m][:] . B[n][:] for the tile's 16 columns, in steps of
   // 32 ranks (A operand: T row m, B operand: B row n, both rank-contiguous). With r % 8 == 0 the
   // operands were loaded before the main loop; otherwise they are read here element by element.
-  if (lvec) {
+  if (lvec && !kMulti) {
 #pragma unroll
     for (int q = 0; q < 4; ++q)
       if (32 * q < g.r) {
@@ -691,6 +745,16 @@ __global__ __launch_bounds__(kThreads) void decode16_fwd_kernel(Dec16Args g) {
     const int64_t m = 4 * gl + v;
     if (m < g.M && gn < N) g.Y[m * N + gn] = (uint16_t)(pack_bf16x2(y[v], 0.f) & 0xFFFFu);
   }
+}
+
+template <bool kFP4, int kQ>
+__global__ __launch_bounds__(kThreads) void decode16_fwd_kernel(Dec16Args g) {
+  stream16_body<kFP4, kQ, false>(g, MultiArgs{});
+}
+
+template <bool kFP4>
+__global__ __launch_bounds__(kThreads) void stream16_multi_kernel(Dec16Args g, MultiArgs mu) {
+  stream16_body<kFP4, 0, true>(g, mu);
 }
 
 }  // namespace
@@ -756,6 +820,23 @@ hipError_t launch_decode16_fwd_tin(const GemmArgs &ga, const uint16_t *A, uint16
   if (ga.r <= 16) return launch_dec16<1>(g, st);
   if (ga.r <= 32) return launch_dec16<2>(g, st);
   return launch_dec16<4>(g, st);
+}
+
+hipError_t launch_stream16_fwd_multi(const GemmArgs &ga, const MultiArgs &mu, const float *tpart, int tsplits,
+                                     uint16_t *tout, hipStream_t st) {
+  if (ga.M > 16 || !(ga.w.dq || ga.w.fp4) || ga.w.k % 256 != 0 || ga.r != 0 || mu.r < 8 || mu.r > 128 || mu.r % 8 != 0 ||
+      !tpart || tsplits < 1 || !tout)
+    return hipErrorInvalidValue;
+  Dec16Args g = dec16_args(ga);
+  g.tpart = tpart;
+  g.tsplits = tsplits;
+  g.tout = tout;
+  const unsigned grid = (unsigned)((g.w.n + kRows - 1) / kRows);
+  if (g.w.fp4)
+    stream16_multi_kernel<true><<<dim3(grid), dim3(kThreads), 0, st>>>(g, mu);
+  else
+    stream16_multi_kernel<false><<<dim3(grid), dim3(kThreads), 0, st>>>(g, mu);
+  return hipGetLastError();
 }
 
 }  // namespace nf4q

@@ -159,8 +159,9 @@ __device__ __forceinline__ void dx_origin(int64_t m_lo, int64_t m_hi, int tiles_
   k0 = (int64_t)(gin / gm) * kT;
 }
 
-// kMulti: the rows have adapters of their own (mu; g.r is 0): after the reduction, each wave adds the
-// low-rank term of its block from the transposed adapters, straight from registers (multi_term,
+// kMulti: the rows have adapters of their own (mu; g.r is 0) and are taken in the order of their
+// adapters, row m of the launch being row mu.perm[m] of dY and dX; after the reduction, each wave adds
+// the low-rank term of its block from the transposed adapters, straight from registers (multi_term,
 // multi.h).
 template <int kFmt, bool kGrp, bool kMulti = false>
 __device__ __forceinline__ void dx_body(const GemmArgs &g, const GroupArgs &gr, const MultiArgs &mu) {
@@ -240,7 +241,7 @@ __device__ __forceinline__ void dx_body(const GemmArgs &g, const GroupArgs &gr, 
   };
   const int64_t nruns = (g.w.n * kblk + 255) / 256;
   const __amdgpu_buffer_rsrc_t rS = make_rsrc(g.w.scale, kDQ ? nruns * 4 : 0);
-  const __amdgpu_buffer_rsrc_t rY = make_rsrc(g.a_side + m0 * N, rows_m * N * 2);
+  const __amdgpu_buffer_rsrc_t rY = kMulti ? make_rsrc(g.a_side, g.M * N * 2) : make_rsrc(g.a_side + m0 * N, rows_m * N * 2);
 
   // dY DMA: instruction i of wave w fills the 1 KB of the tile holding rows 8 (4 w + i) .. +7;
   // lane L writes physical chunk L % 8 of row 8 (4 w + i) + L / 8, i.e. logical chunk
@@ -251,6 +252,7 @@ __device__ __forceinline__ void dx_body(const GemmArgs &g, const GroupArgs &gr, 
     const int row = 8 * (4 * wave + i) + (lane >> 3);
     const int c = (lane & 7) ^ ((row >> 1) & 7);
     yoff[i] = (uint32_t)(row * N * 2 + c * 16);
+    if constexpr (kMulti) yoff[i] = row < rows_m ? (uint32_t)(mu.perm[m0 + row] * N * 2 + c * 16) : 0xFFFFFF00u;
   }
   // Decode ownership: weight row n = 64 s + wr of step s, columns k0 + 32 seg .. + 31.
   const int wr = own_row(tid), seg = own_seg(tid);
@@ -489,7 +491,7 @@ __device__ __forceinline__ void dx_body(const GemmArgs &g, const GroupArgs &gr, 
           for (int mt = 0; mt < 8; ++mt) acc[kt][mt] *= tsc;
         tsc = 1.f;
       }
-      multi_term<4, 8>(acc, mu, m0 + wm * 128, m_hi, k0 + wk * 64, g.C);
+      multi_term<4, 8>(acc, mu, mu.perm, m0 + wm * 128, m_hi, k0 + wk * 64, g.C);
     }
 #pragma unroll
     for (int kt = 0; kt < 4; ++kt)
@@ -506,11 +508,13 @@ __device__ __forceinline__ void dx_body(const GemmArgs &g, const GroupArgs &gr, 
 #pragma unroll
     for (int i = 0; i < 16; ++i) {
       const int row = 8 * i + (lane >> 3);
-      const int64_t m = m0 + wm * 128 + row;
+      int64_t m = m0 + wm * 128 + row;
       const uint4 v = blk[swzd(row, c)];
-      if (m < m_hi && k < g.C)
+      if (m < m_hi && k < g.C) {
+        if constexpr (kMulti) m = mu.perm[m];
         __builtin_nontemporal_store(u32x4{v.x, v.y, v.z, v.w},
                                     reinterpret_cast<u32x4 *>(g.out + m * g.ldo + k));
+      }
     }
   }
 }
@@ -610,7 +614,7 @@ hipError_t launch_gemm_dx_grouped(const GemmArgs &g, const GroupArgs &gr, hipStr
 }
 
 hipError_t launch_gemm_dx_multi(const GemmArgs &g, const MultiArgs &mu, hipStream_t st) {
-  if (((g.C | g.ldo) & 7) != 0 || (reinterpret_cast<uintptr_t>(g.out) & 15) != 0 || g.R != g.w.n || g.r != 0)
+  if (((g.C | g.ldo) & 7) != 0 || (reinterpret_cast<uintptr_t>(g.out) & 15) != 0 || g.R != g.w.n || g.r != 0 || !mu.perm || g.M * g.R * 2 > kMultiMaxGather)
     return hipErrorInvalidValue;
   const int64_t tiles = ((g.C + kT - 1) / kT) * ((g.M + kT - 1) / kT);
   if (g.w.fp4)

@@ -224,8 +224,10 @@ __device__ void stage_lora_pair(const GemmArgs &g, float sb, int64_t m0, int64_t
 // columns of the same indices (weight rows N + n0 .., Bu rows n0 ..),
 // so the epilogue holds Yg and Yu of the same columns: it writes both to g.out ([M, 2N], gate then
 // up) and H = silu(Yg) * Yu, from their float32 sums, to g.hout ([M, N], row stride g.ldh).
-// kMulti: the rows have adapters of their own (mu; g.r is 0): after the walk over K, each wave adds
-// the low-rank term of its block straight from registers (multi_term, multi.h).
+// kMulti: the rows have adapters of their own (mu; g.r is 0) and are taken in the order of their
+// adapters, row m of the launch being row mu.perm[m] of X and Y: the copies of X gather, the store
+// scatters whole row pieces. After the walk over K, each wave adds the low-rank term of its block
+// straight from registers (multi_term, multi.h).
 template <int kFmt, bool kGrp, bool kPair = false, bool kMulti = false>
 __device__ __forceinline__ void fwd_body(const GemmArgs &g, const GroupArgs &gr, const MultiArgs &mu) {
   constexpr bool kDQ = kFmt == 1, kFP4 = kFmt == 2;
@@ -272,7 +274,7 @@ __device__ __forceinline__ void fwd_body(const GemmArgs &g, const GroupArgs &gr,
   const int rot = (int)(((m0 - m_lo) / kT) * 5 % kblk);
   auto phys = [&](int s) { return s + rot < kblk ? s + rot : s + rot - kblk; };
 
-  const __amdgpu_buffer_rsrc_t rX = make_rsrc(g.a_side + m0 * K, rows_m * K * 2);
+  const __amdgpu_buffer_rsrc_t rX = kMulti ? make_rsrc(g.a_side, g.M * K * 2) : make_rsrc(g.a_side + m0 * K, rows_m * K * 2);
   // pair: the buffers span the whole stacked weight, rows addressed per thread (rows past N read
   // as zero through out-of-range offsets)
   const int64_t wrows = kPair ? 2 * g.C : rows_n;
@@ -300,6 +302,7 @@ __device__ __forceinline__ void fwd_body(const GemmArgs &g, const GroupArgs &gr,
     const int row = 8 * (4 * wave + i) + (lane >> 3);
     const int c = (lane & 7) ^ rowx(row);
     xoff[i] = (uint32_t)(row * K * 2 + c * 16);
+    if constexpr (kMulti) xoff[i] = row < rows_m ? (uint32_t)(mu.perm[m0 + row] * K * 2 + c * 16) : 0xFFFFFF00u;
   }
   // Decode ownership: weight row wr of the tile, elements 32 wh .. 32 wh + 31 of each step.
   const int wr = tid >> 1, wh = tid & 1;
@@ -527,7 +530,7 @@ __device__ __forceinline__ void fwd_body(const GemmArgs &g, const GroupArgs &gr,
 #pragma unroll
       for (int mt = 0; mt < 8; ++mt) acc[nt][mt] *= tsc;
   }
-  if constexpr (kMulti) multi_term<4, 8>(acc, mu, m0 + wm * 128, m_hi, n0 + wn * 64, g.C);
+  if constexpr (kMulti) multi_term<4, 8>(acc, mu, mu.perm, m0 + wm * 128, m_hi, n0 + wn * 64, g.C);
   uint4 *blk = (wave >> 1) == 0 ? sX0 : (wave >> 1) == 1 ? sX1 : (wave >> 1) == 2 ? sW0 : sW1;
   blk += (wave & 1) * (kChunks / 2);
   uint2 *b2 = reinterpret_cast<uint2 *>(blk);
@@ -547,11 +550,13 @@ __device__ __forceinline__ void fwd_body(const GemmArgs &g, const GroupArgs &gr,
 #pragma unroll
     for (int i = 0; i < 16; ++i) {
       const int row = 8 * i + (lane >> 3);
-      const int64_t m = m0 + wm * 128 + row;
+      int64_t m = m0 + wm * 128 + row;
       const uint4 v = blk[swzf(row, c)];
-      if (wm * 128 + row < rows_m && ncol < g.C)
+      if (wm * 128 + row < rows_m && ncol < g.C) {
+        if constexpr (kMulti) m = mu.perm[m];
         __builtin_nontemporal_store(u32x4{v.x, v.y, v.z, v.w},
                                     reinterpret_cast<u32x4 *>(g.out + m * g.ldo + n));
+      }
     }
   }
   if (kPair) {
@@ -644,7 +649,8 @@ hipError_t launch_gemm_fwd(const GemmArgs &g, hipStream_t st) {
 }
 
 hipError_t launch_gemm_fwd_multi(const GemmArgs &g, const MultiArgs &mu, hipStream_t st) {
-  if (((g.C | g.ldo) & 7) != 0 || (reinterpret_cast<uintptr_t>(g.out) & 15) != 0 || g.r != 0)
+  if (((g.C | g.ldo) & 7) != 0 || (reinterpret_cast<uintptr_t>(g.out) & 15) != 0 || g.r != 0 || !mu.perm ||
+      g.M * g.R * 2 > kMultiMaxGather)
     return hipErrorInvalidValue;
   const int64_t tiles = ((g.C + kT - 1) / kT) * ((g.M + kT - 1) / kT);
   if (g.w.fp4)

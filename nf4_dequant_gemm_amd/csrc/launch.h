@@ -210,24 +210,45 @@ hipError_t launch_merge(const WDesc &w, const uint16_t *A, const uint16_t *B, in
                         const Tables &t, uint16_t *out, hipStream_t st);
 
 // The layer with an adapter of its own for every row (multi.h). Forward: g.r 0, mu.P = T, mu.Q = B
-// [L][N][r]; dX: mu.P = U, mu.Q = A transposed [L][K][r].
+// [L][N][r]; dX: mu.P = U, mu.Q = A transposed [L][K][r]; both take the rows through mu.perm and
+// reach kMultiMaxGather bytes of X (dY).
 hipError_t launch_gemm_fwd_multi(const GemmArgs &g, const MultiArgs &mu, hipStream_t st);
 hipError_t launch_gemm_dx_multi(const GemmArgs &g, const MultiArgs &mu, hipStream_t st);
 // The rows' order, and the thin products over it (multi.hip): out[i] = in[i] p_a^T for the rows i of
 // adapter a (zero without one), p_a = p + a * pstride of r rows of leading dimension ldp, with
 // splits * M * r partial floats; and out[a] = s[a] * (sum over its rows of P_i^T Q_i), [r][C] or
-// transposed [C][r], with L * splits * r * C partial floats (none for one split).
+// transposed [C][r], with L * splits * r * C partial floats (none for one split); P has row stride
+// ldp, a multiple of 8, zeros from r on.
 hipError_t launch_multi_plan(const int32_t *ids, int64_t M, int L, const MultiPlan &pl, hipStream_t st);
 int multi_rows_splits(int64_t M, int64_t Lr);
 hipError_t launch_multi_rows(const uint16_t *in, int64_t ldin, const uint16_t *p, int64_t pstride, int64_t ldp,
                              int64_t M, int64_t Lr, int r, int L, int splits, float *part, uint16_t *out,
                              const MultiPlan &pl, hipStream_t st);
+// The projection without the table, for at most kMultiSmallM rows (any order of ids), as partial sums
+// float [M][r][splits] of slices of the reduction.
+hipError_t launch_multi_rows_part(const uint16_t *in, int64_t ldin, const uint16_t *p, int64_t pstride, int64_t ldp,
+                                  const int32_t *ids, int64_t M, int64_t Lr, int r, int L, int splits, float *part,
+                                  hipStream_t st);
+// The forward's fused part for batches that do not fill the large kernel's grid (mid.hip), and the
+// float partials it needs.
+// With at most kMultiSmallM rows it forms T itself (A [L][ra][K], T [M][ra] written; mu.P unused),
+// with more T is given (mu.P; A and T unused).
+hipError_t launch_mid_fwd_multi(const GemmArgs &g, const MultiArgs &mu, const uint16_t *A, int ra, uint16_t *T,
+                                float *part, hipStream_t st);
+size_t mid_fwd_bytes(int64_t M, int64_t N, int64_t K, int rp);
+// The same for at most 16 rows of a double-quantised or E2M1 weight, K % 256 == 0 (decode16.hip), with T as
+// split partials float [M][r][tsplits] (launch_multi_rows_part), added inside and written to tout.
+hipError_t launch_stream16_fwd_multi(const GemmArgs &g, const MultiArgs &mu, const float *tpart, int tsplits,
+                                     uint16_t *tout, hipStream_t st);
 int multi_sum_splits(int64_t M, int64_t C, int L);
-hipError_t launch_multi_sum(const uint16_t *P, const uint16_t *Q, int64_t ldq, int64_t C, int r, int L,
+hipError_t launch_multi_sum(const uint16_t *P, int64_t ldp, const uint16_t *Q, int64_t ldq, int64_t C, int r, int L,
                             const float *s, int splits, float *part, uint16_t *out, bool transposed,
                             const MultiPlan &pl, hipStream_t st);
-// dst[b][c][j] = src[b][j][c] of `batch` bf16 matrices [R][C].
-hipError_t launch_multi_transpose(const uint16_t *src, int64_t R, int64_t C, int batch, uint16_t *dst, hipStream_t st);
+// dst[b][c][j] = src[b][j][c] of `batch` bf16 matrices [R][C], rows of dst padded with zeros to ldd; and
+// dst [rows][rp] = src [rows][r] padded with zeros.
+hipError_t launch_multi_transpose(const uint16_t *src, int64_t R, int64_t C, int64_t ldd, int batch, uint16_t *dst,
+                                  hipStream_t st);
+hipError_t launch_multi_pad(const uint16_t *src, int64_t rows, int r, int rp, uint16_t *dst, hipStream_t st);
 
 // Norm and rotation of query and key heads (headnorm.hip). One side (q or k): element strides of a
 // token (ts) and a head (hs), the d elements of a head contiguous; heads == 0: no such side.

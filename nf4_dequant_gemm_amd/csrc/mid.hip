@@ -1,0 +1,557 @@
+// Forward of the layer with an adapter of its own for every row, for the batches between one row and a
+// full grid of 256 x 256 tiles: Y = X deq(W)^T + s_a T B_a^T (gfx950).
+//
+// At these sizes the large kernel has too few tiles for the 256 CUs and the 16-row stream kernel takes
+// too few rows. A workgroup of 8 waves takes 16 kMT rows and 32 kNW columns: kNW waves side by side,
+// each 32 columns, times kKW = 8 / kNW waves that take turns along K, in steps of kBlk blocks of 64.
+//   * Weight codes go straight to the registers of the lanes that multiply them: lane (g, l) of a
+//     16-row tile loads 16 bytes of row l for each 128 elements (whole 64-byte runs of a row), and two
+//     v_permlane32_swap hand every lane 8 bytes of each of the two blocks, so that an MFMA sees one
+//     block only.
+//   * NF4: a code byte (two elements) becomes a pair of unscaled bf16 levels by one lookup in a
+//     256-entry LDS table held 64 times (entry e of copy c at byte 256 e + 4 c: a byte permute forms
+//     the address, every lane has its own bank); the block constant scales the block's float32 sum.
+//     That is one vector instruction and one LDS read for two elements, where decoding through a table
+//     of scaled values in registers takes nine: the 16-row launch of a 4096 x 4096 weight took 33 us
+//     that way.
+//   * E2M1: a lane's 8 bytes are one group of 16. The values times the group scale are exact in bf16;
+//     the tensor scale multiplies the sums at the end.
+//   * X goes to LDS by DMA, 16-byte chunk c of a row's 256 bytes (128 elements) at slot c ^ (row % 16),
+//     which gives the 16 rows of an operand read distinct slots of the 256-byte bank window.
+//   * Codes, constants and X of the next two steps are in flight during a step; one barrier per step.
+// The kKW sums of a tile meet in LDS, in wave order, which also turns them round for whole row pieces.
+// With few tiles the reduction is also split over workgroups, which write float32 sums that
+// mid_final_kernel adds in order.
+//
+// T of at most 256 rows is formed in the same launch, by workgroups of their own (the first ones) that
+// each take 1024 elements of the reduction for 16 rows of an adapter (multi_rows_of) and write float32
+// sums: a launch for T alone took 6 to 9 us, and nothing here needs T before the end. mid_final_kernel
+// then adds both kinds of sums, applies the low-rank term and writes Y and T. More rows bring T from
+// its own launch, and an unsplit reduction then finishes Y itself.
+#include "common.h"
+#include "launch.h"
+#include "multi.h"
+
+namespace nf4q {
+namespace {
+
+constexpr int kThreads = 512;
+
+struct MidArgs {
+  const uint16_t *X;
+  WDesc w;
+  int64_t M, N, K;
+  uint16_t *Y;         // [M][N]
+  float *part;         // [splits][M][N] unless the launch finishes Y itself
+  int splits;
+  bool finish;         // Y is finished in the launch (one split, T in memory)
+  Tables t;
+  // T formed in the launch (tsplits > 0): its first tblocks workgroups
+  const uint16_t *A;   // [L][ra][K]
+  int ra;              // rank (mu.r: padded to a multiple of 8)
+  int tblocks, tsplits;
+  float *tpart;        // [tsplits][M][mu.r]
+  uint16_t *T;         // [M][ra], written by mid_final_kernel
+};
+constexpr int kTSlice = 1024;   // reduction elements of a workgroup that forms T
+
+// Y columns n .. n + 3 of row m from float32 sums.
+__device__ __forceinline__ void store4(uint16_t *Y, int64_t N, int64_t m, int64_t n, const f32x4 &a) {
+  *reinterpret_cast<uint2 *>(Y + m * N + n) = make_uint2(pack_bf16x2(a[0], a[1]), pack_bf16x2(a[2], a[3]));
+}
+
+// The tensor scale of an E2M1 weight (1 for an all-zero weight, whose group scales are all 0).
+__device__ __forceinline__ float tensor_scale(const WDesc &w) {
+  const float S = *w.scale;
+  return S > 0.f ? S : 1.f;
+}
+
+struct Pair {
+  uint32_t a, b;
+};
+// (a, b) -> a's lower 32 lanes with b's lower 32 lanes above them, a's upper with b's upper above.
+__device__ __forceinline__ Pair swap_halves(uint32_t a, uint32_t b) {
+  const auto r = __builtin_amdgcn_permlane32_swap(a, b, false, false);
+  return Pair{r[0], r[1]};
+}
+
+// kFmt: 0 NF4 with float32 constants, 1 NF4 double-quantised, 2 E2M1. kMT: row tiles of 16. kBlk: blocks
+// of a wave's step (2 or 4). kAl: K is a multiple of 64 kBlk, so that a row's constants of a step are
+// one aligned piece (double-quantised: with one run scale); otherwise they are loaded one by one and
+// the last step may hold blocks past K, whose X reads as zero.
+template <int kFmt, int kMT, int kNW, int kBlk, bool kAl>
+__global__ __launch_bounds__(kThreads) void mid_kernel(MidArgs g, MultiArgs mu) {
+  constexpr bool kDQ = kFmt == 1, kFP4 = kFmt == 2;
+  constexpr int kKW = 8 / kNW, kH = kBlk / 2;       // 128-element halves of a step
+  constexpr int kMX = kBlk == 2 ? (kMT + 1) / 2 * 2 : kMT;   // row tiles of X copied: whole pieces for 8 waves
+  constexpr int kHalf = kMX * 16 * 16;              // 16-byte chunks of one half's X
+  constexpr int kSlice = kH * kHalf;                // of one wave step's
+  constexpr int kPieces = kKW * kSlice / 64;        // 1 KB DMA pieces per step
+  static_assert(kPieces % 8 == 0, "every wave issues the same copies");
+  // Vector-memory operations a wave issues per step: its copies, the codes and the constants. The wait
+  // at the start of a step leaves those of the step after it in flight.
+  constexpr int kStepLoads =
+      kPieces / 8 + 2 * (kH + (kAl ? (kDQ ? 2 : 1) : kBlk * (kDQ ? 2 : 1)));
+  // separate arrays, so that the compiler does not take reads of one for reads of a copy in flight
+  __shared__ uint4 sX0[kKW * kSlice], sX1[kKW * kSlice], sX2[kKW * kSlice];
+  // the level table; at the end the sums of a row tile: [wave][row][32 columns, padded to 36]
+  constexpr int kPad = 36, kTiles = kKW == 1 ? 1 : kMT;   // row tiles in LDS at a time
+  constexpr int kSums = 8 * kTiles * 16 * kPad, kTab = kFP4 ? 0 : 256 * 64;
+  __shared__ __align__(16) uint32_t stab[kSums > kTab ? kSums : kTab];
+  int block = blockIdx.x;
+  if (block < g.tblocks) {
+    static_assert(kMultiSmallT<8, 2> <= sizeof(stab), "T's sums fit the table");
+    const int nj = (mu.r + 31) / 32;
+    const int ts = block % g.tsplits, j = block / g.tsplits % nj, row = block / g.tsplits / nj;
+    const int64_t le = (int64_t)(ts + 1) * kTSlice;
+    float *tp = g.tpart + (int64_t)ts * g.M * mu.r;
+    multi_rows_of<8, 2, 4>(g.X, g.K, g.A, (int64_t)g.ra * g.K, g.K, mu.ids, (int)g.M, (int64_t)ts * kTSlice,
+                           le < g.K ? le : g.K, g.ra, mu.r, mu.L, row, j * 32, stab,
+                           [&](int i, int jj, float s) { tp[(int64_t)i * mu.r + jj] = s; });
+    return;
+  }
+  block -= g.tblocks;
+  const int cols = (int)((g.N + 32 * kNW - 1) / (32 * kNW)), rowb = (int)((g.M + 16 * kMT - 1) / (16 * kMT));
+  const int bx = block % cols, by = block / cols % rowb, bz = block / cols / rowb;
+  const int tid = threadIdx.x, lane = tid & 63;
+  const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const int nw = wave % kNW, kw = wave / kNW;
+  const int g16 = lane >> 4, l16 = lane & 15;
+  const int64_t K = g.K, N = g.N;
+  const int kblk = (int)(K / 64);
+  const int64_t n0 = (int64_t)bx * 32 * kNW + 32 * nw;   // this wave's columns
+  const int64_t m0 = (int64_t)by * 16 * kMT;
+  const int64_t rows_m = g.M - m0 < 16 * kMT ? g.M - m0 : 16 * kMT;
+  const int64_t rows_n = n0 >= N ? 0 : N - n0 < 32 ? N - n0 : 32;
+  const int64_t nb = n0 < N ? n0 : 0;               // a wave past the last column reads nothing
+  // this workgroup's steps [sbeg, send); wave kw takes sbeg + kw, + kKW, ...
+  const int nsteps = (kblk + kBlk - 1) / kBlk;
+  const int sbeg = (int)((int64_t)bz * nsteps / g.splits);
+  const int send = (int)((int64_t)(bz + 1) * nsteps / g.splits);
+  const int iters = (send - sbeg + kKW - 1) / kKW;
+  constexpr uint32_t kNone = 0x80000000u;           // an offset outside every buffer: reads zero
+
+  const __amdgpu_buffer_rsrc_t rX = make_rsrc(g.X + m0 * K, rows_m * K * 2);
+  const __amdgpu_buffer_rsrc_t rC = make_rsrc(g.w.codes + nb * (K / 2), rows_n * (K / 2));
+  const __amdgpu_buffer_rsrc_t rQ =
+      kFP4  ? make_rsrc(reinterpret_cast<const uint8_t *>(g.w.absmax) + nb * (K / 16), rows_n * (K / 16))
+      : kDQ ? make_rsrc(reinterpret_cast<const int8_t *>(g.w.absmax) + nb * kblk, rows_n * kblk)
+            : make_rsrc(reinterpret_cast<const float *>(g.w.absmax) + nb * kblk, rows_n * kblk * 4);
+  const int64_t nruns = (g.w.n * kblk + 255) / 256;
+  const __amdgpu_buffer_rsrc_t rS = make_rsrc(g.w.scale, kDQ ? nruns * 4 : 0);
+
+  // X pieces of 1 KB: four rows of one half; lane L writes LDS chunk L % 16 of row 4 q + L / 16, which
+  // holds the row's chunk (L % 16) ^ (row % 16).
+  auto dma_x = [&](int it, uint4 *dst) {
+#pragma unroll
+    for (int i = 0; i < kPieces / 8; ++i) {
+      const int p = wave + 8 * i;
+      const int half = p / (4 * kMX), q = p % (4 * kMX);   // half of the kKW kH of this step
+      const int row = 4 * q + (lane >> 4);
+      const int chunk = (lane & 15) ^ (row & 15);
+      const int st = sbeg + it * kKW + half / kH;
+      const int k = (st * kH + half % kH) * 128 + chunk * 8;
+      // rows past M, steps past the end and chunks past K read as zero (the last by arithmetic: as a
+      // condition it made the compiler spill 200 registers)
+      uint32_t off = st < send ? (uint32_t)((row * K + k) * 2) : kNone;
+      if (!kAl) off |= (uint32_t)(((int)K - 1 - k) >> 31) & kNone;
+      __builtin_amdgcn_raw_ptr_buffer_load_lds(rX, (__attribute__((address_space(3))) void *)(dst + p * 64), 16, off,
+                                               0, 0, 0);
+    }
+  };
+  struct Codes {
+    u32x4 c[2][kH];
+    uint32_t q[2][kBlk];   // NF4: int8 code or float bits of each block; E2M1: its four group scales
+    uint32_t s[2][kAl ? 1 : kBlk];
+  };
+  // byte of the lane's codes and first block of its row, in the wave's rows (and, for the run scales, in
+  // the weight: blocks fit 32 bits)
+  uint32_t cbase[2], bbase[2];
+#pragma unroll
+  for (int nt = 0; nt < 2; ++nt) {
+    cbase[nt] = (uint32_t)((nt * 16 + l16) * (K / 2) + 16 * g16);
+    bbase[nt] = (uint32_t)((nt * 16 + l16) * kblk);
+  }
+  const uint32_t wblk = (uint32_t)(nb * kblk);
+  auto load_c = [&](int it, Codes &c) {
+    const int st = sbeg + it * kKW + kw;
+    const bool in = st < send;
+#pragma unroll
+    for (int nt = 0; nt < 2; ++nt) {
+#pragma unroll
+      for (int h = 0; h < kH; ++h)
+        c.c[nt][h] = __builtin_amdgcn_raw_buffer_load_b128(
+            rC, in ? cbase[nt] + (st * kH + h) * 64 : kNone, 0, 0);
+      const uint32_t b0 = bbase[nt] + st * kBlk;
+      if constexpr (kAl) {
+        if constexpr (kDQ) {
+          c.q[nt][0] = kBlk == 4 ? __builtin_amdgcn_raw_buffer_load_b32(rQ, in ? b0 : kNone, 0, 0)
+                                 : __builtin_amdgcn_raw_buffer_load_b16(rQ, in ? b0 : kNone, 0, 0);
+          c.s[nt][0] = __builtin_amdgcn_raw_buffer_load_b32(rS, ((wblk + b0) >> 8) * 4, 0, 0);
+        } else if constexpr (kBlk == 4) {
+          const u32x4 v = __builtin_amdgcn_raw_buffer_load_b128(rQ, in ? b0 * 4 : kNone, 0, 0);
+#pragma unroll
+          for (int b = 0; b < 4; ++b) c.q[nt][b] = v[b];
+        } else {
+          const u32x2 v = __builtin_amdgcn_raw_buffer_load_b64(rQ, in ? b0 * 4 : kNone, 0, 0);
+          c.q[nt][0] = v[0];
+          c.q[nt][1] = v[1];
+        }
+      } else {
+#pragma unroll
+        for (int b = 0; b < kBlk; ++b) {
+          if constexpr (kDQ) {
+            c.q[nt][b] = __builtin_amdgcn_raw_buffer_load_b8(rQ, in ? b0 + b : kNone, 0, 0);
+            c.s[nt][b] = __builtin_amdgcn_raw_buffer_load_b32(rS, ((wblk + b0 + b) >> 8) * 4, 0, 0);
+          } else {
+            c.q[nt][b] = __builtin_amdgcn_raw_buffer_load_b32(rQ, in ? (b0 + b) * 4 : kNone, 0, 0);
+          }
+        }
+      }
+    }
+  };
+
+  f32x4 acc[2][kMT];   // lane (g16, l16): rows 16 mt + 4 g16 + v of column 16 nt + l16
+#pragma unroll
+  for (int nt = 0; nt < 2; ++nt)
+#pragma unroll
+    for (int mt = 0; mt < kMT; ++mt) acc[nt][mt] = f32x4{0.f, 0.f, 0.f, 0.f};
+
+  const uint32_t copy = (uint32_t)lane * 4;
+  const char *tab = reinterpret_cast<const char *>(stab);
+  // after the swap lane group g holds elements 16 sg .. 16 sg + 15 of a block, sg = 0, 2, 1, 3
+  const int sg = ((g16 & 1) << 1) | (g16 >> 1);
+
+  auto compute = [&](const Codes &c, const uint4 *sX) {
+    const uint4 *mine = sX + kw * kSlice;
+#pragma unroll
+    for (int h = 0; h < kH; ++h) {
+      Pair lo[2], hi[2];   // [nt]: the lane's 8 bytes of the half's first and second block
+#pragma unroll
+      for (int nt = 0; nt < 2; ++nt) {
+        const Pair x = swap_halves(c.c[nt][h][0], c.c[nt][h][2]);
+        const Pair y = swap_halves(c.c[nt][h][1], c.c[nt][h][3]);
+        lo[nt] = Pair{x.a, y.a};
+        hi[nt] = Pair{x.b, y.b};
+      }
+#pragma unroll
+      for (int b = 0; b < 2; ++b) {
+        const int blk = 2 * h + b;
+        bf16x8 w[2][2];
+        float a[2];
+#pragma unroll
+        for (int nt = 0; nt < 2; ++nt) {
+          const Pair d = b ? hi[nt] : lo[nt];
+          if constexpr (kFP4) {
+            const float s = __builtin_amdgcn_cvt_f32_fp8((int)(c.q[nt][blk] >> (8 * sg)), 0);
+            auto pairs = [&](uint32_t v, uint32_t o[4]) {   // bytes hold the earlier element in the high nibble
+              const uint32_t u = ((v >> 4) & 0x0F0F0F0Fu) | ((v << 4) & 0xF0F0F0F0u);
+              const f32x2 p0 = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(u, 1.f, 0);
+              const f32x2 p1 = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(u, 1.f, 1);
+              const f32x2 p2 = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(u, 1.f, 2);
+              const f32x2 p3 = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(u, 1.f, 3);
+              o[0] = pack_bf16x2(p0[0] * s, p0[1] * s);
+              o[1] = pack_bf16x2(p1[0] * s, p1[1] * s);
+              o[2] = pack_bf16x2(p2[0] * s, p2[1] * s);
+              o[3] = pack_bf16x2(p3[0] * s, p3[1] * s);
+            };
+            uint32_t o[8];
+            pairs(d.a, o);
+            pairs(d.b, o + 4);
+            w[nt][0] = __builtin_bit_cast(bf16x8, make_uint4(o[0], o[1], o[2], o[3]));
+            w[nt][1] = __builtin_bit_cast(bf16x8, make_uint4(o[4], o[5], o[6], o[7]));
+          } else {
+            uint32_t o[8];
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+              const uint32_t at = perm(i < 4 ? d.a : d.b, copy, 0x0C0C0400u | ((4u + (i & 3)) << 8));
+              o[i] = *reinterpret_cast<const uint32_t *>(tab + at);
+            }
+            w[nt][0] = __builtin_bit_cast(bf16x8, make_uint4(o[0], o[1], o[2], o[3]));
+            w[nt][1] = __builtin_bit_cast(bf16x8, make_uint4(o[4], o[5], o[6], o[7]));
+            if constexpr (kDQ)
+              a[nt] = int8_code(kAl ? c.q[nt][0] >> (8 * blk) : c.q[nt][blk]) * __uint_as_float(c.s[nt][kAl ? 0 : blk]);
+            else
+              a[nt] = __uint_as_float(c.q[nt][blk]);
+          }
+        }
+#pragma unroll
+        for (int mt = 0; mt < kMT; ++mt) {
+          const uint4 *row = mine + h * kHalf + (mt * 16 + l16) * 16;
+          const bf16x8 x0 = __builtin_bit_cast(bf16x8, row[(8 * b + 2 * sg) ^ l16]);
+          const bf16x8 x1 = __builtin_bit_cast(bf16x8, row[(8 * b + 2 * sg + 1) ^ l16]);
+#pragma unroll
+          for (int nt = 0; nt < 2; ++nt) {
+            if constexpr (kFP4) {
+              acc[nt][mt] = mfma16x16x32(x0, w[nt][0], acc[nt][mt]);
+              acc[nt][mt] = mfma16x16x32(x1, w[nt][1], acc[nt][mt]);
+            } else {
+              f32x4 part = mfma16x16x32(x0, w[nt][0], f32x4{0.f, 0.f, 0.f, 0.f});
+              part = mfma16x16x32(x1, w[nt][1], part);
+#pragma unroll
+              for (int v = 0; v < 4; ++v) acc[nt][mt][v] += a[nt] * part[v];
+            }
+          }
+        }
+      }
+    }
+  };
+
+  // Step it: wait for its X and codes (requested two steps ago; those of the next step stay in flight),
+  // barrier (everyone's copies have landed and everyone is done with the step before, whose buffer
+  // takes the next copies), request step it + 2, multiply.
+  Codes c0, c1, c2;
+  auto step = [&](int it, uint4 *cur, uint4 *next, Codes &c, Codes &cn) {
+    asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)\n\ts_barrier" ::"n"(kStepLoads) : "memory");
+    __builtin_amdgcn_sched_barrier(0);
+    dma_x(it + 2, next);   // past the last step: zeros, into a buffer nobody reads any more
+    load_c(it + 2, cn);
+    __builtin_amdgcn_sched_barrier(0);   // the decode of this step stays behind the requests
+    compute(c, cur);
+    __builtin_amdgcn_sched_barrier(0);
+  };
+  dma_x(0, sX0);
+  load_c(0, c0);
+  __builtin_amdgcn_sched_barrier(0);
+  dma_x(1, sX1);
+  load_c(1, c1);
+  __builtin_amdgcn_sched_barrier(0);
+  if constexpr (!kFP4) {   // uint4 i of the table: four copies of entry i / 16
+    float *lv = reinterpret_cast<float *>(sX2);   // its first copy is requested after the first barrier
+    if (tid == 0) {
+#pragma unroll
+      for (int j = 0; j < 16; ++j) lv[j] = g.t.level[j];
+    }
+    asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory");
+    for (int i = tid; i < 256 * 16; i += kThreads) {
+      const uint32_t v = pack_bf16x2(lv[i >> 8], lv[(i >> 4) & 15]);
+      reinterpret_cast<uint4 *>(stab)[i] = make_uint4(v, v, v, v);
+    }
+  }
+  int it = 0;
+#pragma unroll 1
+  for (; it + 3 <= iters; it += 3) {
+    step(it, sX0, sX2, c0, c2);
+    step(it + 1, sX1, sX0, c1, c0);
+    step(it + 2, sX2, sX1, c2, c1);
+  }
+  if (it < iters) step(it, sX0, sX2, c0, c2);
+  if (it + 1 < iters) step(it + 1, sX1, sX0, c1, c0);
+  // the copies of the steps past the end have landed, and everyone is done with the table
+  asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)\n\ts_barrier" ::: "memory");
+
+  // Wave (nw, kw) adds the kKW sums of its columns for row tiles kw, kw + kKW, ... and reads 4 columns
+  // of a row at a time.
+  float *sums = reinterpret_cast<float *>(stab);
+  auto park = [&](int mt) {
+    float *p = sums + ((wave * kTiles + mt % kTiles) * 16 + 4 * g16) * kPad + l16;
+#pragma unroll
+    for (int nt = 0; nt < 2; ++nt)
+#pragma unroll
+      for (int v = 0; v < 4; ++v) p[v * kPad + 16 * nt] = acc[nt][mt][v];
+  };
+  const float tsc = kFP4 ? tensor_scale(g.w) : 1.f;
+  auto finish = [&](int mt) {
+    f32x4 y[2][1];
+#pragma unroll
+    for (int nt = 0; nt < 2; ++nt) {
+      auto at = [&](int k) {
+        return *reinterpret_cast<const f32x4 *>(
+            sums + (((k * kNW + nw) * kTiles + mt % kTiles) * 16 + l16) * kPad + 16 * nt + 4 * g16);
+      };
+      y[nt][0] = at(kKW == 1 ? kw : 0);
+#pragma unroll
+      for (int k = 1; k < kKW; ++k) y[nt][0] += at(k);
+      if (kFP4) y[nt][0] *= tsc;
+    }
+    const int64_t mb = m0 + mt * 16, m = mb + l16;
+    if (g.finish) {
+      int id = m < g.M ? mu.ids[m] : -1;
+      id = id >= 0 && id < mu.L ? id : -1;
+      int64_t rows = g.M - mb;
+      rows = rows < 0 ? 0 : rows < 16 ? rows : 16;
+      const __amdgpu_buffer_rsrc_t rT = make_rsrc(mu.P + mb * mu.r, rows * mu.r * 2);
+      f32x4 z[2] = {y[0][0], y[1][0]};
+      multi_term_rows<4>(z, mu, id, n0, N, [&](int j) { return rank_frag(rT, l16, j, mu.r); });
+      y[0][0] = z[0];
+      y[1][0] = z[1];
+    }
+#pragma unroll
+    for (int nt = 0; nt < 2; ++nt) {
+      const int64_t n = n0 + nt * 16 + 4 * g16;
+      if (m < g.M && n < N) {
+        if (g.finish)
+          store4(g.Y, N, m, n, y[nt][0]);
+        else
+          *reinterpret_cast<f32x4 *>(g.part + ((int64_t)bz * g.M + m) * N + n) = y[nt][0];
+      }
+    }
+  };
+  if constexpr (kKW == 1) {   // a wave's own tile: its LDS accesses are in order
+#pragma unroll
+    for (int mt = 0; mt < kMT; ++mt) {
+      park(mt);
+      __builtin_amdgcn_wave_barrier();
+      finish(mt);
+      __builtin_amdgcn_wave_barrier();
+    }
+  } else {
+#pragma unroll
+    for (int mt = 0; mt < kMT; ++mt) park(mt);
+    __syncthreads();
+#pragma unroll 1
+    for (int mt = kw; mt < kMT; mt += kKW) finish(mt);
+  }
+}
+
+// Y from the float32 sums of the launch before, added in order, and the low-rank term, with T from its
+// own sums (written here, by the workgroups of the first columns) or from memory. One wave: 16 rows
+// and 64 columns.
+__global__ __launch_bounds__(64) void mid_final_kernel(MidArgs g, MultiArgs mu) {
+  const int lane = threadIdx.x, g16 = lane >> 4, l16 = lane & 15;
+  const int64_t m0 = (int64_t)blockIdx.y * 16, m = m0 + l16, n0 = (int64_t)blockIdx.x * 64;
+  int id = m < g.M ? mu.ids[m] : -1;
+  id = id >= 0 && id < mu.L ? id : -1;
+  f32x4 y[4];
+#pragma unroll
+  for (int nt = 0; nt < 4; ++nt) y[nt] = f32x4{0.f, 0.f, 0.f, 0.f};
+  const f32x4 zero = {0.f, 0.f, 0.f, 0.f};
+  for (int s0 = 0; s0 < g.splits; s0 += 4) {   // 16 loads at a time
+    f32x4 v[4][4];
+#pragma unroll
+    for (int s = 0; s < 4; ++s)
+#pragma unroll
+      for (int nt = 0; nt < 4; ++nt) {
+        const int64_t n = n0 + nt * 16 + 4 * g16;
+        v[s][nt] = s0 + s < g.splits && m < g.M && n < g.N
+                       ? *reinterpret_cast<const f32x4 *>(g.part + ((int64_t)(s0 + s) * g.M + m) * g.N + n)
+                       : zero;
+      }
+#pragma unroll
+    for (int s = 0; s < 4; ++s)
+#pragma unroll
+      for (int nt = 0; nt < 4; ++nt) y[nt] += v[s][nt];
+  }
+  int64_t rows = g.M - m0;
+  rows = rows < 16 ? rows : 16;
+  const __amdgpu_buffer_rsrc_t rT = make_rsrc(mu.P + m0 * mu.r, g.tsplits ? 0 : rows * mu.r * 2);
+  multi_term_rows<4>(y, mu, id, n0, g.N, [&](int j) {
+    if (!g.tsplits) return rank_frag(rT, l16, j, mu.r);
+    f32x4 a = zero, b = zero;
+    if (m < g.M && j < mu.r) {
+      const float *tp = g.tpart + m * mu.r + j;
+      for (int t = 0; t < g.tsplits; ++t, tp += g.M * mu.r) {
+        a += *reinterpret_cast<const f32x4 *>(tp);
+        b += *reinterpret_cast<const f32x4 *>(tp + 4);
+      }
+      if (blockIdx.x == 0) {
+#pragma unroll
+        for (int e = 0; e < 8; ++e)
+          if (j + e < g.ra) g.T[m * g.ra + j + e] = (uint16_t)(pack_bf16x2(e < 4 ? a[e & 3] : b[e & 3], 0.f) & 0xFFFFu);
+      }
+    }
+    return __builtin_bit_cast(bf16x8, make_uint4(pack_bf16x2(a[0], a[1]), pack_bf16x2(a[2], a[3]),
+                                                 pack_bf16x2(b[0], b[1]), pack_bf16x2(b[2], b[3])));
+  });
+#pragma unroll
+  for (int nt = 0; nt < 4; ++nt) {
+    const int64_t n = n0 + nt * 16 + 4 * g16;
+    if (m < g.M && n < g.N) store4(g.Y, g.N, m, n, y[nt]);
+  }
+}
+
+template <int kMT, int kNW, int kBlk, bool kAl>
+void launch_fmt(const MidArgs &a, const MultiArgs &mu, unsigned grid, hipStream_t st) {
+  if (a.w.fp4)
+    mid_kernel<2, kMT, kNW, kBlk, kAl><<<dim3(grid), dim3(kThreads), 0, st>>>(a, mu);
+  else if (a.w.dq)
+    mid_kernel<1, kMT, kNW, kBlk, kAl><<<dim3(grid), dim3(kThreads), 0, st>>>(a, mu);
+  else
+    mid_kernel<0, kMT, kNW, kBlk, kAl><<<dim3(grid), dim3(kThreads), 0, st>>>(a, mu);
+}
+
+// The split of a launch: rows of a workgroup (up to 8 row tiles of 16; as many for every row block as
+// the rows need), waves side by side, blocks of a step (what the LDS holds three times beside the
+// table) and splits of the reduction.
+struct MidShape {
+  int mt, nw, blk, splits;
+  bool al;
+};
+MidShape mid_shape(int64_t M, int64_t N, int64_t K) {
+  MidShape s;
+  const int64_t t = (M + 15) / 16;
+  const int64_t row_blocks = (t + 7) / 8;
+  s.mt = (int)((t + row_blocks - 1) / row_blocks);
+  s.blk = s.mt <= 4 ? 4 : 2;
+  s.al = K % (64 * s.blk) == 0;
+  if (!s.al) s.mt = s.mt <= 2 ? s.mt : s.mt <= 4 ? 4 : 8;   // the other heights are built for aligned K only
+  s.nw = s.mt <= 2 ? 4 : 8;
+  const int64_t kw = 8 / s.nw;
+  const int64_t wgs = (M + 16 * s.mt - 1) / (16 * s.mt) * ((N + 32 * s.nw - 1) / (32 * s.nw));
+  const int64_t steps = (K / 64 + s.blk - 1) / s.blk;
+  // Splits: the least of (rounds of 256 workgroups) x (start and end of one, and its steps) plus the
+  // traffic of the float32 sums, in us, from the times measured for 16 to 128 rows.
+  const double per_step = 0.5 + 0.35 * s.mt * s.blk / 4;
+  double best = 0;
+  s.splits = 1;
+  for (int64_t sp = 1; sp <= 16 && sp * kw <= steps; ++sp) {
+    const int64_t rounds = (wgs * sp + 255) / 256, it = (steps + sp * kw - 1) / (sp * kw);
+    const double us = rounds * (4.0 + it * per_step) + sp * M * N * 8 / 4.0e6;
+    if (sp == 1 || us < best) {
+      best = us;
+      s.splits = (int)sp;
+    }
+  }
+  return s;
+}
+
+size_t up256(size_t x) { return (x + 255) & ~size_t(255); }
+int mid_tsplits(int64_t M, int64_t K) { return M <= kMultiSmallM ? (int)((K + kTSlice - 1) / kTSlice) : 0; }
+
+}  // namespace
+
+size_t mid_fwd_bytes(int64_t M, int64_t N, int64_t K, int rp) {
+  const MidShape s = mid_shape(M, N, K);
+  const int ts = mid_tsplits(M, K);
+  return up256(s.splits > 1 || ts ? (size_t)s.splits * M * N * 4 : 0) + (size_t)ts * M * rp * 4;
+}
+
+hipError_t launch_mid_fwd_multi(const GemmArgs &ga, const MultiArgs &mu, const uint16_t *A, int ra, uint16_t *T,
+                                float *part, hipStream_t st) {
+  if ((ga.C & 7) != 0 || ga.ldo != ga.C || ga.M < 1 || ga.R % 64 != 0 || (mu.r & 7) != 0 || ra > mu.r)
+    return hipErrorInvalidValue;
+  const MidShape s = mid_shape(ga.M, ga.C, ga.R);
+  MidArgs a{ga.a_side, ga.w, ga.M, ga.C, ga.R, ga.out, part, s.splits, false, ga.t, A, ra, 0, 0, nullptr, T};
+  a.tsplits = mid_tsplits(ga.M, ga.R);
+  a.finish = s.splits == 1 && a.tsplits == 0;
+  if (a.tsplits) {
+    a.tblocks = (int)ga.M * ((mu.r + 31) / 32) * a.tsplits;
+    a.tpart = reinterpret_cast<float *>(reinterpret_cast<char *>(part) + up256((size_t)s.splits * ga.M * ga.C * 4));
+  }
+  const int64_t rows = (ga.M + 16 * s.mt - 1) / (16 * s.mt);
+  const int64_t wgs = a.tblocks + rows * ((ga.C + 32 * s.nw - 1) / (32 * s.nw)) * s.splits;
+  if (wgs >= (int64_t(1) << 31)) return hipErrorInvalidValue;
+  const unsigned grid = (unsigned)wgs;
+#define MID_AL(MT, NW, BLK) launch_fmt<MT, NW, BLK, true>(a, mu, grid, st)
+#define MID_ANY(MT, NW, BLK) s.al ? MID_AL(MT, NW, BLK) : launch_fmt<MT, NW, BLK, false>(a, mu, grid, st)
+  switch (s.mt) {
+    case 1: MID_ANY(1, 4, 4); break;
+    case 2: MID_ANY(2, 4, 4); break;
+    case 3: MID_AL(3, 8, 4); break;
+    case 4: MID_ANY(4, 8, 4); break;
+    case 5: MID_AL(5, 8, 2); break;
+    case 6: MID_AL(6, 8, 2); break;
+    case 7: MID_AL(7, 8, 2); break;
+    default: MID_ANY(8, 8, 2); break;
+  }
+#undef MID_ANY
+#undef MID_AL
+  hipError_t e = hipGetLastError();
+  if (e != hipSuccess || a.finish) return e;
+  const int64_t tiles = (ga.M + 15) / 16;
+  if (tiles > 65535) return hipErrorInvalidValue;
+  mid_final_kernel<<<dim3((unsigned)((ga.C + 63) / 64), (unsigned)tiles), dim3(64), 0, st>>>(a, mu);
+  return hipGetLastError();
+}
+
+}  // namespace nf4q

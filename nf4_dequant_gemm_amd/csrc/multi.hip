@@ -286,6 +286,20 @@ __global__ __launch_bounds__(256) void multi_rows64_kernel(const uint16_t *__res
   }
 }
 
+// The same product for a batch of at most kMultiSmallM rows without the table of the rows' order
+// (multi_rows_of): one workgroup for each 16 rows of an adapter, 32 ranks and slice of the reduction, so
+// that a decode step's few adapters are read by many CUs; partial sums [M][r][splits].
+__global__ __launch_bounds__(512) void multi_rows_part_kernel(const uint16_t *__restrict__ in, int64_t ldin,
+                                                              const uint16_t *__restrict__ p, int64_t pstride,
+                                                              int64_t ldp, const int32_t *__restrict__ ids, int M,
+                                                              int64_t Lr, int r, int L, float *__restrict__ part) {
+  __shared__ __align__(16) uint8_t lds[kMultiSmallT<8, 2>];
+  const int splits = gridDim.z, s = blockIdx.z;
+  const int64_t per = ((Lr + splits - 1) / splits + 31) / 32 * 32, lb = s * per, le = lb + per < Lr ? lb + per : Lr;
+  multi_rows_of<8, 2, 4>(in, ldin, p, pstride, ldp, ids, M, lb, le, r, r, L, blockIdx.x, blockIdx.y * 32, lds,
+                         [&](int row, int j, float v) { part[((int64_t)row * r + j) * splits + s] = v; });
+}
+
 // out = bf16(sum over the splits of part [splits][n]), in split order.
 __global__ void multi_rows_sum_kernel(const float *__restrict__ part, int64_t n, int splits,
                                       uint16_t *__restrict__ out) {
@@ -320,7 +334,7 @@ __device__ __forceinline__ s16x4 lds_tr(const uint16_t *p) {
 
 template <int TJ>
 __global__ __launch_bounds__(256) void multi_sum_kernel(const uint16_t *__restrict__ P,
-                                                        const uint16_t *__restrict__ Q, int64_t ldq,
+                                                        int64_t ldp, const uint16_t *__restrict__ Q, int64_t ldq,
                                                         int64_t C, int r, float *__restrict__ part,
                                                         const float *__restrict__ s, bool transposed,
                                                         uint16_t *__restrict__ out, MultiPlan pl) {
@@ -334,7 +348,6 @@ __global__ __launch_bounds__(256) void multi_sum_kernel(const uint16_t *__restri
   int32_t per = (hi - lo + (int)gridDim.y - 1) / (int)gridDim.y;
   per = (per + kRB - 1) / kRB * kRB;
   const int32_t mb = lo + split * per, me = mb + per < hi ? mb + per : hi;
-  const bool pvec = (r & 7) == 0;
   f32x4 acc[TJ][2];
 #pragma unroll
   for (int t = 0; t < TJ; ++t)
@@ -353,34 +366,24 @@ __global__ __launch_bounds__(256) void multi_sum_kernel(const uint16_t *__restri
       st.q[i] = (m < me && c < C) ? *reinterpret_cast<const uint4 *>(Q + (int64_t)pl.perm[m] * ldq + c)
                                   : make_uint4(0, 0, 0, 0);
     }
-    if (pvec) {
 #pragma unroll
-      for (int i = 0; i < (TJ + 1) / 2; ++i) {
-        const int q = tid + 256 * i, row = q / (2 * TJ), j = q % (2 * TJ) * 8;
-        const int32_t m = ms + row;
-        st.p[i] = (row < kRB && m < me && j < r) ? *reinterpret_cast<const uint4 *>(P + (int64_t)pl.perm[m] * r + j)
-                                                 : make_uint4(0, 0, 0, 0);
-      }
+    for (int i = 0; i < (TJ + 1) / 2; ++i) {
+      const int q = tid + 256 * i, row = q / (2 * TJ), j = q % (2 * TJ) * 8;
+      const int32_t m = ms + row;
+      st.p[i] = (row < kRB && m < me && j < r) ? *reinterpret_cast<const uint4 *>(P + (int64_t)pl.perm[m] * ldp + j)
+                                               : make_uint4(0, 0, 0, 0);
     }
   };
-  auto store = [&](int32_t ms, const Stage &st, int buf) {
+  auto store = [&](const Stage &st, int buf) {
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
       const int q = tid + 256 * i;
       *reinterpret_cast<uint4 *>(&sQ[buf][(q >> 4) * kQRow + (q & 15) * 8]) = st.q[i];
     }
-    if (pvec) {
 #pragma unroll
-      for (int i = 0; i < (TJ + 1) / 2; ++i) {
-        const int q = tid + 256 * i, row = q / (2 * TJ);
-        if (row < kRB) *reinterpret_cast<uint4 *>(&sP[buf][row * PROW + q % (2 * TJ) * 8]) = st.p[i];
-      }
-    } else {
-      for (int q = tid; q < kRB * TJ * 16; q += 256) {
-        const int row = q / (TJ * 16), j = q % (TJ * 16);
-        const int32_t m = ms + row;
-        sP[buf][row * PROW + j] = (m < me && j < r) ? P[(int64_t)pl.perm[m] * r + j] : (uint16_t)0;
-      }
+    for (int i = 0; i < (TJ + 1) / 2; ++i) {
+      const int q = tid + 256 * i, row = q / (2 * TJ);
+      if (row < kRB) *reinterpret_cast<uint4 *>(&sP[buf][row * PROW + q % (2 * TJ) * 8]) = st.p[i];
     }
   };
   const int g16 = lane >> 4, l16 = lane & 15;
@@ -408,18 +411,18 @@ __global__ __launch_bounds__(256) void multi_sum_kernel(const uint16_t *__restri
   Stage s0, s1;
   if (nst > 0) load(mb, s0);
   if (nst > 1) load(mb + kRB, s1);
-  if (nst > 0) store(mb, s0, 0);
+  if (nst > 0) store(s0, 0);
   __syncthreads();
 #pragma unroll 1
   for (int i = 0; i < nst; i += 2) {
     if (i + 2 < nst) load(mb + (i + 2) * kRB, s0);
     mma(0);
-    if (i + 1 < nst) store(mb + (i + 1) * kRB, s1, 1);
+    if (i + 1 < nst) store(s1, 1);
     __syncthreads();
     if (i + 1 >= nst) break;
     if (i + 3 < nst) load(mb + (i + 3) * kRB, s1);
     mma(1);
-    if (i + 2 < nst) store(mb + (i + 2) * kRB, s0, 0);
+    if (i + 2 < nst) store(s0, 0);
     __syncthreads();
   }
 #pragma unroll
@@ -467,20 +470,31 @@ __global__ void multi_sum_final_kernel(const float *__restrict__ part, int64_t C
 }
 
 // ------------------------------------------------------------------------------------ transposes
-// dst[b][c][j] = src[b][j][c] for `batch` bf16 matrices [R][C], through 64 x 64 LDS tiles.
+// dst[b][c][j] = src[b][j][c] for `batch` bf16 matrices [R][C], through 64 x 64 LDS tiles; the rows of
+// dst have ldd elements, zeros from R on.
 __global__ __launch_bounds__(256) void multi_transpose_kernel(const uint16_t *__restrict__ src, int64_t R,
-                                                              int64_t C, uint16_t *__restrict__ dst) {
+                                                              int64_t C, int64_t ldd, uint16_t *__restrict__ dst) {
   __shared__ uint16_t t[64][66];
   const int64_t tiles_c = (C + 63) / 64;
   const int64_t c0 = (int64_t)blockIdx.x % tiles_c * 64, r0 = (int64_t)blockIdx.x / tiles_c * 64;
   src += (int64_t)blockIdx.y * R * C;
-  dst += (int64_t)blockIdx.y * R * C;
+  dst += (int64_t)blockIdx.y * ldd * C;
   const int x = threadIdx.x & 63, y = threadIdx.x >> 6;
   for (int i = y; i < 64; i += 4)
-    if (r0 + i < R && c0 + x < C) t[i][x] = src[(r0 + i) * C + c0 + x];
+    t[i][x] = r0 + i < R && c0 + x < C ? src[(r0 + i) * C + c0 + x] : (uint16_t)0;
   __syncthreads();
   for (int i = y; i < 64; i += 4)
-    if (c0 + i < C && r0 + x < R) dst[(c0 + i) * R + r0 + x] = t[x][i];
+    if (c0 + i < C && r0 + x < ldd) dst[(c0 + i) * ldd + r0 + x] = t[x][i];
+}
+
+// dst [rows][rp] = src [rows][r] and zeros.
+__global__ void multi_pad_kernel(const uint16_t *__restrict__ src, int64_t rows, int r, int rp,
+                                 uint16_t *__restrict__ dst) {
+  for (int64_t i = blockIdx.x * (int64_t)blockDim.x + threadIdx.x; i < rows * rp; i += (int64_t)gridDim.x * blockDim.x) {
+    const int64_t row = i / rp;
+    const int j = (int)(i - row * rp);
+    dst[i] = j < r ? src[row * r + j] : (uint16_t)0;
+  }
 }
 
 int64_t blocks_for(int64_t n) {
@@ -537,6 +551,15 @@ hipError_t launch_multi_rows(const uint16_t *in, int64_t ldin, const uint16_t *p
   return hipGetLastError();
 }
 
+hipError_t launch_multi_rows_part(const uint16_t *in, int64_t ldin, const uint16_t *p, int64_t pstride, int64_t ldp,
+                                  const int32_t *ids, int64_t M, int64_t Lr, int r, int L, int splits, float *part,
+                                  hipStream_t st) {
+  if (M < 1 || M > kMultiSmallM || splits < 1 || splits > 65535) return hipErrorInvalidValue;
+  multi_rows_part_kernel<<<dim3((unsigned)M, (unsigned)((r + 31) / 32), (unsigned)splits), dim3(512), 0, st>>>(
+      in, ldin, p, pstride, ldp, ids, (int)M, Lr, r, L, part);
+  return hipGetLastError();
+}
+
 // Splits of the sums over rows: about 1024 workgroups over the column tiles and adapters.
 int multi_sum_splits(int64_t M, int64_t C, int L) {
   const int64_t tiles = (C + kCB - 1) / kCB * L;
@@ -546,13 +569,14 @@ int multi_sum_splits(int64_t M, int64_t C, int L) {
   return (int)(s > 1 ? s : 1);
 }
 
-hipError_t launch_multi_sum(const uint16_t *P, const uint16_t *Q, int64_t ldq, int64_t C, int r, int L,
+hipError_t launch_multi_sum(const uint16_t *P, int64_t ldp, const uint16_t *Q, int64_t ldq, int64_t C, int r, int L,
                             const float *s, int splits, float *part, uint16_t *out, bool transposed,
                             const MultiPlan &pl, hipStream_t st) {
+  if ((ldp & 7) != 0 || ldp < r) return hipErrorInvalidValue;
   const dim3 grid((unsigned)((C + kCB - 1) / kCB), (unsigned)splits, (unsigned)L);
   switch ((r + 15) / 16) {
 #define MS_CASE(T) \
-  case T: multi_sum_kernel<T><<<grid, dim3(256), 0, st>>>(P, Q, ldq, C, r, part, s, transposed, out, pl); break;
+  case T: multi_sum_kernel<T><<<grid, dim3(256), 0, st>>>(P, ldp, Q, ldq, C, r, part, s, transposed, out, pl); break;
     MS_CASE(1) MS_CASE(2) MS_CASE(3) MS_CASE(4) MS_CASE(5) MS_CASE(6) MS_CASE(7) MS_CASE(8)
 #undef MS_CASE
     default: return hipErrorInvalidValue;
@@ -564,9 +588,16 @@ hipError_t launch_multi_sum(const uint16_t *P, const uint16_t *Q, int64_t ldq, i
   return hipGetLastError();
 }
 
-hipError_t launch_multi_transpose(const uint16_t *src, int64_t R, int64_t C, int batch, uint16_t *dst, hipStream_t st) {
-  const dim3 grid((unsigned)((C + 63) / 64 * ((R + 63) / 64)), (unsigned)batch);
-  multi_transpose_kernel<<<grid, dim3(256), 0, st>>>(src, R, C, dst);
+hipError_t launch_multi_transpose(const uint16_t *src, int64_t R, int64_t C, int64_t ldd, int batch, uint16_t *dst,
+                                  hipStream_t st) {
+  if (ldd < R) return hipErrorInvalidValue;
+  const dim3 grid((unsigned)((C + 63) / 64 * ((ldd + 63) / 64)), (unsigned)batch);
+  multi_transpose_kernel<<<grid, dim3(256), 0, st>>>(src, R, C, ldd, dst);
+  return hipGetLastError();
+}
+
+hipError_t launch_multi_pad(const uint16_t *src, int64_t rows, int r, int rp, uint16_t *dst, hipStream_t st) {
+  multi_pad_kernel<<<dim3((unsigned)blocks_for(rows * rp)), dim3(256), 0, st>>>(src, rows, r, rp, dst);
   return hipGetLastError();
 }
 

@@ -41,6 +41,12 @@ SHAPES = [(1, 64, 8, 1, 1, "one"), (1, 512, 136, 16, 4, "each"), (2, 256, 264, 8
           (64, 512, 520, 33, 3, "runs"), (130, 320, 264, 16, 64, "mixed"), (257, 256, 264, 20, 300, "each"),
           (300, 64, 520, 64, 2, "one"), (600, 192, 72, 8, 1024, "mixed"), (1025, 128, 136, 48, 6, "runs"),
           (1100, 256, 264, 7, 40, "outside")]
+# one shape for every height of the mid kernel's row blocks, with K a multiple of its step and not, and
+# wide weights for the 16-row stream kernel
+HEIGHTS = [(m, k, 264, 16, 3, "mixed") for m in (20, 40, 60, 75, 95, 110, 125, 260) for k in (512, 576)]
+WIDE = [(16, 512, 14400, 16, 16, "each"), (9, 256, 14400, 128, 4, "mixed"), (3, 256, 14344, 8, 2, "one"),
+        (16, 256, 14400, 40, 20, "outside")]
+SHAPES += HEIGHTS + WIDE
 
 
 @pytest.mark.parametrize("fmt", ["nf4", "nf4f", "e2m1"])
