@@ -23,7 +23,9 @@ from __future__ import annotations
 
 import ctypes
 import dataclasses
+import functools
 import os
+import struct
 from typing import Optional, Tuple
 
 import torch
@@ -81,7 +83,6 @@ def library() -> ctypes.CDLL:
     lib = ctypes.CDLL(_LIB_PATH)
     vp, i64, i32, f32, sz = ctypes.c_void_p, ctypes.c_int64, ctypes.c_int32, ctypes.c_float, ctypes.c_size_t
     P = ctypes.POINTER(_NF4TensorC)
-    N, H = ctypes.POINTER(_HeadNormC), ctypes.POINTER(_HeadsC)
     sig = {
         "nf4_quantize": (ctypes.c_int, [vp, ctypes.c_int, P, vp]),
         "nf4_dequantize": (ctypes.c_int, [P, vp, ctypes.c_int, vp]),
@@ -111,11 +112,11 @@ def library() -> ctypes.CDLL:
         "nf4_last_error": (ctypes.c_char_p, []),
         "qlora_multi_fwd_workspace_bytes": (sz, [i64, i64, i64, i32, i32]),
         "qlora_multi_bwd_workspace_bytes": (sz, [i64, i64, i64, i32, i32]),
-        "qlora_multi_fwd": (ctypes.c_int, [vp, i64, P, vp, vp, vp, vp, i32, i32, vp, vp, vp, sz, vp]),
-        "qlora_multi_bwd": (ctypes.c_int, [vp, vp, i64, P, vp, vp, vp, vp, i32, i32, vp, vp, vp, vp, vp, sz, vp]),
-        "qk_norm_rope_fwd": (ctypes.c_int, [N, H, H, H, H, vp]),
+        "qlora_multi_fwd": (ctypes.c_int, [vp, i64, vp, vp, vp, vp, vp, i32, i32, vp, vp, vp, sz, vp]),
+        "qlora_multi_bwd": (ctypes.c_int, [vp, vp, i64, vp, vp, vp, vp, vp, i32, i32, vp, vp, vp, vp, vp, sz, vp]),
+        "qk_norm_rope_fwd": (ctypes.c_int, [vp] * 6),
         "qk_norm_rope_bwd_workspace_bytes": (sz, [i32]),
-        "qk_norm_rope_bwd": (ctypes.c_int, [N, H, H, H, H, H, H, vp, vp, vp, sz, vp]),
+        "qk_norm_rope_bwd": (ctypes.c_int, [vp] * 10 + [sz, vp]),
         "distill_topk_fwd": (ctypes.c_int, [vp, ctypes.c_int, i64, i64, i64, vp, vp, i32, f32, vp, vp, vp]),
         "distill_topk_bwd": (ctypes.c_int, [vp, ctypes.c_int, i64, i64, i64, vp, vp, i32, f32, vp, vp, vp, i64, vp]),
         "distill_topk_step": (ctypes.c_int, [vp, ctypes.c_int, i64, i64, i64, vp, vp, i32, f32, vp, vp, vp, i64, vp]),
@@ -582,22 +583,53 @@ def qlora_swiglu_bwd(dH: torch.Tensor, X: torch.Tensor, q: NF4Tensor, Agu: Optio
     return dX, dAgu, dBg, dBu
 
 
-def _same_device(dev: torch.device, **tensors):
-    for name, t in tensors.items():
-        if t is not None and t.device != dev:
-            raise ValueError(f"{name} must be on {dev} (got {t.device})")
+# The operators below serve single tokens too, where a call's host time is what counts: addresses go to
+# the library as plain integers, descriptors as packed bytes laid out as the header's structs.
+_NF4_STRUCT = struct.Struct("@qqiiPPP")
+_HEADS_STRUCT = struct.Struct("@Pqqi0q")
+_HEAD_NORM_STRUCT = struct.Struct("@qiiiiiPPffPPqPi0q")
+
+
+def _raw_stream(device: torch.device) -> int:
+    """The current stream of a device as an address (torch's own accessor of it: making a Stream object
+    to ask takes 1.7 us, a tenth of a decode step's call)."""
+    return torch._C._cuda_getCurrentRawStream(device.index)
+
+
+def _addr(t: Optional[torch.Tensor]):
+    return None if t is None else t.data_ptr()
+
+
+@functools.lru_cache(maxsize=None)
+def _bytes_of(name: str, *sizes: int) -> int:
+    """Workspace bytes, a function of the sizes alone."""
+    return getattr(library(), name)(*sizes)
+
+
+def _is(t: torch.Tensor, name: str, dtype, shape, device) -> None:
+    """A contiguous tensor of this type, shape and device, or an error that says what is wrong."""
+    if t.dtype is dtype and t.shape == shape and t.is_cuda and t.device == device and t.is_contiguous():
+        return
+    _need(t, name, dtype, shape)
+    raise ValueError(f"{name} must be on {device} (got {t.device})")
+
+
+def _packed(q: NF4Tensor) -> bytes:
+    return _NF4_STRUCT.pack(q.n, q.k, q.block, q.dq_block, q.codes.data_ptr(), q.absmax.data_ptr(),
+                            q.scale.data_ptr() if q.scale is not None else 0)
 
 
 def _multi_args(X, q: NF4Tensor, A, B, s, ids):
     if A.dim() != 3 or B.dim() != 3:
         raise ValueError("A must be [L, r, k] and B [L, n, r]")
-    m, (L, r) = X.shape[0], A.shape[:2]
-    _need(X, "X", torch.bfloat16, (m, q.k))
-    _need(A, "A", torch.bfloat16, (L, r, q.k))
-    _need(B, "B", torch.bfloat16, (L, q.n, r))
-    _need(s, "s", torch.float32, (L,))
-    _need(ids, "ids", torch.int32, (m,))
-    _same_device(X.device, q=q, A=A, B=B, s=s, ids=ids)
+    m, (L, r, _), dev = X.shape[0], A.shape, X.device
+    _is(X, "X", torch.bfloat16, (m, q.k), dev)
+    _is(A, "A", torch.bfloat16, (L, r, q.k), dev)
+    _is(B, "B", torch.bfloat16, (L, q.n, r), dev)
+    _is(s, "s", torch.float32, (L,), dev)
+    _is(ids, "ids", torch.int32, (m,), dev)
+    if q.codes.device != dev:
+        raise ValueError(f"q must be on {dev} (got {q.codes.device})")
     return m, L, r
 
 
@@ -607,15 +639,12 @@ def qlora_multi_fwd(X: torch.Tensor, q: NF4Tensor, A: torch.Tensor, B: torch.Ten
     scale s[a] (float32 [L]): Y_i = X_i deq(W)^T + s[a] T_i B_a^T, T_i = X_i A_a^T. ids int32 [m], in
     any order; a row whose id lies outside [0, L) has no adapter (T_i = 0)."""
     m, L, r = _multi_args(X, q, A, B, s, ids)
-    dev = X.device
-    Y = torch.empty(m, q.n, dtype=torch.bfloat16, device=dev)
-    T = torch.empty(m, r, dtype=torch.bfloat16, device=dev)
-    lib = library()
-    wsb = lib.qlora_multi_fwd_workspace_bytes(m, q.n, q.k, r, L)
-    ws = torch.empty(max(wsb, 1), dtype=torch.uint8, device=dev)
-    st = q.c_struct()
-    _check(lib.qlora_multi_fwd(_ptr(X), m, ctypes.byref(st), _ptr(A), _ptr(B), _ptr(s), _ptr(ids), L, r,
-                               _ptr(Y), _ptr(T), _ptr(ws), wsb, _stream(dev)))
+    Y, T = X.new_empty((m, q.n)), X.new_empty((m, r))
+    wsb = _bytes_of("qlora_multi_fwd_workspace_bytes", m, q.n, q.k, r, L)
+    ws = X.new_empty(max(wsb, 1), dtype=torch.uint8)
+    _check(library().qlora_multi_fwd(X.data_ptr(), m, _packed(q), A.data_ptr(), B.data_ptr(), s.data_ptr(),
+                                     ids.data_ptr(), L, r, Y.data_ptr(), T.data_ptr(), ws.data_ptr(), wsb,
+                                     _raw_stream(X.device)))
     return Y, T
 
 
@@ -624,80 +653,87 @@ def qlora_multi_bwd(dY: torch.Tensor, X: torch.Tensor, q: NF4Tensor, A: torch.Te
     """(dX, dA, dB) of qlora_multi_fwd for dY [m, n]; dX is None when need_dx is False, T None is
     recomputed. dA [L, r, k] and dB [L, n, r] are zero for an adapter without rows."""
     m, L, r = _multi_args(X, q, A, B, s, ids)
-    _need(dY, "dY", torch.bfloat16, (m, q.n))
-    if T is not None:
-        _need(T, "T", torch.bfloat16, (m, r))
     dev = X.device
-    _same_device(dev, dY=dY, T=T)
-    dX = torch.empty(m, q.k, dtype=torch.bfloat16, device=dev) if need_dx else None
-    dA, dB = torch.empty_like(A), torch.empty_like(B)
-    lib = library()
-    wsb = lib.qlora_multi_bwd_workspace_bytes(m, q.n, q.k, r, L)
-    ws = torch.empty(max(wsb, 1), dtype=torch.uint8, device=dev)
-    st = q.c_struct()
-    _check(lib.qlora_multi_bwd(_ptr(dY), _ptr(X), m, ctypes.byref(st), _ptr(A), _ptr(B), _ptr(s), _ptr(ids), L, r,
-                               _ptr(T), _ptr(dX), _ptr(dA), _ptr(dB), _ptr(ws), wsb, _stream(dev)))
+    _is(dY, "dY", torch.bfloat16, (m, q.n), dev)
+    if T is not None:
+        _is(T, "T", torch.bfloat16, (m, r), dev)
+    dX = X.new_empty((m, q.k)) if need_dx else None
+    dA, dB = A.new_empty(A.shape), B.new_empty(B.shape)
+    wsb = _bytes_of("qlora_multi_bwd_workspace_bytes", m, q.n, q.k, r, L)
+    ws = X.new_empty(max(wsb, 1), dtype=torch.uint8)
+    _check(library().qlora_multi_bwd(dY.data_ptr(), X.data_ptr(), m, _packed(q), A.data_ptr(), B.data_ptr(),
+                                     s.data_ptr(), ids.data_ptr(), L, r, _addr(T), _addr(dX), dA.data_ptr(),
+                                     dB.data_ptr(), ws.data_ptr(), wsb, _raw_stream(dev)))
     return dX, dA, dB
 
 
 def _dtype_code(t: torch.Tensor, name: str) -> int:
-    if t.dtype not in (torch.bfloat16, torch.float32):
-        raise ValueError(f"{name} must be bfloat16 or float32 (got {t.dtype})")
-    return NF4_F32 if t.dtype == torch.float32 else NF4_BF16
+    if t.dtype is torch.bfloat16:
+        return NF4_BF16
+    if t.dtype is torch.float32:
+        return NF4_F32
+    raise ValueError(f"{name} must be bfloat16 or float32 (got {t.dtype})")
 
 
-def _heads(t: Optional[torch.Tensor], name: str, like: Optional[torch.Tensor] = None) -> _HeadsC:
+_NO_HEADS = _HEADS_STRUCT.pack(0, 0, 0, 0)
+
+
+def _heads(t: Optional[torch.Tensor], name: str, like: Optional[torch.Tensor] = None) -> bytes:
     """Descriptor of a [m, heads, d] tensor whose heads are contiguous (None: no heads)."""
     if t is None:
-        return _HeadsC(None, 0, 0, 0)
+        return _NO_HEADS
     if not t.is_cuda or t.dim() != 3:
         raise ValueError(f"{name} must be a device tensor [m, heads, d]")
-    if like is not None and (t.shape != like.shape or t.dtype != like.dtype or t.device != like.device):
+    if like is not None and (t.shape != like.shape or t.dtype is not like.dtype or t.device != like.device):
         raise ValueError(f"{name} must match its input in shape, type and device")
-    if t.numel() and t.shape[2] > 1 and t.stride(2) != 1:
+    ts, hs, es = t.stride()
+    if es != 1 and t.numel() and t.shape[2] > 1:
         raise ValueError(f"{name} must have contiguous heads")
-    return _HeadsC(t.data_ptr(), t.stride(0), t.stride(1), t.shape[1])
+    return _HEADS_STRUCT.pack(t.data_ptr(), ts, hs, t.shape[1])
 
 
-def _head_norm(q, k, wq, wk, cos, sin, pos, eps, interleaved, weight_offset) -> _HeadNormC:
+def _head_norm(q, k, wq, wk, cos, sin, pos, eps, interleaved, weight_offset):
     x, w = (q, wq) if q is not None else (k, wk)
     if x is None or w is None:
         raise ValueError("q or k must be given, with its weight")
     if x.dim() != 3:
         raise ValueError("q and k must be [m, heads, d]")
-    m, _, d = x.shape
-    if q is not None and k is not None and (k.dim() != 3 or k.shape[0] != m or k.shape[2] != d or
-                                            k.dtype != q.dtype or k.device != q.device):
-        raise ValueError("q and k must agree in tokens, head size, type and device")
+    (m, _, d), dev = x.shape, x.device
     code, w_code = _dtype_code(x, "q and k"), _dtype_code(w, "the weights")
-    for t, wt, name in ((q, wq, "wq"), (k, wk, "wk")):
-        if t is not None:
-            _need(wt, name, w.dtype, (d,))
-    rot = 0
-    if cos is not None:
-        if pos is None or sin is None:
-            raise ValueError("cos, sin and pos come together")
-        if pos.dtype not in (torch.int32, torch.int64):
-            raise ValueError("pos must be int32 or int64")
-        rot = 2 * cos.shape[1]
-        _need(cos, "cos", torch.float32)
-        _need(sin, "sin", torch.float32, cos.shape)
-        _need(pos, "pos", pos.dtype, (m,))
-    _same_device(x.device, wq=wq if q is not None else None, wk=wk if k is not None else None,
-                 cos=cos, sin=sin if rot else None, pos=pos if rot else None)
-    return _HeadNormC(m, d, rot, int(interleaved), code, w_code, wq.data_ptr() if q is not None else None,
-                      wk.data_ptr() if k is not None else None, float(weight_offset), float(eps),
-                      cos.data_ptr() if rot else None, sin.data_ptr() if rot else None,
-                      cos.shape[0] if rot else 0, pos.data_ptr() if rot else None,
-                      int(rot and pos.dtype == torch.int64))
+    if q is not None:
+        _is(wq, "wq", w.dtype, (d,), dev)
+    if k is not None:
+        if k.dim() != 3 or k.shape[0] != m or k.shape[2] != d or k.dtype is not x.dtype or k.device != dev:
+            raise ValueError("q and k must agree in tokens, head size, type and device")
+        if wk is None:
+            raise ValueError("q or k must be given, with its weight")
+        _is(wk, "wk", w.dtype, (d,), dev)
+    if cos is None:
+        return d, _HEAD_NORM_STRUCT.pack(m, d, 0, int(interleaved), code, w_code, wq.data_ptr() if q is not None else 0,
+                                         wk.data_ptr() if k is not None else 0, weight_offset, eps, 0, 0, 0, 0, 0)
+    if pos is None or sin is None:
+        raise ValueError("cos, sin and pos come together")
+    if pos.dtype is not torch.int32 and pos.dtype is not torch.int64:
+        raise ValueError("pos must be int32 or int64")
+    places, half = cos.shape
+    _is(cos, "cos", torch.float32, (places, half), dev)
+    _is(sin, "sin", torch.float32, (places, half), dev)
+    _is(pos, "pos", pos.dtype, (m,), dev)
+    return d, _HEAD_NORM_STRUCT.pack(m, d, 2 * half, int(interleaved), code, w_code,
+                                     wq.data_ptr() if q is not None else 0, wk.data_ptr() if k is not None else 0,
+                                     weight_offset, eps, cos.data_ptr(), sin.data_ptr(), places, pos.data_ptr(),
+                                     int(pos.dtype is torch.int64))
 
 
-def _out_like(t, out, name):
+def _out_heads(t, out, name):
+    """The output for t (out, or a new tensor) and its descriptor."""
     if t is None:
-        return None
-    if out is None:
-        return torch.empty(t.shape, dtype=t.dtype, device=t.device)
-    return out
+        return None, _NO_HEADS
+    if out is not None:
+        return out, _heads(out, name, t)
+    _, h, d = t.shape
+    out = t.new_empty(t.shape)
+    return out, _HEADS_STRUCT.pack(out.data_ptr(), h * d, d, h)
 
 
 def qk_norm_rope_fwd(q: Optional[torch.Tensor], k: Optional[torch.Tensor], wq: Optional[torch.Tensor],
@@ -710,12 +746,11 @@ def qk_norm_rope_fwd(q: Optional[torch.Tensor], k: Optional[torch.Tensor], wq: O
     cos, sin (float32 [places, rot/2]) of pos (int32 or int64 [m]): pairs (i, i + rot/2), or
     (2i, 2i + 1) when interleaved. cos None: the norms alone. A token whose position lies outside the
     table gets NaN. k (or q) may be None. out: tensors to write, the inputs themselves among them."""
-    p = _head_norm(q, k, wq, wk, cos, sin, pos, eps, interleaved, weight_offset)
-    qo, ko = _out_like(q, out[0], "q_out"), _out_like(k, out[1], "k_out")
-    dev = (q if q is not None else k).device
-    _check(library().qk_norm_rope_fwd(ctypes.byref(p), ctypes.byref(_heads(q, "q")), ctypes.byref(_heads(k, "k")),
-                                      ctypes.byref(_heads(qo, "q_out", q)), ctypes.byref(_heads(ko, "k_out", k)),
-                                      _stream(dev)))
+    _, p = _head_norm(q, k, wq, wk, cos, sin, pos, eps, interleaved, weight_offset)
+    hq, hk = _heads(q, "q"), _heads(k, "k")
+    qo, hqo = _out_heads(q, out[0], "q_out")
+    ko, hko = _out_heads(k, out[1], "k_out")
+    _check(library().qk_norm_rope_fwd(p, hq, hk, hqo, hko, _raw_stream((q if q is not None else k).device)))
     return qo, ko
 
 
@@ -726,48 +761,46 @@ def qk_norm_rope_bwd(gq: Optional[torch.Tensor], gk: Optional[torch.Tensor], q: 
                      out=(None, None)):
     """(dq, dk, dwq, dwk) of qk_norm_rope_fwd for the gradients gq, gk of its outputs; dwq and dwk are
     float32 [d]. out: tensors for dq and dk (the slices of a packed gradient)."""
-    p = _head_norm(q, k, wq, wk, cos, sin, pos, eps, interleaved, weight_offset)
-    dq, dk = _out_like(q, out[0], "dq"), _out_like(k, out[1], "dk")
-    dev, d = (q if q is not None else k).device, int(p.d)
-    dwq = torch.empty(d, dtype=torch.float32, device=dev) if q is not None else None
-    dwk = torch.empty(d, dtype=torch.float32, device=dev) if k is not None else None
-    lib = library()
-    wsb = lib.qk_norm_rope_bwd_workspace_bytes(d)
-    ws = torch.empty(wsb, dtype=torch.uint8, device=dev)
     if (gq is None) != (q is None) or (gk is None) != (k is None):
         raise ValueError("gq and gk must be given for the inputs that are")
-    _check(lib.qk_norm_rope_bwd(ctypes.byref(p), ctypes.byref(_heads(gq, "gq", q)),
-                                ctypes.byref(_heads(gk, "gk", k)), ctypes.byref(_heads(q, "q")),
-                                ctypes.byref(_heads(k, "k")), ctypes.byref(_heads(dq, "dq", q)),
-                                ctypes.byref(_heads(dk, "dk", k)), _ptr(dwq), _ptr(dwk), _ptr(ws), wsb,
-                                _stream(dev)))
+    d, p = _head_norm(q, k, wq, wk, cos, sin, pos, eps, interleaved, weight_offset)
+    x = q if q is not None else k
+    hq, hk = _heads(q, "q"), _heads(k, "k")
+    hgq, hgk = _heads(gq, "gq", q), _heads(gk, "gk", k)
+    dq, hdq = _out_heads(q, out[0], "dq")
+    dk, hdk = _out_heads(k, out[1], "dk")
+    dwq = x.new_empty(d, dtype=torch.float32) if q is not None else None
+    dwk = x.new_empty(d, dtype=torch.float32) if k is not None else None
+    wsb = _bytes_of("qk_norm_rope_bwd_workspace_bytes", d)
+    ws = x.new_empty(wsb, dtype=torch.uint8)
+    _check(library().qk_norm_rope_bwd(p, hgq, hgk, hq, hk, hdq, hdk, _addr(dwq), _addr(dwk), ws.data_ptr(), wsb,
+                                      _raw_stream(x.device)))
     return dq, dk, dwq, dwk
 
 
 def _distill_args(logits, idx, teacher):
     if logits.dim() != 2 or not logits.is_cuda:
         raise ValueError("logits must be a device tensor [t, v]")
-    code = _dtype_code(logits, "logits")
-    t, v = logits.shape
-    if logits.numel() and v > 1 and logits.stride(1) != 1:
+    code, (t, v), dev = _dtype_code(logits, "logits"), logits.shape, logits.device
+    ld, es = logits.stride()
+    if es != 1 and v > 1 and t:
         raise ValueError("logits must have contiguous rows")
     if idx.dim() != 2:
         raise ValueError("idx must be [t, top]")
-    _need(idx, "idx", torch.int32, (t, idx.shape[1]))
-    _need(teacher, "teacher", torch.float32, idx.shape)
-    _same_device(logits.device, idx=idx, teacher=teacher)
-    ld = logits.stride(0) if t > 1 else v
-    return code, t, v, ld, idx.shape[1]
+    top = idx.shape[1]
+    _is(idx, "idx", torch.int32, (t, top), dev)
+    _is(teacher, "teacher", torch.float32, (t, top), dev)
+    return code, t, v, ld if t > 1 else v, top, dev
 
 
 def _distill_out(logits, out):
     if out is None:
-        return torch.empty(logits.shape, dtype=logits.dtype, device=logits.device)
-    if out.shape != logits.shape or out.dtype != logits.dtype or out.device != logits.device:
+        out = logits.new_empty(logits.shape)
+    elif out.shape != logits.shape or out.dtype is not logits.dtype or out.device != logits.device:
         raise ValueError("out must match logits in shape, type and device")
-    if out.numel() and out.shape[1] > 1 and out.stride(1) != 1:
+    elif out.numel() and out.shape[1] > 1 and out.stride(1) != 1:
         raise ValueError("out must have contiguous rows")
-    return out
+    return out, out.stride(0) if out.shape[0] > 1 else out.shape[1]
 
 
 def distill_topk_fwd(logits: torch.Tensor, idx: torch.Tensor, teacher: torch.Tensor, tau: float):
@@ -775,25 +808,22 @@ def distill_topk_fwd(logits: torch.Tensor, idx: torch.Tensor, teacher: torch.Ten
     teacher's, softmax(teacher / tau) over its kept entries. logits bfloat16 or float32 [t, v] (rows
     contiguous), idx int32 [t, top], teacher float32 [t, top]. An index outside [0, v) or a teacher
     logit of -inf marks an entry that is not there; a row without entries has loss 0."""
-    code, t, v, ld, top = _distill_args(logits, idx, teacher)
-    loss = torch.empty(t, dtype=torch.float32, device=logits.device)
-    lse = torch.empty(t, dtype=torch.float32, device=logits.device)
-    _check(library().distill_topk_fwd(_ptr(logits), code, t, v, ld, _ptr(idx), _ptr(teacher), top, float(tau),
-                                      _ptr(loss), _ptr(lse), _stream(logits.device)))
+    code, t, v, ld, top, dev = _distill_args(logits, idx, teacher)
+    loss, lse = teacher.new_empty(t), teacher.new_empty(t)
+    _check(library().distill_topk_fwd(logits.data_ptr(), code, t, v, ld, idx.data_ptr(), teacher.data_ptr(), top, tau,
+                                      loss.data_ptr(), lse.data_ptr(), _raw_stream(dev)))
     return loss, lse
 
 
 def distill_topk_bwd(grad: torch.Tensor, logits: torch.Tensor, idx: torch.Tensor, teacher: torch.Tensor,
                      tau: float, lse: torch.Tensor, out: Optional[torch.Tensor] = None) -> torch.Tensor:
     """dlogits for the gradients grad (float32 [t]) of distill_topk_fwd's losses; out may be logits."""
-    code, t, v, ld, top = _distill_args(logits, idx, teacher)
-    _need(grad, "grad", torch.float32, (t,))
-    _need(lse, "lse", torch.float32, (t,))
-    _same_device(logits.device, grad=grad, lse=lse)
-    dz = _distill_out(logits, out)
-    _check(library().distill_topk_bwd(_ptr(logits), code, t, v, ld, _ptr(idx), _ptr(teacher), top, float(tau),
-                                      _ptr(lse), _ptr(grad), _ptr(dz), dz.stride(0) if t > 1 else v,
-                                      _stream(logits.device)))
+    code, t, v, ld, top, dev = _distill_args(logits, idx, teacher)
+    _is(grad, "grad", torch.float32, (t,), dev)
+    _is(lse, "lse", torch.float32, (t,), dev)
+    dz, ldd = _distill_out(logits, out)
+    _check(library().distill_topk_bwd(logits.data_ptr(), code, t, v, ld, idx.data_ptr(), teacher.data_ptr(), top, tau,
+                                      lse.data_ptr(), grad.data_ptr(), dz.data_ptr(), ldd, _raw_stream(dev)))
     return dz
 
 
@@ -802,15 +832,13 @@ def distill_topk_step(logits: torch.Tensor, idx: torch.Tensor, teacher: torch.Te
     """(loss, dlogits) in one pass over the logits: loss float32 [t] as distill_topk_fwd (0 where the
     weight is 0) and the gradient of sum(weight * loss), weight float32 [t] (None: all 1). out may be
     logits."""
-    code, t, v, ld, top = _distill_args(logits, idx, teacher)
+    code, t, v, ld, top, dev = _distill_args(logits, idx, teacher)
     if weight is not None:
-        _need(weight, "weight", torch.float32, (t,))
-        _same_device(logits.device, weight=weight)
-    loss = torch.empty(t, dtype=torch.float32, device=logits.device)
-    dz = _distill_out(logits, out)
-    _check(library().distill_topk_step(_ptr(logits), code, t, v, ld, _ptr(idx), _ptr(teacher), top, float(tau),
-                                       _ptr(weight), _ptr(loss), _ptr(dz), dz.stride(0) if t > 1 else v,
-                                       _stream(logits.device)))
+        _is(weight, "weight", torch.float32, (t,), dev)
+    loss = teacher.new_empty(t)
+    dz, ldd = _distill_out(logits, out)
+    _check(library().distill_topk_step(logits.data_ptr(), code, t, v, ld, idx.data_ptr(), teacher.data_ptr(), top, tau,
+                                       _addr(weight), loss.data_ptr(), dz.data_ptr(), ldd, _raw_stream(dev)))
     return loss, dz
 
 

@@ -18,7 +18,7 @@
 // interleaved pairs two neighbouring chunks), so that the rotation needs no exchange between
 // lanes: a lane holds both members of each of its pairs. A head's units take the first lanes of a
 // power of two of lanes, whose float sums meet by lane exchanges; kVec is the largest power of two
-// up to 16 bytes that divides rot/2, d - rot and the strides. Threads keep their unit and walk over
+// up to 16 bytes that divides rot/2, d - rot, the strides and the addresses. Threads keep their unit and walk over
 // (token, head) items, so the weight stays in registers; q and k items go to separate workgroups,
 // and dw is summed in registers over a thread's items, over the workgroup in LDS and over the
 // workgroups by a second launch, in an order that the sizes alone fix.
@@ -61,7 +61,10 @@ __device__ __forceinline__ void store_chunk(XT *p, const float in[kVec]) {
   Chunk<XT, kVec> c;
 #pragma unroll
   for (int i = 0; i < kVec; ++i) c.v[i] = Elem<XT>::from_f32(in[i]);
-  *reinterpret_cast<Chunk<XT, kVec> *>(p) = c;
+  if constexpr (sizeof(c) == 16)   // not read again here: streamed out (41 -> 31 us on 8192 x 40 heads of 128)
+    __builtin_nontemporal_store(__builtin_bit_cast(u32x4, c), reinterpret_cast<u32x4 *>(p));
+  else
+    *reinterpret_cast<Chunk<XT, kVec> *>(p) = c;
 }
 
 // Sum over the `lph` (a power of two) neighbouring lanes that hold a head.
@@ -82,6 +85,7 @@ __global__ __launch_bounds__(kThreads) void head_norm_kernel(HeadArgs a) {
   const int unit0 = threadIdx.x & (lph - 1);
   const int per_block = kThreads / lph;            // heads a workgroup holds at once
   const int rot_units = half / kVec;
+  const float inv_d = 1.f / (float)d;
   const int64_t items = a.m * h.heads;
 
   // this lane's units: places of the two chunks (-1: none) and the weight there
@@ -99,17 +103,19 @@ __global__ __launch_bounds__(kThreads) void head_norm_kernel(HeadArgs a) {
       if (pa[u] >= d) pa[u] = -1;
       if (pb[u] >= d) pb[u] = -1;
     }
+    auto weight = [&](int p, float *w) {
 #pragma unroll
-    for (int i = 0; i < kVec; ++i) {
-      auto weight = [&](int p) {
-        if (p < 0) return 0.f;
-        const float w = a.w_f32 ? reinterpret_cast<const float *>(h.w)[p + i]
-                                : bf16_to_f32(reinterpret_cast<const uint16_t *>(h.w)[p + i]);
-        return w + a.w_offset;
-      };
-      wa[u][i] = weight(pa[u]);
-      wb[u][i] = weight(pb[u]);
-    }
+      for (int i = 0; i < kVec; ++i) w[i] = 0.f;
+      if (p < 0) return;
+      if (a.w_f32)
+        load_chunk<float, kVec>(reinterpret_cast<const float *>(h.w) + p, w);
+      else
+        load_chunk<uint16_t, kVec>(reinterpret_cast<const uint16_t *>(h.w) + p, w);
+#pragma unroll
+      for (int i = 0; i < kVec; ++i) w[i] += a.w_offset;
+    };
+    weight(pa[u], wa[u]);
+    weight(pb[u], wb[u]);
   }
   float da[kUnits][kVec], db[kUnits][kVec];        // backward: this thread's part of dw
   if constexpr (kBwd) {
@@ -139,22 +145,17 @@ __global__ __launch_bounds__(kThreads) void head_norm_kernel(HeadArgs a) {
     }
   };
 
+  const uint32_t stride = (uint32_t)nblocks * per_block;   // items fit 31 bits (checked at launch)
 #pragma unroll 1
-  for (int64_t it = (int64_t)block * per_block + threadIdx.x / lph; it < items;
-       it += (int64_t)nblocks * per_block) {
-    // items fit 32 bits (checked at launch)
-    const uint32_t tok = (uint32_t)it / (uint32_t)h.heads;
-    const uint32_t head = (uint32_t)it - tok * (uint32_t)h.heads;
-    const XT *x = reinterpret_cast<const XT *>(h.x) + tok * h.x_ts + head * h.x_hs;
-    float xa[kUnits][kVec], xb[kUnits][kVec];
-    float ga[kUnits][kVec], gb[kUnits][kVec];
-    float cs[kUnits][kVec], sn[kUnits][kVec];
+  for (uint32_t it = (uint32_t)block * per_block + threadIdx.x / lph; it < (uint32_t)items; it += stride) {
+    const uint32_t tok = it / (uint32_t)h.heads, head = it - tok * (uint32_t)h.heads;
     int64_t pos = 0;
     if (rot > 0)
       pos = a.pos64 ? reinterpret_cast<const int64_t *>(a.pos)[tok]
                     : (int64_t) reinterpret_cast<const int32_t *>(a.pos)[tok];
-    // a position outside the table reads nothing there: the token's outputs are NaN
-    const bool placed = rot == 0 || (pos >= 0 && pos < a.places);
+    const XT *x = reinterpret_cast<const XT *>(h.x) + tok * h.x_ts + head * h.x_hs;
+    float xa[kUnits][kVec], xb[kUnits][kVec], ga[kUnits][kVec], gb[kUnits][kVec];
+    float cs[kUnits][kVec], sn[kUnits][kVec];
     float ss = 0.f;
 #pragma unroll
     for (int u = 0; u < kUnits; ++u) {
@@ -169,6 +170,11 @@ __global__ __launch_bounds__(kThreads) void head_norm_kernel(HeadArgs a) {
         if (pa[u] >= 0) load_chunk<XT, kVec>(g + pa[u], ga[u]);
         if (pb[u] >= 0) load_chunk<XT, kVec>(g + pb[u], gb[u]);
       }
+    }
+    // a position outside the table reads nothing there: the token's outputs are NaN
+    const bool placed = rot == 0 || (pos >= 0 && pos < a.places);
+#pragma unroll
+    for (int u = 0; u < kUnits; ++u) {
       const int unit = unit0 + u * lph;
       if (unit < rot_units && placed) {
         load_chunk<float, kVec>(a.cos + pos * half + unit * kVec, cs[u]);
@@ -184,7 +190,7 @@ __global__ __launch_bounds__(kThreads) void head_norm_kernel(HeadArgs a) {
       for (int i = 0; i < kVec; ++i) ss += xa[u][i] * xa[u][i] + xb[u][i] * xb[u][i];
     }
     ss = head_sum(ss, lph);
-    float inv = 1.f / sqrtf(ss / (float)d + a.eps);
+    float inv = rsqrtf(ss * inv_d + a.eps);
     if (!placed) inv = __builtin_nanf("");
     XT *y = reinterpret_cast<XT *>(h.y) + tok * h.y_ts + head * h.y_hs;
     if constexpr (!kBwd) {
@@ -215,7 +221,7 @@ __global__ __launch_bounds__(kThreads) void head_norm_kernel(HeadArgs a) {
           dot += ga[u][i] * xa[u][i] + gb[u][i] * xb[u][i];
         }
       }
-      dot = head_sum(dot, lph) / (float)d;
+      dot = head_sum(dot, lph) * inv_d;
 #pragma unroll
       for (int u = 0; u < kUnits; ++u) {
 #pragma unroll
@@ -316,6 +322,7 @@ int chunk_of(const HeadArgs &a, bool f32, bool bwd) {
     if (!h.heads) return;
     all |= (uint64_t)h.x_ts | (uint64_t)h.x_hs | (uint64_t)h.y_ts | (uint64_t)h.y_hs;
     all |= reinterpret_cast<uintptr_t>(h.x) / esz | reinterpret_cast<uintptr_t>(h.y) / esz;
+    all |= reinterpret_cast<uintptr_t>(h.w) / (a.w_f32 ? 4 : 2);
     if (bwd) all |= (uint64_t)h.g_ts | (uint64_t)h.g_hs | reinterpret_cast<uintptr_t>(h.g) / esz;
   };
   side(a.q);
@@ -328,10 +335,14 @@ int chunk_of(const HeadArgs &a, bool f32, bool bwd) {
 
 }  // namespace
 
-int head_norm_max_blocks() { return 2048; }
+// Workgroups at most: a few for each of the 256 CUs, each walking over several items so that the weight
+// is loaded once for them. 8192 tokens of 32 + 8 heads of 128: forward 33.0 us with 1024, 30.7 with
+// 1536, 35.4 with 2048; backward (110 registers, four waves a SIMD: 1024 run at once) 75 us with 1024,
+// 79 with 2048. Two heads at a time a thread took 50 and 110 us (registers).
+constexpr int kMostFwd = 1536, kMostBwd = 1024;
+int head_norm_max_blocks() { return kMostBwd; }   // parts of dw
 
-// Workgroups: enough for every item at once, at most 2048 (8 for each of 256 CUs, which is what
-// their registers let run together), split between q and k by their heads.
+// Enough workgroups for every item, split between q and k by their heads.
 static int head_norm_blocks(int64_t items, int per_block, int64_t most) {
   const int64_t b = (items + per_block - 1) / per_block;
   return (int)(b < most ? b : most);
@@ -347,7 +358,7 @@ hipError_t launch_head_norm(HeadArgs a, bool f32, bool inter, bool bwd, float *d
   int lanes = 1;
   while (lanes < units && lanes < 64) lanes <<= 1;
   a.lanes = lanes;
-  const int per_block = kThreads / lanes, most = head_norm_max_blocks();
+  const int per_block = kThreads / lanes, most = bwd ? kMostBwd : kMostFwd;
   const int64_t most_q = heads ? (most * (int64_t)a.q.heads + heads - 1) / heads : 0;
   a.blocks_q = a.q.heads ? head_norm_blocks(a.m * a.q.heads, per_block, most_q < most - 1 ? most_q : most - 1) : 0;
   const int blocks_k = a.k.heads ? head_norm_blocks(a.m * a.k.heads, per_block, most - a.blocks_q) : 0;
