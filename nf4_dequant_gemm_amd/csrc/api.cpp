@@ -1068,9 +1068,9 @@ int stream_tsplits(int64_t k, int32_t r) {
 // ranks padded to a multiple of 8 (when they are not one), then float sums (of T, then of Y).
 // Backward: the rows' order, U [m, r] and its padded form, B transposed [L, r, n], A transposed [L, k,
 // r padded], T (recomputed when the caller passes none) and its padded form, then float sums of the
-// row projections or of the sums over rows (never both at once).
+// row projections, of dX or of the sums over rows (one at a time).
 struct MultiWs {
-  int sp_k = 1, sp_n = 1, sa = 1, sb = 1;
+  int sp_k = 1, sp_n = 1, pieces = 1;
   size_t plan = 0, bp = 0, u = 0, up = 0, bt = 0, at = 0, t = 0, tp = 0, part = 0, total = 0;
 };
 
@@ -1083,15 +1083,15 @@ MultiWs multi_ws(int64_t m, int64_t n, int64_t k, int32_t r, int32_t L, bool bwd
   size_t p = w.sp_k > 1 ? (size_t)w.sp_k * m * r * 4 : 0;
   if (bwd) {
     w.sp_n = nf4q::multi_rows_splits(m, n);
-    w.sa = nf4q::multi_sum_splits(m, k, L);
-    w.sb = nf4q::multi_sum_splits(m, n, L);
     w.u = w.t = align256((size_t)m * r * 2);
     w.up = w.tp;
     w.bt = align256((size_t)L * r * n * 2);
     w.at = align256((size_t)L * rp * k * 2);
+    w.pieces = nf4q::dx_multi_pieces(m, k, n);
     if (w.sp_n > 1) p = std::max(p, (size_t)w.sp_n * m * r * 4);
-    if (w.sa > 1) p = std::max(p, (size_t)L * w.sa * r * k * 4);
-    if (w.sb > 1) p = std::max(p, (size_t)L * w.sb * r * n * 4);
+    if (w.pieces > 1) p = std::max(p, (size_t)w.pieces * m * k * 4);
+    p = std::max(p, (size_t)nf4q::multi_sum_blocks(m, k, L) * r * k * 4);
+    p = std::max(p, (size_t)nf4q::multi_sum_blocks(m, n, L) * r * n * 4);
   } else {
     if (rp != r) w.bp = align256((size_t)L * n * rp * 2);
     p = std::max(p, nf4q::mid_fwd_bytes(m, n, k, rp));   // T is whole before the sums of Y start
@@ -1192,7 +1192,7 @@ int qlora_multi_fwd(const void *X, int64_t m, const nf4_tensor *W, const void *A
     return hip_status(nf4q::launch_stream16_fwd_multi(g, mu, part, splits, (uint16_t *)T, sm), "qlora_multi_fwd launch");
   }
   if (m > nf4q::kMultiSmallM) {
-    const nf4q::MultiPlan pl = nf4q::multi_plan_at(base, m, L);
+    const nf4q::MultiPlan pl = nf4q::multi_plan_at(base, m, L, nf4q::multi_sum_rows(m, k), nf4q::multi_sum_rows(m, n));
     e = nf4q::launch_multi_plan(ids, m, L, pl, sm);
     if (e == hipSuccess)
       e = nf4q::launch_multi_rows(x, k, a, (int64_t)r * k, k, m, k, r, L, lay.sp_k, part, (uint16_t *)T, pl, sm);
@@ -1221,7 +1221,7 @@ int qlora_multi_bwd(const void *dY, const void *X, int64_t m, const nf4_tensor *
   if (st) return st;
   hipStream_t sm = (hipStream_t)stream;
   char *base = (char *)ws;
-  const nf4q::MultiPlan pl = nf4q::multi_plan_at(base, m, L);
+  const nf4q::MultiPlan pl = nf4q::multi_plan_at(base, m, L, nf4q::multi_sum_rows(m, k), nf4q::multi_sum_rows(m, n));
   char *at = base + lay.plan;
   auto take = [&](size_t bytes) {
     char *q = at;
@@ -1245,21 +1245,23 @@ int qlora_multi_bwd(const void *dY, const void *X, int64_t m, const nf4_tensor *
     t = Tw;
   }
   e = pad_ranks(&t, m, r, Tp, sm);
-  if (e == hipSuccess) e = nf4q::launch_multi_transpose((const uint16_t *)B, n, r, n, L, Bt, sm);
+  if (e == hipSuccess) e = nf4q::launch_multi_transpose((const uint16_t *)B, n, r, n, L, pl, Bt, sm);
   if (e != hipSuccess) return hip_status(e, "qlora_multi_bwd transpose launch");
   e = nf4q::launch_multi_rows(dy, n, Bt, (int64_t)r * n, n, m, n, r, L, lay.sp_n, part, U, pl, sm);
   if (e == hipSuccess) e = pad_ranks(&u, m, r, Up, sm);
   if (e != hipSuccess) return hip_status(e, "qlora_multi_bwd U launch");
   if (dX) {
-    e = nf4q::launch_multi_transpose((const uint16_t *)A, r, k, rp, L, At, sm);
+    e = nf4q::launch_multi_transpose((const uint16_t *)A, r, k, rp, L, pl, At, sm);
     if (e != hipSuccess) return hip_status(e, "qlora_multi_bwd transpose launch");
-    const nf4q::MultiArgs mu{ids, s, u, At, L, rp, pl.perm};
+    const nf4q::MultiArgs mu{ids, s, u, At, L, rp, pl.perm, lay.pieces, part};
     e = nf4q::launch_gemm_dx_multi(multi_gemm(dY, m, W, k, n, dX), mu, sm);
+    if (e == hipSuccess && lay.pieces > 1)
+      e = nf4q::launch_multi_final(part, lay.pieces, m, k, mu, (uint16_t *)dX, sm);
     if (e != hipSuccess) return hip_status(e, "qlora_multi_bwd dX launch");
   }
-  e = nf4q::launch_multi_sum(u, rp, x, k, k, r, L, s, lay.sa, part, (uint16_t *)dA, false, pl, sm);
+  e = nf4q::launch_multi_sum(u, rp, x, k, m, k, r, L, s, nf4q::kPlanSumA, part, (uint16_t *)dA, false, pl, sm);
   if (e != hipSuccess) return hip_status(e, "qlora_multi_bwd dA launch");
-  e = nf4q::launch_multi_sum(t, rp, dy, n, n, r, L, s, lay.sb, part, (uint16_t *)dB, true, pl, sm);
+  e = nf4q::launch_multi_sum(t, rp, dy, n, m, n, r, L, s, nf4q::kPlanSumB, part, (uint16_t *)dB, true, pl, sm);
   return hip_status(e, "qlora_multi_bwd dB launch");
 }
 

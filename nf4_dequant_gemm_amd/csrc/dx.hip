@@ -162,8 +162,9 @@ __device__ __forceinline__ void dx_origin(int64_t m_lo, int64_t m_hi, int tiles_
 // kMulti: the rows have adapters of their own (mu; g.r is 0) and are taken in the order of their
 // adapters, row m of the launch being row mu.perm[m] of dY and dX; after the reduction, each wave adds
 // the low-rank term of its block from the transposed adapters, straight from registers (multi_term,
-// multi.h).
-template <int kFmt, bool kGrp, bool kMulti = false>
+// multi.h). kSplit: a workgroup runs one of mu.pieces parts of the reduction and leaves its float32 sums
+// in mu.part (a kernel of its own: both endings in one spilled 120 registers and cost 100 us of 670).
+template <int kFmt, bool kGrp, bool kMulti = false, bool kSplit = false>
 __device__ __forceinline__ void dx_body(const GemmArgs &g, const GroupArgs &gr, const MultiArgs &mu) {
   constexpr bool kDQ = kFmt == 1, kFP4 = kFmt == 2;
   // separate LDS arrays per buffer: the compiler then knows that accesses to one do not alias
@@ -210,6 +211,11 @@ __device__ __forceinline__ void dx_body(const GemmArgs &g, const GroupArgs &gr, 
     m_lo = grp_m_off(gr, e);
     m_hi = grp_m_off(gr, e + 1);
     wbase = (int64_t)e * g.R;
+  } else if (kSplit) {
+    const int tiles = (int)gridDim.x / mu.pieces;
+    logical = tile_remap(blockIdx.x % tiles, tiles);
+    piece = (int)blockIdx.x / tiles;
+    sp.S = mu.pieces;
   } else {
     logical = tile_remap(blockIdx.x, gridDim.x);
   }
@@ -473,6 +479,23 @@ __device__ __forceinline__ void dx_body(const GemmArgs &g, const GroupArgs &gr, 
     return;
   }
 
+  // The sums of a part at the rows' own places, 4 columns a lane.
+  if constexpr (kSplit) {
+    const float tsc = kFP4 ? tscale() : 1.f;
+#pragma unroll
+    for (int mt = 0; mt < 8; ++mt) {
+      const int64_t m = m0 + wm * 128 + mt * 16 + l16;
+      if (m >= m_hi) continue;
+      float *row = mu.part + ((int64_t)piece * g.M + mu.perm[m]) * g.C;
+#pragma unroll
+      for (int kt = 0; kt < 4; ++kt) {
+        const int64_t k = k0 + wk * 64 + kt * 16 + 4 * g16;
+        if (k < g.C) *reinterpret_cast<f32x4 *>(row + k) = kFP4 ? acc[kt][mt] * tsc : acc[kt][mt];
+      }
+    }
+    return;
+  }
+
   // Epilogue. With the weight as the MFMA A operand, a lane holds columns k..k+3 of row m. Each
   // wave packs its 128 x 64 block to bf16 in 16 KB of the (now idle) LDS and writes it out as whole
   // 128-byte row pieces, 16 bytes per lane, with non-temporal stores (dX is not read again by this
@@ -483,7 +506,7 @@ __device__ __forceinline__ void dx_body(const GemmArgs &g, const GroupArgs &gr, 
     blk += (wave & 1) * (kYChunks / 2);
     uint2 *b2 = reinterpret_cast<uint2 *>(blk);
     float tsc = kFP4 ? tscale() : 1.f;
-    if constexpr (kMulti) {   // E2M1: the sums leave the units of the tensor scale first
+    if constexpr (kMulti && !kSplit) {   // E2M1: the sums leave the units of the tensor scale first
       if (kFP4) {
 #pragma unroll
         for (int kt = 0; kt < 4; ++kt)
@@ -530,6 +553,10 @@ __global__ __launch_bounds__(kThreads) void dx_grouped_kernel(GemmArgs g, GroupA
 template <int kFmt>
 __global__ __launch_bounds__(kThreads) void dx_multi_kernel(GemmArgs g, MultiArgs mu) {
   dx_body<kFmt, false, true>(g, GroupArgs{}, mu);
+}
+template <int kFmt>
+__global__ __launch_bounds__(kThreads) void dx_split_kernel(GemmArgs g, MultiArgs mu) {
+  dx_body<kFmt, false, true, true>(g, GroupArgs{}, mu);
 }
 
 // The split tiles of a grouped dX launch: workgroups 4 i .. 4 i + 3 add the S float32 pieces of
@@ -613,10 +640,38 @@ hipError_t launch_gemm_dx_grouped(const GemmArgs &g, const GroupArgs &gr, hipStr
   return hipGetLastError();
 }
 
+// Pieces of the reduction of a dX launch whose 256 x 256 tiles would leave CUs idle: the least of (rounds
+// of 256 workgroups) x (start and end, 12 us, and 2.2 us a step of 64) plus the traffic of the float32
+// sums, in us.
+int dx_multi_pieces(int64_t M, int64_t K, int64_t N) {
+  const int64_t tiles = ((K + kT - 1) / kT) * ((M + kT - 1) / kT), steps = (N + kS - 1) / kS;
+  double best = 0;
+  int pieces = 1;
+  for (int64_t p = 1; p <= 64 && p <= steps; ++p) {
+    const double us = (double)((tiles * p + 255) / 256) * (12.0 + 2.2 * (double)((steps + p - 1) / p)) +
+                      (p > 1 ? 5.0 + (double)(p * M * K) * 8 / 4.0e6 : 0.0);
+    if (p == 1 || us < best) {
+      best = us;
+      pieces = (int)p;
+    }
+  }
+  return pieces;
+}
+
 hipError_t launch_gemm_dx_multi(const GemmArgs &g, const MultiArgs &mu, hipStream_t st) {
-  if (((g.C | g.ldo) & 7) != 0 || (reinterpret_cast<uintptr_t>(g.out) & 15) != 0 || g.R != g.w.n || g.r != 0 || !mu.perm || g.M * g.R * 2 > kMultiMaxGather)
+  if (((g.C | g.ldo) & 7) != 0 || (reinterpret_cast<uintptr_t>(g.out) & 15) != 0 || g.R != g.w.n || g.r != 0 || !mu.perm || g.M * g.R * 2 > kMultiMaxGather || mu.pieces < 1 ||
+      (mu.pieces > 1 && !mu.part))
     return hipErrorInvalidValue;
-  const int64_t tiles = ((g.C + kT - 1) / kT) * ((g.M + kT - 1) / kT);
+  const int64_t tiles = ((g.C + kT - 1) / kT) * ((g.M + kT - 1) / kT) * mu.pieces;
+  if (mu.pieces > 1) {
+    if (g.w.fp4)
+      dx_split_kernel<2><<<dim3((unsigned)tiles), dim3(kThreads), 0, st>>>(g, mu);
+    else if (g.w.dq)
+      dx_split_kernel<1><<<dim3((unsigned)tiles), dim3(kThreads), 0, st>>>(g, mu);
+    else
+      dx_split_kernel<0><<<dim3((unsigned)tiles), dim3(kThreads), 0, st>>>(g, mu);
+    return hipGetLastError();
+  }
   if (g.w.fp4)
     dx_multi_kernel<2><<<dim3((unsigned)tiles), dim3(kThreads), 0, st>>>(g, mu);
   else if (g.w.dq)

@@ -214,11 +214,15 @@ hipError_t launch_merge(const WDesc &w, const uint16_t *A, const uint16_t *B, in
 // reach kMultiMaxGather bytes of X (dY).
 hipError_t launch_gemm_fwd_multi(const GemmArgs &g, const MultiArgs &mu, hipStream_t st);
 hipError_t launch_gemm_dx_multi(const GemmArgs &g, const MultiArgs &mu, hipStream_t st);
+// With mu.pieces > 1 (dx_multi_pieces) dX leaves float32 sums in mu.part, which launch_multi_final turns
+// into out [M][C] (at most 2^20 rows), adding the low-rank term.
+int dx_multi_pieces(int64_t M, int64_t K, int64_t N);
+hipError_t launch_multi_final(const float *part, int splits, int64_t M, int64_t C, const MultiArgs &mu, uint16_t *out,
+                              hipStream_t st);
 // The rows' order, and the thin products over it (multi.hip): out[i] = in[i] p_a^T for the rows i of
 // adapter a (zero without one), p_a = p + a * pstride of r rows of leading dimension ldp, with
 // splits * M * r partial floats; and out[a] = s[a] * (sum over its rows of P_i^T Q_i), [r][C] or
-// transposed [C][r], with L * splits * r * C partial floats (none for one split); P has row stride
-// ldp, a multiple of 8, zeros from r on.
+// transposed [C][r]; P has row stride ldp, a multiple of 8, zeros from r on.
 hipError_t launch_multi_plan(const int32_t *ids, int64_t M, int L, const MultiPlan &pl, hipStream_t st);
 int multi_rows_splits(int64_t M, int64_t Lr);
 hipError_t launch_multi_rows(const uint16_t *in, int64_t ldin, const uint16_t *p, int64_t pstride, int64_t ldp,
@@ -240,14 +244,17 @@ size_t mid_fwd_bytes(int64_t M, int64_t N, int64_t K, int rp);
 // split partials float [M][r][tsplits] (launch_multi_rows_part), added inside and written to tout.
 hipError_t launch_stream16_fwd_multi(const GemmArgs &g, const MultiArgs &mu, const float *tpart, int tsplits,
                                      uint16_t *tout, hipStream_t st);
-int multi_sum_splits(int64_t M, int64_t C, int L);
-hipError_t launch_multi_sum(const uint16_t *P, int64_t ldp, const uint16_t *Q, int64_t ldq, int64_t C, int r, int L,
-                            const float *s, int splits, float *part, uint16_t *out, bool transposed,
+// The sums over rows: blocks of multi_sum_rows(M, C) rows, which is what pl.rows[which] has to be
+// (kPlanSumA or kPlanSumB); partial floats: multi_sum_blocks * r * C.
+int multi_sum_rows(int64_t M, int64_t C);
+int64_t multi_sum_blocks(int64_t M, int64_t C, int L);
+hipError_t launch_multi_sum(const uint16_t *P, int64_t ldp, const uint16_t *Q, int64_t ldq, int64_t M, int64_t C, int r,
+                            int L, const float *s, int which, float *part, uint16_t *out, bool transposed,
                             const MultiPlan &pl, hipStream_t st);
-// dst[b][c][j] = src[b][j][c] of `batch` bf16 matrices [R][C], rows of dst padded with zeros to ldd; and
-// dst [rows][rp] = src [rows][r] padded with zeros.
-hipError_t launch_multi_transpose(const uint16_t *src, int64_t R, int64_t C, int64_t ldd, int batch, uint16_t *dst,
-                                  hipStream_t st);
+// dst[a][c][j] = src[a][j][c] of the bf16 matrices [R][C] of the adapters that have rows, rows of dst
+// padded with zeros to ldd, a multiple of 8; and dst [rows][rp] = src [rows][r] padded with zeros.
+hipError_t launch_multi_transpose(const uint16_t *src, int64_t R, int64_t C, int64_t ldd, int L, const MultiPlan &pl,
+                                  uint16_t *dst, hipStream_t st);
 hipError_t launch_multi_pad(const uint16_t *src, int64_t rows, int r, int rp, uint16_t *dst, hipStream_t st);
 
 // Norm and rotation of query and key heads (headnorm.hip). One side (q or k): element strides of a

@@ -404,9 +404,9 @@ __global__ __launch_bounds__(kThreads) void mid_kernel(MidArgs g, MultiArgs mu) 
   }
 }
 
-// Y from the float32 sums of the launch before, added in order, and the low-rank term, with T from its
-// own sums (written here, by the workgroups of the first columns) or from memory. One wave: 16 rows
-// and 64 columns.
+// Y (or dX) from the float32 sums of the launch before, added in order, and the low-rank term, with T from
+// its own sums (written here, by the workgroups of the first columns) or T (U) from memory. One wave:
+// 16 rows and 64 columns.
 __global__ __launch_bounds__(64) void mid_final_kernel(MidArgs g, MultiArgs mu) {
   const int lane = threadIdx.x, g16 = lane >> 4, l16 = lane & 15;
   const int64_t m0 = (int64_t)blockIdx.y * 16, m = m0 + l16, n0 = (int64_t)blockIdx.x * 64;
@@ -514,6 +514,20 @@ size_t mid_fwd_bytes(int64_t M, int64_t N, int64_t K, int rp) {
   const MidShape s = mid_shape(M, N, K);
   const int ts = mid_tsplits(M, K);
   return up256(s.splits > 1 || ts ? (size_t)s.splits * M * N * 4 : 0) + (size_t)ts * M * rp * 4;
+}
+
+hipError_t launch_multi_final(const float *part, int splits, int64_t M, int64_t C, const MultiArgs &mu, uint16_t *out,
+                              hipStream_t st) {
+  const int64_t tiles = (M + 15) / 16;
+  if (tiles > 65535 || (C & 7) != 0 || splits < 1) return hipErrorInvalidValue;
+  MidArgs a{};
+  a.M = M;
+  a.N = C;
+  a.Y = out;
+  a.part = const_cast<float *>(part);
+  a.splits = splits;
+  mid_final_kernel<<<dim3((unsigned)((C + 63) / 64), (unsigned)tiles), dim3(64), 0, st>>>(a, mu);
+  return hipGetLastError();
 }
 
 hipError_t launch_mid_fwd_multi(const GemmArgs &ga, const MultiArgs &mu, const uint16_t *A, int ra, uint16_t *T,

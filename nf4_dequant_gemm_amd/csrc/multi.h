@@ -16,6 +16,10 @@ struct MultiArgs {
   const uint16_t *Q;     // [L][C][r]
   int L, r;
   const int32_t *perm = nullptr;   // [M]: the rows in the order of their adapters, where a kernel takes them so
+  // dX with its reduction split over `pieces` workgroups: their float32 sums, [pieces][M][K], which
+  // launch_multi_final adds (with the low-rank term)
+  int pieces = 1;
+  float *part = nullptr;
 };
 // Bytes of X (dY) that the gathering copies reach with 32-bit offsets; past-the-end rows use an offset
 // above it.
@@ -231,19 +235,23 @@ __device__ __forceinline__ void multi_rows_of(const uint16_t *in, int64_t ldin, 
 }
 
 // The rows in the order of their adapters (rows without one last, as group L), each group's rows in
-// their own order, and each group's first row and first 16- and 64-row block. int32 tables of a
-// workspace, written by launch_multi_plan.
+// their own order, and each group's first row and first block of 16 rows, of 64 rows, and of the two
+// row counts that the sums over rows take at a time. int32 tables of a workspace, written by
+// launch_multi_plan.
 constexpr int kMultiMaxAdapters = 1024;
+constexpr int kMultiTables = 5;
 struct MultiPlan {
-  int32_t *perm;    // [M]
-  int32_t *off;     // [L + 2]
-  int32_t *blk16;   // [L + 2]
-  int32_t *blk64;   // [L + 2]
+  int32_t *perm;                 // [M]
+  int32_t *table[kMultiTables];  // [L + 2] each: first row, then first blocks
+  int rows[kMultiTables];        // rows of a block: 1, 16, 64, and the sums'
 };
-inline size_t multi_plan_bytes(int64_t m, int L) { return 4 * ((size_t)m + 3 * (size_t)(L + 2)); }
-inline MultiPlan multi_plan_at(void *ws, int64_t m, int L) {
+enum { kPlanRow = 0, kPlan16 = 1, kPlan64 = 2, kPlanSumA = 3, kPlanSumB = 4 };
+inline size_t multi_plan_bytes(int64_t m, int L) { return 4 * ((size_t)m + kMultiTables * (size_t)(L + 2)); }
+inline MultiPlan multi_plan_at(void *ws, int64_t m, int L, int rows_a, int rows_b) {
   int32_t *p = reinterpret_cast<int32_t *>(ws);
-  return MultiPlan{p, p + m, p + m + (L + 2), p + m + 2 * (L + 2)};
+  MultiPlan pl{p, {}, {1, 16, 64, rows_a, rows_b}};
+  for (int t = 0; t < kMultiTables; ++t) pl.table[t] = p + m + t * (L + 2);
+  return pl;
 }
 
 }  // namespace nf4q

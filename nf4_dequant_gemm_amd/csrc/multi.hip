@@ -15,13 +15,13 @@ namespace {
 // ------------------------------------------------------------------------------------ row order
 // One workgroup: a stable counting sort of the rows by adapter. Wave w counts its run of rows in LDS,
 // the counts are scanned over adapters and waves, and each wave then places its rows in order,
-// ranking the lanes of equal adapter by a ballot.
-constexpr int kPlanThreads = 1024, kPlanWaves = kPlanThreads / 64;
+// ranking the lanes of equal adapter by a ballot. A wave's ids are loaded eight 64-row pieces at a time.
+constexpr int kPlanThreads = 1024, kPlanWaves = kPlanThreads / 64, kPlanAhead = 8;
 
 __global__ __launch_bounds__(kPlanThreads) void multi_plan_kernel(const int32_t *__restrict__ ids, int64_t M,
                                                                   int L, MultiPlan pl) {
   extern __shared__ int32_t cnt[];   // [kPlanWaves][L + 1]
-  __shared__ int32_t scan[3][kPlanThreads];
+  __shared__ int32_t scan[kMultiTables][kPlanThreads];
   const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
   const int G = L + 1;
   for (int i = tid; i < kPlanWaves * G; i += kPlanThreads) cnt[i] = 0;
@@ -29,33 +29,54 @@ __global__ __launch_bounds__(kPlanThreads) void multi_plan_kernel(const int32_t 
   const int64_t per = ((M + kPlanWaves - 1) / kPlanWaves + 63) / 64 * 64;
   const int64_t lo = wave * per, hi = lo + per < M ? lo + per : M;
   volatile int32_t *mine = cnt + wave * G;   // written by one lane, read by the others of its wave
-  auto group = [&](int64_t i) {
-    const int a = ids[i];
-    return a >= 0 && a < L ? a : L;
+  // groups of the lane's rows i0 + lane, + 64, ... (-1: past the run)
+  auto load = [&](int64_t i0, int (&g)[kPlanAhead]) {
+    int a[kPlanAhead];
+#pragma unroll
+    for (int q = 0; q < kPlanAhead; ++q) {
+      const int64_t i = i0 + 64 * q + lane;
+      a[q] = i < hi ? ids[i] : -1;
+    }
+#pragma unroll
+    for (int q = 0; q < kPlanAhead; ++q) g[q] = i0 + 64 * q + lane >= hi ? -1 : a[q] >= 0 && a[q] < L ? a[q] : L;
   };
-  for (int64_t i = lo + lane; i < hi; i += 64) atomicAdd(&cnt[wave * G + group(i)], 1);
+  for (int64_t i0 = lo; i0 < hi; i0 += 64 * kPlanAhead) {
+    int g[kPlanAhead];
+    load(i0, g);
+#pragma unroll
+    for (int q = 0; q < kPlanAhead; ++q) {   // one addition for each distinct adapter of a piece
+      uint64_t left = __ballot(g[q] >= 0);
+      while (left) {
+        const int a = __builtin_amdgcn_readlane(g[q], __builtin_ctzll(left));
+        const uint64_t same = __ballot(g[q] == a);
+        if (lane == 0) mine[a] = mine[a] + __popcll(same);
+        left &= ~same;
+      }
+    }
+  }
   __syncthreads();
-  // adapter g = thread g: its rows, and blocks of 16 and 64; inclusive scans over the adapters
+  // adapter g = thread g: its rows and blocks; inclusive scans over the adapters
   int32_t n = 0;
   if (tid < L)
     for (int w = 0; w < kPlanWaves; ++w) n += cnt[w * G + tid];
-  int32_t v[3] = {n, (n + 15) / 16, (n + 63) / 64};
-  const int32_t own[3] = {v[0], v[1], v[2]};
+  int32_t own[kMultiTables], v[kMultiTables];
 #pragma unroll
-  for (int q = 0; q < 3; ++q) scan[q][tid] = v[q];
+  for (int q = 0; q < kMultiTables; ++q) {
+    own[q] = (n + pl.rows[q] - 1) / pl.rows[q];
+    scan[q][tid] = own[q];
+  }
   __syncthreads();
   for (int o = 1; o < L; o <<= 1) {
 #pragma unroll
-    for (int q = 0; q < 3; ++q) v[q] = tid >= o ? scan[q][tid - o] : 0;
+    for (int q = 0; q < kMultiTables; ++q) v[q] = tid >= o ? scan[q][tid - o] : 0;
     __syncthreads();
 #pragma unroll
-    for (int q = 0; q < 3; ++q) scan[q][tid] += v[q];
+    for (int q = 0; q < kMultiTables; ++q) scan[q][tid] += v[q];
     __syncthreads();
   }
-  int32_t *out[3] = {pl.off, pl.blk16, pl.blk64};
   if (tid < L) {
 #pragma unroll
-    for (int q = 0; q < 3; ++q) out[q][tid] = scan[q][tid] - own[q];
+    for (int q = 0; q < kMultiTables; ++q) pl.table[q][tid] = scan[q][tid] - own[q];
     int32_t at = scan[0][tid] - own[0];
     for (int w = 0; w < kPlanWaves; ++w) {
       const int32_t c = cnt[w * G + tid];
@@ -66,12 +87,11 @@ __global__ __launch_bounds__(kPlanThreads) void multi_plan_kernel(const int32_t 
   if (tid == 0) {
     int32_t at = scan[0][L - 1];
     const int32_t none = (int32_t)M - at;
-    pl.off[L] = at;
-    pl.off[L + 1] = (int32_t)M;
-    pl.blk16[L] = scan[1][L - 1];
-    pl.blk16[L + 1] = scan[1][L - 1] + (none + 15) / 16;
-    pl.blk64[L] = scan[2][L - 1];
-    pl.blk64[L + 1] = scan[2][L - 1] + (none + 63) / 64;
+#pragma unroll
+    for (int q = 0; q < kMultiTables; ++q) {
+      pl.table[q][L] = scan[q][L - 1];
+      pl.table[q][L + 1] = scan[q][L - 1] + (none + pl.rows[q] - 1) / pl.rows[q];
+    }
     for (int w = 0; w < kPlanWaves; ++w) {
       const int32_t c = cnt[w * G + L];
       cnt[w * G + L] = at;
@@ -79,20 +99,23 @@ __global__ __launch_bounds__(kPlanThreads) void multi_plan_kernel(const int32_t 
     }
   }
   __syncthreads();
-  for (int64_t i0 = lo; i0 < hi; i0 += 64) {
-    const int64_t i = i0 + lane;
-    const int g = i < hi ? group(i) : -1;
-    uint64_t left = __ballot(i < hi);
-    while (left) {
-      const int a = __builtin_amdgcn_readlane(g, __builtin_ctzll(left));
-      const uint64_t same = __ballot(g == a);
-      const int32_t at = mine[a];   // a wave's LDS accesses are in order
-      if (g == a) {
-        const int32_t rank = __popcll(same & ((uint64_t(1) << lane) - 1));
-        pl.perm[at + rank] = (int32_t)i;
-        if (rank == 0) mine[a] = at + __popcll(same);
+  for (int64_t i0 = lo; i0 < hi; i0 += 64 * kPlanAhead) {
+    int g[kPlanAhead];
+    load(i0, g);
+#pragma unroll
+    for (int q = 0; q < kPlanAhead; ++q) {
+      uint64_t left = __ballot(g[q] >= 0);
+      while (left) {
+        const int a = __builtin_amdgcn_readlane(g[q], __builtin_ctzll(left));
+        const uint64_t same = __ballot(g[q] == a);
+        const int32_t at = mine[a];   // a wave's LDS accesses are in order
+        if (g[q] == a) {
+          const int32_t rank = __popcll(same & ((uint64_t(1) << lane) - 1));
+          pl.perm[at + rank] = (int32_t)(i0 + 64 * q + lane);
+          if (rank == 0) mine[a] = at + __popcll(same);
+        }
+        left &= ~same;
       }
-      left &= ~same;
     }
   }
 }
@@ -122,11 +145,11 @@ __global__ __launch_bounds__(256) void multi_rows16_kernel(const uint16_t *__res
                                                            uint16_t *__restrict__ out, MultiPlan pl) {
   __shared__ f32x4 red[4][TN][64];
   const int b = blockIdx.x;
-  if (b >= pl.blk16[L + 1]) return;
-  const int a = group_of_block(pl.blk16, L, b);
+  if (b >= pl.table[kPlan16][L + 1]) return;
+  const int a = group_of_block(pl.table[kPlan16], L, b);
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
   const int split = blockIdx.y, nl = lane & 15, kg = lane >> 4;
-  const int32_t row0 = pl.off[a] + (b - pl.blk16[a]) * 16, rowe = pl.off[a + 1];
+  const int32_t row0 = pl.table[kPlanRow][a] + (b - pl.table[kPlan16][a]) * 16, rowe = pl.table[kPlanRow][a + 1];
   const bool have = row0 + nl < rowe && a < L;
   const uint16_t *x = in + (have ? (int64_t)pl.perm[row0 + nl] * ldin : 0);
   const uint16_t *pa = p + (a < L ? a : 0) * pstride;
@@ -194,11 +217,11 @@ __global__ __launch_bounds__(256) void multi_rows64_kernel(const uint16_t *__res
   __shared__ uint4 sI[2][64 * 8];
   __shared__ uint4 sP[2][PCH];
   const int b = blockIdx.x;
-  if (b >= pl.blk64[L + 1]) return;
-  const int a = group_of_block(pl.blk64, L, b);
+  if (b >= pl.table[kPlan64][L + 1]) return;
+  const int a = group_of_block(pl.table[kPlan64], L, b);
   const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
   const int split = blockIdx.y;
-  const int32_t row0 = pl.off[a] + (b - pl.blk64[a]) * 64, rowe = pl.off[a + 1];
+  const int32_t row0 = pl.table[kPlanRow][a] + (b - pl.table[kPlan64][a]) * 64, rowe = pl.table[kPlanRow][a + 1];
   const uint16_t *pa = p + (a < L ? a : 0) * pstride;
   const int64_t lb = split * lsplit, le = lb + lsplit < Lr ? lb + lsplit : Lr;
   // this thread's rows of the in-tile (tid / 8 and 32 more), and chunk tid % 8 of each
@@ -319,11 +342,15 @@ __global__ void multi_rows_sum_kernel(const float *__restrict__ part, int64_t n,
 }
 
 // ------------------------------------------------------------------------------------ sums over rows
-// part[a][split][j][c] = sum over the rows i of adapter a in the split of P[i][j] * Q[i][c]
-// (dA: P = U, Q = X; dB: P = T, Q = dY); with one split, s[a] times it goes straight to out. Workgroup: 128 columns x all r ranks, in stages of 64 rows
-// loaded two stages ahead, staged row-major in LDS (rows padded by 32 bytes) and read with the
-// transposing LDS load, which gives a lane 4 consecutive rows of one column: the MFMA operand with
-// the rows as its reduction index.
+// A block of rows (block blockIdx.y of the plan's table `which`, at most kSumRows rows, all of one adapter
+// a): the sum over them of P[i][j] * Q[i][c] (dA: P = U, Q = X; dB: P = T, Q = dY), as out holds it
+// ([r][C], transposed [C][r]). An adapter of one block writes s[a] times it to out; otherwise it goes to
+// part[block] and multi_sum_final_kernel adds the adapter's blocks in order. Blocks of equal size, not a
+// split count for every adapter, because one adapter may hold most of the rows.
+// Workgroup: 128 columns x all r ranks, in stages of 64 rows loaded two stages ahead, staged row-major
+// in LDS (rows padded by 32 bytes) and read with the transposing LDS load, which gives a lane 4
+// consecutive rows of one column: the MFMA operand with the rows as its reduction index.
+constexpr int kSumRows = 1024;
 constexpr int kRB = 64, kCB = 128, kQRow = kCB + 16;
 typedef __attribute__((ext_vector_type(4))) short s16x4;
 typedef __attribute__((ext_vector_type(8))) short s16x8;
@@ -335,19 +362,24 @@ __device__ __forceinline__ s16x4 lds_tr(const uint16_t *p) {
 template <int TJ>
 __global__ __launch_bounds__(256) void multi_sum_kernel(const uint16_t *__restrict__ P,
                                                         int64_t ldp, const uint16_t *__restrict__ Q, int64_t ldq,
-                                                        int64_t C, int r, float *__restrict__ part,
-                                                        const float *__restrict__ s, bool transposed,
-                                                        uint16_t *__restrict__ out, MultiPlan pl) {
+                                                        int64_t C, int r, int L, int which,
+                                                        float *__restrict__ part, const float *__restrict__ s,
+                                                        bool transposed, uint16_t *__restrict__ out, MultiPlan pl) {
   constexpr int PROW = TJ * 16 + 16;
   __shared__ uint16_t sQ[2][kRB * kQRow];
   __shared__ uint16_t sP[2][kRB * PROW];
   const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
   const int64_t c0 = (int64_t)blockIdx.x * kCB;
-  const int a = blockIdx.z, split = blockIdx.y;
-  const int32_t lo = pl.off[a], hi = pl.off[a + 1];
-  int32_t per = (hi - lo + (int)gridDim.y - 1) / (int)gridDim.y;
-  per = (per + kRB - 1) / kRB * kRB;
-  const int32_t mb = lo + split * per, me = mb + per < hi ? mb + per : hi;
+  __shared__ int32_t srow[kSumRows];
+  const int32_t *first = pl.table[which];
+  if ((int)blockIdx.y >= first[L]) return;   // the grid is an upper bound; rows without an adapter add to no sum
+  const int a = group_of_block(first, L - 1, blockIdx.y);
+  const int nb = first[a + 1] - first[a], size = pl.rows[which];
+  const int32_t lo = pl.table[kPlanRow][a] + ((int)blockIdx.y - first[a]) * size;
+  const int32_t hi = pl.table[kPlanRow][a + 1];
+  const int32_t me = lo + size < hi ? size : hi - lo;   // rows of this block
+  for (int i = tid; i < me; i += 256) srow[i] = pl.perm[lo + i];
+  __syncthreads();
   f32x4 acc[TJ][2];
 #pragma unroll
   for (int t = 0; t < TJ; ++t)
@@ -363,14 +395,14 @@ __global__ __launch_bounds__(256) void multi_sum_kernel(const uint16_t *__restri
       const int q = tid + 256 * i;
       const int32_t m = ms + (q >> 4);
       const int64_t c = c0 + (q & 15) * 8;
-      st.q[i] = (m < me && c < C) ? *reinterpret_cast<const uint4 *>(Q + (int64_t)pl.perm[m] * ldq + c)
+      st.q[i] = (m < me && c < C) ? *reinterpret_cast<const uint4 *>(Q + (int64_t)srow[m] * ldq + c)
                                   : make_uint4(0, 0, 0, 0);
     }
 #pragma unroll
     for (int i = 0; i < (TJ + 1) / 2; ++i) {
       const int q = tid + 256 * i, row = q / (2 * TJ), j = q % (2 * TJ) * 8;
       const int32_t m = ms + row;
-      st.p[i] = (row < kRB && m < me && j < r) ? *reinterpret_cast<const uint4 *>(P + (int64_t)pl.perm[m] * ldp + j)
+      st.p[i] = (row < kRB && m < me && j < r) ? *reinterpret_cast<const uint4 *>(P + (int64_t)srow[m] * ldp + j)
                                                : make_uint4(0, 0, 0, 0);
     }
   };
@@ -407,20 +439,20 @@ __global__ __launch_bounds__(256) void multi_sum_kernel(const uint16_t *__restri
       }
     }
   };
-  const int nst = me > mb ? (me - mb + kRB - 1) / kRB : 0;
+  const int nst = (me + kRB - 1) / kRB;
   Stage s0, s1;
-  if (nst > 0) load(mb, s0);
-  if (nst > 1) load(mb + kRB, s1);
+  if (nst > 0) load(0, s0);
+  if (nst > 1) load(kRB, s1);
   if (nst > 0) store(s0, 0);
   __syncthreads();
 #pragma unroll 1
   for (int i = 0; i < nst; i += 2) {
-    if (i + 2 < nst) load(mb + (i + 2) * kRB, s0);
+    if (i + 2 < nst) load((i + 2) * kRB, s0);
     mma(0);
     if (i + 1 < nst) store(s1, 1);
     __syncthreads();
     if (i + 1 >= nst) break;
-    if (i + 3 < nst) load(mb + (i + 3) * kRB, s1);
+    if (i + 3 < nst) load((i + 3) * kRB, s1);
     mma(1);
     if (i + 2 < nst) store(s0, 0);
     __syncthreads();
@@ -434,57 +466,76 @@ __global__ __launch_bounds__(256) void multi_sum_kernel(const uint16_t *__restri
         const int j = t * 16 + 4 * g16 + v;
         const int64_t c = c0 + wave * 32 + u * 16 + l16;
         if (j >= r || c >= C) continue;
-        if (gridDim.y > 1) {
-          part[(((int64_t)a * gridDim.y + split) * r + j) * C + c] = acc[t][u][v];
-        } else {
-          const uint16_t y = (uint16_t)(pack_bf16x2(s[a] * acc[t][u][v], 0.f) & 0xFFFFu);
-          out[(int64_t)a * r * C + (transposed ? c * r + j : j * C + c)] = y;
-        }
+        const int64_t at = transposed ? c * r + j : j * C + c;   // as in out
+        if (nb > 1)
+          part[(int64_t)blockIdx.y * r * C + at] = acc[t][u][v];
+        else
+          out[(int64_t)a * r * C + at] = (uint16_t)(pack_bf16x2(s[a] * acc[t][u][v], 0.f) & 0xFFFFu);
       }
 }
 
-// out[a] = bf16(s[a] * (sum over the splits of part[a])): [r][C], or [C][r] when transposed.
-__global__ void multi_sum_final_kernel(const float *__restrict__ part, int64_t C, int r, int splits, int L,
-                                       const float *__restrict__ s, bool transposed, uint16_t *__restrict__ out) {
-  const int64_t n = (int64_t)r * C;
-  for (int64_t i = blockIdx.x * (int64_t)blockDim.x + threadIdx.x; i < n * L; i += (int64_t)gridDim.x * blockDim.x) {
-    const int64_t a = i / n, ia = i - a * n;
-    const float *pa = part + a * splits * n + ia;
-    float x = 0.f;
+// out[a] = bf16(s[a] * (sum over the adapter's blocks of part)) where the adapter (blockIdx.y) has more
+// than one block, zeros where it has none; n values an adapter, two a thread (n is even: r C with
+// C % 8 == 0).
+__global__ void multi_sum_final_kernel(const float *__restrict__ part, int64_t n, const int32_t *__restrict__ first,
+                                       const float *__restrict__ s, uint16_t *__restrict__ out) {
+  const int a = blockIdx.y, lo = first[a], nb = first[a + 1] - lo;
+  if (nb == 1) return;
+  const float sa = s[a];
+  for (int64_t i = (blockIdx.x * (int64_t)blockDim.x + threadIdx.x) * 2; i < n; i += (int64_t)gridDim.x * blockDim.x * 2) {
+    const float *pa = part + (int64_t)lo * n + i;
+    f32x2 x = {0.f, 0.f};
     int q = 0;
-    for (; q + 8 <= splits; q += 8) {
-      float v[8];
+    for (; q + 8 <= nb; q += 8) {
+      f32x2 v[8];
 #pragma unroll
-      for (int j = 0; j < 8; ++j) v[j] = pa[(int64_t)(q + j) * n];
+      for (int j = 0; j < 8; ++j) v[j] = *reinterpret_cast<const f32x2 *>(pa + (int64_t)(q + j) * n);
 #pragma unroll
       for (int j = 0; j < 8; ++j) x += v[j];
     }
-    for (; q < splits; ++q) x += pa[(int64_t)q * n];
-    const uint16_t y = (uint16_t)(pack_bf16x2(s[a] * x, 0.f) & 0xFFFFu);
-    const int64_t j = ia / C, c = ia % C;
-    if (transposed)
-      out[a * n + c * r + j] = y;
-    else
-      out[i] = y;
+    for (; q < nb; ++q) x += *reinterpret_cast<const f32x2 *>(pa + (int64_t)q * n);
+    *reinterpret_cast<uint32_t *>(out + a * n + i) = nb ? pack_bf16x2(sa * x[0], sa * x[1]) : 0u;
   }
 }
 
 // ------------------------------------------------------------------------------------ transposes
-// dst[b][c][j] = src[b][j][c] for `batch` bf16 matrices [R][C], through 64 x 64 LDS tiles; the rows of
-// dst have ldd elements, zeros from R on.
+// dst[b][c][j] = src[b][j][c] for the bf16 matrices [R][C] of the adapters b that have rows (the others
+// are not read by anyone), through 64 x 64 LDS tiles; the rows of dst have ldd elements (a multiple of
+// 8), zeros from R on. 16-byte loads where C % 8 == 0, 16-byte stores.
 __global__ __launch_bounds__(256) void multi_transpose_kernel(const uint16_t *__restrict__ src, int64_t R,
-                                                              int64_t C, int64_t ldd, uint16_t *__restrict__ dst) {
-  __shared__ uint16_t t[64][66];
+                                                              int64_t C, int64_t ldd, const int32_t *__restrict__ row,
+                                                              uint16_t *__restrict__ dst) {
+  __shared__ uint16_t t[64][66];   // [c][r]
+  if (row[blockIdx.y] == row[blockIdx.y + 1]) return;
   const int64_t tiles_c = (C + 63) / 64;
   const int64_t c0 = (int64_t)blockIdx.x % tiles_c * 64, r0 = (int64_t)blockIdx.x / tiles_c * 64;
   src += (int64_t)blockIdx.y * R * C;
   dst += (int64_t)blockIdx.y * ldd * C;
-  const int x = threadIdx.x & 63, y = threadIdx.x >> 6;
-  for (int i = y; i < 64; i += 4)
-    t[i][x] = r0 + i < R && c0 + x < C ? src[(r0 + i) * C + c0 + x] : (uint16_t)0;
+  const int tid = threadIdx.x;
+  if ((C & 7) == 0) {
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      const int r = (tid >> 3) + 32 * h, c = (tid & 7) * 8;
+      u32x4 v = {0u, 0u, 0u, 0u};
+      if (r0 + r < R && c0 + c < C) v = *reinterpret_cast<const u32x4 *>(src + (r0 + r) * C + c0 + c);
+#pragma unroll
+      for (int e = 0; e < 8; ++e) t[c + e][r] = (uint16_t)(v[e >> 1] >> (16 * (e & 1)));
+    }
+  } else {
+    const int x = tid & 63;
+    for (int r = tid >> 6; r < 64; r += 4)
+      t[x][r] = r0 + r < R && c0 + x < C ? src[(r0 + r) * C + c0 + x] : (uint16_t)0;
+  }
   __syncthreads();
-  for (int i = y; i < 64; i += 4)
-    if (c0 + i < C && r0 + x < ldd) dst[(c0 + i) * ldd + r0 + x] = t[x][i];
+#pragma unroll
+  for (int h = 0; h < 2; ++h) {
+    const int c = (tid >> 3) + 32 * h, r = (tid & 7) * 8;
+    if (c0 + c >= C || r0 + r >= ldd) continue;
+    u32x4 v;
+#pragma unroll
+    for (int e = 0; e < 4; ++e) v[e] = t[c][r + 2 * e] | ((uint32_t)t[c][r + 2 * e + 1] << 16);
+    *reinterpret_cast<u32x4 *>(dst + (c0 + c) * ldd + r0 + r) = v;
+  }
 }
 
 // dst [rows][rp] = src [rows][r] and zeros.
@@ -560,39 +611,45 @@ hipError_t launch_multi_rows_part(const uint16_t *in, int64_t ldin, const uint16
   return hipGetLastError();
 }
 
-// Splits of the sums over rows: about 1024 workgroups over the column tiles and adapters.
-int multi_sum_splits(int64_t M, int64_t C, int L) {
-  const int64_t tiles = (C + kCB - 1) / kCB * L;
-  int64_t s = (1024 + tiles - 1) / tiles;
-  const int64_t most = (M + kRB - 1) / kRB;
-  s = s < most ? s : most;
-  return (int)(s > 1 ? s : 1);
+// Rows of a block of the sums over rows: about four workgroups for each of the 256 CUs over the column
+// tiles, 64 to 1024 rows.
+int multi_sum_rows(int64_t M, int64_t C) {
+  const int64_t rows = (M * ((C + kCB - 1) / kCB) / 1024 + kRB - 1) / kRB * kRB;
+  return (int)(rows < kRB ? kRB : rows < kSumRows ? rows : kSumRows);
+}
+int64_t multi_sum_blocks(int64_t M, int64_t C, int L) {
+  const int64_t rows = multi_sum_rows(M, C), b = (M + (rows - 1) * L) / rows;   // >= the sum of ceil(rows of a / rows)
+  return b < M ? b : M;
 }
 
-hipError_t launch_multi_sum(const uint16_t *P, int64_t ldp, const uint16_t *Q, int64_t ldq, int64_t C, int r, int L,
-                            const float *s, int splits, float *part, uint16_t *out, bool transposed,
+hipError_t launch_multi_sum(const uint16_t *P, int64_t ldp, const uint16_t *Q, int64_t ldq, int64_t M, int64_t C, int r,
+                            int L, const float *s, int which, float *part, uint16_t *out, bool transposed,
                             const MultiPlan &pl, hipStream_t st) {
-  if ((ldp & 7) != 0 || ldp < r) return hipErrorInvalidValue;
-  const dim3 grid((unsigned)((C + kCB - 1) / kCB), (unsigned)splits, (unsigned)L);
+  const int64_t blocks = multi_sum_blocks(M, C, L);
+  if ((ldp & 7) != 0 || ldp < r || (C & 7) != 0 || pl.rows[which] != multi_sum_rows(M, C)) return hipErrorInvalidValue;
+  const int64_t tiles = (C + kCB - 1) / kCB;
+  if (blocks > 65535) return hipErrorInvalidValue;
+  const dim3 grid((unsigned)tiles, (unsigned)blocks);
   switch ((r + 15) / 16) {
-#define MS_CASE(T) \
-  case T: multi_sum_kernel<T><<<grid, dim3(256), 0, st>>>(P, ldp, Q, ldq, C, r, part, s, transposed, out, pl); break;
+#define MS_CASE(T)                                                                                                  case T:                                                                                                             multi_sum_kernel<T><<<grid, dim3(256), 0, st>>>(P, ldp, Q, ldq, C, r, L, which, part, s, transposed, out, pl);     break;
     MS_CASE(1) MS_CASE(2) MS_CASE(3) MS_CASE(4) MS_CASE(5) MS_CASE(6) MS_CASE(7) MS_CASE(8)
 #undef MS_CASE
     default: return hipErrorInvalidValue;
   }
   hipError_t e = hipGetLastError();
-  if (e != hipSuccess || splits == 1) return e;
-  multi_sum_final_kernel<<<dim3((unsigned)blocks_for((int64_t)L * r * C)), dim3(256), 0, st>>>(part, C, r, splits, L, s,
-                                                                                             transposed, out);
+  if (e != hipSuccess) return e;
+  const int64_t n = (int64_t)r * C;
+  int64_t b = (n / 2 + 255) / 256;
+  b = b < 1024 ? b : 1024;
+  multi_sum_final_kernel<<<dim3((unsigned)b, (unsigned)L), dim3(256), 0, st>>>(part, n, pl.table[which], s, out);
   return hipGetLastError();
 }
 
-hipError_t launch_multi_transpose(const uint16_t *src, int64_t R, int64_t C, int64_t ldd, int batch, uint16_t *dst,
-                                  hipStream_t st) {
-  if (ldd < R) return hipErrorInvalidValue;
-  const dim3 grid((unsigned)((C + 63) / 64 * ((ldd + 63) / 64)), (unsigned)batch);
-  multi_transpose_kernel<<<grid, dim3(256), 0, st>>>(src, R, C, ldd, dst);
+hipError_t launch_multi_transpose(const uint16_t *src, int64_t R, int64_t C, int64_t ldd, int L, const MultiPlan &pl,
+                                  uint16_t *dst, hipStream_t st) {
+  if (ldd < R || (ldd & 7) != 0) return hipErrorInvalidValue;
+  const dim3 grid((unsigned)((C + 63) / 64 * ((ldd + 63) / 64)), (unsigned)L);
+  multi_transpose_kernel<<<grid, dim3(256), 0, st>>>(src, R, C, ldd, pl.table[kPlanRow], dst);
   return hipGetLastError();
 }
 

@@ -37,7 +37,8 @@ def test_mid_kernel_step_waits(tmp_path):
                 assert k == "mem" or vmcnt(t) >= seen, (name, t)
 
 
-@pytest.mark.parametrize("src,pattern", [("fwd.hip", "fwd_multi_kernel"), ("dx.hip", "dx_multi_kernel")])
+@pytest.mark.parametrize("src,pattern", [("fwd.hip", "fwd_multi_kernel"), ("dx.hip", "dx_multi_kernel"),
+                                         ("dx.hip", "dx_split_kernel")])
 def test_large_kernel_step_waits(tmp_path, src, pattern):
     ks = {k: b for k, b in kernels(device_asm(src, str(tmp_path))).items() if pattern in k}
     assert len(ks) == 3
