@@ -1064,14 +1064,14 @@ int stream_tsplits(int64_t k, int32_t r) {
   return (int)std::max<int64_t>(s, 1);
 }
 
-// Workspace of the layer with an adapter for every row. Forward: the rows' order, then B and T with the
-// ranks padded to a multiple of 8 (when they are not one), then float sums (of T, then of Y).
-// Backward: the rows' order, U [m, r] and its padded form, B transposed [L, r, n], A transposed [L, k,
-// r padded], T (recomputed when the caller passes none) and its padded form, then float sums of the
-// row projections, of dX or of the sums over rows (one at a time).
+// Workspace of the layer with an adapter for every row; tensors whose ranks are padded to a multiple of 8
+// only where r is not one. Forward: the rows' order, B padded, T padded, float sums of T, float sums of Y.
+// Backward: the rows' order, U (padded), B transposed [L, r, n], A transposed [L, k, r padded], T padded
+// (recomputed when the caller passes none), then float sums of the row projections, of dX or of the
+// sums over rows (one at a time).
 struct MultiWs {
   int sp_k = 1, sp_n = 1, pieces = 1;
-  size_t plan = 0, bp = 0, u = 0, up = 0, bt = 0, at = 0, t = 0, tp = 0, part = 0, total = 0;
+  size_t plan = 0, bp = 0, u = 0, bt = 0, at = 0, tp = 0, tpart = 0, part = 0, total = 0;
 };
 
 MultiWs multi_ws(int64_t m, int64_t n, int64_t k, int32_t r, int32_t L, bool bwd) {
@@ -1079,35 +1079,29 @@ MultiWs multi_ws(int64_t m, int64_t n, int64_t k, int32_t r, int32_t L, bool bwd
   const int rp = padded(r);
   w.sp_k = nf4q::multi_rows_splits(m, k);
   w.plan = align256(nf4q::multi_plan_bytes(m, L));
-  if (rp != r) w.tp = align256((size_t)m * rp * 2);
-  size_t p = w.sp_k > 1 ? (size_t)w.sp_k * m * r * 4 : 0;
   if (bwd) {
     w.sp_n = nf4q::multi_rows_splits(m, n);
-    w.u = w.t = align256((size_t)m * r * 2);
-    w.up = w.tp;
+    w.pieces = nf4q::dx_multi_pieces(m, k, n);
+    w.u = w.tp = align256((size_t)m * rp * 2);
     w.bt = align256((size_t)L * r * n * 2);
     w.at = align256((size_t)L * rp * k * 2);
-    w.pieces = nf4q::dx_multi_pieces(m, k, n);
-    if (w.sp_n > 1) p = std::max(p, (size_t)w.sp_n * m * r * 4);
+    size_t p = (size_t)std::max(w.sp_n, w.sp_k) * m * rp * 4;
     if (w.pieces > 1) p = std::max(p, (size_t)w.pieces * m * k * 4);
     p = std::max(p, (size_t)nf4q::multi_sum_blocks(m, k, L) * r * k * 4);
     p = std::max(p, (size_t)nf4q::multi_sum_blocks(m, n, L) * r * n * 4);
+    w.part = align256(p);
   } else {
-    if (rp != r) w.bp = align256((size_t)L * n * rp * 2);
-    p = std::max(p, nf4q::mid_fwd_bytes(m, n, k, rp));   // T is whole before the sums of Y start
-    if (m <= 16) p = std::max(p, (size_t)stream_tsplits(k, r) * m * r * 4);
+    if (rp != r) {
+      w.bp = align256((size_t)L * n * rp * 2);
+      w.tp = align256((size_t)m * rp * 2);
+    }
+    int ts = m <= nf4q::kMultiSmallM ? nf4q::mid_tsplits(m, k) : w.sp_k;
+    if (m <= 16) ts = std::max(ts, stream_tsplits(k, r));
+    w.tpart = align256((size_t)ts * m * rp * 4);
+    w.part = nf4q::mid_fwd_bytes(m, n, k);
   }
-  w.part = align256(p);
-  w.total = w.plan + w.bp + w.u + w.up + w.bt + w.at + w.t + w.tp + w.part;
+  w.total = w.plan + w.bp + w.u + w.bt + w.at + w.tp + w.tpart + w.part;
   return w;
-}
-
-// bf16 [rows, r] with the ranks padded to a multiple of 8: itself, or a copy in the workspace.
-hipError_t pad_ranks(const uint16_t **src, int64_t rows, int32_t r, char *to, hipStream_t sm) {
-  if (padded(r) == r) return hipSuccess;
-  const hipError_t e = nf4q::launch_multi_pad(*src, rows, r, padded(r), (uint16_t *)to, sm);
-  *src = (const uint16_t *)to;
-  return e;
 }
 
 int check_multi_rest(const float *s, const int32_t *ids, const MultiWs &lay, void *ws, size_t ws_bytes) {
@@ -1176,34 +1170,45 @@ int qlora_multi_fwd(const void *X, int64_t m, const nf4_tensor *W, const void *A
   if (st) return st;
   hipStream_t sm = (hipStream_t)stream;
   char *base = (char *)ws;
+  char *at = base + lay.plan;
+  auto take = [&](size_t bytes) {
+    char *q = at;
+    at += bytes;
+    return q;
+  };
+  uint16_t *Bp = (uint16_t *)take(lay.bp), *Tp = (uint16_t *)take(lay.tp);
+  float *tpart = (float *)take(lay.tpart), *part = (float *)take(lay.part);
   const uint16_t *x = (const uint16_t *)X, *a = (const uint16_t *)A, *b = (const uint16_t *)B;
-  const uint16_t *t = (const uint16_t *)T;
-  float *part = (float *)(base + lay.plan + lay.bp + lay.tp);
+  uint16_t *t = (uint16_t *)T;
   const int rp = padded(r);
-  hipError_t e = pad_ranks(&b, (int64_t)L * n, r, base + lay.plan, sm);
-  if (e != hipSuccess) return hip_status(e, "qlora_multi_fwd launch");
+  const int64_t pstride = (int64_t)r * k;
   const MultiKernel kernel = multi_kernel(m, W, r);
-  nf4q::MultiArgs mu{ids, s, nullptr, b, L, rp};
+  nf4q::MultiArgs mu{ids, s, nullptr, rp == r ? b : Bp, L, rp};
   const nf4q::GemmArgs g = multi_gemm(X, m, W, n, k, Y);
-  if (kernel == MultiKernel::kStream) {
+  hipError_t e = hipSuccess;
+  if (kernel == MultiKernel::kStream) {   // r % 8 == 0
     const int splits = stream_tsplits(k, r);
-    e = nf4q::launch_multi_rows_part(x, k, a, (int64_t)r * k, k, ids, m, k, r, L, splits, part, sm);
+    e = nf4q::launch_multi_rows_part(x, k, a, pstride, k, ids, m, k, r, L, splits, tpart, sm);
     if (e != hipSuccess) return hip_status(e, "qlora_multi_fwd T launch");
-    return hip_status(nf4q::launch_stream16_fwd_multi(g, mu, part, splits, (uint16_t *)T, sm), "qlora_multi_fwd launch");
+    return hip_status(nf4q::launch_stream16_fwd_multi(g, mu, tpart, splits, t, sm), "qlora_multi_fwd launch");
   }
-  if (m > nf4q::kMultiSmallM) {
-    const nf4q::MultiPlan pl = nf4q::multi_plan_at(base, m, L, nf4q::multi_sum_rows(m, k), nf4q::multi_sum_rows(m, n));
-    e = nf4q::launch_multi_plan(ids, m, L, pl, sm);
+  if (m <= nf4q::kMultiSmallM) {
+    if (rp != r) e = nf4q::launch_multi_pad(b, (int64_t)L * n, r, rp, Bp, sm);
     if (e == hipSuccess)
-      e = nf4q::launch_multi_rows(x, k, a, (int64_t)r * k, k, m, k, r, L, lay.sp_k, part, (uint16_t *)T, pl, sm);
-    if (e == hipSuccess) e = pad_ranks(&t, m, r, base + lay.plan + lay.bp, sm);
-    if (e != hipSuccess) return hip_status(e, "qlora_multi_fwd T launch");
-    mu.P = t;
-    mu.perm = pl.perm;
+      e = nf4q::launch_mid_fwd_multi(g, mu, a, r, tpart, nf4q::mid_tsplits(m, k), t, part, sm);
+    return hip_status(e, "qlora_multi_fwd launch");
   }
-  e = kernel == MultiKernel::kMid ? nf4q::launch_mid_fwd_multi(g, mu, a, r, (uint16_t *)T, part, sm)
-                                  : nf4q::launch_gemm_fwd_multi(g, mu, sm);
-  return hip_status(e, "qlora_multi_fwd launch");
+  const nf4q::MultiPlan pl = nf4q::multi_plan_at(base, m, L, nf4q::multi_sum_rows(m, k), nf4q::multi_sum_rows(m, n));
+  e = nf4q::launch_multi_plan(ids, m, L, pl, b, (int64_t)L * n, r, rp, Bp, sm);
+  if (e == hipSuccess) e = nf4q::launch_multi_rows(x, k, a, pstride, k, m, k, r, rp, L, lay.sp_k, tpart, pl, sm);
+  if (e != hipSuccess) return hip_status(e, "qlora_multi_fwd T launch");
+  if (kernel == MultiKernel::kMid)
+    return hip_status(nf4q::launch_mid_fwd_multi(g, mu, a, r, tpart, lay.sp_k, t, part, sm), "qlora_multi_fwd launch");
+  e = nf4q::launch_multi_rows_sum(tpart, m, r, rp, lay.sp_k, t, rp == r ? nullptr : Tp, sm);
+  if (e != hipSuccess) return hip_status(e, "qlora_multi_fwd T launch");
+  mu.P = rp == r ? t : Tp;
+  mu.perm = pl.perm;
+  return hip_status(nf4q::launch_gemm_fwd_multi(g, mu, sm), "qlora_multi_fwd launch");
 }
 
 int qlora_multi_bwd(const void *dY, const void *X, int64_t m, const nf4_tensor *W, const void *A,
@@ -1228,38 +1233,33 @@ int qlora_multi_bwd(const void *dY, const void *X, int64_t m, const nf4_tensor *
     at += bytes;
     return q;
   };
-  uint16_t *U = (uint16_t *)take(lay.u);
-  char *Up = take(lay.up);
-  uint16_t *Bt = (uint16_t *)take(lay.bt);
-  uint16_t *At = (uint16_t *)take(lay.at);
-  uint16_t *Tw = (uint16_t *)take(lay.t);
-  char *Tp = take(lay.tp);
-  float *part = (float *)at;
+  uint16_t *U = (uint16_t *)take(lay.u), *Bt = (uint16_t *)take(lay.bt), *At = (uint16_t *)take(lay.at);
+  uint16_t *Tp = (uint16_t *)take(lay.tp);
+  float *part = (float *)take(lay.part);
   const int rp = padded(r);
-  const uint16_t *dy = (const uint16_t *)dY, *x = (const uint16_t *)X, *t = (const uint16_t *)T, *u = U;
-  hipError_t e = nf4q::launch_multi_plan(ids, m, L, pl, sm);
+  const uint16_t *dy = (const uint16_t *)dY, *x = (const uint16_t *)X, *t = (const uint16_t *)T;
+  hipError_t e = nf4q::launch_multi_plan(ids, m, L, pl, t, t ? m : 0, r, rp, Tp, sm);
   if (e != hipSuccess) return hip_status(e, "qlora_multi_bwd plan launch");
   if (!t) {
-    e = nf4q::launch_multi_rows(x, k, (const uint16_t *)A, (int64_t)r * k, k, m, k, r, L, lay.sp_k, part, Tw, pl, sm);
+    e = nf4q::launch_multi_rows(x, k, (const uint16_t *)A, (int64_t)r * k, k, m, k, r, rp, L, lay.sp_k, part, pl, sm);
+    if (e == hipSuccess) e = nf4q::launch_multi_rows_sum(part, m, r, rp, lay.sp_k, nullptr, Tp, sm);
     if (e != hipSuccess) return hip_status(e, "qlora_multi_bwd T launch");
-    t = Tw;
   }
-  e = pad_ranks(&t, m, r, Tp, sm);
-  if (e == hipSuccess) e = nf4q::launch_multi_transpose((const uint16_t *)B, n, r, n, L, pl, Bt, sm);
+  if (!t || rp != r) t = Tp;
+  e = nf4q::launch_multi_transposes((const uint16_t *)B, n, (const uint16_t *)A, k, r, rp, L, pl, Bt,
+                                    dX ? At : nullptr, sm);
   if (e != hipSuccess) return hip_status(e, "qlora_multi_bwd transpose launch");
-  e = nf4q::launch_multi_rows(dy, n, Bt, (int64_t)r * n, n, m, n, r, L, lay.sp_n, part, U, pl, sm);
-  if (e == hipSuccess) e = pad_ranks(&u, m, r, Up, sm);
+  e = nf4q::launch_multi_rows(dy, n, Bt, (int64_t)r * n, n, m, n, r, rp, L, lay.sp_n, part, pl, sm);
+  if (e == hipSuccess) e = nf4q::launch_multi_rows_sum(part, m, r, rp, lay.sp_n, nullptr, U, sm);
   if (e != hipSuccess) return hip_status(e, "qlora_multi_bwd U launch");
   if (dX) {
-    e = nf4q::launch_multi_transpose((const uint16_t *)A, r, k, rp, L, pl, At, sm);
-    if (e != hipSuccess) return hip_status(e, "qlora_multi_bwd transpose launch");
-    const nf4q::MultiArgs mu{ids, s, u, At, L, rp, pl.perm, lay.pieces, part};
+    const nf4q::MultiArgs mu{ids, s, U, At, L, rp, pl.perm, lay.pieces, part};
     e = nf4q::launch_gemm_dx_multi(multi_gemm(dY, m, W, k, n, dX), mu, sm);
     if (e == hipSuccess && lay.pieces > 1)
       e = nf4q::launch_multi_final(part, lay.pieces, m, k, mu, (uint16_t *)dX, sm);
     if (e != hipSuccess) return hip_status(e, "qlora_multi_bwd dX launch");
   }
-  e = nf4q::launch_multi_sum(u, rp, x, k, m, k, r, L, s, nf4q::kPlanSumA, part, (uint16_t *)dA, false, pl, sm);
+  e = nf4q::launch_multi_sum(U, rp, x, k, m, k, r, L, s, nf4q::kPlanSumA, part, (uint16_t *)dA, false, pl, sm);
   if (e != hipSuccess) return hip_status(e, "qlora_multi_bwd dA launch");
   e = nf4q::launch_multi_sum(t, rp, dy, n, m, n, r, L, s, nf4q::kPlanSumB, part, (uint16_t *)dB, true, pl, sm);
   return hip_status(e, "qlora_multi_bwd dB launch");

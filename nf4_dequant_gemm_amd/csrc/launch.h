@@ -219,27 +219,32 @@ hipError_t launch_gemm_dx_multi(const GemmArgs &g, const MultiArgs &mu, hipStrea
 int dx_multi_pieces(int64_t M, int64_t K, int64_t N);
 hipError_t launch_multi_final(const float *part, int splits, int64_t M, int64_t C, const MultiArgs &mu, uint16_t *out,
                               hipStream_t st);
-// The rows' order, and the thin products over it (multi.hip): out[i] = in[i] p_a^T for the rows i of
-// adapter a (zero without one), p_a = p + a * pstride of r rows of leading dimension ldp, with
-// splits * M * r partial floats; and out[a] = s[a] * (sum over its rows of P_i^T Q_i), [r][C] or
-// transposed [C][r]; P has row stride ldp, a multiple of 8, zeros from r on.
-hipError_t launch_multi_plan(const int32_t *ids, int64_t M, int L, const MultiPlan &pl, hipStream_t st);
+// The rows' order, and the thin products over it (multi.hip). The plan's launch also pads the ranks of a
+// factor where rp != r: dst [rows][rp] = src [rows][r] and zeros. Row projection: part [splits][M][rp]
+// = in[i] p_a^T for the rows i of adapter a (zeros without one and past r), p_a = p + a * pstride of r
+// rows of leading dimension ldp, and its sum over the splits in bf16, to out [M][r] and outp [M][rp]
+// (either may be NULL). Sum: out[a] = s[a] * (sum over its rows of P_i^T Q_i), [r][C] or transposed
+// [C][r]; P has row stride ldp, a multiple of 8, zeros from r on.
+hipError_t launch_multi_plan(const int32_t *ids, int64_t M, int L, const MultiPlan &pl, const uint16_t *src, int64_t rows,
+                             int r, int rp, uint16_t *dst, hipStream_t st);
 int multi_rows_splits(int64_t M, int64_t Lr);
 hipError_t launch_multi_rows(const uint16_t *in, int64_t ldin, const uint16_t *p, int64_t pstride, int64_t ldp,
-                             int64_t M, int64_t Lr, int r, int L, int splits, float *part, uint16_t *out,
+                             int64_t M, int64_t Lr, int r, int rp, int L, int splits, float *part,
                              const MultiPlan &pl, hipStream_t st);
+hipError_t launch_multi_rows_sum(const float *part, int64_t M, int r, int rp, int splits, uint16_t *out, uint16_t *outp,
+                                 hipStream_t st);
 // The projection without the table, for at most kMultiSmallM rows (any order of ids), as partial sums
 // float [M][r][splits] of slices of the reduction.
 hipError_t launch_multi_rows_part(const uint16_t *in, int64_t ldin, const uint16_t *p, int64_t pstride, int64_t ldp,
                                   const int32_t *ids, int64_t M, int64_t Lr, int r, int L, int splits, float *part,
                                   hipStream_t st);
-// The forward's fused part for batches that do not fill the large kernel's grid (mid.hip), and the
-// float partials it needs.
-// With at most kMultiSmallM rows it forms T itself (A [L][ra][K], T [M][ra] written; mu.P unused),
-// with more T is given (mu.P; A and T unused).
-hipError_t launch_mid_fwd_multi(const GemmArgs &g, const MultiArgs &mu, const uint16_t *A, int ra, uint16_t *T,
-                                float *part, hipStream_t st);
-size_t mid_fwd_bytes(int64_t M, int64_t N, int64_t K, int rp);
+// The forward's fused part for batches that do not fill the large kernel's grid (mid.hip), Y's float sums
+// in part (mid_fwd_bytes) and T's in tpart [tsplits][M][mu.r]: with at most kMultiSmallM rows it forms
+// them itself, from A [L][ra][K] in mid_tsplits parts, with more they are given. Writes Y and T [M][ra].
+int mid_tsplits(int64_t M, int64_t K);
+size_t mid_fwd_bytes(int64_t M, int64_t N, int64_t K);
+hipError_t launch_mid_fwd_multi(const GemmArgs &g, const MultiArgs &mu, const uint16_t *A, int ra, float *tpart,
+                                int tsplits, uint16_t *T, float *part, hipStream_t st);
 // The same for at most 16 rows of a double-quantised or E2M1 weight, K % 256 == 0 (decode16.hip), with T as
 // split partials float [M][r][tsplits] (launch_multi_rows_part), added inside and written to tout.
 hipError_t launch_stream16_fwd_multi(const GemmArgs &g, const MultiArgs &mu, const float *tpart, int tsplits,
@@ -251,10 +256,10 @@ int64_t multi_sum_blocks(int64_t M, int64_t C, int L);
 hipError_t launch_multi_sum(const uint16_t *P, int64_t ldp, const uint16_t *Q, int64_t ldq, int64_t M, int64_t C, int r,
                             int L, const float *s, int which, float *part, uint16_t *out, bool transposed,
                             const MultiPlan &pl, hipStream_t st);
-// dst[a][c][j] = src[a][j][c] of the bf16 matrices [R][C] of the adapters that have rows, rows of dst
-// padded with zeros to ldd, a multiple of 8; and dst [rows][rp] = src [rows][r] padded with zeros.
-hipError_t launch_multi_transpose(const uint16_t *src, int64_t R, int64_t C, int64_t ldd, int L, const MultiPlan &pl,
-                                  uint16_t *dst, hipStream_t st);
+// Bt [L][r][n] and, unless At is NULL, At [L][k][rp] from B [L][n][r] and A [L][r][k], for the adapters that
+// have rows; and dst [rows][rp] = src [rows][r] padded with zeros.
+hipError_t launch_multi_transposes(const uint16_t *B, int64_t n, const uint16_t *A, int64_t k, int r, int rp, int L,
+                                   const MultiPlan &pl, uint16_t *Bt, uint16_t *At, hipStream_t st);
 hipError_t launch_multi_pad(const uint16_t *src, int64_t rows, int r, int rp, uint16_t *dst, hipStream_t st);
 
 // Norm and rotation of query and key heads (headnorm.hip). One side (q or k): element strides of a

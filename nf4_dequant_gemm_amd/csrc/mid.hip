@@ -20,14 +20,13 @@
 //     which gives the 16 rows of an operand read distinct slots of the 256-byte bank window.
 //   * Codes, constants and X of the next two steps are in flight during a step; one barrier per step.
 // The kKW sums of a tile meet in LDS, in wave order, which also turns them round for whole row pieces.
-// With few tiles the reduction is also split over workgroups, which write float32 sums that
-// mid_final_kernel adds in order.
+// With few tiles the reduction is also split over workgroups. All write float32 sums, which
+// mid_final_kernel adds in order; it then applies the low-rank term and writes Y and T.
 //
-// T of at most 256 rows is formed in the same launch, by workgroups of their own (the first ones) that
-// each take 1024 elements of the reduction for 16 rows of an adapter (multi_rows_of) and write float32
-// sums: a launch for T alone took 6 to 9 us, and nothing here needs T before the end. mid_final_kernel
-// then adds both kinds of sums, applies the low-rank term and writes Y and T. More rows bring T from
-// its own launch, and an unsplit reduction then finishes Y itself.
+// T of at most 256 rows is formed in the same launch, by workgroups of their own that each take 1024
+// elements of the reduction for 16 rows of an adapter (multi_rows_of) and write float32 sums too: a
+// launch for T alone took 6 to 9 us, and nothing needs T before the end. They come last in the grid, for
+// the CUs that the tiles leave idle. More rows bring T's sums from the row projection.
 #include "common.h"
 #include "launch.h"
 #include "multi.h"
@@ -42,16 +41,17 @@ struct MidArgs {
   WDesc w;
   int64_t M, N, K;
   uint16_t *Y;         // [M][N]
-  float *part;         // [splits][M][N] unless the launch finishes Y itself
+  float *part;         // [splits][M][N]
   int splits;
-  bool finish;         // Y is finished in the launch (one split, T in memory)
   Tables t;
-  // T formed in the launch (tsplits > 0): its first tblocks workgroups
-  const uint16_t *A;   // [L][ra][K]
-  int ra;              // rank (mu.r: padded to a multiple of 8)
-  int tblocks, tsplits;
-  float *tpart;        // [tsplits][M][mu.r]
-  uint16_t *T;         // [M][ra], written by mid_final_kernel
+  // T's sums, [tsplits][M][mu.r] (tsplits 0: T is whole, in mu.P), and T [M][ra], written by
+  // mid_final_kernel; mu.r is the rank ra padded to a multiple of 8
+  float *tpart;
+  int tsplits, ra;
+  uint16_t *T;
+  // T formed in the launch: the workgroups from tfirst on, from A [L][ra][K]
+  int tfirst;
+  const uint16_t *A;
 };
 constexpr int kTSlice = 1024;   // reduction elements of a workgroup that forms T
 
@@ -98,11 +98,12 @@ __global__ __launch_bounds__(kThreads) void mid_kernel(MidArgs g, MultiArgs mu) 
   constexpr int kPad = 36, kTiles = kKW == 1 ? 1 : kMT;   // row tiles in LDS at a time
   constexpr int kSums = 8 * kTiles * 16 * kPad, kTab = kFP4 ? 0 : 256 * 64;
   __shared__ __align__(16) uint32_t stab[kSums > kTab ? kSums : kTab];
-  int block = blockIdx.x;
-  if (block < g.tblocks) {
+  const int block = blockIdx.x;
+  if (block >= g.tfirst) {
     static_assert(kMultiSmallT<8, 2> <= sizeof(stab), "T's sums fit the table");
     const int nj = (mu.r + 31) / 32;
-    const int ts = block % g.tsplits, j = block / g.tsplits % nj, row = block / g.tsplits / nj;
+    const int tb = block - g.tfirst;
+    const int ts = tb % g.tsplits, j = tb / g.tsplits % nj, row = tb / g.tsplits / nj;
     const int64_t le = (int64_t)(ts + 1) * kTSlice;
     float *tp = g.tpart + (int64_t)ts * g.M * mu.r;
     multi_rows_of<8, 2, 4>(g.X, g.K, g.A, (int64_t)g.ra * g.K, g.K, mu.ids, (int)g.M, (int64_t)ts * kTSlice,
@@ -110,7 +111,6 @@ __global__ __launch_bounds__(kThreads) void mid_kernel(MidArgs g, MultiArgs mu) 
                            [&](int i, int jj, float s) { tp[(int64_t)i * mu.r + jj] = s; });
     return;
   }
-  block -= g.tblocks;
   const int cols = (int)((g.N + 32 * kNW - 1) / (32 * kNW)), rowb = (int)((g.M + 16 * kMT - 1) / (16 * kMT));
   const int bx = block % cols, by = block / cols % rowb, bz = block / cols / rowb;
   const int tid = threadIdx.x, lane = tid & 63;
@@ -352,39 +352,23 @@ __global__ __launch_bounds__(kThreads) void mid_kernel(MidArgs g, MultiArgs mu) 
   };
   const float tsc = kFP4 ? tensor_scale(g.w) : 1.f;
   auto finish = [&](int mt) {
-    f32x4 y[2][1];
+    f32x4 y[2];
 #pragma unroll
     for (int nt = 0; nt < 2; ++nt) {
       auto at = [&](int k) {
         return *reinterpret_cast<const f32x4 *>(
             sums + (((k * kNW + nw) * kTiles + mt % kTiles) * 16 + l16) * kPad + 16 * nt + 4 * g16);
       };
-      y[nt][0] = at(kKW == 1 ? kw : 0);
+      y[nt] = at(kKW == 1 ? kw : 0);
 #pragma unroll
-      for (int k = 1; k < kKW; ++k) y[nt][0] += at(k);
-      if (kFP4) y[nt][0] *= tsc;
+      for (int k = 1; k < kKW; ++k) y[nt] += at(k);
+      if (kFP4) y[nt] *= tsc;
     }
-    const int64_t mb = m0 + mt * 16, m = mb + l16;
-    if (g.finish) {
-      int id = m < g.M ? mu.ids[m] : -1;
-      id = id >= 0 && id < mu.L ? id : -1;
-      int64_t rows = g.M - mb;
-      rows = rows < 0 ? 0 : rows < 16 ? rows : 16;
-      const __amdgpu_buffer_rsrc_t rT = make_rsrc(mu.P + mb * mu.r, rows * mu.r * 2);
-      f32x4 z[2] = {y[0][0], y[1][0]};
-      multi_term_rows<4>(z, mu, id, n0, N, [&](int j) { return rank_frag(rT, l16, j, mu.r); });
-      y[0][0] = z[0];
-      y[1][0] = z[1];
-    }
+    const int64_t m = m0 + mt * 16 + l16;
 #pragma unroll
     for (int nt = 0; nt < 2; ++nt) {
       const int64_t n = n0 + nt * 16 + 4 * g16;
-      if (m < g.M && n < N) {
-        if (g.finish)
-          store4(g.Y, N, m, n, y[nt][0]);
-        else
-          *reinterpret_cast<f32x4 *>(g.part + ((int64_t)bz * g.M + m) * N + n) = y[nt][0];
-      }
+      if (m < g.M && n < N) *reinterpret_cast<f32x4 *>(g.part + ((int64_t)bz * g.M + m) * N + n) = y[nt];
     }
   };
   if constexpr (kKW == 1) {   // a wave's own tile: its LDS accesses are in order
@@ -506,14 +490,13 @@ MidShape mid_shape(int64_t M, int64_t N, int64_t K) {
 }
 
 size_t up256(size_t x) { return (x + 255) & ~size_t(255); }
-int mid_tsplits(int64_t M, int64_t K) { return M <= kMultiSmallM ? (int)((K + kTSlice - 1) / kTSlice) : 0; }
 
 }  // namespace
 
-size_t mid_fwd_bytes(int64_t M, int64_t N, int64_t K, int rp) {
-  const MidShape s = mid_shape(M, N, K);
-  const int ts = mid_tsplits(M, K);
-  return up256(s.splits > 1 || ts ? (size_t)s.splits * M * N * 4 : 0) + (size_t)ts * M * rp * 4;
+int mid_tsplits(int64_t M, int64_t K) { return M <= kMultiSmallM ? (int)((K + kTSlice - 1) / kTSlice) : 0; }
+
+size_t mid_fwd_bytes(int64_t M, int64_t N, int64_t K) {
+  return up256((size_t)mid_shape(M, N, K).splits * M * N * 4);
 }
 
 hipError_t launch_multi_final(const float *part, int splits, int64_t M, int64_t C, const MultiArgs &mu, uint16_t *out,
@@ -530,21 +513,18 @@ hipError_t launch_multi_final(const float *part, int splits, int64_t M, int64_t 
   return hipGetLastError();
 }
 
-hipError_t launch_mid_fwd_multi(const GemmArgs &ga, const MultiArgs &mu, const uint16_t *A, int ra, uint16_t *T,
-                                float *part, hipStream_t st) {
-  if ((ga.C & 7) != 0 || ga.ldo != ga.C || ga.M < 1 || ga.R % 64 != 0 || (mu.r & 7) != 0 || ra > mu.r)
+hipError_t launch_mid_fwd_multi(const GemmArgs &ga, const MultiArgs &mu, const uint16_t *A, int ra, float *tpart,
+                                int tsplits, uint16_t *T, float *part, hipStream_t st) {
+  if ((ga.C & 7) != 0 || ga.ldo != ga.C || ga.M < 1 || ga.R % 64 != 0 || (mu.r & 7) != 0 || ra > mu.r || tsplits < 1)
     return hipErrorInvalidValue;
   const MidShape s = mid_shape(ga.M, ga.C, ga.R);
-  MidArgs a{ga.a_side, ga.w, ga.M, ga.C, ga.R, ga.out, part, s.splits, false, ga.t, A, ra, 0, 0, nullptr, T};
-  a.tsplits = mid_tsplits(ga.M, ga.R);
-  a.finish = s.splits == 1 && a.tsplits == 0;
-  if (a.tsplits) {
-    a.tblocks = (int)ga.M * ((mu.r + 31) / 32) * a.tsplits;
-    a.tpart = reinterpret_cast<float *>(reinterpret_cast<char *>(part) + up256((size_t)s.splits * ga.M * ga.C * 4));
-  }
   const int64_t rows = (ga.M + 16 * s.mt - 1) / (16 * s.mt);
-  const int64_t wgs = a.tblocks + rows * ((ga.C + 32 * s.nw - 1) / (32 * s.nw)) * s.splits;
-  if (wgs >= (int64_t(1) << 31)) return hipErrorInvalidValue;
+  const int64_t tiles = rows * ((ga.C + 32 * s.nw - 1) / (32 * s.nw)) * s.splits;
+  const int64_t wgs = tiles + (ga.M <= kMultiSmallM ? ga.M * ((mu.r + 31) / 32) * tsplits : 0);
+  const int64_t frows = (ga.M + 15) / 16;
+  if (wgs >= (int64_t(1) << 31) || frows > 65535 || (ga.M <= kMultiSmallM && tsplits != mid_tsplits(ga.M, ga.R)))
+    return hipErrorInvalidValue;
+  const MidArgs a{ga.a_side, ga.w, ga.M, ga.C, ga.R, ga.out, part, s.splits, ga.t, tpart, tsplits, ra, T, (int)tiles, A};
   const unsigned grid = (unsigned)wgs;
 #define MID_AL(MT, NW, BLK) launch_fmt<MT, NW, BLK, true>(a, mu, grid, st)
 #define MID_ANY(MT, NW, BLK) s.al ? MID_AL(MT, NW, BLK) : launch_fmt<MT, NW, BLK, false>(a, mu, grid, st)
@@ -561,10 +541,8 @@ hipError_t launch_mid_fwd_multi(const GemmArgs &ga, const MultiArgs &mu, const u
 #undef MID_ANY
 #undef MID_AL
   hipError_t e = hipGetLastError();
-  if (e != hipSuccess || a.finish) return e;
-  const int64_t tiles = (ga.M + 15) / 16;
-  if (tiles > 65535) return hipErrorInvalidValue;
-  mid_final_kernel<<<dim3((unsigned)((ga.C + 63) / 64), (unsigned)tiles), dim3(64), 0, st>>>(a, mu);
+  if (e != hipSuccess) return e;
+  mid_final_kernel<<<dim3((unsigned)((ga.C + 63) / 64), (unsigned)frows), dim3(64), 0, st>>>(a, mu);
   return hipGetLastError();
 }
 

@@ -18,11 +18,31 @@ namespace {
 // ranking the lanes of equal adapter by a ballot. A wave's ids are loaded eight 64-row pieces at a time.
 constexpr int kPlanThreads = 1024, kPlanWaves = kPlanThreads / 64, kPlanAhead = 8;
 
+// Padding of ranks: dst [rows][rp] = src [rows][r] and zeros.
+struct PadArgs {
+  const uint16_t *src;
+  uint16_t *dst;
+  int64_t rows;
+  int r, rp;
+};
+__device__ __forceinline__ void pad_rows(const PadArgs &p, int64_t i0, int64_t step) {
+  for (int64_t i = i0; i < p.rows * p.rp; i += step) {
+    const int64_t row = i / p.rp;
+    const int j = (int)(i - row * p.rp);
+    p.dst[i] = j < p.r ? p.src[row * p.r + j] : (uint16_t)0;
+  }
+}
+
+// Workgroups past the first pad the ranks of a factor meanwhile (pad.rows 0: there is none to pad).
 __global__ __launch_bounds__(kPlanThreads) void multi_plan_kernel(const int32_t *__restrict__ ids, int64_t M,
-                                                                  int L, MultiPlan pl) {
+                                                                  int L, MultiPlan pl, PadArgs pad) {
   extern __shared__ int32_t cnt[];   // [kPlanWaves][L + 1]
   __shared__ int32_t scan[kMultiTables][kPlanThreads];
   const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+  if (blockIdx.x > 0) {
+    pad_rows(pad, (int64_t)(blockIdx.x - 1) * kPlanThreads + tid, (int64_t)(gridDim.x - 1) * kPlanThreads);
+    return;
+  }
   const int G = L + 1;
   for (int i = tid; i < kPlanWaves * G; i += kPlanThreads) cnt[i] = 0;
   __syncthreads();
@@ -131,8 +151,9 @@ __device__ __forceinline__ int group_of_block(const int32_t *first, int L, int b
 }
 
 // ------------------------------------------------------------------------------------ row projection
-// out[i][j] = sum over l of in[i][l] * p_a[j][l] for the rows i of adapter a; zero for rows without
-// one. p_a = p + a * pstride, rows of leading dimension ldp.
+// part[split][i][j] = sum over the split's l of in[i][l] * p_a[j][l] for the rows i of adapter a and j < r;
+// zero for rows without an adapter and for the padding, j < rp. p_a = p + a * pstride, rows of leading
+// dimension ldp.
 
 // Blocks of at most 16 rows: latency sets the time, so each wave issues all the loads of a pass
 // straight into operand registers. Wave w takes 32-column slices 4 u + w of the workgroup's split
@@ -140,9 +161,9 @@ __device__ __forceinline__ int group_of_block(const int32_t *first, int L, int b
 template <int TN>
 __global__ __launch_bounds__(256) void multi_rows16_kernel(const uint16_t *__restrict__ in, int64_t ldin,
                                                            const uint16_t *__restrict__ p, int64_t pstride,
-                                                           int64_t ldp, int64_t M, int64_t Lr, int r, int L,
-                                                           int64_t lsplit, float *__restrict__ part,
-                                                           uint16_t *__restrict__ out, MultiPlan pl) {
+                                                           int64_t ldp, int64_t M, int64_t Lr, int r, int rp,
+                                                           int L, int64_t lsplit, float *__restrict__ part,
+                                                           MultiPlan pl) {
   __shared__ f32x4 red[4][TN][64];
   const int b = blockIdx.x;
   if (b >= pl.table[kPlan16][L + 1]) return;
@@ -191,13 +212,7 @@ __global__ __launch_bounds__(256) void multi_rows16_kernel(const uint16_t *__res
     for (int v = 0; v < 4; ++v) {
       const int32_t row = row0 + 4 * kg + v;
       const int j = 16 * t + nl;
-      if (row < rowe && j < r) {
-        const int64_t i = pl.perm[row];
-        if (part)
-          part[((int64_t)split * M + i) * r + j] = s[v];
-        else
-          out[i * r + j] = (uint16_t)(pack_bf16x2(s[v], 0.f) & 0xFFFFu);
-      }
+      if (row < rowe && j < rp) part[((int64_t)split * M + pl.perm[row]) * rp + j] = s[v];
     }
   }
 }
@@ -209,9 +224,9 @@ __device__ __forceinline__ int swzm(int row, int c) { return row * 8 + (c ^ ((ro
 template <int TN>
 __global__ __launch_bounds__(256) void multi_rows64_kernel(const uint16_t *__restrict__ in, int64_t ldin,
                                                            const uint16_t *__restrict__ p, int64_t pstride,
-                                                           int64_t ldp, int64_t M, int64_t Lr, int r, int L,
-                                                           int64_t lsplit, float *__restrict__ part,
-                                                           uint16_t *__restrict__ out, MultiPlan pl) {
+                                                           int64_t ldp, int64_t M, int64_t Lr, int r, int rp,
+                                                           int L, int64_t lsplit, float *__restrict__ part,
+                                                           MultiPlan pl) {
   constexpr int PCH = TN * 16 * 8;                 // p-tile chunks per step
   constexpr int PPT = (PCH + 255) / 256;           // p-tile chunks per thread
   __shared__ uint4 sI[2][64 * 8];
@@ -299,12 +314,7 @@ __global__ __launch_bounds__(256) void multi_rows64_kernel(const uint16_t *__res
 #pragma unroll
     for (int t = 0; t < TN; ++t) {
       const int j = t * 16 + (lane & 15);
-      if (j < r) {
-        if (part)
-          part[((int64_t)split * M + i) * r + j] = acc[t][v];
-        else
-          out[i * r + j] = (uint16_t)(pack_bf16x2(acc[t][v], 0.f) & 0xFFFFu);
-      }
+      if (j < rp) part[((int64_t)split * M + i) * rp + j] = acc[t][v];
     }
   }
 }
@@ -323,9 +333,11 @@ __global__ __launch_bounds__(512) void multi_rows_part_kernel(const uint16_t *__
                          [&](int row, int j, float v) { part[((int64_t)row * r + j) * splits + s] = v; });
 }
 
-// out = bf16(sum over the splits of part [splits][n]), in split order.
-__global__ void multi_rows_sum_kernel(const float *__restrict__ part, int64_t n, int splits,
-                                      uint16_t *__restrict__ out) {
+// bf16(sum over the splits of part [splits][M][rp]), in split order, to out [M][r] and, where the ranks are
+// padded, to outp [M][rp].
+__global__ void multi_rows_sum_kernel(const float *__restrict__ part, int64_t M, int r, int rp, int splits,
+                                      uint16_t *__restrict__ out, uint16_t *__restrict__ outp) {
+  const int64_t n = M * rp;
   for (int64_t i = blockIdx.x * (int64_t)blockDim.x + threadIdx.x; i < n; i += (int64_t)gridDim.x * blockDim.x) {
     float a = 0.f;
     int s = 0;
@@ -337,7 +349,13 @@ __global__ void multi_rows_sum_kernel(const float *__restrict__ part, int64_t n,
       for (int j = 0; j < 8; ++j) a += v[j];
     }
     for (; s < splits; ++s) a += part[(int64_t)s * n + i];
-    out[i] = (uint16_t)(pack_bf16x2(a, 0.f) & 0xFFFFu);
+    const uint16_t y = (uint16_t)(pack_bf16x2(a, 0.f) & 0xFFFFu);
+    if (outp) outp[i] = y;
+    if (out) {
+      const int64_t row = i / rp;
+      const int j = (int)(i - row * rp);
+      if (j < r) out[row * r + j] = y;
+    }
   }
 }
 
@@ -499,14 +517,22 @@ __global__ void multi_sum_final_kernel(const float *__restrict__ part, int64_t n
 }
 
 // ------------------------------------------------------------------------------------ transposes
-// dst[b][c][j] = src[b][j][c] for the bf16 matrices [R][C] of the adapters b that have rows (the others
-// are not read by anyone), through 64 x 64 LDS tiles; the rows of dst have ldd elements (a multiple of
+// dst[b][c][j] = src[b][j][c] for the bf16 matrices [R][C] of the adapters b that have rows (nobody reads
+// the others), of both factors in one launch (blockIdx.z), through 64 x 64 LDS tiles; the rows of dst have ldd elements (a multiple of
 // 8), zeros from R on. 16-byte loads where C % 8 == 0, 16-byte stores.
-__global__ __launch_bounds__(256) void multi_transpose_kernel(const uint16_t *__restrict__ src, int64_t R,
-                                                              int64_t C, int64_t ldd, const int32_t *__restrict__ row,
-                                                              uint16_t *__restrict__ dst) {
+struct TransposeArgs {
+  const uint16_t *src;
+  uint16_t *dst;
+  int64_t R, C, ldd;
+};
+__global__ __launch_bounds__(256) void multi_transpose_kernel(TransposeArgs b, TransposeArgs a, const int32_t *row) {
   __shared__ uint16_t t[64][66];   // [c][r]
   if (row[blockIdx.y] == row[blockIdx.y + 1]) return;
+  const TransposeArgs &g = blockIdx.z ? a : b;
+  const int64_t R = g.R, C = g.C, ldd = g.ldd;
+  const uint16_t *src = g.src;
+  uint16_t *dst = g.dst;
+  if ((int64_t)blockIdx.x >= (C + 63) / 64 * ((ldd + 63) / 64)) return;
   const int64_t tiles_c = (C + 63) / 64;
   const int64_t c0 = (int64_t)blockIdx.x % tiles_c * 64, r0 = (int64_t)blockIdx.x / tiles_c * 64;
   src += (int64_t)blockIdx.y * R * C;
@@ -538,14 +564,8 @@ __global__ __launch_bounds__(256) void multi_transpose_kernel(const uint16_t *__
   }
 }
 
-// dst [rows][rp] = src [rows][r] and zeros.
-__global__ void multi_pad_kernel(const uint16_t *__restrict__ src, int64_t rows, int r, int rp,
-                                 uint16_t *__restrict__ dst) {
-  for (int64_t i = blockIdx.x * (int64_t)blockDim.x + threadIdx.x; i < rows * rp; i += (int64_t)gridDim.x * blockDim.x) {
-    const int64_t row = i / rp;
-    const int j = (int)(i - row * rp);
-    dst[i] = j < r ? src[row * r + j] : (uint16_t)0;
-  }
+__global__ void multi_pad_kernel(PadArgs p) {
+  pad_rows(p, blockIdx.x * (int64_t)blockDim.x + threadIdx.x, (int64_t)gridDim.x * blockDim.x);
 }
 
 int64_t blocks_for(int64_t n) {
@@ -555,9 +575,13 @@ int64_t blocks_for(int64_t n) {
 
 }  // namespace
 
-hipError_t launch_multi_plan(const int32_t *ids, int64_t M, int L, const MultiPlan &pl, hipStream_t st) {
+hipError_t launch_multi_plan(const int32_t *ids, int64_t M, int L, const MultiPlan &pl, const uint16_t *src, int64_t rows,
+                             int r, int rp, uint16_t *dst, hipStream_t st) {
   if (L < 1 || L > kMultiMaxAdapters || M < 1 || M >= (int64_t(1) << 30)) return hipErrorInvalidValue;
-  multi_plan_kernel<<<dim3(1), dim3(kPlanThreads), sizeof(int32_t) * kPlanWaves * (L + 1), st>>>(ids, M, L, pl);
+  const PadArgs pad{src, dst, r == rp ? 0 : rows, r, rp};
+  int64_t blocks = (pad.rows * rp + 4 * kPlanThreads - 1) / (4 * kPlanThreads);
+  blocks = 1 + (blocks < 1024 ? blocks : 1024);
+  multi_plan_kernel<<<dim3((unsigned)blocks), dim3(kPlanThreads), sizeof(int32_t) * kPlanWaves * (L + 1), st>>>(ids, M, L, pl, pad);
   return hipGetLastError();
 }
 
@@ -575,7 +599,7 @@ int multi_rows_splits(int64_t M, int64_t Lr) {
 }
 
 hipError_t launch_multi_rows(const uint16_t *in, int64_t ldin, const uint16_t *p, int64_t pstride, int64_t ldp,
-                             int64_t M, int64_t Lr, int r, int L, int splits, float *part, uint16_t *out,
+                             int64_t M, int64_t Lr, int r, int rp, int L, int splits, float *part,
                              const MultiPlan &pl, hipStream_t st) {
   const int64_t rows = multi_rows_block(M);
   int64_t lsplit = (Lr + splits - 1) / splits;
@@ -583,22 +607,24 @@ hipError_t launch_multi_rows(const uint16_t *in, int64_t ldin, const uint16_t *p
   int64_t blocks = (M + (rows - 1) * (L + 1)) / rows;   // >= the sum of ceil(rows of a group / rows)
   blocks = blocks < M ? blocks : M;
   const dim3 grid((unsigned)blocks, (unsigned)splits);
-  float *pp = splits > 1 ? part : nullptr;
   switch ((r + 15) / 16) {
 #define MR_CASE(T)                                                                                                 \
   case T:                                                                                                          \
     if (rows == 16)                                                                                                \
-      multi_rows16_kernel<T><<<grid, dim3(256), 0, st>>>(in, ldin, p, pstride, ldp, M, Lr, r, L, lsplit, pp, out, pl); \
+      multi_rows16_kernel<T><<<grid, dim3(256), 0, st>>>(in, ldin, p, pstride, ldp, M, Lr, r, rp, L, lsplit, part, pl); \
     else                                                                                                           \
-      multi_rows64_kernel<T><<<grid, dim3(256), 0, st>>>(in, ldin, p, pstride, ldp, M, Lr, r, L, lsplit, pp, out, pl); \
+      multi_rows64_kernel<T><<<grid, dim3(256), 0, st>>>(in, ldin, p, pstride, ldp, M, Lr, r, rp, L, lsplit, part, pl); \
     break;
     MR_CASE(1) MR_CASE(2) MR_CASE(3) MR_CASE(4) MR_CASE(5) MR_CASE(6) MR_CASE(7) MR_CASE(8)
 #undef MR_CASE
     default: return hipErrorInvalidValue;
   }
-  hipError_t e = hipGetLastError();
-  if (e != hipSuccess || splits == 1) return e;
-  multi_rows_sum_kernel<<<dim3((unsigned)blocks_for(M * r)), dim3(256), 0, st>>>(part, M * r, splits, out);
+  return hipGetLastError();
+}
+
+hipError_t launch_multi_rows_sum(const float *part, int64_t M, int r, int rp, int splits, uint16_t *out, uint16_t *outp,
+                                 hipStream_t st) {
+  multi_rows_sum_kernel<<<dim3((unsigned)blocks_for(M * rp)), dim3(256), 0, st>>>(part, M, r, rp, splits, out, outp);
   return hipGetLastError();
 }
 
@@ -645,16 +671,19 @@ hipError_t launch_multi_sum(const uint16_t *P, int64_t ldp, const uint16_t *Q, i
   return hipGetLastError();
 }
 
-hipError_t launch_multi_transpose(const uint16_t *src, int64_t R, int64_t C, int64_t ldd, int L, const MultiPlan &pl,
-                                  uint16_t *dst, hipStream_t st) {
-  if (ldd < R || (ldd & 7) != 0) return hipErrorInvalidValue;
-  const dim3 grid((unsigned)((C + 63) / 64 * ((ldd + 63) / 64)), (unsigned)L);
-  multi_transpose_kernel<<<grid, dim3(256), 0, st>>>(src, R, C, ldd, pl.table[kPlanRow], dst);
+hipError_t launch_multi_transposes(const uint16_t *B, int64_t n, const uint16_t *A, int64_t k, int r, int rp, int L,
+                                   const MultiPlan &pl, uint16_t *Bt, uint16_t *At, hipStream_t st) {
+  if (rp < r || (rp & 7) != 0 || (n & 7) != 0) return hipErrorInvalidValue;
+  const TransposeArgs b{B, Bt, n, r, n}, a{A, At, r, k, rp};
+  auto tiles = [](const TransposeArgs &g) { return (g.C + 63) / 64 * ((g.ldd + 63) / 64); };
+  const int64_t x = At && tiles(a) > tiles(b) ? tiles(a) : tiles(b);
+  multi_transpose_kernel<<<dim3((unsigned)x, (unsigned)L, At ? 2 : 1), dim3(256), 0, st>>>(b, a, pl.table[kPlanRow]);
   return hipGetLastError();
 }
 
 hipError_t launch_multi_pad(const uint16_t *src, int64_t rows, int r, int rp, uint16_t *dst, hipStream_t st) {
-  multi_pad_kernel<<<dim3((unsigned)blocks_for(rows * rp)), dim3(256), 0, st>>>(src, rows, r, rp, dst);
+  const PadArgs p{src, dst, rows, r, rp};
+  multi_pad_kernel<<<dim3((unsigned)blocks_for(rows * rp)), dim3(256), 0, st>>>(p);
   return hipGetLastError();
 }
 
