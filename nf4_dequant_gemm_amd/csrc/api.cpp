@@ -1067,11 +1067,11 @@ int stream_tsplits(int64_t k, int32_t r) {
 // Workspace of the layer with an adapter for every row; tensors whose ranks are padded to a multiple of 8
 // only where r is not one. Forward: the rows' order, B padded, T padded, float sums of T, float sums of Y.
 // Backward: the rows' order, U (padded), B transposed [L, r, n], A transposed [L, k, r padded], T padded
-// (recomputed when the caller passes none), then float sums of the row projections, of dX or of the
-// sums over rows (one at a time).
+// (recomputed when the caller passes none), T and U in float32 for a small batch, then float sums of the
+// row projections, of dX or of the sums over rows (one at a time).
 struct MultiWs {
   int sp_k = 1, sp_n = 1, pieces = 1;
-  size_t plan = 0, bp = 0, u = 0, bt = 0, at = 0, tp = 0, tpart = 0, part = 0, total = 0;
+  size_t plan = 0, bp = 0, u = 0, bt = 0, at = 0, tp = 0, wide = 0, tpart = 0, part = 0, total = 0;
 };
 
 MultiWs multi_ws(int64_t m, int64_t n, int64_t k, int32_t r, int32_t L, bool bwd) {
@@ -1085,10 +1085,11 @@ MultiWs multi_ws(int64_t m, int64_t n, int64_t k, int32_t r, int32_t L, bool bwd
     w.u = w.tp = align256((size_t)m * rp * 2);
     w.bt = align256((size_t)L * r * n * 2);
     w.at = align256((size_t)L * rp * k * 2);
-    size_t p = (size_t)std::max(w.sp_n, w.sp_k) * m * rp * 4;
+    const bool small = m <= nf4q::kMultiSmallM;
+    w.wide = small ? align256((size_t)2 * m * rp * 4) : 0;
+    size_t p = (size_t)(small ? w.sp_n + w.sp_k : std::max(w.sp_n, w.sp_k)) * m * rp * 4;
     if (w.pieces > 1) p = std::max(p, (size_t)w.pieces * m * k * 4);
-    p = std::max(p, (size_t)nf4q::multi_sum_blocks(m, k, L) * r * k * 4);
-    p = std::max(p, (size_t)nf4q::multi_sum_blocks(m, n, L) * r * n * 4);
+    p = std::max(p, ((size_t)nf4q::multi_sum_blocks(m, k, L) * k + (size_t)nf4q::multi_sum_blocks(m, n, L) * n) * r * 4);
     w.part = align256(p);
   } else {
     if (rp != r) {
@@ -1100,7 +1101,7 @@ MultiWs multi_ws(int64_t m, int64_t n, int64_t k, int32_t r, int32_t L, bool bwd
     w.tpart = align256((size_t)ts * m * rp * 4);
     w.part = nf4q::mid_fwd_bytes(m, n, k);
   }
-  w.total = w.plan + w.bp + w.u + w.bt + w.at + w.tp + w.tpart + w.part;
+  w.total = w.plan + w.bp + w.u + w.bt + w.at + w.tp + w.wide + w.tpart + w.part;
   return w;
 }
 
@@ -1199,13 +1200,18 @@ int qlora_multi_fwd(const void *X, int64_t m, const nf4_tensor *W, const void *A
     return hip_status(e, "qlora_multi_fwd launch");
   }
   const nf4q::MultiPlan pl = nf4q::multi_plan_at(base, m, L, nf4q::multi_sum_rows(m, k), nf4q::multi_sum_rows(m, n));
-  e = nf4q::launch_multi_plan(ids, m, L, pl, b, (int64_t)L * n, r, rp, Bp, sm);
-  if (e == hipSuccess) e = nf4q::launch_multi_rows(x, k, a, pstride, k, m, k, r, rp, L, lay.sp_k, tpart, pl, sm);
+  const nf4q::MultiPad pad{rp == r ? nullptr : b, (int64_t)L * n, r, rp, Bp};
+  e = nf4q::launch_multi_plan(ids, m, L, pl, pad, nf4q::MultiFactors{}, sm);
+  if (e != hipSuccess) return hip_status(e, "qlora_multi_fwd plan launch");
+  nf4q::MultiRows rows{x, k, a, lay.sp_k, tpart, nullptr, nullptr, nullptr};
+  if (kernel == MultiKernel::kLarge) {   // the mid kernel adds the sums itself
+    rows.out = t;
+    rows.padded = rp == r ? nullptr : Tp;
+  }
+  e = nf4q::launch_multi_rows(&rows, 1, m, r, rp, L, pl, sm);
   if (e != hipSuccess) return hip_status(e, "qlora_multi_fwd T launch");
   if (kernel == MultiKernel::kMid)
     return hip_status(nf4q::launch_mid_fwd_multi(g, mu, a, r, tpart, lay.sp_k, t, part, sm), "qlora_multi_fwd launch");
-  e = nf4q::launch_multi_rows_sum(tpart, m, r, rp, lay.sp_k, t, rp == r ? nullptr : Tp, sm);
-  if (e != hipSuccess) return hip_status(e, "qlora_multi_fwd T launch");
   mu.P = rp == r ? t : Tp;
   mu.perm = pl.perm;
   return hip_status(nf4q::launch_gemm_fwd_multi(g, mu, sm), "qlora_multi_fwd launch");
@@ -1235,23 +1241,29 @@ int qlora_multi_bwd(const void *dY, const void *X, int64_t m, const nf4_tensor *
   };
   uint16_t *U = (uint16_t *)take(lay.u), *Bt = (uint16_t *)take(lay.bt), *At = (uint16_t *)take(lay.at);
   uint16_t *Tp = (uint16_t *)take(lay.tp);
-  float *part = (float *)take(lay.part);
+  float *wide = (float *)take(lay.wide), *part = (float *)take(lay.part);
   const int rp = padded(r);
   const uint16_t *dy = (const uint16_t *)dY, *x = (const uint16_t *)X, *t = (const uint16_t *)T;
-  hipError_t e = nf4q::launch_multi_plan(ids, m, L, pl, t, t ? m : 0, r, rp, Tp, sm);
+  const uint16_t *a = (const uint16_t *)A, *b = (const uint16_t *)B;
+  const bool small = m <= nf4q::kMultiSmallM;
+  // a small batch forms T again, beside U and in float32, whether it was passed or not
+  const nf4q::MultiPad pad{!small && rp != r ? t : nullptr, m, r, rp, Tp};
+  hipError_t e = nf4q::launch_multi_plan(ids, m, L, pl, pad, nf4q::MultiFactors{b, n, a, k, r, rp, Bt, dX ? At : nullptr}, sm);
   if (e != hipSuccess) return hip_status(e, "qlora_multi_bwd plan launch");
-  if (!t) {
-    e = nf4q::launch_multi_rows(x, k, (const uint16_t *)A, (int64_t)r * k, k, m, k, r, rp, L, lay.sp_k, part, pl, sm);
-    if (e == hipSuccess) e = nf4q::launch_multi_rows_sum(part, m, r, rp, lay.sp_k, nullptr, Tp, sm);
-    if (e != hipSuccess) return hip_status(e, "qlora_multi_bwd T launch");
+  nf4q::MultiRows u{dy, n, Bt, lay.sp_n, part, nullptr, U, nullptr}, tr{x, k, a, lay.sp_k, part, nullptr, Tp, nullptr};
+  if (small) {
+    u.wide = wide;
+    tr.wide = wide + m * rp;
+    tr.padded = nullptr;
+    tr.part = part + (int64_t)lay.sp_n * m * rp;
+    const nf4q::MultiRows both[2] = {u, tr};
+    e = nf4q::launch_multi_rows(both, 2, m, r, rp, L, pl, sm);
+  } else {
+    if (!t) e = nf4q::launch_multi_rows(&tr, 1, m, r, rp, L, pl, sm);
+    if (e == hipSuccess) e = nf4q::launch_multi_rows(&u, 1, m, r, rp, L, pl, sm);
+    if (!t || rp != r) t = Tp;
   }
-  if (!t || rp != r) t = Tp;
-  e = nf4q::launch_multi_transposes((const uint16_t *)B, n, (const uint16_t *)A, k, r, rp, L, pl, Bt,
-                                    dX ? At : nullptr, sm);
-  if (e != hipSuccess) return hip_status(e, "qlora_multi_bwd transpose launch");
-  e = nf4q::launch_multi_rows(dy, n, Bt, (int64_t)r * n, n, m, n, r, rp, L, lay.sp_n, part, pl, sm);
-  if (e == hipSuccess) e = nf4q::launch_multi_rows_sum(part, m, r, rp, lay.sp_n, nullptr, U, sm);
-  if (e != hipSuccess) return hip_status(e, "qlora_multi_bwd U launch");
+  if (e != hipSuccess) return hip_status(e, "qlora_multi_bwd projection launch");
   if (dX) {
     const nf4q::MultiArgs mu{ids, s, U, At, L, rp, pl.perm, lay.pieces, part};
     e = nf4q::launch_gemm_dx_multi(multi_gemm(dY, m, W, k, n, dX), mu, sm);
@@ -1259,10 +1271,10 @@ int qlora_multi_bwd(const void *dY, const void *X, int64_t m, const nf4_tensor *
       e = nf4q::launch_multi_final(part, lay.pieces, m, k, mu, (uint16_t *)dX, sm);
     if (e != hipSuccess) return hip_status(e, "qlora_multi_bwd dX launch");
   }
-  e = nf4q::launch_multi_sum(U, rp, x, k, m, k, r, L, s, nf4q::kPlanSumA, part, (uint16_t *)dA, false, pl, sm);
-  if (e != hipSuccess) return hip_status(e, "qlora_multi_bwd dA launch");
-  e = nf4q::launch_multi_sum(t, rp, dy, n, m, n, r, L, s, nf4q::kPlanSumB, part, (uint16_t *)dB, true, pl, sm);
-  return hip_status(e, "qlora_multi_bwd dB launch");
+  const nf4q::MultiSum da{small ? (const void *)u.wide : U, x, k, nf4q::kPlanSumA, false, part, (uint16_t *)dA};
+  const nf4q::MultiSum db{small ? (const void *)tr.wide : t, dy, n, nf4q::kPlanSumB, true,
+                          part + nf4q::multi_sum_blocks(m, k, L) * r * k, (uint16_t *)dB};
+  return hip_status(nf4q::launch_multi_sums(da, db, m, r, rp, L, s, pl, sm), "qlora_multi_bwd dA and dB launch");
 }
 
 }  // extern "C"

@@ -220,19 +220,39 @@ int dx_multi_pieces(int64_t M, int64_t K, int64_t N);
 hipError_t launch_multi_final(const float *part, int splits, int64_t M, int64_t C, const MultiArgs &mu, uint16_t *out,
                               hipStream_t st);
 // The rows' order, and the thin products over it (multi.hip). The plan's launch also pads the ranks of a
-// factor where rp != r: dst [rows][rp] = src [rows][r] and zeros. Row projection: part [splits][M][rp]
-// = in[i] p_a^T for the rows i of adapter a (zeros without one and past r), p_a = p + a * pstride of r
-// rows of leading dimension ldp, and its sum over the splits in bf16, to out [M][r] and outp [M][rp]
-// (either may be NULL). Sum: out[a] = s[a] * (sum over its rows of P_i^T Q_i), [r][C] or transposed
-// [C][r]; P has row stride ldp, a multiple of 8, zeros from r on.
-hipError_t launch_multi_plan(const int32_t *ids, int64_t M, int L, const MultiPlan &pl, const uint16_t *src, int64_t rows,
-                             int r, int rp, uint16_t *dst, hipStream_t st);
-int multi_rows_splits(int64_t M, int64_t Lr);
-hipError_t launch_multi_rows(const uint16_t *in, int64_t ldin, const uint16_t *p, int64_t pstride, int64_t ldp,
-                             int64_t M, int64_t Lr, int r, int rp, int L, int splits, float *part,
-                             const MultiPlan &pl, hipStream_t st);
-hipError_t launch_multi_rows_sum(const float *part, int64_t M, int r, int rp, int splits, uint16_t *out, uint16_t *outp,
-                                 hipStream_t st);
+// factor, dst [rows][rp] = src [rows][r] and zeros (src NULL: none), and transposes the adapters that
+// have rows: Bt [L][r][n] (NULL: none) and At [L][k][rp] (NULL: not that one) from B [L][n][r], A [L][r][k].
+struct MultiPad {
+  const uint16_t *src;
+  int64_t rows;
+  int r, rp;
+  uint16_t *dst;
+};
+struct MultiFactors {
+  const uint16_t *B;
+  int64_t n;
+  const uint16_t *A;
+  int64_t k;
+  int r, rp;
+  uint16_t *Bt, *At;
+};
+hipError_t launch_multi_plan(const int32_t *ids, int64_t M, int L, const MultiPlan &pl, const MultiPad &pd,
+                             const MultiFactors &f, hipStream_t st);
+// Row projections, up to two in a launch: part [splits][M][rp] = in[i] p_a^T for the rows i of adapter a (zeros
+// without one and past r), in [M][l], p [L][r][l], l % 8 == 0; then the sum over the splits to out (bf16
+// [M][r]), padded (bf16 [M][rp]) and wide (float32 [M][rp]), each where it is given (none: no sum).
+struct MultiRows {
+  const uint16_t *in;
+  int64_t l;
+  const uint16_t *p;
+  int splits;   // multi_rows_splits(M, l)
+  float *part;
+  uint16_t *out, *padded;
+  float *wide;
+};
+int multi_rows_splits(int64_t M, int64_t l);
+hipError_t launch_multi_rows(const MultiRows *g, int count, int64_t M, int r, int rp, int L, const MultiPlan &pl,
+                             hipStream_t st);
 // The projection without the table, for at most kMultiSmallM rows (any order of ids), as partial sums
 // float [M][r][splits] of slices of the reduction.
 hipError_t launch_multi_rows_part(const uint16_t *in, int64_t ldin, const uint16_t *p, int64_t pstride, int64_t ldp,
@@ -249,17 +269,24 @@ hipError_t launch_mid_fwd_multi(const GemmArgs &g, const MultiArgs &mu, const ui
 // split partials float [M][r][tsplits] (launch_multi_rows_part), added inside and written to tout.
 hipError_t launch_stream16_fwd_multi(const GemmArgs &g, const MultiArgs &mu, const float *tpart, int tsplits,
                                      uint16_t *tout, hipStream_t st);
-// The sums over rows: blocks of multi_sum_rows(M, C) rows, which is what pl.rows[which] has to be
-// (kPlanSumA or kPlanSumB); partial floats: multi_sum_blocks * r * C.
-int multi_sum_rows(int64_t M, int64_t C);
-int64_t multi_sum_blocks(int64_t M, int64_t C, int L);
-hipError_t launch_multi_sum(const uint16_t *P, int64_t ldp, const uint16_t *Q, int64_t ldq, int64_t M, int64_t C, int r,
-                            int L, const float *s, int which, float *part, uint16_t *out, bool transposed,
-                            const MultiPlan &pl, hipStream_t st);
-// Bt [L][r][n] and, unless At is NULL, At [L][k][rp] from B [L][n][r] and A [L][r][k], for the adapters that
-// have rows; and dst [rows][rp] = src [rows][r] padded with zeros.
-hipError_t launch_multi_transposes(const uint16_t *B, int64_t n, const uint16_t *A, int64_t k, int r, int rp, int L,
-                                   const MultiPlan &pl, uint16_t *Bt, uint16_t *At, hipStream_t st);
+// The sums over rows, two in a launch: out[a] = s[a] * (sum over its rows of p_i^T q_i), [r][c] or transposed
+// [c][r]; q [M][c]; p [M][rp] with zeros from r on, bf16, or float32 with at most kMultiSmallM rows. Blocks
+// of multi_sum_rows(M, c) rows, which is what pl.rows[which] has to be (kPlanSumA or kPlanSumB); part:
+// multi_sum_blocks * r * c floats.
+struct MultiSum {
+  const void *p;
+  const uint16_t *q;
+  int64_t c;
+  int which;
+  bool transposed;
+  float *part;
+  uint16_t *out;
+};
+int multi_sum_rows(int64_t M, int64_t c);
+int64_t multi_sum_blocks(int64_t M, int64_t c, int L);
+hipError_t launch_multi_sums(const MultiSum &a, const MultiSum &b, int64_t M, int r, int rp, int L, const float *s,
+                             const MultiPlan &pl, hipStream_t st);
+// dst [rows][rp] = src [rows][r] padded with zeros, by itself.
 hipError_t launch_multi_pad(const uint16_t *src, int64_t rows, int r, int rp, uint16_t *dst, hipStream_t st);
 
 // Norm and rotation of query and key heads (headnorm.hip). One side (q or k): element strides of a

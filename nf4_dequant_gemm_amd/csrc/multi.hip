@@ -6,6 +6,9 @@
 // Rows are not moved: a table holds them in the order of their adapters and the kernels gather
 // through it, so that every 16- or 64-row block has one adapter, whose factor is read once for the
 // block. Sums over rows are split into float32 parts that are added in a fixed order.
+#include <algorithm>
+#include <cmath>
+
 #include "launch.h"
 #include "multi.h"
 
@@ -14,8 +17,9 @@ namespace {
 
 // ------------------------------------------------------------------------------------ row order
 // One workgroup: a stable counting sort of the rows by adapter. Wave w counts its run of rows in LDS,
-// the counts are scanned over adapters and waves, and each wave then places its rows in order,
-// ranking the lanes of equal adapter by a ballot. A wave's ids are loaded eight 64-row pieces at a time.
+// the counts are scanned over adapters and waves, and each wave then places its rows in order. The
+// lanes of a 64-row piece are ranked within their adapter by ballots, one for each adapter in the
+// piece, so that LDS is read and written once a piece. A wave's ids are loaded eight pieces at a time.
 constexpr int kPlanThreads = 1024, kPlanWaves = kPlanThreads / 64, kPlanAhead = 8;
 
 // Padding of ranks: dst [rows][rp] = src [rows][r] and zeros.
@@ -33,14 +37,82 @@ __device__ __forceinline__ void pad_rows(const PadArgs &p, int64_t i0, int64_t s
   }
 }
 
-// Workgroups past the first pad the ranks of a factor meanwhile (pad.rows 0: there is none to pad).
+// dst[a][c][j] = src[a][j][c] of the bf16 matrices [R][C] of an adapter a that has rows (nobody reads the
+// others), through 64 x 64 LDS tiles, four to a workgroup; the rows of dst have ldd elements (a multiple
+// of 8), zeros from R on. 16-byte loads where C % 8 == 0, 16-byte stores.
+struct TransposeArgs {
+  const uint16_t *src;
+  uint16_t *dst;
+  int64_t R, C, ldd;
+  __host__ __device__ int64_t tiles() const { return (C + 63) / 64 * ((ldd + 63) / 64); }
+  __host__ __device__ int64_t blocks() const { return src ? (tiles() + 3) / 4 : 0; }
+};
+// Rows that are looked through for an adapter's use; one that they do not show in a longer batch is
+// transposed unused.
+constexpr int64_t kUseRows = 8192;
+__device__ __forceinline__ void transpose_tiles(const TransposeArgs &g, const int32_t *ids, int64_t M, int a,
+                                                int64_t block, uint16_t (&lds)[4][64][66]) {
+  bool used = M > kUseRows;
+  for (int64_t i0 = threadIdx.x; i0 < M && i0 < kUseRows; i0 += kPlanThreads) used |= ids[i0] == a;
+  if (!__syncthreads_or(used)) return;
+  const int tid = threadIdx.x & 255;
+  const int64_t tile = block * 4 + (threadIdx.x >> 8), tiles_c = (g.C + 63) / 64;
+  const int64_t c0 = tile % tiles_c * 64, r0 = tile / tiles_c * 64;
+  const bool mine = tile < g.tiles();
+  auto &t = lds[threadIdx.x >> 8];   // [c][r]
+  const uint16_t *src = g.src + (int64_t)a * g.R * g.C;
+  uint16_t *dst = g.dst + (int64_t)a * g.ldd * g.C;
+  if (!mine) {
+  } else if ((g.C & 7) == 0) {
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      const int r = (tid >> 3) + 32 * h, c = (tid & 7) * 8;
+      u32x4 v = {0u, 0u, 0u, 0u};
+      if (r0 + r < g.R && c0 + c < g.C) v = *reinterpret_cast<const u32x4 *>(src + (r0 + r) * g.C + c0 + c);
+#pragma unroll
+      for (int e = 0; e < 8; ++e) t[c + e][r] = (uint16_t)(v[e >> 1] >> (16 * (e & 1)));
+    }
+  } else {
+    const int x = tid & 63;
+    for (int r = tid >> 6; r < 64; r += 4)
+      t[x][r] = r0 + r < g.R && c0 + x < g.C ? src[(r0 + r) * g.C + c0 + x] : (uint16_t)0;
+  }
+  __syncthreads();
+#pragma unroll
+  for (int h = 0; h < 2; ++h) {
+    const int c = (tid >> 3) + 32 * h, r = (tid & 7) * 8;
+    if (!mine || c0 + c >= g.C || r0 + r >= g.ldd) continue;
+    u32x4 v;
+#pragma unroll
+    for (int e = 0; e < 4; ++e) v[e] = t[c][r + 2 * e] | ((uint32_t)t[c][r + 2 * e + 1] << 16);
+    *reinterpret_cast<u32x4 *>(dst + (c0 + c) * g.ldd + r0 + r) = v;
+  }
+}
+
+// The first workgroup orders the rows, which leaves the card idle for 7 to 12 us; the others meanwhile pad the
+// ranks of a factor (pad.rows 0: there is none to pad) and transpose the adapters for the backward.
+struct PlanWork {
+  PadArgs pad;
+  int pad_blocks;
+  TransposeArgs tr[2];
+};
 __global__ __launch_bounds__(kPlanThreads) void multi_plan_kernel(const int32_t *__restrict__ ids, int64_t M,
-                                                                  int L, MultiPlan pl, PadArgs pad) {
+                                                                  int L, MultiPlan pl, PlanWork work) {
   extern __shared__ int32_t cnt[];   // [kPlanWaves][L + 1]
   __shared__ int32_t scan[kMultiTables][kPlanThreads];
+  __shared__ __align__(16) uint16_t tile[4][64][66];
   const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
   if (blockIdx.x > 0) {
-    pad_rows(pad, (int64_t)(blockIdx.x - 1) * kPlanThreads + tid, (int64_t)(gridDim.x - 1) * kPlanThreads);
+    int64_t b = (int64_t)blockIdx.x - 1;
+    if (b < work.pad_blocks) {
+      pad_rows(work.pad, b * kPlanThreads + tid, (int64_t)work.pad_blocks * kPlanThreads);
+      return;
+    }
+    b -= work.pad_blocks;
+    const bool second = b >= work.tr[0].blocks() * L;
+    if (second) b -= work.tr[0].blocks() * L;
+    const TransposeArgs g = second ? work.tr[1] : work.tr[0];
+    transpose_tiles(g, ids, M, (int)(b / g.blocks()), b % g.blocks(), tile);
     return;
   }
   const int G = L + 1;
@@ -48,9 +120,10 @@ __global__ __launch_bounds__(kPlanThreads) void multi_plan_kernel(const int32_t 
   __syncthreads();
   const int64_t per = ((M + kPlanWaves - 1) / kPlanWaves + 63) / 64 * 64;
   const int64_t lo = wave * per, hi = lo + per < M ? lo + per : M;
-  volatile int32_t *mine = cnt + wave * G;   // written by one lane, read by the others of its wave
+  volatile int32_t *mine = cnt + wave * G;   // a wave's LDS accesses are in order
   // groups of the lane's rows i0 + lane, + 64, ... (-1: past the run)
-  auto load = [&](int64_t i0, int (&g)[kPlanAhead]) {
+  int g[kPlanAhead];
+  auto load = [&](int64_t i0) {
     int a[kPlanAhead];
 #pragma unroll
     for (int q = 0; q < kPlanAhead; ++q) {
@@ -60,18 +133,26 @@ __global__ __launch_bounds__(kPlanThreads) void multi_plan_kernel(const int32_t 
 #pragma unroll
     for (int q = 0; q < kPlanAhead; ++q) g[q] = i0 + 64 * q + lane >= hi ? -1 : a[q] >= 0 && a[q] < L ? a[q] : L;
   };
-  for (int64_t i0 = lo; i0 < hi; i0 += 64 * kPlanAhead) {
-    int g[kPlanAhead];
-    load(i0, g);
-#pragma unroll
-    for (int q = 0; q < kPlanAhead; ++q) {   // one addition for each distinct adapter of a piece
-      uint64_t left = __ballot(g[q] >= 0);
-      while (left) {
-        const int a = __builtin_amdgcn_readlane(g[q], __builtin_ctzll(left));
-        const uint64_t same = __ballot(g[q] == a);
-        if (lane == 0) mine[a] = mine[a] + __popcll(same);
-        left &= ~same;
+  // the lane's rank among the piece's rows of its group, and their number
+  auto rank_of = [&](int group, int &rank, int &rows) {
+    rank = rows = 0;
+    for (uint64_t left = __ballot(group >= 0); left;) {
+      const int a = __builtin_amdgcn_readlane(group, __builtin_ctzll(left));
+      const uint64_t same = __ballot(group == a);
+      if (group == a) {
+        rank = __popcll(same & ((uint64_t(1) << lane) - 1));
+        rows = __popcll(same);
       }
+      left &= ~same;
+    }
+  };
+  for (int64_t i0 = lo; i0 < hi; i0 += 64 * kPlanAhead) {
+    load(i0);
+#pragma unroll
+    for (int q = 0; q < kPlanAhead; ++q) {
+      int rank, rows;
+      rank_of(g[q], rank, rows);
+      if (g[q] >= 0 && rank == 0) mine[g[q]] = mine[g[q]] + rows;
     }
   }
   __syncthreads();
@@ -94,15 +175,21 @@ __global__ __launch_bounds__(kPlanThreads) void multi_plan_kernel(const int32_t 
     for (int q = 0; q < kMultiTables; ++q) scan[q][tid] += v[q];
     __syncthreads();
   }
+  // a group's first place in every wave's run, from its first place
+  auto place = [&](int group, int32_t at) {
+    int32_t c[kPlanWaves];
+#pragma unroll
+    for (int w = 0; w < kPlanWaves; ++w) c[w] = cnt[w * G + group];
+#pragma unroll
+    for (int w = 0; w < kPlanWaves; ++w) {
+      cnt[w * G + group] = at;
+      at += c[w];
+    }
+  };
   if (tid < L) {
 #pragma unroll
     for (int q = 0; q < kMultiTables; ++q) pl.table[q][tid] = scan[q][tid] - own[q];
-    int32_t at = scan[0][tid] - own[0];
-    for (int w = 0; w < kPlanWaves; ++w) {
-      const int32_t c = cnt[w * G + tid];
-      cnt[w * G + tid] = at;
-      at += c;
-    }
+    place(tid, scan[0][tid] - own[0]);
   }
   if (tid == 0) {
     int32_t at = scan[0][L - 1];
@@ -112,30 +199,19 @@ __global__ __launch_bounds__(kPlanThreads) void multi_plan_kernel(const int32_t 
       pl.table[q][L] = scan[q][L - 1];
       pl.table[q][L + 1] = scan[q][L - 1] + (none + pl.rows[q] - 1) / pl.rows[q];
     }
-    for (int w = 0; w < kPlanWaves; ++w) {
-      const int32_t c = cnt[w * G + L];
-      cnt[w * G + L] = at;
-      at += c;
-    }
+    place(L, at);
   }
   __syncthreads();
   for (int64_t i0 = lo; i0 < hi; i0 += 64 * kPlanAhead) {
-    int g[kPlanAhead];
-    load(i0, g);
+    if (per > 64 * kPlanAhead) load(i0);   // else they are still here
 #pragma unroll
     for (int q = 0; q < kPlanAhead; ++q) {
-      uint64_t left = __ballot(g[q] >= 0);
-      while (left) {
-        const int a = __builtin_amdgcn_readlane(g[q], __builtin_ctzll(left));
-        const uint64_t same = __ballot(g[q] == a);
-        const int32_t at = mine[a];   // a wave's LDS accesses are in order
-        if (g[q] == a) {
-          const int32_t rank = __popcll(same & ((uint64_t(1) << lane) - 1));
-          pl.perm[at + rank] = (int32_t)(i0 + 64 * q + lane);
-          if (rank == 0) mine[a] = at + __popcll(same);
-        }
-        left &= ~same;
-      }
+      int rank, rows;
+      rank_of(g[q], rank, rows);
+      if (g[q] < 0) continue;
+      const int32_t at = mine[g[q]];
+      pl.perm[at + rank] = (int32_t)(i0 + 64 * q + lane);
+      if (rank == 0) mine[g[q]] = at + rows;
     }
   }
 }
@@ -151,30 +227,33 @@ __device__ __forceinline__ int group_of_block(const int32_t *first, int L, int b
 }
 
 // ------------------------------------------------------------------------------------ row projection
-// part[split][i][j] = sum over the split's l of in[i][l] * p_a[j][l] for the rows i of adapter a and j < r;
-// zero for rows without an adapter and for the padding, j < rp. p_a = p + a * pstride, rows of leading
-// dimension ldp.
+// MultiRows (launch.h): part[split][i][j] = sum over the split's l of in[i][l] * p_a[j][l] for the rows i of
+// adapter a and j < r; zero for rows without an adapter and for the padding, j < rp. Up to two products
+// in a launch (blockIdx.z).
+struct RowsArgs {
+  MultiRows g[2];
+  int64_t lsplit[2], M;
+  int r, rp, L;
+};
 
 // Blocks of at most 16 rows: latency sets the time, so each wave issues all the loads of a pass
 // straight into operand registers. Wave w takes 32-column slices 4 u + w of the workgroup's split
 // of the reduction; the four waves' sums are added in wave order in LDS. L % 8 == 0.
 template <int TN>
-__global__ __launch_bounds__(256) void multi_rows16_kernel(const uint16_t *__restrict__ in, int64_t ldin,
-                                                           const uint16_t *__restrict__ p, int64_t pstride,
-                                                           int64_t ldp, int64_t M, int64_t Lr, int r, int rp,
-                                                           int L, int64_t lsplit, float *__restrict__ part,
-                                                           MultiPlan pl) {
+__global__ __launch_bounds__(256) void multi_rows16_kernel(RowsArgs w, MultiPlan pl) {
   __shared__ f32x4 red[4][TN][64];
-  const int b = blockIdx.x;
-  if (b >= pl.table[kPlan16][L + 1]) return;
+  const int b = blockIdx.x, split = blockIdx.y, L = w.L, r = w.r, rp = w.rp;
+  const MultiRows g = blockIdx.z ? w.g[1] : w.g[0];
+  if (split >= g.splits || b >= pl.table[kPlan16][L + 1]) return;
   const int a = group_of_block(pl.table[kPlan16], L, b);
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-  const int split = blockIdx.y, nl = lane & 15, kg = lane >> 4;
+  const int nl = lane & 15, kg = lane >> 4;
   const int32_t row0 = pl.table[kPlanRow][a] + (b - pl.table[kPlan16][a]) * 16, rowe = pl.table[kPlanRow][a + 1];
   const bool have = row0 + nl < rowe && a < L;
-  const uint16_t *x = in + (have ? (int64_t)pl.perm[row0 + nl] * ldin : 0);
-  const uint16_t *pa = p + (a < L ? a : 0) * pstride;
-  const int64_t lb = split * lsplit, le = lb + lsplit < Lr ? lb + lsplit : Lr;
+  const uint16_t *x = g.in + (have ? (int64_t)pl.perm[row0 + nl] * g.l : 0);
+  const uint16_t *pa = g.p + (int64_t)(a < L ? a : 0) * r * g.l;
+  const int64_t lsplit = blockIdx.z ? w.lsplit[1] : w.lsplit[0];
+  const int64_t lb = split * lsplit, le = lb + lsplit < g.l ? lb + lsplit : g.l;
   f32x4 acc[TN];
 #pragma unroll
   for (int t = 0; t < TN; ++t) acc[t] = f32x4{0.f, 0.f, 0.f, 0.f};
@@ -190,7 +269,7 @@ __global__ __launch_bounds__(256) void multi_rows16_kernel(const uint16_t *__res
 #pragma unroll
         for (int t = 0; t < TN; ++t) {
           const int j = 16 * t + nl;
-          pv[h][t] = j < r && c < le ? *reinterpret_cast<const u32x4 *>(pa + j * ldp + c) : zero;
+          pv[h][t] = j < r && c < le ? *reinterpret_cast<const u32x4 *>(pa + j * g.l + c) : zero;
         }
       }
 #pragma unroll
@@ -207,12 +286,12 @@ __global__ __launch_bounds__(256) void multi_rows16_kernel(const uint16_t *__res
   for (int t = wave; t < TN; t += 4) {
     f32x4 s = red[0][t][lane];
 #pragma unroll
-    for (int w = 1; w < 4; ++w) s += red[w][t][lane];
+    for (int q = 1; q < 4; ++q) s += red[q][t][lane];
 #pragma unroll
     for (int v = 0; v < 4; ++v) {
       const int32_t row = row0 + 4 * kg + v;
       const int j = 16 * t + nl;
-      if (row < rowe && j < rp) part[((int64_t)split * M + pl.perm[row]) * rp + j] = s[v];
+      if (row < rowe && j < rp) g.part[((int64_t)split * w.M + pl.perm[row]) * rp + j] = s[v];
     }
   }
 }
@@ -222,23 +301,20 @@ __global__ __launch_bounds__(256) void multi_rows16_kernel(const uint16_t *__res
 __device__ __forceinline__ int swzm(int row, int c) { return row * 8 + (c ^ ((row >> 1) & 7)); }
 
 template <int TN>
-__global__ __launch_bounds__(256) void multi_rows64_kernel(const uint16_t *__restrict__ in, int64_t ldin,
-                                                           const uint16_t *__restrict__ p, int64_t pstride,
-                                                           int64_t ldp, int64_t M, int64_t Lr, int r, int rp,
-                                                           int L, int64_t lsplit, float *__restrict__ part,
-                                                           MultiPlan pl) {
+__global__ __launch_bounds__(256) void multi_rows64_kernel(RowsArgs w, MultiPlan pl) {
   constexpr int PCH = TN * 16 * 8;                 // p-tile chunks per step
   constexpr int PPT = (PCH + 255) / 256;           // p-tile chunks per thread
   __shared__ uint4 sI[2][64 * 8];
   __shared__ uint4 sP[2][PCH];
-  const int b = blockIdx.x;
-  if (b >= pl.table[kPlan64][L + 1]) return;
+  const int b = blockIdx.x, split = blockIdx.y, L = w.L, r = w.r, rp = w.rp;
+  const MultiRows g = blockIdx.z ? w.g[1] : w.g[0];
+  if (split >= g.splits || b >= pl.table[kPlan64][L + 1]) return;
   const int a = group_of_block(pl.table[kPlan64], L, b);
   const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
-  const int split = blockIdx.y;
   const int32_t row0 = pl.table[kPlanRow][a] + (b - pl.table[kPlan64][a]) * 64, rowe = pl.table[kPlanRow][a + 1];
-  const uint16_t *pa = p + (a < L ? a : 0) * pstride;
-  const int64_t lb = split * lsplit, le = lb + lsplit < Lr ? lb + lsplit : Lr;
+  const uint16_t *pa = g.p + (int64_t)(a < L ? a : 0) * r * g.l;
+  const int64_t lsplit = blockIdx.z ? w.lsplit[1] : w.lsplit[0];
+  const int64_t lb = split * lsplit, le = lb + lsplit < g.l ? lb + lsplit : g.l;
   // this thread's rows of the in-tile (tid / 8 and 32 more), and chunk tid % 8 of each
   const uint16_t *x[2];
   bool have[2];
@@ -246,7 +322,7 @@ __global__ __launch_bounds__(256) void multi_rows64_kernel(const uint16_t *__res
   for (int i = 0; i < 2; ++i) {
     const int32_t row = row0 + (tid >> 3) + 32 * i;
     have[i] = row < rowe && a < L;
-    x[i] = in + (have[i] ? (int64_t)pl.perm[row] * ldin : 0) + (tid & 7) * 8;
+    x[i] = g.in + (have[i] ? (int64_t)pl.perm[row] * g.l : 0) + (tid & 7) * 8;
   }
   f32x4 acc[TN];
 #pragma unroll
@@ -264,7 +340,7 @@ __global__ __launch_bounds__(256) void multi_rows64_kernel(const uint16_t *__res
       const int qd = tid + 256 * i;
       const int j = qd >> 3;
       const int64_t l = l0 + (qd & 7) * 8;
-      st.q[i] = (qd < PCH && j < r && l < le) ? *reinterpret_cast<const uint4 *>(pa + (int64_t)j * ldp + l)
+      st.q[i] = (qd < PCH && j < r && l < le) ? *reinterpret_cast<const uint4 *>(pa + (int64_t)j * g.l + l)
                                               : make_uint4(0, 0, 0, 0);
     }
   };
@@ -314,7 +390,7 @@ __global__ __launch_bounds__(256) void multi_rows64_kernel(const uint16_t *__res
 #pragma unroll
     for (int t = 0; t < TN; ++t) {
       const int j = t * 16 + (lane & 15);
-      if (j < rp) part[((int64_t)split * M + i) * rp + j] = acc[t][v];
+      if (j < rp) g.part[((int64_t)split * w.M + i) * rp + j] = acc[t][v];
     }
   }
 }
@@ -333,38 +409,42 @@ __global__ __launch_bounds__(512) void multi_rows_part_kernel(const uint16_t *__
                          [&](int row, int j, float v) { part[((int64_t)row * r + j) * splits + s] = v; });
 }
 
-// bf16(sum over the splits of part [splits][M][rp]), in split order, to out [M][r] and, where the ranks are
-// padded, to outp [M][rp].
-__global__ void multi_rows_sum_kernel(const float *__restrict__ part, int64_t M, int r, int rp, int splits,
-                                      uint16_t *__restrict__ out, uint16_t *__restrict__ outp) {
-  const int64_t n = M * rp;
+// The sum over the splits of part [splits][M][rp], in split order, in bf16 to out [M][r] and padded [M][rp] and
+// in float32 to wide [M][rp], each where it is given.
+__global__ void multi_rows_sum_kernel(RowsArgs w) {
+  const MultiRows g = blockIdx.y ? w.g[1] : w.g[0];
+  const int64_t n = w.M * w.rp;
   for (int64_t i = blockIdx.x * (int64_t)blockDim.x + threadIdx.x; i < n; i += (int64_t)gridDim.x * blockDim.x) {
     float a = 0.f;
     int s = 0;
-    for (; s + 8 <= splits; s += 8) {
+    for (; s + 8 <= g.splits; s += 8) {
       float v[8];
 #pragma unroll
-      for (int j = 0; j < 8; ++j) v[j] = part[(int64_t)(s + j) * n + i];
+      for (int j = 0; j < 8; ++j) v[j] = g.part[(int64_t)(s + j) * n + i];
 #pragma unroll
       for (int j = 0; j < 8; ++j) a += v[j];
     }
-    for (; s < splits; ++s) a += part[(int64_t)s * n + i];
+    for (; s < g.splits; ++s) a += g.part[(int64_t)s * n + i];
     const uint16_t y = (uint16_t)(pack_bf16x2(a, 0.f) & 0xFFFFu);
-    if (outp) outp[i] = y;
-    if (out) {
-      const int64_t row = i / rp;
-      const int j = (int)(i - row * rp);
-      if (j < r) out[row * r + j] = y;
+    if (g.padded) g.padded[i] = y;
+    if (g.wide) g.wide[i] = a;
+    if (g.out) {
+      const int64_t row = i / w.rp;
+      const int j = (int)(i - row * w.rp);
+      if (j < w.r) g.out[row * w.r + j] = y;
     }
   }
 }
 
 // ------------------------------------------------------------------------------------ sums over rows
-// A block of rows (block blockIdx.y of the plan's table `which`, at most kSumRows rows, all of one adapter
-// a): the sum over them of P[i][j] * Q[i][c] (dA: P = U, Q = X; dB: P = T, Q = dY), as out holds it
-// ([r][C], transposed [C][r]). An adapter of one block writes s[a] times it to out; otherwise it goes to
-// part[block] and multi_sum_final_kernel adds the adapter's blocks in order. Blocks of equal size, not a
-// split count for every adapter, because one adapter may hold most of the rows.
+// dA and dB in one launch (blockIdx.z). A block of rows (block blockIdx.y of the plan's table `which`, at
+// most kSumRows rows, all of one adapter a): the sum over them of P[i][j] * Q[i][c] (dA: P = U, Q = X; dB:
+// P = T, Q = dY), as out holds it ([r][C], transposed [C][r]). An adapter of one block writes s[a] times
+// it to out; otherwise it goes to part[block] and multi_sum_final_kernel adds the adapter's blocks in
+// order. Blocks of equal size, not a split count for every adapter, because one adapter may hold most of
+// the rows. At most kMultiSmallM rows (kSmall): a block is an adapter, which writes its zeros too, and P
+// is float32, taken as the sum of two bf16 numbers (16 bits of mantissa): the products are few, and with
+// one row to an adapter P's rounding to bf16 would be half the error of dA and dB.
 // Workgroup: 128 columns x all r ranks, in stages of 64 rows loaded two stages ahead, staged row-major
 // in LDS (rows padded by 32 bytes) and read with the transposing LDS load, which gives a lane 4
 // consecutive rows of one column: the MFMA operand with the rows as its reduction index.
@@ -377,25 +457,37 @@ __device__ __forceinline__ s16x4 lds_tr(const uint16_t *p) {
   return __builtin_amdgcn_ds_read_tr16_b64_v4i16((__attribute__((address_space(3))) s16x4 *)(p));
 }
 
-template <int TJ>
-__global__ __launch_bounds__(256) void multi_sum_kernel(const uint16_t *__restrict__ P,
-                                                        int64_t ldp, const uint16_t *__restrict__ Q, int64_t ldq,
-                                                        int64_t C, int r, int L, int which,
-                                                        float *__restrict__ part, const float *__restrict__ s,
-                                                        bool transposed, uint16_t *__restrict__ out, MultiPlan pl) {
-  constexpr int PROW = TJ * 16 + 16;
-  __shared__ uint16_t sQ[2][kRB * kQRow];
-  __shared__ uint16_t sP[2][kRB * PROW];
-  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
-  const int64_t c0 = (int64_t)blockIdx.x * kCB;
+struct SumArgs {
+  MultiSum g[2];
+  const float *s;
+  int r, rp, L;
+};
+
+template <int TJ, bool kSmall>
+__global__ __launch_bounds__(256) void multi_sum_kernel(SumArgs w, MultiPlan pl) {
+  constexpr int PROW = TJ * 16 + 16, kParts = kSmall ? 2 : 1;
+  __shared__ __align__(16) uint16_t sQ[2][kRB * kQRow];
+  __shared__ __align__(16) uint16_t sP[2][kParts][kRB * PROW];
+  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6, r = w.r;
+  const MultiSum g = blockIdx.z ? w.g[1] : w.g[0];
+  const int64_t c0 = (int64_t)blockIdx.x * kCB, C = g.c;
+  if (c0 >= C) return;
   __shared__ int32_t srow[kSumRows];
-  const int32_t *first = pl.table[which];
-  if ((int)blockIdx.y >= first[L]) return;   // the grid is an upper bound; rows without an adapter add to no sum
-  const int a = group_of_block(first, L - 1, blockIdx.y);
-  const int nb = first[a + 1] - first[a], size = pl.rows[which];
-  const int32_t lo = pl.table[kPlanRow][a] + ((int)blockIdx.y - first[a]) * size;
-  const int32_t hi = pl.table[kPlanRow][a + 1];
-  const int32_t me = lo + size < hi ? size : hi - lo;   // rows of this block
+  int a = blockIdx.y, nb = 1;
+  int32_t lo, me;   // first row of this block, and its rows
+  if constexpr (kSmall) {
+    lo = pl.table[kPlanRow][a];
+    me = pl.table[kPlanRow][a + 1] - lo;
+  } else {
+    const int32_t *first = pl.table[g.which];
+    if ((int)blockIdx.y >= first[w.L]) return;   // the grid is an upper bound; rows without an adapter add to no sum
+    a = group_of_block(first, w.L - 1, blockIdx.y);
+    nb = first[a + 1] - first[a];
+    const int size = pl.rows[g.which];
+    lo = pl.table[kPlanRow][a] + ((int)blockIdx.y - first[a]) * size;
+    const int32_t hi = pl.table[kPlanRow][a + 1];
+    me = lo + size < hi ? size : hi - lo;
+  }
   for (int i = tid; i < me; i += 256) srow[i] = pl.perm[lo + i];
   __syncthreads();
   f32x4 acc[TJ][2];
@@ -405,7 +497,7 @@ __global__ __launch_bounds__(256) void multi_sum_kernel(const uint16_t *__restri
     for (int u = 0; u < 2; ++u) acc[t][u] = f32x4{0.f, 0.f, 0.f, 0.f};
   struct Stage {
     uint4 q[4];
-    uint4 p[(TJ + 1) / 2];
+    uint4 p[(TJ + 1) / 2][kParts];   // 8 ranks, in bf16 or float32
   };
   auto load = [&](int32_t ms, Stage &st) {
 #pragma unroll
@@ -413,15 +505,18 @@ __global__ __launch_bounds__(256) void multi_sum_kernel(const uint16_t *__restri
       const int q = tid + 256 * i;
       const int32_t m = ms + (q >> 4);
       const int64_t c = c0 + (q & 15) * 8;
-      st.q[i] = (m < me && c < C) ? *reinterpret_cast<const uint4 *>(Q + (int64_t)srow[m] * ldq + c)
+      st.q[i] = (m < me && c < C) ? *reinterpret_cast<const uint4 *>(g.q + (int64_t)srow[m] * C + c)
                                   : make_uint4(0, 0, 0, 0);
     }
 #pragma unroll
     for (int i = 0; i < (TJ + 1) / 2; ++i) {
       const int q = tid + 256 * i, row = q / (2 * TJ), j = q % (2 * TJ) * 8;
       const int32_t m = ms + row;
-      st.p[i] = (row < kRB && m < me && j < r) ? *reinterpret_cast<const uint4 *>(P + (int64_t)srow[m] * ldp + j)
-                                               : make_uint4(0, 0, 0, 0);
+      const bool have = row < kRB && m < me && j < r;
+#pragma unroll
+      for (int e = 0; e < kParts; ++e)
+        st.p[i][e] = have ? *(reinterpret_cast<const uint4 *>((const uint16_t *)g.p + ((int64_t)srow[m] * w.rp + j) * kParts) + e)
+                          : make_uint4(0, 0, 0, 0);
     }
   };
   auto store = [&](const Stage &st, int buf) {
@@ -433,7 +528,23 @@ __global__ __launch_bounds__(256) void multi_sum_kernel(const uint16_t *__restri
 #pragma unroll
     for (int i = 0; i < (TJ + 1) / 2; ++i) {
       const int q = tid + 256 * i, row = q / (2 * TJ);
-      if (row < kRB) *reinterpret_cast<uint4 *>(&sP[buf][row * PROW + q % (2 * TJ) * 8]) = st.p[i];
+      if (row >= kRB) continue;
+      uint16_t *at = &sP[buf][0][row * PROW + q % (2 * TJ) * 8];
+      if constexpr (kSmall) {
+        const float *v = reinterpret_cast<const float *>(&st.p[i][0]);
+        uint32_t hi[4], rest[4];
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          hi[e] = pack_bf16x2(v[2 * e], v[2 * e + 1]);
+          const float x = __builtin_bit_cast(float, hi[e] << 16), y = __builtin_bit_cast(float, hi[e] & 0xFFFF0000u);
+          // nothing is left of an infinity
+          rest[e] = pack_bf16x2(fabsf(x) < INFINITY ? v[2 * e] - x : 0.f, fabsf(y) < INFINITY ? v[2 * e + 1] - y : 0.f);
+        }
+        *reinterpret_cast<uint4 *>(at) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
+        *reinterpret_cast<uint4 *>(at + kRB * PROW) = make_uint4(rest[0], rest[1], rest[2], rest[3]);
+      } else {
+        *reinterpret_cast<uint4 *>(at) = st.p[i][0];
+      }
     }
   };
   const int g16 = lane >> 4, l16 = lane & 15;
@@ -451,9 +562,18 @@ __global__ __launch_bounds__(256) void multi_sum_kernel(const uint16_t *__restri
       for (int u = 0; u < 2; ++u) q[u] = frag(sQ[buf], kQRow, wave * 32 + u * 16, ks);
 #pragma unroll
       for (int t = 0; t < TJ; ++t) {
-        const bf16x8 p = frag(sP[buf], PROW, t * 16, ks);
 #pragma unroll
-        for (int u = 0; u < 2; ++u) acc[t][u] = mfma16x16x32(p, q[u], acc[t][u]);
+        for (int e = 0; e < kParts; ++e) {
+          const bf16x8 p = frag(sP[buf][e], PROW, t * 16, ks);
+          // the operand whose index runs along out's rows comes first: a lane then holds 4 of them
+          if (g.transposed) {
+#pragma unroll
+            for (int u = 0; u < 2; ++u) acc[t][u] = mfma16x16x32(p, q[u], acc[t][u]);
+          } else {
+#pragma unroll
+            for (int u = 0; u < 2; ++u) acc[t][u] = mfma16x16x32(q[u], p, acc[t][u]);
+          }
+        }
       }
     }
   };
@@ -475,33 +595,49 @@ __global__ __launch_bounds__(256) void multi_sum_kernel(const uint16_t *__restri
     if (i + 2 < nst) store(s0, 0);
     __syncthreads();
   }
+  const float sa = w.s[a];
+  uint16_t *out = g.out + (int64_t)a * r * C;
+  float *part = g.part + (int64_t)blockIdx.y * r * C;
 #pragma unroll
   for (int t = 0; t < TJ; ++t)
 #pragma unroll
-    for (int u = 0; u < 2; ++u)
+    for (int u = 0; u < 2; ++u) {
+      // 4 ranks from j of column c, or rank j of 4 columns from c
+      const int j = t * 16 + (g.transposed ? 4 * g16 : l16);
+      const int64_t c = c0 + wave * 32 + u * 16 + (g.transposed ? l16 : 4 * g16);
+      if (j >= r || c >= C) continue;
+      const int64_t at = g.transposed ? c * r + j : j * C + c;
+      const f32x4 y = acc[t][u];
+      const uint2 z = me ? make_uint2(pack_bf16x2(sa * y[0], sa * y[1]), pack_bf16x2(sa * y[2], sa * y[3])) : make_uint2(0, 0);
+      if (g.transposed && (r & 3) != 0) {   // rows of out that are not 8-byte aligned
 #pragma unroll
-      for (int v = 0; v < 4; ++v) {
-        const int j = t * 16 + 4 * g16 + v;
-        const int64_t c = c0 + wave * 32 + u * 16 + l16;
-        if (j >= r || c >= C) continue;
-        const int64_t at = transposed ? c * r + j : j * C + c;   // as in out
-        if (nb > 1)
-          part[(int64_t)blockIdx.y * r * C + at] = acc[t][u][v];
-        else
-          out[(int64_t)a * r * C + at] = (uint16_t)(pack_bf16x2(s[a] * acc[t][u][v], 0.f) & 0xFFFFu);
+        for (int v = 0; v < 4; ++v) {
+          if (j + v >= r) break;
+          if (nb > 1)
+            part[at + v] = y[v];
+          else
+            out[at + v] = (uint16_t)((v < 2 ? z.x : z.y) >> (16 * (v & 1)));
+        }
+      } else if (nb > 1) {
+        *reinterpret_cast<f32x4 *>(part + at) = y;
+      } else {
+        *reinterpret_cast<uint2 *>(out + at) = z;
       }
+    }
 }
 
 // out[a] = bf16(s[a] * (sum over the adapter's blocks of part)) where the adapter (blockIdx.y) has more
 // than one block, zeros where it has none; n values an adapter, two a thread (n is even: r C with
 // C % 8 == 0).
-__global__ void multi_sum_final_kernel(const float *__restrict__ part, int64_t n, const int32_t *__restrict__ first,
-                                       const float *__restrict__ s, uint16_t *__restrict__ out) {
+__global__ void multi_sum_final_kernel(SumArgs w, MultiPlan pl) {
+  const MultiSum g = blockIdx.z ? w.g[1] : w.g[0];
+  const int32_t *first = pl.table[g.which];
   const int a = blockIdx.y, lo = first[a], nb = first[a + 1] - lo;
+  const int64_t n = (int64_t)w.r * g.c;
   if (nb == 1) return;
-  const float sa = s[a];
+  const float sa = w.s[a];
   for (int64_t i = (blockIdx.x * (int64_t)blockDim.x + threadIdx.x) * 2; i < n; i += (int64_t)gridDim.x * blockDim.x * 2) {
-    const float *pa = part + (int64_t)lo * n + i;
+    const float *pa = g.part + (int64_t)lo * n + i;
     f32x2 x = {0.f, 0.f};
     int q = 0;
     for (; q + 8 <= nb; q += 8) {
@@ -512,55 +648,7 @@ __global__ void multi_sum_final_kernel(const float *__restrict__ part, int64_t n
       for (int j = 0; j < 8; ++j) x += v[j];
     }
     for (; q < nb; ++q) x += *reinterpret_cast<const f32x2 *>(pa + (int64_t)q * n);
-    *reinterpret_cast<uint32_t *>(out + a * n + i) = nb ? pack_bf16x2(sa * x[0], sa * x[1]) : 0u;
-  }
-}
-
-// ------------------------------------------------------------------------------------ transposes
-// dst[b][c][j] = src[b][j][c] for the bf16 matrices [R][C] of the adapters b that have rows (nobody reads
-// the others), of both factors in one launch (blockIdx.z), through 64 x 64 LDS tiles; the rows of dst have ldd elements (a multiple of
-// 8), zeros from R on. 16-byte loads where C % 8 == 0, 16-byte stores.
-struct TransposeArgs {
-  const uint16_t *src;
-  uint16_t *dst;
-  int64_t R, C, ldd;
-};
-__global__ __launch_bounds__(256) void multi_transpose_kernel(TransposeArgs b, TransposeArgs a, const int32_t *row) {
-  __shared__ uint16_t t[64][66];   // [c][r]
-  if (row[blockIdx.y] == row[blockIdx.y + 1]) return;
-  const TransposeArgs &g = blockIdx.z ? a : b;
-  const int64_t R = g.R, C = g.C, ldd = g.ldd;
-  const uint16_t *src = g.src;
-  uint16_t *dst = g.dst;
-  if ((int64_t)blockIdx.x >= (C + 63) / 64 * ((ldd + 63) / 64)) return;
-  const int64_t tiles_c = (C + 63) / 64;
-  const int64_t c0 = (int64_t)blockIdx.x % tiles_c * 64, r0 = (int64_t)blockIdx.x / tiles_c * 64;
-  src += (int64_t)blockIdx.y * R * C;
-  dst += (int64_t)blockIdx.y * ldd * C;
-  const int tid = threadIdx.x;
-  if ((C & 7) == 0) {
-#pragma unroll
-    for (int h = 0; h < 2; ++h) {
-      const int r = (tid >> 3) + 32 * h, c = (tid & 7) * 8;
-      u32x4 v = {0u, 0u, 0u, 0u};
-      if (r0 + r < R && c0 + c < C) v = *reinterpret_cast<const u32x4 *>(src + (r0 + r) * C + c0 + c);
-#pragma unroll
-      for (int e = 0; e < 8; ++e) t[c + e][r] = (uint16_t)(v[e >> 1] >> (16 * (e & 1)));
-    }
-  } else {
-    const int x = tid & 63;
-    for (int r = tid >> 6; r < 64; r += 4)
-      t[x][r] = r0 + r < R && c0 + x < C ? src[(r0 + r) * C + c0 + x] : (uint16_t)0;
-  }
-  __syncthreads();
-#pragma unroll
-  for (int h = 0; h < 2; ++h) {
-    const int c = (tid >> 3) + 32 * h, r = (tid & 7) * 8;
-    if (c0 + c >= C || r0 + r >= ldd) continue;
-    u32x4 v;
-#pragma unroll
-    for (int e = 0; e < 4; ++e) v[e] = t[c][r + 2 * e] | ((uint32_t)t[c][r + 2 * e + 1] << 16);
-    *reinterpret_cast<u32x4 *>(dst + (c0 + c) * ldd + r0 + r) = v;
+    *reinterpret_cast<uint32_t *>(g.out + a * n + i) = nb ? pack_bf16x2(sa * x[0], sa * x[1]) : 0u;
   }
 }
 
@@ -575,13 +663,21 @@ int64_t blocks_for(int64_t n) {
 
 }  // namespace
 
-hipError_t launch_multi_plan(const int32_t *ids, int64_t M, int L, const MultiPlan &pl, const uint16_t *src, int64_t rows,
-                             int r, int rp, uint16_t *dst, hipStream_t st) {
+hipError_t launch_multi_plan(const int32_t *ids, int64_t M, int L, const MultiPlan &pl, const MultiPad &pd,
+                             const MultiFactors &f, hipStream_t st) {
   if (L < 1 || L > kMultiMaxAdapters || M < 1 || M >= (int64_t(1) << 30)) return hipErrorInvalidValue;
-  const PadArgs pad{src, dst, r == rp ? 0 : rows, r, rp};
-  int64_t blocks = (pad.rows * rp + 4 * kPlanThreads - 1) / (4 * kPlanThreads);
-  blocks = 1 + (blocks < 1024 ? blocks : 1024);
-  multi_plan_kernel<<<dim3((unsigned)blocks), dim3(kPlanThreads), sizeof(int32_t) * kPlanWaves * (L + 1), st>>>(ids, M, L, pl, pad);
+  PlanWork w{};
+  w.pad = PadArgs{pd.src, pd.dst, pd.src ? pd.rows : 0, pd.r, pd.rp};
+  const int64_t pads = (w.pad.rows * pd.rp + 4 * kPlanThreads - 1) / (4 * kPlanThreads);
+  w.pad_blocks = (int)(pads < 1024 ? pads : 1024);
+  if (f.Bt) {
+    if (f.rp < f.r || (f.rp & 7) != 0 || (f.n & 7) != 0) return hipErrorInvalidValue;
+    w.tr[0] = TransposeArgs{f.B, f.Bt, f.n, f.r, f.n};
+    if (f.At) w.tr[1] = TransposeArgs{f.A, f.At, f.r, f.k, f.rp};
+  }
+  const int64_t blocks = 1 + w.pad_blocks + (w.tr[0].blocks() + w.tr[1].blocks()) * L;
+  if (blocks >= (int64_t(1) << 32) / kPlanThreads) return hipErrorInvalidValue;
+  multi_plan_kernel<<<dim3((unsigned)blocks), dim3(kPlanThreads), sizeof(int32_t) * kPlanWaves * (L + 1), st>>>(ids, M, L, pl, w);
   return hipGetLastError();
 }
 
@@ -598,33 +694,35 @@ int multi_rows_splits(int64_t M, int64_t Lr) {
   return (int)(s > 1 ? s : 1);
 }
 
-hipError_t launch_multi_rows(const uint16_t *in, int64_t ldin, const uint16_t *p, int64_t pstride, int64_t ldp,
-                             int64_t M, int64_t Lr, int r, int rp, int L, int splits, float *part,
-                             const MultiPlan &pl, hipStream_t st) {
+hipError_t launch_multi_rows(const MultiRows *g, int count, int64_t M, int r, int rp, int L, const MultiPlan &pl,
+                             hipStream_t st) {
+  if (count < 1 || count > 2 || rp < r || (rp & 7) != 0) return hipErrorInvalidValue;
   const int64_t rows = multi_rows_block(M);
-  int64_t lsplit = (Lr + splits - 1) / splits;
-  lsplit = (lsplit + 63) / 64 * 64;
+  RowsArgs w{{g[0], g[count - 1]}, {}, M, r, rp, L};
+  int most = 1;
+  for (int i = 0; i < 2; ++i) {
+    if ((w.g[i].l & 7) != 0 || w.g[i].splits < 1 || w.g[i].splits > 65535) return hipErrorInvalidValue;
+    w.lsplit[i] = ((w.g[i].l + w.g[i].splits - 1) / w.g[i].splits + 63) / 64 * 64;
+    most = most > w.g[i].splits ? most : w.g[i].splits;
+  }
   int64_t blocks = (M + (rows - 1) * (L + 1)) / rows;   // >= the sum of ceil(rows of a group / rows)
   blocks = blocks < M ? blocks : M;
-  const dim3 grid((unsigned)blocks, (unsigned)splits);
+  const dim3 grid((unsigned)blocks, (unsigned)most, (unsigned)count);
   switch ((r + 15) / 16) {
-#define MR_CASE(T)                                                                                                 \
-  case T:                                                                                                          \
-    if (rows == 16)                                                                                                \
-      multi_rows16_kernel<T><<<grid, dim3(256), 0, st>>>(in, ldin, p, pstride, ldp, M, Lr, r, rp, L, lsplit, part, pl); \
-    else                                                                                                           \
-      multi_rows64_kernel<T><<<grid, dim3(256), 0, st>>>(in, ldin, p, pstride, ldp, M, Lr, r, rp, L, lsplit, part, pl); \
+#define MR_CASE(T)                                                       \
+  case T:                                                                \
+    if (rows == 16)                                                      \
+      multi_rows16_kernel<T><<<grid, dim3(256), 0, st>>>(w, pl);         \
+    else                                                                 \
+      multi_rows64_kernel<T><<<grid, dim3(256), 0, st>>>(w, pl);         \
     break;
     MR_CASE(1) MR_CASE(2) MR_CASE(3) MR_CASE(4) MR_CASE(5) MR_CASE(6) MR_CASE(7) MR_CASE(8)
 #undef MR_CASE
     default: return hipErrorInvalidValue;
   }
-  return hipGetLastError();
-}
-
-hipError_t launch_multi_rows_sum(const float *part, int64_t M, int r, int rp, int splits, uint16_t *out, uint16_t *outp,
-                                 hipStream_t st) {
-  multi_rows_sum_kernel<<<dim3((unsigned)blocks_for(M * rp)), dim3(256), 0, st>>>(part, M, r, rp, splits, out, outp);
+  const hipError_t e = hipGetLastError();
+  if (e != hipSuccess || (!g[0].out && !g[0].padded && !g[0].wide)) return e;
+  multi_rows_sum_kernel<<<dim3((unsigned)blocks_for(M * rp), (unsigned)count), dim3(256), 0, st>>>(w);
   return hipGetLastError();
 }
 
@@ -638,46 +736,48 @@ hipError_t launch_multi_rows_part(const uint16_t *in, int64_t ldin, const uint16
 }
 
 // Rows of a block of the sums over rows: about four workgroups for each of the 256 CUs over the column
-// tiles, 64 to 1024 rows.
+// tiles, 64 to 1024 rows. Up to kMultiSmallM rows are one block.
 int multi_sum_rows(int64_t M, int64_t C) {
+  if (M <= kMultiSmallM) return kMultiSmallM;
   const int64_t rows = (M * ((C + kCB - 1) / kCB) / 1024 + kRB - 1) / kRB * kRB;
   return (int)(rows < kRB ? kRB : rows < kSumRows ? rows : kSumRows);
 }
 int64_t multi_sum_blocks(int64_t M, int64_t C, int L) {
+  if (M <= kMultiSmallM) return 0;   // nothing to add afterwards
   const int64_t rows = multi_sum_rows(M, C), b = (M + (rows - 1) * L) / rows;   // >= the sum of ceil(rows of a / rows)
   return b < M ? b : M;
 }
 
-hipError_t launch_multi_sum(const uint16_t *P, int64_t ldp, const uint16_t *Q, int64_t ldq, int64_t M, int64_t C, int r,
-                            int L, const float *s, int which, float *part, uint16_t *out, bool transposed,
-                            const MultiPlan &pl, hipStream_t st) {
-  const int64_t blocks = multi_sum_blocks(M, C, L);
-  if ((ldp & 7) != 0 || ldp < r || (C & 7) != 0 || pl.rows[which] != multi_sum_rows(M, C)) return hipErrorInvalidValue;
-  const int64_t tiles = (C + kCB - 1) / kCB;
+hipError_t launch_multi_sums(const MultiSum &a, const MultiSum &b, int64_t M, int r, int rp, int L, const float *s,
+                             const MultiPlan &pl, hipStream_t st) {
+  const SumArgs w{{a, b}, s, r, rp, L};
+  const bool small = M <= kMultiSmallM;
+  int64_t tiles = 1, blocks = small ? L : 1, most = 1;
+  if (rp < r || (rp & 7) != 0) return hipErrorInvalidValue;
+  for (const MultiSum &g : w.g) {
+    if ((g.c & 7) != 0 || pl.rows[g.which] != multi_sum_rows(M, g.c)) return hipErrorInvalidValue;
+    tiles = std::max(tiles, (g.c + kCB - 1) / kCB);
+    blocks = std::max(blocks, multi_sum_blocks(M, g.c, L));
+    most = std::max(most, g.c);
+  }
   if (blocks > 65535) return hipErrorInvalidValue;
-  const dim3 grid((unsigned)tiles, (unsigned)blocks);
+  const dim3 grid((unsigned)tiles, (unsigned)blocks, 2);
   switch ((r + 15) / 16) {
-#define MS_CASE(T)                                                                                                  case T:                                                                                                             multi_sum_kernel<T><<<grid, dim3(256), 0, st>>>(P, ldp, Q, ldq, C, r, L, which, part, s, transposed, out, pl);     break;
+#define MS_CASE(T)                                                       \
+  case T:                                                                \
+    if (small)                                                           \
+      multi_sum_kernel<T, true><<<grid, dim3(256), 0, st>>>(w, pl);      \
+    else                                                                 \
+      multi_sum_kernel<T, false><<<grid, dim3(256), 0, st>>>(w, pl);     \
+    break;
     MS_CASE(1) MS_CASE(2) MS_CASE(3) MS_CASE(4) MS_CASE(5) MS_CASE(6) MS_CASE(7) MS_CASE(8)
 #undef MS_CASE
     default: return hipErrorInvalidValue;
   }
-  hipError_t e = hipGetLastError();
-  if (e != hipSuccess) return e;
-  const int64_t n = (int64_t)r * C;
-  int64_t b = (n / 2 + 255) / 256;
-  b = b < 1024 ? b : 1024;
-  multi_sum_final_kernel<<<dim3((unsigned)b, (unsigned)L), dim3(256), 0, st>>>(part, n, pl.table[which], s, out);
-  return hipGetLastError();
-}
-
-hipError_t launch_multi_transposes(const uint16_t *B, int64_t n, const uint16_t *A, int64_t k, int r, int rp, int L,
-                                   const MultiPlan &pl, uint16_t *Bt, uint16_t *At, hipStream_t st) {
-  if (rp < r || (rp & 7) != 0 || (n & 7) != 0) return hipErrorInvalidValue;
-  const TransposeArgs b{B, Bt, n, r, n}, a{A, At, r, k, rp};
-  auto tiles = [](const TransposeArgs &g) { return (g.C + 63) / 64 * ((g.ldd + 63) / 64); };
-  const int64_t x = At && tiles(a) > tiles(b) ? tiles(a) : tiles(b);
-  multi_transpose_kernel<<<dim3((unsigned)x, (unsigned)L, At ? 2 : 1), dim3(256), 0, st>>>(b, a, pl.table[kPlanRow]);
+  const hipError_t e = hipGetLastError();
+  if (e != hipSuccess || small) return e;
+  const int64_t x = std::min<int64_t>(((int64_t)r * most / 2 + 255) / 256, 1024);
+  multi_sum_final_kernel<<<dim3((unsigned)x, (unsigned)L, 2), dim3(256), 0, st>>>(w, pl);
   return hipGetLastError();
 }
 

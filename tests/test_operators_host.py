@@ -19,7 +19,7 @@ def test_multi_refuses():
     lib = m.library()
     M, n, k, r, L = 100, 64, 128, 8, 3
     wf, wb = lib.qlora_multi_fwd_workspace_bytes(M, n, k, r, L), lib.qlora_multi_bwd_workspace_bytes(M, n, k, r, L)
-    assert 0 < wf < wb and lib.qlora_multi_fwd_workspace_bytes(0, n, k, r, L) == 0
+    assert wf > 0 and wb > 0 and lib.qlora_multi_fwd_workspace_bytes(0, n, k, r, L) == 0
     assert wb >= 2 * M * r * 2 + L * r * (n + k) * 2        # U, T and both transposed factors
 
     def fwd(**o):
