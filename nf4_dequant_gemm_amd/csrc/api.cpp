@@ -1089,7 +1089,7 @@ MultiWs multi_ws(int64_t m, int64_t n, int64_t k, int32_t r, int32_t L, bool bwd
     w.wide = small ? align256((size_t)2 * m * rp * 4) : 0;
     size_t p = (size_t)(small ? w.sp_n + w.sp_k : std::max(w.sp_n, w.sp_k)) * m * rp * 4;
     if (w.pieces > 1) p = std::max(p, (size_t)w.pieces * m * k * 4);
-    p = std::max(p, ((size_t)nf4q::multi_sum_blocks(m, k, L) * k + (size_t)nf4q::multi_sum_blocks(m, n, L) * n) * r * 4);
+    p = std::max(p, (size_t)nf4q::multi_sum_blocks(m, k, n, L) * r * (n + k) * 4);
     w.part = align256(p);
   } else {
     if (rp != r) {
@@ -1199,7 +1199,7 @@ int qlora_multi_fwd(const void *X, int64_t m, const nf4_tensor *W, const void *A
       e = nf4q::launch_mid_fwd_multi(g, mu, a, r, tpart, nf4q::mid_tsplits(m, k), t, part, sm);
     return hip_status(e, "qlora_multi_fwd launch");
   }
-  const nf4q::MultiPlan pl = nf4q::multi_plan_at(base, m, L, nf4q::multi_sum_rows(m, k), nf4q::multi_sum_rows(m, n));
+  const nf4q::MultiPlan pl = nf4q::multi_plan_at(base, m, L, nf4q::multi_sum_rows(m, k, n));
   const nf4q::MultiPad pad{rp == r ? nullptr : b, (int64_t)L * n, r, rp, Bp};
   e = nf4q::launch_multi_plan(ids, m, L, pl, pad, nf4q::MultiFactors{}, sm);
   if (e != hipSuccess) return hip_status(e, "qlora_multi_fwd plan launch");
@@ -1210,10 +1210,10 @@ int qlora_multi_fwd(const void *X, int64_t m, const nf4_tensor *W, const void *A
   }
   e = nf4q::launch_multi_rows(&rows, 1, m, r, rp, L, pl, sm);
   if (e != hipSuccess) return hip_status(e, "qlora_multi_fwd T launch");
+  mu.perm = pl.perm;
   if (kernel == MultiKernel::kMid)
     return hip_status(nf4q::launch_mid_fwd_multi(g, mu, a, r, tpart, lay.sp_k, t, part, sm), "qlora_multi_fwd launch");
   mu.P = rp == r ? t : Tp;
-  mu.perm = pl.perm;
   return hip_status(nf4q::launch_gemm_fwd_multi(g, mu, sm), "qlora_multi_fwd launch");
 }
 
@@ -1232,7 +1232,7 @@ int qlora_multi_bwd(const void *dY, const void *X, int64_t m, const nf4_tensor *
   if (st) return st;
   hipStream_t sm = (hipStream_t)stream;
   char *base = (char *)ws;
-  const nf4q::MultiPlan pl = nf4q::multi_plan_at(base, m, L, nf4q::multi_sum_rows(m, k), nf4q::multi_sum_rows(m, n));
+  const nf4q::MultiPlan pl = nf4q::multi_plan_at(base, m, L, nf4q::multi_sum_rows(m, k, n));
   char *at = base + lay.plan;
   auto take = [&](size_t bytes) {
     char *q = at;
@@ -1271,9 +1271,9 @@ int qlora_multi_bwd(const void *dY, const void *X, int64_t m, const nf4_tensor *
       e = nf4q::launch_multi_final(part, lay.pieces, m, k, mu, (uint16_t *)dX, sm);
     if (e != hipSuccess) return hip_status(e, "qlora_multi_bwd dX launch");
   }
-  const nf4q::MultiSum da{small ? (const void *)u.wide : U, x, k, nf4q::kPlanSumA, false, part, (uint16_t *)dA};
-  const nf4q::MultiSum db{small ? (const void *)tr.wide : t, dy, n, nf4q::kPlanSumB, true,
-                          part + nf4q::multi_sum_blocks(m, k, L) * r * k, (uint16_t *)dB};
+  const nf4q::MultiSum da{small ? (const void *)u.wide : U, x, k, false, part, (uint16_t *)dA};
+  const nf4q::MultiSum db{small ? (const void *)tr.wide : t, dy, n, true,
+                          part + nf4q::multi_sum_blocks(m, k, n, L) * r * k, (uint16_t *)dB};
   return hip_status(nf4q::launch_multi_sums(da, db, m, r, rp, L, s, pl, sm), "qlora_multi_bwd dA and dB launch");
 }
 

@@ -271,19 +271,18 @@ hipError_t launch_stream16_fwd_multi(const GemmArgs &g, const MultiArgs &mu, con
                                      uint16_t *tout, hipStream_t st);
 // The sums over rows, two in a launch: out[a] = s[a] * (sum over its rows of p_i^T q_i), [r][c] or transposed
 // [c][r]; q [M][c]; p [M][rp] with zeros from r on, bf16, or float32 with at most kMultiSmallM rows. Blocks
-// of multi_sum_rows(M, c) rows, which is what pl.rows[which] has to be (kPlanSumA or kPlanSumB); part:
-// multi_sum_blocks * r * c floats.
+// of multi_sum_rows(M, c of both) rows, which is what pl.rows[kPlanSum] has to be; part: multi_sum_blocks
+// * r * c floats.
 struct MultiSum {
   const void *p;
   const uint16_t *q;
   int64_t c;
-  int which;
   bool transposed;
   float *part;
   uint16_t *out;
 };
-int multi_sum_rows(int64_t M, int64_t c);
-int64_t multi_sum_blocks(int64_t M, int64_t c, int L);
+int multi_sum_rows(int64_t M, int64_t c0, int64_t c1);
+int64_t multi_sum_blocks(int64_t M, int64_t c0, int64_t c1, int L);
 hipError_t launch_multi_sums(const MultiSum &a, const MultiSum &b, int64_t M, int r, int rp, int L, const float *s,
                              const MultiPlan &pl, hipStream_t st);
 // dst [rows][rp] = src [rows][r] padded with zeros, by itself.

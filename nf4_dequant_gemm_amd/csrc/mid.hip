@@ -49,9 +49,11 @@ struct MidArgs {
   float *tpart;
   int tsplits, ra;
   uint16_t *T;
-  // T formed in the launch: the workgroups from tfirst on, from A [L][ra][K]
+  // T formed in the launch: the workgroups from tfirst on, from A [L][ra][K], and the last of them puts
+  // the rows in the order of their adapters: order [M]
   int tfirst;
   const uint16_t *A;
+  int32_t *order;
 };
 constexpr int kTSlice = 1024;   // reduction elements of a workgroup that forms T
 
@@ -103,6 +105,22 @@ __global__ __launch_bounds__(kThreads) void mid_kernel(MidArgs g, MultiArgs mu) 
     static_assert(kMultiSmallT<8, 2> <= sizeof(stab), "T's sums fit the table");
     const int nj = (mu.r + 31) / 32;
     const int tb = block - g.tfirst;
+    if (tb == (int)g.M * nj * g.tsplits) {   // a row's place: the rows before it by adapter, then by number
+      int *key = reinterpret_cast<int *>(stab);
+      const int i = threadIdx.x, M = (int)g.M;
+      int mine = 0;
+      if (i < M) {
+        const int a = mu.ids[i];
+        key[i] = mine = a >= 0 && a < mu.L ? a : mu.L;
+      }
+      __syncthreads();
+      if (i < M) {
+        int at = 0;
+        for (int j = 0; j < M; ++j) at += key[j] < mine || (key[j] == mine && j < i);
+        g.order[at] = i;
+      }
+      return;
+    }
     const int ts = tb % g.tsplits, j = tb / g.tsplits % nj, row = tb / g.tsplits / nj;
     const int64_t le = (int64_t)(ts + 1) * kTSlice;
     float *tp = g.tpart + (int64_t)ts * g.M * mu.r;
@@ -390,58 +408,88 @@ __global__ __launch_bounds__(kThreads) void mid_kernel(MidArgs g, MultiArgs mu) 
 
 // Y (or dX) from the float32 sums of the launch before, added in order, and the low-rank term, with T from
 // its own sums (written here, by the workgroups of the first columns) or T (U) from memory. One wave:
-// 16 rows and 64 columns.
+// 16 rows, in the order of their adapters (perm, unless there is one row tile only), and kFinalTiles
+// 16-column tiles. It is bound by its chain of loads, so those of the first four splits are in flight
+// during the term. 200 rows of 64 adapters x 11008, two splits: 11.4 us for 22 MB and the factors; 14.4 us
+// with the rows in the batch's order (14 adapters to a row tile instead of 5).
+template <int kFinalTiles>
 __global__ __launch_bounds__(64) void mid_final_kernel(MidArgs g, MultiArgs mu) {
   const int lane = threadIdx.x, g16 = lane >> 4, l16 = lane & 15;
-  const int64_t m0 = (int64_t)blockIdx.y * 16, m = m0 + l16, n0 = (int64_t)blockIdx.x * 64;
-  int id = m < g.M ? mu.ids[m] : -1;
+  const int64_t n0 = (int64_t)blockIdx.x * 16 * kFinalTiles;
+  int64_t m = (int64_t)blockIdx.y * 16 + l16;
+  const bool have = m < g.M;
+  if (mu.perm) m = have ? mu.perm[m] : 0;
+  int id = have ? mu.ids[m] : -1;
   id = id >= 0 && id < mu.L ? id : -1;
-  f32x4 y[4];
-#pragma unroll
-  for (int nt = 0; nt < 4; ++nt) y[nt] = f32x4{0.f, 0.f, 0.f, 0.f};
   const f32x4 zero = {0.f, 0.f, 0.f, 0.f};
-  for (int s0 = 0; s0 < g.splits; s0 += 4) {   // 16 loads at a time
-    f32x4 v[4][4];
+  auto load = [&](int s0, f32x4 (&v)[4][kFinalTiles]) {   // four splits
 #pragma unroll
     for (int s = 0; s < 4; ++s)
 #pragma unroll
-      for (int nt = 0; nt < 4; ++nt) {
+      for (int nt = 0; nt < kFinalTiles; ++nt) {
         const int64_t n = n0 + nt * 16 + 4 * g16;
-        v[s][nt] = s0 + s < g.splits && m < g.M && n < g.N
+        v[s][nt] = s0 + s < g.splits && have && n < g.N
                        ? *reinterpret_cast<const f32x4 *>(g.part + ((int64_t)(s0 + s) * g.M + m) * g.N + n)
                        : zero;
       }
+  };
+  f32x4 v[4][kFinalTiles], y[kFinalTiles], term[kFinalTiles];
+  load(0, v);
 #pragma unroll
-    for (int s = 0; s < 4; ++s)
-#pragma unroll
-      for (int nt = 0; nt < 4; ++nt) y[nt] += v[s][nt];
-  }
-  int64_t rows = g.M - m0;
-  rows = rows < 16 ? rows : 16;
-  const __amdgpu_buffer_rsrc_t rT = make_rsrc(mu.P + m0 * mu.r, g.tsplits ? 0 : rows * mu.r * 2);
-  multi_term_rows<4>(y, mu, id, n0, g.N, [&](int j) {
-    if (!g.tsplits) return rank_frag(rT, l16, j, mu.r);
+  for (int nt = 0; nt < kFinalTiles; ++nt) y[nt] = term[nt] = zero;
+  multi_term_rows<4>(term, mu, id, n0, g.N, [&](int j) {
+    const bool mine = have && j < mu.r;
+    if (!g.tsplits)
+      return __builtin_bit_cast(bf16x8, mine ? *reinterpret_cast<const u32x4 *>(mu.P + m * mu.r + j) : u32x4{0u, 0u, 0u, 0u});
     f32x4 a = zero, b = zero;
-    if (m < g.M && j < mu.r) {
-      const float *tp = g.tpart + m * mu.r + j;
-      for (int t = 0; t < g.tsplits; ++t, tp += g.M * mu.r) {
-        a += *reinterpret_cast<const f32x4 *>(tp);
-        b += *reinterpret_cast<const f32x4 *>(tp + 4);
-      }
-      if (blockIdx.x == 0) {
+    const float *tp = g.tpart + m * mu.r + j;
+    for (int t0 = 0; t0 < g.tsplits; t0 += 4) {
+      f32x4 x[4][2];
 #pragma unroll
-        for (int e = 0; e < 8; ++e)
-          if (j + e < g.ra) g.T[m * g.ra + j + e] = (uint16_t)(pack_bf16x2(e < 4 ? a[e & 3] : b[e & 3], 0.f) & 0xFFFFu);
+      for (int t = 0; t < 4; ++t)
+#pragma unroll
+        for (int h = 0; h < 2; ++h)
+          x[t][h] = mine && t0 + t < g.tsplits
+                        ? *reinterpret_cast<const f32x4 *>(tp + (t0 + t) * g.M * mu.r + 4 * h) : zero;
+#pragma unroll
+      for (int t = 0; t < 4; ++t) {
+        a += x[t][0];
+        b += x[t][1];
       }
+    }
+    if (mine && blockIdx.x == 0) {
+#pragma unroll
+      for (int e = 0; e < 8; ++e)
+        if (j + e < g.ra) g.T[m * g.ra + j + e] = (uint16_t)(pack_bf16x2(e < 4 ? a[e & 3] : b[e & 3], 0.f) & 0xFFFFu);
     }
     return __builtin_bit_cast(bf16x8, make_uint4(pack_bf16x2(a[0], a[1]), pack_bf16x2(a[2], a[3]),
                                                  pack_bf16x2(b[0], b[1]), pack_bf16x2(b[2], b[3])));
   });
+  for (int s0 = 0;;) {
 #pragma unroll
-  for (int nt = 0; nt < 4; ++nt) {
-    const int64_t n = n0 + nt * 16 + 4 * g16;
-    if (m < g.M && n < g.N) store4(g.Y, g.N, m, n, y[nt]);
+    for (int s = 0; s < 4; ++s)
+#pragma unroll
+      for (int nt = 0; nt < kFinalTiles; ++nt) y[nt] += v[s][nt];
+    s0 += 4;
+    if (s0 >= g.splits) break;
+    load(s0, v);
   }
+#pragma unroll
+  for (int nt = 0; nt < kFinalTiles; ++nt) {
+    const int64_t n = n0 + nt * 16 + 4 * g16;
+    if (have && n < g.N) store4(g.Y, g.N, m, n, y[nt] + term[nt]);
+  }
+}
+
+// 64 columns a wave read a row tile's adapters least often; a grid of under 8 such waves for each CU is
+// latency alone, and 32 columns then shorten every wave (4096 columns: 12 rows 17.4 -> 15.7 us for the
+// whole call; 500 rows, 64 adapters 61.0 -> 64.5 us, where there are enough waves without).
+void launch_final(const MidArgs &a, const MultiArgs &mu, hipStream_t st) {
+  const int64_t rows = (a.M + 15) / 16, cols = (a.N + 63) / 64;
+  if (rows * cols < 8 * 256)
+    mid_final_kernel<2><<<dim3((unsigned)((a.N + 31) / 32), (unsigned)rows), dim3(64), 0, st>>>(a, mu);
+  else
+    mid_final_kernel<4><<<dim3((unsigned)cols, (unsigned)rows), dim3(64), 0, st>>>(a, mu);
 }
 
 template <int kMT, int kNW, int kBlk, bool kAl>
@@ -496,7 +544,7 @@ size_t up256(size_t x) { return (x + 255) & ~size_t(255); }
 int mid_tsplits(int64_t M, int64_t K) { return M <= kMultiSmallM ? (int)((K + kTSlice - 1) / kTSlice) : 0; }
 
 size_t mid_fwd_bytes(int64_t M, int64_t N, int64_t K) {
-  return up256((size_t)mid_shape(M, N, K).splits * M * N * 4);
+  return up256((size_t)mid_shape(M, N, K).splits * M * N * 4) + (M <= kMultiSmallM ? up256((size_t)M * 4) : 0);
 }
 
 hipError_t launch_multi_final(const float *part, int splits, int64_t M, int64_t C, const MultiArgs &mu, uint16_t *out,
@@ -509,7 +557,7 @@ hipError_t launch_multi_final(const float *part, int splits, int64_t M, int64_t 
   a.Y = out;
   a.part = const_cast<float *>(part);
   a.splits = splits;
-  mid_final_kernel<<<dim3((unsigned)((C + 63) / 64), (unsigned)tiles), dim3(64), 0, st>>>(a, mu);
+  launch_final(a, mu, st);
   return hipGetLastError();
 }
 
@@ -517,14 +565,16 @@ hipError_t launch_mid_fwd_multi(const GemmArgs &ga, const MultiArgs &mu, const u
                                 int tsplits, uint16_t *T, float *part, hipStream_t st) {
   if ((ga.C & 7) != 0 || ga.ldo != ga.C || ga.M < 1 || ga.R % 64 != 0 || (mu.r & 7) != 0 || ra > mu.r || tsplits < 1)
     return hipErrorInvalidValue;
+  const bool small = ga.M <= kMultiSmallM;
   const MidShape s = mid_shape(ga.M, ga.C, ga.R);
   const int64_t rows = (ga.M + 16 * s.mt - 1) / (16 * s.mt);
   const int64_t tiles = rows * ((ga.C + 32 * s.nw - 1) / (32 * s.nw)) * s.splits;
-  const int64_t wgs = tiles + (ga.M <= kMultiSmallM ? ga.M * ((mu.r + 31) / 32) * tsplits : 0);
+  const int64_t wgs = tiles + (small ? ga.M * ((mu.r + 31) / 32) * tsplits + (ga.M > 16) : 0);
   const int64_t frows = (ga.M + 15) / 16;
-  if (wgs >= (int64_t(1) << 31) || frows > 65535 || (ga.M <= kMultiSmallM && tsplits != mid_tsplits(ga.M, ga.R)))
+  int32_t *order = reinterpret_cast<int32_t *>(reinterpret_cast<char *>(part) + up256((size_t)s.splits * ga.M * ga.C * 4));
+  if (wgs >= (int64_t(1) << 31) || frows > 65535 || (small && tsplits != mid_tsplits(ga.M, ga.R)))
     return hipErrorInvalidValue;
-  const MidArgs a{ga.a_side, ga.w, ga.M, ga.C, ga.R, ga.out, part, s.splits, ga.t, tpart, tsplits, ra, T, (int)tiles, A};
+  const MidArgs a{ga.a_side, ga.w, ga.M, ga.C, ga.R, ga.out, part, s.splits, ga.t, tpart, tsplits, ra, T, (int)tiles, A, order};
   const unsigned grid = (unsigned)wgs;
 #define MID_AL(MT, NW, BLK) launch_fmt<MT, NW, BLK, true>(a, mu, grid, st)
 #define MID_ANY(MT, NW, BLK) s.al ? MID_AL(MT, NW, BLK) : launch_fmt<MT, NW, BLK, false>(a, mu, grid, st)
@@ -542,7 +592,9 @@ hipError_t launch_mid_fwd_multi(const GemmArgs &ga, const MultiArgs &mu, const u
 #undef MID_AL
   hipError_t e = hipGetLastError();
   if (e != hipSuccess) return e;
-  mid_final_kernel<<<dim3((unsigned)((ga.C + 63) / 64), (unsigned)frows), dim3(64), 0, st>>>(a, mu);
+  MultiArgs mf = mu;
+  if (small) mf.perm = ga.M > 16 ? order : nullptr;
+  launch_final(a, mf, st);
   return hipGetLastError();
 }
 

@@ -235,21 +235,20 @@ __device__ __forceinline__ void multi_rows_of(const uint16_t *in, int64_t ldin, 
 }
 
 // The rows in the order of their adapters (rows without one last, as group L), each group's rows in
-// their own order, and each group's first row and first block of 16 rows, of 64 rows, and of the two
-// row counts that the sums over rows take at a time. int32 tables of a workspace, written by
-// launch_multi_plan.
+// their own order, and each group's first row and first block of 16 rows, of 64 rows, and of the rows
+// that the sums over rows take at a time. int32 tables of a workspace, written by launch_multi_plan.
 constexpr int kMultiMaxAdapters = 1024;
-constexpr int kMultiTables = 5;
+constexpr int kMultiTables = 4;
 struct MultiPlan {
   int32_t *perm;                 // [M]
   int32_t *table[kMultiTables];  // [L + 2] each: first row, then first blocks
   int rows[kMultiTables];        // rows of a block: 1, 16, 64, and the sums'
 };
-enum { kPlanRow = 0, kPlan16 = 1, kPlan64 = 2, kPlanSumA = 3, kPlanSumB = 4 };
+enum { kPlanRow = 0, kPlan16 = 1, kPlan64 = 2, kPlanSum = 3 };
 inline size_t multi_plan_bytes(int64_t m, int L) { return 4 * ((size_t)m + kMultiTables * (size_t)(L + 2)); }
-inline MultiPlan multi_plan_at(void *ws, int64_t m, int L, int rows_a, int rows_b) {
+inline MultiPlan multi_plan_at(void *ws, int64_t m, int L, int sum_rows) {
   int32_t *p = reinterpret_cast<int32_t *>(ws);
-  MultiPlan pl{p, {}, {1, 16, 64, rows_a, rows_b}};
+  MultiPlan pl{p, {}, {1, 16, 64, sum_rows}};
   for (int t = 0; t < kMultiTables; ++t) pl.table[t] = p + m + t * (L + 2);
   return pl;
 }

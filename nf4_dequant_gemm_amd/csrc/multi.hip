@@ -437,7 +437,7 @@ __global__ void multi_rows_sum_kernel(RowsArgs w) {
 }
 
 // ------------------------------------------------------------------------------------ sums over rows
-// dA and dB in one launch (blockIdx.z). A block of rows (block blockIdx.y of the plan's table `which`, at
+// dA and dB in one launch (blockIdx.z). A block of rows (block blockIdx.y of the plan's table kPlanSum, at
 // most kSumRows rows, all of one adapter a): the sum over them of P[i][j] * Q[i][c] (dA: P = U, Q = X; dB:
 // P = T, Q = dY), as out holds it ([r][C], transposed [C][r]). An adapter of one block writes s[a] times
 // it to out; otherwise it goes to part[block] and multi_sum_final_kernel adds the adapter's blocks in
@@ -479,11 +479,11 @@ __global__ __launch_bounds__(256) void multi_sum_kernel(SumArgs w, MultiPlan pl)
     lo = pl.table[kPlanRow][a];
     me = pl.table[kPlanRow][a + 1] - lo;
   } else {
-    const int32_t *first = pl.table[g.which];
+    const int32_t *first = pl.table[kPlanSum];
     if ((int)blockIdx.y >= first[w.L]) return;   // the grid is an upper bound; rows without an adapter add to no sum
     a = group_of_block(first, w.L - 1, blockIdx.y);
     nb = first[a + 1] - first[a];
-    const int size = pl.rows[g.which];
+    const int size = pl.rows[kPlanSum];
     lo = pl.table[kPlanRow][a] + ((int)blockIdx.y - first[a]) * size;
     const int32_t hi = pl.table[kPlanRow][a + 1];
     me = lo + size < hi ? size : hi - lo;
@@ -631,7 +631,7 @@ __global__ __launch_bounds__(256) void multi_sum_kernel(SumArgs w, MultiPlan pl)
 // C % 8 == 0).
 __global__ void multi_sum_final_kernel(SumArgs w, MultiPlan pl) {
   const MultiSum g = blockIdx.z ? w.g[1] : w.g[0];
-  const int32_t *first = pl.table[g.which];
+  const int32_t *first = pl.table[kPlanSum];
   const int a = blockIdx.y, lo = first[a], nb = first[a + 1] - lo;
   const int64_t n = (int64_t)w.r * g.c;
   if (nb == 1) return;
@@ -736,15 +736,16 @@ hipError_t launch_multi_rows_part(const uint16_t *in, int64_t ldin, const uint16
 }
 
 // Rows of a block of the sums over rows: about four workgroups for each of the 256 CUs over the column
-// tiles, 64 to 1024 rows. Up to kMultiSmallM rows are one block.
-int multi_sum_rows(int64_t M, int64_t C) {
+// tiles of both sums, 64 to 1024 rows. Up to kMultiSmallM rows are one block.
+int multi_sum_rows(int64_t M, int64_t c0, int64_t c1) {
   if (M <= kMultiSmallM) return kMultiSmallM;
-  const int64_t rows = (M * ((C + kCB - 1) / kCB) / 1024 + kRB - 1) / kRB * kRB;
+  const int64_t tiles = (c0 + kCB - 1) / kCB + (c1 + kCB - 1) / kCB;
+  const int64_t rows = (M * tiles / 1024 + kRB - 1) / kRB * kRB;
   return (int)(rows < kRB ? kRB : rows < kSumRows ? rows : kSumRows);
 }
-int64_t multi_sum_blocks(int64_t M, int64_t C, int L) {
+int64_t multi_sum_blocks(int64_t M, int64_t c0, int64_t c1, int L) {
   if (M <= kMultiSmallM) return 0;   // nothing to add afterwards
-  const int64_t rows = multi_sum_rows(M, C), b = (M + (rows - 1) * L) / rows;   // >= the sum of ceil(rows of a / rows)
+  const int64_t rows = multi_sum_rows(M, c0, c1), b = (M + (rows - 1) * L) / rows;   // >= the sum of ceil(rows of a / rows)
   return b < M ? b : M;
 }
 
@@ -752,15 +753,10 @@ hipError_t launch_multi_sums(const MultiSum &a, const MultiSum &b, int64_t M, in
                              const MultiPlan &pl, hipStream_t st) {
   const SumArgs w{{a, b}, s, r, rp, L};
   const bool small = M <= kMultiSmallM;
-  int64_t tiles = 1, blocks = small ? L : 1, most = 1;
-  if (rp < r || (rp & 7) != 0) return hipErrorInvalidValue;
-  for (const MultiSum &g : w.g) {
-    if ((g.c & 7) != 0 || pl.rows[g.which] != multi_sum_rows(M, g.c)) return hipErrorInvalidValue;
-    tiles = std::max(tiles, (g.c + kCB - 1) / kCB);
-    blocks = std::max(blocks, multi_sum_blocks(M, g.c, L));
-    most = std::max(most, g.c);
-  }
-  if (blocks > 65535) return hipErrorInvalidValue;
+  const int64_t most = std::max(a.c, b.c), tiles = (most + kCB - 1) / kCB;
+  const int64_t blocks = small ? L : multi_sum_blocks(M, a.c, b.c, L);
+  if (rp < r || (rp & 7) != 0 || ((a.c | b.c) & 7) != 0 || pl.rows[kPlanSum] != multi_sum_rows(M, a.c, b.c) || blocks > 65535)
+    return hipErrorInvalidValue;
   const dim3 grid((unsigned)tiles, (unsigned)blocks, 2);
   switch ((r + 15) / 16) {
 #define MS_CASE(T)                                                       \
