@@ -1077,10 +1077,10 @@ struct MultiWs {
 MultiWs multi_ws(int64_t m, int64_t n, int64_t k, int32_t r, int32_t L, bool bwd) {
   MultiWs w;
   const int rp = padded(r);
-  w.sp_k = nf4q::multi_rows_splits(m, k);
+  w.sp_k = nf4q::multi_rows_splits(m, k, L);
   w.plan = align256(nf4q::multi_plan_bytes(m, L));
   if (bwd) {
-    w.sp_n = nf4q::multi_rows_splits(m, n);
+    w.sp_n = nf4q::multi_rows_splits(m, n, L);
     w.pieces = nf4q::dx_multi_pieces(m, k, n);
     w.u = w.tp = align256((size_t)m * rp * 2);
     w.bt = align256((size_t)L * r * n * 2);

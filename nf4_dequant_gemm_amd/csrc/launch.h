@@ -245,12 +245,12 @@ struct MultiRows {
   const uint16_t *in;
   int64_t l;
   const uint16_t *p;
-  int splits;   // multi_rows_splits(M, l)
+  int splits;   // multi_rows_splits(M, l, L)
   float *part;
   uint16_t *out, *padded;
   float *wide;
 };
-int multi_rows_splits(int64_t M, int64_t l);
+int multi_rows_splits(int64_t M, int64_t l, int L);
 hipError_t launch_multi_rows(const MultiRows *g, int count, int64_t M, int r, int rp, int L, const MultiPlan &pl,
                              hipStream_t st);
 // The projection without the table, for at most kMultiSmallM rows (any order of ids), as partial sums

@@ -523,11 +523,14 @@ MidShape mid_shape(int64_t M, int64_t N, int64_t K) {
   const int64_t steps = (K / 64 + s.blk - 1) / s.blk;
   // Splits: the least of (rounds of 256 workgroups) x (start and end of one, and its steps) plus the
   // traffic of the float32 sums, in us, from the times measured for 16 to 128 rows.
+  // With one row tile T's workgroups count as well: in a second round they made 1 to 12 rows x 4096 x 4096
+  // 1.1 to 1.6 us slower (with more rows most of them have no row to start from).
   const double per_step = 0.5 + 0.35 * s.mt * s.blk / 4;
+  const int64_t for_t = M <= 16 ? M * ((K + kTSlice - 1) / kTSlice) : 0;
   double best = 0;
   s.splits = 1;
   for (int64_t sp = 1; sp <= 16 && sp * kw <= steps; ++sp) {
-    const int64_t rounds = (wgs * sp + 255) / 256, it = (steps + sp * kw - 1) / (sp * kw);
+    const int64_t rounds = (wgs * sp + for_t + 255) / 256, it = (steps + sp * kw - 1) / (sp * kw);
     const double us = rounds * (4.0 + it * per_step) + sp * M * N * 8 / 4.0e6;
     if (sp == 1 || us < best) {
       best = us;
