@@ -240,79 +240,98 @@ __global__ __launch_bounds__(kThreads) void mid_kernel(MidArgs g, MultiArgs mu) 
   // after the swap lane group g holds elements 16 sg .. 16 sg + 15 of a block, sg = 0, 2, 1, 3
   const int sg = ((g16 & 1) << 1) | (g16 >> 1);
 
-  auto compute = [&](const Codes &c, const uint4 *sX) {
-    const uint4 *mine = sX + kw * kSlice;
+  // A block's weights as operands, decoded in four parts (column tile, half), and its constants.
+  struct Block {
+    bf16x8 w[2][2];
+    float a[2];   // NF4: the block's constant; E2M1: the lane's group scale
+  };
+  Pair turned[2][2];   // the lane's 8 bytes of a half's first and second block
+  auto decode = [&](const Codes &c, int blk, int part, Block &d) {
+    const int nt = part >> 1, e = part & 1, h = blk >> 1;
+    if ((blk & 1) == 0) turned[nt][e] = swap_halves(c.c[nt][h][e], c.c[nt][h][e + 2]);
+    const uint32_t code = blk & 1 ? turned[nt][e].b : turned[nt][e].a;
+    if constexpr (kFP4) {
+      if (e == 0) d.a[nt] = __builtin_amdgcn_cvt_f32_fp8((int)(c.q[nt][blk] >> (8 * sg)), 0);
+      const float s = d.a[nt];
+      // bytes hold the earlier element in the high nibble
+      const uint32_t u = ((code >> 4) & 0x0F0F0F0Fu) | ((code << 4) & 0xF0F0F0F0u);
+      const f32x2 p0 = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(u, 1.f, 0);
+      const f32x2 p1 = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(u, 1.f, 1);
+      const f32x2 p2 = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(u, 1.f, 2);
+      const f32x2 p3 = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(u, 1.f, 3);
+      d.w[nt][e] = __builtin_bit_cast(
+          bf16x8, make_uint4(pack_bf16x2(p0[0] * s, p0[1] * s), pack_bf16x2(p1[0] * s, p1[1] * s),
+                             pack_bf16x2(p2[0] * s, p2[1] * s), pack_bf16x2(p3[0] * s, p3[1] * s)));
+    } else {
+      uint32_t o[4];
 #pragma unroll
-    for (int h = 0; h < kH; ++h) {
-      Pair lo[2], hi[2];   // [nt]: the lane's 8 bytes of the half's first and second block
-#pragma unroll
-      for (int nt = 0; nt < 2; ++nt) {
-        const Pair x = swap_halves(c.c[nt][h][0], c.c[nt][h][2]);
-        const Pair y = swap_halves(c.c[nt][h][1], c.c[nt][h][3]);
-        lo[nt] = Pair{x.a, y.a};
-        hi[nt] = Pair{x.b, y.b};
+      for (int i = 0; i < 4; ++i) {
+        const uint32_t at = perm(code, copy, 0x0C0C0400u | ((4u + i) << 8));
+        o[i] = *reinterpret_cast<const uint32_t *>(tab + at);
       }
-#pragma unroll
-      for (int b = 0; b < 2; ++b) {
-        const int blk = 2 * h + b;
-        bf16x8 w[2][2];
-        float a[2];
-#pragma unroll
-        for (int nt = 0; nt < 2; ++nt) {
-          const Pair d = b ? hi[nt] : lo[nt];
-          if constexpr (kFP4) {
-            const float s = __builtin_amdgcn_cvt_f32_fp8((int)(c.q[nt][blk] >> (8 * sg)), 0);
-            auto pairs = [&](uint32_t v, uint32_t o[4]) {   // bytes hold the earlier element in the high nibble
-              const uint32_t u = ((v >> 4) & 0x0F0F0F0Fu) | ((v << 4) & 0xF0F0F0F0u);
-              const f32x2 p0 = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(u, 1.f, 0);
-              const f32x2 p1 = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(u, 1.f, 1);
-              const f32x2 p2 = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(u, 1.f, 2);
-              const f32x2 p3 = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(u, 1.f, 3);
-              o[0] = pack_bf16x2(p0[0] * s, p0[1] * s);
-              o[1] = pack_bf16x2(p1[0] * s, p1[1] * s);
-              o[2] = pack_bf16x2(p2[0] * s, p2[1] * s);
-              o[3] = pack_bf16x2(p3[0] * s, p3[1] * s);
-            };
-            uint32_t o[8];
-            pairs(d.a, o);
-            pairs(d.b, o + 4);
-            w[nt][0] = __builtin_bit_cast(bf16x8, make_uint4(o[0], o[1], o[2], o[3]));
-            w[nt][1] = __builtin_bit_cast(bf16x8, make_uint4(o[4], o[5], o[6], o[7]));
-          } else {
-            uint32_t o[8];
-#pragma unroll
-            for (int i = 0; i < 8; ++i) {
-              const uint32_t at = perm(i < 4 ? d.a : d.b, copy, 0x0C0C0400u | ((4u + (i & 3)) << 8));
-              o[i] = *reinterpret_cast<const uint32_t *>(tab + at);
-            }
-            w[nt][0] = __builtin_bit_cast(bf16x8, make_uint4(o[0], o[1], o[2], o[3]));
-            w[nt][1] = __builtin_bit_cast(bf16x8, make_uint4(o[4], o[5], o[6], o[7]));
-            if constexpr (kDQ)
-              a[nt] = int8_code(kAl ? c.q[nt][0] >> (8 * blk) : c.q[nt][blk]) * __uint_as_float(c.s[nt][kAl ? 0 : blk]);
-            else
-              a[nt] = __uint_as_float(c.q[nt][blk]);
-          }
-        }
-#pragma unroll
-        for (int mt = 0; mt < kMT; ++mt) {
-          const uint4 *row = mine + h * kHalf + (mt * 16 + l16) * 16;
-          const bf16x8 x0 = __builtin_bit_cast(bf16x8, row[(8 * b + 2 * sg) ^ l16]);
-          const bf16x8 x1 = __builtin_bit_cast(bf16x8, row[(8 * b + 2 * sg + 1) ^ l16]);
-#pragma unroll
-          for (int nt = 0; nt < 2; ++nt) {
-            if constexpr (kFP4) {
-              acc[nt][mt] = mfma16x16x32(x0, w[nt][0], acc[nt][mt]);
-              acc[nt][mt] = mfma16x16x32(x1, w[nt][1], acc[nt][mt]);
-            } else {
-              f32x4 part = mfma16x16x32(x0, w[nt][0], f32x4{0.f, 0.f, 0.f, 0.f});
-              part = mfma16x16x32(x1, w[nt][1], part);
-#pragma unroll
-              for (int v = 0; v < 4; ++v) acc[nt][mt][v] += a[nt] * part[v];
-            }
-          }
-        }
+      d.w[nt][e] = __builtin_bit_cast(bf16x8, make_uint4(o[0], o[1], o[2], o[3]));
+      if (e == 0) {
+        if constexpr (kDQ)
+          d.a[nt] = int8_code(kAl ? c.q[nt][0] >> (8 * blk) : c.q[nt][blk]) * __uint_as_float(c.s[nt][kAl ? 0 : blk]);
+        else
+          d.a[nt] = __uint_as_float(c.q[nt][blk]);
       }
     }
+  };
+
+  // One step's blocks, a row tile at a time, in an order that keeps the LDS reads behind the products:
+  // while a row tile multiplies, the next one's X and a part of the next block's weights are read, and
+  // the tile before is scaled and added.
+  auto compute = [&](const Codes &c, const uint4 *sX) {
+    const uint4 *mine = sX + kw * kSlice;
+    constexpr int kAll = kBlk * kMT;
+    Block d[2];
+    bf16x8 x[2][2];
+    f32x4 part[2][2];
+    float scale[2][2];
+    auto load_x = [&](int i) {
+      const int blk = i / kMT, mt = i % kMT;
+      const uint4 *row = mine + (blk >> 1) * kHalf + (mt * 16 + l16) * 16;
+#pragma unroll
+      for (int e = 0; e < 2; ++e)
+        x[i & 1][e] = __builtin_bit_cast(bf16x8, row[(8 * (blk & 1) + 2 * sg + e) ^ l16]);
+    };
+    auto add = [&](int i) {
+#pragma unroll
+      for (int nt = 0; nt < 2; ++nt)
+#pragma unroll
+        for (int v = 0; v < 4; ++v) acc[nt][i % kMT][v] += scale[i & 1][nt] * part[i & 1][nt][v];
+    };
+#pragma unroll
+    for (int q = 0; q < 4; ++q) decode(c, 0, q, d[0]);
+    load_x(0);
+#pragma unroll
+    for (int i = 0; i < kAll; ++i) {
+      const int blk = i / kMT, mt = i % kMT;
+      const Block &now = d[blk & 1];
+      if (i + 1 < kAll) load_x(i + 1);
+#pragma unroll
+      for (int nt = 0; nt < 2; ++nt) {
+        scale[i & 1][nt] = now.a[nt];
+        if constexpr (kFP4)
+          acc[nt][mt] = mfma16x16x32(x[i & 1][0], now.w[nt][0], acc[nt][mt]);
+        else
+          part[i & 1][nt] = mfma16x16x32(x[i & 1][0], now.w[nt][0], f32x4{0.f, 0.f, 0.f, 0.f});
+      }
+#pragma unroll
+      for (int nt = 0; nt < 2; ++nt) {
+        f32x4 &to = kFP4 ? acc[nt][mt] : part[i & 1][nt];
+        to = mfma16x16x32(x[i & 1][1], now.w[nt][1], to);
+      }
+      if (!kFP4 && i > 0) add(i - 1);
+      if (blk + 1 < kBlk) {
+#pragma unroll
+        for (int q = 0; q < 4; ++q)
+          if (q * kMT / 4 == mt) decode(c, blk + 1, q, d[(blk + 1) & 1]);
+      }
+      __builtin_amdgcn_sched_barrier(0);
+    }
+    if (!kFP4) add(kAll - 1);
   };
 
   // Step it: wait for its X and codes (requested two steps ago; those of the next step stay in flight),
@@ -502,42 +521,38 @@ void launch_fmt(const MidArgs &a, const MultiArgs &mu, unsigned grid, hipStream_
     mid_kernel<0, kMT, kNW, kBlk, kAl><<<dim3(grid), dim3(kThreads), 0, st>>>(a, mu);
 }
 
-// The split of a launch: rows of a workgroup (up to 8 row tiles of 16; as many for every row block as
-// the rows need), waves side by side, blocks of a step (what the LDS holds three times beside the
-// table) and splits of the reduction.
+// The split of a launch: rows of a workgroup (up to 8 row tiles of 16), waves side by side, blocks of a
+// step (what the LDS holds three times beside the table) and splits of the reduction. Of all of them the
+// least of (rounds of 256 workgroups) x (start and end of one, and its steps) plus the traffic of the
+// float32 sums, in us, with the times measured for 16 to 128 rows. With one row tile T's workgroups
+// count as well: in a second round they made 1 to 12 rows x 4096 x 4096 1.1 to 1.6 us slower (with
+// more rows most of them have no row to start from).
 struct MidShape {
   int mt, nw, blk, splits;
   bool al;
 };
 MidShape mid_shape(int64_t M, int64_t N, int64_t K) {
-  MidShape s;
-  const int64_t t = (M + 15) / 16;
-  const int64_t row_blocks = (t + 7) / 8;
-  s.mt = (int)((t + row_blocks - 1) / row_blocks);
-  s.blk = s.mt <= 4 ? 4 : 2;
-  s.al = K % (64 * s.blk) == 0;
-  if (!s.al) s.mt = s.mt <= 2 ? s.mt : s.mt <= 4 ? 4 : 8;   // the other heights are built for aligned K only
-  s.nw = s.mt <= 2 ? 4 : 8;
-  const int64_t kw = 8 / s.nw;
-  const int64_t wgs = (M + 16 * s.mt - 1) / (16 * s.mt) * ((N + 32 * s.nw - 1) / (32 * s.nw));
-  const int64_t steps = (K / 64 + s.blk - 1) / s.blk;
-  // Splits: the least of (rounds of 256 workgroups) x (start and end of one, and its steps) plus the
-  // traffic of the float32 sums, in us, from the times measured for 16 to 128 rows.
-  // With one row tile T's workgroups count as well: in a second round they made 1 to 12 rows x 4096 x 4096
-  // 1.1 to 1.6 us slower (with more rows most of them have no row to start from).
-  const double per_step = 0.5 + 0.35 * s.mt * s.blk / 4;
-  const int64_t for_t = M <= 16 ? M * ((K + kTSlice - 1) / kTSlice) : 0;
-  double best = 0;
-  s.splits = 1;
-  for (int64_t sp = 1; sp <= 16 && sp * kw <= steps; ++sp) {
-    const int64_t rounds = (wgs * sp + for_t + 255) / 256, it = (steps + sp * kw - 1) / (sp * kw);
-    const double us = rounds * (4.0 + it * per_step) + sp * M * N * 8 / 4.0e6;
-    if (sp == 1 || us < best) {
-      best = us;
-      s.splits = (int)sp;
+  MidShape best{};
+  const int64_t t = (M + 15) / 16, for_t = M <= 16 ? M * ((K + kTSlice - 1) / kTSlice) : 0;
+  double least = 0;
+  for (int mt = 1; mt <= 8 && mt <= t; ++mt) {
+    const int64_t row_blocks = (t + mt - 1) / mt;
+    MidShape s{mt, mt <= 2 ? 4 : 8, mt <= 4 ? 4 : 2, 1, false};
+    s.al = K % (64 * s.blk) == 0;
+    const int64_t kw = 8 / s.nw, wgs = row_blocks * ((N + 32 * s.nw - 1) / (32 * s.nw));
+    const int64_t steps = (K / 64 + s.blk - 1) / s.blk;
+    const double per_step = s.blk * (0.3 + 0.13 * mt);
+    for (int64_t sp = 1; sp == 1 || (sp <= 16 && sp * kw <= steps); ++sp) {
+      const int64_t rounds = (wgs * sp + for_t + 255) / 256, it = (steps + sp * kw - 1) / (sp * kw);
+      const double us = rounds * (4.0 + it * per_step) + sp * M * N * 8 / 4.0e6;
+      if (best.mt == 0 || us < least) {
+        least = us;
+        best = s;
+        best.splits = (int)sp;
+      }
     }
   }
-  return s;
+  return best;
 }
 
 size_t up256(size_t x) { return (x + 255) & ~size_t(255); }
@@ -579,20 +594,19 @@ hipError_t launch_mid_fwd_multi(const GemmArgs &ga, const MultiArgs &mu, const u
     return hipErrorInvalidValue;
   const MidArgs a{ga.a_side, ga.w, ga.M, ga.C, ga.R, ga.out, part, s.splits, ga.t, tpart, tsplits, ra, T, (int)tiles, A, order};
   const unsigned grid = (unsigned)wgs;
-#define MID_AL(MT, NW, BLK) launch_fmt<MT, NW, BLK, true>(a, mu, grid, st)
-#define MID_ANY(MT, NW, BLK) s.al ? MID_AL(MT, NW, BLK) : launch_fmt<MT, NW, BLK, false>(a, mu, grid, st)
   switch (s.mt) {
-    case 1: MID_ANY(1, 4, 4); break;
-    case 2: MID_ANY(2, 4, 4); break;
-    case 3: MID_AL(3, 8, 4); break;
-    case 4: MID_ANY(4, 8, 4); break;
-    case 5: MID_AL(5, 8, 2); break;
-    case 6: MID_AL(6, 8, 2); break;
-    case 7: MID_AL(7, 8, 2); break;
-    default: MID_ANY(8, 8, 2); break;
+#define MID_CASE(MT, NW, BLK)                            \
+  case MT:                                               \
+    if (s.al)                                            \
+      launch_fmt<MT, NW, BLK, true>(a, mu, grid, st);    \
+    else                                                 \
+      launch_fmt<MT, NW, BLK, false>(a, mu, grid, st);   \
+    break;
+    MID_CASE(1, 4, 4) MID_CASE(2, 4, 4) MID_CASE(3, 8, 4) MID_CASE(4, 8, 4)
+    MID_CASE(5, 8, 2) MID_CASE(6, 8, 2) MID_CASE(7, 8, 2) MID_CASE(8, 8, 2)
+#undef MID_CASE
+    default: return hipErrorInvalidValue;
   }
-#undef MID_ANY
-#undef MID_AL
   hipError_t e = hipGetLastError();
   if (e != hipSuccess) return e;
   MultiArgs mf = mu;
