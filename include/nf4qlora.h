@@ -363,8 +363,9 @@ int qlora_moe_bwd_dev(const void *dY, const void *X, int64_t m, const int64_t *c
  * gradient but dX. Rows may come in any order. Layout: ids int32 [m]; A bf16 [L, r, k]; B bf16
  * [L, n, r]; s float32 [L]; all in device memory (nothing waits for it, so the calls can be captured
  * in a graph whose replays bring other ids). Adapters of a lower rank are padded with zeros.
- * The low-rank term is part of the fused launch of Y (dX); it is scaled by s[a] in float32. T and U
- * are rounded to bf16.
+ * The low-rank term is added to the float32 sums of Y (dX) and scaled by s[a] in float32. T and U are
+ * rounded to bf16 first, as the layer's are; the sums over the rows of a batch of at most 256 rows take
+ * them in float32.
  *
  * Bytes of device workspace of the forward and the backward. */
 size_t qlora_multi_fwd_workspace_bytes(int64_t m, int64_t n, int64_t k, int32_t r, int32_t L);
@@ -372,14 +373,16 @@ size_t qlora_multi_bwd_workspace_bytes(int64_t m, int64_t n, int64_t k, int32_t 
 
 /* Forward: Y bf16 [m, n] and T bf16 [m, r] (kept for the backward). Requires n % 8 == 0 and
  * 1 <= r <= 128. Errors: as qlora_fwd; NF4_EINVAL also for L or r out of range, a NULL or
- * misaligned ids, s or T (ids and s: 4-byte aligned). */
+ * misaligned ids, s or T (ids and s: 4-byte aligned); NF4_EUNSUPPORTED where X or Y takes more than
+ * 4293918720 bytes (the gathering copies have 32-bit offsets). */
 int qlora_multi_fwd(const void *X, int64_t m, const nf4_tensor *W, const void *A, const void *B,
                     const float *s, const int32_t *ids, int32_t L, int32_t r, void *Y, void *T, void *ws,
                     size_t ws_bytes, void *stream);
 
 /* Backward for dY bf16 [m, n]: dX bf16 [m, k] (skipped when NULL), dA bf16 [L, r, k], dB bf16
- * [L, n, r], zero for an adapter without rows; T from the forward or NULL (recomputed). Sums over
- * rows are float32, in an order that the ids alone fix. Non-finite dY: as qlora_bwd.
+ * [L, n, r], zero for an adapter without rows; T from the forward or NULL (recomputed; a batch of at
+ * most 256 rows recomputes it in any case, beside U in one launch, and does not read T). Sums over
+ * rows are float32, in an order that the ids and sizes alone fix. Non-finite dY: as qlora_bwd.
  * Errors: as qlora_multi_fwd. */
 int qlora_multi_bwd(const void *dY, const void *X, int64_t m, const nf4_tensor *W, const void *A,
                     const void *B, const float *s, const int32_t *ids, int32_t L, int32_t r, const void *T,
@@ -459,7 +462,8 @@ int distill_topk_bwd(const void *logits, int dtype, int64_t t, int64_t v, int64_
 
 /* Both in one pass over the logits, for a training step that knows each row's weight (its mask, over
  * the number of tokens): loss float32 [t] (unweighted; 0 for a row of weight 0, which is not read)
- * and dlogits for weight float32 [t] (NULL: every weight 1). */
+ * and dlogits for weight float32 [t] (NULL: every weight 1). The losses of rows that are read equal
+ * those of distill_topk_fwd bit for bit. */
 int distill_topk_step(const void *logits, int dtype, int64_t t, int64_t v, int64_t ld, const int32_t *idx,
                       const float *teacher, int32_t top, float tau, const float *weight, float *loss,
                       void *dlogits, int64_t ldd, void *stream);

@@ -651,7 +651,7 @@ def qlora_multi_fwd(X: torch.Tensor, q: NF4Tensor, A: torch.Tensor, B: torch.Ten
 def qlora_multi_bwd(dY: torch.Tensor, X: torch.Tensor, q: NF4Tensor, A: torch.Tensor, B: torch.Tensor,
                     s: torch.Tensor, ids: torch.Tensor, T: Optional[torch.Tensor], need_dx: bool = True):
     """(dX, dA, dB) of qlora_multi_fwd for dY [m, n]; dX is None when need_dx is False, T None is
-    recomputed. dA [L, r, k] and dB [L, n, r] are zero for an adapter without rows."""
+    recomputed (as it is for at most 256 rows in any case). dA [L, r, k] and dB [L, n, r] are zero for an adapter without rows."""
     m, L, r = _multi_args(X, q, A, B, s, ids)
     dev = X.device
     _is(dY, "dY", torch.bfloat16, (m, q.n), dev)

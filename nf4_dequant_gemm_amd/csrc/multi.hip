@@ -20,6 +20,7 @@ namespace {
 // the counts are scanned over adapters and waves, and each wave then places its rows in order. The
 // lanes of a 64-row piece are ranked within their adapter by ballots, one for each adapter in the
 // piece, so that LDS is read and written once a piece. A wave's ids are loaded eight pieces at a time.
+// Bound by latency (two passes over the ids, a scan, barriers): 64 to 4096 rows 7 to 8 us, 8192 rows 9 us.
 constexpr int kPlanThreads = 1024, kPlanWaves = kPlanThreads / 64, kPlanAhead = 8;
 
 // Padding of ranks: dst [rows][rp] = src [rows][r] and zeros.
@@ -297,7 +298,8 @@ __global__ __launch_bounds__(256) void multi_rows16_kernel(RowsArgs w, MultiPlan
 }
 
 // Blocks of at most 64 rows (one 16-row tile a wave): in- and p-tiles of 64 columns loaded two steps
-// ahead in whole 128-byte rows and staged in LDS, chunk c of row i at slot c ^ ((i >> 1) & 7).
+// ahead in whole 128-byte rows and staged in LDS, chunk c of row i at slot c ^ ((i >> 1) & 7). Bound by its
+// loads: 8192 rows of 4 adapters, r 64, 4096 columns 21 us (3.2 TB/s), 11008 columns 50 us (3.6 TB/s).
 __device__ __forceinline__ int swzm(int row, int c) { return row * 8 + (c ^ ((row >> 1) & 7)); }
 
 template <int TN>
@@ -447,7 +449,8 @@ __global__ void multi_rows_sum_kernel(RowsArgs w) {
 // one row to an adapter P's rounding to bf16 would be half the error of dA and dB.
 // Workgroup: 128 columns x all r ranks, in stages of 64 rows loaded two stages ahead, staged row-major
 // in LDS (rows padded by 32 bytes) and read with the transposing LDS load, which gives a lane 4
-// consecutive rows of one column: the MFMA operand with the rows as its reduction index.
+// consecutive rows of one column: the MFMA operand with the rows as its reduction index. dA and dB of 8192
+// rows of 4 adapters, r 64, 4096 and 11008 columns: 61 us (4 TB/s of X and dY) and 14 us to add the blocks.
 constexpr int kSumRows = 1024;
 constexpr int kRB = 64, kCB = 128, kQRow = kCB + 16;
 typedef __attribute__((ext_vector_type(4))) short s16x4;
