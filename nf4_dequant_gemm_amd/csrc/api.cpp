@@ -1041,12 +1041,12 @@ int qlora_bwd_dx(const void *dY, int64_t m, const nf4_tensor *W, const void *U, 
 namespace {
 
 // The kernel of a forward. Up to 16 rows: the stream kernel when its workgroups of 112 weight rows are
-// more than 128, half the CUs; below that the mid kernel splits the reduction instead (16 rows, k
-// 4096, r 16, whole call, stream / mid: n 4096 24.3 / 18.9 us, 11008 24.9 / 21.2, 14336 24.8 / 23.9,
-// 22016 25.4 / 27.5, 28672 27.1 / 31.9). More rows: the mid kernel while 256 x 256 tiles would fill at
-// most half the CUs, then the large one (k 4096, mid / large: 64 tiles 75 / 123 us, 128 tiles
-// 107 / 125, 172 tiles 179 / 128). Up to 256 rows have no table of the rows' order and always take
-// the small kernels.
+// more than 128, half the CUs; below that the mid kernel splits the reduction instead (16 rows, r 16,
+// whole call, stream / mid: k 4096, n 4096 23.9 / 14.8 us, 11008 25.4 / 19.6, 14336 25.5 / 23.1, 22016
+// 25.8 / 25.6, 28672 26.4 / 30.4; k 8192, n 8192 33.4 / 26.3, 14336 33.9 / 35.6). More rows: the mid kernel
+// while 256 x 256 tiles would fill at most half the CUs, then the large one (k 4096, mid / large: 86
+// tiles 108 / 126 us, 128 tiles 124 / 125, 129 tiles 139 / 124, 172 tiles 178 / 129). Up to 256 rows have
+// no table of the rows' order and always take the small kernels.
 enum class MultiKernel { kStream, kMid, kLarge };
 MultiKernel multi_kernel(int64_t m, const nf4_tensor *W, int32_t r) {
   if (stream16_shape(m, W) && r % 8 == 0 && W->n > 128 * 112) return MultiKernel::kStream;

@@ -648,7 +648,8 @@ int dx_multi_pieces(int64_t M, int64_t K, int64_t N) {
   const int64_t tiles = ((K + kT - 1) / kT) * ((M + kT - 1) / kT), steps = (N + kS - 1) / kS;
   double best = 0;
   int pieces = 1;
-  for (int64_t p = 1; p <= 64 && p <= steps; ++p) {
+  const int64_t most = M <= 16 * 65535 ? 64 : 1;   // the last launch's grid has a row for every 16 rows
+  for (int64_t p = 1; p <= most && p <= steps; ++p) {
     const double us = (double)((tiles * p + 255) / 256) * (12.0 + 2.2 * (double)((steps + p - 1) / p)) +
                       (p > 1 ? 5.0 + (double)(p * M * K) * 8 / 4.0e6 : 0.0);
     if (p == 1 || us < best) {

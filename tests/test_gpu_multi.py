@@ -93,6 +93,27 @@ def test_parity(lib, m, k, n, r, L, kind, fmt):
         check_close(name, f32(got), ref)
 
 
+# one shape for every row tile height that the split of the mid kernel chooses, K a multiple of its step and not
+TILES = [(37, 64, 14376), (69, 256, 8928), (53, 2176, 80), (64, 768, 240), (121, 576, 8800), (193, 256, 13616),
+         (333, 576, 120), (197, 1792, 80), (1258, 64, 4216), (864, 256, 6480), (410, 64, 14696), (609, 128, 9968),
+         (2219, 64, 3240), (2155, 128, 3288)]
+
+
+@pytest.mark.parametrize("fmt", ["nf4", "nf4f", "e2m1"])
+@pytest.mark.parametrize("m,k,n", TILES)
+def test_forward_of_every_height(lib, m, k, n, fmt):
+    say(f"multi height m={m} k={k} n={n} {fmt}")
+    r, L = 16, 5
+    X, W = wl.normal_bf16(1 + m, (m, k), 1.0), wl.normal_bf16(2 + m, (n, k), 0.02)
+    A, B = wl.normal_bf16(3 + m, (L, r, k), k ** -0.5), wl.normal_bf16(4 + m, (L, n, r), 0.1)
+    s, ids = wl.uniform_f32(6 + m, (L,), 0.25, 2.0), make_ids("mixed", m, L)
+    q, Wd = quantise(lib, W, fmt)
+    Yo, To = multi.forward(f32(X), Wd, f32(A), f32(B), s.numpy(), ids.numpy())
+    Y, T = lib.qlora_multi_fwd(*(t if t is q else t.to(DEV) for t in (X, q, A, B, s, ids)))
+    check_close("Y", f32(Y), Yo)
+    check_close("T", f32(T), To)
+
+
 @pytest.mark.parametrize("m", [7, 40, 300])
 def test_rows_do_not_touch_one_another(lib, m):
     """Infinities and NaN in one row of X, or in an adapter no row has, stay there."""

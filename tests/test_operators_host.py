@@ -41,6 +41,7 @@ def test_multi_refuses():
         for o in (dict(m=0), dict(L=0), dict(L=1025), dict(r=0), dict(r=129), dict(wsb=need - 1)):
             assert call(**o) == INVALID, o
         assert call(W=weight(n=60)) == UNSUPPORTED and call(W=weight(k=96)) == UNSUPPORTED
+        assert call(m=2 ** 24) == UNSUPPORTED               # X of 4 GiB: past the gathers' offsets
     assert bwd(dY=None) == INVALID and bwd(dX=ODD) == INVALID and bwd(T=ODD) == INVALID
 
 
