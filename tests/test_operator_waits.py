@@ -15,7 +15,7 @@ from tests.test_kernel_waits import check_step_pipeline, device_asm, kernels, ma
 
 def test_mid_kernel_step_waits(tmp_path):
     ks = {k: b for k, b in kernels(device_asm("mid.hip", str(tmp_path))).items() if "mid_kernel" in k}
-    assert len(ks) == 36     # 3 formats x (8 heights with K a multiple of the step, 4 without)
+    assert len(ks) == 48     # 3 formats x 8 heights x K a multiple of the step or not
     for name, body in ks.items():
         loops = main_loops(body)
         assert len(loops) == 1, name
