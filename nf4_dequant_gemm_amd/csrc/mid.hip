@@ -433,11 +433,14 @@ __global__ __launch_bounds__(kThreads) void mid_kernel(MidArgs g, MultiArgs mu) 
 // Y (or dX) from the float32 sums of the launch before, added in order, and the low-rank term, with T from
 // its own sums (written here, by the workgroups of the first columns) or T (U) from memory. One wave:
 // 16 rows, in the order of their adapters (perm, unless there is one row tile only), and kFinalTiles
-// 16-column tiles. It is bound by its chain of loads, so those of the first four splits are in flight
+// 16-column tiles. It is bound by its chain of loads, so those of the first splits are in flight
 // during the term. 200 rows of 64 adapters x 11008, two splits: 11.4 us for 22 MB and the factors; 14.4 us
 // with the rows in the batch's order (14 adapters to a row tile instead of 5).
 template <int kFinalTiles>
 __global__ __launch_bounds__(64) void mid_final_kernel(MidArgs g, MultiArgs mu) {
+  // splits and adapters whose loads are in flight together: fewer with 64 columns, where there are waves
+  // enough to hide them if the registers let them on (1000 rows x 8000, whole call, 119 -> 115 us)
+  constexpr int kAhead = kFinalTiles == 2 ? 4 : 2, kTogether = kAhead;
   const int lane = threadIdx.x, g16 = lane >> 4, l16 = lane & 15;
   const int64_t n0 = (int64_t)blockIdx.x * 16 * kFinalTiles;
   int64_t m = (int64_t)blockIdx.y * 16 + l16;
@@ -446,9 +449,9 @@ __global__ __launch_bounds__(64) void mid_final_kernel(MidArgs g, MultiArgs mu) 
   int id = have ? mu.ids[m] : -1;
   id = id >= 0 && id < mu.L ? id : -1;
   const f32x4 zero = {0.f, 0.f, 0.f, 0.f};
-  auto load = [&](int s0, f32x4 (&v)[4][kFinalTiles]) {   // four splits
+  auto load = [&](int s0, f32x4 (&v)[kAhead][kFinalTiles]) {   // kAhead splits
 #pragma unroll
-    for (int s = 0; s < 4; ++s)
+    for (int s = 0; s < kAhead; ++s)
 #pragma unroll
       for (int nt = 0; nt < kFinalTiles; ++nt) {
         const int64_t n = n0 + nt * 16 + 4 * g16;
@@ -457,11 +460,11 @@ __global__ __launch_bounds__(64) void mid_final_kernel(MidArgs g, MultiArgs mu) 
                        : zero;
       }
   };
-  f32x4 v[4][kFinalTiles], y[kFinalTiles], term[kFinalTiles];
+  f32x4 v[kAhead][kFinalTiles], y[kFinalTiles], term[kFinalTiles];
   load(0, v);
 #pragma unroll
   for (int nt = 0; nt < kFinalTiles; ++nt) y[nt] = term[nt] = zero;
-  multi_term_rows<4>(term, mu, id, n0, g.N, [&](int j) {
+  multi_term_rows<kTogether>(term, mu, id, n0, g.N, [&](int j) {
     const bool mine = have && j < mu.r;
     if (!g.tsplits)
       return __builtin_bit_cast(bf16x8, mine ? *reinterpret_cast<const u32x4 *>(mu.P + m * mu.r + j) : u32x4{0u, 0u, 0u, 0u});
@@ -491,10 +494,10 @@ __global__ __launch_bounds__(64) void mid_final_kernel(MidArgs g, MultiArgs mu) 
   });
   for (int s0 = 0;;) {
 #pragma unroll
-    for (int s = 0; s < 4; ++s)
+    for (int s = 0; s < kAhead; ++s)
 #pragma unroll
       for (int nt = 0; nt < kFinalTiles; ++nt) y[nt] += v[s][nt];
-    s0 += 4;
+    s0 += kAhead;
     if (s0 >= g.splits) break;
     load(s0, v);
   }
