@@ -534,7 +534,8 @@ void launch_fmt(const MidArgs &a, const MultiArgs &mu, unsigned grid, hipStream_
 // least of (rounds of 256 workgroups) x (start and end of one, and its steps) plus the traffic of the
 // float32 sums, in us, with the times measured for 16 to 128 rows. With one row tile T's workgroups
 // count as well: in a second round they made 1 to 12 rows x 4096 x 4096 1.1 to 1.6 us slower (with
-// more rows most of them have no row to start from).
+// more rows most of them have no row to start from, and a few idle CUs are enough: where there are none
+// 128 rows x 8192 x 4096 took 40.6 us instead of 37.7).
 struct MidShape {
   int mt, nw, blk, splits;
   bool al;
@@ -552,7 +553,8 @@ MidShape mid_shape(int64_t M, int64_t N, int64_t K) {
     const double per_step = s.blk * (0.3 + 0.13 * mt);
     for (int64_t sp = 1; sp == 1 || (sp <= 16 && sp * kw <= steps); ++sp) {
       const int64_t rounds = (wgs * sp + for_t + 255) / 256, it = (steps + sp * kw - 1) / (sp * kw);
-      const double us = rounds * (4.0 + it * per_step) + sp * M * N * 8 / 4.0e6;
+      const bool full = M > 16 && M <= kMultiSmallM && rounds * 256 - wgs * sp < 16;
+      const double us = rounds * (4.0 + it * per_step) + sp * M * N * 8 / 4.0e6 + (full ? 5.0 : 0.0);
       if (best.mt == 0 || us < least) {
         least = us;
         best = s;

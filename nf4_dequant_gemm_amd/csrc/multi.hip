@@ -39,53 +39,63 @@ __device__ __forceinline__ void pad_rows(const PadArgs &p, int64_t i0, int64_t s
 }
 
 // dst[a][c][j] = src[a][j][c] of the bf16 matrices [R][C] of an adapter a that has rows (nobody reads the
-// others), through 64 x 64 LDS tiles, four to a workgroup; the rows of dst have ldd elements (a multiple
-// of 8), zeros from R on. 16-byte loads where C % 8 == 0, 16-byte stores.
+// others), through LDS tiles of 4096 elements, four to a workgroup; the rows of dst have ldd elements (a
+// multiple of 8), zeros from R on. 16-byte loads where C % 8 == 0, 16-byte stores. A tile is as wide as
+// the rank (8, 16, 32 or 64) and takes more of the long side instead: square ones left 60 adapters of rank 8
+// x 4096 seven eighths empty and took 18 us; 8 x 8 elements a thread in registers, without LDS, were
+// 4 to 26 us slower (scattered 16-byte loads of few workgroups).
 struct TransposeArgs {
   const uint16_t *src;
   uint16_t *dst;
   int64_t R, C, ldd;
-  __host__ __device__ int64_t tiles() const { return (C + 63) / 64 * ((ldd + 63) / 64); }
-  __host__ __device__ int64_t blocks() const { return src ? (tiles() + 3) / 4 : 0; }
+  int lr, lc;   // log2 of a tile's rows and columns: lr + lc = 12, each at least 3
+  __host__ __device__ int64_t tiles_r() const { return (ldd + (1 << lr) - 1) >> lr; }
+  __host__ __device__ int64_t tiles_c() const { return (C + (1 << lc) - 1) >> lc; }
+  __host__ __device__ int64_t blocks() const { return src ? (tiles_r() * tiles_c() + 3) / 4 : 0; }
 };
+constexpr int kTileLds = 4096 + 512;   // its columns, each padded by one (an even stride: 16 lanes on a bank)
+// log2 of a tile's extent along ranks
+int rank_log(int r) { return r <= 8 ? 3 : r <= 16 ? 4 : r <= 32 ? 5 : 6; }
 // Rows that are looked through for an adapter's use; one that they do not show in a longer batch is
 // transposed unused.
 constexpr int64_t kUseRows = 8192;
 __device__ __forceinline__ void transpose_tiles(const TransposeArgs &g, const int32_t *ids, int64_t M, int a,
-                                                int64_t block, uint16_t (&lds)[4][64][66]) {
+                                                int64_t block, uint16_t (&lds)[4][kTileLds]) {
   bool used = M > kUseRows;
   for (int64_t i0 = threadIdx.x; i0 < M && i0 < kUseRows; i0 += kPlanThreads) used |= ids[i0] == a;
   if (!__syncthreads_or(used)) return;
-  const int tid = threadIdx.x & 255;
-  const int64_t tile = block * 4 + (threadIdx.x >> 8), tiles_c = (g.C + 63) / 64;
-  const int64_t c0 = tile % tiles_c * 64, r0 = tile / tiles_c * 64;
-  const bool mine = tile < g.tiles();
-  auto &t = lds[threadIdx.x >> 8];   // [c][r]
+  const int tid = threadIdx.x & 255, stride = (1 << g.lr) + 1;
+  const int64_t tile = block * 4 + (threadIdx.x >> 8), tiles_c = g.tiles_c();
+  const int64_t c0 = (tile % tiles_c) << g.lc, r0 = (tile / tiles_c) << g.lr;
+  const bool mine = r0 < g.ldd;
+  uint16_t *t = lds[threadIdx.x >> 8];   // [c][r]
   const uint16_t *src = g.src + (int64_t)a * g.R * g.C;
   uint16_t *dst = g.dst + (int64_t)a * g.ldd * g.C;
   if (!mine) {
   } else if ((g.C & 7) == 0) {
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
-      const int r = (tid >> 3) + 32 * h, c = (tid & 7) * 8;
+      const int q = tid + 256 * h, r = q >> (g.lc - 3), c = (q & ((1 << (g.lc - 3)) - 1)) * 8;
       u32x4 v = {0u, 0u, 0u, 0u};
       if (r0 + r < g.R && c0 + c < g.C) v = *reinterpret_cast<const u32x4 *>(src + (r0 + r) * g.C + c0 + c);
 #pragma unroll
-      for (int e = 0; e < 8; ++e) t[c + e][r] = (uint16_t)(v[e >> 1] >> (16 * (e & 1)));
+      for (int e = 0; e < 8; ++e) t[(c + e) * stride + r] = (uint16_t)(v[e >> 1] >> (16 * (e & 1)));
     }
   } else {
-    const int x = tid & 63;
-    for (int r = tid >> 6; r < 64; r += 4)
-      t[x][r] = r0 + r < g.R && c0 + x < g.C ? src[(r0 + r) * g.C + c0 + x] : (uint16_t)0;
+#pragma unroll
+    for (int h = 0; h < 16; ++h) {
+      const int q = tid + 256 * h, r = q >> g.lc, c = q & ((1 << g.lc) - 1);
+      t[c * stride + r] = r0 + r < g.R && c0 + c < g.C ? src[(r0 + r) * g.C + c0 + c] : (uint16_t)0;
+    }
   }
   __syncthreads();
 #pragma unroll
   for (int h = 0; h < 2; ++h) {
-    const int c = (tid >> 3) + 32 * h, r = (tid & 7) * 8;
+    const int q = tid + 256 * h, c = q >> (g.lr - 3), r = (q & ((1 << (g.lr - 3)) - 1)) * 8;
     if (!mine || c0 + c >= g.C || r0 + r >= g.ldd) continue;
     u32x4 v;
 #pragma unroll
-    for (int e = 0; e < 4; ++e) v[e] = t[c][r + 2 * e] | ((uint32_t)t[c][r + 2 * e + 1] << 16);
+    for (int e = 0; e < 4; ++e) v[e] = t[c * stride + r + 2 * e] | ((uint32_t)t[c * stride + r + 2 * e + 1] << 16);
     *reinterpret_cast<u32x4 *>(dst + (c0 + c) * g.ldd + r0 + r) = v;
   }
 }
@@ -101,7 +111,7 @@ __global__ __launch_bounds__(kPlanThreads) void multi_plan_kernel(const int32_t 
                                                                   int L, MultiPlan pl, PlanWork work) {
   extern __shared__ int32_t cnt[];   // [kPlanWaves][L + 1]
   __shared__ int32_t scan[kMultiTables][kPlanThreads];
-  __shared__ __align__(16) uint16_t tile[4][64][66];
+  __shared__ __align__(16) uint16_t tile[4][kTileLds];
   const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
   if (blockIdx.x > 0) {
     int64_t b = (int64_t)blockIdx.x - 1;
@@ -447,7 +457,7 @@ __global__ void multi_rows_sum_kernel(RowsArgs w) {
 // the rows. At most kMultiSmallM rows (kSmall): a block is an adapter, which writes its zeros too, and P
 // is float32, taken as the sum of two bf16 numbers (16 bits of mantissa): the products are few, and with
 // one row to an adapter P's rounding to bf16 would be half the error of dA and dB.
-// Workgroup: 128 columns x all r ranks, in stages of 64 rows loaded two stages ahead, staged row-major
+// Workgroup: 128 columns x all r ranks, in stages of kR = 64 rows loaded two stages ahead, staged row-major
 // in LDS (rows padded by 32 bytes) and read with the transposing LDS load, which gives a lane 4
 // consecutive rows of one column: the MFMA operand with the rows as its reduction index. dA and dB of 8192
 // rows of 4 adapters, r 64, 4096 and 11008 columns: 61 us (4 TB/s of X and dY) and 14 us to add the blocks.
@@ -466,16 +476,17 @@ struct SumArgs {
   int r, rp, L;
 };
 
-template <int TJ, bool kSmall>
+template <int TJ, bool kSmall, int kR>
 __global__ __launch_bounds__(256) void multi_sum_kernel(SumArgs w, MultiPlan pl) {
   constexpr int PROW = TJ * 16 + 16, kParts = kSmall ? 2 : 1;
-  __shared__ __align__(16) uint16_t sQ[2][kRB * kQRow];
-  __shared__ __align__(16) uint16_t sP[2][kParts][kRB * PROW];
+  constexpr int kPI = (kR * 2 * TJ + 255) / 256;   // 8-rank pieces of a thread
+  __shared__ __align__(16) uint16_t sQ[2][kR * kQRow];
+  __shared__ __align__(16) uint16_t sP[2][kParts][kR * PROW];
   const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6, r = w.r;
   const MultiSum g = blockIdx.z ? w.g[1] : w.g[0];
   const int64_t c0 = (int64_t)blockIdx.x * kCB, C = g.c;
   if (c0 >= C) return;
-  __shared__ int32_t srow[kSumRows];
+  __shared__ int32_t srow[kSmall ? kMultiSmallM : kSumRows];
   int a = blockIdx.y, nb = 1;
   int32_t lo, me;   // first row of this block, and its rows
   if constexpr (kSmall) {
@@ -499,12 +510,12 @@ __global__ __launch_bounds__(256) void multi_sum_kernel(SumArgs w, MultiPlan pl)
 #pragma unroll
     for (int u = 0; u < 2; ++u) acc[t][u] = f32x4{0.f, 0.f, 0.f, 0.f};
   struct Stage {
-    uint4 q[4];
-    uint4 p[(TJ + 1) / 2][kParts];   // 8 ranks, in bf16 or float32
+    uint4 q[kR / 16];
+    uint4 p[kPI][kParts];   // 8 ranks, in bf16 or float32
   };
   auto load = [&](int32_t ms, Stage &st) {
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
+    for (int i = 0; i < kR / 16; ++i) {
       const int q = tid + 256 * i;
       const int32_t m = ms + (q >> 4);
       const int64_t c = c0 + (q & 15) * 8;
@@ -512,10 +523,10 @@ __global__ __launch_bounds__(256) void multi_sum_kernel(SumArgs w, MultiPlan pl)
                                   : make_uint4(0, 0, 0, 0);
     }
 #pragma unroll
-    for (int i = 0; i < (TJ + 1) / 2; ++i) {
+    for (int i = 0; i < kPI; ++i) {
       const int q = tid + 256 * i, row = q / (2 * TJ), j = q % (2 * TJ) * 8;
       const int32_t m = ms + row;
-      const bool have = row < kRB && m < me && j < r;
+      const bool have = row < kR && m < me && j < r;
 #pragma unroll
       for (int e = 0; e < kParts; ++e)
         st.p[i][e] = have ? *(reinterpret_cast<const uint4 *>((const uint16_t *)g.p + ((int64_t)srow[m] * w.rp + j) * kParts) + e)
@@ -524,14 +535,14 @@ __global__ __launch_bounds__(256) void multi_sum_kernel(SumArgs w, MultiPlan pl)
   };
   auto store = [&](const Stage &st, int buf) {
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
+    for (int i = 0; i < kR / 16; ++i) {
       const int q = tid + 256 * i;
       *reinterpret_cast<uint4 *>(&sQ[buf][(q >> 4) * kQRow + (q & 15) * 8]) = st.q[i];
     }
 #pragma unroll
-    for (int i = 0; i < (TJ + 1) / 2; ++i) {
+    for (int i = 0; i < kPI; ++i) {
       const int q = tid + 256 * i, row = q / (2 * TJ);
-      if (row >= kRB) continue;
+      if (row >= kR) continue;
       uint16_t *at = &sP[buf][0][row * PROW + q % (2 * TJ) * 8];
       if constexpr (kSmall) {
         const float *v = reinterpret_cast<const float *>(&st.p[i][0]);
@@ -544,7 +555,7 @@ __global__ __launch_bounds__(256) void multi_sum_kernel(SumArgs w, MultiPlan pl)
           rest[e] = pack_bf16x2(fabsf(x) < INFINITY ? v[2 * e] - x : 0.f, fabsf(y) < INFINITY ? v[2 * e + 1] - y : 0.f);
         }
         *reinterpret_cast<uint4 *>(at) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
-        *reinterpret_cast<uint4 *>(at + kRB * PROW) = make_uint4(rest[0], rest[1], rest[2], rest[3]);
+        *reinterpret_cast<uint4 *>(at + kR * PROW) = make_uint4(rest[0], rest[1], rest[2], rest[3]);
       } else {
         *reinterpret_cast<uint4 *>(at) = st.p[i][0];
       }
@@ -559,7 +570,7 @@ __global__ __launch_bounds__(256) void multi_sum_kernel(SumArgs w, MultiPlan pl)
   };
   auto mma = [&](int buf) {
 #pragma unroll
-    for (int ks = 0; ks < 2; ++ks) {
+    for (int ks = 0; ks < kR / 32; ++ks) {
       bf16x8 q[2];
 #pragma unroll
       for (int u = 0; u < 2; ++u) q[u] = frag(sQ[buf], kQRow, wave * 32 + u * 16, ks);
@@ -580,20 +591,20 @@ __global__ __launch_bounds__(256) void multi_sum_kernel(SumArgs w, MultiPlan pl)
       }
     }
   };
-  const int nst = (me + kRB - 1) / kRB;
+  const int nst = (me + kR - 1) / kR;
   Stage s0, s1;
   if (nst > 0) load(0, s0);
-  if (nst > 1) load(kRB, s1);
+  if (nst > 1) load(kR, s1);
   if (nst > 0) store(s0, 0);
   __syncthreads();
 #pragma unroll 1
   for (int i = 0; i < nst; i += 2) {
-    if (i + 2 < nst) load((i + 2) * kRB, s0);
+    if (i + 2 < nst) load((i + 2) * kR, s0);
     mma(0);
     if (i + 1 < nst) store(s1, 1);
     __syncthreads();
     if (i + 1 >= nst) break;
-    if (i + 3 < nst) load((i + 3) * kRB, s1);
+    if (i + 3 < nst) load((i + 3) * kR, s1);
     mma(1);
     if (i + 2 < nst) store(s0, 0);
     __syncthreads();
@@ -675,8 +686,9 @@ hipError_t launch_multi_plan(const int32_t *ids, int64_t M, int L, const MultiPl
   w.pad_blocks = (int)(pads < 1024 ? pads : 1024);
   if (f.Bt) {
     if (f.rp < f.r || (f.rp & 7) != 0 || (f.n & 7) != 0) return hipErrorInvalidValue;
-    w.tr[0] = TransposeArgs{f.B, f.Bt, f.n, f.r, f.n};
-    if (f.At) w.tr[1] = TransposeArgs{f.A, f.At, f.r, f.k, f.rp};
+    const int lr = rank_log(f.r);
+    w.tr[0] = TransposeArgs{f.B, f.Bt, f.n, f.r, f.n, 12 - lr, lr};
+    if (f.At) w.tr[1] = TransposeArgs{f.A, f.At, f.r, f.k, f.rp, lr, 12 - lr};
   }
   const int64_t blocks = 1 + w.pad_blocks + (w.tr[0].blocks() + w.tr[1].blocks()) * L;
   if (blocks >= (int64_t(1) << 32) / kPlanThreads) return hipErrorInvalidValue;
@@ -755,7 +767,10 @@ int64_t multi_sum_blocks(int64_t M, int64_t c0, int64_t c1, int L) {
 hipError_t launch_multi_sums(const MultiSum &a, const MultiSum &b, int64_t M, int r, int rp, int L, const float *s,
                              const MultiPlan &pl, hipStream_t st) {
   const SumArgs w{{a, b}, s, r, rp, L};
-  const bool small = M <= kMultiSmallM;
+  // Stages of 32 rows let more of the workgroups of many adapters with few rows share a CU (forward and
+  // backward of 255 rows of 60 adapters, 4096 x 4096: 125 -> 111 us); an adapter of many rows then takes twice
+  // the steps (250 rows of one: 100 -> 108 us).
+  const bool small = M <= kMultiSmallM, few = small && M <= 32 * (int64_t)L;
   const int64_t most = std::max(a.c, b.c), tiles = (most + kCB - 1) / kCB;
   const int64_t blocks = small ? L : multi_sum_blocks(M, a.c, b.c, L);
   if (rp < r || (rp & 7) != 0 || ((a.c | b.c) & 7) != 0 || pl.rows[kPlanSum] != multi_sum_rows(M, a.c, b.c) || blocks > 65535)
@@ -764,10 +779,12 @@ hipError_t launch_multi_sums(const MultiSum &a, const MultiSum &b, int64_t M, in
   switch ((r + 15) / 16) {
 #define MS_CASE(T)                                                       \
   case T:                                                                \
-    if (small)                                                           \
-      multi_sum_kernel<T, true><<<grid, dim3(256), 0, st>>>(w, pl);      \
+    if (few)                                                             \
+      multi_sum_kernel<T, true, 32><<<grid, dim3(256), 0, st>>>(w, pl);  \
+    else if (small)                                                      \
+      multi_sum_kernel<T, true, kRB><<<grid, dim3(256), 0, st>>>(w, pl); \
     else                                                                 \
-      multi_sum_kernel<T, false><<<grid, dim3(256), 0, st>>>(w, pl);     \
+      multi_sum_kernel<T, false, kRB><<<grid, dim3(256), 0, st>>>(w, pl);\
     break;
     MS_CASE(1) MS_CASE(2) MS_CASE(3) MS_CASE(4) MS_CASE(5) MS_CASE(6) MS_CASE(7) MS_CASE(8)
 #undef MS_CASE
