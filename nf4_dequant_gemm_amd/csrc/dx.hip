@@ -164,8 +164,10 @@ __device__ __forceinline__ void dx_origin(int64_t m_lo, int64_t m_hi, int tiles_
 // the low-rank term of its block from the transposed adapters, straight from registers (multi_term,
 // multi.h). kSplit: a workgroup runs one of mu.pieces parts of the reduction and leaves its float32 sums
 // in mu.part (a kernel of its own: both endings in one spilled 120 registers and cost 100 us of 670).
-// 8192 x 11008 x 4096, 4 adapters of rank 64: 681 us; split, 64 x 11008 x 4096: 29 us (380 us unsplit).
-template <int kFmt, bool kGrp, bool kMulti = false, bool kSplit = false>
+// kMT: row tiles of 16 that a wave multiplies, fewer than 8 where the launch has at most 32 kMT rows.
+// 8192 x 11008 x 4096, 4 adapters of rank 64: 676 us; split, 64 x 11008 x 4096: 23 us (29 us with 8 row tiles,
+// 380 us unsplit).
+template <int kFmt, bool kGrp, bool kMulti = false, bool kSplit = false, int kMT = 8>
 __device__ __forceinline__ void dx_body(const GemmArgs &g, const GroupArgs &gr, const MultiArgs &mu) {
   constexpr bool kDQ = kFmt == 1, kFP4 = kFmt == 2;
   // separate LDS arrays per buffer: the compiler then knows that accesses to one do not alias
@@ -282,11 +284,12 @@ __device__ __forceinline__ void dx_body(const GemmArgs &g, const GroupArgs &gr, 
                              : (uint32_t)(wr * kblk + (kvalid ? kcol / 64 : 0));
   const uint32_t qstep = kFP4 ? (uint32_t)(kS * (K / 16)) : (uint32_t)(kS * kblk);
 
-  f32x4 acc[4][8];   // [k-tile][m-tile]
+  static_assert(kMT == 8 || kSplit, "the other endings have 8 row tiles");
+  f32x4 acc[4][kMT];   // [k-tile][m-tile]
 #pragma unroll
   for (int a = 0; a < 4; ++a)
 #pragma unroll
-    for (int b = 0; b < 8; ++b) acc[a][b] = f32x4{0.f, 0.f, 0.f, 0.f};
+    for (int b = 0; b < kMT; ++b) acc[a][b] = f32x4{0.f, 0.f, 0.f, 0.f};
 
   auto dma_y = [&](int s, uint4 *sA) {
 #pragma unroll
@@ -345,7 +348,7 @@ __device__ __forceinline__ void dx_body(const GemmArgs &g, const GroupArgs &gr, 
     return __builtin_bit_cast(bf16x8, v);
   };
   auto yfrag = [&](const uint4 *sA, int ks, int mt) {
-    return __builtin_bit_cast(bf16x8, sA[swzd(wm * 128 + mt * 16 + l16, ks * 4 + g16)]);
+    return __builtin_bit_cast(bf16x8, sA[swzd(wm * 16 * kMT + mt * 16 + l16, ks * 4 + g16)]);
   };
   // Plain MFMA pass over k-slice ks of one step (used for the LoRA steps).
   auto mma = [&](const uint4 *sA, const uint16_t *sW, int ks) {
@@ -353,7 +356,7 @@ __device__ __forceinline__ void dx_body(const GemmArgs &g, const GroupArgs &gr, 
 #pragma unroll
     for (int kt = 0; kt < 4; ++kt) aw[kt] = wfrag(sW, ks, kt);
 #pragma unroll
-    for (int mt = 0; mt < 8; ++mt) {
+    for (int mt = 0; mt < kMT; ++mt) {
       const bf16x8 b = yfrag(sA, ks, mt);
 #pragma unroll
       for (int kt = 0; kt < 4; ++kt) acc[kt][mt] = mfma16x16x32(aw[kt], b, acc[kt][mt]);
@@ -390,9 +393,12 @@ __device__ __forceinline__ void dx_body(const GemmArgs &g, const GroupArgs &gr, 
 #pragma unroll
         for (int kt = 0; kt < 4; ++kt) aw[kt] = wfrag(W, 1, kt);
       }
-      if (grp + 1 < 16) yb[(grp + 1) & 1] = yfrag(Y, (grp + 1) >> 3, (grp + 1) & 7);
+      if (mt < kMT) {
+        const int at = ks * kMT + mt;
+        if (at + 1 < 2 * kMT) yb[(at + 1) & 1] = yfrag(Y, (at + 1) / kMT, (at + 1) % kMT);
 #pragma unroll
-      for (int kt = 0; kt < 4; ++kt) acc[kt][mt] = mfma16x16x32(aw[kt], yb[grp & 1], acc[kt][mt]);
+        for (int kt = 0; kt < 4; ++kt) acc[kt][mt] = mfma16x16x32(aw[kt], yb[at & 1], acc[kt][mt]);
+      }
       // decode of step s+1: table in groups 0..3, then word j = (grp - 4) / 3 in pieces over
       // three groups (pieces 0-1, 2-3, 4 + store)
       if (kFP4 && grp < 4) {
@@ -476,7 +482,7 @@ __device__ __forceinline__ void dx_body(const GemmArgs &g, const GroupArgs &gr, 
 #pragma unroll
     for (int kt = 0; kt < 4; ++kt)
 #pragma unroll
-      for (int mt = 0; mt < 8; ++mt) pp[(kt * 8 + mt) * 64] = acc[kt][mt];
+      for (int mt = 0; mt < kMT; ++mt) pp[(kt * 8 + mt) * 64] = acc[kt][mt];
     return;
   }
 
@@ -484,8 +490,8 @@ __device__ __forceinline__ void dx_body(const GemmArgs &g, const GroupArgs &gr, 
   if constexpr (kSplit) {
     const float tsc = kFP4 ? tscale() : 1.f;
 #pragma unroll
-    for (int mt = 0; mt < 8; ++mt) {
-      const int64_t m = m0 + wm * 128 + mt * 16 + l16;
+    for (int mt = 0; mt < kMT; ++mt) {
+      const int64_t m = m0 + wm * 16 * kMT + mt * 16 + l16;
       if (m >= m_hi) continue;
       float *row = mu.part + ((int64_t)piece * g.M + mu.perm[m]) * g.C;
 #pragma unroll
@@ -512,7 +518,7 @@ __device__ __forceinline__ void dx_body(const GemmArgs &g, const GroupArgs &gr, 
 #pragma unroll
         for (int kt = 0; kt < 4; ++kt)
 #pragma unroll
-          for (int mt = 0; mt < 8; ++mt) acc[kt][mt] *= tsc;
+          for (int mt = 0; mt < kMT; ++mt) acc[kt][mt] *= tsc;
         tsc = 1.f;
       }
       multi_term<4, 8>(acc, mu, mu.perm, m0 + wm * 128, m_hi, k0 + wk * 64, g.C);
@@ -520,7 +526,7 @@ __device__ __forceinline__ void dx_body(const GemmArgs &g, const GroupArgs &gr, 
 #pragma unroll
     for (int kt = 0; kt < 4; ++kt)
 #pragma unroll
-      for (int mt = 0; mt < 8; ++mt)
+      for (int mt = 0; mt < kMT; ++mt)
         b2[swzd(mt * 16 + l16, 2 * kt + (g16 >> 1)) * 2 + (g16 & 1)] =
             kFP4 ? make_uint2(pack_bf16x2(tsc * acc[kt][mt][0], tsc * acc[kt][mt][1]),
                               pack_bf16x2(tsc * acc[kt][mt][2], tsc * acc[kt][mt][3]))
@@ -555,9 +561,18 @@ template <int kFmt>
 __global__ __launch_bounds__(kThreads) void dx_multi_kernel(GemmArgs g, MultiArgs mu) {
   dx_body<kFmt, false, true>(g, GroupArgs{}, mu);
 }
-template <int kFmt>
+template <int kFmt, int kMT>
 __global__ __launch_bounds__(kThreads) void dx_split_kernel(GemmArgs g, MultiArgs mu) {
-  dx_body<kFmt, false, true, true>(g, GroupArgs{}, mu);
+  dx_body<kFmt, false, true, true, kMT>(g, GroupArgs{}, mu);
+}
+template <int kFmt>
+void launch_split(const GemmArgs &g, const MultiArgs &mu, unsigned grid, hipStream_t st) {
+  if (g.M <= 64)
+    dx_split_kernel<kFmt, 2><<<dim3(grid), dim3(kThreads), 0, st>>>(g, mu);
+  else if (g.M <= 128)
+    dx_split_kernel<kFmt, 4><<<dim3(grid), dim3(kThreads), 0, st>>>(g, mu);
+  else
+    dx_split_kernel<kFmt, 8><<<dim3(grid), dim3(kThreads), 0, st>>>(g, mu);
 }
 
 // The split tiles of a grouped dX launch: workgroups 4 i .. 4 i + 3 add the S float32 pieces of
@@ -667,11 +682,11 @@ hipError_t launch_gemm_dx_multi(const GemmArgs &g, const MultiArgs &mu, hipStrea
   const int64_t tiles = ((g.C + kT - 1) / kT) * ((g.M + kT - 1) / kT) * mu.pieces;
   if (mu.pieces > 1) {
     if (g.w.fp4)
-      dx_split_kernel<2><<<dim3((unsigned)tiles), dim3(kThreads), 0, st>>>(g, mu);
+      launch_split<2>(g, mu, (unsigned)tiles, st);
     else if (g.w.dq)
-      dx_split_kernel<1><<<dim3((unsigned)tiles), dim3(kThreads), 0, st>>>(g, mu);
+      launch_split<1>(g, mu, (unsigned)tiles, st);
     else
-      dx_split_kernel<0><<<dim3((unsigned)tiles), dim3(kThreads), 0, st>>>(g, mu);
+      launch_split<0>(g, mu, (unsigned)tiles, st);
     return hipGetLastError();
   }
   if (g.w.fp4)

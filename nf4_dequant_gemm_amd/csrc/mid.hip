@@ -30,8 +30,8 @@
 //
 // What bounds it: a step's matrix (37% of the time at 7 row tiles) and vector instructions (34%: two of
 // the three for each product scale and add a block's sums) take turns on a SIMD, and its LDS reads (40% of
-// the LDS's time) do not hide behind them completely. 200 rows x 4096 x 11008: 43 us, and 11 us for the
-// last launch; 1111 rows x 2880 x 2952 in E2M1: 35 and 16 us; one row x 4096 x 4096: 8.5 and 3.9 us.
+// the LDS's time) do not hide behind them completely. 200 rows x 4096 x 11008: 43 us, and 10 us for the
+// last launch; 1111 rows x 2880 x 2952 in E2M1: 35 and 15 us; one row x 4096 x 4096: 8.5 and 4.2 us.
 #include "common.h"
 #include "launch.h"
 #include "multi.h"
@@ -434,7 +434,7 @@ __global__ __launch_bounds__(kThreads) void mid_kernel(MidArgs g, MultiArgs mu) 
 // its own sums (written here, by the workgroups of the first columns) or T (U) from memory. One wave:
 // 16 rows, in the order of their adapters (perm, unless there is one row tile only), and kFinalTiles
 // 16-column tiles. It is bound by its chain of loads, so those of the first splits are in flight
-// during the term. 200 rows of 64 adapters x 11008, two splits: 11.4 us for 22 MB and the factors; 14.4 us
+// during the term. 200 rows of 64 adapters x 11008, two splits: 10.4 us for 22 MB and the factors; 14.4 us
 // with the rows in the batch's order (14 adapters to a row tile instead of 5).
 template <int kFinalTiles>
 __global__ __launch_bounds__(64) void mid_final_kernel(MidArgs g, MultiArgs mu) {
