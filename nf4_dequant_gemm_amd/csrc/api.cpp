@@ -1248,7 +1248,8 @@ int qlora_multi_bwd(const void *dY, const void *X, int64_t m, const nf4_tensor *
   const bool small = m <= nf4q::kMultiSmallM;
   // a small batch forms T again, beside U and in float32, whether it was passed or not
   const nf4q::MultiPad pad{!small && rp != r ? t : nullptr, m, r, rp, Tp};
-  hipError_t e = nf4q::launch_multi_plan(ids, m, L, pl, pad, nf4q::MultiFactors{b, n, a, k, r, rp, Bt, dX ? At : nullptr}, sm);
+  const nf4q::MultiFactors factors{b, n, a, k, r, rp, Bt, dX ? At : nullptr};
+  hipError_t e = nf4q::launch_multi_plan(ids, m, L, pl, pad, factors, sm);
   if (e != hipSuccess) return hip_status(e, "qlora_multi_bwd plan launch");
   nf4q::MultiRows u{dy, n, Bt, lay.sp_n, part, nullptr, U, nullptr}, tr{x, k, a, lay.sp_k, part, nullptr, Tp, nullptr};
   if (small) {

@@ -250,7 +250,8 @@ __device__ __forceinline__ void dx_body(const GemmArgs &g, const GroupArgs &gr, 
   };
   const int64_t nruns = (g.w.n * kblk + 255) / 256;
   const __amdgpu_buffer_rsrc_t rS = make_rsrc(g.w.scale, kDQ ? nruns * 4 : 0);
-  const __amdgpu_buffer_rsrc_t rY = kMulti ? make_rsrc(g.a_side, g.M * N * 2) : make_rsrc(g.a_side + m0 * N, rows_m * N * 2);
+  const __amdgpu_buffer_rsrc_t rY =
+      kMulti ? make_rsrc(g.a_side, g.M * N * 2) : make_rsrc(g.a_side + m0 * N, rows_m * N * 2);
 
   // dY DMA: instruction i of wave w fills the 1 KB of the tile holding rows 8 (4 w + i) .. +7;
   // lane L writes physical chunk L % 8 of row 8 (4 w + i) + L / 8, i.e. logical chunk

@@ -275,7 +275,8 @@ __device__ __forceinline__ void fwd_body(const GemmArgs &g, const GroupArgs &gr,
   const int rot = (int)(((m0 - m_lo) / kT) * 5 % kblk);
   auto phys = [&](int s) { return s + rot < kblk ? s + rot : s + rot - kblk; };
 
-  const __amdgpu_buffer_rsrc_t rX = kMulti ? make_rsrc(g.a_side, g.M * K * 2) : make_rsrc(g.a_side + m0 * K, rows_m * K * 2);
+  const __amdgpu_buffer_rsrc_t rX =
+      kMulti ? make_rsrc(g.a_side, g.M * K * 2) : make_rsrc(g.a_side + m0 * K, rows_m * K * 2);
   // pair: the buffers span the whole stacked weight, rows addressed per thread (rows past N read
   // as zero through out-of-range offsets)
   const int64_t wrows = kPair ? 2 * g.C : rows_n;

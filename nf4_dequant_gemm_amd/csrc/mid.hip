@@ -467,7 +467,8 @@ __global__ __launch_bounds__(64) void mid_final_kernel(MidArgs g, MultiArgs mu) 
   multi_term_rows<kTogether>(term, mu, id, n0, g.N, [&](int j) {
     const bool mine = have && j < mu.r;
     if (!g.tsplits)
-      return __builtin_bit_cast(bf16x8, mine ? *reinterpret_cast<const u32x4 *>(mu.P + m * mu.r + j) : u32x4{0u, 0u, 0u, 0u});
+      return __builtin_bit_cast(bf16x8, mine ? *reinterpret_cast<const u32x4 *>(mu.P + m * mu.r + j)
+                                             : u32x4{0u, 0u, 0u, 0u});
     f32x4 a = zero, b = zero;
     const float *tp = g.tpart + m * mu.r + j;
     for (int t0 = 0; t0 < g.tsplits; t0 += 4) {
@@ -602,7 +603,8 @@ hipError_t launch_mid_fwd_multi(const GemmArgs &ga, const MultiArgs &mu, const u
   int32_t *order = reinterpret_cast<int32_t *>(reinterpret_cast<char *>(part) + up256((size_t)s.splits * ga.M * ga.C * 4));
   if (wgs >= (int64_t(1) << 31) || frows > 65535 || (small && tsplits != mid_tsplits(ga.M, ga.R)))
     return hipErrorInvalidValue;
-  const MidArgs a{ga.a_side, ga.w, ga.M, ga.C, ga.R, ga.out, part, s.splits, ga.t, tpart, tsplits, ra, T, (int)tiles, A, order};
+  const MidArgs a{ga.a_side, ga.w, ga.M, ga.C, ga.R, ga.out, part, s.splits, ga.t, tpart, tsplits, ra, T, (int)tiles,
+                  A, order};
   const unsigned grid = (unsigned)wgs;
   switch (s.mt) {
 #define MID_CASE(MT, NW, BLK)                            \

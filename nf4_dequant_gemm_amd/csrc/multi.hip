@@ -529,7 +529,8 @@ __global__ __launch_bounds__(256) void multi_sum_kernel(SumArgs w, MultiPlan pl)
       const bool have = row < kR && m < me && j < r;
 #pragma unroll
       for (int e = 0; e < kParts; ++e)
-        st.p[i][e] = have ? *(reinterpret_cast<const uint4 *>((const uint16_t *)g.p + ((int64_t)srow[m] * w.rp + j) * kParts) + e)
+        st.p[i][e] = have ? reinterpret_cast<const uint4 *>((const uint16_t *)g.p +
+                                                            ((int64_t)srow[m] * w.rp + j) * kParts)[e]
                           : make_uint4(0, 0, 0, 0);
     }
   };
@@ -622,7 +623,8 @@ __global__ __launch_bounds__(256) void multi_sum_kernel(SumArgs w, MultiPlan pl)
       if (j >= r || c >= C) continue;
       const int64_t at = g.transposed ? c * r + j : j * C + c;
       const f32x4 y = acc[t][u];
-      const uint2 z = me ? make_uint2(pack_bf16x2(sa * y[0], sa * y[1]), pack_bf16x2(sa * y[2], sa * y[3])) : make_uint2(0, 0);
+      const uint2 z = me ? make_uint2(pack_bf16x2(sa * y[0], sa * y[1]), pack_bf16x2(sa * y[2], sa * y[3]))
+                         : make_uint2(0, 0);
       if (g.transposed && (r & 3) != 0) {   // rows of out that are not 8-byte aligned
 #pragma unroll
         for (int v = 0; v < 4; ++v) {
@@ -692,7 +694,8 @@ hipError_t launch_multi_plan(const int32_t *ids, int64_t M, int L, const MultiPl
   }
   const int64_t blocks = 1 + w.pad_blocks + (w.tr[0].blocks() + w.tr[1].blocks()) * L;
   if (blocks >= (int64_t(1) << 32) / kPlanThreads) return hipErrorInvalidValue;
-  multi_plan_kernel<<<dim3((unsigned)blocks), dim3(kPlanThreads), sizeof(int32_t) * kPlanWaves * (L + 1), st>>>(ids, M, L, pl, w);
+  const size_t lds = sizeof(int32_t) * kPlanWaves * (L + 1);
+  multi_plan_kernel<<<dim3((unsigned)blocks), dim3(kPlanThreads), lds, st>>>(ids, M, L, pl, w);
   return hipGetLastError();
 }
 
@@ -773,7 +776,8 @@ hipError_t launch_multi_sums(const MultiSum &a, const MultiSum &b, int64_t M, in
   const bool small = M <= kMultiSmallM, few = small && M <= 32 * (int64_t)L;
   const int64_t most = std::max(a.c, b.c), tiles = (most + kCB - 1) / kCB;
   const int64_t blocks = small ? L : multi_sum_blocks(M, a.c, b.c, L);
-  if (rp < r || (rp & 7) != 0 || ((a.c | b.c) & 7) != 0 || pl.rows[kPlanSum] != multi_sum_rows(M, a.c, b.c) || blocks > 65535)
+  if (rp < r || (rp & 7) != 0 || ((a.c | b.c) & 7) != 0 || pl.rows[kPlanSum] != multi_sum_rows(M, a.c, b.c) ||
+      blocks > 65535)
     return hipErrorInvalidValue;
   const dim3 grid((unsigned)tiles, (unsigned)blocks, 2);
   switch ((r + 15) / 16) {
