@@ -443,7 +443,7 @@ int qk_norm_rope_bwd(const nf4_head_norm *p, const nf4_heads *gq, const nf4_head
  *   dlogits_i = (w / tau) (exp(z_i - lse) - sum of p_j over the entries j with idx_j == i).
  * An entry whose index lies outside [0, v) or whose teacher logit is -inf is not there; a row
  * without entries has loss 0 and a zero gradient. Logits of -inf are masked (they have probability
- * 0); a row without a finite logit gives NaN.
+ * 0); a row without a finite logit gives NaN, and so does a NaN logit wherever it lies.
  * logits, dlogits: `dtype` [t, v] with row strides ld, ldd >= v in elements (rows need no
  * alignment); idx int32 [t, top], teacher float32 [t, top], 1 <= top <= 1024; t >= 0 (0: nothing to
  * do), 1 <= v < 2^30; tau > 0, finite. dlogits may be logits.

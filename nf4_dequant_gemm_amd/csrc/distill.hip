@@ -166,16 +166,17 @@ __global__ __launch_bounds__(kThreads, kChunks <= 8 ? 6 : 4) void distill_kernel
 #pragma unroll
         for (int e = 0; e < P; ++e) m = fmaxf(m, elem<XT>(b[j], e));
     if (m > top_z) {
-      s *= __builtin_amdgcn_exp2f((top_z - m) * c2);   // from -inf: s is 0, exp2(-inf) = 0
+      s *= __builtin_amdgcn_exp2f((top_z - m) * c2);   // from -inf: s is 0 or NaN, exp2(-inf) = 0
       top_z = m;
     }
-    if (m > -INFINITY) {
+    // The maximum passes over a NaN, so the sum takes every element whatever the maximum is: against 0
+    // while that is -inf, exp2(-inf) = 0 for the masked ones and NaN for a NaN.
+    const float ref = m > -INFINITY ? m : 0.f;
 #pragma unroll
-      for (int j = 0; j < 4; ++j)
-        if (i0 + j * kThreads < n)
+    for (int j = 0; j < 4; ++j)
+      if (i0 + j * kThreads < n)
 #pragma unroll
-          for (int e = 0; e < P; ++e) s += __builtin_amdgcn_exp2f((elem<XT>(b[j], e) - m) * c2);
-    }
+        for (int e = 0; e < P; ++e) s += __builtin_amdgcn_exp2f((elem<XT>(b[j], e) - ref) * c2);
   };
   if (!known) {
     if constexpr (kChunks > 0) {
@@ -212,7 +213,8 @@ __global__ __launch_bounds__(kThreads, kChunks <= 8 ? 6 : 4) void distill_kernel
   // ---- the sums: exp2((z - max) c2), u_k, u_k times the difference of the logs
   float sum = 0.f, us = 0.f, ds = 0.f;
   if (!known) {
-    if (mine > -INFINITY) sum = s * __builtin_amdgcn_exp2f((mine - top_z) * c2);
+    // of -inf alone, or with NaN: s is 0, or NaN, which stays
+    sum = mine > -INFINITY ? s * __builtin_amdgcn_exp2f((mine - top_z) * c2) : s;
     if (odd >= 0) sum += __builtin_amdgcn_exp2f((zo - top_z) * c2);
   }
 #pragma unroll

@@ -1,0 +1,47 @@
+"""Distillation from a teacher's top logits at the values and sizes where a running maximum and sum can
+go wrong: NaN beside masked logits."""
+import pytest
+import torch
+
+from tests.gpu_helpers import say
+from tests.test_gpu_distill import DEV, inputs
+
+pytestmark = pytest.mark.gpu
+
+# rows of each launch: one chunk a thread and less, in registers of 64, 256, 512 and 1024 threads, walked
+LENGTHS = [9, 400, 1000, 8191, 20001, 50001, 140003]
+
+
+@pytest.mark.parametrize("dt", ["bf16", "f32"])
+@pytest.mark.parametrize("v", LENGTHS)
+def test_nan_logits_are_not_hidden(lib, v, dt):
+    """A NaN makes its row's loss, lse and whole gradient NaN wherever it lies: alone among ordinary
+    logits, in a run that fills whole 16-byte chunks, and among logits that are otherwise masked with -inf
+    (all but one, elsewhere in the row). The other rows keep their values bit for bit."""
+    say(f"distill NaN v={v} {dt}")
+    t, top = 12, 4
+    z, idx, teacher, w = inputs(t, v, top, dt)
+    idx[:] = torch.arange(top) + v - top              # the teacher's entries: the row's last logits
+    clean = z.clone()
+    bad = {0: v // 2, 1: 0, 2: v - top - 1, 3: min(16, v // 3)}
+    for row, at in bad.items():
+        z[row, at] = float("nan")
+    z[4, :v // 2] = float("nan")
+    z[5] = float("nan")
+    for row, at in ((6, 0), (7, v // 2), (8, min(8 * 70, v - top - 1))):
+        z[row] = float("-inf")
+        z[row, at] = float("nan")
+        z[row, v - top:] = 1.0
+    clean, z, idx, teacher, w = (x.to(DEV) for x in (clean, z, idx, teacher, w))
+    rest = torch.arange(9, t, device=DEV)
+    loss, lse = lib.distill_topk_fwd(z, idx, teacher, 2.0)
+    step_loss, step_grad = lib.distill_topk_step(z, idx, teacher, 2.0, w)
+    back = lib.distill_topk_bwd(w, z, idx, teacher, 2.0, lse)
+    for x in (loss, lse, step_loss):
+        assert x[:9].isnan().all(), x[:9]
+    for g in (step_grad, back):
+        assert g[:9].isnan().all()
+    want, want_lse = lib.distill_topk_fwd(clean, idx, teacher, 2.0)
+    want_step, want_grad = lib.distill_topk_step(clean, idx, teacher, 2.0, w)
+    assert torch.equal(loss[rest], want[rest]) and torch.equal(lse[rest], want_lse[rest])
+    assert torch.equal(step_loss[rest], want_step[rest]) and torch.equal(step_grad[rest], want_grad[rest])
