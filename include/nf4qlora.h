@@ -382,7 +382,8 @@ int qlora_multi_fwd(const void *X, int64_t m, const nf4_tensor *W, const void *A
 /* Backward for dY bf16 [m, n]: dX bf16 [m, k] (skipped when NULL), dA bf16 [L, r, k], dB bf16
  * [L, n, r], zero for an adapter without rows; T from the forward or NULL (recomputed; a batch of at
  * most 256 rows recomputes it in any case, beside U in one launch, and does not read T). Sums over
- * rows are float32, in an order that the ids and sizes alone fix. Non-finite dY: as qlora_bwd.
+ * rows are float32, in an order that the ids and sizes alone fix. An Inf or NaN in a row of X or dY
+ * reaches that row's T, Y and dX and its adapter's dA and dB, nothing else (whatever n is).
  * Errors: as qlora_multi_fwd. */
 int qlora_multi_bwd(const void *dY, const void *X, int64_t m, const nf4_tensor *W, const void *A,
                     const void *B, const float *s, const int32_t *ids, int32_t L, int32_t r, const void *T,
