@@ -898,7 +898,7 @@ class QLoRAMultiFunction(torch.autograd.Function):
 
 
 class QKNormRopeFunction(torch.autograd.Function):
-    """Head norms and rotation (qk_norm_rope_fwd); gradients flow to q, k, wq and wk."""
+    """Head norms and rotation (qk_norm_rope_fwd); gradients flow to those of q, k, wq and wk that are given."""
 
     @staticmethod
     def forward(ctx, q, k, wq, wk, cos, sin, pos, eps: float = 1e-6, interleaved: bool = False,
@@ -910,9 +910,10 @@ class QKNormRopeFunction(torch.autograd.Function):
     @staticmethod
     def backward(ctx, gq, gk):
         q, k, wq, wk, cos, sin, pos = ctx.saved_tensors
-        rows = lambda g: g if g.stride(2) == 1 else g.contiguous()
+        rows = lambda g: g if g is None or g.stride(2) == 1 else g.contiguous()   # None: no q, or no k
         dq, dk, dwq, dwk = qk_norm_rope_bwd(rows(gq), rows(gk), q, k, wq, wk, cos, sin, pos, *ctx.args)
-        return dq, dk, dwq.to(wq.dtype), dwk.to(wk.dtype), None, None, None, None, None, None
+        like = lambda dw, w: None if dw is None else dw.to(w.dtype)
+        return dq, dk, like(dwq, wq), like(dwk, wk), None, None, None, None, None, None
 
 
 class DistillTopKFunction(torch.autograd.Function):
