@@ -1048,11 +1048,12 @@ namespace {
 // tiles 108 / 126 us, 128 tiles 124 / 125, 129 tiles 139 / 124, 172 tiles 178 / 129). Up to 256 rows have
 // no table of the rows' order and always take the small kernels.
 enum class MultiKernel { kStream, kMid, kLarge };
+bool multi_large(int64_t m, int64_t n) {
+  return m > nf4q::kMultiSmallM && ((m + 255) / 256) * ((n + 255) / 256) > 128;
+}
 MultiKernel multi_kernel(int64_t m, const nf4_tensor *W, int32_t r) {
   if (stream16_shape(m, W) && r % 8 == 0 && W->n > 128 * 112) return MultiKernel::kStream;
-  if (m <= nf4q::kMultiSmallM) return MultiKernel::kMid;
-  const int64_t tiles = ((m + 255) / 256) * ((W->n + 255) / 256);
-  return tiles <= 128 ? MultiKernel::kMid : MultiKernel::kLarge;
+  return multi_large(m, W->n) ? MultiKernel::kLarge : MultiKernel::kMid;
 }
 
 int padded(int32_t r) { return (r + 7) & ~7; }
@@ -1065,7 +1066,8 @@ int stream_tsplits(int64_t k, int32_t r) {
 }
 
 // Workspace of the layer with an adapter for every row; tensors whose ranks are padded to a multiple of 8
-// only where r is not one. Forward: the rows' order, B padded, T padded, float sums of T, float sums of Y.
+// only where r is not one. Forward: the rows' order, B padded, T padded, float sums of T, float sums of Y (not
+// for the large kernel, which keeps them in registers).
 // Backward: the rows' order, U (padded), B transposed [L, r, n], A transposed [L, k, r padded], T padded
 // (recomputed when the caller passes none), T and U in float32 for a small batch, then float sums of the
 // row projections, of dX or of the sums over rows (one at a time).
@@ -1099,7 +1101,7 @@ MultiWs multi_ws(int64_t m, int64_t n, int64_t k, int32_t r, int32_t L, bool bwd
     int ts = m <= nf4q::kMultiSmallM ? nf4q::mid_tsplits(m, k) : w.sp_k;
     if (m <= 16) ts = std::max(ts, stream_tsplits(k, r));
     w.tpart = align256((size_t)ts * m * rp * 4);
-    w.part = nf4q::mid_fwd_bytes(m, n, k);
+    w.part = multi_large(m, n) ? 0 : nf4q::mid_fwd_bytes(m, n, k);
   }
   w.total = w.plan + w.bp + w.u + w.bt + w.at + w.tp + w.wide + w.tpart + w.part;
   return w;
