@@ -455,7 +455,8 @@ int qk_norm_rope_bwd(const nf4_head_norm *p, const nf4_heads *gq, const nf4_head
 int distill_topk_fwd(const void *logits, int dtype, int64_t t, int64_t v, int64_t ld, const int32_t *idx,
                      const float *teacher, int32_t top, float tau, float *loss, float *lse, void *stream);
 
-/* dlogits for the gradients grad float32 [t] of the rows' losses, given lse from the forward. A row
+/* dlogits for the gradients grad float32 [t] of the rows' losses, given lse from the forward (where a
+ * float32 lse has lost the sum, at 256 and more either side of 0, the row is summed again). A row
  * whose gradient is 0 is not read: its dlogits are 0. */
 int distill_topk_bwd(const void *logits, int dtype, int64_t t, int64_t v, int64_t ld, const int32_t *idx,
                      const float *teacher, int32_t top, float tau, const float *lse, const float *grad,

@@ -156,7 +156,9 @@ __global__ __launch_bounds__(kThreads, kChunks <= 8 ? 6 : 4) void distill_kernel
 
   // ---- the maxima
   float top_z = zo, s = 0.f;   // this thread's running maximum, and its sum relative to it
-  const bool known = a.lse_in != nullptr;
+  // A large lse has lost the digits of the sum (in a row masked with -1e9 throughout, log v of it) or has
+  // overflowed: such a row's sum is formed again. Below 256 lse is off by at most 2^-17.
+  const bool known = a.lse_in && fabsf(a.lse_in[row]) < 256.f;
   // four chunks (i0 + j kThreads, those below n) into the running maximum and sum
   auto take = [&](const u32x4 *b, int i0) {
     float m = top_z;

@@ -1,10 +1,10 @@
 """Distillation from a teacher's top logits at the values and sizes where a running maximum and sum can
-go wrong: NaN beside masked logits."""
+go wrong: NaN beside masked logits, rows whose mask leaves nothing."""
 import pytest
 import torch
 
 from tests.gpu_helpers import say
-from tests.test_gpu_distill import DEV, inputs
+from tests.test_gpu_distill import DEV, check, inputs
 
 pytestmark = pytest.mark.gpu
 
@@ -45,3 +45,33 @@ def test_nan_logits_are_not_hidden(lib, v, dt):
     want_step, want_grad = lib.distill_topk_step(clean, idx, teacher, 2.0, w)
     assert torch.equal(loss[rest], want[rest]) and torch.equal(lse[rest], want_lse[rest])
     assert torch.equal(step_loss[rest], want_step[rest]) and torch.equal(step_grad[rest], want_grad[rest])
+
+
+@pytest.mark.parametrize("dt", ["bf16", "f32"])
+@pytest.mark.parametrize("tau", [0.5, 2.0])
+@pytest.mark.parametrize("v", LENGTHS)
+def test_rows_far_from_zero(lib, v, tau, dt):
+    """Rows masked throughout with the type's lowest value, with -1e9, -1e4 and -1e3, and rows of ordinary
+    logits about 1e5 and 300 away from 0: a constant added to a row changes neither its loss nor its
+    gradient, so both are held to the values of the row less its maximum (exact in float32 here), by every
+    entry point. Only lse moves with the row: in float32 it has lost the sum there, and beside the
+    lowest value at tau < 1 it is -inf."""
+    say(f"distill far v={v} tau={tau} {dt}")
+    z, idx, teacher, w = inputs(7, v, 3, dt)
+    low = torch.finfo(z.dtype).min
+    for row, x in enumerate((low, -1e9, -1e4, -1e3)):
+        z[row] = x
+    z[4] += 1e5
+    z[5] -= 1e5
+    z[6] -= 300
+    near = (z.double() - z.double().amax(1, keepdim=True)).float()
+    assert torch.equal(near.double(), z.double() - z.double().amax(1, keepdim=True))
+    z, near, idx, teacher, w = (x.to(DEV) for x in (z, near, idx, teacher, w))
+    loss, lse = lib.distill_topk_fwd(z, idx, teacher, tau)
+    step_loss, step_grad = lib.distill_topk_step(z, idx, teacher, tau, w)
+    assert torch.equal(loss, step_loss)
+    check(near, idx, teacher, w, tau, loss, None, step_grad)
+    check(near, idx, teacher, w, tau, None, None, lib.distill_topk_bwd(w, z, idx, teacher, tau, lse))
+    x = z.clone().requires_grad_()
+    (lib.DistillTopKFunction.apply(x, idx, teacher, tau) * w).sum().backward()
+    check(near, idx, teacher, w, tau, None, None, x.grad)
