@@ -72,7 +72,8 @@ __global__ __launch_bounds__(kThreads, kChunks <= 8 ? 6 : 4) void distill_kernel
   __shared__ __align__(16) int s_idx[kTop<kThreads>];
   __shared__ float s_u[kTop<kThreads>];
   const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
-  const int64_t row = blockIdx.x;
+  const int64_t row = (int64_t)blockIdx.y * gridDim.x + blockIdx.x;
+  if (row >= a.t) return;
   const XT *z = reinterpret_cast<const XT *>(a.z) + row * a.ld;
   XT *dz = a.dz ? reinterpret_cast<XT *>(a.dz) + row * a.ldd : nullptr;
   const float w = dz && a.weight ? a.weight[row] : 1.f;
@@ -321,9 +322,14 @@ __global__ __launch_bounds__(kThreads, kChunks <= 8 ? 6 : 4) void distill_kernel
   }
 }
 
+constexpr int64_t kGridRows = int64_t(1) << 21;
 template <typename XT, int kThreads, int kChunks>
 hipError_t launch_row(const DistillArgs &a, hipStream_t st) {
-  distill_kernel<XT, kThreads, kChunks><<<dim3((unsigned)a.t), dim3(kThreads), 0, st>>>(a);
+  // Fewer than 2^32 threads along a dimension: 67 million rows of 64 threads in one were taken modulo that,
+  // without an error, and left all but the first few rows unwritten.
+  const int64_t x = a.t < kGridRows ? a.t : kGridRows;
+  const dim3 grid((unsigned)x, (unsigned)((a.t + x - 1) / x));
+  distill_kernel<XT, kThreads, kChunks><<<grid, dim3(kThreads), 0, st>>>(a);
   return hipGetLastError();
 }
 

@@ -1,5 +1,6 @@
 """Distillation from a teacher's top logits at the values and sizes where a running maximum and sum can
-go wrong: NaN beside masked logits, rows whose mask leaves nothing."""
+go wrong: NaN beside masked logits, rows whose mask leaves nothing, more rows than one dimension of a
+launch."""
 import pytest
 import torch
 
@@ -75,3 +76,20 @@ def test_rows_far_from_zero(lib, v, tau, dt):
     x = z.clone().requires_grad_()
     (lib.DistillTopKFunction.apply(x, idx, teacher, tau) * w).sum().backward()
     check(near, idx, teacher, w, tau, None, None, x.grad)
+
+
+def test_many_short_rows(lib):
+    """More than 2^26 rows: with 64 threads a row their number passes 2^32. Rows repeat every 8 (in content and in
+    alignment), and so do the results, bit for bit."""
+    t, v = 2 ** 26 + 16, 3
+    z, idx, teacher, w = (x.to(DEV) for x in inputs(8, v, 1, "bf16"))
+    want = lib.distill_topk_fwd(z, idx, teacher, 2.0) + lib.distill_topk_step(z, idx, teacher, 2.0, w)
+    want_back = lib.distill_topk_bwd(w, z, idx, teacher, 2.0, want[1])
+    many = lambda x: x.repeat((t // 8,) + (1,) * (x.dim() - 1))
+    same = lambda got, ref: bool((got.view(t // 8, *ref.shape) == ref).all())
+    z, idx, teacher, w = (many(x) for x in (z, idx, teacher, w))
+    loss, lse = lib.distill_topk_fwd(z, idx, teacher, 2.0)
+    assert same(loss, want[0]) and same(lse, want[1])
+    assert same(lib.distill_topk_bwd(w, z, idx, teacher, 2.0, lse), want_back)
+    step_loss, grad = lib.distill_topk_step(z, idx, teacher, 2.0, w)
+    assert same(step_loss, want[2]) and same(grad, want[3])
