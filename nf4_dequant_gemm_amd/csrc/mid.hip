@@ -223,11 +223,14 @@ __global__ __launch_bounds__(kThreads) void mid_kernel(MidArgs g, MultiArgs mu) 
       } else {
 #pragma unroll
         for (int b = 0; b < kBlk; ++b) {
+          // a block past K: a constant of 0, not the next row's, whose Inf or NaN would meet the zeros of X
+          // (by arithmetic, as the copies of X)
+          const uint32_t past = (uint32_t)((kblk - 1 - st * kBlk - b) >> 31) & kNone;
           if constexpr (kDQ) {
-            c.q[nt][b] = __builtin_amdgcn_raw_buffer_load_b8(rQ, in ? b0 + b : kNone, 0, 0);
-            c.s[nt][b] = __builtin_amdgcn_raw_buffer_load_b32(rS, ((wblk + b0 + b) >> 8) * 4, 0, 0);
+            c.q[nt][b] = __builtin_amdgcn_raw_buffer_load_b8(rQ, (in ? b0 + b : kNone) | past, 0, 0);
+            c.s[nt][b] = __builtin_amdgcn_raw_buffer_load_b32(rS, (((wblk + b0 + b) >> 8) * 4) | past, 0, 0);
           } else {
-            c.q[nt][b] = __builtin_amdgcn_raw_buffer_load_b32(rQ, in ? (b0 + b) * 4 : kNone, 0, 0);
+            c.q[nt][b] = __builtin_amdgcn_raw_buffer_load_b32(rQ, (in ? (b0 + b) * 4 : kNone) | past, 0, 0);
           }
         }
       }

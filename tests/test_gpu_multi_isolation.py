@@ -1,5 +1,6 @@
 """Rows of different jobs in one batch stay apart: infinities and NaN in a row's X or dY, or in an adapter
-that no row has, change no bit of another row's T, Y or dX, nor of another adapter's dA and dB.
+that no row has, change no bit of another row's T, Y or dX, nor of another adapter's dA and dB; and those in
+a weight row's constants stay in its column of Y.
 
 n % 64 != 0 in most shapes: the last step of dX's reduction then reaches past the end of a row of dY.
 """
@@ -68,3 +69,26 @@ def test_a_row_of_x(lib, m, k, n, fmt):
     for got, ref in ((dA, want[1]), (dB, want[2])):
         assert torch.equal(got[[0, 2, 3]], ref[[0, 2, 3]])
         assert got[1].isnan().any()
+
+
+@pytest.mark.parametrize("fmt", ["nf4", "nf4f", "e2m1"])
+@pytest.mark.parametrize("m", [3, 20, 40, 60, 75, 95, 110, 125, 300])
+def test_a_weight_row(lib, m, fmt):
+    """K = 320 is no multiple of the mid kernel's step at any height, so that a step reaches past the end of
+    a weight row. Blocks of row 51 and on have a constant of NaN, none of row 50."""
+    k, n = 320, 136
+    say(f"multi isolation W m={m} {fmt}")
+    X, q, A, B, s, ids, _ = inputs(lib, m, k, n, fmt)
+    Y, T = lib.qlora_multi_fwd(X, q, A, B, s, ids)
+    q2 = q.clone()
+    if fmt == "nf4":
+        q2.scale[1] = float("nan")                    # of blocks 256 to 511: rows 51 to 102
+    elif fmt == "nf4f":
+        q2.absmax.view(n, -1)[51:103] = float("nan")
+    else:
+        q2.absmax.view(n, -1)[51:103] = 0x7F          # the E4M3 NaN
+    Y2, T2 = lib.qlora_multi_fwd(X, q2, A, B, s, ids)
+    bad = torch.zeros(n, dtype=torch.bool, device=DEV)
+    bad[51:103] = True
+    assert torch.equal(Y2[:, ~bad], Y[:, ~bad]) and torch.equal(T2, T)
+    assert Y2[:, bad].isnan().all()
