@@ -420,8 +420,8 @@ typedef struct {
 
 /* Forward: q_out, k_out as above, of the heads of q and k. Sums in float32, one rounding.
  * Errors: NF4_EINVAL for a NULL pointer that is needed, head counts that differ, negative sizes or
- * strides, a pointer not aligned to its elements, an unknown dtype; NF4_EUNSUPPORTED for d or rot out
- * of range or odd, or too many heads. */
+ * strides, outputs whose heads overlap (a stride below d), a pointer not aligned to its elements, an
+ * unknown dtype; NF4_EUNSUPPORTED for d or rot out of range or odd, or too many heads. */
 int qk_norm_rope_fwd(const nf4_head_norm *p, const nf4_heads *q, const nf4_heads *k,
                      const nf4_heads *q_out, const nf4_heads *k_out, void *stream);
 

@@ -1294,6 +1294,17 @@ int check_heads(const nf4_heads *h, const char *name, int32_t heads, size_t esz,
   return NF4_OK;
 }
 
+// Heads that are written: no two may share a place, which two threads would race for (an expanded tensor).
+int check_out_heads(const nf4_heads *h, const char *name, int32_t heads, size_t esz, const nf4_head_norm *p) {
+  const int st = check_heads(h, name, heads, esz, p->tokens);
+  if (st) return st;
+  const bool tokens = p->tokens > 1 && heads > 0, many = heads > 1 && p->tokens > 0;
+  if ((tokens && h->token_stride < p->d) || (many && h->head_stride < p->d) ||
+      (tokens && many && h->token_stride == h->head_stride))
+    return fail(NF4_EINVAL, "the heads of %s overlap", name);
+  return NF4_OK;
+}
+
 int check_head_norm(const nf4_head_norm *p, const nf4_heads *q, const nf4_heads *k, size_t *esz) {
   if (!p || !q || !k) return fail(NF4_EINVAL, "the descriptor, q and k must be non-NULL");
   if (p->tokens < 0) return fail(NF4_EINVAL, "tokens must be >= 0 (got %lld)", (long long)p->tokens);
@@ -1367,8 +1378,8 @@ int qk_norm_rope_fwd(const nf4_head_norm *p, const nf4_heads *q, const nf4_heads
   size_t esz = 0;
   int st = check_head_norm(p, q, k, &esz);
   if (st) return st;
-  if ((st = check_heads(q_out, "q_out", q->heads, esz, p->tokens))) return st;
-  if ((st = check_heads(k_out, "k_out", k->heads, esz, p->tokens))) return st;
+  if ((st = check_out_heads(q_out, "q_out", q->heads, esz, p))) return st;
+  if ((st = check_out_heads(k_out, "k_out", k->heads, esz, p))) return st;
   if (p->tokens == 0) return ok();
   nf4q::HeadArgs a = head_args(p);
   a.q = head_side(q, q_out, nullptr, p->wq);
@@ -1390,8 +1401,8 @@ int qk_norm_rope_bwd(const nf4_head_norm *p, const nf4_heads *gq, const nf4_head
   if (st) return st;
   if ((st = check_heads(gq, "gq", q->heads, esz, p->tokens))) return st;
   if ((st = check_heads(gk, "gk", k->heads, esz, p->tokens))) return st;
-  if ((st = check_heads(dq, "dq", q->heads, esz, p->tokens))) return st;
-  if ((st = check_heads(dk, "dk", k->heads, esz, p->tokens))) return st;
+  if ((st = check_out_heads(dq, "dq", q->heads, esz, p))) return st;
+  if ((st = check_out_heads(dk, "dk", k->heads, esz, p))) return st;
   if ((reinterpret_cast<uintptr_t>(dwq) | reinterpret_cast<uintptr_t>(dwk)) & 3)
     return fail(NF4_EINVAL, "dwq and dwk must be 4-byte aligned");
   const size_t need = qk_norm_rope_bwd_workspace_bytes(p->d);
