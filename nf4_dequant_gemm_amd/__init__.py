@@ -600,9 +600,9 @@ def _addr(t: Optional[torch.Tensor]):
     return None if t is None else t.data_ptr()
 
 
-@functools.lru_cache(maxsize=None)
+@functools.lru_cache(maxsize=1024)
 def _bytes_of(name: str, *sizes: int) -> int:
-    """Workspace bytes, a function of the sizes alone."""
+    """Workspace bytes, a function of the sizes alone; those of the last sizes are remembered."""
     return getattr(library(), name)(*sizes)
 
 

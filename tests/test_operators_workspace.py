@@ -1,5 +1,5 @@
 """Device workspace of the layer with an adapter for every row (no GPU needed): no float32 copy of Y beside
-the kernel that keeps its sums in registers."""
+the kernel that keeps its sums in registers, and a bounded number of remembered sizes."""
 import pytest
 
 import nf4_dequant_gemm_amd as m
@@ -24,3 +24,11 @@ def test_large_forward_holds_no_copy_of_y(rows, n, k, r, L):
 def test_split_sums_have_their_place(rows, n, k, r, L):
     """Up to 256 rows or 128 tiles Y's float sums are in the workspace."""
     assert m.library().qlora_multi_fwd_workspace_bytes(rows, n, k, r, L) >= rows * n * 4
+
+
+def test_remembered_sizes_are_bounded():
+    """A server sees a new batch size in many of its steps: the sizes that the binding remembers do not grow
+    with them."""
+    for rows in range(1, 3000):
+        m._bytes_of("qlora_multi_fwd_workspace_bytes", rows, 64, 64, 8, 2)
+    assert m._bytes_of.cache_info().currsize <= 1024
