@@ -447,7 +447,7 @@ int qk_norm_rope_bwd(const nf4_head_norm *p, const nf4_heads *gq, const nf4_head
  * 0); a row without a finite logit gives NaN, and so does a NaN logit wherever it lies.
  * logits, dlogits: `dtype` [t, v] with row strides ld, ldd >= v in elements (rows need no
  * alignment); idx int32 [t, top], teacher float32 [t, top], 1 <= top <= 1024; t >= 0 (0: nothing to
- * do), 1 <= v < 2^30; tau > 0, finite. dlogits may be logits.
+ * do), 1 <= v < 2^30; tau > 0, it and log2(e) / tau finite. dlogits may be logits.
  * Errors: NF4_EINVAL for a NULL pointer, sizes or tau out of range, a stride below v, a pointer not
  * aligned to its elements or an unknown dtype; NF4_EUNSUPPORTED for t or v too large. */
 

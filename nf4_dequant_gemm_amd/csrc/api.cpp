@@ -1432,8 +1432,9 @@ int check_distill(const void *logits, int dtype, int64_t t, int64_t v, int64_t l
     return fail(NF4_EUNSUPPORTED, "t must be below 2^31 and v below 2^30");
   if (top < 1 || top > nf4q::kDistillMaxTop)
     return fail(NF4_EINVAL, "top must lie in [1, %d] (got %d)", nf4q::kDistillMaxTop, top);
-  if (!(tau > 0.f) || !std::isfinite(tau) || !std::isfinite(1.f / tau))
-    return fail(NF4_EINVAL, "tau must be positive, it and its inverse finite");
+  // the kernel works with log2(e) / tau
+  if (!(tau > 0.f) || !std::isfinite(tau) || !std::isfinite(1.44269504f / tau))
+    return fail(NF4_EINVAL, "tau must be positive, it and log2(e) / tau finite");
   if (ld < v) return fail(NF4_EINVAL, "ld must be >= v (got %lld)", (long long)ld);
   if (t == 0) return NF4_OK;
   if (!logits || !idx || !teacher) return fail(NF4_EINVAL, "logits, idx and teacher must be non-NULL");

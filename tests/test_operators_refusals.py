@@ -1,5 +1,5 @@
-"""Refusals of the head norms' outputs (no GPU needed): every call below is invalid by construction, so the
-host's checks refuse it before a pointer is used or anything is launched."""
+"""Refusals of the head norms' outputs and of the distillation's temperature (no GPU needed): every call below
+is invalid by construction, so the host's checks refuse it before a pointer is used or anything is launched."""
 import ctypes
 
 import pytest
@@ -39,3 +39,14 @@ def test_strides_of_one(ts, hs, tokens, n):
     h = heads(ts=ts, hs=hs, n=n)
     assert calls(q_out=h, k_out=heads(data=ctypes.c_void_p(4097)), tokens=tokens, hq=n) == (m.NF4_EINVAL, m.NF4_EINVAL)
     assert b"overlap" not in m.library().nf4_last_error()
+
+
+@pytest.mark.parametrize("tau", [3.0e-39, 3.5e-39, 4.2e-39])
+def test_temperature_whose_scale_overflows(tau):
+    """1 / tau is finite, log2(e) / tau is not: every probability would be NaN."""
+    assert 1 / ctypes.c_float(tau).value < 3.4028234e38
+    lib = m.library()
+    head = (FAKE, m.NF4_BF16, 4, 100, 100, FAKE, FAKE, 8, tau)
+    assert lib.distill_topk_fwd(*head, FAKE, FAKE, None) == m.NF4_EINVAL
+    assert lib.distill_topk_bwd(*head, FAKE, FAKE, FAKE, 100, None) == m.NF4_EINVAL
+    assert lib.distill_topk_step(*head, FAKE, FAKE, FAKE, 100, None) == m.NF4_EINVAL
