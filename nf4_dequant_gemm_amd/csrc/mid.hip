@@ -210,7 +210,8 @@ __global__ __launch_bounds__(kThreads) void mid_kernel(MidArgs g, MultiArgs mu) 
         if constexpr (kDQ) {
           c.q[nt][0] = kBlk == 4 ? __builtin_amdgcn_raw_buffer_load_b32(rQ, in ? b0 : kNone, 0, 0)
                                  : __builtin_amdgcn_raw_buffer_load_b16(rQ, in ? b0 : kNone, 0, 0);
-          c.s[nt][0] = __builtin_amdgcn_raw_buffer_load_b32(rS, ((wblk + b0) >> 8) * 4, 0, 0);
+          // a step past the end: nothing of the next row's run, as below
+          c.s[nt][0] = __builtin_amdgcn_raw_buffer_load_b32(rS, in ? ((wblk + b0) >> 8) * 4 : kNone, 0, 0);
         } else if constexpr (kBlk == 4) {
           const u32x4 v = __builtin_amdgcn_raw_buffer_load_b128(rQ, in ? b0 * 4 : kNone, 0, 0);
 #pragma unroll

@@ -92,3 +92,23 @@ def test_a_weight_row(lib, m, fmt):
     bad[51:103] = True
     assert torch.equal(Y2[:, ~bad], Y[:, ~bad]) and torch.equal(T2, T)
     assert Y2[:, bad].isnan().all()
+
+
+@pytest.mark.parametrize("k", [128, 256, 640, 768])
+@pytest.mark.parametrize("m", [3, 20, 40, 60, 75, 95, 110, 125, 300])
+def test_a_run_of_weight_rows(lib, m, k):
+    """As above where K is a multiple of the step but the waves that take turns along K are not as many: a
+    wave whose turn lies past the end of a weight row. The run of the double quantisation that starts with a
+    row has a scale of NaN; the row before it has none of it."""
+    n, kblk = 520, k // 64
+    row = next(r for r in range(1, n) if r * kblk % 256 == 0)       # first row that starts a run
+    say(f"multi isolation run m={m} k={k} row={row}")
+    X, q, A, B, s, ids, _ = inputs(lib, m, k, n, "nf4")
+    Y, T = lib.qlora_multi_fwd(X, q, A, B, s, ids)
+    q2 = q.clone()
+    q2.scale[row * kblk // 256] = float("nan")
+    Y2, T2 = lib.qlora_multi_fwd(X, q2, A, B, s, ids)
+    bad = torch.zeros(n, dtype=torch.bool, device=DEV)
+    bad[row:-(-(row * kblk + 256) // kblk)] = True
+    assert torch.equal(Y2[:, ~bad], Y[:, ~bad]) and torch.equal(T2, T)
+    assert Y2[:, bad].isnan().all()
