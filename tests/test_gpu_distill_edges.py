@@ -93,3 +93,20 @@ def test_many_short_rows(lib):
     assert same(lib.distill_topk_bwd(w, z, idx, teacher, 2.0, lse), want_back)
     step_loss, grad = lib.distill_topk_step(z, idx, teacher, 2.0, w)
     assert same(step_loss, want[2]) and same(grad, want[3])
+
+
+def test_offsets_past_32_bits(lib):
+    """More than 2^32 bytes and 2^31 elements of logits: the last rows are those of a call for them alone."""
+    t, v = 17000, 131073
+    g = torch.Generator(device=DEV).manual_seed(3)
+    z = torch.randn(t, v, generator=g, device=DEV, dtype=torch.bfloat16)
+    idx = torch.randint(0, v, (t, 8), generator=g, device=DEV).int()
+    teacher, w = torch.randn(t, 8, generator=g, device=DEV), torch.rand(t, generator=g, device=DEV)
+    loss, lse = lib.distill_topk_fwd(z, idx, teacher, 2.0)
+    back = lib.distill_topk_bwd(w, z, idx, teacher, 2.0, lse)
+    step_loss, grad = lib.distill_topk_step(z, idx, teacher, 2.0, w)
+    for rows in (slice(0, 8), slice(t - 8, t)):        # rows of the same alignment
+        want, want_lse = lib.distill_topk_fwd(z[rows], idx[rows], teacher[rows], 2.0)
+        assert torch.equal(loss[rows], want) and torch.equal(lse[rows], want_lse) and torch.equal(step_loss[rows], want)
+        assert torch.equal(grad[rows], lib.distill_topk_step(z[rows], idx[rows], teacher[rows], 2.0, w[rows])[1])
+        assert torch.equal(back[rows], lib.distill_topk_bwd(w[rows], z[rows], idx[rows], teacher[rows], 2.0, want_lse))

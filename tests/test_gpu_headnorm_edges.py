@@ -1,4 +1,4 @@
-"""Norm and rotation of heads through autograd with queries or keys alone."""
+"""Norm and rotation of heads through autograd with queries or keys alone, and past 32-bit offsets."""
 import pytest
 import torch
 
@@ -26,3 +26,20 @@ def test_autograd_of_one_side(lib, given, rot):
             want = lib.qk_norm_rope_bwd(*pair(grad.contiguous()), *pair(x), *pair(w), *table)
             assert torch.equal(xl.grad, want[side]) and torch.equal(wl.grad, want[2 + side].to(w.dtype))
             assert want[1 - side] is None and want[3 - side] is None
+
+
+def test_offsets_past_32_bits(lib):
+    """More than 2^32 bytes and 2^31 elements of q: the last tokens are those of a call for them alone."""
+    m, h, d = 530000, 32, 128
+    g = torch.Generator(device="cuda").manual_seed(3)
+    q, gq = (torch.randn(m, h, d, generator=g, device="cuda", dtype=torch.bfloat16) for _ in range(2))
+    w = torch.rand(d, generator=g, device="cuda") + 0.5
+    ang = torch.rand(100, d // 2, generator=g, device="cuda") * 6
+    pos = torch.randint(0, 100, (m,), generator=g, device="cuda")
+    y, _ = lib.qk_norm_rope_fwd(q, None, w, None, ang.cos(), ang.sin(), pos)
+    dq, _, dw, _ = lib.qk_norm_rope_bwd(gq, None, q, None, w, None, ang.cos(), ang.sin(), pos)
+    assert dw.isfinite().all()
+    for rows in (slice(0, 5), slice(m - 5, m)):
+        args = (q[rows], None, w, None, ang.cos(), ang.sin(), pos[rows])
+        assert torch.equal(y[rows], lib.qk_norm_rope_fwd(*args)[0])
+        assert torch.equal(dq[rows], lib.qk_norm_rope_bwd(gq[rows], None, *args)[0])

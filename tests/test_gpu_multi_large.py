@@ -1,6 +1,6 @@
 """An adapter for every row at the sizes of prompts and training: more than 256 rows and 128 tiles of
-256 x 256 (the large forward kernel), the sums over rows in several stages, ranks above 64, and more rows
-than the transposes look through for an adapter's use.
+256 x 256 (the large forward kernel), the sums over rows in several stages, ranks above 64, more rows
+than the transposes look through for an adapter's use, and X and dY of nearly 4 GiB.
 
 The float64 oracle goes row by row; at these sizes `reference` computes the same per adapter, and is itself
 held against the oracle at a small size. Tolerances as in test_gpu_multi.py.
@@ -110,6 +110,38 @@ def test_sums_of_whole_blocks(lib):
         x, y, A64, B64 = X[i].double(), dY[i].double(), A[a].double(), B[a].double()
         check_close("dA", f32(dA[a]), f32((s[a].double() * ((y @ B64).T @ x)).float()))
         check_close("dB", f32(dB[a]), f32((s[a].double() * (y.T @ (x @ A64.T))).float()))
+
+
+@pytest.mark.parametrize("m,k,n", [(520001, 4096, 72), (60000, 64, 35776)])
+def test_offsets_past_31_bits(lib, m, k, n):
+    """X (Y and dY) of nearly the 4293918720 bytes that the gathering copies reach. Y and dX at the first, the
+    last and some random rows, dA and dB whole, against float64 on the device."""
+    r, L = 8, 3
+    assert 0.98 * 4293918720 < m * max(n, k) * 2 <= 4293918720
+    g = torch.Generator(device=DEV).manual_seed(7)
+    X, dY = (torch.randn(m, c, generator=g, device=DEV, dtype=torch.bfloat16) for c in (k, n))
+    A, B = wl.normal_bf16(3, (L, r, k), k ** -0.5).to(DEV), wl.normal_bf16(4, (L, n, r), 0.1).to(DEV)
+    s, ids = wl.uniform_f32(6, (L,), 0.25, 2.0).to(DEV), (torch.randperm(m, generator=g, device=DEV) % (L + 1) - 1).int()
+    q = lib.nf4_quantize(wl.normal_bf16(2, (n, k), 0.02).to(DEV), 256)
+    W = lib.nf4_dequantize(q, torch.float32).double()
+    Y, T = lib.qlora_multi_fwd(X, q, A, B, s, ids)
+    dX, dA, dB = lib.qlora_multi_bwd(dY, X, q, A, B, s, ids, T)
+    some = torch.cat((torch.arange(20, device=DEV), torch.arange(m - 20, m, device=DEV),
+                      torch.randint(0, m, (200,), generator=g, device=DEV)))
+    x, y, a = X[some].double(), dY[some].double(), ids[some].long()
+    sa = torch.where(a >= 0, s[a].double(), 0.0)[:, None]
+    t, u = (x[:, None] * A[a].double()).sum(2), (y[:, :, None] * B[a].double()).sum(1)
+    check_close("Y", f32(Y[some]), (x @ W.T.contiguous() + sa * (B[a].double() * t[:, None]).sum(2)).cpu().numpy())
+    check_close("dX", f32(dX[some]), (y @ W + sa * (A[a].double() * u[:, :, None]).sum(1)).cpu().numpy())
+    check_close("T", f32(T[some]), torch.where(a[:, None] >= 0, t, 0.0).cpu().numpy())
+    for a in range(L):
+        dA64, dB64 = torch.zeros(r, k, device=DEV, dtype=torch.float64), torch.zeros(n, r, device=DEV, dtype=torch.float64)
+        for i in (ids == a).nonzero()[:, 0].split(40000):
+            x, y = X[i].double(), dY[i].double()
+            dA64 += s[a].double() * ((y @ B[a].double()).T.contiguous() @ x)
+            dB64 += s[a].double() * (y.T.contiguous() @ (x @ A[a].double().T.contiguous()))
+        check_close("dA", f32(dA[a]), dA64.cpu().numpy())
+        check_close("dB", f32(dB[a]), dB64.cpu().numpy())
 
 
 @pytest.mark.parametrize("m,k,n,r,L", [(1, 256, 136, 12, 2), (16, 256, 14408, 16, 4), (130, 320, 264, 16, 64),
