@@ -1046,7 +1046,9 @@ namespace {
 // 25.8 / 25.6, 28672 26.4 / 30.4; k 8192, n 8192 33.4 / 26.3, 14336 33.9 / 35.6). More rows: the mid kernel
 // while 256 x 256 tiles would fill at most half the CUs, then the large one (k 4096, mid / large: 86
 // tiles 108 / 126 us, 128 tiles 124 / 125, 129 tiles 139 / 124, 172 tiles 178 / 129). Up to 256 rows have
-// no table of the rows' order and always take the small kernels.
+// no table of the rows' order and always take the small kernels, which is right but for a batch near 256
+// rows beside a very wide weight (k 4096, mid / large with the order and T before it: 64 rows, n 65536 83 /
+// 160 us, 128256 153 / 299; 200 rows, n 34048 135 / 160, 49152 169 / 163, 65536 205 / 176, 128256 391 / 321).
 enum class MultiKernel { kStream, kMid, kLarge };
 bool multi_large(int64_t m, int64_t n) {
   return m > nf4q::kMultiSmallM && ((m + 255) / 256) * ((n + 255) / 256) > 128;

@@ -15,7 +15,8 @@
 // takes a row. With the gradient it keeps the row in registers (16 bytes a chunk, all of a thread's loads
 // issued before the first is used), so that maximum, sum and gradient need no second read; a row longer
 // than that, and a row whose gradient is not wanted or whose lse is known, is walked with a running
-// maximum and sum, for the gradient a second time (from the caches). Two exchanges over the workgroup are
+// maximum and sum, for the gradient a second time (from the caches; with a known lse that time only:
+// 4096 x 128000 399 us, 1024 x 50001 in float32 90 us). Two exchanges over the workgroup are
 // enough, since with u_k = exp((y_k - max y) / tau)
 //
 //   loss = sum_k u_k ((y_k - max y) - (z[idx_k] - max z)) / tau / sum u - log sum u + log sum exp((z - max z) / tau):
@@ -337,7 +338,7 @@ hipError_t launch_row(const DistillArgs &a, hipStream_t st) {
 // several small workgroups on a CU overlap their loads and their arithmetic (4096 x 32000 in bf16 with the
 // gradient: 256 threads of 16 chunks 110 us, 512 of 8 106 us, 1024 of 4 132 us, walked by 512 122 us); past
 // 512 of 16, walked by 1024 (4096 x 128000: 451 us, 512 of 32 489 us, 1024 of 16 472 us). Without the
-// gradient nothing need stay: walked (1024 x 50001 in float32: 41 us, in registers 56 us). The sum runs
+// gradient nothing need stay: walked (1024 x 50001 in float32: 38 us, in registers 56 us). The sum runs
 // over the same chunks in the same order either way, so the loss alone and the loss with the gradient
 // agree bit for bit. 64-thread workgroups need no more than 256 entries.
 template <typename XT>

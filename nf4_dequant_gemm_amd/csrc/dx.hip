@@ -165,8 +165,8 @@ __device__ __forceinline__ void dx_origin(int64_t m_lo, int64_t m_hi, int tiles_
 // multi.h). kSplit: a workgroup runs one of mu.pieces parts of the reduction and leaves its float32 sums
 // in mu.part (a kernel of its own: both endings in one spilled 120 registers and cost 100 us of 670).
 // kMT: row tiles of 16 that a wave multiplies, fewer than 8 where the launch has at most 32 kMT rows.
-// 8192 x 11008 x 4096, 4 adapters of rank 64: 676 us; split, 64 x 11008 x 4096: 23 us (29 us with 8 row tiles,
-// 380 us unsplit).
+// Medians of 40 launches: 8192 x 11008 x 4096, 4 adapters of rank 64: 626 us (719 on another card); split,
+// 64 x 11008 x 4096: 23 us (29 us with 8 row tiles, 380 us unsplit).
 template <int kFmt, bool kGrp, bool kMulti = false, bool kSplit = false, int kMT = 8>
 __device__ __forceinline__ void dx_body(const GemmArgs &g, const GroupArgs &gr, const MultiArgs &mu) {
   constexpr bool kDQ = kFmt == 1, kFP4 = kFmt == 2;

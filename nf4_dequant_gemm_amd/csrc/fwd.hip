@@ -227,8 +227,9 @@ __device__ void stage_lora_pair(const GemmArgs &g, float sb, int64_t m0, int64_t
 // kMulti: the rows have adapters of their own (mu; g.r is 0) and are taken in the order of their
 // adapters, row m of the launch being row mu.perm[m] of X and Y: the copies of X gather, the store
 // scatters whole row pieces. After the walk over K, each wave adds the low-rank term of its block
-// straight from registers (multi_term, multi.h). 8192 x 4096 x 11008, 4 adapters of rank 64: 798 us (925
-// TFLOP/s); 4096 x 4096 x 4096, 8 adapters of rank 16: 134 us.
+// straight from registers (multi_term, multi.h). Medians of 40 launches: 8192 x 4096 x
+// 11008, 4 adapters of rank 64: 754 us (995 TFLOP/s; 826 on another card); 4096 x 4096 x 4096, 8 adapters of
+// rank 16: 147 us (least 134).
 template <int kFmt, bool kGrp, bool kPair = false, bool kMulti = false>
 __device__ __forceinline__ void fwd_body(const GemmArgs &g, const GroupArgs &gr, const MultiArgs &mu) {
   constexpr bool kDQ = kFmt == 1, kFP4 = kFmt == 2;

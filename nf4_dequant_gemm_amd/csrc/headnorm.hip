@@ -61,7 +61,10 @@ __device__ __forceinline__ void store_chunk(XT *p, const float in[kVec]) {
   Chunk<XT, kVec> c;
 #pragma unroll
   for (int i = 0; i < kVec; ++i) c.v[i] = Elem<XT>::from_f32(in[i]);
-  if constexpr (sizeof(c) == 16)   // not read again here: streamed out (41 -> 31 us on 8192 x 40 heads of 128)
+  // Streamed out, since it is not read again here: forward and backward of 8192 tokens of 40 heads of 128 take
+  // 98.5 us, 103 without; the forward alone 35.6 and 32.5 in bf16 (the outputs then stay in the last cache),
+  // 61.3 and 63.3 in float32.
+  if constexpr (sizeof(c) == 16)
     __builtin_nontemporal_store(__builtin_bit_cast(u32x4, c), reinterpret_cast<u32x4 *>(p));
   else
     *reinterpret_cast<Chunk<XT, kVec> *>(p) = c;
@@ -336,9 +339,10 @@ int chunk_of(const HeadArgs &a, bool f32, bool bwd) {
 }  // namespace
 
 // Workgroups at most: a few for each of the 256 CUs, each walking over several items so that the weight
-// is loaded once for them. 8192 tokens of 32 + 8 heads of 128: forward 33.0 us with 1024, 30.7 with
-// 1536, 35.4 with 2048; backward (110 registers, four waves a SIMD: 1024 run at once) 75 us with 1024,
-// 79 with 2048. Two heads at a time a thread took 50 and 110 us (registers).
+// is loaded once for them. 8192 tokens of 32 + 8 heads of 128, whole calls in a row: forward 38.3 us
+// with 1024, 35.6 with 1536, 40.6 with 2048 (float32: 62.2, 61.3, 62.6); backward (110 registers, four waves a
+// SIMD: 1024 run at once) 62.4 us with 1024, 66.8 with 2048 (float32: 98.1, 105). Two heads at a time a thread
+// were slower (registers).
 constexpr int kMostFwd = 1536, kMostBwd = 1024;
 int head_norm_max_blocks() { return kMostBwd; }   // parts of dw
 

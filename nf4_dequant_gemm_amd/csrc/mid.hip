@@ -31,7 +31,7 @@
 // What bounds it: a step's matrix (37% of the time at 7 row tiles) and vector instructions (34%: two of
 // the three for each product scale and add a block's sums) take turns on a SIMD, and its LDS reads (40% of
 // the LDS's time) do not hide behind them completely. 200 rows x 4096 x 11008: 43 us, and 10 us for the
-// last launch; 1111 rows x 2880 x 2952 in E2M1: 35 and 15 us; one row x 4096 x 4096: 8.5 and 4.2 us.
+// last launch; 1111 rows x 2880 x 2952 in E2M1: 36 and 16 us; one row x 4096 x 4096: 8.3 and 3.9 us.
 #include "common.h"
 #include "launch.h"
 #include "multi.h"

@@ -20,7 +20,7 @@ namespace {
 // the counts are scanned over adapters and waves, and each wave then places its rows in order. The
 // lanes of a 64-row piece are ranked within their adapter by ballots, one for each adapter in the
 // piece, so that LDS is read and written once a piece. A wave's ids are loaded eight pieces at a time.
-// Bound by latency (two passes over the ids, a scan, barriers): 64 to 4096 rows 7 to 8 us, 8192 rows 9 us.
+// Bound by latency (two passes over the ids, a scan, barriers): 500 rows 6.2 us, 4096 rows 8.4, 8192 rows 9.4.
 constexpr int kPlanThreads = 1024, kPlanWaves = kPlanThreads / 64, kPlanAhead = 8;
 
 // Padding of ranks: dst [rows][rp] = src [rows][r] and zeros.
@@ -100,7 +100,7 @@ __device__ __forceinline__ void transpose_tiles(const TransposeArgs &g, const in
   }
 }
 
-// The first workgroup orders the rows, which leaves the card idle for 7 to 12 us; the others meanwhile pad the
+// The first workgroup orders the rows, which leaves the card idle for 6 to 9 us; the others meanwhile pad the
 // ranks of a factor (pad.rows 0: there is none to pad) and transpose the adapters for the backward.
 struct PlanWork {
   PadArgs pad;
@@ -309,7 +309,7 @@ __global__ __launch_bounds__(256) void multi_rows16_kernel(RowsArgs w, MultiPlan
 
 // Blocks of at most 64 rows (one 16-row tile a wave): in- and p-tiles of 64 columns loaded two steps
 // ahead in whole 128-byte rows and staged in LDS, chunk c of row i at slot c ^ ((i >> 1) & 7). Bound by its
-// loads: 8192 rows of 4 adapters, r 64, 4096 columns 21 us (3.2 TB/s), 11008 columns 50 us (3.6 TB/s).
+// loads: 8192 rows of 4 adapters, r 64, 4096 columns 22 us (3.1 TB/s), 11008 columns 50 us (3.6 TB/s).
 __device__ __forceinline__ int swzm(int row, int c) { return row * 8 + (c ^ ((row >> 1) & 7)); }
 
 template <int TN>
@@ -460,7 +460,7 @@ __global__ void multi_rows_sum_kernel(RowsArgs w) {
 // Workgroup: 128 columns x all r ranks, in stages of kR = 64 rows loaded two stages ahead, staged row-major
 // in LDS (rows padded by 32 bytes) and read with the transposing LDS load, which gives a lane 4
 // consecutive rows of one column: the MFMA operand with the rows as its reduction index. dA and dB of 8192
-// rows of 4 adapters, r 64, 4096 and 11008 columns: 61 us (4 TB/s of X and dY) and 14 us to add the blocks.
+// rows of 4 adapters, r 64, 4096 and 11008 columns: 62 us (4 TB/s of X and dY) and 14 us to add the blocks.
 constexpr int kSumRows = 1024;
 constexpr int kRB = 64, kCB = 128, kQRow = kCB + 16;
 typedef __attribute__((ext_vector_type(4))) short s16x4;
