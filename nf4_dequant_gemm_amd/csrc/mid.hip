@@ -8,7 +8,8 @@
 //     16-row tile loads 16 bytes of row l for each 128 elements (whole 64-byte runs of a row), and two
 //     v_permlane32_swap hand every lane 8 bytes of each of the two blocks, so that an MFMA sees one
 //     block only.
-//   * NF4: a code byte (two elements) becomes a pair of unscaled bf16 levels by one lookup in a
+//   * NF4: a code byte (two elements) becomes a pair of unscaled bf16 levels (rounded: the matrix
+//     instructions take bf16; the layer's kernels round level times constant) by one lookup in a
 //     256-entry LDS table held 64 times (entry e of copy c at byte 256 e + 4 c: a byte permute forms
 //     the address, every lane has its own bank); the block constant scales the block's float32 sum.
 //     That is one vector instruction and one LDS read for two elements, where decoding through a table

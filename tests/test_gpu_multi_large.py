@@ -112,6 +112,24 @@ def test_sums_of_whole_blocks(lib):
         check_close("dB", f32(dB[a]), f32((s[a].double() * (y.T @ (x @ A64.T))).float()))
 
 
+@pytest.mark.parametrize("m", [100, 255, 256, 257])
+@pytest.mark.parametrize("r", [8, 33, 57, 72, 96, 112, 128])
+def test_many_rows_to_an_adapter(lib, m, r):
+    """Two adapters, on either side of the 256 rows up to which a block of the sums is an adapter: every rank
+    tile of the sums and of the row projections, in stages of 64 rows."""
+    k, n, L = 320, 264, 2
+    say(f"multi rank m={m} r={r}")
+    X, W = wl.normal_bf16(1 + m, (m, k), 1.0), wl.normal_bf16(2 + m, (n, k), 0.02)
+    A, B = wl.normal_bf16(3 + m, (L, r, k), k ** -0.5), wl.normal_bf16(4 + m, (L, n, r), 0.1)
+    dY, s, ids = wl.normal_bf16(5 + m, (m, n), 1.0), wl.uniform_f32(6 + m, (L,), 0.25, 2.0), make_ids("mixed", m, L)
+    q, Wd = quantise(lib, W, "nf4")
+    want = reference(f32(dY), f32(X), Wd, f32(A), f32(B), s.numpy(), ids.numpy())
+    X, A, B, dY, s, ids = (t.to(DEV) for t in (X, A, B, dY, s, ids))
+    Y, T = lib.qlora_multi_fwd(X, q, A, B, s, ids)
+    for name, got, ref in zip(("Y", "T", "dX", "dA", "dB"), (Y, T) + lib.qlora_multi_bwd(dY, X, q, A, B, s, ids, T), want):
+        check_close(name, f32(got), ref)
+
+
 @pytest.mark.parametrize("m,k,n", [(520001, 4096, 72), (60000, 64, 35776)])
 def test_offsets_past_31_bits(lib, m, k, n):
     """X (Y and dY) of nearly the 4293918720 bytes that the gathering copies reach. Y and dX at the first, the
