@@ -470,6 +470,96 @@ int distill_topk_step(const void *logits, int dtype, int64_t t, int64_t v, int64
                       const float *teacher, int32_t top, float tau, const float *weight, float *loss,
                       void *dlogits, int64_t ldd, void *stream);
 
+/* ---- Choice of experts -----------------------------------------------------------------------------
+ * What the grouped layer's rows come from: for the router's logits x of a token over E experts (1 <= E
+ * <= 256), p = softmax(x), its choices are the `top` largest logits (1 <= top <= min(16, E)), best first,
+ * ties to the lower index; a logit of -inf is never chosen. A choice's gate is its p or, renormalised,
+ * its share of the softmax over the token's choices alone. A token whose keep is 0 (padding), or without a
+ * logit above -inf, is not routed; n tokens are, with N choices. A NaN among a token's logits makes its
+ * gates and the losses NaN; its choices are valid all the same.
+ *   idx    int32 [t, top]     expert of each choice; -1 where there is none (then gate 0, place -1)
+ *   gate   float32 [t, top]
+ *   place  int32 [t, top]     the choice's row when all of them are ordered by expert, then by token
+ *   source int32 [t * top]    the token of every row; -1 from row N on
+ *   counts int64 [E]          the rows of every expert: the counts of qlora_moe_fwd_dev (whose m is t * top)
+ *   sizes  int64 [2]          n, N
+ *   mean_p float32 [E]        the mean of p over the n tokens (0 without any)
+ *   losses float32 [2]        balance = E sum_e (counts_e / N) mean_p_e, which is 1 when all is even;
+ *                             z = the mean of lse^2, lse = log sum exp(x) (0 without routed tokens)
+ * All outputs are the caller's. logits: `dtype` [t, E] with the row stride ld >= E in elements; keep uint8
+ * [t] or NULL; t >= 0, t * top < 2^31. Everything stays on the device, so the calls can be captured.
+ * Errors: NF4_EINVAL for a NULL pointer (keep apart), sizes out of range, a stride below E, a pointer not
+ * aligned to its elements, a short workspace or an unknown dtype; NF4_EUNSUPPORTED for t too large. */
+size_t moe_route_workspace_bytes(int64_t t, int32_t E);
+int moe_route(const void *logits, int dtype, int64_t t, int32_t E, int64_t ld, const uint8_t *keep, int32_t top,
+              int renormalize, int32_t *idx, float *gate, int32_t *place, int32_t *source, int64_t *counts,
+              int64_t *sizes, float *mean_p, float *losses, void *ws, size_t ws_bytes, void *stream);
+
+/* dlogits (`dtype` [t, E], row stride ldd; may be logits) for the gradients dgate float32 [t, top] and
+ * dlosses float32 [2] (either NULL: zeros) of moe_route's gates and losses, given its idx, counts and
+ * sizes. The counts are constants; a token that is not routed gets zeros. Errors: as moe_route. */
+int moe_route_bwd(const void *logits, int dtype, int64_t t, int32_t E, int64_t ld, int32_t top, int renormalize,
+                  const int32_t *idx, const int64_t *counts, const int64_t *sizes, const float *dgate,
+                  const float *dlosses, void *dlogits, int64_t ldd, void *stream);
+
+/* ---- Tokens into expert order, and back ------------------------------------------------------------
+ * With place int32 [t, top] and source int32 [t * top] as moe_route writes them (a place outside
+ * [0, t * top) is none, a source outside [0, t) no token; `top` is not limited here):
+ *   moe_gather       out[place_ij] = X_i; rows without a token are 0. out [t * top, d]
+ *   moe_combine      Y_i = base_i + sum_j gate_ij Z[place_ij] (base NULL: 0; gate NULL: ones, which is the
+ *                    gradient of moe_gather). Y [t, d]; Z [t * top, d], whose rows without a token are not
+ *                    read; Y may be base
+ *   moe_combine_bwd  dZ[place_ij] = gate_ij dY_i, rows without a token 0; dgate_ij = <dY_i, Z[place_ij]>
+ *                    (0 without a place); the gradient of base is dY. dZ may be Z
+ * Elements are `dtype`; X, dY, base and Y have row strides >= d in elements, the grouped rows are
+ * contiguous; gate and dgate float32 [t, top]. Sums in float32, rounded once. t >= 0, t * top < 2^31,
+ * 1 <= d < 2^31. Errors: as moe_route. */
+int moe_gather(const void *X, int dtype, int64_t t, int64_t d, int64_t ldx, const int32_t *place, const int32_t *source,
+               int32_t top, void *out, void *stream);
+int moe_combine(const void *Z, int dtype, int64_t t, int64_t d, const int32_t *place, int32_t top, const float *gate,
+                const void *base, int64_t ldb, void *Y, int64_t ldy, void *stream);
+int moe_combine_bwd(const void *dY, int dtype, int64_t t, int64_t d, int64_t ldy, const void *Z, const int32_t *place,
+                    const int32_t *source, int32_t top, const float *gate, void *dZ, float *dgate, void *stream);
+
+/* ---- Activations kept in 8 bits for the backward pass ----------------------------------------------
+ * The inputs that a backward pass needs again, in half the memory (of bf16). A row of k elements is cut
+ * into blocks of 64 (the last may be short); with a = max |x| over a block,
+ *   code = 127 x / a, rounded to the nearest integer, ties to even;   scale = fl32(a / 127),
+ * and the block stands for fl32(code * scale). A block with a < 2^-119 is kept as zeros (scale 0); one that
+ * holds an Inf or NaN gets the scale NaN and codes 0, so that it reads back as NaN. */
+typedef struct {
+  int8_t *codes;   /* [rows, kp], kp = k rounded up to a multiple of 64 (zeros from k on); 16-byte aligned */
+  float *scale;    /* [rows, kp / 64]                                                                      */
+  int64_t rows, k; /* rows >= 0, k >= 1, both below 2^31, rows * kp <= 2^42                                */
+} nf4_act8;
+
+/* Fill q from X (`dtype` [rows, k], row stride ldx >= k in elements); write what q stands for to X (bf16:
+ * rounded). Errors: NF4_EINVAL for a NULL pointer, sizes out of range, a stride below k, a pointer not
+ * aligned to its elements or an unknown dtype; NF4_EUNSUPPORTED for too many elements. */
+int act8_pack(const void *X, int dtype, int64_t ldx, const nf4_act8 *q, void *stream);
+int act8_unpack(const nf4_act8 *q, void *X, int dtype, int64_t ldx, void *stream);
+
+/* qlora_bwd with X in 8 bits (m = X->rows): the same dX and dB, and dA = s U^T X from what the codes
+ * stand for, rounded to bf16 as the matrix cores take it; equal, bit for bit, to qlora_bwd of the unpacked
+ * X. T must be given when r > 0. ws: qlora_bwd_workspace_bytes. Errors: as qlora_bwd and act8_pack. */
+int qlora_bwd_act8(const void *dY, const nf4_act8 *X, const nf4_tensor *W, const void *A, const void *B, int32_t r,
+                   float s, const void *T, void *dX, void *dA, void *dB, void *ws, size_t ws_bytes, void *stream);
+
+/* qlora_swiglu_bwd with X and Ygu in 8 bits: the activation's gradient is formed in float32 from what
+ * Ygu's codes stand for. Tgu must be given when r > 0. ws: qlora_swiglu_workspace_bytes. Errors: as
+ * qlora_swiglu_bwd and act8_pack. */
+int qlora_swiglu_bwd_act8(const void *dH, const nf4_act8 *X, const nf4_tensor *Wgu, const void *Agu, const void *Bg,
+                          const void *Bu, int32_t r, float s, const nf4_act8 *Ygu, const void *Tgu, void *dX, void *dAgu,
+                          void *dBg, void *dBu, void *ws, size_t ws_bytes, void *stream);
+
+/* qlora_moe_bwd_dev with X in 8 bits: grouped row i is row source[i] of X (a source outside X's rows: zeros),
+ * so that a token's activation is kept once, not once for each of its experts; source NULL: row i, and X
+ * has m rows. T must be given when r > 0. ws: qlora_moe_workspace_bytes_dev. Errors: as qlora_moe_bwd_dev
+ * and act8_pack. */
+int qlora_moe_bwd_dev_act8(const void *dY, const nf4_act8 *X, const int32_t *source, int64_t m, const int64_t *counts,
+                           int32_t E, const nf4_tensor *W, const void *A, const void *B, int32_t r, float s,
+                           const void *T, void *dX, void *dA, void *dB, void *ws, size_t ws_bytes, void *stream);
+
 /* Thread-local description of the last non-OK status returned on this thread ("" if none). */
 const char *nf4_last_error(void);
 

@@ -18,6 +18,11 @@ torch fallback: if the library is not built, every call raises.
     qo, ko = qk_norm_rope_fwd(q, k, wq, wk, cos, sin, pos)   # head norms and rotation, q [m, heads, d]
     loss, lse = distill_topk_fwd(logits, idx, teacher, tau)  # from a teacher's top logits
     loss, dlogits = distill_topk_step(logits, idx, teacher, tau, weight)   # with the gradient, one pass
+    r = moe_route(logits, top)                        # experts of every token, gates, counts, losses
+    Xg = moe_gather(X, r.place, r.source)             # tokens in expert order, for qlora_moe_fwd_dev
+    Y = moe_combine(Z, r.place, r.gate)               # the experts' outputs joined again
+    X8 = act8_pack(X)                                 # an activation kept in 8 bits for the backward pass
+    dX, dA, dB = qlora_bwd_act8(dY, X8, q, A, B, s, T)
 """
 from __future__ import annotations
 
@@ -26,7 +31,7 @@ import dataclasses
 import functools
 import os
 import struct
-from typing import Optional, Tuple
+from typing import NamedTuple, Optional, Tuple
 
 import torch
 
@@ -45,7 +50,10 @@ EXPORTED = ("nf4_quantize", "nf4_dequantize", "nf4_codebook", "qlora_fwd_workspa
             "qlora_moe_bwd_dev", "qlora_fwd_noalloc", "nf4_last_error",
             "qlora_multi_fwd_workspace_bytes", "qlora_multi_bwd_workspace_bytes", "qlora_multi_fwd",
             "qlora_multi_bwd", "qk_norm_rope_fwd", "qk_norm_rope_bwd_workspace_bytes", "qk_norm_rope_bwd",
-            "distill_topk_fwd", "distill_topk_bwd", "distill_topk_step")
+            "distill_topk_fwd", "distill_topk_bwd", "distill_topk_step",
+            "moe_route_workspace_bytes", "moe_route", "moe_route_bwd", "moe_gather", "moe_combine",
+            "moe_combine_bwd", "act8_pack", "act8_unpack", "qlora_bwd_act8", "qlora_swiglu_bwd_act8",
+            "qlora_moe_bwd_dev_act8")
 
 
 class NF4Error(RuntimeError):
@@ -120,6 +128,17 @@ def library() -> ctypes.CDLL:
         "distill_topk_fwd": (ctypes.c_int, [vp, ctypes.c_int, i64, i64, i64, vp, vp, i32, f32, vp, vp, vp]),
         "distill_topk_bwd": (ctypes.c_int, [vp, ctypes.c_int, i64, i64, i64, vp, vp, i32, f32, vp, vp, vp, i64, vp]),
         "distill_topk_step": (ctypes.c_int, [vp, ctypes.c_int, i64, i64, i64, vp, vp, i32, f32, vp, vp, vp, i64, vp]),
+        "moe_route_workspace_bytes": (sz, [i64, i32]),
+        "moe_route": (ctypes.c_int, [vp, ctypes.c_int, i64, i32, i64, vp, i32, ctypes.c_int] + [vp] * 9 + [sz, vp]),
+        "moe_route_bwd": (ctypes.c_int, [vp, ctypes.c_int, i64, i32, i64, i32, ctypes.c_int] + [vp] * 6 + [i64, vp]),
+        "moe_gather": (ctypes.c_int, [vp, ctypes.c_int, i64, i64, i64, vp, vp, i32, vp, vp]),
+        "moe_combine": (ctypes.c_int, [vp, ctypes.c_int, i64, i64, vp, i32, vp, vp, i64, vp, i64, vp]),
+        "moe_combine_bwd": (ctypes.c_int, [vp, ctypes.c_int, i64, i64, i64, vp, vp, vp, i32, vp, vp, vp, vp]),
+        "act8_pack": (ctypes.c_int, [vp, ctypes.c_int, i64, vp, vp]),
+        "act8_unpack": (ctypes.c_int, [vp, vp, ctypes.c_int, i64, vp]),
+        "qlora_bwd_act8": (ctypes.c_int, [vp, vp, vp, vp, vp, i32, f32, vp, vp, vp, vp, vp, sz, vp]),
+        "qlora_swiglu_bwd_act8": (ctypes.c_int, [vp, vp, vp, vp, vp, vp, i32, f32] + [vp] * 7 + [sz, vp]),
+        "qlora_moe_bwd_dev_act8": (ctypes.c_int, [vp, vp, vp, i64, vp, i32, vp, vp, vp, i32, f32] + [vp] * 5 + [sz, vp]),
     }
     for name, (res, args) in sig.items():
         fn = getattr(lib, name)
@@ -840,6 +859,299 @@ def distill_topk_step(logits: torch.Tensor, idx: torch.Tensor, teacher: torch.Te
     _check(library().distill_topk_step(logits.data_ptr(), code, t, v, ld, idx.data_ptr(), teacher.data_ptr(), top, tau,
                                        _addr(weight), loss.data_ptr(), dz.data_ptr(), ldd, _raw_stream(dev)))
     return loss, dz
+
+
+def _call(device: torch.device, name: str, *args) -> None:
+    """A library call with the tensors' device current, on its current stream."""
+    lib = library()
+    if torch._C._cuda_getDevice() == device.index:
+        _check(getattr(lib, name)(*args, _raw_stream(device)))
+        return
+    with torch.cuda.device(device):
+        _check(getattr(lib, name)(*args, _raw_stream(device)))
+
+
+def _rows_of(t: torch.Tensor, name: str, shape=None, like: Optional[torch.Tensor] = None) -> int:
+    """The row stride of a device matrix whose rows are contiguous (any stride >= their length)."""
+    if not t.is_cuda or t.dim() != 2:
+        raise ValueError(f"{name} must be a device matrix")
+    if shape is not None and t.shape != shape:
+        raise ValueError(f"{name} must have shape {tuple(shape)} (got {tuple(t.shape)})")
+    if like is not None and (t.dtype is not like.dtype or t.device != like.device):
+        raise ValueError(f"{name} must be {like.dtype} on {like.device} (got {t.dtype} on {t.device})")
+    n, d = t.shape
+    ld, es = t.stride()
+    if es != 1 and d > 1 and n:
+        raise ValueError(f"{name} must have contiguous rows")
+    return ld if n > 1 else d
+
+
+class MoERouting(NamedTuple):
+    """The choice of experts of t tokens, `top` for each (see moe_route)."""
+    gate: torch.Tensor      # float32 [t, top]
+    losses: torch.Tensor    # float32 [2]: balance and z loss
+    idx: torch.Tensor       # int32 [t, top]: the expert of each choice, best first; -1: none
+    place: torch.Tensor     # int32 [t, top]: its row in expert order; -1: none
+    source: torch.Tensor    # int32 [t * top]: the token of every row; -1 behind the last
+    counts: torch.Tensor    # int64 [E]: the rows of every expert
+    sizes: torch.Tensor     # int64 [2]: routed tokens, rows
+    mean_p: torch.Tensor    # float32 [E]: mean probabilities
+
+
+def moe_route(logits: torch.Tensor, top: int, keep: Optional[torch.Tensor] = None,
+              renormalize: bool = True) -> MoERouting:
+    """The `top` experts of every token from the router's logits [t, E] (bfloat16 or float32, contiguous
+    rows): the largest logits, best first, ties to the lower index, -inf never. Gates are softmax
+    probabilities, over the token's own choices when renormalize. keep (bool or uint8 [t]): 0 marks padding,
+    which is not routed. losses[0] is the balance loss E sum_e share_e mean_p_e, losses[1] the mean of
+    logsumexp(logits)^2. counts, place and source are what qlora_moe_fwd_dev, moe_gather and moe_combine
+    take. Nothing waits for the device."""
+    ld = _rows_of(logits, "logits")
+    code, (t, E), dev = _dtype_code(logits, "logits"), logits.shape, logits.device
+    if keep is not None:
+        if keep.dtype is torch.bool:
+            keep = keep.view(torch.uint8)
+        _is(keep, "keep", torch.uint8, (t,), dev)
+    top = int(top)
+    if not 1 <= top <= min(16, E):
+        raise ValueError(f"top must lie in [1, min(16, E)] (got {top})")
+    place, source, idx = logits.new_empty((3, t * top), dtype=torch.int32).unbind()
+    place, idx = place.view(t, top), idx.view(t, top)
+    gate = logits.new_empty((t, top), dtype=torch.float32)
+    counts, sizes = logits.new_empty(E + 2, dtype=torch.int64).split((E, 2))
+    mean_p, losses = logits.new_empty(E + 2, dtype=torch.float32).split((E, 2))
+    wsb = _bytes_of("moe_route_workspace_bytes", t, E)
+    ws = logits.new_empty(wsb, dtype=torch.uint8) if wsb else None
+    _call(dev, "moe_route", logits.data_ptr(), code, t, E, ld, _addr(keep), top, bool(renormalize), idx.data_ptr(),
+          gate.data_ptr(), place.data_ptr(), source.data_ptr(), counts.data_ptr(), sizes.data_ptr(),
+          mean_p.data_ptr(), losses.data_ptr(), _addr(ws), wsb)
+    return MoERouting(gate, losses, idx, place, source, counts, sizes, mean_p)
+
+
+def moe_route_bwd(dgate: Optional[torch.Tensor], dlosses: Optional[torch.Tensor], logits: torch.Tensor,
+                  idx: torch.Tensor, counts: torch.Tensor, sizes: torch.Tensor, renormalize: bool = True,
+                  out: Optional[torch.Tensor] = None) -> torch.Tensor:
+    """dlogits for the gradients dgate (float32 [t, top]) and dlosses (float32 [2]) of moe_route's gates and
+    losses (None: zeros); counts are constants. out may be logits."""
+    ld = _rows_of(logits, "logits")
+    code, (t, E), dev = _dtype_code(logits, "logits"), logits.shape, logits.device
+    if idx.dim() != 2:
+        raise ValueError("idx must be [t, top]")
+    top = idx.shape[1]
+    _is(idx, "idx", torch.int32, (t, top), dev)
+    _is(counts, "counts", torch.int64, (E,), dev)
+    _is(sizes, "sizes", torch.int64, (2,), dev)
+    if dgate is not None:
+        _is(dgate, "dgate", torch.float32, (t, top), dev)
+    if dlosses is not None:
+        _is(dlosses, "dlosses", torch.float32, (2,), dev)
+    if out is None:
+        out = logits.new_empty((t, E))
+    ldd = _rows_of(out, "out", logits.shape, logits)
+    _call(dev, "moe_route_bwd", logits.data_ptr(), code, t, E, ld, top, bool(renormalize), idx.data_ptr(),
+          counts.data_ptr(), sizes.data_ptr(), _addr(dgate), _addr(dlosses), out.data_ptr(), ldd)
+    return out
+
+
+def _place_args(place: torch.Tensor, source: Optional[torch.Tensor], dev):
+    if place.dim() != 2:
+        raise ValueError("place must be [t, top]")
+    t, top = place.shape
+    _is(place, "place", torch.int32, (t, top), dev)
+    if source is not None:
+        _is(source, "source", torch.int32, (t * top,), dev)
+    return t, top
+
+
+def moe_gather(X: torch.Tensor, place: torch.Tensor, source: torch.Tensor) -> torch.Tensor:
+    """The tokens X [t, d] (bfloat16 or float32, contiguous rows) in expert order [t * top, d], once for each
+    of their choices; rows without a token are zeros. Its gradient is moe_combine(dXg, place)."""
+    ldx = _rows_of(X, "X")
+    code, dev, d = _dtype_code(X, "X"), X.device, X.shape[1]
+    t, top = _place_args(place, source, dev)
+    if X.shape[0] != t:
+        raise ValueError(f"X must have {t} rows (got {X.shape[0]})")
+    out = X.new_empty((t * top, d))
+    _call(dev, "moe_gather", X.data_ptr(), code, t, d, ldx, place.data_ptr(), source.data_ptr(), top, out.data_ptr())
+    return out
+
+
+def moe_combine(Z: torch.Tensor, place: torch.Tensor, gate: Optional[torch.Tensor] = None,
+                base: Optional[torch.Tensor] = None, out: Optional[torch.Tensor] = None) -> torch.Tensor:
+    """[t, d]: base (or 0) plus the sum of the rows of Z [t * top, d] at a token's places, times its gates
+    (None: ones). Rows of Z without a token are not read. out may be base."""
+    code, dev = _dtype_code(Z, "Z"), Z.device
+    t, top = _place_args(place, None, dev)
+    if Z.dim() != 2:
+        raise ValueError("Z must be [t * top, d]")
+    d = Z.shape[1]
+    _is(Z, "Z", Z.dtype, (t * top, d), dev)
+    if gate is not None:
+        _is(gate, "gate", torch.float32, (t, top), dev)
+    ldb = _rows_of(base, "base", (t, d), Z) if base is not None else 0
+    if out is None:
+        out = Z.new_empty((t, d))
+    ldo = _rows_of(out, "out", (t, d), Z)
+    _call(dev, "moe_combine", Z.data_ptr(), code, t, d, place.data_ptr(), top, _addr(gate), _addr(base), ldb,
+          out.data_ptr(), ldo)
+    return out
+
+
+def moe_combine_bwd(dY: torch.Tensor, Z: torch.Tensor, place: torch.Tensor, source: torch.Tensor,
+                    gate: torch.Tensor):
+    """(dZ, dgate) of moe_combine for dY [t, d] (contiguous rows): dZ [t * top, d] with zeros in rows without
+    a token, dgate float32 [t, top]. The gradient of its base is dY."""
+    code, dev = _dtype_code(Z, "Z"), Z.device
+    t, top = _place_args(place, source, dev)
+    if Z.dim() != 2:
+        raise ValueError("Z must be [t * top, d]")
+    d = Z.shape[1]
+    _is(Z, "Z", Z.dtype, (t * top, d), dev)
+    _is(gate, "gate", torch.float32, (t, top), dev)
+    ldy = _rows_of(dY, "dY", (t, d), Z)
+    dZ, dgate = torch.empty_like(Z), torch.empty_like(gate)
+    _call(dev, "moe_combine_bwd", dY.data_ptr(), code, t, d, ldy, Z.data_ptr(), place.data_ptr(), source.data_ptr(),
+          top, gate.data_ptr(), dZ.data_ptr(), dgate.data_ptr())
+    return dZ, dgate
+
+
+_ACT8_STRUCT = struct.Struct("@PPqq")
+
+
+@dataclasses.dataclass
+class Act8Tensor:
+    """An activation [rows, k] in 8 bits: signed codes, rows padded with zeros to a multiple of 64, and a scale
+    for every 64 elements of a row. It stands for codes * scale."""
+    codes: torch.Tensor     # int8 [rows, kp]
+    scale: torch.Tensor     # float32 [rows, kp / 64]
+    k: int
+
+    @property
+    def shape(self) -> Tuple[int, int]:
+        return self.codes.shape[0], self.k
+
+    @property
+    def device(self) -> torch.device:
+        return self.codes.device
+
+    def packed(self) -> bytes:
+        """The C descriptor, after its checks."""
+        rows, nb = self.codes.shape[0], (self.k + 63) // 64
+        _is(self.codes, "codes", torch.int8, (rows, 64 * nb), self.codes.device)
+        _is(self.scale, "scale", torch.float32, (rows, nb), self.codes.device)
+        return _ACT8_STRUCT.pack(self.codes.data_ptr(), self.scale.data_ptr(), rows, self.k)
+
+
+def act8_pack(X: torch.Tensor) -> Act8Tensor:
+    """X [rows, k] (bfloat16 or float32, contiguous rows) in 8 bits, blocks of 64 along a row: code =
+    127 x / max|x| to the nearest, ties to even; a block with Inf or NaN reads back as NaN."""
+    ldx = _rows_of(X, "X")
+    code, (rows, k) = _dtype_code(X, "X"), X.shape
+    if k < 1:
+        raise ValueError("X must have columns")
+    nb = (k + 63) // 64
+    q = Act8Tensor(X.new_empty((rows, 64 * nb), dtype=torch.int8), X.new_empty((rows, nb), dtype=torch.float32), k)
+    _call(X.device, "act8_pack", X.data_ptr(), code, ldx, q.packed())
+    return q
+
+
+def act8_unpack(q: Act8Tensor, dtype=torch.bfloat16, out: Optional[torch.Tensor] = None) -> torch.Tensor:
+    """What q stands for [rows, k], as bfloat16 (rounded) or float32."""
+    if out is None:
+        if dtype is not torch.bfloat16 and dtype is not torch.float32:
+            raise ValueError("dtype must be bfloat16 or float32")
+        out = q.scale.new_empty(q.shape, dtype=dtype)
+    ldx = _rows_of(out, "out", q.shape)
+    if out.device != q.device:
+        raise ValueError(f"out must be on {q.device} (got {out.device})")
+    _call(q.device, "act8_unpack", q.packed(), out.data_ptr(), _dtype_code(out, "out"), ldx)
+    return out
+
+
+def _act8_layer(X: Act8Tensor, q: NF4Tensor, A, B, T, rows: int, experts: int = 1, pair: bool = False):
+    """The rank, after the checks that the 8-bit forms of the backward passes share; rows of T and dY."""
+    dev, r = X.device, 0 if A is None else A.shape[0] // experts
+    if X.k != q.k:
+        raise ValueError(f"X must have k = {q.k} (got {X.k})")
+    if q.codes.device != dev:
+        raise ValueError(f"q must be on {dev} (got {q.codes.device})")
+    if r:
+        if T is None:
+            raise ValueError("T must be given with X in 8 bits")
+        _is(A, "A", torch.bfloat16, (experts * r, q.k), dev)
+        if not pair:
+            _is(B, "B", torch.bfloat16, (q.n, r), dev)
+        _is(T, "T", torch.bfloat16, (rows, r), dev)
+    return dev, r
+
+
+def qlora_bwd_act8(dY: torch.Tensor, X: Act8Tensor, q: NF4Tensor, A: Optional[torch.Tensor],
+                   B: Optional[torch.Tensor], s: float, T: Optional[torch.Tensor], need_dx: bool = True):
+    """(dX, dA, dB) of the layer from X in 8 bits (act8_pack) and T from the forward: dA is the sum over what
+    the codes stand for, dX and dB are qlora_bwd's."""
+    m = X.shape[0]
+    dev, r = _act8_layer(X, q, A, B, T, m)
+    _is(dY, "dY", torch.bfloat16, (m, q.n), dev)
+    dX = dY.new_empty((m, q.k)) if need_dx else None
+    dA, dB = (torch.empty_like(A), torch.empty_like(B)) if r else (None, None)
+    wsb = _bytes_of("qlora_bwd_workspace_bytes", m, q.n, q.k, r)
+    ws = dY.new_empty(max(wsb, 1), dtype=torch.uint8)
+    _call(dev, "qlora_bwd_act8", dY.data_ptr(), X.packed(), _packed(q), _addr(A if r else None), _addr(B if r else None),
+          r, float(s), _addr(T if r else None), _addr(dX), _addr(dA), _addr(dB), ws.data_ptr(), wsb)
+    return dX, dA, dB
+
+
+def qlora_swiglu_bwd_act8(dH: torch.Tensor, X: Act8Tensor, q: NF4Tensor, Agu: Optional[torch.Tensor],
+                          Bg: Optional[torch.Tensor], Bu: Optional[torch.Tensor], s: float, Ygu: Act8Tensor,
+                          Tgu: Optional[torch.Tensor], need_dx: bool = True):
+    """(dX, dAgu, dBg, dBu) of the gate/up pair from X and Ygu in 8 bits (act8_pack) and Tgu from the forward."""
+    if q.n % 2:
+        raise ValueError("the gate/up weight must hold 2n rows (gate rows, then up rows)")
+    m, n = X.shape[0], q.n // 2
+    dev, r2 = _act8_layer(X, q, Agu, None, Tgu, m, pair=True)
+    r = r2 // 2
+    if r2 % 2:
+        raise ValueError("Agu must hold 2r rows (gate, then up)")
+    if r:
+        _is(Bg, "Bg", torch.bfloat16, (n, r), dev)
+        _is(Bu, "Bu", torch.bfloat16, (n, r), dev)
+    if Ygu.shape != (m, 2 * n) or Ygu.device != dev:
+        raise ValueError(f"Ygu must be [{m}, {2 * n}] on {dev}")
+    _is(dH, "dH", torch.bfloat16, (m, n), dev)
+    dX = dH.new_empty((m, q.k)) if need_dx else None
+    dA, dBg, dBu = (torch.empty_like(Agu), torch.empty_like(Bg), torch.empty_like(Bu)) if r else (None,) * 3
+    wsb = _bytes_of("qlora_swiglu_workspace_bytes", m, n, q.k, r)
+    ws = dH.new_empty(max(wsb, 1), dtype=torch.uint8)
+    on = lambda t: _addr(t if r else None)
+    _call(dev, "qlora_swiglu_bwd_act8", dH.data_ptr(), X.packed(), _packed(q), on(Agu), on(Bg), on(Bu), r, float(s),
+          Ygu.packed(), on(Tgu), _addr(dX), _addr(dA), _addr(dBg), _addr(dBu), ws.data_ptr(), wsb)
+    return dX, dA, dBg, dBu
+
+
+def qlora_moe_bwd_act8(dY: torch.Tensor, X: Act8Tensor, source: Optional[torch.Tensor], counts: torch.Tensor,
+                       q: NF4Tensor, A: Optional[torch.Tensor], B: Optional[torch.Tensor], s: float,
+                       T: Optional[torch.Tensor], need_dx: bool = True):
+    """(dX, dA, dB) of the grouped layer with the routing on the device (qlora_moe_bwd_dev) from X in 8 bits:
+    the tokens' activations, kept once, with source (int32 [m], moe_route's) the token of every grouped row;
+    source None: X holds the grouped rows. dY [m, n] and T [m, r] are grouped, counts int64 [E]."""
+    dev, E, m = X.device, counts.numel(), dY.shape[0]
+    _is(counts, "counts", torch.int64, (E,), dev)
+    if E < 1 or q.n % E:
+        raise ValueError("the stacked weight must hold E*n rows for E = counts.numel() experts")
+    _, r = _act8_layer(X, q, A, B, T, m, E)
+    _is(dY, "dY", torch.bfloat16, (m, q.n // E), dev)
+    if source is not None:
+        _is(source, "source", torch.int32, (m,), dev)
+    elif X.shape[0] != m:
+        raise ValueError(f"X must hold {m} rows without a source (got {X.shape[0]})")
+    dX = dY.new_empty((m, q.k)) if need_dx else None
+    dA, dB = (torch.empty_like(A), torch.empty_like(B)) if r else (None, None)
+    wsb = _bytes_of("qlora_moe_workspace_bytes_dev", m, E, q.n // E, q.k, r)
+    ws = dY.new_empty(max(wsb, 1), dtype=torch.uint8)
+    on = lambda t: _addr(t if r else None)
+    _call(dev, "qlora_moe_bwd_dev_act8", dY.data_ptr(), X.packed(), _addr(source), m, counts.data_ptr(), E, _packed(q),
+          on(A), on(B), r, float(s), on(T), _addr(dX), _addr(dA), _addr(dB), ws.data_ptr(), wsb)
+    return dX, dA, dB
 
 
 class QLoRALinearFunction(torch.autograd.Function):

@@ -1,0 +1,451 @@
+// Activations kept in 8 bits for the backward pass (gfx950).
+//
+// A row is cut into blocks of 64 elements (the last may be short; code rows are padded with zeros to a
+// multiple of 64). With a = max |x| of a block,
+//
+//   code = 127 x / a rounded to the nearest integer, ties to even;   scale = fl32(a / 127)
+//
+// and the block stands for fl32(code scale): at most a / 254 (half a step) from x, up to the rounding of
+// the scale. A block whose a is below 2^-119 is stored as zeros, so that 127 / a is finite; one with an Inf
+// or NaN gets the scale NaN, so that whatever uses it is NaN.
+//
+// act8_pack and act8_unpack read and write each element once and are bound by memory. Where the layer's
+// backward pass uses the kept activation, the codes are read in its place, decoded on the way into the
+// matrix cores or the activation's derivative, and never expanded in memory.
+#include "common.h"
+#include "launch.h"
+
+namespace nf4q {
+namespace {
+
+typedef __attribute__((ext_vector_type(2))) uint16_t u16x2;
+
+// ---------------------------------------------------------------------------------- pack, unpack
+// The 16 elements of a thread as words (bf16 pairs, or float32).
+template <typename XT>
+struct Piece {
+  static constexpr int kWords = 16 * (int)sizeof(XT) / 4;
+  uint32_t w[kWords];
+};
+
+// Bits of the largest |x| (as of float32): an unsigned maximum, in which Inf and NaN come last.
+__device__ __forceinline__ uint32_t top_bits(const Piece<uint16_t> &p) {
+  u16x2 m = {0, 0};
+#pragma unroll
+  for (int i = 0; i < 8; ++i) m = __builtin_elementwise_max(m, __builtin_bit_cast(u16x2, p.w[i] & 0x7FFF7FFFu));
+  return (uint32_t)(m[0] > m[1] ? m[0] : m[1]) << 16;
+}
+__device__ __forceinline__ uint32_t top_bits(const Piece<float> &p) {
+  uint32_t m = 0;
+#pragma unroll
+  for (int i = 0; i < 16; ++i) {
+    const uint32_t b = p.w[i] & 0x7FFFFFFFu;
+    m = b > m ? b : m;
+  }
+  return m;
+}
+__device__ __forceinline__ uint32_t umax(uint32_t a, uint32_t b) { return a > b ? a : b; }
+
+// The code of a float32 x whose 127 x / a may lie too close to a border for float32: compared there with
+// the border in float64, where both sides are exact.
+__device__ __forceinline__ int code_at_border(float x, float a, float t) {
+  const double h = floor(fabs((double)t));              // between h and h + 1, |t| near h + 1/2
+  const double d = 254.0 * fabs((double)x) - (2.0 * h + 1.0) * (double)a;
+  const int c = (int)h + (d > 0.0 || (d == 0.0 && ((int)h & 1)) ? 1 : 0);
+  return x < 0.f ? -c : c;
+}
+
+// Codes by one fused multiply-add each: x inv + 1.5 2^23 is rounded, ties to even, at the integers, which
+// leaves the code in the low bits. inv is 127 / a rounded up. For bf16 x and a that gives the exact code:
+// 127 x / a differs from a half-integer, if at all, by more than 2^-17 of itself (its distance times 2 a is
+// an integer multiple of the last bits of both 8-bit significands), far above the 2^-23 of inv; and where it
+// is a half-integer, either 127 / a is exact (a = 127 2^i) and the tie goes to even, or x = +-a / 2, and the
+// rounded-up inv takes 63.5 to 64, which is even.
+constexpr float kRound = 12582912.f;
+
+template <typename XT>
+__device__ __forceinline__ uint32_t four_codes(const Piece<XT> &p, int i, float inv, float a) {
+  uint32_t c[4];
+#pragma unroll
+  for (int e = 0; e < 4; ++e) {
+    if constexpr (sizeof(XT) == 2) {
+      const uint32_t w = p.w[2 * i + (e >> 1)];
+      c[e] = __float_as_uint(__builtin_fmaf((e & 1) ? bf16_hi(w) : bf16_lo(w), inv, kRound));
+    } else {
+      const float x = __uint_as_float(p.w[4 * i + e]);
+      c[e] = __float_as_uint(__builtin_fmaf(x, inv, kRound));
+      // t is off by at most 2^-15; rare (about 2^-14 of the elements), so the branch costs next to nothing
+      const float t = x * inv;
+      if (fabsf(fabsf(t - rintf(t)) - 0.5f) < 0x1p-14f) c[e] = (uint32_t)code_at_border(x, a, t);
+    }
+  }
+  return perm(perm(c[3], c[2], 0x0C0C0400u), perm(c[1], c[0], 0x0C0C0400u), 0x05040100u);
+}
+
+// A thread packs 16 elements; four lanes make a block. kVec: whole 16-byte loads (k, ldx and the base allow
+// them); otherwise element by element.
+template <typename XT, bool kVec>
+__global__ __launch_bounds__(256) void act8_pack_kernel(const XT *__restrict__ x, int64_t ldx, Act8 q) {
+  const uint32_t pieces = (uint32_t)(q.kp / 16);
+  const int64_t first = (int64_t)blockIdx.x * 256, row0 = first / pieces;
+  const uint32_t at = (uint32_t)(first - row0 * pieces) + threadIdx.x;
+  const int64_t row = row0 + at / pieces;
+  const int64_t c = (int64_t)(at % pieces) * 16;
+  const bool live = row < q.rows;         // whole blocks of four lanes
+  Piece<XT> p;
+  const XT *src = x + row * ldx + c;
+  if constexpr (kVec) {
+#pragma unroll
+    for (int i = 0; i < Piece<XT>::kWords / 4; ++i) {
+      u32x4 v = {0, 0, 0, 0};
+      if (live && c + i * (16 / (int)sizeof(XT)) < q.k) v = *(reinterpret_cast<const u32x4 *>(src) + i);
+#pragma unroll
+      for (int e = 0; e < 4; ++e) p.w[4 * i + e] = v[e];
+    }
+  } else {
+#pragma unroll
+    for (int e = 0; e < 16; ++e) {
+      uint32_t v = 0;
+      if (live && c + e < q.k) {
+        if constexpr (sizeof(XT) == 2) v = src[e];
+        else v = __float_as_uint(src[e]);
+      }
+      if constexpr (sizeof(XT) == 2) p.w[e / 2] = (e & 1) ? (p.w[e / 2] | (v << 16)) : v;
+      else p.w[e] = v;
+    }
+  }
+  uint32_t m = top_bits(p);
+  m = umax(m, (uint32_t)__builtin_amdgcn_mov_dpp((int)m, 0xB1, 0xF, 0xF, true));   // lanes 1, 0, 3, 2
+  m = umax(m, (uint32_t)__builtin_amdgcn_mov_dpp((int)m, 0x4E, 0xF, 0xF, true));   // lanes 2, 3, 0, 1
+  if (!live) return;
+  const float a = __uint_as_float(m);
+  u32x4 codes = {0, 0, 0, 0};
+  float scale = 0.f;
+  if (m >= 0x7F800000u) {
+    scale = __uint_as_float(0x7FC00000u);
+  } else if (a >= 0x1p-119f) {
+    scale = a / 127.f;
+    float inv = 127.f / a;
+    if (__builtin_fmaf(-inv, a, 127.f) > 0.f) inv = __uint_as_float(__float_as_uint(inv) + 1);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) codes[i] = four_codes<XT>(p, i, inv, a);
+  }
+  *reinterpret_cast<u32x4 *>(q.codes + row * q.kp + c) = codes;
+  if ((threadIdx.x & 3) == 0) q.scale[row * (q.kp / kAct8Block) + c / kAct8Block] = scale;
+}
+
+// Byte e of a word of codes, with its sign bit flipped beforehand, as the value (u - 128) scale: one
+// conversion and one fused multiply-add, rounded as the product is (128 scale is exact).
+__device__ __forceinline__ float code_value(uint32_t flipped, int e, float scale, float off) {
+  return __builtin_fmaf((float)((flipped >> (8 * e)) & 0xFFu), scale, off);
+}
+
+template <typename XT, bool kVec>
+__global__ __launch_bounds__(256) void act8_unpack_kernel(Act8 q, XT *__restrict__ x, int64_t ldx) {
+  const uint32_t pieces = (uint32_t)(q.kp / 16);
+  const int64_t first = (int64_t)blockIdx.x * 256, row0 = first / pieces;
+  const uint32_t at = (uint32_t)(first - row0 * pieces) + threadIdx.x;
+  const int64_t row = row0 + at / pieces;
+  const int64_t c = (int64_t)(at % pieces) * 16;
+  if (row >= q.rows) return;
+  const u32x4 codes = *reinterpret_cast<const u32x4 *>(q.codes + row * q.kp + c);
+  const float scale = q.scale[row * (q.kp / kAct8Block) + c / kAct8Block], off = -128.f * scale;
+  float v[16];
+#pragma unroll
+  for (int e = 0; e < 16; ++e) v[e] = code_value(codes[e >> 2] ^ 0x80808080u, e & 3, scale, off);
+  XT *dst = x + row * ldx + c;
+  if constexpr (kVec) {
+    constexpr int P = 16 / (int)sizeof(XT);
+#pragma unroll
+    for (int i = 0; i < 16 / P; ++i) {
+      u32x4 o;
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        if constexpr (sizeof(XT) == 2) o[e] = pack_bf16x2(v[P * i + 2 * e], v[P * i + 2 * e + 1]);
+        else o[e] = __float_as_uint(v[P * i + e]);
+      }
+      if (c + i * P < q.k) *(reinterpret_cast<u32x4 *>(dst) + i) = o;
+    }
+  } else {
+#pragma unroll
+    for (int e = 0; e < 16; ++e)
+      if (c + e < q.k) {
+        if constexpr (sizeof(XT) == 2) dst[e] = (uint16_t)(pack_bf16x2(v[e], 0.f) & 0xFFFFu);
+        else dst[e] = v[e];
+      }
+  }
+}
+
+// ---------------------------------------------------------------------------------- sums over rows
+// out[j][c] = sum over m of P[m][j] Q[m][c], Q in 8 bits, rounded to bf16 as the bf16 activation would be:
+// the sums over the rows of lora.hip with the codes decoded on their way into LDS. Workgroup: 128 columns x
+// all r (<= 128) rows j over one split of the rows, in stages of 64 rows loaded two stages ahead.
+constexpr int kBM = 64, kBC = 128, kQRow = kBC + 16;
+typedef __attribute__((ext_vector_type(4))) short s16x4;
+typedef __attribute__((ext_vector_type(8))) short s16x8;
+
+__device__ __forceinline__ s16x4 lds_tr16(const uint16_t *p) {
+  return __builtin_amdgcn_ds_read_tr16_b64_v4i16((__attribute__((address_space(3))) s16x4 *)(p));
+}
+
+// kGrp: one sum for each expert blockIdx.z over its own rows.
+template <int TJ, bool kGrp>
+__device__ __forceinline__ void mreduce_act8_body(const uint16_t *__restrict__ P, const Act8 &q,
+                                                  const int *__restrict__ map, int64_t M, int r, int64_t msplit,
+                                                  float *__restrict__ part, const GroupArgs &gr) {
+  constexpr int PROW = TJ * 16 + 16;          // P row stride in bf16 (padded by 32 bytes)
+  __shared__ __align__(16) uint16_t sQ[2][kBM * kQRow];
+  __shared__ __align__(16) uint16_t sP[2][kBM * PROW];
+  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+  const int64_t c0 = (int64_t)blockIdx.x * kBC, C = q.k;
+  const int split = blockIdx.y;
+  int64_t lo = 0, hi = M;
+  if (kGrp) {
+    lo = grp_m_off(gr, blockIdx.z);
+    hi = grp_m_off(gr, blockIdx.z + 1);
+    msplit = (hi - lo + gridDim.y - 1) / gridDim.y;
+    msplit = (msplit + kBM - 1) / kBM * kBM;
+  }
+  const int64_t mb = lo + split * msplit;
+  const int64_t me = (mb + msplit < hi) ? mb + msplit : hi;
+  const bool pvec = (r & 7) == 0;
+  const int64_t nb = q.kp / kAct8Block;
+
+  f32x4 acc[TJ][2];
+#pragma unroll
+  for (int t = 0; t < TJ; ++t)
+#pragma unroll
+    for (int u = 0; u < 2; ++u) acc[t][u] = f32x4{0.f, 0.f, 0.f, 0.f};
+
+  struct Stage {
+    u32x4 q[2];
+    float s[2];
+    uint4 p[(TJ + 1) / 2];
+  };
+  auto load = [&](int64_t ms, Stage &st) {
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      const int k = tid + 256 * i;                   // chunk k of 16 codes: row k / 8
+      const int64_t m = ms + (k >> 3), c = c0 + (k & 7) * 16;
+      int64_t row = m < me ? (map ? map[m] : m) : -1;
+      if (row < 0 || row >= q.rows || c >= q.kp) {
+        st.q[i] = u32x4{0, 0, 0, 0};
+        st.s[i] = 0.f;
+      } else {
+        st.q[i] = *reinterpret_cast<const u32x4 *>(q.codes + row * q.kp + c);
+        st.s[i] = q.scale[row * nb + c / kAct8Block];
+      }
+    }
+    if (pvec) {
+#pragma unroll
+      for (int i = 0; i < (TJ + 1) / 2; ++i) {
+        const int k = tid + 256 * i;                 // chunk k of the P tile: row k / (2 TJ)
+        const int row = k / (2 * TJ), j = k % (2 * TJ) * 8;
+        const int64_t m = ms + row;
+        st.p[i] = (row < kBM && m < me && j < r) ? *reinterpret_cast<const uint4 *>(P + m * r + j)
+                                                 : make_uint4(0, 0, 0, 0);
+      }
+    }
+  };
+  auto store = [&](int64_t ms, const Stage &st, int buf) {
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      const int k = tid + 256 * i;
+      const float off = -128.f * st.s[i];
+      u32x4 o[2];
+#pragma unroll
+      for (int w = 0; w < 4; ++w) {
+        const uint32_t f = st.q[i][w] ^ 0x80808080u;
+#pragma unroll
+        for (int h = 0; h < 2; ++h)
+          o[w >> 1][2 * (w & 1) + h] = pack_bf16x2(code_value(f, 2 * h, st.s[i], off), code_value(f, 2 * h + 1, st.s[i], off));
+      }
+      u32x4 *d = reinterpret_cast<u32x4 *>(&sQ[buf][(k >> 3) * kQRow + (k & 7) * 16]);
+      d[0] = o[0];
+      d[1] = o[1];
+    }
+    if (pvec) {
+#pragma unroll
+      for (int i = 0; i < (TJ + 1) / 2; ++i) {
+        const int k = tid + 256 * i;
+        const int row = k / (2 * TJ), ch = k % (2 * TJ);
+        if (row < kBM) *reinterpret_cast<uint4 *>(&sP[buf][row * PROW + ch * 8]) = st.p[i];
+      }
+    } else {
+      for (int k = tid; k < kBM * TJ * 16; k += 256) {
+        const int row = k / (TJ * 16), j = k % (TJ * 16);
+        const int64_t m = ms + row;
+        sP[buf][row * PROW + j] = (m < me && j < r) ? P[m * r + j] : (uint16_t)0;
+      }
+    }
+  };
+  const int g16 = lane >> 4, l16 = lane & 15;
+  auto frag = [&](const uint16_t *S, int rowstride, int colbase, int kslice) {
+    const int m0 = kslice * 32 + g16 * 8 + (l16 >> 2);
+    const int col = colbase + 4 * (l16 & 3);
+    const s16x4 a = lds_tr16(S + m0 * rowstride + col);
+    const s16x4 b = lds_tr16(S + (m0 + 4) * rowstride + col);
+    const s16x8 v = {a[0], a[1], a[2], a[3], b[0], b[1], b[2], b[3]};
+    return __builtin_bit_cast(bf16x8, v);
+  };
+  auto mma = [&](int buf) {
+#pragma unroll
+    for (int ks = 0; ks < 2; ++ks) {
+      bf16x8 bq[2];
+#pragma unroll
+      for (int u = 0; u < 2; ++u) bq[u] = frag(sQ[buf], kQRow, wave * 32 + u * 16, ks);
+#pragma unroll
+      for (int t = 0; t < TJ; ++t) {
+        const bf16x8 ap = frag(sP[buf], PROW, t * 16, ks);
+#pragma unroll
+        for (int u = 0; u < 2; ++u) acc[t][u] = mfma16x16x32(ap, bq[u], acc[t][u]);
+      }
+    }
+  };
+
+  const int64_t nst = (me > mb) ? (me - mb + kBM - 1) / kBM : 0;
+  Stage s0, s1;
+  if (nst > 0) load(mb, s0);
+  if (nst > 1) load(mb + kBM, s1);
+  if (nst > 0) store(mb, s0, 0);
+  __syncthreads();
+#pragma unroll 1
+  for (int64_t i = 0; i < nst; i += 2) {
+    if (i + 2 < nst) load(mb + (i + 2) * kBM, s0);
+    mma(0);
+    if (i + 1 < nst) store(mb + (i + 1) * kBM, s1, 1);
+    __syncthreads();
+    if (i + 1 >= nst) break;
+    if (i + 3 < nst) load(mb + (i + 3) * kBM, s1);
+    mma(1);
+    if (i + 2 < nst) store(mb + (i + 2) * kBM, s0, 0);
+    __syncthreads();
+  }
+
+#pragma unroll
+  for (int t = 0; t < TJ; ++t)
+#pragma unroll
+    for (int u = 0; u < 2; ++u)
+#pragma unroll
+      for (int v = 0; v < 4; ++v) {
+        const int j = t * 16 + 4 * g16 + v;
+        const int64_t c = c0 + wave * 32 + u * 16 + l16;
+        if (j < r && c < C) part[(((int64_t)blockIdx.z * gridDim.y + split) * r + j) * C + c] = acc[t][u][v];
+      }
+}
+
+template <int TJ>
+__global__ __launch_bounds__(256) void mreduce_act8_kernel(const uint16_t *__restrict__ P, Act8 q,
+                                                           const int *__restrict__ map, int64_t M, int r,
+                                                           int64_t msplit, float *__restrict__ part) {
+  mreduce_act8_body<TJ, false>(P, q, map, M, r, msplit, part, GroupArgs{});
+}
+
+template <int TJ>
+__global__ __launch_bounds__(256) void mreduce_act8_grouped_kernel(const uint16_t *__restrict__ P, Act8 q,
+                                                                   const int *__restrict__ map, int r,
+                                                                   float *__restrict__ part, GroupArgs gr) {
+  mreduce_act8_body<TJ, true>(P, q, map, 0, r, 0, part, gr);
+}
+
+// ---------------------------------------------------------------------------------- gate/up pair
+__device__ __forceinline__ float sigmoid(float x) { return 1.f / (1.f + __expf(-x)); }
+
+// dYg = dH Yu silu'(Yg), dYu = dH silu(Yg), as in swiglu.hip, with Yg and Yu (2n columns a row) in 8 bits.
+// A piece is 8 columns; n % 8 == 0, so that each lies in one block.
+__global__ __launch_bounds__(256) void swiglu_bwd_act8_kernel(const uint16_t *__restrict__ dh, Act8 y, int64_t n,
+                                                              uint16_t *__restrict__ dygu) {
+  const int64_t pieces = n / 8, total = y.rows * pieces, nb = y.kp / kAct8Block;
+  for (int64_t i = blockIdx.x * (int64_t)blockDim.x + threadIdx.x; i < total; i += (int64_t)gridDim.x * blockDim.x) {
+    const int64_t row = i / pieces, c = (i - row * pieces) * 8;
+    const u32x4 d = *reinterpret_cast<const u32x4 *>(dh + row * n + c);
+    const u32x2 g = *reinterpret_cast<const u32x2 *>(y.codes + row * y.kp + c);
+    const u32x2 u = *reinterpret_cast<const u32x2 *>(y.codes + row * y.kp + n + c);
+    const float sg = y.scale[row * nb + c / kAct8Block], su = y.scale[row * nb + (n + c) / kAct8Block];
+    u32x4 og, ou;
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      float rg[2], ru[2];
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        const float dv = h ? bf16_hi(d[e]) : bf16_lo(d[e]);
+        const float gv = code_value(g[e >> 1] ^ 0x80808080u, 2 * (e & 1) + h, sg, -128.f * sg);
+        const float uv = code_value(u[e >> 1] ^ 0x80808080u, 2 * (e & 1) + h, su, -128.f * su);
+        const float s = sigmoid(gv);
+        rg[h] = dv * uv * (s * (1.f + gv * (1.f - s)));
+        ru[h] = dv * (gv * s);
+      }
+      og[e] = pack_bf16x2(rg[0], rg[1]);
+      ou[e] = pack_bf16x2(ru[0], ru[1]);
+    }
+    *reinterpret_cast<u32x4 *>(dygu + row * 2 * n + c) = og;
+    *reinterpret_cast<u32x4 *>(dygu + row * 2 * n + n + c) = ou;
+  }
+}
+
+bool vec_rows(const void *x, int64_t ldx, int64_t k, size_t esz) {
+  return (((uintptr_t)x | (uintptr_t)(ldx * (int64_t)esz) | (uintptr_t)(k * (int64_t)esz)) & 15) == 0;
+}
+
+}  // namespace
+
+hipError_t launch_act8_pack(const void *x, bool f32, int64_t ldx, const Act8 &q, hipStream_t st) {
+  const int64_t blocks = (q.rows * (q.kp / 16) + 255) / 256;
+  if (blocks > 0x7FFFFFFF) return hipErrorInvalidValue;
+  const dim3 g((unsigned)blocks), b(256);
+  const bool vec = vec_rows(x, ldx, q.k, f32 ? 4 : 2);
+  if (f32) {
+    if (vec) act8_pack_kernel<float, true><<<g, b, 0, st>>>((const float *)x, ldx, q);
+    else act8_pack_kernel<float, false><<<g, b, 0, st>>>((const float *)x, ldx, q);
+  } else {
+    if (vec) act8_pack_kernel<uint16_t, true><<<g, b, 0, st>>>((const uint16_t *)x, ldx, q);
+    else act8_pack_kernel<uint16_t, false><<<g, b, 0, st>>>((const uint16_t *)x, ldx, q);
+  }
+  return hipGetLastError();
+}
+
+hipError_t launch_act8_unpack(const Act8 &q, void *x, bool f32, int64_t ldx, hipStream_t st) {
+  const int64_t blocks = (q.rows * (q.kp / 16) + 255) / 256;
+  if (blocks > 0x7FFFFFFF) return hipErrorInvalidValue;
+  const dim3 g((unsigned)blocks), b(256);
+  const bool vec = vec_rows(x, ldx, q.k, f32 ? 4 : 2);
+  if (f32) {
+    if (vec) act8_unpack_kernel<float, true><<<g, b, 0, st>>>(q, (float *)x, ldx);
+    else act8_unpack_kernel<float, false><<<g, b, 0, st>>>(q, (float *)x, ldx);
+  } else {
+    if (vec) act8_unpack_kernel<uint16_t, true><<<g, b, 0, st>>>(q, (uint16_t *)x, ldx);
+    else act8_unpack_kernel<uint16_t, false><<<g, b, 0, st>>>(q, (uint16_t *)x, ldx);
+  }
+  return hipGetLastError();
+}
+
+hipError_t launch_mreduce_act8(const uint16_t *P, const Act8 &q, const int *map, int64_t M, int r, float s, int splits,
+                               float *part, uint16_t *out, const GroupArgs *gr, hipStream_t st) {
+  int64_t msplit = (M + splits - 1) / splits;
+  msplit = (msplit + kBM - 1) / kBM * kBM;
+  const int E = gr ? gr->E : 1;
+  const dim3 grid((unsigned)((q.k + kBC - 1) / kBC), (unsigned)splits, (unsigned)E);
+  switch ((r + 15) / 16) {
+#define MR_CASE(T)                                                                                             \
+  case T:                                                                                                      \
+    if (gr) mreduce_act8_grouped_kernel<T><<<grid, dim3(256), 0, st>>>(P, q, map, r, part, *gr);               \
+    else mreduce_act8_kernel<T><<<grid, dim3(256), 0, st>>>(P, q, map, M, r, msplit, part);                    \
+    break;
+    MR_CASE(1) MR_CASE(2) MR_CASE(3) MR_CASE(4) MR_CASE(5) MR_CASE(6) MR_CASE(7) MR_CASE(8)
+#undef MR_CASE
+    default: return hipErrorInvalidValue;
+  }
+  const hipError_t e = hipGetLastError();
+  if (e != hipSuccess) return e;
+  return launch_mreduce_final(part, q.k, r, splits, E, s, false, out, st);
+}
+
+hipError_t launch_swiglu_bwd_act8(const uint16_t *dh, const Act8 &ygu, int64_t n, uint16_t *dygu, hipStream_t st) {
+  if (n % 8) return hipErrorInvalidValue;
+  int64_t b = (ygu.rows * n / 8 + 255) / 256;
+  if (b > 8192) b = 8192;
+  swiglu_bwd_act8_kernel<<<dim3((unsigned)(b < 1 ? 1 : b)), dim3(256), 0, st>>>(dh, ygu, n, dygu);
+  return hipGetLastError();
+}
+
+}  // namespace nf4q

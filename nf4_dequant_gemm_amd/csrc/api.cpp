@@ -612,9 +612,14 @@ size_t qlora_bwd_workspace_bytes(int64_t m, int64_t n, int64_t k, int32_t r) {
   return bwd_ws(m, n, k, r).total;
 }
 
-int qlora_bwd(const void *dY, const void *X, int64_t m, const nf4_tensor *W, const void *A,
-              const void *B, int32_t r, float s, const void *T, void *dX, void *dA, void *dB,
-              void *ws, size_t ws_bytes, void *stream) {
+}  // extern "C"
+
+namespace {
+
+// The backward pass with X in bf16, or (x8 given, X its codes) in 8 bits; T is then given where r > 0.
+int bwd_impl(const void *dY, const void *X, const nf4q::Act8 *x8, int64_t m, const nf4_tensor *W, const void *A,
+             const void *B, int32_t r, float s, const void *T, void *dX, void *dA, void *dB,
+             void *ws, size_t ws_bytes, void *stream) {
   int st = check_layer(X, m, W, A, B, r);
   if (st) return st;
   if (!dY || !aligned16(dY)) return fail(NF4_EINVAL, "dY must be non-NULL and 16-byte aligned");
@@ -656,14 +661,25 @@ int qlora_bwd(const void *dY, const void *X, int64_t m, const nf4_tensor *W, con
     if (e != hipSuccess) return hip_status(e, "qlora_bwd dX launch");
   }
   if (r > 0) {
-    e = nf4q::launch_mreduce(U, (const uint16_t *)X, k, m, k, r, s, lay.splits_a, part,
-                             (uint16_t *)dA, false, sm);
+    e = x8 ? nf4q::launch_mreduce_act8(U, *x8, nullptr, m, r, s, lay.splits_a, part, (uint16_t *)dA, nullptr, sm)
+           : nf4q::launch_mreduce(U, (const uint16_t *)X, k, m, k, r, s, lay.splits_a, part,
+                                  (uint16_t *)dA, false, sm);
     if (e != hipSuccess) return hip_status(e, "qlora_bwd dA launch");
     e = nf4q::launch_mreduce((const uint16_t *)T, dy, n, m, n, r, s, lay.splits_b, part,
                              (uint16_t *)dB, true, sm);
     if (e != hipSuccess) return hip_status(e, "qlora_bwd dB launch");
   }
   return ok();
+}
+
+}  // namespace
+
+extern "C" {
+
+int qlora_bwd(const void *dY, const void *X, int64_t m, const nf4_tensor *W, const void *A,
+              const void *B, int32_t r, float s, const void *T, void *dX, void *dA, void *dB,
+              void *ws, size_t ws_bytes, void *stream) {
+  return bwd_impl(dY, X, nullptr, m, W, A, B, r, s, T, dX, dA, dB, ws, ws_bytes, stream);
 }
 
 size_t qlora_swiglu_workspace_bytes(int64_t m, int64_t n, int64_t k, int32_t r) {
@@ -756,10 +772,15 @@ int qlora_swiglu_fwd_fused(const void *X, int64_t m, const nf4_tensor *Wgu, cons
                             "qlora_swiglu_fwd_fused launch");
 }
 
-int qlora_swiglu_bwd(const void *dH, const void *X, int64_t m, const nf4_tensor *Wgu,
-                     const void *Agu, const void *Bg, const void *Bu, int32_t r, float s,
-                     const void *Ygu, const void *Tgu, void *dX, void *dAgu, void *dBg, void *dBu,
-                     void *ws, size_t ws_bytes, void *stream) {
+}  // extern "C"
+
+namespace {
+
+// The pair's backward pass with X and Ygu in bf16, or (x8 and y8 given, X and Ygu their codes) in 8 bits.
+int swiglu_bwd_impl(const void *dH, const void *X, const nf4q::Act8 *x8, int64_t m, const nf4_tensor *Wgu,
+                    const void *Agu, const void *Bg, const void *Bu, int32_t r, float s,
+                    const void *Ygu, const nf4q::Act8 *y8, const void *Tgu, void *dX, void *dAgu, void *dBg, void *dBu,
+                    void *ws, size_t ws_bytes, void *stream) {
   size_t need = 0;
   int st = check_swiglu(X, m, Wgu, Agu, Bg, Bu, r, ws, ws_bytes, &need);
   if (st) return st;
@@ -779,19 +800,32 @@ int qlora_swiglu_bwd(const void *dH, const void *X, int64_t m, const nf4_tensor 
   uint16_t *B2 = r > 0 ? (uint16_t *)base : nullptr;
   uint16_t *dY2 = (uint16_t *)(base + lay.b2);
   uint16_t *dB2 = r > 0 ? (uint16_t *)(base + lay.b2 + lay.dy2) : nullptr;
-  hipError_t e = nf4q::launch_swiglu_bwd((const uint16_t *)dH, (const uint16_t *)Ygu, m, n, dY2, sm);
+  hipError_t e = y8 ? nf4q::launch_swiglu_bwd_act8((const uint16_t *)dH, *y8, n, dY2, sm)
+                    : nf4q::launch_swiglu_bwd((const uint16_t *)dH, (const uint16_t *)Ygu, m, n, dY2, sm);
   if (e != hipSuccess) return hip_status(e, "qlora_swiglu_bwd launch");
   if (r > 0) {
     e = nf4q::launch_blockdiag((const uint16_t *)Bg, (const uint16_t *)Bu, n, r, B2, sm);
     if (e != hipSuccess) return hip_status(e, "qlora_swiglu_bwd launch");
   }
-  st = qlora_bwd(dY2, X, m, Wgu, r > 0 ? Agu : nullptr, B2, 2 * r, s, r > 0 ? Tgu : nullptr, dX,
-                 r > 0 ? dAgu : nullptr, dB2, base + lay.b2 + lay.dy2 + lay.db2, lay.bwd, stream);
+  st = bwd_impl(dY2, X, x8, m, Wgu, r > 0 ? Agu : nullptr, B2, 2 * r, s, r > 0 ? Tgu : nullptr, dX,
+                r > 0 ? dAgu : nullptr, dB2, base + lay.b2 + lay.dy2 + lay.db2, lay.bwd, stream);
   if (st) return st;
   if (r > 0)
     return hip_status(nf4q::launch_diagblocks(dB2, n, r, (uint16_t *)dBg, (uint16_t *)dBu, sm),
                       "qlora_swiglu_bwd launch");
   return ok();
+}
+
+}  // namespace
+
+extern "C" {
+
+int qlora_swiglu_bwd(const void *dH, const void *X, int64_t m, const nf4_tensor *Wgu,
+                     const void *Agu, const void *Bg, const void *Bu, int32_t r, float s,
+                     const void *Ygu, const void *Tgu, void *dX, void *dAgu, void *dBg, void *dBu,
+                     void *ws, size_t ws_bytes, void *stream) {
+  return swiglu_bwd_impl(dH, X, nullptr, m, Wgu, Agu, Bg, Bu, r, s, Ygu, nullptr, Tgu, dX, dAgu, dBg, dBu, ws, ws_bytes,
+                         stream);
 }
 
 int qlora_merge(const nf4_tensor *W, const void *A, const void *B, int32_t r, float s, void *Wout,
@@ -886,8 +920,9 @@ int moe_fwd_impl(const void *X, const Moe &mo, int32_t E, const nf4_tensor *W, c
   return moe_fused_impl(X, mo, E, W, T, B, r, s, Y, table, sm);
 }
 
-int moe_bwd_impl(const void *dY, const void *X, const Moe &mo, int32_t E, const nf4_tensor *W,
-                 const void *A, const void *B, int32_t r, float s, const void *T, void *dX, void *dA,
+// x8 given: X in 8 bits (X is its codes), row i of the grouped rows its row map[i] (NULL: i), and T is given.
+int moe_bwd_impl(const void *dY, const void *X, const nf4q::Act8 *x8, const int32_t *map, const Moe &mo, int32_t E,
+                 const nf4_tensor *W, const void *A, const void *B, int32_t r, float s, const void *T, void *dX, void *dA,
                  void *dB, void *ws, size_t ws_bytes, hipStream_t sm) {
   if (!dY || !aligned16(dY)) return fail(NF4_EINVAL, "dY must be non-NULL and 16-byte aligned");
   if (dX && !aligned16(dX)) return fail(NF4_EINVAL, "dX must be 16-byte aligned");
@@ -964,7 +999,8 @@ int moe_bwd_impl(const void *dY, const void *X, const Moe &mo, int32_t E, const 
   // dA_e = s U_e^T X_e, dB_e = s dY_e^T T_e over each expert's own rows, every expert in one
   // launch each (an expert with no rows sums nothing: zero gradients)
   if (r > 0) {
-    he = nf4q::launch_mreduce_grouped(U, x, k, k, r, s, pl.sa, part, (uint16_t *)dA, false, g64, sm);
+    he = x8 ? nf4q::launch_mreduce_act8(U, *x8, map, mo.mtotal, r, s, pl.sa, part, (uint16_t *)dA, &g64, sm)
+            : nf4q::launch_mreduce_grouped(U, x, k, k, r, s, pl.sa, part, (uint16_t *)dA, false, g64, sm);
     if (he != hipSuccess) return hip_status(he, "grouped backward dA launch");
     he = nf4q::launch_mreduce_grouped((const uint16_t *)T, dy, n, n, r, s, pl.sb, part, (uint16_t *)dB,
                                       true, g64, sm);
@@ -1011,7 +1047,7 @@ int qlora_moe_bwd(const void *dY, const void *X, const int64_t *counts, int32_t 
   Moe mo;
   int st = check_moe(X, counts, E, W, A, B, r, &mo);
   if (st) return st;
-  return moe_bwd_impl(dY, X, mo, E, W, A, B, r, s, T, dX, dA, dB, ws, ws_bytes, (hipStream_t)stream);
+  return moe_bwd_impl(dY, X, nullptr, nullptr, mo, E, W, A, B, r, s, T, dX, dA, dB, ws, ws_bytes, (hipStream_t)stream);
 }
 
 int qlora_moe_bwd_dev(const void *dY, const void *X, int64_t m, const int64_t *counts, int32_t E,
@@ -1021,7 +1057,7 @@ int qlora_moe_bwd_dev(const void *dY, const void *X, int64_t m, const int64_t *c
   Moe mo;
   int st = check_moe_dev(X, m, counts, E, W, A, B, r, &mo);
   if (st) return st;
-  return moe_bwd_impl(dY, X, mo, E, W, A, B, r, s, T, dX, dA, dB, ws, ws_bytes, (hipStream_t)stream);
+  return moe_bwd_impl(dY, X, nullptr, nullptr, mo, E, W, A, B, r, s, T, dX, dA, dB, ws, ws_bytes, (hipStream_t)stream);
 }
 
 int qlora_bwd_dx(const void *dY, int64_t m, const nf4_tensor *W, const void *U, const void *A,
@@ -1495,6 +1531,279 @@ int distill_topk_step(const void *logits, int dtype, int64_t t, int64_t v, int64
   if (t == 0) return ok();
   const nf4q::DistillArgs a{logits, t, v, ld, idx, teacher, top, tau, weight, nullptr, loss, nullptr, dlogits, ldd};
   return hip_status(nf4q::launch_distill(a, dtype == NF4_F32, (hipStream_t)stream), "distill_topk_step launch");
+}
+
+}  // extern "C"
+
+// ---------------------------------------------------------------- choice of experts
+namespace {
+
+bool apart(const void *p, size_t esz) { return reinterpret_cast<uintptr_t>(p) % esz == 0; }
+
+int check_route(const void *logits, int dtype, int64_t t, int32_t E, int64_t ld, int32_t top) {
+  if (dtype != NF4_BF16 && dtype != NF4_F32) return fail(NF4_EINVAL, "unknown dtype %d", dtype);
+  if (t < 0) return fail(NF4_EINVAL, "t must be >= 0 (got %lld)", (long long)t);
+  if (E < 1 || E > nf4q::kMaxExperts) return fail(NF4_EINVAL, "E must lie in [1, %d] (got %d)", nf4q::kMaxExperts, E);
+  if (top < 1 || top > nf4q::kRouteMaxTop || top > E)
+    return fail(NF4_EINVAL, "top must lie in [1, min(%d, E)] (got %d)", nf4q::kRouteMaxTop, top);
+  if (t > ((int64_t(1) << 31) - 1) / top) return fail(NF4_EUNSUPPORTED, "t * top must be below 2^31");
+  if (ld < E) return fail(NF4_EINVAL, "ld must be >= E (got %lld)", (long long)ld);
+  if (t && (!logits || !apart(logits, dtype == NF4_F32 ? 4 : 2)))
+    return fail(NF4_EINVAL, "logits must be non-NULL and aligned to its elements");
+  return NF4_OK;
+}
+
+}  // namespace
+
+extern "C" {
+
+size_t moe_route_workspace_bytes(int64_t t, int32_t E) {
+  return t < 1 || E < 1 || E > nf4q::kMaxExperts ? 0 : align256(nf4q::route_plan(t, E).bytes);
+}
+
+int moe_route(const void *logits, int dtype, int64_t t, int32_t E, int64_t ld, const uint8_t *keep, int32_t top,
+              int renormalize, int32_t *idx, float *gate, int32_t *place, int32_t *source, int64_t *counts,
+              int64_t *sizes, float *mean_p, float *losses, void *ws, size_t ws_bytes, void *stream) {
+  int st = check_route(logits, dtype, t, E, ld, top);
+  if (st) return st;
+  if (t && (!idx || !gate || !place || !source || !words(idx) || !words(gate) || !words(place) || !words(source)))
+    return fail(NF4_EINVAL, "idx, gate, place and source must be non-NULL and 4-byte aligned");
+  if (!counts || !sizes || !apart(counts, 8) || !apart(sizes, 8))
+    return fail(NF4_EINVAL, "counts and sizes must be non-NULL and 8-byte aligned");
+  if (!mean_p || !losses || !words(mean_p) || !words(losses))
+    return fail(NF4_EINVAL, "mean_p and losses must be non-NULL and 4-byte aligned");
+  const size_t need = moe_route_workspace_bytes(t, E);
+  if (ws_bytes < need || (need && !ws))
+    return fail(NF4_EINVAL, "workspace of %zu bytes is smaller than the %zu required", ws_bytes, need);
+  if (need && !aligned16(ws)) return fail(NF4_EINVAL, "ws must be 16-byte aligned");
+  nf4q::RouteArgs a{};
+  a.x = logits;
+  a.t = t;
+  a.ld = ld;
+  a.E = E;
+  a.top = top;
+  a.keep = keep;
+  a.renorm = renormalize != 0;
+  a.idx = idx;
+  a.gate = gate;
+  a.place = place;
+  a.source = source;
+  a.counts = counts;
+  a.sizes = sizes;
+  a.mean_p = mean_p;
+  a.losses = losses;
+  return hip_status(nf4q::launch_route(a, dtype == NF4_F32, ws, (hipStream_t)stream), "moe_route launch");
+}
+
+int moe_route_bwd(const void *logits, int dtype, int64_t t, int32_t E, int64_t ld, int32_t top, int renormalize,
+                  const int32_t *idx, const int64_t *counts, const int64_t *sizes, const float *dgate,
+                  const float *dlosses, void *dlogits, int64_t ldd, void *stream) {
+  int st = check_route(logits, dtype, t, E, ld, top);
+  if (st) return st;
+  if (ldd < E) return fail(NF4_EINVAL, "ldd must be >= E (got %lld)", (long long)ldd);
+  if (!counts || !sizes || !apart(counts, 8) || !apart(sizes, 8))
+    return fail(NF4_EINVAL, "counts and sizes must be non-NULL and 8-byte aligned");
+  if (!words(dgate) || !words(dlosses)) return fail(NF4_EINVAL, "dgate and dlosses must be 4-byte aligned");
+  if (t == 0) return ok();
+  if (!idx || !words(idx)) return fail(NF4_EINVAL, "idx must be non-NULL and 4-byte aligned");
+  if (!dlogits || !apart(dlogits, dtype == NF4_F32 ? 4 : 2))
+    return fail(NF4_EINVAL, "dlogits must be non-NULL and aligned to its elements");
+  const nf4q::RouteBwdArgs a{logits, t, ld, E, top, renormalize != 0, idx, counts, sizes, dgate, dlosses, dlogits, ldd};
+  return hip_status(nf4q::launch_route_bwd(a, dtype == NF4_F32, (hipStream_t)stream), "moe_route_bwd launch");
+}
+
+}  // extern "C"
+
+// ---------------------------------------------------------------- tokens into expert order and back
+namespace {
+
+int check_rows(int dtype, int64_t t, int64_t d, int32_t top, const int32_t *place) {
+  if (dtype != NF4_BF16 && dtype != NF4_F32) return fail(NF4_EINVAL, "unknown dtype %d", dtype);
+  if (t < 0) return fail(NF4_EINVAL, "t must be >= 0 (got %lld)", (long long)t);
+  if (d < 1 || top < 1) return fail(NF4_EINVAL, "d and top must be >= 1 (got %lld, %d)", (long long)d, top);
+  if (d >= (int64_t(1) << 31)) return fail(NF4_EUNSUPPORTED, "d must be below 2^31");
+  if (t > ((int64_t(1) << 31) - 1) / top) return fail(NF4_EUNSUPPORTED, "t * top must be below 2^31");
+  if (t && (!place || !words(place))) return fail(NF4_EINVAL, "place must be non-NULL and 4-byte aligned");
+  return NF4_OK;
+}
+
+// A matrix of t rows of d elements with the row stride ld.
+int check_matrix(const void *p, const char *name, int dtype, int64_t t, int64_t d, int64_t ld) {
+  if (ld < d) return fail(NF4_EINVAL, "the row stride of %s must be >= d (got %lld)", name, (long long)ld);
+  if (t && (!p || !apart(p, dtype == NF4_F32 ? 4 : 2)))
+    return fail(NF4_EINVAL, "%s must be non-NULL and aligned to its elements", name);
+  return NF4_OK;
+}
+
+nf4q::MoeRowsArgs rows_args(int64_t t, int64_t d, int32_t top, const int32_t *place) {
+  nf4q::MoeRowsArgs a{};
+  a.t = t;
+  a.d = d;
+  a.top = top;
+  a.place = place;
+  return a;
+}
+
+}  // namespace
+
+extern "C" {
+
+int moe_gather(const void *X, int dtype, int64_t t, int64_t d, int64_t ldx, const int32_t *place, const int32_t *source,
+               int32_t top, void *out, void *stream) {
+  int st = check_rows(dtype, t, d, top, place);
+  if (!st) st = check_matrix(X, "X", dtype, t, d, ldx);
+  if (!st) st = check_matrix(out, "out", dtype, t, d, d);
+  if (st) return st;
+  if (t == 0) return ok();
+  if (!source || !words(source)) return fail(NF4_EINVAL, "source must be non-NULL and 4-byte aligned");
+  nf4q::MoeRowsArgs a = rows_args(t, d, top, place);
+  a.x = X;
+  a.ldx = ldx;
+  a.source = source;
+  a.out = out;
+  return hip_status(nf4q::launch_gather(a, dtype == NF4_F32, (hipStream_t)stream), "moe_gather launch");
+}
+
+int moe_combine(const void *Z, int dtype, int64_t t, int64_t d, const int32_t *place, int32_t top, const float *gate,
+                const void *base, int64_t ldb, void *Y, int64_t ldy, void *stream) {
+  int st = check_rows(dtype, t, d, top, place);
+  if (!st) st = check_matrix(Z, "Z", dtype, t, d, d);
+  if (!st && base) st = check_matrix(base, "base", dtype, t, d, ldb);
+  if (!st) st = check_matrix(Y, "Y", dtype, t, d, ldy);
+  if (st) return st;
+  if (!words(gate)) return fail(NF4_EINVAL, "gate must be 4-byte aligned");
+  if (t == 0) return ok();
+  nf4q::MoeRowsArgs a = rows_args(t, d, top, place);
+  a.x = Z;
+  a.gate = gate;
+  a.base = base;
+  a.ldb = base ? ldb : 0;
+  a.out = Y;
+  a.ldo = ldy;
+  return hip_status(nf4q::launch_combine(a, dtype == NF4_F32, (hipStream_t)stream), "moe_combine launch");
+}
+
+int moe_combine_bwd(const void *dY, int dtype, int64_t t, int64_t d, int64_t ldy, const void *Z, const int32_t *place,
+                    const int32_t *source, int32_t top, const float *gate, void *dZ, float *dgate, void *stream) {
+  int st = check_rows(dtype, t, d, top, place);
+  if (!st) st = check_matrix(dY, "dY", dtype, t, d, ldy);
+  if (!st) st = check_matrix(Z, "Z", dtype, t, d, d);
+  if (!st) st = check_matrix(dZ, "dZ", dtype, t, d, d);
+  if (st) return st;
+  if (t == 0) return ok();
+  if (!source || !gate || !dgate || !words(source) || !words(gate) || !words(dgate))
+    return fail(NF4_EINVAL, "source, gate and dgate must be non-NULL and 4-byte aligned");
+  nf4q::MoeRowsArgs a = rows_args(t, d, top, place);
+  a.x = dY;
+  a.ldx = ldy;
+  a.z = Z;
+  a.source = source;
+  a.gate = gate;
+  a.out = dZ;
+  a.dgate = dgate;
+  return hip_status(nf4q::launch_combine_bwd(a, dtype == NF4_F32, (hipStream_t)stream), "moe_combine_bwd launch");
+}
+
+}  // extern "C"
+
+// ---------------------------------------------------------------- activations in 8 bits
+namespace {
+
+int check_act8(const nf4_act8 *q, const char *name, nf4q::Act8 *out) {
+  if (!q) return fail(NF4_EINVAL, "%s is NULL", name);
+  if (q->rows < 0 || q->k < 1)
+    return fail(NF4_EINVAL, "%s must have rows >= 0 and k >= 1 (got %lld, %lld)", name, (long long)q->rows, (long long)q->k);
+  if (q->rows >= (int64_t(1) << 31) || q->k > (int64_t(1) << 31) - 64)
+    return fail(NF4_EUNSUPPORTED, "%s must have rows and k below 2^31", name);
+  out->codes = q->codes;
+  out->scale = q->scale;
+  out->rows = q->rows;
+  out->k = q->k;
+  out->kp = (q->k + nf4q::kAct8Block - 1) / nf4q::kAct8Block * nf4q::kAct8Block;
+  if (q->rows * out->kp > (int64_t(1) << 42)) return fail(NF4_EUNSUPPORTED, "%s must have at most 2^42 elements", name);
+  if (q->rows && (!q->codes || !q->scale || !aligned16(q->codes) || !words(q->scale)))
+    return fail(NF4_EINVAL, "the codes of %s must be non-NULL and 16-byte aligned, its scales 4-byte aligned", name);
+  return NF4_OK;
+}
+
+int check_act8_side(const void *X, int dtype, int64_t ldx, const nf4q::Act8 &q) {
+  if (dtype != NF4_BF16 && dtype != NF4_F32) return fail(NF4_EINVAL, "unknown dtype %d", dtype);
+  if (ldx < q.k) return fail(NF4_EINVAL, "ldx must be >= k (got %lld)", (long long)ldx);
+  if (q.rows && (!X || !apart(X, dtype == NF4_F32 ? 4 : 2)))
+    return fail(NF4_EINVAL, "X must be non-NULL and aligned to its elements");
+  return NF4_OK;
+}
+
+// An activation of a layer: m rows (m < 0: any number) of k elements, k as the weight's, T given where r > 0.
+int check_act8_layer(const nf4q::Act8 &q, int64_t k, int32_t r, const void *T) {
+  if (q.k != k) return fail(NF4_EINVAL, "X must have the weight's k = %lld (got %lld)", (long long)k, (long long)q.k);
+  if (r > 0 && !T) return fail(NF4_EINVAL, "T must be given when r > 0");
+  return NF4_OK;
+}
+
+}  // namespace
+
+extern "C" {
+
+int act8_pack(const void *X, int dtype, int64_t ldx, const nf4_act8 *q, void *stream) {
+  nf4q::Act8 a;
+  int st = check_act8(q, "q", &a);
+  if (!st) st = check_act8_side(X, dtype, ldx, a);
+  if (st) return st;
+  if (a.rows == 0) return ok();
+  return hip_status(nf4q::launch_act8_pack(X, dtype == NF4_F32, ldx, a, (hipStream_t)stream), "act8_pack launch");
+}
+
+int act8_unpack(const nf4_act8 *q, void *X, int dtype, int64_t ldx, void *stream) {
+  nf4q::Act8 a;
+  int st = check_act8(q, "q", &a);
+  if (!st) st = check_act8_side(X, dtype, ldx, a);
+  if (st) return st;
+  if (a.rows == 0) return ok();
+  return hip_status(nf4q::launch_act8_unpack(a, X, dtype == NF4_F32, ldx, (hipStream_t)stream), "act8_unpack launch");
+}
+
+int qlora_bwd_act8(const void *dY, const nf4_act8 *X, const nf4_tensor *W, const void *A, const void *B, int32_t r,
+                   float s, const void *T, void *dX, void *dA, void *dB, void *ws, size_t ws_bytes, void *stream) {
+  nf4q::Act8 x;
+  int st = check_act8(X, "X", &x);
+  if (!st) st = check_weight(W);
+  if (!st) st = check_act8_layer(x, W->k, r, T);
+  if (st) return st;
+  return bwd_impl(dY, x.codes, &x, x.rows, W, A, B, r, s, T, dX, dA, dB, ws, ws_bytes, stream);
+}
+
+int qlora_swiglu_bwd_act8(const void *dH, const nf4_act8 *X, const nf4_tensor *Wgu, const void *Agu, const void *Bg,
+                          const void *Bu, int32_t r, float s, const nf4_act8 *Ygu, const void *Tgu, void *dX, void *dAgu,
+                          void *dBg, void *dBu, void *ws, size_t ws_bytes, void *stream) {
+  nf4q::Act8 x, y;
+  int st = check_act8(X, "X", &x);
+  if (!st) st = check_act8(Ygu, "Ygu", &y);
+  if (!st) st = check_weight(Wgu);
+  if (!st) st = check_act8_layer(x, Wgu->k, r, Tgu);
+  if (st) return st;
+  if (y.rows != x.rows || y.k != Wgu->n)
+    return fail(NF4_EINVAL, "Ygu must be [%lld, %lld] (got [%lld, %lld])", (long long)x.rows, (long long)Wgu->n,
+                (long long)y.rows, (long long)y.k);
+  return swiglu_bwd_impl(dH, x.codes, &x, x.rows, Wgu, Agu, Bg, Bu, r, s, y.codes, &y, Tgu, dX, dAgu, dBg, dBu, ws,
+                         ws_bytes, stream);
+}
+
+int qlora_moe_bwd_dev_act8(const void *dY, const nf4_act8 *X, const int32_t *source, int64_t m, const int64_t *counts,
+                           int32_t E, const nf4_tensor *W, const void *A, const void *B, int32_t r, float s,
+                           const void *T, void *dX, void *dA, void *dB, void *ws, size_t ws_bytes, void *stream) {
+  nf4q::Act8 x;
+  int st = check_act8(X, "X", &x);
+  if (!st) st = check_weight(W);
+  if (!st) st = check_act8_layer(x, W->k, r, T);
+  if (st) return st;
+  if (!source && x.rows != m)
+    return fail(NF4_EINVAL, "X must have m = %lld rows without a source (got %lld)", (long long)m, (long long)x.rows);
+  if (!words(source)) return fail(NF4_EINVAL, "source must be 4-byte aligned");
+  Moe mo;
+  st = check_moe_dev(x.codes, m, counts, E, W, A, B, r, &mo);
+  if (st) return st;
+  return moe_bwd_impl(dY, x.codes, &x, source, mo, E, W, A, B, r, s, T, dX, dA, dB, ws, ws_bytes, (hipStream_t)stream);
 }
 
 }  // extern "C"

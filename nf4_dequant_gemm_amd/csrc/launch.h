@@ -331,4 +331,83 @@ struct DistillArgs {
 constexpr int kDistillMaxTop = 1024;
 hipError_t launch_distill(const DistillArgs &a, bool f32, hipStream_t st);
 
+// Choice of experts (route.hip).
+constexpr int kRouteMaxTop = 16;       // a lane of 16 for each choice
+constexpr int kRouteMaxBlocks = 256;
+struct RouteArgs {
+  const void *x;             // logits [t][E], row stride ld
+  int64_t t, ld;
+  int E, top;                // 1 <= top <= E <= kMaxExperts, top <= kRouteMaxTop; t * top < 2^31
+  const uint8_t *keep;       // [t] or NULL
+  bool renorm;
+  int *idx;                  // [t][top]
+  float *gate;               // [t][top]
+  int *place, *source;       // [t][top], [t * top]
+  int64_t *counts, *sizes;   // [E], [2]
+  float *mean_p, *losses;    // [E], [2]
+  // set by launch_route: tokens a block, blocks, E up to a multiple of 16; in the workspace the blocks'
+  // counts and sums of p [blocks][Ep], sums of lse^2 and numbers of tokens [blocks]
+  int64_t rows;
+  int blocks, Ep;
+  int *cnt;
+  float *psum, *zsum;
+  int *nsum;
+};
+struct RoutePlan {
+  int64_t rows;
+  int blocks, threads, Ep;
+  size_t bytes;              // of workspace
+};
+RoutePlan route_plan(int64_t t, int E);
+hipError_t launch_route(RouteArgs a, bool f32, void *ws, hipStream_t st);
+struct RouteBwdArgs {
+  const void *x;
+  int64_t t, ld;
+  int E, top;
+  bool renorm;
+  const int *idx;
+  const int64_t *counts, *sizes;
+  const float *dgate, *dlosses;   // [t][top], [2]; NULL: zeros
+  void *dx;                       // [t][E], row stride ldd
+  int64_t ldd;
+};
+hipError_t launch_route_bwd(const RouteBwdArgs &a, bool f32, hipStream_t st);
+
+// Tokens into expert order and back (rows.hip).
+struct MoeRowsArgs {
+  const void *x;             // gather: X [t][d], ldx; combine: Z [t * top][d]; combine_bwd: dY [t][d], ldx
+  const void *z;             // combine_bwd: Z
+  const void *base;          // combine: [t][d], ldb, or NULL
+  int64_t t, d, ldx, ldb, ldo;
+  int top;
+  const int *place, *source; // [t][top], [t * top] (combine: no source)
+  const float *gate;         // combine: NULL for ones
+  void *out;                 // gather: [t * top][d]; combine: Y [t][d], ldo; combine_bwd: dZ
+  float *dgate;              // combine_bwd: [t][top]
+};
+hipError_t launch_gather(const MoeRowsArgs &a, bool f32, hipStream_t st);
+hipError_t launch_combine(const MoeRowsArgs &a, bool f32, hipStream_t st);
+hipError_t launch_combine_bwd(const MoeRowsArgs &a, bool f32, hipStream_t st);
+
+// Activations in 8 bits (act8.hip): code rows of kp bytes (k up to a multiple of kAct8Block), a float32
+// scale for each block.
+constexpr int kAct8Block = 64;
+struct Act8 {
+  int8_t *codes;
+  float *scale;
+  int64_t rows, k, kp;
+};
+hipError_t launch_act8_pack(const void *x, bool f32, int64_t ldx, const Act8 &q, hipStream_t st);
+hipError_t launch_act8_unpack(const Act8 &q, void *x, bool f32, int64_t ldx, hipStream_t st);
+// launch_mreduce (E == 0: rows 0 .. M - 1, one sum) and launch_mreduce_grouped with the second factor in 8
+// bits: row m is row (map ? map[m] : m) of q, of zeros where that is not one of its rows. part: splits *
+// r * C floats for each sum; splits as there.
+hipError_t launch_mreduce_act8(const uint16_t *P, const Act8 &q, const int *map, int64_t M, int r, float s, int splits,
+                               float *part, uint16_t *out, const GroupArgs *gr, hipStream_t st);
+// launch_swiglu_bwd from the 8-bit form of ygu [m][2n].
+hipError_t launch_swiglu_bwd_act8(const uint16_t *dh, const Act8 &ygu, int64_t n, uint16_t *dygu, hipStream_t st);
+// The sum over the splits that launch_mreduce ends with (E blocks of [r][C]).
+hipError_t launch_mreduce_final(const float *part, int64_t C, int r, int splits, int E, float s, bool transposed,
+                                uint16_t *out, hipStream_t st);
+
 }  // namespace nf4q

@@ -585,6 +585,15 @@ int mreduce_splits(int64_t M, int64_t C, int r, int E) {
   return (int)s;
 }
 
+hipError_t launch_mreduce_final(const float *part, int64_t C, int r, int splits, int E, float s, bool transposed,
+                                uint16_t *out, hipStream_t st) {
+  const int64_t n = (int64_t)E * r * C;
+  int64_t blocks = (n + 255) / 256;
+  if (blocks > 4096) blocks = 4096;
+  mreduce_final_kernel<<<dim3((unsigned)blocks), dim3(256), 0, st>>>(part, C, r, splits, E, s, transposed, out);
+  return hipGetLastError();
+}
+
 hipError_t launch_mreduce(const uint16_t *P, const uint16_t *Q, int64_t ldq, int64_t M, int64_t C,
                           int r, float s, int splits, float *part, uint16_t *out,
                           bool transposed_out, hipStream_t st) {
@@ -601,12 +610,7 @@ hipError_t launch_mreduce(const uint16_t *P, const uint16_t *Q, int64_t ldq, int
   }
   hipError_t e = hipGetLastError();
   if (e != hipSuccess) return e;
-  const int64_t n = (int64_t)r * C;
-  int64_t blocks = (n + 255) / 256;
-  if (blocks > 4096) blocks = 4096;
-  mreduce_final_kernel<<<dim3((unsigned)blocks), dim3(256), 0, st>>>(part, C, r, splits, 1, s,
-                                                                     transposed_out, out);
-  return hipGetLastError();
+  return launch_mreduce_final(part, C, r, splits, 1, s, transposed_out, out, st);
 }
 
 hipError_t launch_mreduce_grouped(const uint16_t *P, const uint16_t *Q, int64_t ldq, int64_t C, int r,
@@ -623,12 +627,7 @@ hipError_t launch_mreduce_grouped(const uint16_t *P, const uint16_t *Q, int64_t 
   }
   hipError_t e = hipGetLastError();
   if (e != hipSuccess) return e;
-  const int64_t n = (int64_t)gr.E * r * C;
-  int64_t blocks = (n + 255) / 256;
-  if (blocks > 4096) blocks = 4096;
-  mreduce_final_kernel<<<dim3((unsigned)blocks), dim3(256), 0, st>>>(part, C, r, splits, gr.E, s,
-                                                                     transposed_out, out);
-  return hipGetLastError();
+  return launch_mreduce_final(part, C, r, splits, gr.E, s, transposed_out, out, st);
 }
 
 // ---------------------------------------------------------------------------------- transpose
