@@ -525,8 +525,9 @@ int moe_combine_bwd(const void *dY, int dtype, int64_t t, int64_t d, int64_t ldy
  * The inputs that a backward pass needs again, in half the memory (of bf16). A row of k elements is cut
  * into blocks of 64 (the last may be short); with a = max |x| over a block,
  *   code = 127 x / a, rounded to the nearest integer, ties to even;   scale = fl32(a / 127),
- * and the block stands for fl32(code * scale). A block with a < 2^-119 is kept as zeros (scale 0); one that
- * holds an Inf or NaN gets the scale NaN and codes 0, so that it reads back as NaN. */
+ * and the block stands for fl32(code * scale). The scale is at most 0x1.020406p121, so that this is finite
+ * for every finite a. A block with a < 2^-119 is kept as zeros (scale 0); one that holds an Inf or NaN gets
+ * the scale NaN and codes 0, so that it reads back as NaN. */
 typedef struct {
   int8_t *codes;   /* [rows, kp], kp = k rounded up to a multiple of 64 (zeros from k on); 16-byte aligned */
   float *scale;    /* [rows, kp / 64]                                                                      */

@@ -1242,3 +1242,123 @@ class DistillTopKFunction(torch.autograd.Function):
     def backward(ctx, grad):
         logits, idx, teacher, lse = ctx.saved_tensors
         return distill_topk_bwd(grad.contiguous(), logits, idx, teacher, ctx.tau, lse), None, None, None
+
+
+class QLoRALinearAct8Function(torch.autograd.Function):
+    """QLoRALinearFunction that keeps X for its backward pass in 8 bits (act8_pack) instead of bf16."""
+
+    @staticmethod
+    def forward(ctx, X, q: NF4Tensor, A, B, s: float):
+        Y, T = qlora_fwd(X, q, A, B, s)
+        kept = act8_pack(X)
+        ctx.q, ctx.s, ctx.k = q, s, kept.k
+        ctx.save_for_backward(kept.codes, kept.scale, A, B, T)
+        return Y
+
+    @staticmethod
+    def backward(ctx, dY):
+        codes, scale, A, B, T = ctx.saved_tensors
+        dX, dA, dB = qlora_bwd_act8(dY.contiguous(), Act8Tensor(codes, scale, ctx.k), ctx.q, A, B, ctx.s, T,
+                                    need_dx=ctx.needs_input_grad[0])
+        return dX, None, dA, dB, None
+
+
+class QLoRASwiGLUAct8Function(torch.autograd.Function):
+    """QLoRASwiGLUFunction that keeps X and the pair's projections for its backward pass in 8 bits."""
+
+    @staticmethod
+    def forward(ctx, X, q: NF4Tensor, Agu, Bg, Bu, s: float):
+        H, Ygu, Tgu = qlora_swiglu_fwd(X, q, Agu, Bg, Bu, s)
+        x, y = act8_pack(X), act8_pack(Ygu)
+        ctx.q, ctx.s = q, s
+        ctx.save_for_backward(x.codes, x.scale, y.codes, y.scale, Agu, Bg, Bu, Tgu)
+        return H
+
+    @staticmethod
+    def backward(ctx, dH):
+        xc, xs, yc, ys, Agu, Bg, Bu, Tgu = ctx.saved_tensors
+        dX, dAgu, dBg, dBu = qlora_swiglu_bwd_act8(dH.contiguous(), Act8Tensor(xc, xs, ctx.q.k), ctx.q, Agu, Bg, Bu, ctx.s,
+                                                   Act8Tensor(yc, ys, ctx.q.n), Tgu, need_dx=ctx.needs_input_grad[0])
+        return dX, None, dAgu, dBg, dBu, None
+
+
+class QLoRAMoEFunction(torch.autograd.Function):
+    """The grouped layer with the routing on the device (qlora_moe_fwd_dev): X [m, k] in expert order, counts
+    int64 [E]; gradients flow to X, A and B. With kept (an Act8Tensor of the tokens, or of X) the backward pass
+    reads X from it, through source (int32 [m], moe_route's; None: kept holds X's rows), and X itself is not
+    kept. Rows past the counts' sum are left unwritten, in Y as in dX."""
+
+    @staticmethod
+    def forward(ctx, X, q: NF4Tensor, A, B, s: float, counts, kept: Optional[Act8Tensor] = None, source=None):
+        E, m = counts.numel(), X.shape[0]
+        n, r = q.n // E, 0 if A is None else A.shape[0] // E
+        Y, T = X.new_empty((m, n)), X.new_empty((m, r)) if r else None
+        ws = X.new_empty(max(1, moe_workspace_bytes_dev(m, E, n, q.k, r)), dtype=torch.uint8)
+        qlora_moe_fwd_dev(X, counts, q, A, B, s, Y, T, ws)
+        ctx.q, ctx.s, ctx.k = q, s, None if kept is None else kept.k
+        ctx.save_for_backward(A, B, T, counts, *((X,) if kept is None else (kept.codes, kept.scale, source)))
+        return Y
+
+    @staticmethod
+    def backward(ctx, dY):
+        A, B, T, counts, X, *of = ctx.saved_tensors
+        q, s, need_dx, dY = ctx.q, ctx.s, ctx.needs_input_grad[0], dY.contiguous()
+        if of:
+            dX, dA, dB = qlora_moe_bwd_act8(dY, Act8Tensor(X, of[0], ctx.k), of[1], counts, q, A, B, s, T, need_dx)
+        else:
+            E, m = counts.numel(), X.shape[0]
+            n, r = q.n // E, 0 if A is None else A.shape[0] // E
+            dX = torch.empty_like(X) if need_dx else None
+            dA, dB = (torch.empty_like(A), torch.empty_like(B)) if r else (None, None)
+            ws = X.new_empty(max(1, moe_workspace_bytes_dev(m, E, n, q.k, r)), dtype=torch.uint8)
+            qlora_moe_bwd_dev(dY, X, counts, q, A, B, s, T, dX, dA, dB, ws)
+        return dX, None, dA, dB, None, None, None, None
+
+
+class MoERouteFunction(torch.autograd.Function):
+    """moe_route as a MoERouting's fields; gradients flow from gate and losses to the logits."""
+
+    @staticmethod
+    def forward(ctx, logits, top: int, keep=None, renormalize: bool = True):
+        r = moe_route(logits, top, keep, renormalize)
+        ctx.renormalize = renormalize
+        ctx.save_for_backward(logits, r.idx, r.counts, r.sizes)
+        ctx.mark_non_differentiable(r.idx, r.place, r.source, r.counts, r.sizes, r.mean_p)
+        ctx.set_materialize_grads(False)
+        return tuple(r)
+
+    @staticmethod
+    def backward(ctx, dgate, dlosses, *_):
+        logits, idx, counts, sizes = ctx.saved_tensors
+        flat = lambda g: None if g is None else g.contiguous()
+        return moe_route_bwd(flat(dgate), flat(dlosses), logits, idx, counts, sizes, ctx.renormalize), None, None, None
+
+
+class MoEGatherFunction(torch.autograd.Function):
+    """moe_gather; the gradient flows to X."""
+
+    @staticmethod
+    def forward(ctx, X, place, source):
+        ctx.save_for_backward(place)
+        return moe_gather(X, place, source)
+
+    @staticmethod
+    def backward(ctx, dXg):
+        place, = ctx.saved_tensors
+        return moe_combine(dXg.contiguous(), place), None, None
+
+
+class MoECombineFunction(torch.autograd.Function):
+    """moe_combine; gradients flow to Z, gate and base (None: no base)."""
+
+    @staticmethod
+    def forward(ctx, Z, place, source, gate, base=None):
+        ctx.save_for_backward(Z, place, source, gate)
+        ctx.based = base is not None
+        return moe_combine(Z, place, gate, base)
+
+    @staticmethod
+    def backward(ctx, dY):
+        Z, place, source, gate = ctx.saved_tensors
+        dZ, dgate = moe_combine_bwd(dY if dY.stride(1) == 1 else dY.contiguous(), Z, place, source, gate)
+        return dZ, None, None, dgate, dY if ctx.based else None

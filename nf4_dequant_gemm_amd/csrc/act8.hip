@@ -6,7 +6,7 @@
 //   code = 127 x / a rounded to the nearest integer, ties to even;   scale = fl32(a / 127)
 //
 // and the block stands for fl32(code scale): at most a / 254 (half a step) from x, up to the rounding of
-// the scale. A block whose a is below 2^-119 is stored as zeros, so that 127 / a is finite; one with an Inf
+// the scale (at the largest float32 the scale is cut so that 127 of it stay finite). A block whose a is below 2^-119 is stored as zeros, so that 127 / a is finite; one with an Inf
 // or NaN gets the scale NaN, so that whatever uses it is NaN.
 //
 // act8_pack and act8_unpack read and write each element once and are bound by memory. Where the layer's
@@ -62,6 +62,7 @@ __device__ __forceinline__ int code_at_border(float x, float a, float t) {
 // is a half-integer, either 127 / a is exact (a = 127 2^i) and the tie goes to even, or x = +-a / 2, and the
 // rounded-up inv takes 63.5 to 64, which is even.
 constexpr float kRound = 12582912.f;
+constexpr float kTopScale = 0x1.020406p+121f;     // the largest whose 127-fold is finite
 
 template <typename XT>
 __device__ __forceinline__ uint32_t four_codes(const Piece<XT> &p, int i, float inv, float a) {
@@ -124,7 +125,7 @@ __global__ __launch_bounds__(256) void act8_pack_kernel(const XT *__restrict__ x
   if (m >= 0x7F800000u) {
     scale = __uint_as_float(0x7FC00000u);
   } else if (a >= 0x1p-119f) {
-    scale = a / 127.f;
+    scale = fminf(a / 127.f, kTopScale);
     float inv = 127.f / a;
     if (__builtin_fmaf(-inv, a, 127.f) > 0.f) inv = __uint_as_float(__float_as_uint(inv) + 1);
 #pragma unroll
@@ -134,10 +135,9 @@ __global__ __launch_bounds__(256) void act8_pack_kernel(const XT *__restrict__ x
   if ((threadIdx.x & 3) == 0) q.scale[row * (q.kp / kAct8Block) + c / kAct8Block] = scale;
 }
 
-// Byte e of a word of codes, with its sign bit flipped beforehand, as the value (u - 128) scale: one
-// conversion and one fused multiply-add, rounded as the product is (128 scale is exact).
-__device__ __forceinline__ float code_value(uint32_t flipped, int e, float scale, float off) {
-  return __builtin_fmaf((float)((flipped >> (8 * e)) & 0xFFu), scale, off);
+// What code e of a word of codes stands for.
+__device__ __forceinline__ float code_value(uint32_t codes, int e, float scale) {
+  return (float)(int8_t)(codes >> (8 * e)) * scale;
 }
 
 template <typename XT, bool kVec>
@@ -149,10 +149,10 @@ __global__ __launch_bounds__(256) void act8_unpack_kernel(Act8 q, XT *__restrict
   const int64_t c = (int64_t)(at % pieces) * 16;
   if (row >= q.rows) return;
   const u32x4 codes = *reinterpret_cast<const u32x4 *>(q.codes + row * q.kp + c);
-  const float scale = q.scale[row * (q.kp / kAct8Block) + c / kAct8Block], off = -128.f * scale;
+  const float scale = q.scale[row * (q.kp / kAct8Block) + c / kAct8Block];
   float v[16];
 #pragma unroll
-  for (int e = 0; e < 16; ++e) v[e] = code_value(codes[e >> 2] ^ 0x80808080u, e & 3, scale, off);
+  for (int e = 0; e < 16; ++e) v[e] = code_value(codes[e >> 2], e & 3, scale);
   XT *dst = x + row * ldx + c;
   if constexpr (kVec) {
     constexpr int P = 16 / (int)sizeof(XT);
@@ -251,14 +251,13 @@ __device__ __forceinline__ void mreduce_act8_body(const uint16_t *__restrict__ P
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
       const int k = tid + 256 * i;
-      const float off = -128.f * st.s[i];
       u32x4 o[2];
 #pragma unroll
       for (int w = 0; w < 4; ++w) {
-        const uint32_t f = st.q[i][w] ^ 0x80808080u;
+        const uint32_t f = st.q[i][w];
 #pragma unroll
         for (int h = 0; h < 2; ++h)
-          o[w >> 1][2 * (w & 1) + h] = pack_bf16x2(code_value(f, 2 * h, st.s[i], off), code_value(f, 2 * h + 1, st.s[i], off));
+          o[w >> 1][2 * (w & 1) + h] = pack_bf16x2(code_value(f, 2 * h, st.s[i]), code_value(f, 2 * h + 1, st.s[i]));
       }
       u32x4 *d = reinterpret_cast<u32x4 *>(&sQ[buf][(k >> 3) * kQRow + (k & 7) * 16]);
       d[0] = o[0];
@@ -369,8 +368,8 @@ __global__ __launch_bounds__(256) void swiglu_bwd_act8_kernel(const uint16_t *__
 #pragma unroll
       for (int h = 0; h < 2; ++h) {
         const float dv = h ? bf16_hi(d[e]) : bf16_lo(d[e]);
-        const float gv = code_value(g[e >> 1] ^ 0x80808080u, 2 * (e & 1) + h, sg, -128.f * sg);
-        const float uv = code_value(u[e >> 1] ^ 0x80808080u, 2 * (e & 1) + h, su, -128.f * su);
+        const float gv = code_value(g[e >> 1], 2 * (e & 1) + h, sg);
+        const float uv = code_value(u[e >> 1], 2 * (e & 1) + h, su);
         const float s = sigmoid(gv);
         rg[h] = dv * uv * (s * (1.f + gv * (1.f - s)));
         ru[h] = dv * (gv * s);
