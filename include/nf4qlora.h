@@ -540,9 +540,9 @@ typedef struct {
 int act8_pack(const void *X, int dtype, int64_t ldx, const nf4_act8 *q, void *stream);
 int act8_unpack(const nf4_act8 *q, void *X, int dtype, int64_t ldx, void *stream);
 
-/* qlora_bwd with X in 8 bits (m = X->rows): the same dX and dB, and dA = s U^T X from what the codes
- * stand for, rounded to bf16 as the matrix cores take it; equal, bit for bit, to qlora_bwd of the unpacked
- * X. T must be given when r > 0. ws: qlora_bwd_workspace_bytes. Errors: as qlora_bwd and act8_pack. */
+/* qlora_bwd with X in 8 bits (m = X->rows): the same U, dX and dB, bit for bit, and dA = s U^T X from U in
+ * float32 and what the codes stand for: U times a block's scale is rounded to bf16, the codes are not
+ * rounded. T must be given when r > 0. ws: qlora_bwd_workspace_bytes. Errors: as qlora_bwd and act8_pack. */
 int qlora_bwd_act8(const void *dY, const nf4_act8 *X, const nf4_tensor *W, const void *A, const void *B, int32_t r,
                    float s, const void *T, void *dX, void *dA, void *dB, void *ws, size_t ws_bytes, void *stream);
 

@@ -177,28 +177,53 @@ __global__ __launch_bounds__(256) void act8_unpack_kernel(Act8 q, XT *__restrict
 }
 
 // ---------------------------------------------------------------------------------- sums over rows
-// out[j][c] = sum over m of P[m][j] Q[m][c], Q in 8 bits, rounded to bf16 as the bf16 activation would be:
-// the sums over the rows of lora.hip with the codes decoded on their way into LDS. Workgroup: 128 columns x
-// all r (<= 128) rows j over one split of the rows, in stages of 64 rows loaded two stages ahead.
-constexpr int kBM = 64, kBC = 128, kQRow = kBC + 16;
+// out[j][c] = sum over m of P[m][j] Q[m][c], P float32, Q = code x scale in 8 bits. The scale of a row's block of 64
+// columns goes to P: for each of its blocks a workgroup holds bf16(P scale) of the stage's rows, and the codes,
+// which bf16 holds exactly, are multiplied as they are. So the one rounding before the float32 sums is that of
+// P scale, and a code costs one and a half vector instructions (a conversion with byte select and sign
+// extension, half a conversion of a pair). With the scale applied to the codes it was two and a half, and with
+// P's rounding made up for by a second bf16 number twice the products (16384 x 14336, rank 32: 72 us).
+//
+// Workgroup: 32 NW columns x all r (<= 128) rows j over one split of the rows, in stages of 64 rows requested two
+// stages ahead. The codes stay bytes in LDS and are read with the transposing load ds_read_b64_tr_b8, which
+// hands each lane 8 consecutive rows of one column, the matrix cores' operand layout.
+constexpr int kBM = 64;
 typedef __attribute__((ext_vector_type(4))) short s16x4;
 typedef __attribute__((ext_vector_type(8))) short s16x8;
+typedef __attribute__((ext_vector_type(2))) int i32x2;
 
 __device__ __forceinline__ s16x4 lds_tr16(const uint16_t *p) {
   return __builtin_amdgcn_ds_read_tr16_b64_v4i16((__attribute__((address_space(3))) s16x4 *)(p));
 }
+__device__ __forceinline__ u32x2 lds_tr8(const int8_t *p) {
+  return __builtin_bit_cast(u32x2, __builtin_amdgcn_ds_read_tr8_b64_v2i32((__attribute__((address_space(3))) i32x2 *)(p)));
+}
 
-// kGrp: one sum for each expert blockIdx.z over its own rows.
-template <int TJ, bool kGrp>
-__device__ __forceinline__ void mreduce_act8_body(const uint16_t *__restrict__ P, const Act8 &q,
-                                                  const int *__restrict__ map, int64_t M, int r, int64_t msplit,
-                                                  float *__restrict__ part, const GroupArgs &gr) {
-  constexpr int PROW = TJ * 16 + 16;          // P row stride in bf16 (padded by 32 bytes)
-  __shared__ __align__(16) uint16_t sQ[2][kBM * kQRow];
-  __shared__ __align__(16) uint16_t sP[2][kBM * PROW];
+// Waves of a workgroup for TJ tiles of 16 ranks: with 8, the four blocks' P takes too much LDS above 64 ranks.
+constexpr int act8_waves(int tj) { return tj <= 4 ? 8 : 4; }
+
+// kPVec: r is a multiple of 4. kGrp: one sum for each expert blockIdx.z over its own rows. kMap: row m is row map[m]
+// of q (zeros where that is not one of its rows).
+template <int TJ, bool kPVec, bool kGrp, bool kMap>
+__device__ __forceinline__ void mreduce_act8_body(const float *__restrict__ P, const Act8 &q, const int *__restrict__ map,
+                                                  int64_t M, int r, int64_t msplit, float *__restrict__ part,
+                                                  const GroupArgs &gr) {
+  constexpr int NW = act8_waves(TJ), NB = NW / 2;     // waves; blocks of 64 columns
+  constexpr int kT = 64 * NW, kBC = 32 * NW;          // threads, columns
+  constexpr int PROW = TJ * 16 + 8;                   // P row stride in bf16
+  constexpr int kQRow = kBC + 16;                     // code row stride: 8 rows in different banks
+  constexpr int PC = 4 * TJ;                          // 16-byte chunks of a row of P
+  constexpr int PPT = (kBM * PC + kT - 1) / kT;       // chunks of P a thread (past row 63: read as any, not stored)
+  constexpr uint32_t kNowhere = 0x80000000u;          // an offset past every buffer: reads 0
+  __shared__ __align__(16) int8_t sQ[2][kBM * kQRow];
+  __shared__ __align__(16) uint16_t sP[2][NB][kBM * PROW];
   const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
-  const int64_t c0 = (int64_t)blockIdx.x * kBC, C = q.k;
-  const int split = blockIdx.y;
+  // Workgroups go to the 8 XCDs in turn: each takes neighbouring column tiles of the same rows, which share
+  // lines of scales and P in its L2.
+  const int total = gridDim.x * gridDim.y, id = blockIdx.y * gridDim.x + blockIdx.x, per = total / 8, more = total % 8;
+  const int x = id % 8, at = x * per + (x < more ? x : more) + id / 8;
+  const int64_t c0 = (int64_t)(at % gridDim.x) * kBC, C = q.k;
+  const int split = at / gridDim.x;
   int64_t lo = 0, hi = M;
   if (kGrp) {
     lo = grp_m_off(gr, blockIdx.z);
@@ -208,8 +233,7 @@ __device__ __forceinline__ void mreduce_act8_body(const uint16_t *__restrict__ P
   }
   const int64_t mb = lo + split * msplit;
   const int64_t me = (mb + msplit < hi) ? mb + msplit : hi;
-  const bool pvec = (r & 7) == 0;
-  const int64_t nb = q.kp / kAct8Block;
+  const int64_t kp = q.kp, nb = kp / kAct8Block, b0 = c0 / kAct8Block;
 
   f32x4 acc[TJ][2];
 #pragma unroll
@@ -217,108 +241,150 @@ __device__ __forceinline__ void mreduce_act8_body(const uint16_t *__restrict__ P
 #pragma unroll
     for (int u = 0; u < 2; ++u) acc[t][u] = f32x4{0.f, 0.f, 0.f, 0.f};
 
+  // A thread's part of a stage: 16 codes of rows tid / (2 NW) and 32 rows on, columns c0 + 16 (tid % (2 NW)); chunks
+  // of four ranks of P, row (tid + kT i) / PC, with the scales of that row's blocks.
+  const int qr = tid / (2 * NW), qc = tid % (2 * NW) * 16;
+  const bool q_in = c0 + qc < kp;
+  const uint32_t q_off = q_in ? (uint32_t)(qr * kp + c0 + qc) : kNowhere;
+  const uint32_t q_off2 = q_in ? (uint32_t)((qr + 32) * kp + c0 + qc) : kNowhere;
+  auto p_row = [&](int i) { return (tid + kT * i) / PC; };
+  auto p_col = [&](int i) { return (tid + kT * i) % PC * 4; };
+
   struct Stage {
     u32x4 q[2];
-    float s[2];
-    uint4 p[(TJ + 1) / 2];
+    f32x4 p[PPT];
+    float s[PPT][NB];
   };
-  auto load = [&](int64_t ms, Stage &st) {
-#pragma unroll
-    for (int i = 0; i < 2; ++i) {
-      const int k = tid + 256 * i;                   // chunk k of 16 codes: row k / 8
-      const int64_t m = ms + (k >> 3), c = c0 + (k & 7) * 16;
-      int64_t row = m < me ? (map ? map[m] : m) : -1;
-      if (row < 0 || row >= q.rows || c >= q.kp) {
-        st.q[i] = u32x4{0, 0, 0, 0};
-        st.s[i] = 0.f;
-      } else {
-        st.q[i] = *reinterpret_cast<const u32x4 *>(q.codes + row * q.kp + c);
-        st.s[i] = q.scale[row * nb + c / kAct8Block];
-      }
-    }
-    if (pvec) {
-#pragma unroll
-      for (int i = 0; i < (TJ + 1) / 2; ++i) {
-        const int k = tid + 256 * i;                 // chunk k of the P tile: row k / (2 TJ)
-        const int row = k / (2 * TJ), j = k % (2 * TJ) * 8;
-        const int64_t m = ms + row;
-        st.p[i] = (row < kBM && m < me && j < r) ? *reinterpret_cast<const uint4 *>(P + m * r + j)
-                                                 : make_uint4(0, 0, 0, 0);
-      }
-    }
+  struct Rows {       // kMap: the rows of q of this thread's codes and chunks of P
+    int q[2], p[PPT];
   };
-  auto store = [&](int64_t ms, const Stage &st, int buf) {
+  auto find = [&](int64_t ms, Rows &rw) {
+    const __amdgpu_buffer_rsrc_t rm = make_rsrc(map + ms, (me > ms ? me - ms < kBM ? me - ms : kBM : 0) * 4);
+    auto of = [&](int row) { return (int)__builtin_amdgcn_raw_buffer_load_b32(rm, row * 4, 0, 0); };
+    rw.q[0] = of(qr);
+    rw.q[1] = of(qr + 32);
 #pragma unroll
-    for (int i = 0; i < 2; ++i) {
-      const int k = tid + 256 * i;
-      u32x4 o[2];
+    for (int i = 0; i < PPT; ++i) rw.p[i] = of(p_row(i));
+  };
+  // Requests a stage, without a branch: the waits for the stage before then leave these requests in flight. Rows
+  // past the split's end read as zeros (of P too); a row of q that is none as row 0 with the scale 0.
+  auto load = [&](int64_t ms, Stage &st, const Rows &rw) {
+    const int64_t left = me > ms ? me - ms < kBM ? me - ms : kBM : 0;
+    if constexpr (kMap) {
 #pragma unroll
-      for (int w = 0; w < 4; ++w) {
-        const uint32_t f = st.q[i][w];
-#pragma unroll
-        for (int h = 0; h < 2; ++h)
-          o[w >> 1][2 * (w & 1) + h] = pack_bf16x2(code_value(f, 2 * h, st.s[i]), code_value(f, 2 * h + 1, st.s[i]));
-      }
-      u32x4 *d = reinterpret_cast<u32x4 *>(&sQ[buf][(k >> 3) * kQRow + (k & 7) * 16]);
-      d[0] = o[0];
-      d[1] = o[1];
-    }
-    if (pvec) {
-#pragma unroll
-      for (int i = 0; i < (TJ + 1) / 2; ++i) {
-        const int k = tid + 256 * i;
-        const int row = k / (2 * TJ), ch = k % (2 * TJ);
-        if (row < kBM) *reinterpret_cast<uint4 *>(&sP[buf][row * PROW + ch * 8]) = st.p[i];
+      for (int i = 0; i < 2; ++i) {
+        const int64_t row = rw.q[i] >= 0 && rw.q[i] < q.rows ? rw.q[i] : 0;
+        st.q[i] = *reinterpret_cast<const u32x4 *>(q.codes + row * kp + (q_in ? c0 + qc : 0));
       }
     } else {
-      for (int k = tid; k < kBM * TJ * 16; k += 256) {
-        const int row = k / (TJ * 16), j = k % (TJ * 16);
-        const int64_t m = ms + row;
-        sP[buf][row * PROW + j] = (m < me && j < r) ? P[m * r + j] : (uint16_t)0;
+      const __amdgpu_buffer_rsrc_t rq = make_rsrc(q.codes + ms * kp, left * kp);
+      st.q[0] = __builtin_amdgcn_raw_buffer_load_b128(rq, q_off, 0, 0);
+      st.q[1] = __builtin_amdgcn_raw_buffer_load_b128(rq, q_off2, 0, 0);
+    }
+    const __amdgpu_buffer_rsrc_t rp = make_rsrc(P + ms * r, left * r * 4);
+    const __amdgpu_buffer_rsrc_t rs = make_rsrc(q.scale + (kMap ? 0 : ms * nb), kMap ? 0 : left * nb * 4);
+#pragma unroll
+    for (int i = 0; i < PPT; ++i) {
+      const int row = p_row(i), j = p_col(i);
+      if constexpr (kPVec) {
+        st.p[i] = __builtin_bit_cast(f32x4, __builtin_amdgcn_raw_buffer_load_b128(
+                                                rp, j < r ? (uint32_t)((row * r + j) * 4) : kNowhere, 0, 0));
+      } else {
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+          st.p[i][e] = __uint_as_float(__builtin_amdgcn_raw_buffer_load_b32(
+              rp, j + e < r ? (uint32_t)((row * r + j + e) * 4) : kNowhere, 0, 0));
+      }
+      // the scales of the row's blocks; past the row's last block any value will do (no column uses it)
+      if constexpr (kMap) {
+        const bool in = rw.p[i] >= 0 && rw.p[i] < q.rows;
+#pragma unroll
+        for (int b = 0; b < NB; ++b) {
+          const float v = q.scale[(in ? rw.p[i] : 0) * nb + (b0 + b < nb ? b0 + b : 0)];
+          st.s[i][b] = in ? v : 0.f;
+        }
+      } else if constexpr (NB == 4) {
+        const u32x4 v = __builtin_amdgcn_raw_buffer_load_b128(rs, (uint32_t)((row * nb + b0) * 4), 0, 0);
+#pragma unroll
+        for (int b = 0; b < 4; ++b) st.s[i][b] = __uint_as_float(v[b]);
+      } else {
+        const u32x2 v = __builtin_amdgcn_raw_buffer_load_b64(rs, (uint32_t)((row * nb + b0) * 4), 0, 0);
+#pragma unroll
+        for (int b = 0; b < 2; ++b) st.s[i][b] = __uint_as_float(v[b]);
+      }
+    }
+  };
+  auto store = [&](const Stage &st, int buf) {
+    *reinterpret_cast<u32x4 *>(&sQ[buf][qr * kQRow + qc]) = st.q[0];
+    *reinterpret_cast<u32x4 *>(&sQ[buf][(qr + 32) * kQRow + qc]) = st.q[1];
+#pragma unroll
+    for (int i = 0; i < PPT; ++i) {
+      if (kBM * PC % kT != 0 && p_row(i) >= kBM) continue;
+#pragma unroll
+      for (int b = 0; b < NB; ++b) {
+        const float s = st.s[i][b];
+        const u32x2 v = {pack_bf16x2(st.p[i][0] * s, st.p[i][1] * s), pack_bf16x2(st.p[i][2] * s, st.p[i][3] * s)};
+        *reinterpret_cast<u32x2 *>(&sP[buf][b][p_row(i) * PROW + p_col(i)]) = v;
       }
     }
   };
   const int g16 = lane >> 4, l16 = lane & 15;
-  auto frag = [&](const uint16_t *S, int rowstride, int colbase, int kslice) {
-    const int m0 = kslice * 32 + g16 * 8 + (l16 >> 2);
-    const int col = colbase + 4 * (l16 & 3);
-    const s16x4 a = lds_tr16(S + m0 * rowstride + col);
-    const s16x4 b = lds_tr16(S + (m0 + 4) * rowstride + col);
-    const s16x8 v = {a[0], a[1], a[2], a[3], b[0], b[1], b[2], b[3]};
-    return __builtin_bit_cast(bf16x8, v);
-  };
   auto mma = [&](int buf) {
 #pragma unroll
     for (int ks = 0; ks < 2; ++ks) {
+      const int m0 = ks * 32 + g16 * 8;        // this lane's 8 rows
       bf16x8 bq[2];
 #pragma unroll
-      for (int u = 0; u < 2; ++u) bq[u] = frag(sQ[buf], kQRow, wave * 32 + u * 16, ks);
+      for (int u = 0; u < 2; ++u) {
+        const u32x2 w = lds_tr8(&sQ[buf][(m0 + (l16 >> 1)) * kQRow + wave * 32 + u * 16 + (l16 & 1) * 8]);
+        u32x4 v;
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+          v[e] = pack_bf16x2((float)(int8_t)(w[e >> 1] >> (16 * (e & 1))), (float)(int8_t)(w[e >> 1] >> (16 * (e & 1) + 8)));
+        bq[u] = __builtin_bit_cast(bf16x8, v);
+      }
 #pragma unroll
       for (int t = 0; t < TJ; ++t) {
-        const bf16x8 ap = frag(sP[buf], PROW, t * 16, ks);
+        const uint16_t *S = &sP[buf][wave >> 1][(m0 + (l16 >> 2)) * PROW + t * 16 + 4 * (l16 & 3)];
+        const s16x4 a = lds_tr16(S), b = lds_tr16(S + 4 * PROW);
+        const bf16x8 ap = __builtin_bit_cast(bf16x8, s16x8{a[0], a[1], a[2], a[3], b[0], b[1], b[2], b[3]});
 #pragma unroll
         for (int u = 0; u < 2; ++u) acc[t][u] = mfma16x16x32(ap, bq[u], acc[t][u]);
       }
     }
   };
 
+  // stage i: products on buffer i & 1; requests of stage i + 2 (and of the rows of stage i + 4); stores of stage
+  // i + 1. A stage past the last is zeros, so the stages are taken in pairs.
   const int64_t nst = (me > mb) ? (me - mb + kBM - 1) / kBM : 0;
-  Stage s0, s1;
-  if (nst > 0) load(mb, s0);
-  if (nst > 1) load(mb + kBM, s1);
-  if (nst > 0) store(mb, s0, 0);
-  __syncthreads();
+  if (nst > 0) {
+    Stage s0, s1;
+    Rows r0{}, r1{};
+    if constexpr (kMap) {
+      find(mb, r0);
+      find(mb + kBM, r1);
+    }
+    load(mb, s0, r0);
+    load(mb + kBM, s1, r1);
+    if constexpr (kMap) {
+      find(mb + 2 * kBM, r0);
+      find(mb + 3 * kBM, r1);
+    }
+    store(s0, 0);
+    __syncthreads();
 #pragma unroll 1
-  for (int64_t i = 0; i < nst; i += 2) {
-    if (i + 2 < nst) load(mb + (i + 2) * kBM, s0);
-    mma(0);
-    if (i + 1 < nst) store(mb + (i + 1) * kBM, s1, 1);
-    __syncthreads();
-    if (i + 1 >= nst) break;
-    if (i + 3 < nst) load(mb + (i + 3) * kBM, s1);
-    mma(1);
-    if (i + 2 < nst) store(mb + (i + 2) * kBM, s0, 0);
-    __syncthreads();
+    for (int64_t i = 0; i < nst; i += 2) {
+      load(mb + (i + 2) * kBM, s0, r0);
+      if constexpr (kMap) find(mb + (i + 4) * kBM, r0);
+      mma(0);
+      store(s1, 1);
+      __syncthreads();
+      load(mb + (i + 3) * kBM, s1, r1);
+      if constexpr (kMap) find(mb + (i + 5) * kBM, r1);
+      mma(1);
+      store(s0, 0);
+      __syncthreads();
+    }
   }
 
 #pragma unroll
@@ -333,18 +399,34 @@ __device__ __forceinline__ void mreduce_act8_body(const uint16_t *__restrict__ P
       }
 }
 
-template <int TJ>
-__global__ __launch_bounds__(256) void mreduce_act8_kernel(const uint16_t *__restrict__ P, Act8 q,
-                                                           const int *__restrict__ map, int64_t M, int r,
-                                                           int64_t msplit, float *__restrict__ part) {
-  mreduce_act8_body<TJ, false>(P, q, map, M, r, msplit, part, GroupArgs{});
+template <int TJ, bool kPVec>
+__global__ __launch_bounds__(64 * act8_waves(TJ)) void mreduce_act8_kernel(const float *__restrict__ P, Act8 q, int64_t M,
+                                                                           int r, int64_t msplit,
+                                                                           float *__restrict__ part) {
+  mreduce_act8_body<TJ, kPVec, false, false>(P, q, nullptr, M, r, msplit, part, GroupArgs{});
 }
 
-template <int TJ>
-__global__ __launch_bounds__(256) void mreduce_act8_grouped_kernel(const uint16_t *__restrict__ P, Act8 q,
-                                                                   const int *__restrict__ map, int r,
-                                                                   float *__restrict__ part, GroupArgs gr) {
-  mreduce_act8_body<TJ, true>(P, q, map, 0, r, 0, part, gr);
+template <int TJ, bool kPVec, bool kMap>
+__global__ __launch_bounds__(64 * act8_waves(TJ)) void mreduce_act8_grouped_kernel(const float *__restrict__ P, Act8 q,
+                                                                                   const int *__restrict__ map, int r,
+                                                                                   float *__restrict__ part,
+                                                                                   GroupArgs gr) {
+  mreduce_act8_body<TJ, kPVec, true, kMap>(P, q, map, 0, r, 0, part, gr);
+}
+
+// The launch for one height and kind of P.
+template <int TJ, bool kPVec>
+hipError_t launch_mreduce_act8_as(const float *P, const Act8 &q, const int *map, int64_t M, int r, int splits,
+                                  float *part, const GroupArgs *gr, hipStream_t st) {
+  constexpr int kBC = 32 * act8_waves(TJ);
+  const dim3 grid((unsigned)((q.k + kBC - 1) / kBC), (unsigned)splits, (unsigned)(gr ? gr->E : 1));
+  const dim3 block(64 * act8_waves(TJ));
+  int64_t msplit = (M + splits - 1) / splits;
+  msplit = (msplit + kBM - 1) / kBM * kBM;
+  if (gr && map) mreduce_act8_grouped_kernel<TJ, kPVec, true><<<grid, block, 0, st>>>(P, q, map, r, part, *gr);
+  else if (gr) mreduce_act8_grouped_kernel<TJ, kPVec, false><<<grid, block, 0, st>>>(P, q, map, r, part, *gr);
+  else mreduce_act8_kernel<TJ, kPVec><<<grid, block, 0, st>>>(P, q, M, r, msplit, part);
+  return hipGetLastError();
 }
 
 // ---------------------------------------------------------------------------------- gate/up pair
@@ -418,25 +500,34 @@ hipError_t launch_act8_unpack(const Act8 &q, void *x, bool f32, int64_t ldx, hip
   return hipGetLastError();
 }
 
-hipError_t launch_mreduce_act8(const uint16_t *P, const Act8 &q, const int *map, int64_t M, int r, float s, int splits,
+// One round of workgroups, as many as the LDS of the 256 CUs holds (160 KB each; 16384 x 14336, rank 32, two a CU:
+// 224 and 504 workgroups 73 and 67 us; 8192 x 4096, rank 64, one a CU: 256 and 512 workgroups 16.5 and 23 us).
+int mreduce_act8_splits(int64_t M, int64_t C, int r, int E) {
+  const int tj = (r + 15) / 16, nw = act8_waves(tj);
+  const int lds = 2 * kBM * (32 * nw + 16) + 2 * (nw / 2) * kBM * (16 * tj + 8) * 2;
+  const int64_t width = 32 * nw, tiles = (C + width - 1) / width * E;
+  int64_t s = 256 * (160 * 1024 / lds < 2 ? 1 : 2) / tiles;
+  const int64_t maxs = (M + kBM - 1) / kBM;
+  s = s < maxs ? s : maxs;
+  return (int)(s < 1 ? 1 : s);
+}
+
+hipError_t launch_mreduce_act8(const float *P, const Act8 &q, const int *map, int64_t M, int r, float s, int splits,
                                float *part, uint16_t *out, const GroupArgs *gr, hipStream_t st) {
-  int64_t msplit = (M + splits - 1) / splits;
-  msplit = (msplit + kBM - 1) / kBM * kBM;
-  const int E = gr ? gr->E : 1;
-  const dim3 grid((unsigned)((q.k + kBC - 1) / kBC), (unsigned)splits, (unsigned)E);
+  if (map && !gr) return hipErrorInvalidValue;
+  hipError_t e = hipErrorInvalidValue;
   switch ((r + 15) / 16) {
-#define MR_CASE(T)                                                                                             \
-  case T:                                                                                                      \
-    if (gr) mreduce_act8_grouped_kernel<T><<<grid, dim3(256), 0, st>>>(P, q, map, r, part, *gr);               \
-    else mreduce_act8_kernel<T><<<grid, dim3(256), 0, st>>>(P, q, map, M, r, msplit, part);                    \
+#define MR_CASE(T)                                                                       \
+  case T:                                                                                \
+    e = (r & 3) ? launch_mreduce_act8_as<T, false>(P, q, map, M, r, splits, part, gr, st) \
+                : launch_mreduce_act8_as<T, true>(P, q, map, M, r, splits, part, gr, st); \
     break;
     MR_CASE(1) MR_CASE(2) MR_CASE(3) MR_CASE(4) MR_CASE(5) MR_CASE(6) MR_CASE(7) MR_CASE(8)
 #undef MR_CASE
-    default: return hipErrorInvalidValue;
+    default: break;
   }
-  const hipError_t e = hipGetLastError();
   if (e != hipSuccess) return e;
-  return launch_mreduce_final(part, q.k, r, splits, E, s, false, out, st);
+  return launch_mreduce_final(part, q.k, r, splits, gr ? gr->E : 1, s, false, out, st);
 }
 
 hipError_t launch_swiglu_bwd_act8(const uint16_t *dh, const Act8 &ygu, int64_t n, uint16_t *dygu, hipStream_t st) {

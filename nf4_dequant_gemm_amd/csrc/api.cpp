@@ -183,8 +183,9 @@ FwdWs fwd_ws(int64_t m, int64_t k, int32_t r) {
 
 struct BwdWs {
   int splits_u = 1, splits_a = 1, splits_b = 1, splits_t = 1;
-  // byte sizes: U at 0, Bt at u, T (recomputed when the caller passes none) at u + bt, partials
-  // at u + bt + t
+  int splits_a8 = 1;
+  // byte sizes: U at 0, Bt at u, T (recomputed when the caller passes none) or, with X in 8 bits, where T is
+  // given, U in float32 at u + bt, partials at u + bt + t
   size_t u = 0, bt = 0, t = 0, part = 0, total = 0;
 };
 
@@ -193,15 +194,15 @@ BwdWs bwd_ws(int64_t m, int64_t n, int64_t k, int32_t r) {
   if (r <= 0) return w;
   w.u = align256((size_t)m * r * 2);
   w.bt = align256((size_t)r * n * 2);
-  w.t = align256((size_t)m * r * 2);
+  w.t = align256((size_t)m * r * 4);
   w.splits_u = nf4q::rowproj_splits(m, n);
   w.splits_t = nf4q::rowproj_splits(m, k);
   w.splits_a = nf4q::mreduce_splits(m, k, r);
   w.splits_b = nf4q::mreduce_splits(m, n, r);
-  size_t p = 0;
-  if (w.splits_u > 1) p = std::max(p, (size_t)w.splits_u * m * r * 4);
+  w.splits_a8 = nf4q::mreduce_act8_splits(m, k, r);
+  size_t p = (size_t)w.splits_u * m * r * 4;
   if (w.splits_t > 1) p = std::max(p, (size_t)w.splits_t * m * r * 4);
-  p = std::max(p, (size_t)w.splits_a * r * k * 4);
+  p = std::max(p, (size_t)std::max(w.splits_a, w.splits_a8) * r * k * 4);
   p = std::max(p, (size_t)w.splits_b * r * n * 4);
   w.part = align256(p);
   w.total = w.u + w.bt + w.t + w.part;
@@ -303,7 +304,7 @@ int check_moe_dev(const void *X, int64_t m, const int64_t *dcounts, int32_t E, c
 // gives the same sums in the same order whether it is given on the host or on the device, and
 // one expert gives the single layer's.
 struct MoePlan {
-  int sp_k = 1, sp_n = 1, sa = 1, sb = 1;
+  int sp_k = 1, sp_n = 1, sa = 1, sb = 1, sa8 = 1;
 };
 
 MoePlan moe_plan(int64_t mtotal, int32_t E, int64_t n, int64_t k, int32_t r) {
@@ -312,11 +313,13 @@ MoePlan moe_plan(int64_t mtotal, int32_t E, int64_t n, int64_t k, int32_t r) {
   pl.sp_n = nf4q::rowproj_splits(mtotal, n);
   pl.sa = nf4q::mreduce_splits(mtotal, k, r, E);
   pl.sb = nf4q::mreduce_splits(mtotal, n, r, E);
+  pl.sa8 = nf4q::mreduce_act8_splits(mtotal, k, r, E);
   return pl;
 }
 
 // Workspace of the grouped layer: with device routing the group table first (table bytes),
-// then U [m, r], the transposed stacked B [r, E n], T (recomputed when the caller passes none),
+// then U [m, r], the transposed stacked B [r, E n], T (recomputed when the caller passes none) or, with X in
+// 8 bits, U in float32,
 // then float partials of the row projections or of the M-reductions (never both at once).
 struct MoeWs {
   size_t table = 0, u = 0, bt = 0, t = 0, part = 0, total = 0;
@@ -334,10 +337,10 @@ MoeWs moe_ws_layout(int64_t mtotal, int32_t E, int64_t n, int64_t k, int32_t r, 
     const MoePlan pl = moe_plan(mtotal, E, n, k, r);
     w.u = align256((size_t)mtotal * r * 2);
     w.bt = align256((size_t)r * E * n * 2);
-    w.t = w.u;
+    w.t = align256((size_t)mtotal * r * 4);
     if (pl.sp_k > 1) p = std::max(p, (size_t)pl.sp_k * mtotal * r * 4);
-    if (pl.sp_n > 1) p = std::max(p, (size_t)pl.sp_n * mtotal * r * 4);
-    p = std::max(p, (size_t)E * pl.sa * r * k * 4);
+    p = std::max(p, (size_t)pl.sp_n * mtotal * r * 4);
+    p = std::max(p, (size_t)E * std::max(pl.sa, pl.sa8) * r * k * 4);
     p = std::max(p, (size_t)E * pl.sb * r * n * 4);
   }
   w.part = align256(p);
@@ -640,6 +643,7 @@ int bwd_impl(const void *dY, const void *X, const nf4q::Act8 *x8, int64_t m, con
   char *base = (char *)ws;
   uint16_t *U = (uint16_t *)base;
   uint16_t *Bt = (uint16_t *)(base + lay.u);
+  float *Uw = x8 ? (float *)(base + lay.u + lay.bt) : nullptr;
   float *part = (float *)(base + lay.u + lay.bt + lay.t);
   const uint16_t *dy = (const uint16_t *)dY;
   hipError_t e;
@@ -653,7 +657,7 @@ int bwd_impl(const void *dY, const void *X, const nf4q::Act8 *x8, int64_t m, con
   if (r > 0) {
     e = nf4q::launch_transpose((const uint16_t *)B, n, r, Bt, sm);
     if (e != hipSuccess) return hip_status(e, "qlora_bwd transpose launch");
-    e = nf4q::launch_rowproj(dy, n, Bt, n, m, n, r, lay.splits_u, part, U, sm);
+    e = nf4q::launch_rowproj(dy, n, Bt, n, m, n, r, lay.splits_u, part, U, sm, Uw);
     if (e != hipSuccess) return hip_status(e, "qlora_bwd U launch");
   }
   if (dX) {
@@ -661,7 +665,7 @@ int bwd_impl(const void *dY, const void *X, const nf4q::Act8 *x8, int64_t m, con
     if (e != hipSuccess) return hip_status(e, "qlora_bwd dX launch");
   }
   if (r > 0) {
-    e = x8 ? nf4q::launch_mreduce_act8(U, *x8, nullptr, m, r, s, lay.splits_a, part, (uint16_t *)dA, nullptr, sm)
+    e = x8 ? nf4q::launch_mreduce_act8(Uw, *x8, nullptr, m, r, s, lay.splits_a8, part, (uint16_t *)dA, nullptr, sm)
            : nf4q::launch_mreduce(U, (const uint16_t *)X, k, m, k, r, s, lay.splits_a, part,
                                   (uint16_t *)dA, false, sm);
     if (e != hipSuccess) return hip_status(e, "qlora_bwd dA launch");
@@ -941,6 +945,7 @@ int moe_bwd_impl(const void *dY, const void *X, const nf4q::Act8 *x8, const int3
   void *table = dev ? base : nullptr;
   uint16_t *U = (uint16_t *)(base + lay.table);
   uint16_t *Bt = (uint16_t *)(base + lay.table + lay.u);
+  float *Uw = x8 ? (float *)(base + lay.table + lay.u + lay.bt) : nullptr;
   float *part = (float *)(base + lay.table + lay.u + lay.bt + lay.t);
   const uint16_t *dy = (const uint16_t *)dY, *x = (const uint16_t *)X;
   const uint16_t *a = (const uint16_t *)A;
@@ -963,7 +968,7 @@ int moe_bwd_impl(const void *dY, const void *X, const nf4q::Act8 *x8, const int3
       if (he != hipSuccess) return hip_status(he, "grouped backward T launch");
       T = Tw;
     }
-    he = nf4q::launch_rowproj_grouped(dy, n, Bt, n, E * n, mo.mtotal, n, r, pl.sp_n, part, U, g64, sm);
+    he = nf4q::launch_rowproj_grouped(dy, n, Bt, n, E * n, mo.mtotal, n, r, pl.sp_n, part, U, g64, sm, Uw);
     if (he != hipSuccess) return hip_status(he, "grouped backward U launch");
   }
   // dX of every expert in one launch
@@ -999,7 +1004,7 @@ int moe_bwd_impl(const void *dY, const void *X, const nf4q::Act8 *x8, const int3
   // dA_e = s U_e^T X_e, dB_e = s dY_e^T T_e over each expert's own rows, every expert in one
   // launch each (an expert with no rows sums nothing: zero gradients)
   if (r > 0) {
-    he = x8 ? nf4q::launch_mreduce_act8(U, *x8, map, mo.mtotal, r, s, pl.sa, part, (uint16_t *)dA, &g64, sm)
+    he = x8 ? nf4q::launch_mreduce_act8(Uw, *x8, map, mo.mtotal, r, s, pl.sa8, part, (uint16_t *)dA, &g64, sm)
             : nf4q::launch_mreduce_grouped(U, x, k, k, r, s, pl.sa, part, (uint16_t *)dA, false, g64, sm);
     if (he != hipSuccess) return hip_status(he, "grouped backward dA launch");
     he = nf4q::launch_mreduce_grouped((const uint16_t *)T, dy, n, n, r, s, pl.sb, part, (uint16_t *)dB,

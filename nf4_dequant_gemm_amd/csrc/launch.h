@@ -170,10 +170,11 @@ hipError_t launch_gemm_dx_grouped(const GemmArgs &g, const GroupArgs &gr, hipStr
 // out[m][j] = sum_l in[m][l] * p[j][l] for j < r (p row-major [r][L], leading dim ldp).
 // With splits > 1 the partial sums go to part and are added in split order: by a second launch
 // into out, from split-major partials (float [splits][M][r]); or, with out == NULL, by their
-// consumer, from partials with the splits of one output contiguous (float [M][r][splits]).
+// consumer, from partials with the splits of one output contiguous (float [M][r][splits]). With wide
+// (part then holds the partials of a single split, too) the float32 sums are written there as well.
 hipError_t launch_rowproj(const uint16_t *in, int64_t ldin, const uint16_t *p, int64_t ldp,
                           int64_t M, int64_t L, int r, int splits, float *part, uint16_t *out,
-                          hipStream_t st);
+                          hipStream_t st, float *wide = nullptr);
 int rowproj_splits(int64_t M, int64_t L);
 
 // out = bf16(s * sum over m of P[m][j] * Q[m][c]); P [M][r] (ld r), Q [M][C] (ld ldq).
@@ -191,7 +192,8 @@ hipError_t launch_transpose(const uint16_t *src, int64_t L, int r, uint16_t *dst
 // [C][r] there); partials need E * splits * r * C floats.
 hipError_t launch_rowproj_grouped(const uint16_t *in, int64_t ldin, const uint16_t *p, int64_t pstride,
                                   int64_t ldp, int64_t M, int64_t L, int r, int splits, float *part,
-                                  uint16_t *out, const GroupArgs &gr, hipStream_t st);
+                                  uint16_t *out, const GroupArgs &gr, hipStream_t st,
+                                  float *wide = nullptr);
 hipError_t launch_mreduce_grouped(const uint16_t *P, const uint16_t *Q, int64_t ldq, int64_t C, int r,
                                   float s, int splits, float *part, uint16_t *out,
                                   bool transposed_out, const GroupArgs &gr, hipStream_t st);
@@ -399,11 +401,12 @@ struct Act8 {
 };
 hipError_t launch_act8_pack(const void *x, bool f32, int64_t ldx, const Act8 &q, hipStream_t st);
 hipError_t launch_act8_unpack(const Act8 &q, void *x, bool f32, int64_t ldx, hipStream_t st);
-// launch_mreduce (E == 0: rows 0 .. M - 1, one sum) and launch_mreduce_grouped with the second factor in 8
-// bits: row m is row (map ? map[m] : m) of q, of zeros where that is not one of its rows. part: splits *
-// r * C floats for each sum; splits as there.
-hipError_t launch_mreduce_act8(const uint16_t *P, const Act8 &q, const int *map, int64_t M, int r, float s, int splits,
+// launch_mreduce (gr NULL: rows 0 .. M - 1) and launch_mreduce_grouped with the first factor in float32 (16-byte
+// aligned) and the second in 8 bits: row m is row (map ? map[m] : m) of q, zeros where that is not one of its rows
+// (map: grouped only). part: splits * r * C floats for each sum.
+hipError_t launch_mreduce_act8(const float *P, const Act8 &q, const int *map, int64_t M, int r, float s, int splits,
                                float *part, uint16_t *out, const GroupArgs *gr, hipStream_t st);
+int mreduce_act8_splits(int64_t M, int64_t C, int r, int E = 1);
 // launch_swiglu_bwd from the 8-bit form of ygu [m][2n].
 hipError_t launch_swiglu_bwd_act8(const uint16_t *dh, const Act8 &ygu, int64_t n, uint16_t *dygu, hipStream_t st);
 // The sum over the splits that launch_mreduce ends with (E blocks of [r][C]).
