@@ -551,15 +551,15 @@ __global__ __launch_bounds__(256) void mreduce_grouped_kernel(const uint16_t *__
 // The sum of `splits` partials [r][C] at p, four consecutive outputs, in a fixed order (loads issued eight at a time).
 __device__ __forceinline__ f32x4 split_sum4(const float *p, int64_t n, int splits) {
   f32x4 a = {0.f, 0.f, 0.f, 0.f};
-  int sp = 0;
-  for (; sp + 8 <= splits; sp += 8) {
+  for (int sp = 0; sp < splits; sp += 8) {
     f32x4 v[8];
 #pragma unroll
-    for (int j = 0; j < 8; ++j) v[j] = *reinterpret_cast<const f32x4 *>(p + (int64_t)(sp + j) * n);
+    for (int j = 0; j < 8; ++j)
+      if (sp + j < splits) v[j] = *reinterpret_cast<const f32x4 *>(p + (int64_t)(sp + j) * n);
 #pragma unroll
-    for (int j = 0; j < 8; ++j) a += v[j];
+    for (int j = 0; j < 8; ++j)
+      if (sp + j < splits) a += v[j];
   }
-  for (; sp < splits; ++sp) a += *reinterpret_cast<const f32x4 *>(p + (int64_t)sp * n);
   return a;
 }
 
@@ -575,14 +575,14 @@ __global__ __launch_bounds__(256) void mreduce_final_kernel(const float *__restr
 }
 
 // The same with [C][r] outputs: a workgroup takes 64 columns, whose outputs are contiguous, through LDS (written one
-// by one at a stride of r the outputs took 9.1 us at r 64, C 11008).
-__global__ __launch_bounds__(256) void mreduce_final_t_kernel(const float *__restrict__ part, int64_t C, int r, int splits,
+// by one at a stride of r the outputs took 9.1 us at r 64, C 11008). Threads: 16 for each rank, up to 1024.
+__global__ __launch_bounds__(1024) void mreduce_final_t_kernel(const float *__restrict__ part, int64_t C, int r, int splits,
                                                               float s, uint16_t *__restrict__ out) {
   __shared__ uint16_t tile[64 * 129];       // [column][rank], rows of an odd length: columns in different banks
   const int64_t c0 = (int64_t)blockIdx.x * 64, n = (int64_t)r * C;
   const int c = (threadIdx.x & 15) * 4, cols = C - c0 < 64 ? (int)(C - c0) : 64, row = r | 1;
   const float *p = part + (int64_t)blockIdx.y * splits * n + c0 + c;
-  for (int j = threadIdx.x >> 4; j < r; j += 16) {
+  for (int j = threadIdx.x >> 4; j < r; j += blockDim.x >> 4) {
     if (c >= cols) continue;
     const f32x4 a = split_sum4(p + (int64_t)j * C, n, splits);
 #pragma unroll
@@ -590,7 +590,7 @@ __global__ __launch_bounds__(256) void mreduce_final_t_kernel(const float *__res
   }
   __syncthreads();
   uint16_t *o = out + (int64_t)blockIdx.y * n + c0 * r;
-  for (int i = threadIdx.x; i < cols * r / 8; i += 256) {      // cols is a multiple of 8
+  for (int i = threadIdx.x; i < cols * r / 8; i += blockDim.x) {      // cols is a multiple of 8
     int at = 8 * i / r * row + 8 * i % r, left = r - 8 * i % r;
     u32x4 v;
 #pragma unroll
@@ -632,7 +632,8 @@ hipError_t launch_mreduce_final(const float *part, int64_t C, int r, int splits,
   const int64_t n = (int64_t)r * C;
   if (r > 128 || C % 8) return hipErrorInvalidValue;
   if (transposed)
-    mreduce_final_t_kernel<<<dim3((unsigned)((C + 63) / 64), (unsigned)E), dim3(256), 0, st>>>(part, C, r, splits, s, out);
+    mreduce_final_t_kernel<<<dim3((unsigned)((C + 63) / 64), (unsigned)E),
+                             dim3(r > 32 ? 1024 : r > 16 ? 512 : 256), 0, st>>>(part, C, r, splits, s, out);
   else
     mreduce_final_kernel<<<dim3((unsigned)((n + 1023) / 1024), (unsigned)E), dim3(256), 0, st>>>(part, n, splits, s, out);
   return hipGetLastError();
