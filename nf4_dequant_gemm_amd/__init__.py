@@ -915,8 +915,8 @@ def moe_route(logits: torch.Tensor, top: int, keep: Optional[torch.Tensor] = Non
     top = int(top)
     if not 1 <= top <= min(16, E):
         raise ValueError(f"top must lie in [1, min(16, E)] (got {top})")
-    place, source, idx = logits.new_empty((3, t * top), dtype=torch.int32).unbind()
-    place, idx = place.view(t, top), idx.view(t, top)
+    place, idx, source = logits.new_empty((3, t, top), dtype=torch.int32).unbind()
+    source = source.view(-1)
     gate = logits.new_empty((t, top), dtype=torch.float32)
     counts, sizes = logits.new_empty(E + 2, dtype=torch.int64).split((E, 2))
     mean_p, losses = logits.new_empty(E + 2, dtype=torch.float32).split((E, 2))

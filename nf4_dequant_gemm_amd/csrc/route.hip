@@ -61,12 +61,22 @@ __device__ __forceinline__ float sum16(float v) {
   }));
 }
 
+// The logits of a lane's experts l + 16 j, all requested at once (the last expert's in the place of one past it; a
+// branch around each load made eight trips to memory of them).
+template <typename XT, int NV>
+__device__ __forceinline__ void load_row(const XT *x, int l, int E, float *v) {
+  XT raw[NV];
+#pragma unroll
+  for (int j = 0; j < NV; ++j) raw[j] = x[l + 16 * j < E ? l + 16 * j : E - 1];
+#pragma unroll
+  for (int j = 0; j < NV; ++j) v[j] = to_f32<XT>(raw[j]);
+}
+
 // A logit as an integer of the same order: 0 for -inf (never chosen), the largest for NaN, +0 for -0.
 __device__ __forceinline__ uint32_t key_of(float x) {
-  if (x != x) return 0xFFFFFFFFu;
-  if (x == -INFINITY) return 0u;
   const uint32_t b = __float_as_uint(x + 0.f);
-  return b ^ ((b >> 31) ? 0xFFFFFFFFu : 0x80000000u);
+  const uint32_t k = b ^ (uint32_t)((int32_t)b >> 31 | (int32_t)0x80000000);
+  return x != x ? 0xFFFFFFFFu : x == -INFINITY ? 0u : k;
 }
 __device__ __forceinline__ float of_key(uint32_t k) {
   return __uint_as_float(k ^ ((k >> 31) ? 0x80000000u : 0xFFFFFFFFu));
@@ -74,9 +84,9 @@ __device__ __forceinline__ float of_key(uint32_t k) {
 
 struct Shared {
   float psum[16][kE];        // by wave
-  float z[16];
+  float z[16], red[4];
   int n[16];
-  int hist[kE], base[kE];
+  int hist[kE], base[kE], total;
   unsigned long long mask[kE];
 };
 
@@ -108,30 +118,32 @@ __device__ __forceinline__ int first_rows(const int *counts, int E, int *base, i
   return *total;
 }
 
-// Places and sources of the tokens [lo, hi), with base[e] the first row of expert e that is theirs.
-__device__ __forceinline__ void place_rows(const RouteArgs &a, int64_t lo, int64_t hi, int *base,
+// Places and sources of the tokens [lo, hi), with base[e] the first row of expert e that is theirs. A thread takes
+// one choice of up to 64 tokens (64 * kRouteMaxTop <= blockDim.x); `e` is its expert among the first of them, whose
+// mask bits are set.
+__device__ __forceinline__ void place_rows(const RouteArgs &a, int64_t lo, int64_t hi, int e, int *base,
                                            unsigned long long *mask) {
-  const int tid = threadIdx.x, top = a.top;
-  for (int64_t c0 = lo; c0 < hi; c0 += 64) {
-    const int left = hi - c0 < 64 ? (int)(hi - c0) : 64;
-    for (int e = tid; e < a.E; e += blockDim.x) mask[e] = 0;
-    __syncthreads();
-    for (int i = tid; i < left * top; i += blockDim.x) {
-      const int e = a.idx[c0 * top + i];
-      if (e >= 0) atomicOr(&mask[e], 1ull << (i / top));
-    }
-    __syncthreads();
-    for (int i = tid; i < left * top; i += blockDim.x) {
-      const int e = a.idx[c0 * top + i], row = i / top;
+  const int tid = threadIdx.x, top = a.top, row = tid / top;
+  for (int64_t c0 = lo;;) {
+    if (row < 64 && c0 + row < hi) {
       int at = -1;
       if (e >= 0) {
         at = base[e] + __popcll(mask[e] & ((1ull << row) - 1));
         a.source[at] = (int)(c0 + row);
       }
-      a.place[c0 * top + i] = at;
+      a.place[c0 * top + tid] = at;
+    }
+    c0 += 64;
+    if (c0 >= hi) return;
+    __syncthreads();
+    if (tid < a.E) {
+      base[tid] += __popcll(mask[tid]);
+      mask[tid] = 0;
     }
     __syncthreads();
-    for (int e = tid; e < a.E; e += blockDim.x) base[e] += __popcll(mask[e]);
+    e = row < 64 && c0 + row < hi ? a.idx[c0 * top + tid] : -1;
+    if (e >= 0) atomicOr(&mask[e], 1ull << row);
+    __syncthreads();
   }
 }
 
@@ -157,19 +169,23 @@ __device__ __forceinline__ void finish(const RouteArgs &a, int count, float psum
   }
 }
 
-// Block b chooses for its a.rows tokens. With one block the places and totals follow at once; with more it
-// leaves its counts [Ep], sums of p [Ep], of lse^2 and its number of tokens for route_place_kernel.
+// Block b chooses for its a.rows tokens. A single block (at most 64 tokens, one for each group of 16 lanes) goes on
+// to the places and totals; more leave their counts [Ep], sums of p [Ep], of lse^2 and numbers of tokens for
+// route_place_kernel.
 template <typename XT, int NV>
 __global__ __launch_bounds__(1024) void route_choose_kernel(RouteArgs a) {
   __shared__ Shared s;
-  __shared__ int s_total;
-  __shared__ float s_red[4];
   const int tid = threadIdx.x, l = tid & 15, groups = blockDim.x / 16, top = a.top, E = a.E;
+  const bool one = gridDim.x == 1;
   const int64_t lo = (int64_t)blockIdx.x * a.rows;
   const int64_t hi = lo + a.rows < a.t ? lo + a.rows : a.t;
-  for (int e = tid; e < kE; e += blockDim.x) s.hist[e] = 0;
+  for (int e = tid; e < kE; e += blockDim.x) {
+    s.hist[e] = 0;
+    s.mask[e] = 0;
+  }
   __syncthreads();
 
+  int my_e = -1;
   float psum[NV], zsum = 0.f;
   int nsum = 0;
 #pragma unroll
@@ -178,16 +194,15 @@ __global__ __launch_bounds__(1024) void route_choose_kernel(RouteArgs a) {
     const XT *x = reinterpret_cast<const XT *>(a.x) + row * a.ld;
     const bool keep = !a.keep || a.keep[row];
     uint32_t key[NV];
+    float v[NV];
+    load_row<XT, NV>(x, l, E, v);
 #pragma unroll
     for (int j = 0; j < NV; ++j) {
-      const int e = l + 16 * j;
-      key[j] = keep && e < E ? key_of(to_f32<XT>(x[e])) : 0u;
+      key[j] = keep && l + 16 * j < E ? key_of(v[j]) : 0u;
+      v[j] = key[j] ? v[j] : -INFINITY;
     }
-    float v[NV];
-#pragma unroll
-    for (int j = 0; j < NV; ++j) v[j] = key[j] ? of_key(key[j]) : -INFINITY;
     // lane k gets choice k
-    int my_e = -1;
+    my_e = -1;
     uint32_t my_key = 0, first = 0;
     for (int k = 0; k < top; ++k) {
       uint32_t best = 0;
@@ -222,8 +237,9 @@ __global__ __launch_bounds__(1024) void route_choose_kernel(RouteArgs a) {
       sum = sum16(sum);
       const float mine = my_e >= 0 ? expf(of_key(my_key) - mx) : 0.f;
       gate = mine / (a.renorm ? sum16(mine) : sum);
+      const float inv = 1.f / sum;
 #pragma unroll
-      for (int j = 0; j < NV; ++j) psum[j] += ev[j] / sum;
+      for (int j = 0; j < NV; ++j) psum[j] += ev[j] * inv;
       const float lse = mx + logf(sum);
       zsum += lse * lse;
       nsum += 1;
@@ -231,7 +247,10 @@ __global__ __launch_bounds__(1024) void route_choose_kernel(RouteArgs a) {
     if (l < top) {
       a.idx[row * top + l] = my_e;
       a.gate[row * top + l] = gate;
-      if (my_e >= 0) atomicAdd(&s.hist[my_e], 1);
+      if (my_e >= 0) {
+        if (one) atomicOr(&s.mask[my_e], 1ull << row);
+        else atomicAdd(&s.hist[my_e], 1);
+      }
     }
   }
 
@@ -259,11 +278,10 @@ __global__ __launch_bounds__(1024) void route_choose_kernel(RouteArgs a) {
     n += s.n[w];
     if (tid < 16 * NV) p += s.psum[w][tid];
   }
-  const int count = tid < kE ? s.hist[tid] : 0;
-  if (gridDim.x > 1) {
+  if (!one) {
     const int64_t b = blockIdx.x;
     if (tid < a.Ep) {
-      a.cnt[b * a.Ep + tid] = count;
+      a.cnt[b * a.Ep + tid] = s.hist[tid];
       a.psum[b * a.Ep + tid] = p;
     }
     if (tid == 0) {
@@ -272,14 +290,26 @@ __global__ __launch_bounds__(1024) void route_choose_kernel(RouteArgs a) {
     }
     return;
   }
-  const int rows = first_rows(s.hist, E, s.base, &s_total);
-  finish(a, count, p, z, n, rows, s_red);
+  const int count = tid < kE ? __popcll(s.mask[tid]) : 0;
+  if (tid < kE) s.hist[tid] = count;
+  __syncthreads();
+  const int rows = first_rows(s.hist, E, s.base, &s.total);
+  const int64_t row = tid / 16;
+  if (row < hi && l < top) {
+    int at = -1;
+    if (my_e >= 0) {
+      at = s.base[my_e] + __popcll(s.mask[my_e] & ((1ull << row) - 1));
+      a.source[at] = (int)row;
+    }
+    a.place[row * top + l] = at;
+  }
   for (int64_t i = rows + tid; i < a.t * top; i += blockDim.x) a.source[i] = -1;
-  place_rows(a, lo, hi, s.base, s.mask);
+  finish(a, count, p, z, n, rows, s.red);
 }
 
-// Block b < a.blocks: the places of its tokens; the last block: counts, mean probabilities and losses.
-__global__ __launch_bounds__(1024) void route_place_kernel(RouteArgs a) {
+// Block b < a.blocks: the places of its tokens; the last block: counts, mean probabilities and losses. Two blocks
+// have to fit on a CU (64 registers): with 256 blocks of tokens the last one otherwise starts when the first ends.
+__global__ __launch_bounds__(1024, 8) void route_place_kernel(RouteArgs a) {
   constexpr int kSlices = 32;
   __shared__ __align__(16) int s_tot[4096], s_bef[4096];     // [slices][Ep]: four for each thread
   __shared__ int s_base[kE], s_cnt[kE], s_total;
@@ -287,6 +317,10 @@ __global__ __launch_bounds__(1024) void route_place_kernel(RouteArgs a) {
   __shared__ float s_red[4];
   const int tid = threadIdx.x, b = blockIdx.x, quads = a.Ep / 4;
   const bool last = b == a.blocks;
+  const int64_t lo = (int64_t)b * a.rows, hi = lo + a.rows < a.t ? lo + a.rows : a.t;
+  const int row = tid / a.top;
+  const int e = row < 64 && lo + row < hi ? a.idx[lo * a.top + tid] : -1;      // of the first 64 tokens
+  if (tid < kE) s_mask[tid] = 0;
   int slices = (int)blockDim.x / quads;
   slices = slices < kSlices ? slices : kSlices;
   const int sl = tid / quads, q = tid % quads;
@@ -303,6 +337,7 @@ __global__ __launch_bounds__(1024) void route_place_kernel(RouteArgs a) {
     *reinterpret_cast<int4 *>(&s_bef[sl * a.Ep + 4 * q]) = bef;
   }
   __syncthreads();
+  if (e >= 0) atomicOr(&s_mask[e], 1ull << row);
   int tot = 0, bef = 0;
   if (tid < a.Ep) {
     for (int i = 0; i < slices; ++i) {
@@ -317,8 +352,8 @@ __global__ __launch_bounds__(1024) void route_place_kernel(RouteArgs a) {
     if (tid < a.E) s_base[tid] += bef;
     for (int64_t i = rows + (int64_t)b * blockDim.x + tid; i < a.t * a.top; i += (int64_t)a.blocks * blockDim.x)
       a.source[i] = -1;
-    const int64_t lo = (int64_t)b * a.rows;
-    place_rows(a, lo, lo + a.rows < a.t ? lo + a.rows : a.t, s_base, s_mask);
+    __syncthreads();
+    place_rows(a, lo, hi, e, s_base, s_mask);
     return;
   }
   // sums of p: slices of blocks as above, in the memory of s_bef
@@ -352,35 +387,31 @@ __global__ __launch_bounds__(1024) void route_place_kernel(RouteArgs a) {
 template <typename XT, int NV>
 __global__ __launch_bounds__(256) void route_bwd_kernel(RouteBwdArgs a) {
   const int tid = threadIdx.x, l = tid & 15, E = a.E, top = a.top;
-  const float n = (float)a.sizes[0], rows = (float)a.sizes[1];
-  float c[NV], zc = 0.f;
+  // requested here, used behind the first row's requests: one trip to memory
+  const int64_t n = a.sizes[0], rows = a.sizes[1];
+  int64_t count[NV];
 #pragma unroll
-  for (int j = 0; j < NV; ++j) c[j] = 0.f;
-  if (a.dlosses) {
-    const float k = a.dlosses[0] * (float)E / n / rows;      // without routed tokens no row uses it
-    zc = 2.f * a.dlosses[1] / n;
-#pragma unroll
-    for (int j = 0; j < NV; ++j)
-      if (l + 16 * j < E) c[j] = k * (float)a.counts[l + 16 * j];
-  }
+  for (int j = 0; j < NV; ++j) count[j] = a.counts[l + 16 * j < E ? l + 16 * j : E - 1];
+  const float db = a.dlosses ? a.dlosses[0] : 0.f, dz = a.dlosses ? a.dlosses[1] : 0.f;
   for (int64_t row = (int64_t)blockIdx.x * 16 + tid / 16; row < a.t; row += (int64_t)gridDim.x * 16) {
     const XT *x = reinterpret_cast<const XT *>(a.x) + row * a.ld;
     XT *dx = reinterpret_cast<XT *>(a.dx) + row * a.ldd;
     int e = l < top ? a.idx[row * top + l] : -1;
+    float dg = a.dgate && l < top ? a.dgate[row * top + l] : 0.f;
+    float v[NV], d[NV];
+    load_row<XT, NV>(x, l, E, v);
+#pragma unroll
+    for (int j = 0; j < NV; ++j) v[j] = l + 16 * j < E ? v[j] : -INFINITY;
     if (e >= E) e = -1;
-    float d[NV];
     if (max16((uint32_t)(e + 1)) == 0) {       // not routed
 #pragma unroll
       for (int j = 0; j < NV; ++j) d[j] = 0.f;
     } else {
-      float v[NV], mx = -INFINITY, sum = 0.f, dot = 0.f;
-#pragma unroll
-      for (int j = 0; j < NV; ++j) {
-        v[j] = l + 16 * j < E ? to_f32<XT>(x[l + 16 * j]) : -INFINITY;
-        mx = fmaxf(mx, v[j]);
-      }
       const float xe = e >= 0 ? to_f32<XT>(x[e]) : 0.f;
-      const float dg = a.dgate && e >= 0 ? a.dgate[row * top + l] : 0.f;
+      if (e < 0) dg = 0.f;
+      float mx = -INFINITY, sum = 0.f, dot = 0.f;
+#pragma unroll
+      for (int j = 0; j < NV; ++j) mx = fmaxf(mx, v[j]);
       mx = __uint_as_float(over16(__float_as_uint(mx), [](uint32_t p, uint32_t q) {
         return __float_as_uint(fmaxf(__uint_as_float(p), __uint_as_float(q)));
       }));
@@ -396,8 +427,11 @@ __global__ __launch_bounds__(256) void route_bwd_kernel(RouteBwdArgs a) {
       float w = g * dg;
       const float mean = sum16(w);
       if (a.renorm) w -= g * mean;
+      const float k = db * (float)E / (float)n / (float)rows, zc = 2.f * dz / (float)n;
+      float c[NV];
 #pragma unroll
       for (int j = 0; j < NV; ++j) {
+        c[j] = k * (float)count[j];
         v[j] *= inv;
         dot += v[j] * c[j];
       }
@@ -432,7 +466,7 @@ RoutePlan route_plan(int64_t t, int E) {
   p.Ep = (E + 15) / 16 * 16;
   // at most 64 tokens: one workgroup of 16 lanes a token; otherwise 16 tokens a workgroup, and more of
   // them (up to 64 at once, in up to 1024 threads) where that would be over 256 workgroups
-  p.rows = t <= 64 ? 64 : 16 * ((t + 16 * kRouteMaxBlocks - 1) / (16 * kRouteMaxBlocks));
+  p.rows = t <= 64 ? (t <= 16 ? 16 : 64) : 16 * ((t + 16 * kRouteMaxBlocks - 1) / (16 * kRouteMaxBlocks));
   p.blocks = t > 0 ? (int)((t + p.rows - 1) / p.rows) : 1;      // without tokens the totals are still written
   p.threads = p.rows >= 64 ? 1024 : 16 * (int)p.rows;
   p.bytes = p.blocks > 1 ? (size_t)p.blocks * (8 * p.Ep + 8) : 0;
