@@ -12,6 +12,8 @@
 // act8_pack and act8_unpack read and write each element once and are bound by memory. Where the layer's
 // backward pass uses the kept activation, the codes are read in its place, decoded on the way into the
 // matrix cores or the activation's derivative, and never expanded in memory.
+#include <type_traits>
+
 #include "common.h"
 #include "launch.h"
 
@@ -83,8 +85,14 @@ __device__ __forceinline__ uint32_t four_codes(const Piece<XT> &p, int i, float 
   return perm(perm(c[3], c[2], 0x0C0C0400u), perm(c[1], c[0], 0x0C0C0400u), 0x05040100u);
 }
 
-// A thread packs 16 elements; four lanes make a block. kVec: whole 16-byte loads (k, ldx and the base allow
-// them); otherwise element by element.
+// 16 bytes in memory, aligned to that (kVec) or to their elements.
+typedef u32x4 __attribute__((aligned(2))) u32x4_by2;
+typedef u32x4 __attribute__((aligned(4))) u32x4_by4;
+template <typename XT, bool kVec>
+using Mem16 = std::conditional_t<kVec, u32x4, std::conditional_t<sizeof(XT) == 2, u32x4_by2, u32x4_by4>>;
+
+// A thread packs 16 elements; four lanes make a block. kVec: k, ldx and the base are multiples of 16 bytes;
+// otherwise rows lie at any alignment and the last chunk of a row may be short.
 template <typename XT, bool kVec>
 __global__ __launch_bounds__(256) void act8_pack_kernel(const XT *__restrict__ x, int64_t ldx, Act8 q) {
   const uint32_t pieces = (uint32_t)(q.kp / 16);
@@ -95,25 +103,23 @@ __global__ __launch_bounds__(256) void act8_pack_kernel(const XT *__restrict__ x
   const bool live = row < q.rows;         // whole blocks of four lanes
   Piece<XT> p;
   const XT *src = x + row * ldx + c;
-  if constexpr (kVec) {
+  constexpr int P = 16 / (int)sizeof(XT);
 #pragma unroll
-    for (int i = 0; i < Piece<XT>::kWords / 4; ++i) {
-      u32x4 v = {0, 0, 0, 0};
-      if (live && c + i * (16 / (int)sizeof(XT)) < q.k) v = *(reinterpret_cast<const u32x4 *>(src) + i);
+  for (int i = 0; i < 16 / P; ++i) {
+    u32x4 v = {0, 0, 0, 0};
+    const int64_t left = live ? q.k - c - i * P : 0;
+    if (kVec ? left > 0 : left >= P) {
+      v = *reinterpret_cast<const Mem16<XT, kVec> *>(src + i * P);
+    } else if constexpr (!kVec) {
 #pragma unroll
-      for (int e = 0; e < 4; ++e) p.w[4 * i + e] = v[e];
+      for (int e = 0; e < P - 1; ++e)
+        if (e < left) {
+          if constexpr (sizeof(XT) == 2) v[e >> 1] |= (uint32_t)src[i * P + e] << (16 * (e & 1));
+          else v[e] = __float_as_uint(src[i * P + e]);
+        }
     }
-  } else {
 #pragma unroll
-    for (int e = 0; e < 16; ++e) {
-      uint32_t v = 0;
-      if (live && c + e < q.k) {
-        if constexpr (sizeof(XT) == 2) v = src[e];
-        else v = __float_as_uint(src[e]);
-      }
-      if constexpr (sizeof(XT) == 2) p.w[e / 2] = (e & 1) ? (p.w[e / 2] | (v << 16)) : v;
-      else p.w[e] = v;
-    }
+    for (int e = 0; e < 4; ++e) p.w[4 * i + e] = v[e];
   }
   uint32_t m = top_bits(p);
   m = umax(m, (uint32_t)__builtin_amdgcn_mov_dpp((int)m, 0xB1, 0xF, 0xF, true));   // lanes 1, 0, 3, 2
@@ -154,25 +160,26 @@ __global__ __launch_bounds__(256) void act8_unpack_kernel(Act8 q, XT *__restrict
 #pragma unroll
   for (int e = 0; e < 16; ++e) v[e] = code_value(codes[e >> 2], e & 3, scale);
   XT *dst = x + row * ldx + c;
-  if constexpr (kVec) {
-    constexpr int P = 16 / (int)sizeof(XT);
+  constexpr int P = 16 / (int)sizeof(XT);
 #pragma unroll
-    for (int i = 0; i < 16 / P; ++i) {
-      u32x4 o;
+  for (int i = 0; i < 16 / P; ++i) {
+    u32x4 o;
 #pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        if constexpr (sizeof(XT) == 2) o[e] = pack_bf16x2(v[P * i + 2 * e], v[P * i + 2 * e + 1]);
-        else o[e] = __float_as_uint(v[P * i + e]);
-      }
-      if (c + i * P < q.k) *(reinterpret_cast<u32x4 *>(dst) + i) = o;
+    for (int e = 0; e < 4; ++e) {
+      if constexpr (sizeof(XT) == 2) o[e] = pack_bf16x2(v[P * i + 2 * e], v[P * i + 2 * e + 1]);
+      else o[e] = __float_as_uint(v[P * i + e]);
     }
-  } else {
+    const int64_t left = q.k - c - i * P;
+    if (kVec ? left > 0 : left >= P) {
+      *reinterpret_cast<Mem16<XT, kVec> *>(dst + i * P) = o;
+    } else if constexpr (!kVec) {
 #pragma unroll
-    for (int e = 0; e < 16; ++e)
-      if (c + e < q.k) {
-        if constexpr (sizeof(XT) == 2) dst[e] = (uint16_t)(pack_bf16x2(v[e], 0.f) & 0xFFFFu);
-        else dst[e] = v[e];
-      }
+      for (int e = 0; e < P - 1; ++e)
+        if (e < left) {
+          if constexpr (sizeof(XT) == 2) dst[i * P + e] = (uint16_t)(o[e >> 1] >> (16 * (e & 1)));
+          else dst[i * P + e] = __uint_as_float(o[e]);
+        }
+    }
   }
 }
 
