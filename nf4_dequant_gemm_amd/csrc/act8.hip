@@ -6,12 +6,15 @@
 //   code = 127 x / a rounded to the nearest integer, ties to even;   scale = fl32(a / 127)
 //
 // and the block stands for fl32(code scale): at most a / 254 (half a step) from x, up to the rounding of
-// the scale (at the largest float32 the scale is cut so that 127 of it stay finite). A block whose a is below 2^-119 is stored as zeros, so that 127 / a is finite; one with an Inf
-// or NaN gets the scale NaN, so that whatever uses it is NaN.
+// the scale (at the largest float32 the scale is cut so that 127 of it stay finite). A block whose a is below
+// 2^-119 is stored as zeros, so that 127 / a is finite; one with an Inf or NaN gets the scale NaN, so that
+// whatever uses it is NaN.
 //
 // act8_pack and act8_unpack read and write each element once and are bound by memory. Where the layer's
 // backward pass uses the kept activation, the codes are read in its place, decoded on the way into the
 // matrix cores or the activation's derivative, and never expanded in memory.
+//
+// Measured: 16384 x 14336 in bf16 packed in 133 us and unpacked in 137 us (719 MB each, 5.3 TB/s).
 #include <type_traits>
 
 #include "common.h"
@@ -189,7 +192,8 @@ __global__ __launch_bounds__(256) void act8_unpack_kernel(Act8 q, XT *__restrict
 // which bf16 holds exactly, are multiplied as they are. So the one rounding before the float32 sums is that of
 // P scale, and a code costs one and a half vector instructions (a conversion with byte select and sign
 // extension, half a conversion of a pair). With the scale applied to the codes it was two and a half, and with
-// P's rounding made up for by a second bf16 number twice the products (16384 x 14336, rank 32: 72 us).
+// P's rounding made up for by a second bf16 number twice the products (16384 x 14336, rank 32: 72 us). Now that
+// case takes 67 us and 8192 x 4096, rank 64, 16.5 us, most of it memory: without the products 61 us.
 //
 // Workgroup: 32 NW columns x all r (<= 128) rows j over one split of the rows, in stages of 64 rows requested two
 // stages ahead. The codes stay bytes in LDS and are read with the transposing load ds_read_b64_tr_b8, which

@@ -7,10 +7,14 @@
 //   combine      Y_i = base_i + sum_j gate_ij Z[place_ij]      (without gates: the gradient of gather)
 //   combine_bwd  dZ[place_ij] = gate_ij dY_i,  dgate_ij = <dY_i, Z[place_ij]>,  rows without a token 0
 //
-// All three read and write each element once and are bound by memory, so each is organised by token:
-// what belongs to the token (X, dY, the sum of Y) is read or written once, in registers meanwhile, and the
-// rows of its choices are whole contiguous rows. Rows behind the last are zeroed by the token whose share
-// of the row numbers they fall in. Elements move in 16-byte chunks, at any alignment of the rows. Sums are float32 in the order of the choices, rounded once.
+// All three move each element once and are bound by memory, so each is organised by token: what belongs to the
+// token (X, the sum of Y) is read or written once, in registers meanwhile (dY is read by a wave for each choice,
+// neighbours that find it in the caches), and the rows of its choices are whole contiguous rows. Rows behind the
+// last are zeroed by the token whose share of the row numbers they fall in. Elements move in 16-byte chunks, at
+// any alignment of the rows. Sums are float32 in the order of the choices, rounded once.
+//
+// Measured on 8192 tokens of 4096 in bf16, two choices: gather 34.8 us and combine 42.4 us (201 MB each), the
+// backward 57.7 us (335 MB), 4.7 to 5.8 TB/s; 1111 tokens of 1023 float32, six choices: 7.8, 7.8, 11.6 us.
 #include <type_traits>
 
 #include "common.h"
@@ -276,12 +280,14 @@ bool vec_rows(const MoeRowsArgs &a, size_t esz) {
 }  // namespace
 
 hipError_t launch_gather(const MoeRowsArgs &a, bool f32, hipStream_t st) {
-  if (vec_rows(a, f32 ? 4 : 2)) return f32 ? launch_rows_as<float, true, true>(a, st) : launch_rows_as<uint16_t, true, true>(a, st);
+  if (vec_rows(a, f32 ? 4 : 2))
+    return f32 ? launch_rows_as<float, true, true>(a, st) : launch_rows_as<uint16_t, true, true>(a, st);
   return f32 ? launch_rows_as<float, false, true>(a, st) : launch_rows_as<uint16_t, false, true>(a, st);
 }
 
 hipError_t launch_combine(const MoeRowsArgs &a, bool f32, hipStream_t st) {
-  if (vec_rows(a, f32 ? 4 : 2)) return f32 ? launch_rows_as<float, true, false>(a, st) : launch_rows_as<uint16_t, true, false>(a, st);
+  if (vec_rows(a, f32 ? 4 : 2))
+    return f32 ? launch_rows_as<float, true, false>(a, st) : launch_rows_as<uint16_t, true, false>(a, st);
   return f32 ? launch_rows_as<float, false, false>(a, st) : launch_rows_as<uint16_t, false, false>(a, st);
 }
 
