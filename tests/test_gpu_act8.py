@@ -150,6 +150,18 @@ def test_linear(lib, m, k, n, r):
     assert none is None and torch.equal(dA, dA2) and torch.equal(dB, dB2)
 
 
+def test_part_of_the_rows(lib):
+    """Rows of a kept activation are one themselves: a micro-batch's backward from its part."""
+    q, X, A, B, dY = layer(lib, 100, 1088, 72, 8, 3)
+    T = torch.randn(100, 8, device=DEV).bfloat16()
+    whole = lib.act8_pack(X)
+    part = lib.Act8Tensor(whole.codes[37:90], whole.scale[37:90], whole.k)
+    assert torch.equal(lib.act8_unpack(part), lib.act8_unpack(whole)[37:90])
+    got = lib.qlora_bwd_act8(dY[37:90], part, q, A, B, 0.5, T[37:90])
+    want = lib.qlora_bwd_act8(dY[37:90].clone(), lib.act8_pack(X[37:90]), q, A, B, 0.5, T[37:90].clone())
+    assert all(torch.equal(a, b) for a, b in zip(got, want))
+
+
 def test_linear_without_adapter(lib):
     q, X, _, _, dY = layer(lib, 50, 128, 64, 8, 1)
     dX, dA, dB = lib.qlora_bwd_act8(dY, lib.act8_pack(X), q, None, None, 1.0, None)

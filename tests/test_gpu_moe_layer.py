@@ -93,6 +93,31 @@ def test_linear_and_pair_functions(lib):
     assert torch.equal(H, H0) and all(torch.equal(a.grad, b) for a, b in zip(z, want))
 
 
+def test_moe_function_forms(lib):
+    """The grouped function with the rows themselves kept in 8 bits (no source), without adapters, and with an
+    input that needs no gradient."""
+    X, router, q, A, B, _ = layer(lib, 60, 128, 72, 4, 1, 8, 3)
+    counts = torch.tensor([20, 0, 33, 7], device=DEV)
+    dY = torch.randn(60, 72, device=DEV).bfloat16()
+    leaves = [z.clone().requires_grad_() for z in (X, A, B)]
+    kept = lib.act8_pack(X)
+    lib.QLoRAMoEFunction.apply(leaves[0], q, leaves[1], leaves[2], 1.0, counts, kept).backward(dY)
+    ws = torch.empty(lib.moe_workspace_bytes_dev(60, 4, 72, 128, 8), dtype=torch.uint8, device=DEV)
+    Y, T = X.new_empty(60, 72), X.new_empty(60, 8)
+    lib.qlora_moe_fwd_dev(X, counts, q, A, B, 1.0, Y, T, ws)
+    want = lib.qlora_moe_bwd_act8(dY, kept, None, counts, q, A, B, 1.0, T)
+    assert all(torch.equal(a.grad, b) for a, b in zip(leaves, want))
+    x = X.clone().requires_grad_()
+    for k in (None, kept):
+        x.grad = None
+        lib.QLoRAMoEFunction.apply(x, q, None, None, 1.0, counts, k).backward(dY)
+        assert x.grad.isfinite().all() and (k is None or torch.equal(x.grad, first))
+        first = x.grad
+    a, b = (z.clone().requires_grad_() for z in (A, B))
+    lib.QLoRAMoEFunction.apply(X, q, a, b, 1.0, counts).backward(dY)
+    assert torch.equal(b.grad, want[2]) and a.grad.isfinite().all()
+
+
 def step(lib, st):
     """A training step's calls, all on the current stream: everything but the logits' product."""
     r = lib.moe_route(st["x"], 2, st["keep"])

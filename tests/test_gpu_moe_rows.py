@@ -102,6 +102,27 @@ def test_places_outside_the_rows(lib):
     assert torch.equal(dZ[:7], X[source[:7].long()]) and not dZ[7:].any() and not dgate[~live].any()
 
 
+def test_more_choices_than_lanes(lib):
+    """The rows' calls take any number of choices: 70 for each of 5 tokens, in any order of rows."""
+    t, top, d = 5, 70, 40
+    perm = torch.randperm(t * top, generator=torch.Generator().manual_seed(1))
+    place = perm.to(torch.int32).view(t, top)
+    source = torch.empty(t * top, dtype=torch.int32)
+    source[perm] = torch.arange(t, dtype=torch.int32).repeat_interleave(top)
+    X, Z = rows(t, d, torch.float32, 1), rows(t * top, d, torch.float32, 2)
+    gate = torch.rand(t, top, generator=torch.Generator().manual_seed(3))
+    dev = [z.to(DEV) for z in (X, Z, place, source, gate)]
+    assert torch.equal(lib.moe_gather(dev[0], dev[2], dev[3]).cpu(), X[source.long()])
+    want, mag = (route.combine(f(Z.numpy()), place.numpy(), gate.numpy()) for f in (np.asarray, np.abs))
+    assert (np.abs(f32(lib.moe_combine(dev[1], dev[2], dev[4])) - want) <= 80 * U * mag).all()
+    dZ, dg = lib.moe_combine_bwd(dev[0], dev[1], dev[2], dev[3], dev[4])
+    flat = torch.empty(t * top)
+    flat[perm] = gate.reshape(-1)
+    assert torch.equal(dZ.cpu(), flat[:, None] * X[source.long()])
+    z = Z[perm].view(t, top, d).double()
+    assert (dg.cpu().double() - (X.double()[:, None] * z).sum(2)).abs().max() <= 64 * U * d
+
+
 def test_in_place(lib):
     """Y over base, and both directions at once on one buffer where the header allows it."""
     o, place, source = routing(100, 8, 2, 1, 0.1)

@@ -53,7 +53,7 @@ def check(lib, x, top, keep=None, renorm=True, dev_x=None, dl=(0.7, 0.3)):
     return r
 
 
-@pytest.mark.parametrize("t", [1, 2, 63, 64, 65, 1000, 4096, 4097])
+@pytest.mark.parametrize("t", [1, 2, 16, 17, 63, 64, 65, 1000, 4096, 4097])
 @pytest.mark.parametrize("E,top", [(1, 1), (8, 2), (60, 4), (128, 8), (256, 16)])
 def test_route(lib, t, E, top):
     dtype = torch.bfloat16 if t % 2 else torch.float32            # bfloat16 brings ties
@@ -69,13 +69,19 @@ def test_every_register_count(lib, E, top):
 def test_many_tokens(lib):
     """More tokens than the largest grid takes at once."""
     check(lib, logits(20001, 8, torch.float32, 3), 2, renorm=False)
+    check(lib, logits(16500, 16, torch.bfloat16, 3), 16)            # all experts of every token, 80 tokens a block
 
 
 @pytest.mark.parametrize("t", [5, 300])
 def test_padding(lib, t):
+    """Tokens that are not kept, NaN among their logits or not, count for nothing."""
     x = logits(t, 24, torch.float32, 1)
     keep = torch.rand(t, generator=torch.Generator().manual_seed(2)) < 0.6
     check(lib, x, 3, keep)
+    hidden = x.clone()
+    hidden[~keep] = float("nan")
+    a, b = (lib.moe_route(y.to(DEV), 3, keep.to(DEV)) for y in (x, hidden))
+    assert all(torch.equal(p, q) for p, q in zip(a, b))
     check(lib, x, 3, keep.to(torch.uint8) * 2, renorm=False)     # any value but 0
     r = check(lib, x, 3, torch.zeros(t, dtype=torch.bool))       # nothing is routed
     assert not r.counts.any() and not r.losses.any() and (r.source == -1).all()
