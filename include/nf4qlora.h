@@ -540,23 +540,26 @@ typedef struct {
 int act8_pack(const void *X, int dtype, int64_t ldx, const nf4_act8 *q, void *stream);
 int act8_unpack(const nf4_act8 *q, void *X, int dtype, int64_t ldx, void *stream);
 
-/* qlora_bwd with X in 8 bits (m = X->rows): the same U, dX and dB, bit for bit, and dA = s U^T X from U in
+/* qlora_bwd with X in 8 bits (m = X->rows): U, dX and dB as there (up to rank 32 U and dB come from one pass
+ * over dY, in another order of their float32 sums; above they are the same bits), and dA = s U^T X from U in
  * float32 and what the codes stand for: U times a block's scale is rounded to bf16, the codes are not
- * rounded. T must be given when r > 0. ws: qlora_bwd_workspace_bytes. Errors: as qlora_bwd and act8_pack. */
+ * rounded. T must be given when r > 0. Errors: as qlora_bwd and act8_pack. */
+size_t qlora_bwd_act8_workspace_bytes(int64_t m, int64_t n, int64_t k, int32_t r);
 int qlora_bwd_act8(const void *dY, const nf4_act8 *X, const nf4_tensor *W, const void *A, const void *B, int32_t r,
                    float s, const void *T, void *dX, void *dA, void *dB, void *ws, size_t ws_bytes, void *stream);
 
 /* qlora_swiglu_bwd with X and Ygu in 8 bits: the activation's gradient is formed in float32 from what
- * Ygu's codes stand for. Tgu must be given when r > 0. ws: qlora_swiglu_workspace_bytes. Errors: as
- * qlora_swiglu_bwd and act8_pack. */
+ * Ygu's codes stand for. Tgu must be given when r > 0. Errors: as qlora_swiglu_bwd and act8_pack. */
+size_t qlora_swiglu_bwd_act8_workspace_bytes(int64_t m, int64_t n, int64_t k, int32_t r);
 int qlora_swiglu_bwd_act8(const void *dH, const nf4_act8 *X, const nf4_tensor *Wgu, const void *Agu, const void *Bg,
                           const void *Bu, int32_t r, float s, const nf4_act8 *Ygu, const void *Tgu, void *dX, void *dAgu,
                           void *dBg, void *dBu, void *ws, size_t ws_bytes, void *stream);
 
 /* qlora_moe_bwd_dev with X in 8 bits: grouped row i is row source[i] of X (a source outside X's rows: zeros),
  * so that a token's activation is kept once, not once for each of its experts; source NULL: row i, and X
- * has m rows. T must be given when r > 0. ws: qlora_moe_workspace_bytes_dev. Errors: as qlora_moe_bwd_dev
+ * has m rows. T must be given when r > 0. Errors: as qlora_moe_bwd_dev
  * and act8_pack. */
+size_t qlora_moe_bwd_act8_workspace_bytes(int64_t m, int32_t E, int64_t n, int64_t k, int32_t r);
 int qlora_moe_bwd_dev_act8(const void *dY, const nf4_act8 *X, const int32_t *source, int64_t m, const int64_t *counts,
                            int32_t E, const nf4_tensor *W, const void *A, const void *B, int32_t r, float s,
                            const void *T, void *dX, void *dA, void *dB, void *ws, size_t ws_bytes, void *stream);

@@ -53,7 +53,8 @@ EXPORTED = ("nf4_quantize", "nf4_dequantize", "nf4_codebook", "qlora_fwd_workspa
             "distill_topk_fwd", "distill_topk_bwd", "distill_topk_step",
             "moe_route_workspace_bytes", "moe_route", "moe_route_bwd", "moe_gather", "moe_combine",
             "moe_combine_bwd", "act8_pack", "act8_unpack", "qlora_bwd_act8", "qlora_swiglu_bwd_act8",
-            "qlora_moe_bwd_dev_act8")
+            "qlora_moe_bwd_dev_act8", "qlora_bwd_act8_workspace_bytes", "qlora_swiglu_bwd_act8_workspace_bytes",
+            "qlora_moe_bwd_act8_workspace_bytes")
 
 
 class NF4Error(RuntimeError):
@@ -134,6 +135,9 @@ def library() -> ctypes.CDLL:
         "moe_gather": (ctypes.c_int, [vp, ctypes.c_int, i64, i64, i64, vp, vp, i32, vp, vp]),
         "moe_combine": (ctypes.c_int, [vp, ctypes.c_int, i64, i64, vp, i32, vp, vp, i64, vp, i64, vp]),
         "moe_combine_bwd": (ctypes.c_int, [vp, ctypes.c_int, i64, i64, i64, vp, vp, vp, i32, vp, vp, vp, vp]),
+        "qlora_bwd_act8_workspace_bytes": (sz, [i64, i64, i64, i32]),
+        "qlora_swiglu_bwd_act8_workspace_bytes": (sz, [i64, i64, i64, i32]),
+        "qlora_moe_bwd_act8_workspace_bytes": (sz, [i64, i32, i64, i64, i32]),
         "act8_pack": (ctypes.c_int, [vp, ctypes.c_int, i64, vp, vp]),
         "act8_unpack": (ctypes.c_int, [vp, vp, ctypes.c_int, i64, vp]),
         "qlora_bwd_act8": (ctypes.c_int, [vp, vp, vp, vp, vp, i32, f32, vp, vp, vp, vp, vp, sz, vp]),
@@ -1094,7 +1098,7 @@ def qlora_bwd_act8(dY: torch.Tensor, X: Act8Tensor, q: NF4Tensor, A: Optional[to
     _is(dY, "dY", torch.bfloat16, (m, q.n), dev)
     dX = dY.new_empty((m, q.k)) if need_dx else None
     dA, dB = (torch.empty_like(A), torch.empty_like(B)) if r else (None, None)
-    wsb = _bytes_of("qlora_bwd_workspace_bytes", m, q.n, q.k, r)
+    wsb = _bytes_of("qlora_bwd_act8_workspace_bytes", m, q.n, q.k, r)
     ws = dY.new_empty(max(wsb, 1), dtype=torch.uint8)
     _call(dev, "qlora_bwd_act8", dY.data_ptr(), X.packed(), _packed(q), _addr(A if r else None), _addr(B if r else None),
           r, float(s), _addr(T if r else None), _addr(dX), _addr(dA), _addr(dB), ws.data_ptr(), wsb)
@@ -1120,7 +1124,7 @@ def qlora_swiglu_bwd_act8(dH: torch.Tensor, X: Act8Tensor, q: NF4Tensor, Agu: Op
     _is(dH, "dH", torch.bfloat16, (m, n), dev)
     dX = dH.new_empty((m, q.k)) if need_dx else None
     dA, dBg, dBu = (torch.empty_like(Agu), torch.empty_like(Bg), torch.empty_like(Bu)) if r else (None,) * 3
-    wsb = _bytes_of("qlora_swiglu_workspace_bytes", m, n, q.k, r)
+    wsb = _bytes_of("qlora_swiglu_bwd_act8_workspace_bytes", m, n, q.k, r)
     ws = dH.new_empty(max(wsb, 1), dtype=torch.uint8)
     on = lambda t: _addr(t if r else None)
     _call(dev, "qlora_swiglu_bwd_act8", dH.data_ptr(), X.packed(), _packed(q), on(Agu), on(Bg), on(Bu), r, float(s),
@@ -1146,7 +1150,7 @@ def qlora_moe_bwd_act8(dY: torch.Tensor, X: Act8Tensor, source: Optional[torch.T
         raise ValueError(f"X must hold {m} rows without a source (got {X.shape[0]})")
     dX = dY.new_empty((m, q.k)) if need_dx else None
     dA, dB = (torch.empty_like(A), torch.empty_like(B)) if r else (None, None)
-    wsb = _bytes_of("qlora_moe_workspace_bytes_dev", m, E, q.n // E, q.k, r)
+    wsb = _bytes_of("qlora_moe_bwd_act8_workspace_bytes", m, E, q.n // E, q.k, r)
     ws = dY.new_empty(max(wsb, 1), dtype=torch.uint8)
     on = lambda t: _addr(t if r else None)
     _call(dev, "qlora_moe_bwd_dev_act8", dY.data_ptr(), X.packed(), _addr(source), m, counts.data_ptr(), E, _packed(q),

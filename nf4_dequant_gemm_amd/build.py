@@ -26,7 +26,8 @@ ARCH = os.environ.get("NF4Q_ARCH", "gfx950")
 
 SOURCES = ["api.cpp", "quant.hip", "fwd.hip", "decode.hip", "decode16.hip", "dx.hip", "lora.hip",
            "swiglu.hip", "merge.hip", "fp4.hip", "multi.hip", "mid.hip",
-           "headnorm.hip", "distill.hip", "route.hip", "rows.hip", "act8.hip"]
+           "headnorm.hip", "distill.hip", "route.hip", "rows.hip", "act8.hip",
+           "thin.hip"]
 PROBE_SOURCES = ["probe.hip"]
 
 COMMON = ["-O3", "-std=c++17", "-fPIC", f"--offload-arch={ARCH}", "-I", INCLUDE, "-I", CSRC,

@@ -183,27 +183,38 @@ FwdWs fwd_ws(int64_t m, int64_t k, int32_t r) {
 
 struct BwdWs {
   int splits_u = 1, splits_a = 1, splits_b = 1, splits_t = 1;
-  int splits_a8 = 1;
-  // byte sizes: U at 0, Bt at u, T (recomputed when the caller passes none) or, with X in 8 bits, where T is
-  // given, U in float32 at u + bt, partials at u + bt + t
+  // byte sizes: U at 0, Bt at u, T (recomputed when the caller passes none) at u + bt, partials
+  // at u + bt + t. With X in 8 bits T is given and U in float32 stands in its place.
   size_t u = 0, bt = 0, t = 0, part = 0, total = 0;
 };
 
-BwdWs bwd_ws(int64_t m, int64_t n, int64_t k, int32_t r) {
+BwdWs bwd_ws(int64_t m, int64_t n, int64_t k, int32_t r, bool act8 = false) {
   BwdWs w;
   if (r <= 0) return w;
   w.u = align256((size_t)m * r * 2);
-  w.bt = align256((size_t)r * n * 2);
-  w.t = align256((size_t)m * r * 4);
   w.splits_u = nf4q::rowproj_splits(m, n);
-  w.splits_t = nf4q::rowproj_splits(m, k);
-  w.splits_a = nf4q::mreduce_splits(m, k, r);
   w.splits_b = nf4q::mreduce_splits(m, n, r);
-  w.splits_a8 = nf4q::mreduce_act8_splits(m, k, r);
-  size_t p = (size_t)w.splits_u * m * r * 4;
-  if (w.splits_t > 1) p = std::max(p, (size_t)w.splits_t * m * r * 4);
-  p = std::max(p, (size_t)std::max(w.splits_a, w.splits_a8) * r * k * 4);
-  p = std::max(p, (size_t)w.splits_b * r * n * 4);
+  size_t p = 0;
+  if (act8) {
+    w.t = align256((size_t)m * r * 4);
+    w.splits_a = nf4q::mreduce_act8_splits(m, k, r);
+    if (nf4q::thin_takes(n, r)) {
+      const nf4q::ThinPlan t = nf4q::thin_plan(m, n, r, 1);
+      p = (t.u_floats + t.b_floats) * 4;
+    } else {
+      w.bt = align256((size_t)r * n * 2);
+      p = std::max((size_t)w.splits_u * m * r * 4, (size_t)w.splits_b * r * n * 4);
+    }
+  } else {
+    w.bt = align256((size_t)r * n * 2);
+    w.t = align256((size_t)m * r * 2);
+    w.splits_t = nf4q::rowproj_splits(m, k);
+    w.splits_a = nf4q::mreduce_splits(m, k, r);
+    if (w.splits_u > 1) p = std::max(p, (size_t)w.splits_u * m * r * 4);
+    if (w.splits_t > 1) p = std::max(p, (size_t)w.splits_t * m * r * 4);
+    p = std::max(p, (size_t)w.splits_b * r * n * 4);
+  }
+  p = std::max(p, (size_t)w.splits_a * r * k * 4);
   w.part = align256(p);
   w.total = w.u + w.bt + w.t + w.part;
   return w;
@@ -216,7 +227,7 @@ struct SwiWs {
   size_t b2 = 0, t = 0, fwd = 0, dy2 = 0, db2 = 0, bwd = 0, total = 0;
 };
 
-SwiWs swi_ws(int64_t m, int64_t n, int64_t k, int32_t r) {
+SwiWs swi_ws(int64_t m, int64_t n, int64_t k, int32_t r, bool act8 = false) {
   SwiWs w;
   if (r > 0) {
     w.b2 = align256((size_t)(2 * n) * (2 * r) * 2);
@@ -225,13 +236,13 @@ SwiWs swi_ws(int64_t m, int64_t n, int64_t k, int32_t r) {
     w.db2 = w.b2;
   }
   w.dy2 = align256((size_t)m * (2 * n) * 2);
-  w.bwd = bwd_ws(m, 2 * n, k, 2 * r).total;
+  w.bwd = bwd_ws(m, 2 * n, k, 2 * r, act8).total;
   w.total = w.b2 + std::max(w.t + w.fwd, w.dy2 + w.db2 + w.bwd);
   return w;
 }
 
 int check_swiglu(const void *X, int64_t m, const nf4_tensor *Wgu, const void *Agu, const void *Bg,
-                 const void *Bu, int32_t r, void *ws, size_t ws_bytes, size_t *need) {
+                 const void *Bu, int32_t r, void *ws, size_t ws_bytes, size_t *need, bool act8 = false) {
   int st = check_weight(Wgu);
   if (st) return st;
   if (Wgu->n % 2) return fail(NF4_EINVAL, "Wgu must hold 2n rows (got %lld)", (long long)Wgu->n);
@@ -244,7 +255,7 @@ int check_swiglu(const void *X, int64_t m, const nf4_tensor *Wgu, const void *Ag
     if (!Bg || !Bu) return fail(NF4_EINVAL, "Bg and Bu must be non-NULL when r > 0");
     if (!aligned16(Bg) || !aligned16(Bu)) return fail(NF4_EINVAL, "Bg and Bu must be 16-byte aligned");
   }
-  *need = swi_ws(m, n, Wgu->k, r).total;
+  *need = swi_ws(m, n, Wgu->k, r, act8).total;
   if (ws_bytes < *need || !ws)
     return fail(NF4_EINVAL, "workspace of %zu bytes is smaller than the %zu required", ws_bytes,
                 *need);
@@ -304,7 +315,7 @@ int check_moe_dev(const void *X, int64_t m, const int64_t *dcounts, int32_t E, c
 // gives the same sums in the same order whether it is given on the host or on the device, and
 // one expert gives the single layer's.
 struct MoePlan {
-  int sp_k = 1, sp_n = 1, sa = 1, sb = 1, sa8 = 1;
+  int sp_k = 1, sp_n = 1, sa = 1, sb = 1;
 };
 
 MoePlan moe_plan(int64_t mtotal, int32_t E, int64_t n, int64_t k, int32_t r) {
@@ -313,19 +324,19 @@ MoePlan moe_plan(int64_t mtotal, int32_t E, int64_t n, int64_t k, int32_t r) {
   pl.sp_n = nf4q::rowproj_splits(mtotal, n);
   pl.sa = nf4q::mreduce_splits(mtotal, k, r, E);
   pl.sb = nf4q::mreduce_splits(mtotal, n, r, E);
-  pl.sa8 = nf4q::mreduce_act8_splits(mtotal, k, r, E);
   return pl;
 }
 
 // Workspace of the grouped layer: with device routing the group table first (table bytes),
-// then U [m, r], the transposed stacked B [r, E n], T (recomputed when the caller passes none) or, with X in
-// 8 bits, U in float32,
-// then float partials of the row projections or of the M-reductions (never both at once).
+// then U [m, r], the transposed stacked B [r, E n], T (recomputed when the caller passes none),
+// then float partials of the row projections or of the M-reductions (never both at once). With
+// X in 8 bits T is given and U in float32 stands in its place.
 struct MoeWs {
   size_t table = 0, u = 0, bt = 0, t = 0, part = 0, total = 0;
 };
 
-MoeWs moe_ws_layout(int64_t mtotal, int32_t E, int64_t n, int64_t k, int32_t r, bool dev) {
+MoeWs moe_ws_layout(int64_t mtotal, int32_t E, int64_t n, int64_t k, int32_t r, bool dev,
+                    bool act8 = false) {
   MoeWs w;
   if (dev) w.table = align256(nf4q::moe_table_bytes(E));
   // the grouped dX's split tail tiles: at most kDxMaxWidth pieces, and at most kDxMaxPieces per
@@ -336,12 +347,22 @@ MoeWs moe_ws_layout(int64_t mtotal, int32_t E, int64_t n, int64_t k, int32_t r, 
   if (r > 0) {
     const MoePlan pl = moe_plan(mtotal, E, n, k, r);
     w.u = align256((size_t)mtotal * r * 2);
-    w.bt = align256((size_t)r * E * n * 2);
-    w.t = align256((size_t)mtotal * r * 4);
-    if (pl.sp_k > 1) p = std::max(p, (size_t)pl.sp_k * mtotal * r * 4);
-    p = std::max(p, (size_t)pl.sp_n * mtotal * r * 4);
-    p = std::max(p, (size_t)E * std::max(pl.sa, pl.sa8) * r * k * 4);
-    p = std::max(p, (size_t)E * pl.sb * r * n * 4);
+    if (act8 && nf4q::thin_takes(n, r)) {
+      const nf4q::ThinPlan tp = nf4q::thin_plan(mtotal, n, r, E);
+      p = std::max(p, (tp.u_floats + tp.b_floats) * 4);
+    } else {
+      w.bt = align256((size_t)r * E * n * 2);
+      if (pl.sp_n > 1 || act8) p = std::max(p, (size_t)pl.sp_n * mtotal * r * 4);
+      p = std::max(p, (size_t)E * pl.sb * r * n * 4);
+    }
+    if (act8) {
+      w.t = align256((size_t)mtotal * r * 4);
+      p = std::max(p, (size_t)E * nf4q::mreduce_act8_splits(mtotal, k, r, E) * r * k * 4);
+    } else {
+      w.t = w.u;
+      if (pl.sp_k > 1) p = std::max(p, (size_t)pl.sp_k * mtotal * r * 4);
+      p = std::max(p, (size_t)E * pl.sa * r * k * 4);
+    }
   }
   w.part = align256(p);
   w.total = w.table + w.u + w.bt + w.t + w.part;
@@ -634,7 +655,7 @@ int bwd_impl(const void *dY, const void *X, const nf4q::Act8 *x8, int64_t m, con
   }
   if (!dX && r == 0) return ok();
   const int64_t n = W->n, k = W->k;
-  const BwdWs lay = bwd_ws(m, n, k, r);
+  const BwdWs lay = bwd_ws(m, n, k, r, x8 != nullptr);
   if (ws_bytes < lay.total || (lay.total && !ws))
     return fail(NF4_EINVAL, "workspace of %zu bytes is smaller than the %zu required", ws_bytes,
                 lay.total);
@@ -654,7 +675,13 @@ int bwd_impl(const void *dY, const void *X, const nf4q::Act8 *x8, int64_t m, con
     if (e != hipSuccess) return hip_status(e, "qlora_bwd T launch");
     T = Tw;
   }
-  if (r > 0) {
+  // with X in 8 bits (and so T given) U and dB in one pass over dY, up to the rank where that pays
+  const bool thin = x8 && nf4q::thin_takes(n, r);
+  if (thin) {
+    const nf4q::ThinArgs a{dy, (const uint16_t *)B, (const uint16_t *)T, m, n, r, 1, s, part, U, Uw, (uint16_t *)dB};
+    e = nf4q::launch_thin_bwd(a, nullptr, sm);
+    if (e != hipSuccess) return hip_status(e, "qlora_bwd U and dB launch");
+  } else if (r > 0) {
     e = nf4q::launch_transpose((const uint16_t *)B, n, r, Bt, sm);
     if (e != hipSuccess) return hip_status(e, "qlora_bwd transpose launch");
     e = nf4q::launch_rowproj(dy, n, Bt, n, m, n, r, lay.splits_u, part, U, sm, Uw);
@@ -665,10 +692,11 @@ int bwd_impl(const void *dY, const void *X, const nf4q::Act8 *x8, int64_t m, con
     if (e != hipSuccess) return hip_status(e, "qlora_bwd dX launch");
   }
   if (r > 0) {
-    e = x8 ? nf4q::launch_mreduce_act8(Uw, *x8, nullptr, m, r, s, lay.splits_a8, part, (uint16_t *)dA, nullptr, sm)
+    e = x8 ? nf4q::launch_mreduce_act8(Uw, *x8, nullptr, m, r, s, lay.splits_a, part, (uint16_t *)dA, nullptr, sm)
            : nf4q::launch_mreduce(U, (const uint16_t *)X, k, m, k, r, s, lay.splits_a, part,
                                   (uint16_t *)dA, false, sm);
     if (e != hipSuccess) return hip_status(e, "qlora_bwd dA launch");
+    if (thin) return ok();
     e = nf4q::launch_mreduce((const uint16_t *)T, dy, n, m, n, r, s, lay.splits_b, part,
                              (uint16_t *)dB, true, sm);
     if (e != hipSuccess) return hip_status(e, "qlora_bwd dB launch");
@@ -786,7 +814,7 @@ int swiglu_bwd_impl(const void *dH, const void *X, const nf4q::Act8 *x8, int64_t
                     const void *Ygu, const nf4q::Act8 *y8, const void *Tgu, void *dX, void *dAgu, void *dBg, void *dBu,
                     void *ws, size_t ws_bytes, void *stream) {
   size_t need = 0;
-  int st = check_swiglu(X, m, Wgu, Agu, Bg, Bu, r, ws, ws_bytes, &need);
+  int st = check_swiglu(X, m, Wgu, Agu, Bg, Bu, r, ws, ws_bytes, &need, x8 != nullptr);
   if (st) return st;
   if (!dH || !aligned16(dH) || !Ygu || !aligned16(Ygu))
     return fail(NF4_EINVAL, "dH and Ygu must be non-NULL and 16-byte aligned");
@@ -798,7 +826,7 @@ int swiglu_bwd_impl(const void *dH, const void *X, const nf4q::Act8 *x8, int64_t
   }
   if (!dX && r == 0) return ok();
   const int64_t n = Wgu->n / 2;
-  const SwiWs lay = swi_ws(m, n, Wgu->k, r);
+  const SwiWs lay = swi_ws(m, n, Wgu->k, r, x8 != nullptr);
   hipStream_t sm = (hipStream_t)stream;
   char *base = (char *)ws;
   uint16_t *B2 = r > 0 ? (uint16_t *)base : nullptr;
@@ -937,7 +965,7 @@ int moe_bwd_impl(const void *dY, const void *X, const nf4q::Act8 *x8, const int3
   }
   const int64_t k = W->k, n = mo.n;
   const bool dev = mo.dcounts != nullptr;
-  const MoeWs lay = moe_ws_layout(mo.mtotal, E, n, k, r, dev);
+  const MoeWs lay = moe_ws_layout(mo.mtotal, E, n, k, r, dev, x8 != nullptr);
   int st = check_moe_ws(lay, ws, ws_bytes);
   if (st) return st;
   if (!dX && r == 0) return ok();
@@ -958,7 +986,17 @@ int moe_bwd_impl(const void *dY, const void *X, const nf4q::Act8 *x8, const int3
   nf4q::GroupArgs g64;
   st = moe_groups(mo, E, 1, &g64, 64, table, 2);
   if (st) return st;
-  if (r > 0) {
+  const bool thin = x8 && nf4q::thin_takes(n, r);      // as in bwd_impl
+  if (thin) {
+    nf4q::GroupArgs g256;
+    const int64_t per = (n + 255) / 256;      // the table counts the row blocks times the forward's column tiles
+    st = moe_groups(mo, E, per, &g256, nf4q::kThinRows, table, 0);
+    if (st) return st;
+    const nf4q::ThinArgs ta{dy, (const uint16_t *)B, (const uint16_t *)T, mo.mtotal, n, r, (int)per, s, part, U, Uw,
+                            (uint16_t *)dB};
+    he = nf4q::launch_thin_bwd(ta, &g256, sm);
+    if (he != hipSuccess) return hip_status(he, "grouped backward U and dB launch");
+  } else if (r > 0) {
     he = nf4q::launch_transpose((const uint16_t *)B, E * n, r, Bt, sm);
     if (he != hipSuccess) return hip_status(he, "grouped backward transpose launch");
     if (!T) {
@@ -1004,9 +1042,11 @@ int moe_bwd_impl(const void *dY, const void *X, const nf4q::Act8 *x8, const int3
   // dA_e = s U_e^T X_e, dB_e = s dY_e^T T_e over each expert's own rows, every expert in one
   // launch each (an expert with no rows sums nothing: zero gradients)
   if (r > 0) {
-    he = x8 ? nf4q::launch_mreduce_act8(Uw, *x8, map, mo.mtotal, r, s, pl.sa8, part, (uint16_t *)dA, &g64, sm)
+    he = x8 ? nf4q::launch_mreduce_act8(Uw, *x8, map, mo.mtotal, r, s,
+                                       nf4q::mreduce_act8_splits(mo.mtotal, k, r, E), part, (uint16_t *)dA, &g64, sm)
             : nf4q::launch_mreduce_grouped(U, x, k, k, r, s, pl.sa, part, (uint16_t *)dA, false, g64, sm);
     if (he != hipSuccess) return hip_status(he, "grouped backward dA launch");
+    if (thin) return ok();
     he = nf4q::launch_mreduce_grouped((const uint16_t *)T, dy, n, n, r, s, pl.sb, part, (uint16_t *)dB,
                                       true, g64, sm);
     if (he != hipSuccess) return hip_status(he, "grouped backward dB launch");
@@ -1766,6 +1806,19 @@ int act8_unpack(const nf4_act8 *q, void *X, int dtype, int64_t ldx, void *stream
   if (st) return st;
   if (a.rows == 0) return ok();
   return hip_status(nf4q::launch_act8_unpack(a, X, dtype == NF4_F32, ldx, (hipStream_t)stream), "act8_unpack launch");
+}
+
+size_t qlora_bwd_act8_workspace_bytes(int64_t m, int64_t n, int64_t k, int32_t r) {
+  return m < 1 || n < 1 || k < 1 || r < 0 ? 0 : bwd_ws(m, n, k, r, true).total;
+}
+
+size_t qlora_swiglu_bwd_act8_workspace_bytes(int64_t m, int64_t n, int64_t k, int32_t r) {
+  return m < 1 || n < 1 || k < 1 || r < 0 ? 0 : swi_ws(m, n, k, r, true).total;
+}
+
+size_t qlora_moe_bwd_act8_workspace_bytes(int64_t m, int32_t E, int64_t n, int64_t k, int32_t r) {
+  if (m < 1 || E < 1 || E > nf4q::kMaxExperts || n < 1 || k < 1 || r < 0) return 0;
+  return moe_ws_layout(m, E, n, k, r, true, true).total;
 }
 
 int qlora_bwd_act8(const void *dY, const nf4_act8 *X, const nf4_tensor *W, const void *A, const void *B, int32_t r,

@@ -176,6 +176,8 @@ hipError_t launch_rowproj(const uint16_t *in, int64_t ldin, const uint16_t *p, i
                           int64_t M, int64_t L, int r, int splits, float *part, uint16_t *out,
                           hipStream_t st, float *wide = nullptr);
 int rowproj_splits(int64_t M, int64_t L);
+// The sum over the splits that it ends with: out (bf16) and wide (float32; NULL: none) from float [splits][n].
+hipError_t launch_rowproj_reduce(const float *part, int64_t n, int splits, uint16_t *out, float *wide, hipStream_t st);
 
 // out = bf16(s * sum over m of P[m][j] * Q[m][c]); P [M][r] (ld r), Q [M][C] (ld ldq).
 // transposed_out: out[c][j] (ld r) else out[j][c] (ld C). part: float [splits][r][C].
@@ -407,6 +409,27 @@ hipError_t launch_act8_unpack(const Act8 &q, void *x, bool f32, int64_t ldx, hip
 hipError_t launch_mreduce_act8(const float *P, const Act8 &q, const int *map, int64_t M, int r, float s, int splits,
                                float *part, uint16_t *out, const GroupArgs *gr, hipStream_t st);
 int mreduce_act8_splits(int64_t M, int64_t C, int r, int E = 1);
+// U = dY B (bf16, and in float32) and dB = s dY^T T (bf16 [N][r]) in one pass over dY [M][N] (thin.hip), where
+// thin_takes(N, r): up to the rank where it pays, and rows whose 256 are addressed with 31 bits; N % 8 == 0. Grouped (gr: 256-row blocks of the experts, counted times `per`): B [E][N][r] and dB are the
+// experts', the grid is bounded by M and E. part: u_floats + b_floats of thin_plan.
+constexpr int kThinMaxRank = 32, kThinRows = 256;
+inline bool thin_takes(int64_t N, int r) { return r > 0 && r <= kThinMaxRank && N <= (int64_t(1) << 22); }
+struct ThinPlan {
+  int64_t blocks, lsplit;
+  int splits;
+  size_t u_floats, b_floats;
+};
+ThinPlan thin_plan(int64_t M, int64_t N, int r, int E);
+struct ThinArgs {
+  const uint16_t *dy, *B, *T;
+  int64_t M, N;
+  int r, per;
+  float s, *part;
+  uint16_t *U;
+  float *Uw;
+  uint16_t *dB;
+};
+hipError_t launch_thin_bwd(const ThinArgs &a, const GroupArgs *gr, hipStream_t st);
 // launch_swiglu_bwd from the 8-bit form of ygu [m][2n].
 hipError_t launch_swiglu_bwd_act8(const uint16_t *dh, const Act8 &ygu, int64_t n, uint16_t *dygu, hipStream_t st);
 // The sum over the splits that launch_mreduce ends with (E blocks of [r][C]).

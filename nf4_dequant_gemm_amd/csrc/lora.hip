@@ -9,6 +9,7 @@
 // so the results are deterministic (no atomics).
 #include "common.h"
 #include "launch.h"
+#include "sums.h"
 
 namespace nf4q {
 
@@ -258,6 +259,13 @@ __global__ void rowproj_reduce_kernel(const float *__restrict__ part, int64_t n,
   }
 }
 
+hipError_t launch_rowproj_reduce(const float *part, int64_t n, int splits, uint16_t *out, float *wide, hipStream_t st) {
+  int64_t blocks = (n + 255) / 256;
+  if (blocks > 4096) blocks = 4096;
+  rowproj_reduce_kernel<<<dim3((unsigned)blocks), dim3(256), 0, st>>>(part, n, splits, out, wide);
+  return hipGetLastError();
+}
+
 int rowproj_splits(int64_t M, int64_t L) {
   const int64_t wgs = (M + 63) / 64;
   int64_t s = (1024 + wgs - 1) / wgs;
@@ -295,11 +303,7 @@ hipError_t launch_rowproj(const uint16_t *in, int64_t ldin, const uint16_t *p, i
   }
   hipError_t e = hipGetLastError();
   if (e != hipSuccess || !pp || !out) return e;
-  const int64_t n = M * r;
-  int64_t blocks = (n + 255) / 256;
-  if (blocks > 4096) blocks = 4096;
-  rowproj_reduce_kernel<<<dim3((unsigned)blocks), dim3(256), 0, st>>>(part, n, splits, out, wide);
-  return hipGetLastError();
+  return launch_rowproj_reduce(part, M * r, splits, out, wide, st);
 }
 
 hipError_t launch_rowproj_grouped(const uint16_t *in, int64_t ldin, const uint16_t *p, int64_t pstride,
@@ -321,11 +325,7 @@ hipError_t launch_rowproj_grouped(const uint16_t *in, int64_t ldin, const uint16
   }
   hipError_t e = hipGetLastError();
   if (e != hipSuccess || !pp) return e;
-  const int64_t n = M * r;
-  int64_t nb = (n + 255) / 256;
-  if (nb > 4096) nb = 4096;
-  rowproj_reduce_kernel<<<dim3((unsigned)nb), dim3(256), 0, st>>>(part, n, splits, out, wide);
-  return hipGetLastError();
+  return launch_rowproj_reduce(part, M * r, splits, out, wide, st);
 }
 
 // ------------------------------------------------------------------- group tables (routing on the device)
@@ -548,21 +548,6 @@ __global__ __launch_bounds__(256) void mreduce_grouped_kernel(const uint16_t *__
   mreduce_body<TJ, kPVec, true>(P, Q, ldq, 0, C, r, 0, part, gr);
 }
 
-// The sum of `splits` partials [r][C] at p, four consecutive outputs, in a fixed order (loads issued eight at a time).
-__device__ __forceinline__ f32x4 split_sum4(const float *p, int64_t n, int splits) {
-  f32x4 a = {0.f, 0.f, 0.f, 0.f};
-  for (int sp = 0; sp < splits; sp += 8) {
-    f32x4 v[8];
-#pragma unroll
-    for (int j = 0; j < 8; ++j)
-      if (sp + j < splits) v[j] = *reinterpret_cast<const f32x4 *>(p + (int64_t)(sp + j) * n);
-#pragma unroll
-    for (int j = 0; j < 8; ++j)
-      if (sp + j < splits) a += v[j];
-  }
-  return a;
-}
-
 // out = s * (sum over splits of part), for blocks blockIdx.y of [r][C] (one unless grouped); block e of the output is
 // [r][C] at out + e r C. C % 4 == 0 (every C is a multiple of 8).
 __global__ __launch_bounds__(256) void mreduce_final_kernel(const float *__restrict__ part, int64_t n, int splits, float s,
@@ -574,37 +559,11 @@ __global__ __launch_bounds__(256) void mreduce_final_kernel(const float *__restr
                                                                        pack_bf16x2(s * a[2], s * a[3])};
 }
 
-// The same with [C][r] outputs: a workgroup takes 64 columns, whose outputs are contiguous, through LDS (written one
-// by one at a stride of r the outputs took 9.1 us at r 64, C 11008). Threads: 16 for each rank, up to 1024.
-__global__ __launch_bounds__(1024) void mreduce_final_t_kernel(const float *__restrict__ part, int64_t C, int r, int splits,
-                                                              float s, uint16_t *__restrict__ out) {
-  __shared__ uint16_t tile[64 * 129];       // [column][rank], rows of an odd length: columns in different banks
-  const int64_t c0 = (int64_t)blockIdx.x * 64, n = (int64_t)r * C;
-  const int c = (threadIdx.x & 15) * 4, cols = C - c0 < 64 ? (int)(C - c0) : 64, row = r | 1;
-  const float *p = part + (int64_t)blockIdx.y * splits * n + c0 + c;
-  for (int j = threadIdx.x >> 4; j < r; j += blockDim.x >> 4) {
-    if (c >= cols) continue;
-    const f32x4 a = split_sum4(p + (int64_t)j * C, n, splits);
-#pragma unroll
-    for (int e = 0; e < 4; ++e) tile[(c + e) * row + j] = (uint16_t)(pack_bf16x2(s * a[e], 0.f) & 0xFFFFu);
-  }
-  __syncthreads();
-  uint16_t *o = out + (int64_t)blockIdx.y * n + c0 * r;
-  for (int i = threadIdx.x; i < cols * r / 8; i += blockDim.x) {      // cols is a multiple of 8
-    int at = 8 * i / r * row + 8 * i % r, left = r - 8 * i % r;
-    u32x4 v;
-#pragma unroll
-    for (int e = 0; e < 8; ++e) {
-      const uint32_t h = tile[at];
-      v[e / 2] = e & 1 ? v[e / 2] | (h << 16) : h;
-      ++at;
-      if (--left == 0) {
-        at += row - r;
-        left = r;
-      }
-    }
-    *reinterpret_cast<u32x4 *>(o + 8 * i) = v;
-  }
+// The same with [C][r] outputs.
+__global__ __launch_bounds__(1024) void mreduce_final_t_kernel(const float *__restrict__ part, int64_t C, int r,
+                                                               int splits, float s, uint16_t *__restrict__ out) {
+  const int64_t n = (int64_t)r * C;
+  split_sum_t(part + (int64_t)blockIdx.y * splits * n, C, r, splits, s, out + (int64_t)blockIdx.y * n);
 }
 
 // Splits of the M-reduction over C / 128 column tiles. One layer: as many as let ONE round of
@@ -633,7 +592,7 @@ hipError_t launch_mreduce_final(const float *part, int64_t C, int r, int splits,
   if (r > 128 || C % 8) return hipErrorInvalidValue;
   if (transposed)
     mreduce_final_t_kernel<<<dim3((unsigned)((C + 63) / 64), (unsigned)E),
-                             dim3(r > 32 ? 1024 : r > 16 ? 512 : 256), 0, st>>>(part, C, r, splits, s, out);
+                             dim3(split_sum_t_threads(r)), 0, st>>>(part, C, r, splits, s, out);
   else
     mreduce_final_kernel<<<dim3((unsigned)((n + 1023) / 1024), (unsigned)E), dim3(256), 0, st>>>(part, n, splits, s, out);
   return hipGetLastError();

@@ -1,7 +1,7 @@
 """Activations in 8 bits against the oracle: codes, scales and unpacked values have to be equal, bit for bit.
 
 The layers' backward passes from them: what does not touch the kept activation equals the bf16 layer's bit for
-bit. dA = s U^T X is checked against float64 sums: U times the scale as the matrix cores take it (rounded to bf16:
+bit above rank 32; up to there U and dB are other sums of the same products, see close_rest. dA = s U^T X is checked against float64 sums: U times the scale as the matrix cores take it (rounded to bf16:
 half a step, 2^-8 of every term), U's float32 sums (below 2^-14 of the terms in it), float32 sums (m 2^-24 of the magnitudes at most, taken as
 2^-10 for m <= 2^14), and the result's half step 2^-8.
 """
@@ -135,8 +135,25 @@ def close_dA(got, U, X, s):
     assert (np.abs(f32(got) - want) <= 2.0 ** -8 * np.abs(want) + (2.0 ** -8 + 2.0 ** -10) * mag).all()
 
 
+def close_rest(dX, dB, want, dY, W, A, B, T, s):
+    """dX and dB against the bf16 layer's: bit for bit above rank 32. Up to there U's float32 sums are taken in another
+    order, each within 2^-10 of the magnitudes' sum, so its bf16 values differ by that twice and a step of 2^-7, and dX
+    by what s A makes of it, other roundings of its own float32 sums (n <= 2^13: within 2^-11) and a step. dB against float64 sums: 2^-10 of the magnitudes, half a step."""
+    if A.shape[0] > 32:
+        assert torch.equal(dX, want[0]) and torch.equal(dB, want[2])
+        return
+    dY, W, A, B, T = (z.double() for z in (dY, W, A, B, T))
+    U, mag = dY @ B, dY.abs() @ B.abs()
+    assert ((dX.double() - want[0].double()).abs() <=
+            2.0 ** -7 * want[0].double().abs() + s * (2.0 ** -7 * U.abs() + 2.0 ** -8 * mag) @ A.abs()
+            + 2.0 ** -11 * dY.abs() @ W.abs()).all()
+    ref, mag = s * dY.t() @ T, s * dY.abs().t() @ T.abs()
+    assert ((dB.double() - ref).abs() <= 2.0 ** -8 * ref.abs() + 2.0 ** -10 * mag).all()
+
+
 @pytest.mark.parametrize("m,k,n,r", [(1, 64, 8, 1), (17, 320, 72, 7), (64, 256, 256, 8), (300, 1088, 136, 16), (1000, 448, 264, 20),
-                                     (257, 192, 64, 33), (500, 256, 512, 64), (130, 4096, 64, 100), (2100, 128, 64, 128)])
+                                     (257, 192, 64, 33), (500, 256, 512, 64), (130, 4096, 64, 100), (2100, 128, 64, 128),
+                                     (257, 128, 8, 1), (1000, 64, 392, 31), (513, 64, 1032, 32), (2000, 192, 4104, 13), (256, 64, 6152, 24)])
 def test_linear(lib, m, k, n, r):
     q, X, A, B, dY = layer(lib, m, k, n, r, m)
     T = torch.randn(m, r, device=DEV).bfloat16()
@@ -144,7 +161,7 @@ def test_linear(lib, m, k, n, r):
     X8 = lib.act8_pack(X)
     dX, dA, dB = lib.qlora_bwd_act8(dY, X8, q, A, B, s, T)
     want = lib.qlora_bwd(dY, lib.act8_unpack(X8), q, A, B, s, T)
-    assert torch.equal(dX, want[0]) and torch.equal(dB, want[2])
+    close_rest(dX, dB, want, dY, lib.nf4_dequantize(q, F32), A, B, T, s)
     close_dA(dA, dY.double() @ B.double(), lib.act8_unpack(X8, F32), s)
     none, dA2, dB2 = lib.qlora_bwd_act8(dY, X8, q, A, B, s, T, need_dx=False)
     assert none is None and torch.equal(dA, dA2) and torch.equal(dB, dB2)
@@ -196,7 +213,7 @@ def test_pair(lib, m, k, n, r):
 
 
 @pytest.mark.parametrize("t,k,n,E,top,r", [(1, 64, 8, 2, 1, 1), (40, 256, 72, 4, 2, 8), (500, 320, 136, 8, 2, 16),
-                                           (300, 192, 64, 3, 3, 40), (2000, 128, 64, 16, 1, 4)])
+                                           (300, 192, 64, 3, 3, 40), (2000, 128, 64, 16, 1, 4), (900, 64, 1160, 3, 2, 21)])
 @pytest.mark.parametrize("grouped", [False, True])
 def test_moe(lib, t, k, n, E, top, r, grouped):
     """The tokens kept once (through the routing), or the grouped rows themselves; every eighth token is padding."""
@@ -219,14 +236,18 @@ def test_moe(lib, t, k, n, E, top, r, grouped):
     ws = torch.empty(lib.moe_workspace_bytes_dev(m, E, n, k, r), dtype=torch.uint8, device=DEV)
     want = torch.empty(m, k, dtype=BF, device=DEV), torch.empty_like(A), torch.empty_like(B)
     lib.qlora_moe_bwd_dev(dY, Xg, ro.counts, q, A, B, 2.0, T, *want, ws)
-    assert torch.equal(dX[:N], want[0][:N]) and torch.equal(dB, want[2])
+    W = lib.nf4_dequantize(q, F32)
     lo, v = 0, f32(lib.act8_unpack(X8, F32))
     for e, c in enumerate(ro.counts.tolist()):
         rows = v[lo:lo + c] if grouped else v[ro.source[lo:lo + c].cpu().numpy()]
         mine = dA[e * r:(e + 1) * r]
         if c == 0:
             assert not mine.any()
+            assert not dB[e * n:(e + 1) * n].any()
         else:
+            b, a = B[e * n:(e + 1) * n], A[e * r:(e + 1) * r]
+            close_rest(dX[lo:lo + c], dB[e * n:(e + 1) * n], (want[0][lo:lo + c], None, want[2][e * n:(e + 1) * n]),
+                       dY[lo:lo + c], W[e * n:(e + 1) * n], a, b, T[lo:lo + c], 2.0)
             close_dA(mine, dY[lo:lo + c].double() @ B[e * n:(e + 1) * n].double(), torch.from_numpy(rows), 2.0)
         lo += c
 

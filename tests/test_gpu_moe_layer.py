@@ -65,7 +65,7 @@ def test_gradients(lib, t, d, hidden, E, top, r, renorm, eight):
     ((dY * Y).float().sum() + coef[0] * ro.losses[0] + coef[1] * ro.losses[1]).backward()
     want, grads = reference(lib, X, router, q, A, B, 1.5, ro.idx, dY, coef, renorm)
     near = lambda name, got, ref, tol: (lambda e: (say(f"  {name} {e:.1e}"), e)[1])(
-        float((got.double() - ref).norm() / ref.norm())) <= tol
+        float((got.detach().double() - ref).norm() / ref.norm())) <= tol
     assert near("Y", Y, want, 2.0 ** -7) and not Y[~keep].any()
     for name, leaf, g in zip(("X", "router", "A", "B"), leaves, grads):
         assert near(name, leaf.grad, g, 2.0 ** -7 + (2.0 ** -6 if name == "A" and eight else 0)), name
@@ -115,7 +115,11 @@ def test_moe_function_forms(lib):
         first = x.grad
     a, b = (z.clone().requires_grad_() for z in (A, B))
     lib.QLoRAMoEFunction.apply(X, q, a, b, 1.0, counts).backward(dY)
-    assert torch.equal(b.grad, want[2]) and a.grad.isfinite().all()
+    # dB from bf16 rows: the same products in another order of float32 sums (2^-10 of the magnitudes each), and a step
+    rows = lambda z: [e.double().abs() for e in z[:60].split(counts.tolist())]
+    mag = torch.cat([d.t() @ t for d, t in zip(rows(dY), rows(T))])
+    assert ((b.grad.double() - want[2].double()).abs() <= 2.0 ** -7 * want[2].double().abs() + 2.0 ** -9 * mag).all()
+    assert a.grad.isfinite().all()
 
 
 def step(lib, st):

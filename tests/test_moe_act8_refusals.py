@@ -101,8 +101,11 @@ def weight(n=64, k=128):
 def test_act8_layers_refuse():
     lib = m.library()
     M, n, k, r, E = 10, 64, 128, 8, 2
-    wb, wp = lib.qlora_bwd_workspace_bytes(M, n, k, r), lib.qlora_swiglu_workspace_bytes(M, n // 2, k, r)
-    wm = lib.qlora_moe_workspace_bytes_dev(M, E, n // E, k, r)
+    wb, wp = lib.qlora_bwd_act8_workspace_bytes(M, n, k, r), lib.qlora_swiglu_bwd_act8_workspace_bytes(M, n // 2, k, r)
+    wm = lib.qlora_moe_bwd_act8_workspace_bytes(M, E, n // E, k, r)
+    assert min(wb, wp, wm) > 0 and lib.qlora_bwd_act8_workspace_bytes(0, n, k, r) == 0
+    assert lib.qlora_swiglu_bwd_act8_workspace_bytes(M, 0, k, r) == 0
+    assert lib.qlora_moe_bwd_act8_workspace_bytes(M, 257, n, k, r) == 0
 
     def linear(**o):
         a = dict(dY=FAKE, X=act8(), W=weight(), A=FAKE, B=FAKE, r=r, T=FAKE, dX=FAKE, dA=FAKE, dB=FAKE, ws=FAKE, wsb=wb) | o
