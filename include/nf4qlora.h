@@ -540,7 +540,7 @@ typedef struct {
 int act8_pack(const void *X, int dtype, int64_t ldx, const nf4_act8 *q, void *stream);
 int act8_unpack(const nf4_act8 *q, void *X, int dtype, int64_t ldx, void *stream);
 
-/* qlora_bwd with X in 8 bits (m = X->rows): U, dX and dB as there (up to rank 32 U and dB come from one pass
+/* qlora_bwd with X in 8 bits (m = X->rows): U, dX and dB as there (up to rank 64 U and dB come from one pass
  * over dY, in another order of their float32 sums; above they are the same bits), and dA = s U^T X from U in
  * float32 and what the codes stand for: U times a block's scale is rounded to bf16, the codes are not
  * rounded. T must be given when r > 0. Errors: as qlora_bwd and act8_pack. */

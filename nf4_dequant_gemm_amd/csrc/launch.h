@@ -412,7 +412,7 @@ int mreduce_act8_splits(int64_t M, int64_t C, int r, int E = 1);
 // U = dY B (bf16, and in float32) and dB = s dY^T T (bf16 [N][r]) in one pass over dY [M][N] (thin.hip), where
 // thin_takes(N, r): up to the rank where it pays, and rows whose 256 are addressed with 31 bits; N % 8 == 0. Grouped (gr: 256-row blocks of the experts, counted times `per`): B [E][N][r] and dB are the
 // experts', the grid is bounded by M and E. part: u_floats + b_floats of thin_plan.
-constexpr int kThinMaxRank = 32, kThinRows = 256;
+constexpr int kThinMaxRank = 64, kThinRows = 256;
 inline bool thin_takes(int64_t N, int r) { return r > 0 && r <= kThinMaxRank && N <= (int64_t(1) << 22); }
 struct ThinPlan {
   int64_t blocks, lsplit;

@@ -1,15 +1,18 @@
 // Both thin products of the backward pass over dY in one pass over it (gfx950, bf16 MFMA):
 //
-//   U = dY B  [M][r]     and     dB = s dY^T T  [N][r],   r <= 32
+//   U = dY B  [M][r]     and     dB = s dY^T T  [N][r],   r <= 64
 //
 // for the layers that keep X in 8 bits. Each reads all of dY and little else, so the two launches of lora.hip cost
 // two reads of it. Here a workgroup takes 256 rows and a range of columns, in steps of 128 columns that are staged in
 // LDS once and multiplied twice: rows by B (U's sums over the range stay in registers until its end), and columns by T
 // (dB's sums over the 256 rows, written after each step). Sums over ranges and over row blocks are added in a
-// fixed order by further launches. The partials of dB are r / 64 of dY's bytes, written and read, which is
-// what a second read of dY costs at rank 64: above 32 the two launches stay.
+// fixed order by further launches. T, a step of dY and of B are 125 KB of LDS at rank 64; at 128 they are more than
+// there is, and the partials of dB, written and read, twice dY's bytes: above 64 the two launches stay.
 //
-// Bound by memory: a step's 64 KB are requested two steps ahead, 128 KB in flight on every CU.
+// Bound by memory: a step's 64 KB are requested two steps ahead, 128 KB in flight on every CU. All of the adapters'
+// gradients, k 512, against the two launches: 8192 x 14336 at rank 64 163 us (180), 48 155 (171), 40 148 (168);
+// 16384 x 14336 at 64 255 (290); 4096 x 11008 at 64 86 (98), at 8 63 (78); 64 x 4096 at 16 21 (27). This kernel alone
+// reads 16384 x 14336 of 8 experts at rank 16 in 116 us (4.0 TB/s).
 #include "common.h"
 #include "launch.h"
 #include "sums.h"
@@ -68,14 +71,18 @@ __global__ __launch_bounds__(kT) void thin_kernel(const uint16_t *__restrict__ d
   const int64_t lb = split * lsplit, le = lb + lsplit < N ? lb + lsplit : N;
 
   // rows of a matrix [.][r] in LDS rows of PROW: 16-byte chunks, or element by element
+  constexpr int NV = TJ > 2 ? 2 : 1;
   struct Narrow {
-    u32x4 v;
+    u32x4 v[NV];
     uint16_t e[kVec ? 1 : 4 * TJ];
   };
   auto get = [&](__amdgpu_buffer_rsrc_t rs, int first, Narrow &x) {     // 128 rows from `first` on
     if constexpr (kVec) {
-      const int row = tid / CH, j = tid % CH * 8;
-      x.v = load16(rs, row < 128 && j < r ? (uint32_t)(((first + row) * r + j) * 2) : kNowhere);
+#pragma unroll
+      for (int i = 0; i < NV; ++i) {
+        const int row = (tid + kT * i) / CH, j = (tid + kT * i) % CH * 8;
+        x.v[i] = load16(rs, row < 128 && j < r ? (uint32_t)(((first + row) * r + j) * 2) : kNowhere);
+      }
     } else {
 #pragma unroll
       for (int i = 0; i < 4 * TJ; ++i) {
@@ -86,8 +93,11 @@ __global__ __launch_bounds__(kT) void thin_kernel(const uint16_t *__restrict__ d
   };
   auto put = [&](uint16_t *tile, const Narrow &x) {
     if constexpr (kVec) {
-      const int row = tid / CH;
-      if (row < 128) *reinterpret_cast<u32x4 *>(&tile[row * PROW + tid % CH * 8]) = x.v;
+#pragma unroll
+      for (int i = 0; i < NV; ++i) {
+        const int row = (tid + kT * i) / CH;
+        if (row < 128) *reinterpret_cast<u32x4 *>(&tile[row * PROW + (tid + kT * i) % CH * 8]) = x.v[i];
+      }
     } else {
 #pragma unroll
       for (int i = 0; i < 4 * TJ; ++i) tile[(tid + kT * i) / (16 * TJ) * PROW + (tid + kT * i) % (16 * TJ)] = x.e[i];
@@ -247,9 +257,12 @@ hipError_t launch_thin_bwd(const ThinArgs &a, const GroupArgs *gr, hipStream_t s
   if (a.r <= 16) {
     if (a.r & 7) launch_thin_as<1, false>(a, p, part_b, gr, st);
     else launch_thin_as<1, true>(a, p, part_b, gr, st);
-  } else {
+  } else if (a.r <= 32) {
     if (a.r & 7) launch_thin_as<2, false>(a, p, part_b, gr, st);
     else launch_thin_as<2, true>(a, p, part_b, gr, st);
+  } else {
+    if (a.r & 7) launch_thin_as<4, false>(a, p, part_b, gr, st);
+    else launch_thin_as<4, true>(a, p, part_b, gr, st);
   }
   hipError_t e = hipGetLastError();
   if (e != hipSuccess) return e;
