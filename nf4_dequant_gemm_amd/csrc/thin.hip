@@ -12,7 +12,8 @@
 // Bound by memory: a step's 64 KB are requested two steps ahead, 128 KB in flight on every CU. All of the adapters'
 // gradients, k 512, against the two launches: 8192 x 14336 at rank 64 163 us (180), 48 155 (171), 40 148 (168);
 // 16384 x 14336 at 64 255 (290); 4096 x 11008 at 64 86 (98), at 8 63 (78); 64 x 4096 at 16 21 (27). This kernel alone
-// reads 16384 x 14336 of 8 experts at rank 16 in 116 us (4.0 TB/s).
+// reads 16384 x 14336 of 8 experts at rank 16 in 105 us (4.5 TB/s; 116 with ranges of columns sized for the fullest
+// rounds alone), and at rank 64 reads 8192 x 14336 and writes half as many bytes of partials in 67 (5.3 TB/s).
 #include "common.h"
 #include "launch.h"
 #include "sums.h"
@@ -236,14 +237,15 @@ ThinPlan thin_plan(int64_t M, int64_t N, int r, int E) {
   ThinPlan p;
   p.blocks = E > 1 ? (M + (kRB - 1) * (int64_t)E) / kRB : (M + kRB - 1) / kRB;
   if (p.blocks > M) p.blocks = M;
-  // ranges of columns: as many as keep the rounds of 256 workgroups fullest, of at least two steps
-  const int64_t most = (N + 2 * kCB - 1) / (2 * kCB);
-  int64_t best = 1;
-  for (int64_t s = 2; s <= most && s <= 64; ++s) {
-    const int64_t a = (p.blocks * s + 255) / 256, b = (p.blocks * best + 255) / 256;      // rounds
-    if (a * best < b * s) best = s;
+  // ranges of columns of equally many steps (the last one fewer), at least two as the loop takes pairs: the rounds of
+  // 256 workgroups times the steps of one, and one more for its first requests, least
+  const int64_t steps = (N + kCB - 1) / kCB;
+  int64_t best = steps, cost = INT64_MAX;
+  for (int64_t len = steps < 128 ? steps : 128; len >= 2; --len) {
+    const int64_t rounds = (p.blocks * ((steps + len - 1) / len) + 255) / 256;
+    if (rounds * (len + 1) < cost) cost = rounds * (len + 1), best = len;
   }
-  p.lsplit = ((N + best - 1) / best + kCB - 1) / kCB * kCB;
+  p.lsplit = best * kCB;
   p.splits = (int)((N + p.lsplit - 1) / p.lsplit);
   p.u_floats = ((size_t)p.splits * M * r + 63) / 64 * 64;      // the other partials behind them aligned
   p.b_floats = (size_t)p.blocks * r * N;
