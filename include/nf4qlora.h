@@ -540,8 +540,8 @@ typedef struct {
 int act8_pack(const void *X, int dtype, int64_t ldx, const nf4_act8 *q, void *stream);
 int act8_unpack(const nf4_act8 *q, void *X, int dtype, int64_t ldx, void *stream);
 
-/* qlora_bwd with X in 8 bits (m = X->rows): U, dX and dB as there (up to rank 64 U and dB come from one pass
- * over dY, in another order of their float32 sums; above they are the same bits), and dA = s U^T X from U in
+/* qlora_bwd with X in 8 bits (m = X->rows): U, dX and dB as there up to the order of their float32 sums (up to
+ * rank 64 U and dB come from one pass over dY; the reduction of a dX of few tiles is split over workgroups), and dA = s U^T X from U in
  * float32 and what the codes stand for: U times a block's scale is rounded to bf16, the codes are not
  * rounded. T must be given when r > 0. Errors: as qlora_bwd and act8_pack. */
 size_t qlora_bwd_act8_workspace_bytes(int64_t m, int64_t n, int64_t k, int32_t r);

@@ -147,7 +147,8 @@ int check_layer(const void *X, int64_t m, const nf4_tensor *W, const void *A, co
 }
 
 hipError_t launch_dx(const uint16_t *dy, int64_t m, const nf4_tensor *W, const uint16_t *U,
-                     const uint16_t *A, int32_t r, float s, uint16_t *dX, hipStream_t sm) {
+                     const uint16_t *A, int32_t r, float s, uint16_t *dX, hipStream_t sm, int pieces = 1,
+                     float *part = nullptr) {
   nf4q::GemmArgs g;
   g.a_side = dy;
   g.lda = W->n;
@@ -162,7 +163,17 @@ hipError_t launch_dx(const uint16_t *dy, int64_t m, const nf4_tensor *W, const u
   g.out = dX;
   g.ldo = W->k;
   g.t = tables();
-  return nf4q::launch_gemm_dx(g, sm);
+  if (pieces == 1) return nf4q::launch_gemm_dx(g, sm);
+  nf4q::GroupArgs gr{};      // one group of all rows
+  gr.E = 1;
+  gr.m_off[1] = m;
+  gr.tile_off[1] = (int32_t)(((m + 255) / 256) * ((g.C + 255) / 256));
+  gr.grid = gr.tile_off[1];
+  gr.width = nf4q::kDxMaxWidth;
+  gr.smax = pieces;
+  gr.part = part;
+  gr.few = true;
+  return nf4q::launch_gemm_dx_grouped(g, gr, sm);
 }
 
 size_t align256(size_t x) { return (x + 255) & ~size_t(255); }
@@ -182,28 +193,35 @@ FwdWs fwd_ws(int64_t m, int64_t k, int32_t r) {
 }
 
 struct BwdWs {
-  int splits_u = 1, splits_a = 1, splits_b = 1, splits_t = 1;
+  int splits_u = 1, splits_a = 1, splits_b = 1, splits_t = 1, pieces = 1;
   // byte sizes: U at 0, Bt at u, T (recomputed when the caller passes none) at u + bt, partials
-  // at u + bt + t. With X in 8 bits T is given and U in float32 stands in its place.
+  // at u + bt + t. With X in 8 bits T is given and U in float32 stands in its place,
+  // and few tiles of dX are split into `pieces`, whose float32 sums are partials too.
   size_t u = 0, bt = 0, t = 0, part = 0, total = 0;
 };
 
 BwdWs bwd_ws(int64_t m, int64_t n, int64_t k, int32_t r, bool act8 = false) {
   BwdWs w;
+  size_t p = 0;
+  if (act8) {
+    w.pieces = nf4q::dx_few_pieces(m, k, n);
+    if (w.pieces > 1)
+      p = (size_t)(((m + 255) / 256) * ((k + 255) / 256) * w.pieces * nf4q::kDxPieceFloats * 4);
+    if (r <= 0) w.total = w.part = align256(p);
+  }
   if (r <= 0) return w;
   w.u = align256((size_t)m * r * 2);
   w.splits_u = nf4q::rowproj_splits(m, n);
   w.splits_b = nf4q::mreduce_splits(m, n, r);
-  size_t p = 0;
   if (act8) {
     w.t = align256((size_t)m * r * 4);
     w.splits_a = nf4q::mreduce_act8_splits(m, k, r);
     if (nf4q::thin_takes(n, r)) {
       const nf4q::ThinPlan t = nf4q::thin_plan(m, n, r, 1);
-      p = (t.u_floats + t.b_floats) * 4;
+      p = std::max(p, (t.u_floats + t.b_floats) * 4);
     } else {
       w.bt = align256((size_t)r * n * 2);
-      p = std::max((size_t)w.splits_u * m * r * 4, (size_t)w.splits_b * r * n * 4);
+      p = std::max(p, std::max((size_t)w.splits_u * m * r * 4, (size_t)w.splits_b * r * n * 4));
     }
   } else {
     w.bt = align256((size_t)r * n * 2);
@@ -688,7 +706,7 @@ int bwd_impl(const void *dY, const void *X, const nf4q::Act8 *x8, int64_t m, con
     if (e != hipSuccess) return hip_status(e, "qlora_bwd U launch");
   }
   if (dX) {
-    e = launch_dx(dy, m, W, U, (const uint16_t *)A, r, s, (uint16_t *)dX, sm);
+    e = launch_dx(dy, m, W, U, (const uint16_t *)A, r, s, (uint16_t *)dX, sm, lay.pieces, part);
     if (e != hipSuccess) return hip_status(e, "qlora_bwd dX launch");
   }
   if (r > 0) {

@@ -199,7 +199,7 @@ __device__ __forceinline__ void dx_body(const GemmArgs &g, const GroupArgs &gr, 
   if (kGrp) {
     // a grid sized by an upper bound (routing on the device) has workgroups past the last tile
     const int total = grp_tile_off(gr, gr.E);
-    sp = dx_split(gr.width, gr.smax, gr.part != nullptr, total, nsteps);
+    sp = dx_split(gr.width, gr.smax, gr.part != nullptr, total, nsteps, gr.few);
     const int b = (int)blockIdx.x;
     if (b >= sp.full + sp.tail * sp.S) return;
     if (b < sp.full) {
@@ -504,9 +504,11 @@ __device__ __forceinline__ void dx_body(const GemmArgs &g, const GroupArgs &gr, 
     f32x4 *pp = reinterpret_cast<f32x4 *>(gr.part + ((int64_t)tail_i * sp.S + piece) * kDxPieceFloats) +
                 wave * 32 * 64 + lane;
 #pragma unroll
-    for (int kt = 0; kt < 4; ++kt)
+    for (int mt = 0; mt < kMT; ++mt)
+      if (m0 + wm * 128 + mt * 16 < m_hi) {
 #pragma unroll
-      for (int mt = 0; mt < kMT; ++mt) pp[(kt * 8 + mt) * 64] = acc[kt][mt];
+        for (int kt = 0; kt < 4; ++kt) pp[(kt * 8 + mt) * 64] = acc[kt][mt];
+      }
     return;
   }
 
@@ -601,15 +603,15 @@ void launch_split(const GemmArgs &g, const MultiArgs &mu, unsigned grid, hipStre
 
 // The split tiles of a grouped dX launch: workgroups 4 i .. 4 i + 3 add the S float32 pieces of
 // tail tile i in piece order (a fixed order: the result does not depend on which piece finished
-// first), each a quarter of the tile (8 of the 32 accumulator blocks of every wave), scale E2M1
-// sums by the tensor scale, round to bf16 and write the tile. Workgroups past the tail (a grid
+// first), each a quarter of the tile (8 of the 32 accumulator blocks of every wave; a launch of few tiles: 32
+// workgroups of one), scale E2M1 sums by the tensor scale, round to bf16 and write the tile. Workgroups past the tail (a grid
 // sized by an upper bound) exit at once.
 template <int kFmt>
 __global__ __launch_bounds__(kThreads) void dx_tail_kernel(GemmArgs g, GroupArgs gr) {
   const int nsteps = (int)((g.R + kS - 1) / kS);
   const int total = grp_tile_off(gr, gr.E);
-  const DxSplit sp = dx_split(gr.width, gr.smax, gr.part != nullptr, total, nsteps);
-  const int i = (int)blockIdx.x >> 2, quarter = (int)blockIdx.x & 3;
+  const DxSplit sp = dx_split(gr.width, gr.smax, gr.part != nullptr, total, nsteps, gr.few);
+  const int per = gr.few ? 1 : 8, i = (int)blockIdx.x / (32 / per), first = (int)blockIdx.x % (32 / per) * per;
   if (i >= sp.tail) return;
   int logical = sp.full + i;
   const int e = find_group(gr, logical);
@@ -629,11 +631,13 @@ __global__ __launch_bounds__(kThreads) void dx_tail_kernel(GemmArgs g, GroupArgs
                     wave * 32 * 64 + lane;
   constexpr int kPiece = kDxPieceFloats / 4;   // f32x4 per piece
 #pragma unroll 4
-  for (int q = 8 * quarter; q < 8 * quarter + 8; ++q) {   // q = k-tile * 8 + m-tile
-    f32x4 a = pp[q * 64];
-    for (int p = 1; p < sp.S; ++p) a += pp[p * kPiece + q * 64];
+  for (int q = first; q < first + per; ++q) {   // q = k-tile * 8 + m-tile
     const int kt = q >> 3, mt = q & 7;
     const int64_t m = m0 + wm * 128 + mt * 16 + l16;
+    if (m - l16 >= m_hi) continue;              // nothing was written there
+    f32x4 a = pp[q * 64];
+#pragma unroll 4
+    for (int p = 1; p < sp.S; ++p) a += pp[p * kPiece + q * 64];
     const int64_t k = k0 + wk * 64 + kt * 16 + 4 * g16;
     if (m < m_hi && k < g.C)
       *reinterpret_cast<uint2 *>(g.out + m * g.ldo + k) =
@@ -656,7 +660,7 @@ hipError_t launch_gemm_dx_grouped(const GemmArgs &g, const GroupArgs &gr, hipStr
       grid += gr.width;
       tail_grid = gr.width;
     } else {
-      const DxSplit d = dx_split(gr.width, gr.smax, true, gr.tile_off[gr.E], nsteps);
+      const DxSplit d = dx_split(gr.width, gr.smax, true, gr.tile_off[gr.E], nsteps, gr.few);
       grid = d.full + (int64_t)d.tail * d.S;
       tail_grid = d.tail;
     }
@@ -669,7 +673,7 @@ hipError_t launch_gemm_dx_grouped(const GemmArgs &g, const GroupArgs &gr, hipStr
   else
     dx_grouped_kernel<0><<<dim3((unsigned)grid), dim3(kThreads), 0, st>>>(g, gr);
   if (tail_grid > 0) {
-    tail_grid *= 4;   // four workgroups per tile
+    tail_grid *= gr.few ? 32 : 4;   // workgroups per tile
     if (g.w.fp4)
       dx_tail_kernel<2><<<dim3((unsigned)tail_grid), dim3(kThreads), 0, st>>>(g, gr);
     else if (g.w.dq)
@@ -695,6 +699,23 @@ int dx_multi_pieces(int64_t M, int64_t K, int64_t N) {
       best = us;
       pieces = (int)p;
     }
+  }
+  return pieces;
+}
+
+// The same choice for a launch that leaves its pieces by tiles: start and end 10 us, 1.4 a step, and for a split 5 us
+// and the float32 sums of the rows that are there, written and read at 6 TB/s. One piece and the choice (us):
+// 1000 x 1088 x 2832 (20 tiles) 74 and 35, 64 x 4096 x 11008 (16) 251 and 37, 1024 x 4096 x 14336 (64) 332 and 126, 17 x
+// 4096 x 4096 (16) 98 and 26; two pieces of 4096 x 2048 x 2048 (128) took 65 against 60, which the rule leaves whole.
+int dx_few_pieces(int64_t M, int64_t K, int64_t N) {
+  const int64_t tiles_k = (K + kT - 1) / kT, tiles = tiles_k * ((M + kT - 1) / kT), steps = (N + kS - 1) / kS;
+  const double mb = (double)((M + 15) / 16 * 16 * tiles_k * kT) * 4 / 1e6;
+  const int64_t most = kDxMaxWidth / tiles;
+  double best = 10.0 + 1.4 * (double)steps;
+  int pieces = 1;
+  for (int64_t p = 2; p <= most && p <= steps; ++p) {
+    const double us = 15.0 + 1.4 * (double)((steps + p - 1) / p) + (double)p * mb * 2 / 6;
+    if (us < best) best = us, pieces = (int)p;
   }
   return pieces;
 }

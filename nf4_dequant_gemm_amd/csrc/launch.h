@@ -69,20 +69,22 @@ struct GroupArgs {
   // `part`; a second launch adds them (dx_split below). width 0 or part NULL: no split.
   int width = 0, smax = 1;
   float *part = nullptr;
+  bool few = false;             // split the tiles of a launch that is less than one round, too
 };
 
 // The split of a grouped dX launch of `total` tiles with `nsteps` reduction steps per tile: the
 // first `full` tiles run whole (whole rounds of `width` workgroups); each of the `tail` others
 // becomes S pieces of consecutive steps (S >= 2, S <= smax, S * tail <= width, S <= nsteps), or
-// none is split (tail 0, S 1). The workgroups of a launch: full + tail * S. Only a tail behind
-// at least one full round is split: a launch of at most one round keeps whole tiles, as the
+// none is split (tail 0, S 1). The workgroups of a launch: full + tail * S. Unless `few`, only a tail
+// behind at least one full round is split: a launch of at most one round keeps whole tiles, as the
 // plain dX launch does (a grouped launch with one expert then equals it bit for bit).
 struct DxSplit {
   int full, tail, S;
 };
-__host__ __device__ inline DxSplit dx_split(int width, int smax, bool enabled, int total, int nsteps) {
+__host__ __device__ inline DxSplit dx_split(int width, int smax, bool enabled, int total, int nsteps,
+                                                bool few) {
   DxSplit d{total, 0, 1};
-  if (!enabled || width <= 0 || total <= width) return d;
+  if (!enabled || width <= 0 || (total <= width && !few)) return d;
   const int tail = total % width;
   if (tail == 0) return d;
   int S = width / tail;
@@ -166,6 +168,8 @@ hipError_t launch_gemm_dx(const GemmArgs &g, hipStream_t st);
 // kDxPieceFloats float32) set, the tiles of a last, partly filled round are split along the
 // reduction (dx_split) and a second, small launch adds the pieces.
 hipError_t launch_gemm_dx_grouped(const GemmArgs &g, const GroupArgs &gr, hipStream_t st);
+// Pieces for a launch of one layer with few tiles (1: keep them whole).
+int dx_few_pieces(int64_t M, int64_t K, int64_t N);
 
 // out[m][j] = sum_l in[m][l] * p[j][l] for j < r (p row-major [r][L], leading dim ldp).
 // With splits > 1 the partial sums go to part and are added in split order: by a second launch

@@ -65,7 +65,7 @@ def test_gradients(lib, t, d, hidden, E, top, r, renorm, eight):
     ((dY * Y).float().sum() + coef[0] * ro.losses[0] + coef[1] * ro.losses[1]).backward()
     want, grads = reference(lib, X, router, q, A, B, 1.5, ro.idx, dY, coef, renorm)
     near = lambda name, got, ref, tol: (lambda e: (say(f"  {name} {e:.1e}"), e)[1])(
-        float((got.detach().double() - ref).norm() / ref.norm())) <= tol
+        float((got.detach().double() - ref.detach()).norm() / ref.detach().norm())) <= tol
     assert near("Y", Y, want, 2.0 ** -7) and not Y[~keep].any()
     for name, leaf, g in zip(("X", "router", "A", "B"), leaves, grads):
         assert near(name, leaf.grad, g, 2.0 ** -7 + (2.0 ** -6 if name == "A" and eight else 0)), name
