@@ -693,7 +693,7 @@ int bwd_impl(const void *dY, const void *X, const nf4q::Act8 *x8, int64_t m, con
     if (e != hipSuccess) return hip_status(e, "qlora_bwd T launch");
     T = Tw;
   }
-  // with X in 8 bits (and so T given) U and dB in one pass over dY, up to the rank where that pays
+  // with X in 8 bits (and so T given) U and dB in one pass over dY, where thin_takes says so
   const bool thin = x8 && nf4q::thin_takes(n, r);
   if (thin) {
     const nf4q::ThinArgs a{dy, (const uint16_t *)B, (const uint16_t *)T, m, n, r, 1, s, part, U, Uw, (uint16_t *)dB};

@@ -12,8 +12,9 @@
 // Bound by memory: a step's 64 KB are requested two steps ahead, 128 KB in flight on every CU. All of the adapters'
 // gradients, k 512, against the two launches: 8192 x 14336 at rank 64 163 us (180), 48 155 (171), 40 148 (168);
 // 16384 x 14336 at 64 255 (290); 4096 x 11008 at 64 86 (98), at 8 63 (78); 64 x 4096 at 16 21 (27). This kernel alone
-// reads 16384 x 14336 of 8 experts at rank 16 in 105 us (4.5 TB/s; 116 with ranges of columns sized for the fullest
-// rounds alone), and at rank 64 reads 8192 x 14336 and writes half as many bytes of partials in 67 (5.3 TB/s).
+// takes 105 us for 16384 x 11008 of 8 experts at rank 16 (3.4 TB/s; 116 with ranges of columns sized for the fullest
+// rounds alone), and 67 for 8192 x 11008 at rank 64 with half as many bytes of partials (4.0 TB/s). Two workgroups a
+// CU with T in registers at rank 16 took 100, steps in another order for each row block 98 there and 71 for 67 here.
 #include "common.h"
 #include "launch.h"
 #include "sums.h"
