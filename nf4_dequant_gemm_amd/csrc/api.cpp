@@ -216,7 +216,7 @@ BwdWs bwd_ws(int64_t m, int64_t n, int64_t k, int32_t r, bool act8 = false) {
   if (act8) {
     w.t = align256((size_t)m * r * 4);
     w.splits_a = nf4q::mreduce_act8_splits(m, k, r);
-    if (nf4q::thin_takes(n, r)) {
+    if (nf4q::thin_takes(m, n, r)) {
       const nf4q::ThinPlan t = nf4q::thin_plan(m, n, r, 1);
       p = std::max(p, (t.u_floats + t.b_floats) * 4);
     } else {
@@ -365,7 +365,7 @@ MoeWs moe_ws_layout(int64_t mtotal, int32_t E, int64_t n, int64_t k, int32_t r, 
   if (r > 0) {
     const MoePlan pl = moe_plan(mtotal, E, n, k, r);
     w.u = align256((size_t)mtotal * r * 2);
-    if (act8 && nf4q::thin_takes(n, r)) {
+    if (act8 && nf4q::thin_takes(mtotal, n, r, E)) {
       const nf4q::ThinPlan tp = nf4q::thin_plan(mtotal, n, r, E);
       p = std::max(p, (tp.u_floats + tp.b_floats) * 4);
     } else {
@@ -694,7 +694,7 @@ int bwd_impl(const void *dY, const void *X, const nf4q::Act8 *x8, int64_t m, con
     T = Tw;
   }
   // with X in 8 bits (and so T given) U and dB in one pass over dY, where thin_takes says so
-  const bool thin = x8 && nf4q::thin_takes(n, r);
+  const bool thin = x8 && nf4q::thin_takes(m, n, r);
   if (thin) {
     const nf4q::ThinArgs a{dy, (const uint16_t *)B, (const uint16_t *)T, m, n, r, 1, s, part, U, Uw, (uint16_t *)dB};
     e = nf4q::launch_thin_bwd(a, nullptr, sm);
@@ -1004,7 +1004,7 @@ int moe_bwd_impl(const void *dY, const void *X, const nf4q::Act8 *x8, const int3
   nf4q::GroupArgs g64;
   st = moe_groups(mo, E, 1, &g64, 64, table, 2);
   if (st) return st;
-  const bool thin = x8 && nf4q::thin_takes(n, r);      // as in bwd_impl
+  const bool thin = x8 && nf4q::thin_takes(mo.mtotal, n, r, E);      // as in bwd_impl
   if (thin) {
     nf4q::GroupArgs g256;
     const int64_t per = (n + 255) / 256;      // the table counts the row blocks times the forward's column tiles

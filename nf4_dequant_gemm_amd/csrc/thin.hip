@@ -236,8 +236,7 @@ void launch_thin_as(const ThinArgs &a, const ThinPlan &p, float *part_b, const G
 
 ThinPlan thin_plan(int64_t M, int64_t N, int r, int E) {
   ThinPlan p;
-  p.blocks = E > 1 ? (M + (kRB - 1) * (int64_t)E) / kRB : (M + kRB - 1) / kRB;
-  if (p.blocks > M) p.blocks = M;
+  p.blocks = thin_blocks(M, E);
   // ranges of columns of equally many steps (the last one fewer), at least two as the loop takes pairs: the rounds of
   // 256 workgroups times the steps of one, and one more for its first requests, least
   const int64_t steps = (N + kCB - 1) / kCB;
@@ -255,7 +254,7 @@ ThinPlan thin_plan(int64_t M, int64_t N, int r, int E) {
 
 hipError_t launch_thin_bwd(const ThinArgs &a, const GroupArgs *gr, hipStream_t st) {
   const ThinPlan p = thin_plan(a.M, a.N, a.r, gr ? gr->E : 1);
-  if (!thin_takes(a.N, a.r) || a.N % 8 || p.blocks < 1 || p.splits > 65535) return hipErrorInvalidValue;
+  if (!thin_takes(a.M, a.N, a.r, gr ? gr->E : 1) || a.N % 8 || p.blocks < 1 || p.splits > 65535) return hipErrorInvalidValue;
   float *part_b = a.part + p.u_floats;
   if (a.r <= 16) {
     if (a.r & 7) launch_thin_as<1, false>(a, p, part_b, gr, st);

@@ -154,3 +154,12 @@ def test_bindings_refuse():
     w = m.NF4Tensor.empty(64, 192, 0, "cpu")
     with pytest.raises(ValueError, match="k = 192"):
         m.qlora_bwd_act8(x, q, w, None, None, 1.0, None)
+
+
+def test_partials_stay_bounded():
+    """Beside U (in bf16, in float32 and once more as a partial) and B transposed a workspace holds 1 GiB of partials at
+    most, however many rows there are."""
+    lib = m.library()
+    for rows in (1, 256, 5000, 1 << 16, 1 << 20):
+        for n, k, r in ((64, 64, 1), (4096, 14336, 32), (28672, 8192, 64), (14336, 4096, 128)):
+            assert lib.qlora_bwd_act8_workspace_bytes(rows, n, k, r) <= 10 * rows * r + 2 * r * n + (1 << 30) + 1024
