@@ -414,8 +414,8 @@ hipError_t launch_mreduce_act8(const float *P, const Act8 &q, const int *map, in
                                float *part, uint16_t *out, const GroupArgs *gr, hipStream_t st);
 int mreduce_act8_splits(int64_t M, int64_t C, int r, int E = 1);
 // U = dY B (bf16, and in float32) and dB = s dY^T T (bf16 [N][r]) in one pass over dY [M][N] (thin.hip), where
-// thin_takes: up to kThinMaxRank, with rows whose 256 are addressed with 31 bits and 1 GiB of partials of dB at most (they
-// are r / 128 of dY's bytes; those of launch_mreduce do not grow with M); N % 8 == 0. Grouped (gr: 256-row blocks of the experts, counted times `per`): B [E][N][r] and dB are the
+// thin_takes: up to kThinMaxRank, with 1 GiB of partials of dB at most (they are r / 128 of dY's bytes; those
+// of launch_mreduce do not grow with M). N % 8 == 0, N <= 2^22: 256 rows are addressed with 31 bits. Grouped (gr: 256-row blocks of the experts, counted times `per`): B [E][N][r] and dB are the
 // experts', the grid is bounded by M and E. part: u_floats + b_floats of thin_plan.
 constexpr int kThinMaxRank = 64, kThinRows = 256;
 inline int64_t thin_blocks(int64_t M, int E) {
@@ -423,7 +423,7 @@ inline int64_t thin_blocks(int64_t M, int E) {
   return blocks < M ? blocks : M;
 }
 inline bool thin_takes(int64_t M, int64_t N, int r, int E = 1) {
-  return r > 0 && r <= kThinMaxRank && N <= (int64_t(1) << 22) && thin_blocks(M, E) <= (int64_t(1) << 28) / (r * N);
+  return r > 0 && r <= kThinMaxRank && thin_blocks(M, E) <= (int64_t(1) << 28) / (r * N);
 }
 struct ThinPlan {
   int64_t blocks, lsplit;

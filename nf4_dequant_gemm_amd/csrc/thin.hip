@@ -254,7 +254,7 @@ ThinPlan thin_plan(int64_t M, int64_t N, int r, int E) {
 
 hipError_t launch_thin_bwd(const ThinArgs &a, const GroupArgs *gr, hipStream_t st) {
   const ThinPlan p = thin_plan(a.M, a.N, a.r, gr ? gr->E : 1);
-  if (!thin_takes(a.M, a.N, a.r, gr ? gr->E : 1) || a.N % 8 || p.blocks < 1 || p.splits > 65535) return hipErrorInvalidValue;
+  if (!thin_takes(a.M, a.N, a.r, gr ? gr->E : 1) || a.N % 8 || a.N > (int64_t(1) << 22) || p.blocks < 1 || p.splits > 65535) return hipErrorInvalidValue;
   float *part_b = a.part + p.u_floats;
   if (a.r <= 16) {
     if (a.r & 7) launch_thin_as<1, false>(a, p, part_b, gr, st);

@@ -199,7 +199,7 @@ def test_few_tiles(lib, m, k, n, r, form):
     close_rest(dX, dB, lib.qlora_bwd(dY, X, q, A, B, 1.5, T), dY, lib.nf4_dequantize(q, F32), A, B, T, 1.5)
 
 
-@pytest.mark.parametrize("m,k,n,r", [(1, 64, 8, 1), (40, 128, 72, 8), (300, 320, 264, 16), (70, 256, 40, 0), (200, 192, 100 * 8, 64)])
+@pytest.mark.parametrize("m,k,n,r", [(1, 64, 8, 1), (40, 128, 72, 8), (300, 320, 264, 16), (70, 256, 40, 0), (200, 192, 100 * 8, 64), (513, 128, 72, 32)])
 def test_pair(lib, m, k, n, r):
     q, X, A, _, dH = layer(lib, m, k, n, max(r, 1), m, stack=2)
     g = torch.Generator().manual_seed(5)
@@ -227,7 +227,8 @@ def test_pair(lib, m, k, n, r):
 
 
 @pytest.mark.parametrize("t,k,n,E,top,r", [(1, 64, 8, 2, 1, 1), (40, 256, 72, 4, 2, 8), (500, 320, 136, 8, 2, 16),
-                                           (300, 192, 64, 3, 3, 40), (2000, 128, 64, 16, 1, 4), (900, 64, 1160, 3, 2, 21)])
+                                           (300, 192, 64, 3, 3, 40), (2000, 128, 64, 16, 1, 4), (900, 64, 1160, 3, 2, 21),
+                                           (150, 64, 72, 256, 2, 8), (1500, 64, 136, 2, 2, 64)])
 @pytest.mark.parametrize("grouped", [False, True])
 def test_moe(lib, t, k, n, E, top, r, grouped):
     """The tokens kept once (through the routing), or the grouped rows themselves; every eighth token is padding."""
@@ -264,6 +265,49 @@ def test_moe(lib, t, k, n, E, top, r, grouped):
                        dY[lo:lo + c], W[e * n:(e + 1) * n], a, b, T[lo:lo + c], 2.0)
             close_dA(mine, dY[lo:lo + c].double() @ B[e * n:(e + 1) * n].double(), torch.from_numpy(rows), 2.0)
         lo += c
+
+
+def test_longest_rows_of_dy(lib):
+    m, n, k, r, s = 2, 2 ** 22, 64, 4, 0.5
+    rand = lambda *shape: torch.randn(*shape, device=DEV, generator=torch.Generator(DEV).manual_seed(n % 97)).bfloat16()
+    q = lib.NF4Tensor.empty(n, k, 256, torch.device(DEV))       # the weight is not read without dX
+    X, A, B, dY, T = rand(m, k), rand(r, k), rand(n, r), rand(m, n), rand(m, r)
+    X8 = lib.act8_pack(X)
+    none, dA, dB = lib.qlora_bwd_act8(dY, X8, q, A, B, s, T, need_dx=False)
+    assert none is None
+    ref, mag = s * dY.double().t() @ T.double(), s * dY.double().abs().t() @ T.double().abs()
+    assert ((dB.double() - ref).abs() <= 2.0 ** -8 * ref.abs() + 2.0 ** -20 * mag).all()
+    # U is the sum of 2^22 products in chains of at most 2^12 sums: within 2^-12 of its magnitudes' sum
+    U, mag = dY.double() @ B.double(), dY.double().abs() @ B.double().abs()
+    v = lib.act8_unpack(X8, F32).double()
+    want, most = s * U.t() @ v, s * U.abs().t() @ v.abs()
+    assert ((dA.double() - want).abs() <= 2.0 ** -8 * want.abs() + (2.0 ** -8 + 2.0 ** -20) * most
+            + 2.0 ** -12 * s * mag.t() @ v.abs()).all()
+
+
+def test_captured_linear_and_pair(lib):
+    """Captured with few tiles and one pass over dY, replayed with other inputs: the eager call's bits every time."""
+    m, k, n, r = 300, 576, 2048, 8
+    q, X, A, B, dY = layer(lib, m, k, n, r, 1)
+    q2, _, A2, _, _ = layer(lib, m, k, n, r, 2, stack=2)
+    T, T2, Ygu = (torch.randn(m, w, device=DEV).bfloat16() for w in (r, 2 * r, 2 * n))
+    X8, Y8 = lib.act8_pack(X), lib.act8_pack(Ygu)
+    run = lambda: (*lib.qlora_bwd_act8(dY, X8, q, A, B, 0.5, T), *lib.qlora_swiglu_bwd_act8(dY, X8, q2, A2, B, B, 0.5, Y8, T2))
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        run()
+    torch.cuda.current_stream().wait_stream(side)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        outs = run()
+    for i in range(4):
+        dY.copy_(torch.randn(m, n, device=DEV))
+        T.copy_(torch.randn(m, r, device=DEV))
+        graph.replay()
+        torch.cuda.synchronize()
+        got = [o.clone() for o in outs]
+        assert all(torch.equal(a, b) for a, b in zip(got, run())), i
 
 
 def test_moe_foreign_sources(lib):
