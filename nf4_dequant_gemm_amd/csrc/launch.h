@@ -180,8 +180,6 @@ hipError_t launch_rowproj(const uint16_t *in, int64_t ldin, const uint16_t *p, i
                           int64_t M, int64_t L, int r, int splits, float *part, uint16_t *out,
                           hipStream_t st, float *wide = nullptr);
 int rowproj_splits(int64_t M, int64_t L);
-// The sum over the splits that it ends with: out (bf16) and wide (float32; NULL: none) from float [splits][n].
-hipError_t launch_rowproj_reduce(const float *part, int64_t n, int splits, uint16_t *out, float *wide, hipStream_t st);
 
 // out = bf16(s * sum over m of P[m][j] * Q[m][c]); P [M][r] (ld r), Q [M][C] (ld ldq).
 // transposed_out: out[c][j] (ld r) else out[j][c] (ld C). part: float [splits][r][C].
@@ -415,8 +413,9 @@ hipError_t launch_mreduce_act8(const float *P, const Act8 &q, const int *map, in
 int mreduce_act8_splits(int64_t M, int64_t C, int r, int E = 1);
 // U = dY B (bf16, and in float32) and dB = s dY^T T (bf16 [N][r]) in one pass over dY [M][N] (thin.hip), where
 // thin_takes: up to kThinMaxRank, with 1 GiB of partials of dB at most (they are r / 128 of dY's bytes; those
-// of launch_mreduce do not grow with M). N % 8 == 0, N <= 2^22: 256 rows are addressed with 31 bits. Grouped (gr: 256-row blocks of the experts, counted times `per`): B [E][N][r] and dB are the
-// experts', the grid is bounded by M and E. part: u_floats + b_floats of thin_plan.
+// of launch_mreduce do not grow with M). N % 8 == 0, N <= 2^22: 256 rows are addressed with 31 bits. Grouped (gr: 256-row
+// blocks of the experts, counted times `per`): B [E][N][r] and dB are the experts', the grid is bounded by M and E.
+// part: u_floats + b_floats of thin_plan.
 constexpr int kThinMaxRank = 64, kThinRows = 256;
 inline int64_t thin_blocks(int64_t M, int E) {
   const int64_t blocks = (M + (kThinRows - 1) * (int64_t)E) / kThinRows;

@@ -236,30 +236,12 @@ __global__ __launch_bounds__(256) void rowproj16_kernel(const uint16_t *__restri
   }
 }
 
-// wide (NULL: none): the sum before its rounding.
 __global__ void rowproj_reduce_kernel(const float *__restrict__ part, int64_t n, int splits,
                                       uint16_t *__restrict__ out, float *__restrict__ wide) {
-  for (int64_t i = blockIdx.x * (int64_t)blockDim.x + threadIdx.x; i < n;
-       i += (int64_t)gridDim.x * blockDim.x) {
-    // sequential sum over the splits (fixed order) of the split-major partials, its loads issued
-    // eight at a time
-    const float *pi = part + i;
-    float a = 0.f;
-    int s = 0;
-    for (; s + 8 <= splits; s += 8) {
-      float v[8];
-#pragma unroll
-      for (int j = 0; j < 8; ++j) v[j] = pi[(int64_t)(s + j) * n];
-#pragma unroll
-      for (int j = 0; j < 8; ++j) a += v[j];
-    }
-    for (; s < splits; ++s) a += pi[(int64_t)s * n];
-    out[i] = (uint16_t)(pack_bf16x2(a, 0.f) & 0xFFFFu);
-    if (wide) wide[i] = a;
-  }
+  split_sum_each(part, n, splits, out, wide, blockIdx.x, gridDim.x);
 }
 
-hipError_t launch_rowproj_reduce(const float *part, int64_t n, int splits, uint16_t *out, float *wide, hipStream_t st) {
+static hipError_t launch_rowproj_reduce(const float *part, int64_t n, int splits, uint16_t *out, float *wide, hipStream_t st) {
   int64_t blocks = (n + 255) / 256;
   if (blocks > 4096) blocks = 4096;
   rowproj_reduce_kernel<<<dim3((unsigned)blocks), dim3(256), 0, st>>>(part, n, splits, out, wide);
@@ -563,7 +545,8 @@ __global__ __launch_bounds__(256) void mreduce_final_kernel(const float *__restr
 __global__ __launch_bounds__(1024) void mreduce_final_t_kernel(const float *__restrict__ part, int64_t C, int r,
                                                                int splits, float s, uint16_t *__restrict__ out) {
   const int64_t n = (int64_t)r * C;
-  split_sum_t(part + (int64_t)blockIdx.y * splits * n, C, r, splits, s, out + (int64_t)blockIdx.y * n);
+  split_sum_t(part + (int64_t)blockIdx.y * splits * n, C, r, splits, s, out + (int64_t)blockIdx.y * n,
+              (int64_t)blockIdx.x * 64);
 }
 
 // Splits of the M-reduction over C / 128 column tiles. One layer: as many as let ONE round of

@@ -1,4 +1,4 @@
-// Sums of float32 partials in a fixed order, shared by the M-reductions (lora.hip, thin.hip).
+// Sums of float32 partials in a fixed order (lora.hip, thin.hip).
 #pragma once
 
 #include "common.h"
@@ -20,13 +20,35 @@ __device__ __forceinline__ f32x4 split_sum4(const float *p, int64_t n, int split
   return a;
 }
 
-// out[c][j] (bf16, contiguous) = s * the sum of `splits` partials [r][C] at part, for the 64 columns of block blockIdx.x
+// out[i] (bf16) and wide[i] (float32; NULL: none) = the sum of `splits` partials [n] at part, sequential, its loads issued
+// eight at a time; workgroup `block` of `blocks`.
+__device__ __forceinline__ void split_sum_each(const float *__restrict__ part, int64_t n, int splits,
+                                               uint16_t *__restrict__ out, float *__restrict__ wide, int64_t block,
+                                               int64_t blocks) {
+  for (int64_t i = block * blockDim.x + threadIdx.x; i < n; i += blocks * blockDim.x) {
+    const float *pi = part + i;
+    float a = 0.f;
+    int s = 0;
+    for (; s + 8 <= splits; s += 8) {
+      float v[8];
+#pragma unroll
+      for (int j = 0; j < 8; ++j) v[j] = pi[(int64_t)(s + j) * n];
+#pragma unroll
+      for (int j = 0; j < 8; ++j) a += v[j];
+    }
+    for (; s < splits; ++s) a += pi[(int64_t)s * n];
+    out[i] = (uint16_t)(pack_bf16x2(a, 0.f) & 0xFFFFu);
+    if (wide) wide[i] = a;
+  }
+}
+
+// out[c][j] (bf16, contiguous) = s * the sum of `splits` partials [r][C] at part, for the 64 columns from c0 on
 // and all r <= 128 ranks, through LDS: the outputs of 64 columns are contiguous (written one by one at a stride of
 // r they took 9.1 us at r 64, C 11008, now 4.8). C % 8 == 0; split_sum_t_threads(r) threads, 16 for each rank up to 1024.
 __device__ __forceinline__ void split_sum_t(const float *__restrict__ part, int64_t C, int r, int splits, float s,
-                                            uint16_t *__restrict__ out) {
+                                            uint16_t *__restrict__ out, int64_t c0) {
   __shared__ uint16_t tile[64 * 129];       // [column][rank], rows of an odd length: columns in different banks
-  const int64_t c0 = (int64_t)blockIdx.x * 64, n = (int64_t)r * C;
+  const int64_t n = (int64_t)r * C;
   const int c = (threadIdx.x & 15) * 4, cols = C - c0 < 64 ? (int)(C - c0) : 64, row = r | 1;
   const float *p = part + c0 + c;
   for (int j = threadIdx.x >> 4; j < r; j += blockDim.x >> 4) {

@@ -6,7 +6,7 @@
 // two reads of it. Here a workgroup takes 256 rows and a range of columns, in steps of 128 columns that are staged in
 // LDS once and multiplied twice: rows by B (U's sums over the range stay in registers until its end), and columns by T
 // (dB's sums over the 256 rows, written after each step). Sums over ranges and over row blocks are added in a
-// fixed order by further launches. T, a step of dY and of B are 125 KB of LDS at rank 64; at 128 they are more than
+// fixed order by one further launch. T, a step of dY and of B are 125 KB of LDS at rank 64; at 128 they are more than
 // there is, and the partials of dB, written and read, twice dY's bytes: above 64 the two launches stay.
 //
 // Bound by memory: a step's 64 KB are requested two steps ahead, 128 KB in flight on every CU. All of the adapters'
@@ -212,15 +212,23 @@ __global__ __launch_bounds__(kT) void thin_kernel(const uint16_t *__restrict__ d
       }
 }
 
-// dB of expert blockIdx.y from its row blocks (all of them without groups).
-__global__ __launch_bounds__(1024) void thin_final_kernel(const float *__restrict__ part, int64_t N, int r, int blocks,
-                                                          int per, float s, uint16_t *__restrict__ out, GroupArgs gr) {
+// The sums of the partials, one launch for both: workgroups below cb * E take 64 of the cb * 64 columns of an expert's dB
+// (E = 1 without groups) from its row blocks, the others U.
+__global__ __launch_bounds__(1024) void thin_final_kernel(ThinArgs a, const float *__restrict__ part_b, int blocks,
+                                                          int splits, int cb, GroupArgs gr) {
+  const int E = gr.E ? gr.E : 1;
+  if ((int)blockIdx.x >= cb * E) {
+    split_sum_each(a.part, a.M * a.r, splits, a.U, a.Uw, (int)blockIdx.x - cb * E, (int)gridDim.x - cb * E);
+    return;
+  }
+  const int e = (int)blockIdx.x / cb;
   int first = 0, count = blocks;
   if (gr.E) {
-    first = grp_tile_off(gr, blockIdx.y) / per;
-    count = grp_tile_off(gr, blockIdx.y + 1) / per - first;
+    first = grp_tile_off(gr, e) / a.per;
+    count = grp_tile_off(gr, e + 1) / a.per - first;
   }
-  split_sum_t(part + (int64_t)first * r * N, N, r, count, s, out + (int64_t)blockIdx.y * r * N);
+  split_sum_t(part_b + (int64_t)first * a.r * a.N, a.N, a.r, count, a.s, a.dB + (int64_t)e * a.r * a.N,
+              (int64_t)((int)blockIdx.x % cb) * 64);
 }
 
 template <int TJ, bool kVec>
@@ -266,13 +274,12 @@ hipError_t launch_thin_bwd(const ThinArgs &a, const GroupArgs *gr, hipStream_t s
     if (a.r & 7) launch_thin_as<4, false>(a, p, part_b, gr, st);
     else launch_thin_as<4, true>(a, p, part_b, gr, st);
   }
-  hipError_t e = hipGetLastError();
+  const hipError_t e = hipGetLastError();
   if (e != hipSuccess) return e;
-  e = launch_rowproj_reduce(a.part, a.M * a.r, p.splits, a.U, a.Uw, st);
-  if (e != hipSuccess) return e;
-  const dim3 grid((unsigned)((a.N + 63) / 64), (unsigned)(gr ? gr->E : 1));
-  thin_final_kernel<<<grid, dim3(split_sum_t_threads(a.r)), 0, st>>>(part_b, a.N, a.r, (int)p.blocks, gr ? a.per : 1, a.s,
-                                                                     a.dB, gr ? *gr : GroupArgs{});
+  const int threads = split_sum_t_threads(a.r);
+  const int64_t cb = (a.N + 63) / 64, ub = (a.M * a.r + threads - 1) / threads;
+  thin_final_kernel<<<dim3((unsigned)(cb * (gr ? gr->E : 1) + (ub < 1024 ? ub : 1024))), dim3(threads), 0, st>>>(
+      a, part_b, (int)p.blocks, p.splits, (int)cb, gr ? *gr : GroupArgs{});
   return hipGetLastError();
 }
 
