@@ -217,7 +217,7 @@ BwdWs bwd_ws(int64_t m, int64_t n, int64_t k, int32_t r, bool act8 = false) {
     w.t = align256((size_t)m * r * 4);
     w.splits_a = nf4q::mreduce_act8_splits(m, k, r);
     if (nf4q::thin_takes(m, n, r)) {
-      const nf4q::ThinPlan t = nf4q::thin_plan(m, n, r, 1);
+      const nf4q::ThinPlan t = nf4q::thin_plan(m, n, r);
       p = std::max(p, (t.u_floats + t.b_floats) * 4);
     } else {
       w.bt = align256((size_t)r * n * 2);
@@ -366,7 +366,7 @@ MoeWs moe_ws_layout(int64_t mtotal, int32_t E, int64_t n, int64_t k, int32_t r, 
     const MoePlan pl = moe_plan(mtotal, E, n, k, r);
     w.u = align256((size_t)mtotal * r * 2);
     if (act8 && nf4q::thin_takes(mtotal, n, r, E)) {
-      const nf4q::ThinPlan tp = nf4q::thin_plan(mtotal, n, r, E);
+      const nf4q::ThinPlan tp = nf4q::thin_plan(mtotal, n, r, true, E);
       p = std::max(p, (tp.u_floats + tp.b_floats) * 4);
     } else {
       w.bt = align256((size_t)r * E * n * 2);

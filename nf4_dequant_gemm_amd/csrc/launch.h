@@ -426,10 +426,10 @@ inline bool thin_takes(int64_t M, int64_t N, int r, int E = 1) {
 }
 struct ThinPlan {
   int64_t blocks, lsplit;
-  int splits;
+  int splits, halves;
   size_t u_floats, b_floats;
 };
-ThinPlan thin_plan(int64_t M, int64_t N, int r, int E);
+ThinPlan thin_plan(int64_t M, int64_t N, int r, bool grouped = false, int E = 1);
 struct ThinArgs {
   const uint16_t *dy, *B, *T;
   int64_t M, N;

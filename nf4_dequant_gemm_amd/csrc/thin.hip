@@ -3,21 +3,23 @@
 //   U = dY B  [M][r]     and     dB = s dY^T T  [N][r],   r <= 64
 //
 // for the layers that keep X in 8 bits. Each reads all of dY and little else, so the two launches of lora.hip cost
-// two reads of it. Here a workgroup takes 256 rows and a range of columns, in steps of 128 columns that are staged in
+// two reads of it. Here a workgroup takes 256 or 512 rows and a range of columns, in steps of 128 columns that are staged in
 // LDS once and multiplied twice: rows by B (U's sums over the range stay in registers until its end), and columns by T
-// (dB's sums over the 256 rows, written after each step). Sums over ranges and over row blocks are added in a
+// (dB's sums over the rows, written after each step). Sums over ranges and over row blocks are added in a
 // fixed order by one further launch. T, a step of dY and of B are 125 KB of LDS at rank 64; at 128 they are more than
 // there is, and the partials of dB, written and read, twice dY's bytes: above 64 the two launches stay.
 //
 // Bound by memory: a step's 64 KB are requested two steps ahead, 128 KB in flight on every CU. All of the adapters'
-// gradients, k 512, against the two launches: 8192 x 14336 at rank 64 163 us (180), 48 155 (171), 40 148 (168);
-// 16384 x 14336 at 64 255 (290); 4096 x 11008 at 64 86 (98), at 8 63 (78); 64 x 4096 at 16 21 (27). This kernel alone
-// takes 105 us for 16384 x 11008 of 8 experts at rank 16 (3.4 TB/s; 116 with ranges of columns sized for the fullest
-// rounds alone), and 67 for 8192 x 11008 at rank 64 with half as many bytes of partials (4.0 TB/s). Two workgroups a
-// CU with T in registers at rank 16 took 100, steps in another order for each row block 98 there and 71 for 67 here.
+// gradients, k 512, against the two launches (us): 8192 x 14336 at rank 64 151 (180), at 33 149 (315); 16384 x 14336 at 64
+// 223 (290); 4096 x 11008 at 64 80 (98); 64 x 4096 at 16 19 (27). This kernel alone takes 104 us for 16384 x 11008 of 8
+// experts at rank 16 (3.5 TB/s; 116 with ranges of columns sized for the fullest rounds alone) and 57 for 8192 x 11008 at
+// rank 64 (4.5 TB/s with its partials; 67 with blocks of 256 rows). Two workgroups a CU with T in registers took 100 for
+// 104, steps in another order for each row block 98 there and 71 for 67.
 #include "common.h"
 #include "launch.h"
 #include "sums.h"
+
+#include <type_traits>
 
 namespace nf4q {
 namespace {
@@ -47,7 +49,10 @@ __device__ __forceinline__ bf16x8 columns(const uint16_t *tile, int stride, int 
 
 // kVec: r is a multiple of 8. kGrp: rows grouped by expert; B is the expert's, and row blocks are counted through
 // gr.tile_off, which holds them times `per`.
-template <int TJ, bool kVec, bool kGrp>
+// kHalves: blocks of 256 rows that a workgroup takes one after the other at every step, whose sums of dB are one
+// partial (2 without groups only: a group's blocks are numbered through all groups, and with every second workgroup idle 16384 x
+// 11008 of 8 experts took 14 us more).
+template <int TJ, bool kVec, bool kGrp, int kHalves>
 __global__ __launch_bounds__(kT) void thin_kernel(const uint16_t *__restrict__ dy, const uint16_t *__restrict__ B,
                                                   const uint16_t *__restrict__ T, int64_t M, int64_t N, int r,
                                                   int64_t lsplit, int per, float *__restrict__ part_u,
@@ -55,11 +60,11 @@ __global__ __launch_bounds__(kT) void thin_kernel(const uint16_t *__restrict__ d
   constexpr int PROW = TJ * 16 + 8;             // row stride of T and B in bf16
   constexpr int CH = 2 * TJ;                    // 16-byte chunks of such a row
   __shared__ __align__(16) uint16_t sY[kRB * kYRow];
-  __shared__ __align__(16) uint16_t sT[kRB * PROW];
+  __shared__ __align__(16) uint16_t sT[kHalves * kRB * PROW];
   __shared__ __align__(16) uint16_t sB[kCB * PROW];
   const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
   const int64_t blk = blockIdx.x;
-  int64_t mbase = blk * kRB, mhi = M;
+  int64_t mbase = blk * kHalves * kRB, mhi = M;
   if (kGrp) {
     const int local = (int)blk * per;
     if (local >= grp_tile_off(gr, gr.E)) return;      // a grid sized by an upper bound
@@ -68,7 +73,11 @@ __global__ __launch_bounds__(kT) void thin_kernel(const uint16_t *__restrict__ d
     mhi = grp_m_off(gr, e + 1);
     B += e * N * r;
   }
-  const int64_t rows = mhi - mbase < kRB ? mhi - mbase : kRB;
+  // the rows of a half
+  auto rows = [&](int half) {
+    const int64_t left = mhi - mbase - half * kRB;
+    return left < 0 ? 0 : left < kRB ? left : kRB;
+  };
   const int split = blockIdx.y;
   const int64_t lb = split * lsplit, le = lb + lsplit < N ? lb + lsplit : N;
 
@@ -112,31 +121,32 @@ __global__ __launch_bounds__(kT) void thin_kernel(const uint16_t *__restrict__ d
   };
   // Requests a step, without a branch (a skipped request would make the waits for the step before wait for this
   // one's too): rows and columns outside read as zeros.
-  auto load = [&](int64_t l0, Stage &st) {
+  auto load = [&](auto half, int64_t l0, Stage &st) {
     const bool any = l0 < le;
-    const __amdgpu_buffer_rsrc_t ry = make_rsrc(dy + mbase * N + l0, any ? (rows * N - l0) * 2 : 0);
+    const __amdgpu_buffer_rsrc_t ry =
+        make_rsrc(dy + (mbase + half * kRB) * N + l0, any && rows(half) ? (rows(half) * N - l0) * 2 : 0);
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
       const int row = (tid + kT * i) >> 4, c = (tid & 15) * 8;
       st.y[i] = load16(ry, l0 + c < le ? (uint32_t)((row * N + c) * 2) : kNowhere);
     }
-    get(make_rsrc(B + l0 * r, any ? (le - l0) * r * 2 : 0), 0, st.b);
+    if (half == 0) get(make_rsrc(B + l0 * r, any ? (le - l0) * r * 2 : 0), 0, st.b);
   };
-  auto store = [&](const Stage &st) {
+  auto store = [&](auto half, const Stage &st) {
 #pragma unroll
     for (int i = 0; i < 8; ++i)
       *reinterpret_cast<u32x4 *>(&sY[((tid + kT * i) >> 4) * kYRow + (tid & 15) * 8]) = st.y[i];
-    put(sB, st.b);
+    if (half == 0) put(sB, st.b);
   };
 
   const int g16 = lane >> 4, l16 = lane & 15;
   const __amdgpu_buffer_rsrc_t rb = make_rsrc(part_b + blk * r * N, (int64_t)r * N * 4);
-  f32x4 u[2][TJ];
+  f32x4 u[kHalves * 2][TJ], d[TJ];
 #pragma unroll
-  for (int q = 0; q < 2; ++q)
+  for (int q = 0; q < kHalves * 2; ++q)
 #pragma unroll
     for (int t = 0; t < TJ; ++t) u[q][t] = f32x4{0.f, 0.f, 0.f, 0.f};
-  auto step = [&](int64_t l0) {
+  auto step = [&](auto half, int64_t l0) {
     // U: this wave's 32 rows by the step's 128 columns
 #pragma unroll
     for (int k = 0; k < 4; ++k) {
@@ -148,19 +158,21 @@ __global__ __launch_bounds__(kT) void thin_kernel(const uint16_t *__restrict__ d
         const bf16x8 y = __builtin_bit_cast(
             bf16x8, *reinterpret_cast<const u32x4 *>(&sY[(wave * 32 + q * 16 + l16) * kYRow + k * 32 + g16 * 8]));
 #pragma unroll
-        for (int t = 0; t < TJ; ++t) u[q][t] = mfma16x16x32(y, b[t], u[q][t]);
+        for (int t = 0; t < TJ; ++t) u[half * 2 + q][t] = mfma16x16x32(y, b[t], u[half * 2 + q][t]);
       }
     }
     // dB: this wave's 16 columns by the 256 rows
-    f32x4 d[TJ];
+    if (half == 0) {
 #pragma unroll
-    for (int t = 0; t < TJ; ++t) d[t] = f32x4{0.f, 0.f, 0.f, 0.f};
+      for (int t = 0; t < TJ; ++t) d[t] = f32x4{0.f, 0.f, 0.f, 0.f};
+    }
 #pragma unroll
     for (int k = 0; k < kRB / 32; ++k) {
       const bf16x8 y = columns(sY, kYRow, wave * 16, k, lane);
 #pragma unroll
-      for (int t = 0; t < TJ; ++t) d[t] = mfma16x16x32(columns(sT, PROW, t * 16, k, lane), y, d[t]);
+      for (int t = 0; t < TJ; ++t) d[t] = mfma16x16x32(columns(sT + half * kRB * PROW, PROW, t * 16, k, lane), y, d[t]);
     }
+    if (half != kHalves - 1) return;
     const int64_t c = l0 + wave * 16 + l16;
 #pragma unroll
     for (int t = 0; t < TJ; ++t)
@@ -175,38 +187,44 @@ __global__ __launch_bounds__(kT) void thin_kernel(const uint16_t *__restrict__ d
 
   const int64_t nst = le > lb ? (le - lb + kCB - 1) / kCB : 0;
   if (nst == 0) return;       // the whole workgroup
+  constexpr std::integral_constant<int, 0> h0{};
+  constexpr std::integral_constant<int, kHalves - 1> h1{};
+  auto at = [&](int64_t i) { return lb + i / kHalves * kCB; };      // the columns of an item: a step, or half of one
   Stage s0, s1;
   {
-    Narrow t0, t1;
-    const __amdgpu_buffer_rsrc_t rt = make_rsrc(T + mbase * r, rows * r * 2);
-    get(rt, 0, t0);
-    get(rt, 128, t1);
-    load(lb, s0);
-    load(lb + kCB, s1);
-    put(sT, t0);
-    put(sT + 128 * PROW, t1);
+    Narrow t[2 * kHalves];
+#pragma unroll
+    for (int h = 0; h < kHalves; ++h) {
+      const __amdgpu_buffer_rsrc_t rt = make_rsrc(T + (mbase + h * kRB) * r, rows(h) * r * 2);
+      get(rt, 0, t[2 * h]);
+      get(rt, 128, t[2 * h + 1]);
+    }
+    load(h0, at(0), s0);
+    load(h1, at(1), s1);
+#pragma unroll
+    for (int h = 0; h < 2 * kHalves; ++h) put(sT + h * 128 * PROW, t[h]);
   }
-  // steps in pairs; one past the last is zeros and writes nothing
+  // items in pairs; one past the last is zeros and writes nothing
 #pragma unroll 1
-  for (int64_t i = 0; i < nst; i += 2) {
-    store(s0);
+  for (int64_t i = 0; i < nst * kHalves; i += 2) {
+    store(h0, s0);
     __syncthreads();
-    load(lb + (i + 2) * kCB, s0);
-    step(lb + i * kCB);
+    load(h0, at(i + 2), s0);
+    step(h0, at(i));
     __syncthreads();
-    store(s1);
+    store(h1, s1);
     __syncthreads();
-    load(lb + (i + 3) * kCB, s1);
-    step(lb + (i + 1) * kCB);
+    load(h1, at(i + 3), s1);
+    step(h1, at(i + 1));
     __syncthreads();
   }
 #pragma unroll
-  for (int q = 0; q < 2; ++q)
+  for (int q = 0; q < kHalves * 2; ++q)
 #pragma unroll
     for (int t = 0; t < TJ; ++t)
 #pragma unroll
       for (int v = 0; v < 4; ++v) {
-        const int64_t row = mbase + wave * 32 + q * 16 + 4 * g16 + v;
+        const int64_t row = mbase + q / 2 * kRB + wave * 32 + q % 2 * 16 + 4 * g16 + v;
         const int j = t * 16 + l16;
         if (row < mhi && j < r) part_u[((int64_t)split * M + row) * r + j] = u[q][t][v];
       }
@@ -231,20 +249,29 @@ __global__ __launch_bounds__(1024) void thin_final_kernel(ThinArgs a, const floa
               (int64_t)((int)blockIdx.x % cb) * 64);
 }
 
-template <int TJ, bool kVec>
-void launch_thin_as(const ThinArgs &a, const ThinPlan &p, float *part_b, const GroupArgs *gr, hipStream_t st) {
-  const dim3 grid((unsigned)p.blocks, (unsigned)p.splits);
-  if (gr) thin_kernel<TJ, kVec, true><<<grid, dim3(kT), 0, st>>>(a.dy, a.B, a.T, a.M, a.N, a.r, p.lsplit, a.per, a.part,
-                                                                 part_b, *gr);
-  else thin_kernel<TJ, kVec, false><<<grid, dim3(kT), 0, st>>>(a.dy, a.B, a.T, a.M, a.N, a.r, p.lsplit, 1, a.part, part_b,
-                                                               GroupArgs{});
+template <int TJ, bool kVec, bool kGrp, int kHalves>
+void launch_thin_as(const ThinArgs &a, const ThinPlan &p, float *part_b, const GroupArgs &gr, hipStream_t st) {
+  thin_kernel<TJ, kVec, kGrp, kHalves><<<dim3((unsigned)p.blocks, (unsigned)p.splits), dim3(kT), 0, st>>>(
+      a.dy, a.B, a.T, a.M, a.N, a.r, p.lsplit, a.per, a.part, part_b, gr);
+}
+template <int TJ>
+void launch_thin(const ThinArgs &a, const ThinPlan &p, float *part_b, const GroupArgs &gr, hipStream_t st) {
+  const bool vec = a.r % 8 == 0;
+  if (gr.E) vec ? launch_thin_as<TJ, true, true, 1>(a, p, part_b, gr, st) : launch_thin_as<TJ, false, true, 1>(a, p, part_b, gr, st);
+  else if (p.halves == 2) launch_thin_as<TJ, true, false, 2>(a, p, part_b, gr, st);
+  else vec ? launch_thin_as<TJ, true, false, 1>(a, p, part_b, gr, st) : launch_thin_as<TJ, false, false, 1>(a, p, part_b, gr, st);
 }
 
 }  // namespace
 
-ThinPlan thin_plan(int64_t M, int64_t N, int r, int E) {
+ThinPlan thin_plan(int64_t M, int64_t N, int r, bool grouped, int E) {
   ThinPlan p;
-  p.blocks = thin_blocks(M, E);
+  // Two blocks a workgroup halve the partials of dB where there are workgroups enough all the same (M N from 2^24 on),
+  // the adapters' gradients with k 512 in us: 8192 x 14336 at rank 64 150 for 159, 16384 x 14336 222 for 250, 2048 x 11008 at 32
+  // 42.7 for 46.4, 4096 x 11008 at 16 60.4 for 62.6; below, 1024 x 11008 at 32 would take 35.0 for 33.5, 2048 x 4096 at 64 42.8
+  // for 37.9. Ranks that are not a multiple of 8 have no registers for it.
+  p.halves = !grouped && r % 8 == 0 && M >= 4 * kRB && M * N >= (int64_t(1) << 24) ? 2 : 1;
+  p.blocks = p.halves == 2 ? (M + 2 * kRB - 1) / (2 * kRB) : thin_blocks(M, E);
   // ranges of columns of equally many steps (the last one fewer), at least two as the loop takes pairs: the rounds of
   // 256 workgroups times the steps of one, and one more for its first requests, least
   const int64_t steps = (N + kCB - 1) / kCB;
@@ -261,25 +288,19 @@ ThinPlan thin_plan(int64_t M, int64_t N, int r, int E) {
 }
 
 hipError_t launch_thin_bwd(const ThinArgs &a, const GroupArgs *gr, hipStream_t st) {
-  const ThinPlan p = thin_plan(a.M, a.N, a.r, gr ? gr->E : 1);
+  const ThinPlan p = thin_plan(a.M, a.N, a.r, gr != nullptr, gr ? gr->E : 1);
   if (!thin_takes(a.M, a.N, a.r, gr ? gr->E : 1) || a.N % 8 || a.N > (int64_t(1) << 22) || p.blocks < 1 || p.splits > 65535) return hipErrorInvalidValue;
   float *part_b = a.part + p.u_floats;
-  if (a.r <= 16) {
-    if (a.r & 7) launch_thin_as<1, false>(a, p, part_b, gr, st);
-    else launch_thin_as<1, true>(a, p, part_b, gr, st);
-  } else if (a.r <= 32) {
-    if (a.r & 7) launch_thin_as<2, false>(a, p, part_b, gr, st);
-    else launch_thin_as<2, true>(a, p, part_b, gr, st);
-  } else {
-    if (a.r & 7) launch_thin_as<4, false>(a, p, part_b, gr, st);
-    else launch_thin_as<4, true>(a, p, part_b, gr, st);
-  }
+  const GroupArgs groups = gr ? *gr : GroupArgs{};
+  if (a.r <= 16) launch_thin<1>(a, p, part_b, groups, st);
+  else if (a.r <= 32) launch_thin<2>(a, p, part_b, groups, st);
+  else launch_thin<4>(a, p, part_b, groups, st);
   const hipError_t e = hipGetLastError();
   if (e != hipSuccess) return e;
   const int threads = split_sum_t_threads(a.r);
   const int64_t cb = (a.N + 63) / 64, ub = (a.M * a.r + threads - 1) / threads;
   thin_final_kernel<<<dim3((unsigned)(cb * (gr ? gr->E : 1) + (ub < 1024 ? ub : 1024))), dim3(threads), 0, st>>>(
-      a, part_b, (int)p.blocks, p.splits, (int)cb, gr ? *gr : GroupArgs{});
+      a, part_b, (int)p.blocks, p.splits, (int)cb, groups);
   return hipGetLastError();
 }
 
