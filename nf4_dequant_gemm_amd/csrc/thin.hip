@@ -11,10 +11,9 @@
 //
 // Bound by memory: a step's 64 KB are requested two steps ahead, 128 KB in flight on every CU. All of the adapters'
 // gradients, k 512, against the two launches (us): 8192 x 14336 at rank 64 151 (180), at 33 149 (315); 16384 x 14336 at 64
-// 223 (290); 4096 x 11008 at 64 80 (98); 64 x 4096 at 16 19 (27). This kernel alone takes 104 us for 16384 x 11008 of 8
-// experts at rank 16 (3.5 TB/s; 116 with ranges of columns sized for the fullest rounds alone) and 57 for 8192 x 11008 at
-// rank 64 (4.5 TB/s with its partials; 67 with blocks of 256 rows). Two workgroups a CU with T in registers took 100 for
-// 104, steps in another order for each row block 98 there and 71 for 67.
+// 223 (290); 4096 x 11008 at 64 80 (98); 64 x 4096 at 16 19 (27). This kernel alone takes 97 us for 16384 x 11008 of 8
+// experts at rank 16 (3.7 TB/s) and 57 for 8192 x 11008 at rank 64 (4.5 TB/s with its partials; 67 with blocks of 256
+// rows). Two workgroups a CU with T in registers gained 5% at rank 16 where the order of steps gains 7.
 #include "common.h"
 #include "launch.h"
 #include "sums.h"
@@ -189,7 +188,14 @@ __global__ __launch_bounds__(kT) void thin_kernel(const uint16_t *__restrict__ d
   if (nst == 0) return;       // the whole workgroup
   constexpr std::integral_constant<int, 0> h0{};
   constexpr std::integral_constant<int, kHalves - 1> h1{};
-  auto at = [&](int64_t i) { return lb + i / kHalves * kCB; };      // the columns of an item: a step, or half of one
+  // The columns of an item: a step, or half of one. Row blocks begin at different steps, so that not all read the same
+  // columns at a time: 16384 x 11008 at rank 16 166 us for 177, of 8 experts 97 for 104 (this kernel); blocks of 256 rows above
+  // rank 32 lose by it (8192 x 11008 71 for 67).
+  const int steps = (int)nst, turn = TJ == 4 && kHalves == 1 ? 0 : (int)blk % steps;
+  auto at = [&](int i) {
+    const int q = i / kHalves, c = q + turn;
+    return q < steps ? lb + (int64_t)(c < steps ? c : c - steps) * kCB : le;
+  };
   Stage s0, s1;
   {
     Narrow t[2 * kHalves];
@@ -206,7 +212,7 @@ __global__ __launch_bounds__(kT) void thin_kernel(const uint16_t *__restrict__ d
   }
   // items in pairs; one past the last is zeros and writes nothing
 #pragma unroll 1
-  for (int64_t i = 0; i < nst * kHalves; i += 2) {
+  for (int i = 0; i < steps * kHalves; i += 2) {
     store(h0, s0);
     __syncthreads();
     load(h0, at(i + 2), s0);
