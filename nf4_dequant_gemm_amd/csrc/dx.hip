@@ -164,10 +164,12 @@ __device__ __forceinline__ void dx_origin(int64_t m_lo, int64_t m_hi, int tiles_
 // the low-rank term of its block from the transposed adapters, straight from registers (multi_term,
 // multi.h). kSplit: a workgroup runs one of mu.pieces parts of the reduction and leaves its float32 sums
 // in mu.part (a kernel of its own: both endings in one spilled 120 registers and cost 100 us of 670).
+// kFew: grouped, as gr.few says (pieces of rows that are there only); a kernel of its own, too, so that the grouped one stays
+// as it is.
 // kMT: row tiles of 16 that a wave multiplies, fewer than 8 where the launch has at most 32 kMT rows.
 // Medians of 40 launches: 8192 x 11008 x 4096, 4 adapters of rank 64: 626 us (719 on another card); split,
 // 64 x 11008 x 4096: 23 us (29 us with 8 row tiles, 380 us unsplit).
-template <int kFmt, bool kGrp, bool kMulti = false, bool kSplit = false, int kMT = 8>
+template <int kFmt, bool kGrp, bool kMulti = false, bool kSplit = false, int kMT = 8, bool kFew = false>
 __device__ __forceinline__ void dx_body(const GemmArgs &g, const GroupArgs &gr, const MultiArgs &mu) {
   constexpr bool kDQ = kFmt == 1, kFP4 = kFmt == 2;
   // separate LDS arrays per buffer: the compiler then knows that accesses to one do not alias
@@ -199,7 +201,7 @@ __device__ __forceinline__ void dx_body(const GemmArgs &g, const GroupArgs &gr, 
   if (kGrp) {
     // a grid sized by an upper bound (routing on the device) has workgroups past the last tile
     const int total = grp_tile_off(gr, gr.E);
-    sp = dx_split(gr.width, gr.smax, gr.part != nullptr, total, nsteps, gr.few);
+    sp = dx_split(gr.width, gr.smax, gr.part != nullptr, total, nsteps, kFew);
     const int b = (int)blockIdx.x;
     if (b >= sp.full + sp.tail * sp.S) return;
     if (b < sp.full) {
@@ -504,11 +506,10 @@ __device__ __forceinline__ void dx_body(const GemmArgs &g, const GroupArgs &gr, 
     f32x4 *pp = reinterpret_cast<f32x4 *>(gr.part + ((int64_t)tail_i * sp.S + piece) * kDxPieceFloats) +
                 wave * 32 * 64 + lane;
 #pragma unroll
-    for (int mt = 0; mt < kMT; ++mt)
-      if (m0 + wm * 128 + mt * 16 < m_hi) {
+    for (int kt = 0; kt < 4; ++kt)
 #pragma unroll
-        for (int kt = 0; kt < 4; ++kt) pp[(kt * 8 + mt) * 64] = acc[kt][mt];
-      }
+      for (int mt = 0; mt < kMT; ++mt)
+        if (!kFew || m0 + wm * 128 + mt * 16 < m_hi) pp[(kt * 8 + mt) * 64] = acc[kt][mt];
     return;
   }
 
@@ -582,6 +583,17 @@ __global__ __launch_bounds__(kThreads) void dx_fused_kernel(GemmArgs g) {
 template <int kFmt>
 __global__ __launch_bounds__(kThreads) void dx_grouped_kernel(GemmArgs g, GroupArgs gr) {
   dx_body<kFmt, true>(g, gr, MultiArgs{});
+}
+template <int kFmt>
+__global__ __launch_bounds__(kThreads) void dx_few_kernel(GemmArgs g, GroupArgs gr) {
+  dx_body<kFmt, true, false, false, 8, true>(g, gr, MultiArgs{});
+}
+template <int kFmt>
+void launch_grouped(const GemmArgs &g, const GroupArgs &gr, unsigned grid, hipStream_t st) {
+  if (gr.few)
+    dx_few_kernel<kFmt><<<dim3(grid), dim3(kThreads), 0, st>>>(g, gr);
+  else
+    dx_grouped_kernel<kFmt><<<dim3(grid), dim3(kThreads), 0, st>>>(g, gr);
 }
 template <int kFmt>
 __global__ __launch_bounds__(kThreads) void dx_multi_kernel(GemmArgs g, MultiArgs mu) {
@@ -667,11 +679,11 @@ hipError_t launch_gemm_dx_grouped(const GemmArgs &g, const GroupArgs &gr, hipStr
   }
   if (grid < 1) return hipSuccess;
   if (g.w.fp4)
-    dx_grouped_kernel<2><<<dim3((unsigned)grid), dim3(kThreads), 0, st>>>(g, gr);
+    launch_grouped<2>(g, gr, (unsigned)grid, st);
   else if (g.w.dq)
-    dx_grouped_kernel<1><<<dim3((unsigned)grid), dim3(kThreads), 0, st>>>(g, gr);
+    launch_grouped<1>(g, gr, (unsigned)grid, st);
   else
-    dx_grouped_kernel<0><<<dim3((unsigned)grid), dim3(kThreads), 0, st>>>(g, gr);
+    launch_grouped<0>(g, gr, (unsigned)grid, st);
   if (tail_grid > 0) {
     tail_grid *= gr.few ? 32 : 4;   // workgroups per tile
     if (g.w.fp4)

@@ -84,7 +84,7 @@ struct DxSplit {
 __host__ __device__ inline DxSplit dx_split(int width, int smax, bool enabled, int total, int nsteps,
                                                 bool few) {
   DxSplit d{total, 0, 1};
-  if (!enabled || width <= 0 || (total <= width && !few)) return d;
+  if (!enabled || width <= 0 || total <= (few ? 0 : width)) return d;
   const int tail = total % width;
   if (tail == 0) return d;
   int S = width / tail;
