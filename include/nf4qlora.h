@@ -541,9 +541,10 @@ int act8_pack(const void *X, int dtype, int64_t ldx, const nf4_act8 *q, void *st
 int act8_unpack(const nf4_act8 *q, void *X, int dtype, int64_t ldx, void *stream);
 
 /* qlora_bwd with X in 8 bits (m = X->rows): U, dX and dB as there up to the order of their float32 sums (up to
- * rank 64 U and dB come from one pass over dY; the reduction of a dX of few tiles is split over workgroups), and dA = s U^T X from U in
- * float32 and what the codes stand for: U times a block's scale is rounded to bf16, the codes are not
- * rounded. T must be given when r > 0. Errors: as qlora_bwd and act8_pack. */
+ * rank 64 U and dB come from one pass over dY; the reduction of a dX of few tiles is split over workgroups), and
+ * dA = s U^T X from U in float32 and what the codes stand for: U times a block's scale is rounded to bf16, the
+ * codes are not rounded. T must be given when r > 0. ws: at least what the function before it says, as for the
+ * forms below; at most about 1 GiB beside U and B transposed. Errors: as qlora_bwd and act8_pack. */
 size_t qlora_bwd_act8_workspace_bytes(int64_t m, int64_t n, int64_t k, int32_t r);
 int qlora_bwd_act8(const void *dY, const nf4_act8 *X, const nf4_tensor *W, const void *A, const void *B, int32_t r,
                    float s, const void *T, void *dX, void *dA, void *dB, void *ws, size_t ws_bytes, void *stream);
@@ -557,8 +558,7 @@ int qlora_swiglu_bwd_act8(const void *dH, const nf4_act8 *X, const nf4_tensor *W
 
 /* qlora_moe_bwd_dev with X in 8 bits: grouped row i is row source[i] of X (a source outside X's rows: zeros),
  * so that a token's activation is kept once, not once for each of its experts; source NULL: row i, and X
- * has m rows. T must be given when r > 0. Errors: as qlora_moe_bwd_dev
- * and act8_pack. */
+ * has m rows. T must be given when r > 0. Errors: as qlora_moe_bwd_dev and act8_pack. */
 size_t qlora_moe_bwd_act8_workspace_bytes(int64_t m, int32_t E, int64_t n, int64_t k, int32_t r);
 int qlora_moe_bwd_dev_act8(const void *dY, const nf4_act8 *X, const int32_t *source, int64_t m, const int64_t *counts,
                            int32_t E, const nf4_tensor *W, const void *A, const void *B, int32_t r, float s,

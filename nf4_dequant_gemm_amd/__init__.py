@@ -1092,7 +1092,7 @@ def _act8_layer(X: Act8Tensor, q: NF4Tensor, A, B, T, rows: int, experts: int = 
 def qlora_bwd_act8(dY: torch.Tensor, X: Act8Tensor, q: NF4Tensor, A: Optional[torch.Tensor],
                    B: Optional[torch.Tensor], s: float, T: Optional[torch.Tensor], need_dx: bool = True):
     """(dX, dA, dB) of the layer from X in 8 bits (act8_pack) and T from the forward: dA is the sum over what
-    the codes stand for, dX and dB are qlora_bwd's."""
+    the codes stand for, dX and dB are qlora_bwd's up to the order of their float32 sums."""
     m = X.shape[0]
     dev, r = _act8_layer(X, q, A, B, T, m)
     _is(dY, "dY", torch.bfloat16, (m, q.n), dev)
