@@ -266,12 +266,17 @@ __device__ __forceinline__ void mreduce_act8_body(const float *__restrict__ P, c
     f32x4 p[PPT];
     float s[PPT][NB];
   };
-  struct Rows {       // kMap: the rows of q of this thread's codes and chunks of P
+  struct Rows {       // kMap: the rows of q of this thread's codes and chunks of P, -1 past the split's end
     int q[2], p[PPT];
   };
   auto find = [&](int64_t ms, Rows &rw) {
-    const __amdgpu_buffer_rsrc_t rm = make_rsrc(map + ms, (me > ms ? me - ms < kBM ? me - ms : kBM : 0) * 4);
-    auto of = [&](int row) { return (int)__builtin_amdgcn_raw_buffer_load_b32(rm, row * 4, 0, 0); };
+    const int left = me > ms ? me - ms < kBM ? (int)(me - ms) : kBM : 0;
+    const __amdgpu_buffer_rsrc_t rm = make_rsrc(map + ms, left * 4);
+    // past the end the buffer reads as 0, which is a row of q: its scale may be NaN, and P's zeros would not hide it
+    auto of = [&](int row) {
+      const int at = (int)__builtin_amdgcn_raw_buffer_load_b32(rm, row * 4, 0, 0);
+      return row < left ? at : -1;
+    };
     rw.q[0] = of(qr);
     rw.q[1] = of(qr + 32);
 #pragma unroll

@@ -340,3 +340,25 @@ def test_nan_stays_in_its_expert(lib):
     dA, dN = ok[1].view(E, r, k), bad[1].view(E, r, k)
     others = [0, 1, 3]
     assert torch.equal(dA[others], dN[others]) and torch.equal(dA[2, :, :64], dN[2, :, :64]) and dN[2, :, 64:].isnan().all()
+
+
+@pytest.mark.parametrize("t,r,unrouted", [(80, 8, False), (80, 8, True), (400, 7, False), (400, 100, True), (256, 64, True)])
+def test_nan_of_the_first_token_stays_in_its_expert(lib, t, r, unrouted):
+    """A NaN in token 0, the first row that is kept: its expert's dA alone has it, and nobody's where that token is padding.
+    The experts' rows end inside a stage of 64, or their stages are odd in number."""
+    E, k, n = 4, 192, 64
+    x = torch.full((t, E), -5.0, device=DEV)
+    x[torch.arange(t), torch.arange(t) % E] = 5.0
+    keep = torch.arange(t, device=DEV) >= int(unrouted)
+    ro = lib.moe_route(x, 1, keep)
+    q, X, A, B, _ = layer(lib, t, k, n, r, 2, stack=E)
+    dY, T = (torch.randn(t, w, device=DEV).bfloat16() for w in (n, r))
+    ok = lib.qlora_moe_bwd_act8(dY, lib.act8_pack(X), ro.source, ro.counts, q, A, B, 1.0, T)
+    assert all(z[:int(ro.sizes[1])].isfinite().all() for z in ok)
+    X[0, 70] = float("nan")                                  # columns 64 .. 127
+    bad = lib.qlora_moe_bwd_act8(dY, lib.act8_pack(X), ro.source, ro.counts, q, A, B, 1.0, T)
+    N = int(ro.sizes[1])
+    assert torch.equal(ok[0][:N], bad[0][:N]) and torch.equal(ok[2], bad[2])
+    dA, dN = ok[1].view(E, r, k), bad[1].view(E, r, k)
+    assert torch.equal(dA[1:], dN[1:]) and torch.equal(dA[0, :, :64], dN[0, :, :64]) and torch.equal(dA[0, :, 128:], dN[0, :, 128:])
+    assert torch.equal(dA[0], dN[0]) if unrouted else dN[0, :, 64:128].isnan().all()
