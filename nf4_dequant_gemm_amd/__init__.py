@@ -1364,5 +1364,6 @@ class MoECombineFunction(torch.autograd.Function):
     @staticmethod
     def backward(ctx, dY):
         Z, place, source, gate = ctx.saved_tensors
-        dZ, dgate = moe_combine_bwd(dY if dY.stride(1) == 1 else dY.contiguous(), Z, place, source, gate)
+        whole = dY.stride(1) == 1 and dY.stride(0) >= dY.shape[1]       # not so where Y was summed over tokens
+        dZ, dgate = moe_combine_bwd(dY if whole else dY.contiguous(), Z, place, source, gate)
         return dZ, None, None, dgate, dY if ctx.based else None

@@ -204,3 +204,27 @@ def test_example(lib):
     grads = [torch.autograd.grad(model.loss(*data, eight_bits=e)[0], model.leaves()) for e in (True, False)]
     for a, b in zip(*grads):
         assert b.norm() > 0 and (a - b).norm() <= 2.0 ** -5 * b.norm()
+
+
+@pytest.mark.parametrize("reduce", [lambda y: y.sum(0), lambda y: y.mean(0, keepdim=True), lambda y: y.sum(1), lambda y: y.sum()],
+                         ids=["tokens", "mean of tokens", "columns", "both"])
+def test_combine_of_broadcast_gradients(lib, reduce):
+    """The gradient of a sum over tokens, over columns or over both comes as an expanded tensor (a stride of 0)."""
+    t, d, E, top = 30, 72, 5, 2
+    g = torch.Generator(DEV).manual_seed(6)
+    ro = lib.moe_route(torch.randn(t, E, generator=g, device=DEV), top, torch.arange(t, device=DEV) % 7 != 5)
+    Z, base = (torch.randn(n, d, generator=g, device=DEV) for n in (t * top, t))
+
+    def grads(dense):
+        z, b, w = (x.clone().requires_grad_() for x in (Z, base, ro.gate))
+        y = lib.MoECombineFunction.apply(z, ro.place, ro.source, w, b)
+        if dense is None:
+            reduce(y).square().sum().backward()
+        else:
+            y.backward(dense)
+        return y.detach(), z.grad, b.grad, w.grad
+    y, *got = grads(None)
+    x = y.clone().requires_grad_()
+    reduce(x).square().sum().backward()
+    _, *want = grads(x.grad.contiguous())
+    assert all(a.abs().sum() > 0 and torch.equal(a, b) for a, b in zip(got, want))
