@@ -558,7 +558,8 @@ int qlora_swiglu_bwd_act8(const void *dH, const nf4_act8 *X, const nf4_tensor *W
 
 /* qlora_moe_bwd_dev with X in 8 bits: grouped row i is row source[i] of X (a source outside X's rows: zeros),
  * so that a token's activation is kept once, not once for each of its experts; source NULL: row i, and X
- * has m rows. T must be given when r > 0. Errors: as qlora_moe_bwd_dev and act8_pack. */
+ * has m rows. X has a row at least (NF4_EINVAL). T must be given when r > 0. Errors: as qlora_moe_bwd_dev and
+ * act8_pack. */
 size_t qlora_moe_bwd_act8_workspace_bytes(int64_t m, int32_t E, int64_t n, int64_t k, int32_t r);
 int qlora_moe_bwd_dev_act8(const void *dY, const nf4_act8 *X, const int32_t *source, int64_t m, const int64_t *counts,
                            int32_t E, const nf4_tensor *W, const void *A, const void *B, int32_t r, float s,

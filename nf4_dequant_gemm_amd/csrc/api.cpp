@@ -1873,6 +1873,7 @@ int qlora_moe_bwd_dev_act8(const void *dY, const nf4_act8 *X, const int32_t *sou
   if (!st) st = check_weight(W);
   if (!st) st = check_act8_layer(x, W->k, r, T);
   if (st) return st;
+  if (x.rows < 1) return fail(NF4_EINVAL, "X must have a row at least");    // read in the place of foreign ones
   if (!source && x.rows != m)
     return fail(NF4_EINVAL, "X must have m = %lld rows without a source (got %lld)", (long long)m, (long long)x.rows);
   if (!words(source)) return fail(NF4_EINVAL, "source must be 4-byte aligned");

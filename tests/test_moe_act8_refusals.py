@@ -163,3 +163,15 @@ def test_partials_stay_bounded():
     for rows in (1, 256, 5000, 1 << 16, 1 << 20):
         for n, k, r in ((64, 64, 1), (4096, 14336, 32), (28672, 8192, 64), (14336, 4096, 128)):
             assert lib.qlora_bwd_act8_workspace_bytes(rows, n, k, r) <= 10 * rows * r + 2 * r * n + (1 << 30) + 1024
+
+
+def test_grouped_rows_of_no_tokens():
+    """The grouped layer's kept activation has a row at least, also where every source is foreign: there is no row to read
+    in the place of one that is not there."""
+    lib = m.library()
+    M, n, k, r, E = 10, 64, 128, 8, 2
+    wsb = lib.qlora_moe_bwd_act8_workspace_bytes(M, E, n // E, k, r)
+    for codes in (0, 4096):
+        assert lib.qlora_moe_bwd_dev_act8(FAKE, act8(codes=codes, rows=0), FAKE, M, FAKE, E, weight(), FAKE, FAKE, r, 1.0, FAKE,
+                                          FAKE, FAKE, FAKE, FAKE, wsb, None) == INVALID
+        assert b"row" in lib.nf4_last_error()
