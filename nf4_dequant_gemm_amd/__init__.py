@@ -1353,7 +1353,7 @@ class MoEGatherFunction(torch.autograd.Function):
 
 
 class MoECombineFunction(torch.autograd.Function):
-    """moe_combine; gradients flow to Z, gate and base (None: no base)."""
+    """moe_combine; gradients flow to Z, gate (None: ones) and base (None: no base)."""
 
     @staticmethod
     def forward(ctx, Z, place, source, gate, base=None):
@@ -1365,5 +1365,9 @@ class MoECombineFunction(torch.autograd.Function):
     def backward(ctx, dY):
         Z, place, source, gate = ctx.saved_tensors
         whole = dY.stride(1) == 1 and dY.stride(0) >= dY.shape[1]       # not so where Y was summed over tokens
-        dZ, dgate = moe_combine_bwd(dY if whole else dY.contiguous(), Z, place, source, gate)
+        rows = dY if whole else dY.contiguous()
+        if gate is None:
+            dZ, dgate = moe_gather(rows, place, source), None
+        else:
+            dZ, dgate = moe_combine_bwd(rows, Z, place, source, gate)
         return dZ, None, None, dgate, dY if ctx.based else None

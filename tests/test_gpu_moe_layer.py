@@ -228,3 +228,21 @@ def test_combine_of_broadcast_gradients(lib, reduce):
     reduce(x).square().sum().backward()
     _, *want = grads(x.grad.contiguous())
     assert all(a.abs().sum() > 0 and torch.equal(a, b) for a, b in zip(got, want))
+
+
+def test_combine_without_gates(lib):
+    """No gates are ones, in the gradient too; it flows to Z and base."""
+    t, d, E, top = 30, 72, 5, 2
+    g = torch.Generator(DEV).manual_seed(7)
+    ro = lib.moe_route(torch.randn(t, E, generator=g, device=DEV), top, torch.arange(t, device=DEV) % 7 != 5)
+    Z, base, dY = (torch.randn(n, d, generator=g, device=DEV) for n in (t * top, t, t))
+    outs = []
+    for gate in (None, torch.ones_like(ro.gate)):
+        z, b = Z.clone().requires_grad_(), base.clone().requires_grad_()
+        y = lib.MoECombineFunction.apply(z, ro.place, ro.source, gate, b)
+        y.backward(dY)
+        outs.append((y.detach(), z.grad, b.grad))
+    assert all(torch.equal(a, b) for a, b in zip(*outs)) and not outs[0][1][int(ro.sizes[1]):].any()
+    z = Z.clone().requires_grad_()
+    lib.MoECombineFunction.apply(z, ro.place, ro.source, None).sum(0).backward(dY[0])
+    assert torch.equal(z.grad, lib.moe_gather(dY[:1].expand(t, d).contiguous(), ro.place, ro.source))
