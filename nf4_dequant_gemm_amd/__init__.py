@@ -919,11 +919,12 @@ def moe_route(logits: torch.Tensor, top: int, keep: Optional[torch.Tensor] = Non
     top = int(top)
     if not 1 <= top <= min(16, E):
         raise ValueError(f"top must lie in [1, min(16, E)] (got {top})")
-    place, idx, source = logits.new_empty((3, t, top), dtype=torch.int32).unbind()
-    source = source.view(-1)
+    # each in memory of its own but counts and sizes, as callers change some in place and autograd keeps others
+    idx, place = (logits.new_empty((t, top), dtype=torch.int32) for _ in range(2))
+    source = logits.new_empty(t * top, dtype=torch.int32)
     gate = logits.new_empty((t, top), dtype=torch.float32)
     counts, sizes = logits.new_empty(E + 2, dtype=torch.int64).split((E, 2))
-    mean_p, losses = logits.new_empty(E + 2, dtype=torch.float32).split((E, 2))
+    mean_p, losses = (logits.new_empty(n, dtype=torch.float32) for n in (E, 2))
     wsb = _bytes_of("moe_route_workspace_bytes", t, E)
     ws = logits.new_empty(wsb, dtype=torch.uint8) if wsb else None
     _call(dev, "moe_route", logits.data_ptr(), code, t, E, ld, _addr(keep), top, bool(renormalize), idx.data_ptr(),

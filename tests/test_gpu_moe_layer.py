@@ -246,3 +246,24 @@ def test_combine_without_gates(lib):
     z = Z.clone().requires_grad_()
     lib.MoECombineFunction.apply(z, ro.place, ro.source, None).sum(0).backward(dY[0])
     assert torch.equal(z.grad, lib.moe_gather(dY[:1].expand(t, d).contiguous(), ro.place, ro.source))
+
+
+def test_losses_scaled_in_place(lib):
+    """What a caller does to the outputs in place: scaled losses reach the logits scaled; the mean probabilities (summed over
+    processes, say) and the places of dropped rows are no part of the gradient."""
+    x = torch.randn(30, 6, device=DEV, generator=torch.Generator(DEV).manual_seed(8))
+    grads = []
+    for in_place in (False, True):
+        leaf = x.clone().requires_grad_()
+        r = lib.MoERouting(*lib.MoERouteFunction.apply(leaf, 2))
+        losses = r.losses
+        if in_place:
+            losses *= 0.5
+            r.mean_p.mul_(2)
+            r.place[3] = -1
+            r.source.fill_(-1)
+        else:
+            losses = losses * 0.5
+        (losses.sum() + r.gate.square().sum()).backward()
+        grads.append(leaf.grad)
+    assert grads[0].abs().sum() > 0 and torch.equal(*grads)
