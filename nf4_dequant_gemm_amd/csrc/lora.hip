@@ -561,6 +561,17 @@ __global__ __launch_bounds__(1024) void mreduce_final_t_kernel(const float *__re
               (int64_t)blockIdx.x * 64);
 }
 
+// Either for few outputs, one to a thread.
+template <bool kTransposed>
+__global__ __launch_bounds__(256) void mreduce_final_few_kernel(const float *__restrict__ part, int64_t C, int r, int splits,
+                                                                float s, uint16_t *__restrict__ out) {
+  const int64_t n = (int64_t)r * C, i = (int64_t)blockIdx.x * 256 + threadIdx.x;
+  if (i >= n) return;
+  const float a = split_sum1(part + (int64_t)blockIdx.y * splits * n + i, n, splits);
+  const int64_t j = i / C, at = kTransposed ? (i - j * C) * r + j : i;
+  out[(int64_t)blockIdx.y * n + at] = (uint16_t)(pack_bf16x2(s * a, 0.f) & 0xFFFFu);
+}
+
 // Splits of the M-reduction over C / 128 column tiles. One layer: as many as let ONE round of
 // workgroups fill the GPU, so that each workgroup streams the longest run of rows and no partial
 // round trails (measured: the backward's rank-r part of the mlp_up shape 0.153 -> 0.130 ms). A
@@ -585,7 +596,16 @@ hipError_t launch_mreduce_final(const float *part, int64_t C, int r, int splits,
                                 uint16_t *out, hipStream_t st) {
   const int64_t n = (int64_t)r * C;
   if (r > 128 || C % 8) return hipErrorInvalidValue;
-  if (transposed)
+  // Few workgroups of several outputs a thread do not draw on the whole memory, so few outputs go one to a thread
+  // (medians of a launch, few / several): 64 x 128 from 128 partials 7.1 and 41 us transposed, 6.8 and 11.5 not; 2048 x 64 of
+  // 8192 rows 4.3 and 8.4, 4.1 and 5.1; 8192 x 64 of 1000 rows 6.3 and 5.3, 5.2 and 4.1; 11008 x 128 14 and 5.2, 5.3 and 4.9.
+  const bool few = transposed ? C * E < 8192 : n * E < (1 << 18);
+  const dim3 each((unsigned)((n + 255) / 256), (unsigned)E);
+  if (few && transposed)
+    mreduce_final_few_kernel<true><<<each, dim3(256), 0, st>>>(part, C, r, splits, s, out);
+  else if (few)
+    mreduce_final_few_kernel<false><<<each, dim3(256), 0, st>>>(part, C, r, splits, s, out);
+  else if (transposed)
     mreduce_final_t_kernel<<<dim3((unsigned)((C + 63) / 64), (unsigned)E),
                              dim3(split_sum_t_threads(r)), 0, st>>>(part, C, r, splits, s, out);
   else

@@ -20,23 +20,28 @@ __device__ __forceinline__ f32x4 split_sum4(const float *p, int64_t n, int split
   return a;
 }
 
-// out[i] (bf16) and wide[i] (float32; NULL: none) = the sum of `splits` partials [n] at part, sequential, its loads issued
-// eight at a time; workgroup `block` of `blocks`.
+// The sum of `splits` partials at p, n apart, sequential, loads issued eight at a time.
+__device__ __forceinline__ float split_sum1(const float *p, int64_t n, int splits) {
+  float a = 0.f;
+  int s = 0;
+  for (; s + 8 <= splits; s += 8) {
+    float v[8];
+#pragma unroll
+    for (int j = 0; j < 8; ++j) v[j] = p[(int64_t)(s + j) * n];
+#pragma unroll
+    for (int j = 0; j < 8; ++j) a += v[j];
+  }
+  for (; s < splits; ++s) a += p[(int64_t)s * n];
+  return a;
+}
+
+// out[i] (bf16) and wide[i] (float32; NULL: none) = the sum of `splits` partials [n] at part; workgroup `block` of
+// `blocks`.
 __device__ __forceinline__ void split_sum_each(const float *__restrict__ part, int64_t n, int splits,
                                                uint16_t *__restrict__ out, float *__restrict__ wide, int64_t block,
                                                int64_t blocks) {
   for (int64_t i = block * blockDim.x + threadIdx.x; i < n; i += blocks * blockDim.x) {
-    const float *pi = part + i;
-    float a = 0.f;
-    int s = 0;
-    for (; s + 8 <= splits; s += 8) {
-      float v[8];
-#pragma unroll
-      for (int j = 0; j < 8; ++j) v[j] = pi[(int64_t)(s + j) * n];
-#pragma unroll
-      for (int j = 0; j < 8; ++j) a += v[j];
-    }
-    for (; s < splits; ++s) a += pi[(int64_t)s * n];
+    const float a = split_sum1(part + i, n, splits);
     out[i] = (uint16_t)(pack_bf16x2(a, 0.f) & 0xFFFFu);
     if (wide) wide[i] = a;
   }
