@@ -656,25 +656,38 @@ hipError_t launch_mreduce_grouped(const uint16_t *P, const uint16_t *Q, int64_t 
 }
 
 // ---------------------------------------------------------------------------------- transpose
-// dst[j][l] = src[l][j]: a workgroup takes 64 rows l of src, which are contiguous, through LDS.
-__global__ __launch_bounds__(256) void transpose_kernel(const uint16_t *__restrict__ src, int64_t L, int r,
+// dst[j][l] = src[l][j]: a workgroup takes 64 rows l of src, which are contiguous, through LDS rows of an odd length
+// (32 rows' elements are in different banks; at rank 128 the unpadded rows' were all in one: 6.2 us for 2048 rows, now
+// 3.3).
+__global__ __launch_bounds__(1024) void transpose_kernel(const uint16_t *__restrict__ src, int64_t L, int r,
                                                         uint16_t *__restrict__ dst) {
-  __shared__ uint16_t tile[64 * 128];
+  __shared__ uint16_t tile[64 * 129];
   const int64_t l0 = (int64_t)blockIdx.x * 64;
-  const int rows = L - l0 < 64 ? (int)(L - l0) : 64;
-  for (int i = threadIdx.x; i < rows * r / 8; i += 256)        // rows is a multiple of 8
-    *reinterpret_cast<u32x4 *>(tile + 8 * i) = *reinterpret_cast<const u32x4 *>(src + l0 * r + 8 * i);
+  const int rows = L - l0 < 64 ? (int)(L - l0) : 64, row = r | 1, pad = row - r;
+  for (int i = threadIdx.x; i < rows * r / 8; i += blockDim.x) {      // rows is a multiple of 8
+    const u32x4 v = *reinterpret_cast<const u32x4 *>(src + l0 * r + 8 * i);
+    int at = 8 * i + 8 * i / r * pad, left = r - 8 * i % r;    // left: elements up to the row's end
+#pragma unroll
+    for (int e = 0; e < 8; ++e) {
+      tile[at] = (uint16_t)(v[e / 2] >> (16 * (e & 1)));
+      ++at;
+      if (--left == 0) {
+        at += pad;
+        left = r;
+      }
+    }
+  }
   __syncthreads();
   const int l = (threadIdx.x & 31) * 2;
   if (l >= rows) return;
-  for (int j = threadIdx.x >> 5; j < r; j += 8)
-    *reinterpret_cast<uint32_t *>(dst + (int64_t)j * L + l0 + l) = tile[l * r + j] | ((uint32_t)tile[(l + 1) * r + j] << 16);
+  for (int j = threadIdx.x >> 5; j < r; j += blockDim.x >> 5)
+    *reinterpret_cast<uint32_t *>(dst + (int64_t)j * L + l0 + l) = tile[l * row + j] | ((uint32_t)tile[(l + 1) * row + j] << 16);
 }
 
 // L % 8 == 0, r <= 128, both matrices 16-byte aligned.
 hipError_t launch_transpose(const uint16_t *src, int64_t L, int r, uint16_t *dst, hipStream_t st) {
   if (r > 128 || L % 8) return hipErrorInvalidValue;
-  transpose_kernel<<<dim3((unsigned)((L + 63) / 64)), dim3(256), 0, st>>>(src, L, r, dst);
+  transpose_kernel<<<dim3((unsigned)((L + 63) / 64)), dim3(r > 64 ? 1024 : r > 32 ? 512 : 256), 0, st>>>(src, L, r, dst);
   return hipGetLastError();
 }
 

@@ -1,0 +1,60 @@
+"""The adapters' gradients at ranks, stages and sizes on either side of the kernels' choices, against float64 sums.
+
+dB = s dY^T T: float32 sums over m rows (m 2^-24 of the magnitudes' sum at most, taken as 2^-10 for m <= 2^14), and half a
+step of bf16 of the result, 2^-8. dA = s U^T X: the same, and of U = dY B the sums over n <= 2^15 columns (2^-9 of their
+magnitudes) and the rounding to bf16, 2^-8.
+"""
+import pytest
+import torch
+
+from tests.gpu_helpers import say
+
+pytestmark = pytest.mark.gpu
+
+DEV = "cuda"
+BF = torch.bfloat16
+
+
+def near(got, want, allowed):
+    return bool(((got.double() - want).abs() <= 2.0 ** -8 * want.abs() + allowed).all())
+
+
+def check(dA, dB, dY, X, B, T, s):
+    dY, X, B, T = (z.double() for z in (dY, X, B, T))
+    U, most, x = dY @ B, dY.abs() @ B.abs(), X.abs()
+    assert near(dB, s * dY.t() @ T, s * 2.0 ** -10 * (dY.abs().t() @ T.abs()))
+    assert near(dA, s * U.t() @ X, s * ((2.0 ** -8 + 2.0 ** -10) * (U.abs().t() @ x) + 2.0 ** -9 * (most.t() @ x)))
+
+
+@pytest.mark.parametrize("m,k,n,r", [
+    (1, 64, 8, 1), (64, 64, 72, 7), (65, 128, 64, 33), (128, 64, 520, 100), (129, 192, 264, 127), (200, 4096, 64, 63),
+    (200, 4096, 64, 64), (300, 2112, 8184, 9), (300, 64, 8192, 8), (700, 64, 8192, 33), (9000, 64, 128, 128),
+    (9000, 64, 128, 100), (1000, 2048, 2048, 128), (1000, 2048, 2048, 101), (77, 64, 20000, 128), (77, 64, 20000, 65),
+    (2500, 320, 1000, 31), (130, 64, 32768, 2)])
+def test_one_layer(lib, m, k, n, r):
+    say(f"adapter sums m={m} k={k} n={n} r={r}")
+    g = torch.Generator(DEV).manual_seed(m + n + r)
+    rand = lambda *shape: torch.randn(*shape, generator=g, device=DEV).to(BF)
+    X, A, B, dY, T = rand(m, k), rand(r, k), rand(n, r), rand(m, n), rand(m, r)
+    q = lib.NF4Tensor.empty(n, k, 256, torch.device(DEV))       # the weight is not read without dX
+    none, dA, dB = lib.qlora_bwd(dY, X, q, A, B, 0.5, T, need_dx=False)
+    assert none is None
+    check(dA, dB, dY, X, B, T, 0.5)
+
+
+@pytest.mark.parametrize("counts,k,n,r", [((1, 64, 0, 65), 64, 72, 33), ((200, 129), 128, 4088, 7), ((200, 129), 128, 4096, 100),
+                                          ((0, 1000, 63, 2, 191), 1024, 520, 101), ((30, 70), 2048, 64, 64)])
+def test_grouped(lib, counts, k, n, r):
+    say(f"adapter sums of experts {counts} k={k} n={n} r={r}")
+    E, m = len(counts), sum(counts)
+    g = torch.Generator(DEV).manual_seed(m + n + r)
+    rand = lambda *shape: torch.randn(*shape, generator=g, device=DEV).to(BF)
+    X, A, B, dY, T = rand(m, k), rand(E * r, k), rand(E * n, r), rand(m, n), rand(m, r)
+    q = lib.NF4Tensor.empty(E * n, k, 256, torch.device(DEV))
+    dA, dB = torch.empty_like(A), torch.empty_like(B)
+    ws = torch.empty(lib.moe_workspace_bytes_dev(m, E, n, k, r), dtype=torch.uint8, device=DEV)
+    lib.qlora_moe_bwd_dev(dY, X, torch.tensor(counts, device=DEV), q, A, B, 0.5, T, None, dA, dB, ws)
+    lo = 0
+    for e, c in enumerate(counts):
+        check(dA[e * r:(e + 1) * r], dB[e * n:(e + 1) * n], dY[lo:lo + c], X[lo:lo + c], B[e * n:(e + 1) * n], T[lo:lo + c], 0.5)
+        lo += c
