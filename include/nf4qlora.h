@@ -508,7 +508,7 @@ int moe_route_bwd(const void *logits, int dtype, int64_t t, int32_t E, int64_t l
  *   moe_gather       out[place_ij] = X_i; rows without a token are 0. out [t * top, d]
  *   moe_combine      Y_i = base_i + sum_j gate_ij Z[place_ij] (base NULL: 0; gate NULL: ones, which is the
  *                    gradient of moe_gather). Y [t, d]; Z [t * top, d], whose rows without a token are not
- *                    read; Y may be base
+ *                    used (any values, Inf and NaN too); Y may be base
  *   moe_combine_bwd  dZ[place_ij] = gate_ij dY_i, rows without a token 0; dgate_ij = <dY_i, Z[place_ij]>
  *                    (0 without a place); the gradient of base is dY. dZ may be Z
  * Elements are `dtype`; X, dY, base and Y have row strides >= d in elements, the grouped rows are
@@ -544,13 +544,17 @@ int act8_unpack(const nf4_act8 *q, void *X, int dtype, int64_t ldx, void *stream
  * rank 64 U and dB come from one pass over dY; the reduction of a dX of few tiles is split over workgroups), and
  * dA = s U^T X from U in float32 and what the codes stand for: U times a block's scale is rounded to bf16, the
  * codes are not rounded. T must be given when r > 0. ws: at least what the function before it says, as for the
- * forms below; at most about 1 GiB beside U and B transposed. Errors: as qlora_bwd and act8_pack. */
+ * forms below. It holds U in bf16 and in float32 (6 m r bytes), B transposed (2 r n) where U and dB take two launches
+ * (above rank 64, or where the partials of one would be over 1 GiB), and the largest of the partials that are in use at a
+ * time: float32 copies of U and dB, of dA, or tiles of dX (at most 64 MiB). Errors: as qlora_bwd and act8_pack. */
 size_t qlora_bwd_act8_workspace_bytes(int64_t m, int64_t n, int64_t k, int32_t r);
 int qlora_bwd_act8(const void *dY, const nf4_act8 *X, const nf4_tensor *W, const void *A, const void *B, int32_t r,
                    float s, const void *T, void *dX, void *dA, void *dB, void *ws, size_t ws_bytes, void *stream);
 
 /* qlora_swiglu_bwd with X and Ygu in 8 bits: the activation's gradient is formed in float32 from what
- * Ygu's codes stand for. Tgu must be given when r > 0. Errors: as qlora_swiglu_bwd and act8_pack. */
+ * Ygu's codes stand for, and rounded to bf16 for the products, as there. Tgu must be given when r > 0. ws: what
+ * qlora_bwd_act8 needs for the stacked weight at rank 2r, and the gradients of Yg and Yu (4 m n bytes) and B and dB
+ * as block diagonals (16 n r). Errors: as qlora_swiglu_bwd and act8_pack. */
 size_t qlora_swiglu_bwd_act8_workspace_bytes(int64_t m, int64_t n, int64_t k, int32_t r);
 int qlora_swiglu_bwd_act8(const void *dH, const nf4_act8 *X, const nf4_tensor *Wgu, const void *Agu, const void *Bg,
                           const void *Bu, int32_t r, float s, const nf4_act8 *Ygu, const void *Tgu, void *dX, void *dAgu,
@@ -558,8 +562,8 @@ int qlora_swiglu_bwd_act8(const void *dH, const nf4_act8 *X, const nf4_tensor *W
 
 /* qlora_moe_bwd_dev with X in 8 bits: grouped row i is row source[i] of X (a source outside X's rows: zeros),
  * so that a token's activation is kept once, not once for each of its experts; source NULL: row i, and X
- * has m rows. X has a row at least (NF4_EINVAL). T must be given when r > 0. Errors: as qlora_moe_bwd_dev and
- * act8_pack. */
+ * has m rows. X has a row at least (NF4_EINVAL). T must be given when r > 0. ws: as for qlora_bwd_act8, with m the
+ * grouped rows, B, dA and dB those of all experts, and the group table. Errors: as qlora_moe_bwd_dev and act8_pack. */
 size_t qlora_moe_bwd_act8_workspace_bytes(int64_t m, int32_t E, int64_t n, int64_t k, int32_t r);
 int qlora_moe_bwd_dev_act8(const void *dY, const nf4_act8 *X, const int32_t *source, int64_t m, const int64_t *counts,
                            int32_t E, const nf4_tensor *W, const void *A, const void *B, int32_t r, float s,

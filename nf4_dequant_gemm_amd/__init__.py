@@ -984,7 +984,7 @@ def moe_gather(X: torch.Tensor, place: torch.Tensor, source: torch.Tensor) -> to
 def moe_combine(Z: torch.Tensor, place: torch.Tensor, gate: Optional[torch.Tensor] = None,
                 base: Optional[torch.Tensor] = None, out: Optional[torch.Tensor] = None) -> torch.Tensor:
     """[t, d]: base (or 0) plus the sum of the rows of Z [t * top, d] at a token's places, times its gates
-    (None: ones). Rows of Z without a token are not read. out may be base."""
+    (None: ones). Rows of Z without a token are not used. out may be base."""
     code, dev = _dtype_code(Z, "Z"), Z.device
     t, top = _place_args(place, None, dev)
     if Z.dim() != 2:

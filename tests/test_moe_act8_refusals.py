@@ -175,3 +175,18 @@ def test_grouped_rows_of_no_tokens():
         assert lib.qlora_moe_bwd_dev_act8(FAKE, act8(codes=codes, rows=0), FAKE, M, FAKE, E, weight(), FAKE, FAKE, r, 1.0, FAKE,
                                           FAKE, FAKE, FAKE, FAKE, wsb, None) == INVALID
         assert b"row" in lib.nf4_last_error()
+
+
+def test_workspaces_of_the_pair_and_of_experts():
+    """The pair's workspace is the stacked layer's at twice the rank, the projections' gradients and two block diagonals; that of
+    experts holds U (in bf16, in float32 and once more as a partial), at most 1 GiB of dB's partials, or those of their
+    dA and dB (one copy each where there are many experts), B transposed where it is used, and a table."""
+    lib = m.library()
+    for rows in (1, 300, 1 << 16, 1 << 20):
+        for n, k, r in ((64, 64, 0), (64, 64, 1), (11008, 4096, 16), (11008, 4096, 64), (28672, 8192, 33)):
+            pair, one = lib.qlora_swiglu_bwd_act8_workspace_bytes(rows, n, k, r), lib.qlora_bwd_act8_workspace_bytes(rows, 2 * n, k, 2 * r)
+            assert one + 4 * rows * n + 16 * n * r <= pair <= one + 4 * rows * n + 16 * n * r + 3 * 256
+        for E in (1, 8, 256):
+            for n, k, r in ((64, 64, 1), (2048, 7168, 128), (11008, 4096, 64)):
+                assert lib.qlora_moe_bwd_act8_workspace_bytes(rows, E, n, k, r) <= (
+                    10 * rows * r + 2 * r * E * n + (1 << 30) + 4 * r * E * (n + k) + (1 << 16))
