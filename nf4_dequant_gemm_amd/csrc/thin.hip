@@ -6,12 +6,13 @@
 // two reads of it. Here a workgroup takes 256 or 512 rows and a range of columns, in steps of 128 columns that are staged in
 // LDS once and multiplied twice: rows by B (U's sums over the range stay in registers until its end), and columns by T
 // (dB's sums over the rows, written after each step). Sums over ranges and over row blocks are added in a
-// fixed order by one further launch. T, a step of dY and of B are 125 KB of LDS at rank 64; at 128 they are more than
-// there is, and the partials of dB, written and read, twice dY's bytes: above 64 the two launches stay.
+// fixed order by one further launch. T, a step of dY and of B are 122 KiB of LDS at rank 64, 158 of the CU's 160 with 512
+// rows; at 128 they are more than there is, and the partials of dB, written and read, twice dY's bytes: above 64 the two
+// launches stay.
 //
 // Bound by memory: a step's 64 KB are requested two steps ahead, 128 KB in flight on every CU. All of the adapters'
-// gradients, k 512, against the two launches (us): 8192 x 14336 at rank 64 151 (180), at 33 149 (315); 16384 x 14336 at 64
-// 223 (290); 4096 x 11008 at 64 80 (98); 64 x 4096 at 16 19 (27). This kernel alone takes 97 us for 16384 x 11008 of 8
+// gradients, k 512, against the two launches (us): 8192 x 14336 at rank 64 102 (117); 16384 x 14336 at 64 175 (232);
+// 4096 x 11008 at 64 53 (68); 8192 x 14336 at 20 70 (98); 64 x 4096 at 16 24 (30). This kernel alone takes 97 us for 16384 x 11008 of 8
 // experts at rank 16 (3.7 TB/s) and 57 for 8192 x 11008 at rank 64 (4.5 TB/s with its partials; 67 with blocks of 256
 // rows). Two workgroups a CU with T in registers gained 5% at rank 16 where the order of steps gains 7.
 #include "common.h"
@@ -61,6 +62,7 @@ __global__ __launch_bounds__(kT) void thin_kernel(const uint16_t *__restrict__ d
   __shared__ __align__(16) uint16_t sY[kRB * kYRow];
   __shared__ __align__(16) uint16_t sT[kHalves * kRB * PROW];
   __shared__ __align__(16) uint16_t sB[kCB * PROW];
+  static_assert(sizeof(sY) + sizeof(sT) + sizeof(sB) <= 160 * 1024, "the LDS of a CU");
   const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
   const int64_t blk = blockIdx.x;
   int64_t mbase = blk * kHalves * kRB, mhi = M;
