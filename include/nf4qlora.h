@@ -540,13 +540,14 @@ typedef struct {
 int act8_pack(const void *X, int dtype, int64_t ldx, const nf4_act8 *q, void *stream);
 int act8_unpack(const nf4_act8 *q, void *X, int dtype, int64_t ldx, void *stream);
 
-/* qlora_bwd with X in 8 bits (m = X->rows): U, dX and dB as there up to the order of their float32 sums (up to
- * rank 64 U and dB come from one pass over dY; the reduction of a dX of few tiles is split over workgroups), and
+/* qlora_bwd with X in 8 bits (m = X->rows): U, dX and dB as there up to the order of their float32 sums (mostly
+ * U and dB come from one pass over dY, up to rank 64; the reduction of a dX of few tiles is split over workgroups), and
  * dA = s U^T X from U in float32 and what the codes stand for: U times a block's scale is rounded to bf16, the
  * codes are not rounded. T must be given when r > 0. ws: at least what the function before it says, as for the
  * forms below. It holds U in bf16 and in float32 (6 m r bytes), B transposed (2 r n) where U and dB take two launches
- * (above rank 64, or where the partials of one would be over 1 GiB), and the largest of the partials that are in use at a
- * time: float32 copies of U and dB, of dA, or tiles of dX (at most 64 MiB). Errors: as qlora_bwd and act8_pack. */
+ * (above rank 64, in large calls at other ranks above 32 that are not a multiple of 8, and where the partials of one would
+ * be over 1 GiB), and the largest of the partials that are in use at a time: float32 copies of U and dB, of dA, or tiles of
+ * dX (at most 64 MiB). Errors: as qlora_bwd and act8_pack. */
 size_t qlora_bwd_act8_workspace_bytes(int64_t m, int64_t n, int64_t k, int32_t r);
 int qlora_bwd_act8(const void *dY, const nf4_act8 *X, const nf4_tensor *W, const void *A, const void *B, int32_t r,
                    float s, const void *T, void *dX, void *dA, void *dB, void *ws, size_t ws_bytes, void *stream);

@@ -413,7 +413,10 @@ hipError_t launch_mreduce_act8(const float *P, const Act8 &q, const int *map, in
 int mreduce_act8_splits(int64_t M, int64_t C, int r, int E = 1);
 // U = dY B (bf16, and in float32) and dB = s dY^T T (bf16 [N][r]) in one pass over dY [M][N] (thin.hip), where
 // thin_takes: up to kThinMaxRank, with 1 GiB of partials of dB at most (they are r / 128 of dY's bytes; those
-// of launch_mreduce do not grow with M). N % 8 == 0, N <= 2^22: 256 rows are addressed with 31 bits. Grouped (gr: 256-row
+// of launch_mreduce do not grow with M). Ranks above 32 that are not a multiple of 8 read B and T element by element for
+// each workgroup, and stay with the two launches from M N = 2^24 on (all of the adapters' gradients with k 512 in us, one
+// pass and two launches: rank 33, 8192 x 14336 144 and 106, 2048 x 11008 52 and 47, 4096 x 2048 41 and 40, 1000 x 4096 31 and
+// 34; rank 31, 8192 x 14336 83 and 102; 64 experts, 8192 x 2048 at rank 33 91 and 74). N % 8 == 0, N <= 2^22: 256 rows are addressed with 31 bits. Grouped (gr: 256-row
 // blocks of the experts, counted times `per`): B [E][N][r] and dB are the experts', the grid is bounded by M and E.
 // part: u_floats + b_floats of thin_plan.
 constexpr int kThinMaxRank = 64, kThinRows = 256;
@@ -422,7 +425,8 @@ inline int64_t thin_blocks(int64_t M, int E) {
   return blocks < M ? blocks : M;
 }
 inline bool thin_takes(int64_t M, int64_t N, int r, int E = 1) {
-  return r > 0 && r <= kThinMaxRank && thin_blocks(M, E) <= (int64_t(1) << 28) / (r * N);
+  return r > 0 && r <= kThinMaxRank && (r <= 32 || r % 8 == 0 || M * N < (int64_t(1) << 24)) &&
+         thin_blocks(M, E) <= (int64_t(1) << 28) / (r * N);
 }
 struct ThinPlan {
   int64_t blocks, lsplit;

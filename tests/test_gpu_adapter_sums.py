@@ -58,3 +58,16 @@ def test_grouped(lib, counts, k, n, r):
     for e, c in enumerate(counts):
         check(dA[e * r:(e + 1) * r], dB[e * n:(e + 1) * n], dY[lo:lo + c], X[lo:lo + c], B[e * n:(e + 1) * n], T[lo:lo + c], 0.5)
         lo += c
+
+
+@pytest.mark.parametrize("m,k,n,r", [(4100, 64, 4104, 33), (4000, 64, 4104, 33), (2100, 128, 8192, 63), (4100, 64, 4104, 40),
+                                     (4100, 64, 4104, 31)])
+def test_eight_bits(lib, m, k, n, r):
+    """X in 8 bits, U and dB from one pass or two launches. U times a scale is rounded to bf16 in the place of U."""
+    g = torch.Generator(DEV).manual_seed(m + n + r)
+    rand = lambda *shape: torch.randn(*shape, generator=g, device=DEV).to(BF)
+    X, A, B, dY, T = lib.act8_pack(rand(m, k)), rand(r, k), rand(n, r), rand(m, n), rand(m, r)
+    q = lib.NF4Tensor.empty(n, k, 256, torch.device(DEV))
+    none, dA, dB = lib.qlora_bwd_act8(dY, X, q, A, B, 0.5, T, need_dx=False)
+    assert none is None
+    check(dA, dB, dY, lib.act8_unpack(X, torch.float32), B, T, 0.5)
