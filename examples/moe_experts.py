@@ -1,12 +1,12 @@
 #!/usr/bin/env python3
-"""A small mixture-of-experts model on 4-bit bases: trained with a balance loss, its activations kept in 8 bits,
+"""A small mixture-of-experts model on 4-bit bases: trained with a balance loss, its blocks' tokens kept in 8 bits,
 then served token by token.
 
 Every block sends a token to TOP of E experts, each a gate, an up and a down projection with a frozen NF4 base
 and low-rank adapters. moe_route chooses the experts and gives the counts, moe_gather brings the tokens into
 expert order, the grouped layers (QLoRAMoEFunction) run all experts at once, and moe_combine adds their outputs,
 weighted by the gates, to the token. The gate and up projections keep for their backward pass not the gathered
-rows but the tokens, once, in 8 bits. The loss is that of the next token plus the balance and z losses of the
+rows but the tokens, once, in 8 bits; their outputs, and what the down projection and the gates need, stay in bf16. The loss is that of the next token plus the balance and z losses of the
 routers.
 
     python examples/moe_experts.py [--steps 40]
