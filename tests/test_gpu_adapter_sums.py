@@ -71,3 +71,29 @@ def test_eight_bits(lib, m, k, n, r):
     none, dA, dB = lib.qlora_bwd_act8(dY, X, q, A, B, 0.5, T, need_dx=False)
     assert none is None
     check(dA, dB, dY, lib.act8_unpack(X, torch.float32), B, T, 0.5)
+
+
+@pytest.mark.parametrize("m,k,n,r", [(1, 64, 72, 128), (16, 128, 4096, 100), (5, 64, 520, 65), (17, 64, 8, 127)])
+def test_eight_bits_few_rows_high_rank(lib, m, k, n, r):
+    """The two launches with the rows of a decode batch, U in float32 beside its bf16 form."""
+    test_eight_bits(lib, m, k, n, r)
+
+
+@pytest.mark.parametrize("t,top,E,k,n,r", [(300, 2, 4, 192, 264, 100), (37, 1, 3, 64, 72, 128), (9, 3, 5, 128, 520, 65),
+                                           (4200, 1, 2, 64, 4104, 33)])
+@pytest.mark.parametrize("grouped", [False, True])
+def test_experts_from_eight_bits_at_high_rank(lib, t, top, E, k, n, r, grouped):
+    """The grouped layer's two launches, from the tokens' codes or the grouped rows'."""
+    g = torch.Generator(DEV).manual_seed(t + n + r)
+    rand = lambda *shape: torch.randn(*shape, generator=g, device=DEV).to(BF)
+    ro = lib.moe_route(torch.randn(t, E, generator=g, device=DEV), top, torch.arange(t, device=DEV) % 5 != 2)
+    X, A, B, dY, T = rand(t, k), rand(E * r, k), rand(E * n, r), rand(t * top, n), rand(t * top, r)
+    q = lib.NF4Tensor.empty(E * n, k, 256, torch.device(DEV))
+    X8 = lib.act8_pack(lib.moe_gather(X, ro.place, ro.source) if grouped else X)
+    none, dA, dB = lib.qlora_moe_bwd_act8(dY, X8, None if grouped else ro.source, ro.counts, q, A, B, 0.5, T, need_dx=False)
+    assert none is None
+    x, lo = lib.act8_unpack(X8, torch.float32), 0
+    for e, c in enumerate(ro.counts.tolist()):
+        rows = x[lo:lo + c] if grouped else x[ro.source[lo:lo + c].long()]
+        check(dA[e * r:(e + 1) * r], dB[e * n:(e + 1) * n], dY[lo:lo + c], rows, B[e * n:(e + 1) * n], T[lo:lo + c], 0.5)
+        lo += c
